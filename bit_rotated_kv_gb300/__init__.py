@@ -7,6 +7,8 @@ this module fails loudly when it is missing -- there is no CPU fallback.
 
 Entry points (same names as the C ABI in include/kvq.h):
   kv_rotate_qk, kv_quant_flush, kv_attn_decode, kv_attn_decode_bf16, kv_attn_workspace_bytes,
+  kv_attn_tree, kv_verify_tree, kv_tree_commit (a tree of drafted tokens: attention, check, rows kept),
+  kv_pages_reserve, kv_seq_fork, kv_seq_free, kv_pages_compact (the page pool),
   kvq_page_head_bytes, kvq_page_bytes, kvq_status_string
 plus ``KVConfig`` / ``KVCache`` helpers that allocate the caller-owned buffers.
 """
@@ -37,9 +39,13 @@ KVQ_TRANSFORM_DENSE = 0
 KVQ_TRANSFORM_HADAMARD = 1
 KVQ_KEY_PER_TOKEN = 0
 KVQ_KEY_PER_CHANNEL = 1
+KVQ_TREE_MAX_NODES = 128
+KVQ_POOL_MAX_SEQS = 16384
 
 EXPORTED = ("kv_rotate_qk", "kv_quant_flush", "kv_append_chunk", "kv_attn_chunk", "kv_attn_chunk_workspace_bytes", "kv_attn_decode", "kv_attn_decode_bf16", "kv_attn_decode_noalloc",
             "kv_attn_workspace_bytes",
+            "kv_attn_tree", "kv_attn_tree_workspace_bytes", "kv_verify_tree", "kv_tree_commit",
+            "kv_pages_reserve", "kv_seq_fork", "kv_seq_free", "kv_pages_compact", "kv_pages_compact_workspace_bytes",
             "kvq_page_head_bytes", "kvq_page_bytes", "kvq_status_string", "kvq_version",
             "kvq_selftest_scale_division", "kvq_selftest_tc_integer_sums")
 
@@ -91,6 +97,25 @@ def lib() -> ctypes.CDLL:
         l.kv_attn_chunk_workspace_bytes.restype = sz
         l.kv_append_chunk.argtypes = [P(CConfig), P(CTransform), vp, vp, vp, i32, P(CCache), vp, vp]
         l.kv_quant_flush.restype = ctypes.c_int
+        i64 = ctypes.c_int64
+        l.kv_attn_tree.argtypes = [P(CConfig), P(CCache), vp, vp, vp, i32, vp, ctypes.c_float, i32, vp, sz, vp, vp]
+        l.kv_attn_tree.restype = ctypes.c_int
+        l.kv_attn_tree_workspace_bytes.argtypes = [P(CConfig), i32, i32]
+        l.kv_attn_tree_workspace_bytes.restype = sz
+        l.kv_verify_tree.argtypes = [P(CConfig), vp, vp, vp, i32, vp, i64, vp, i64, i32, vp, vp, vp, vp, vp, vp]
+        l.kv_verify_tree.restype = ctypes.c_int
+        l.kv_tree_commit.argtypes = [P(CConfig), P(CCache), vp, i32, vp, vp, vp, vp]
+        l.kv_tree_commit.restype = ctypes.c_int
+        l.kv_pages_reserve.argtypes = [P(CConfig), P(CCache), vp, vp, vp, vp]
+        l.kv_pages_reserve.restype = ctypes.c_int
+        l.kv_seq_fork.argtypes = [P(CConfig), P(CCache), vp, vp, vp, i32, vp, vp]
+        l.kv_seq_fork.restype = ctypes.c_int
+        l.kv_seq_free.argtypes = [P(CConfig), P(CCache), vp, vp, i32, vp, vp]
+        l.kv_seq_free.restype = ctypes.c_int
+        l.kv_pages_compact.argtypes = [P(CConfig), P(CCache), vp, vp, vp, sz, vp, vp]
+        l.kv_pages_compact.restype = ctypes.c_int
+        l.kv_pages_compact_workspace_bytes.argtypes = [P(CConfig)]
+        l.kv_pages_compact_workspace_bytes.restype = sz
         l.kv_attn_decode.argtypes = [P(CConfig), P(CCache), vp, vp, ctypes.c_float, i32, vp, sz, vp, vp]
         l.kv_attn_decode.restype = ctypes.c_int
         l.kv_attn_decode_bf16.argtypes = [P(CConfig), P(CCache), vp, vp, ctypes.c_float, i32, vp, sz, vp, vp]
@@ -328,6 +353,87 @@ def kv_attn_decode_noalloc(cfg: KVConfig, cache: KVCache, q_rot, out, sm_scale: 
     rc = lib().kv_attn_decode_noalloc(ctypes.byref(c), ctypes.byref(cc), _ptr(q_rot), _ptr(out), float(sm_scale),
                                       int(max_ctx), _ptr(status), _stream(stream))
     _check(rc, "kv_attn_decode_noalloc")
+
+
+def _nbytes(t) -> int:
+    return int(t.numel() * t.element_size())
+
+
+def kv_attn_tree_workspace_bytes(cfg: KVConfig, n_rows: int, max_ctx: int) -> int:
+    return int(lib().kv_attn_tree_workspace_bytes(ctypes.byref(cfg.c()), int(n_rows), int(max_ctx)))
+
+
+def kv_attn_tree(cfg: KVConfig, cache: KVCache, q_rot, cu_rows, parent, out, sm_scale: float, max_ctx: int,
+                 workspace, status, stream=None) -> None:
+    """q_rot [n, Hq, d] (rows cu_rows[b] .. cu_rows[b+1]-1 the drafted nodes of sequence b, its last
+    tokens; parent [n] int32 local to the sequence, -1 for a root) -> out [n, Hq, d] bf16: every node
+    attends to the tokens before the drafts, its ancestors and itself."""
+    n = int(q_rot.shape[0])
+    c, cc = cfg.c(), cache.c()
+    rc = lib().kv_attn_tree(ctypes.byref(c), ctypes.byref(cc), _ptr(q_rot), _ptr(cu_rows), _ptr(parent), n, _ptr(out),
+                            float(sm_scale), int(max_ctx), _ptr(workspace), _nbytes(workspace), _ptr(status),
+                            _stream(stream))
+    _check(rc, "kv_attn_tree")
+
+
+def kv_verify_tree(cfg: KVConfig, cu_rows, parent, token, p, q, u, path, n_accept, next_token, status,
+                   stream=None) -> None:
+    """p (and q, or None for chosen drafts) [n, vocab] float32 with contiguous rows; token, parent, path [n]
+    int32; u [n] float32; n_accept, next_token [batch] int32."""
+    n = int(token.shape[0])
+    for t in (p, q):
+        if t is not None and (t.dim() != 2 or t.dtype != torch.float32 or (t.shape[1] > 1 and t.stride(1) != 1)
+                              or t.shape[0] != n or t.shape[1] != p.shape[1] or (n > 1 and t.stride(0) < t.shape[1])):
+            raise KVQError(KVQ_ERR_INVALID_ARG, "kv_verify_tree")
+    rc = lib().kv_verify_tree(ctypes.byref(cfg.c()), _ptr(cu_rows), _ptr(parent), _ptr(token), n, _ptr(p), _row_stride(p),
+                              _ptr(q), 0 if q is None else _row_stride(q), int(p.shape[1]), _ptr(u), _ptr(path),
+                              _ptr(n_accept), _ptr(next_token), _ptr(status), _stream(stream))
+    _check(rc, "kv_verify_tree")
+
+
+def _row_stride(t) -> int:
+    return max(int(t.stride(0)), int(t.shape[1]))
+
+
+def kv_tree_commit(cfg: KVConfig, cache: KVCache, cu_rows, path, n_accept, status, stream=None) -> None:
+    """Keep the rows of the accepted paths (kv_verify_tree's path and n_accept); seq_len drops the others."""
+    rc = lib().kv_tree_commit(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(cu_rows), int(path.shape[0]),
+                              _ptr(path), _ptr(n_accept), _ptr(status), _stream(stream))
+    _check(rc, "kv_tree_commit")
+
+
+def kv_pages_reserve(cfg: KVConfig, cache: KVCache, page_ref, n_tokens, status, stream=None) -> None:
+    """Pages for n_tokens[b] (int32 [batch]) more tokens of every sequence, lowest free ids first."""
+    rc = lib().kv_pages_reserve(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(page_ref), _ptr(n_tokens),
+                                _ptr(status), _stream(stream))
+    _check(rc, "kv_pages_reserve")
+
+
+def kv_seq_fork(cfg: KVConfig, cache: KVCache, page_ref, src, dst, status, stream=None) -> None:
+    """Sequence dst[i] becomes a copy of sequence src[i] (int32 [n] each), sharing its whole INT2 pages."""
+    if src.shape != dst.shape:
+        raise KVQError(KVQ_ERR_INVALID_ARG, "kv_seq_fork")
+    rc = lib().kv_seq_fork(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(page_ref), _ptr(src), _ptr(dst),
+                           int(src.shape[0]), _ptr(status), _stream(stream))
+    _check(rc, "kv_seq_fork")
+
+
+def kv_seq_free(cfg: KVConfig, cache: KVCache, page_ref, seqs, status, stream=None) -> None:
+    """Sequences seqs (int32 [n]) give up their pages and become empty."""
+    rc = lib().kv_seq_free(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(page_ref), _ptr(seqs),
+                           int(seqs.shape[0]), _ptr(status), _stream(stream))
+    _check(rc, "kv_seq_free")
+
+
+def kv_pages_compact_workspace_bytes(cfg: KVConfig) -> int:
+    return int(lib().kv_pages_compact_workspace_bytes(ctypes.byref(cfg.c())))
+
+
+def kv_pages_compact(cfg: KVConfig, cache: KVCache, page_ref, n_live, workspace, status, stream=None) -> None:
+    """Held pages move to ids 0 .. n_live - 1 (n_live int32 [1], out) and the tables follow them."""
+    rc = lib().kv_pages_compact(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(page_ref), _ptr(n_live),
+                                _ptr(workspace), _nbytes(workspace), _ptr(status), _stream(stream))
+    _check(rc, "kv_pages_compact")
 
 
 def kvq_selftest_scale_division(mismatches, stream=None) -> None:

@@ -193,6 +193,115 @@ KVQ_API int kv_attn_chunk(const kvq_config* cfg, const kvq_cache* cache, const u
                                (cudaStream_t)stream);
 }
 
+KVQ_API size_t kv_attn_tree_workspace_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
+  if (check_config(cfg) != KVQ_OK || max_ctx < 0 || n_rows < 0 || n_rows > 65535) return 0;
+  return kvq_attn_chunk_ws_bytes(cfg, n_rows, max_ctx);
+}
+
+KVQ_API int kv_attn_tree(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot, const int32_t* cu_rows,
+                         const int32_t* parent, int32_t n_rows, uint16_t* out, float sm_scale, int32_t max_ctx,
+                         void* workspace, size_t ws_bytes, int32_t* d_status, void* stream) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  rc = check_cache(cfg, cache);
+  if (rc) return rc;
+  if (n_rows < 0 || max_ctx < 0 || !cu_rows || !aligned(cu_rows, 4)) return KVQ_ERR_INVALID_ARG;
+  if (n_rows > 65535) return KVQ_ERR_UNSUPPORTED;
+  if (n_rows == 0) return KVQ_OK;
+  if (!parent || !aligned(parent, 4)) return KVQ_ERR_INVALID_ARG;
+  if (!q_rot || !out || !aligned(q_rot, 16) || !aligned(out, 16)) return KVQ_ERR_INVALID_ARG;
+  if (!(sm_scale == sm_scale)) return KVQ_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256)) return KVQ_ERR_INVALID_ARG;
+  if (ws_bytes < kvq_attn_chunk_ws_bytes(cfg, n_rows, max_ctx)) return KVQ_ERR_WORKSPACE;
+  return kvq_launch_attn_tree_rows(cfg, cache, q_rot, cu_rows, parent, n_rows, out, sm_scale, max_ctx, workspace,
+                                   d_status, (cudaStream_t)stream);
+}
+
+KVQ_API int kv_verify_tree(const kvq_config* cfg, const int32_t* cu_rows, const int32_t* parent, const int32_t* token,
+                           int32_t n_rows, const float* p, int64_t p_stride, const float* q, int64_t q_stride,
+                           int32_t vocab, const float* u, int32_t* path, int32_t* n_accept, int32_t* next_token,
+                           int32_t* d_status, void* stream) {
+  const int rc = check_config(cfg);
+  if (rc) return rc;
+  if (n_rows < 0 || vocab < 1 || !cu_rows || !n_accept || !next_token || !aligned(cu_rows, 4) ||
+      !aligned(n_accept, 4) || !aligned(next_token, 4))
+    return KVQ_ERR_INVALID_ARG;
+  if (cfg->batch > 65535) return KVQ_ERR_UNSUPPORTED;              // a grid dimension
+  if (n_rows > 0) {
+    if (!parent || !token || !p || !u || !path || p_stride < vocab || (q && q_stride < vocab))
+      return KVQ_ERR_INVALID_ARG;
+    if (!aligned(parent, 4) || !aligned(token, 4) || !aligned(p, 4) || !aligned(q, 4) || !aligned(u, 4) ||
+        !aligned(path, 4))
+      return KVQ_ERR_INVALID_ARG;
+  }
+  return kvq_launch_verify_tree(cfg, cu_rows, parent, token, n_rows, p, p_stride, q, q_stride, vocab, u, path,
+                                n_accept, next_token, d_status, (cudaStream_t)stream);
+}
+
+KVQ_API int kv_tree_commit(const kvq_config* cfg, const kvq_cache* cache, const int32_t* cu_rows, int32_t n_rows,
+                           const int32_t* path, const int32_t* n_accept, int32_t* d_status, void* stream) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  rc = check_cache(cfg, cache);
+  if (rc) return rc;
+  if (n_rows < 0 || !cu_rows || !n_accept || !aligned(cu_rows, 4) || !aligned(n_accept, 4)) return KVQ_ERR_INVALID_ARG;
+  if (n_rows == 0) return KVQ_OK;
+  if (!path || !aligned(path, 4)) return KVQ_ERR_INVALID_ARG;
+  return kvq_launch_tree_commit(cfg, cache, cu_rows, n_rows, path, n_accept, d_status, (cudaStream_t)stream);
+}
+
+KVQ_API int kv_pages_reserve(const kvq_config* cfg, const kvq_cache* cache, int32_t* page_ref,
+                             const int32_t* n_tokens, int32_t* d_status, void* stream) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  rc = check_cache(cfg, cache);
+  if (rc) return rc;
+  if (!page_ref || !n_tokens || !aligned(page_ref, 4) || !aligned(n_tokens, 4)) return KVQ_ERR_INVALID_ARG;
+  if (cfg->batch > KVQ_POOL_MAX_SEQS) return KVQ_ERR_UNSUPPORTED;
+  return kvq_launch_pages_reserve(cfg, cache, page_ref, n_tokens, d_status, (cudaStream_t)stream);
+}
+
+KVQ_API int kv_seq_fork(const kvq_config* cfg, const kvq_cache* cache, int32_t* page_ref, const int32_t* src,
+                        const int32_t* dst, int32_t n, int32_t* d_status, void* stream) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  rc = check_cache(cfg, cache);
+  if (rc) return rc;
+  if (n < 0 || !page_ref || !aligned(page_ref, 4)) return KVQ_ERR_INVALID_ARG;
+  if (n > KVQ_POOL_MAX_SEQS) return KVQ_ERR_UNSUPPORTED;
+  if (n > 0 && (!src || !dst || !aligned(src, 4) || !aligned(dst, 4))) return KVQ_ERR_INVALID_ARG;
+  return kvq_launch_seq_fork(cfg, cache, page_ref, src, dst, n, d_status, (cudaStream_t)stream);
+}
+
+KVQ_API int kv_seq_free(const kvq_config* cfg, const kvq_cache* cache, int32_t* page_ref, const int32_t* seqs,
+                        int32_t n, int32_t* d_status, void* stream) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  rc = check_cache(cfg, cache);
+  if (rc) return rc;
+  if (n < 0 || !page_ref || !aligned(page_ref, 4)) return KVQ_ERR_INVALID_ARG;
+  if (n > KVQ_POOL_MAX_SEQS) return KVQ_ERR_UNSUPPORTED;
+  if (n > 0 && (!seqs || !aligned(seqs, 4))) return KVQ_ERR_INVALID_ARG;
+  return kvq_launch_seq_free(cfg, cache, page_ref, seqs, n, d_status, (cudaStream_t)stream);
+}
+
+KVQ_API size_t kv_pages_compact_workspace_bytes(const kvq_config* cfg) {
+  if (check_config(cfg) != KVQ_OK) return 0;
+  return kvq_compact_ws_bytes(cfg);
+}
+
+KVQ_API int kv_pages_compact(const kvq_config* cfg, const kvq_cache* cache, int32_t* page_ref, int32_t* n_live,
+                             void* workspace, size_t ws_bytes, int32_t* d_status, void* stream) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  rc = check_cache(cfg, cache);
+  if (rc) return rc;
+  if (!page_ref || !n_live || !aligned(page_ref, 4) || !aligned(n_live, 4)) return KVQ_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256)) return KVQ_ERR_INVALID_ARG;
+  if (ws_bytes < kvq_compact_ws_bytes(cfg)) return KVQ_ERR_WORKSPACE;
+  return kvq_launch_pages_compact(cfg, cache, page_ref, n_live, workspace, d_status, (cudaStream_t)stream);
+}
+
 KVQ_API int kv_attn_decode_noalloc(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot,
                                    float* out, float sm_scale, int32_t max_ctx, int32_t* d_status, void* stream) {
   int rc = check_config(cfg);

@@ -77,6 +77,9 @@ struct AttnParams {
   // position seq_len[bc] - (cu_rows[bc + 1] - b).  nullptr: one decode query per sequence.
   const int32_t* cu_rows;
   int seqs;
+  // drafted trees (kv_attn_tree): parent node of every row, local to its sequence (-1: a root);
+  // the row then sees the tokens before the sequence's rows, its ancestors and itself.
+  const int32_t* parent;
 };
 
 // Cache sequence of grid row b (-1: a chunk row outside cu_rows).  cu_rows is a per-call input:
@@ -95,14 +98,29 @@ __device__ __forceinline__ int attn_seq(const AttnParams& P, int b) {
 
 // Length and INT2 edge that grid row b sees (after the dependency wait): a decode query sees
 // its sequence's seq_len tokens; a chunk query the tokens up to its own position.
-__device__ __forceinline__ void unit_state(const AttnParams& P, int b, int bc, int& L, int& sq) {
+// TREE: L0 is the sequence's length before its rows, which must all lie in the BF16 windows
+// (otherwise the row sees nothing and the fault is reported).
+template <bool TREE = false>
+__device__ __forceinline__ void unit_state(const AttnParams& P, int b, int bc, int& L, int& sq, int* L0 = nullptr) {
   if (bc < 0) {
     L = 0;
     sq = P.s_sink;
+    if (TREE) *L0 = 0;
     return;
   }
   L = P.seq_len[bc];
   sq = P.s_quant[bc];
+  if constexpr (TREE) {
+    const int n = __ldg(P.cu_rows + bc + 1) - __ldg(P.cu_rows + bc);
+    *L0 = L - n;
+    if (n > KVQ_TREE_MAX_NODES || *L0 < 0 || sq > max(*L0, P.s_sink)) {
+      L = 0;
+      *L0 = 0;
+      sq = P.s_sink;
+      set_status(P.status, KVQ_ERR_BOUNDS);
+      return;
+    }
+  }
   if (P.cu_rows) L = max(0, min(L, L - (__ldg(P.cu_rows + bc + 1) - b) + 1));
 }
 
@@ -311,7 +329,7 @@ __device__ __forceinline__ uint32_t dz_operand(uint32_t dz, bool odd) {
   return odd ? (lo & 0xffffu) : hi;
 }
 
-template <int NG, bool L2, bool KC>
+template <int NG, bool L2, bool KC, bool TREE>
 __device__ void int2_split(const AttnParams& P, uint8_t* smem, int b, int bc, int h, int split, float* res,
                            size_t wstride) {
   // accumulators per group; with one group the k-steps alternate between two accumulators so
@@ -379,8 +397,8 @@ __device__ void int2_split(const AttnParams& P, uint8_t* smem, int b, int bc, in
     const int pid = __shfl_sync(0xffffffffu, pid_a, k);
     if (lane == 0 && k < n_first) refill(k, pid);
   }
-  int Lraw, sqraw;
-  unit_state(P, b, bc, Lraw, sqraw);
+  int Lraw, sqraw, L0raw;
+  unit_state<TREE>(P, b, bc, Lraw, sqraw, &L0raw);
 
   // ---- this warp's pages inside the INT2 region
   const int L = Lraw;
@@ -857,12 +875,33 @@ __device__ void int2_split(const AttnParams& P, uint8_t* smem, int b, int bc, in
 }
 
 // ---- BF16 windows --------------------------------------------------------------------------
+template <bool TREE>
 __device__ void window_split(const AttnParams& P, int b, int bc, int h, int wsplit, float* res, size_t wstride) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = P.gqa;
   pdl_wait();
-  int L, sqw;
-  unit_state(P, b, bc, L, sqw);
+  int L, sqw, L0;
+  unit_state<TREE>(P, b, bc, L, sqw, &L0);
+  // TREE: bit i of seen: node i of the sequence is this row's ancestor or the row itself
+  uint32_t seen[KVQ_TREE_MAX_NODES / 32];
+  if constexpr (TREE) {
+#pragma unroll
+    for (int w = 0; w < KVQ_TREE_MAX_NODES / 32; ++w) seen[w] = 0u;
+    if (L > 0) {
+      const int first = __ldg(P.cu_rows + bc);
+      for (int at = b - first, step = 0; at >= 0 && step < KVQ_TREE_MAX_NODES; ++step) {
+#pragma unroll
+        for (int w = 0; w < KVQ_TREE_MAX_NODES / 32; ++w)
+          if ((at >> 5) == w) seen[w] |= 1u << (at & 31);
+        const int up = __ldg(P.parent + first + at);
+        if (up >= at || up < -1) {               // not a tree in index order
+          if (lane == 0) set_status(P.status, KVQ_ERR_BOUNDS);
+          break;
+        }
+        at = up;
+      }
+    }
+  }
   const int n_sink = min(P.s_sink, max(L, 0));
   const int r0 = max(min(sqw, L), P.s_sink);              // first recent token
   const int bcc = bc < 0 ? 0 : bc;                        // the cache rows (none read when L = 0)
@@ -921,7 +960,19 @@ __device__ void window_split(const AttnParams& P, int b, int bc, int h, int wspl
       vbase = P.ring_v + off;
       rows_avail = kPage;
     }
-    auto row_ok = [&](int t) { return tok0 + t >= lo && tok0 + t < hi; };
+    auto row_ok = [&](int t) {
+      bool ok = tok0 + t >= lo && tok0 + t < hi;
+      if constexpr (TREE) {
+        const int i = tok0 + t - L0;
+        if (ok && i >= 0) {
+          uint32_t word = 0u;
+#pragma unroll
+          for (int w = 0; w < KVQ_TREE_MAX_NODES / 32; ++w) word = (i >> 5) == w ? seen[w] : word;
+          ok = (word >> (i & 31)) & 1u;
+        }
+      }
+      return ok;
+    };
     auto row_ptr = [&](const uint16_t* base, int t) { return base + (size_t)(t < rows_avail ? t : 0) * kHeadDim; };
     // ---- scores (bf16 MMA): K rows tA, tB, channels 32*quad .. +32
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1088,7 +1139,7 @@ __device__ __noinline__ void merge_global(const float* src, int n, int g, void* 
 
 // One kernel per (groups per row, key norms, per-channel keys) variant, so that each launch's
 // code is only its own page loop (a short loop per warp is sensitive to instruction-fetch misses).
-template <int NG, bool L2, bool KC>
+template <int NG, bool L2, bool KC, bool TREE = false>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const __grid_constant__ AttnParams P) {
   extern __shared__ __align__(128) uint8_t smem[];
   pdl_trigger();
@@ -1106,10 +1157,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   size_t wstride;
   if (split < P.n_int2) {
     wstride = (size_t)kStages * P.page_bytes / sizeof(float);
-    int2_split<NG, L2, KC>(P, smem, b, bc, h, split, res, wstride);
+    int2_split<NG, L2, KC, TREE>(P, smem, b, bc, h, split, res, wstride);
   } else {
     wstride = (size_t)g * kRow;
-    window_split(P, b, bc, h, split - P.n_int2, res, wstride);
+    window_split<TREE>(P, b, bc, h, split - P.n_int2, res, wstride);
   }
   __syncthreads();
   // ---- CTA partial: merge the warps, store to the workspace
@@ -1270,8 +1321,10 @@ extern "C" size_t kvq_attn_ws_bytes(const kvq_config* cfg, int32_t max_ctx) {
 // with cu_rows over seqs sequences).
 static int launch_attn_impl(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot, void* out,
                             int out_bf16, float sm_scale, int32_t max_ctx, void* ws, int32_t* d_status,
-                            cudaStream_t stream, const int32_t* cu_rows, int seqs) {
+                            cudaStream_t stream, const int32_t* cu_rows, int seqs,
+                            const int32_t* parent = nullptr) {
   AttnParams P{};
+  P.parent = parent;
   P.cu_rows = cu_rows;
   P.seqs = seqs;
   P.pages = (const uint8_t*)cache->pages;
@@ -1312,26 +1365,28 @@ static int launch_attn_impl(const kvq_config* cfg, const kvq_cache* cache, const
   size_t smem = 1024 + (ring_bytes > res_bytes ? ring_bytes : res_bytes);
   if (P.merge1 && 1024 + merge_bytes > smem) smem = 1024 + merge_bytes;
   void (*kern)(const AttnParams) = nullptr;
-  const int vi = (ng == 1 ? 0 : ng == 2 ? 1 : 2) + (cfg->key_l2norm ? 3 : 0) + (cfg->key_axis ? 6 : 0);
-  if (cfg->key_axis == KVQ_KEY_PER_CHANNEL) {
+  const int vi = (ng == 1 ? 0 : ng == 2 ? 1 : 2) + (cfg->key_l2norm ? 3 : 0) + (cfg->key_axis ? 6 : 0) + (parent ? 12 : 0);
+  const auto pick = [&](auto tree) {
+    constexpr bool T = decltype(tree)::value;
+    if (cfg->key_axis == KVQ_KEY_PER_CHANNEL) {
+      if (cfg->key_l2norm)
+        return ng == 1 ? attn_decode_kernel<1, true, true, T> : ng == 2 ? attn_decode_kernel<2, true, true, T>
+                                                                       : attn_decode_kernel<4, true, true, T>;
+      return ng == 1 ? attn_decode_kernel<1, false, true, T> : ng == 2 ? attn_decode_kernel<2, false, true, T>
+                                                                      : attn_decode_kernel<4, false, true, T>;
+    }
     if (cfg->key_l2norm)
-      kern = ng == 1 ? attn_decode_kernel<1, true, true> : ng == 2 ? attn_decode_kernel<2, true, true>
-                                                                  : attn_decode_kernel<4, true, true>;
-    else
-      kern = ng == 1 ? attn_decode_kernel<1, false, true> : ng == 2 ? attn_decode_kernel<2, false, true>
-                                                                   : attn_decode_kernel<4, false, true>;
-  } else if (cfg->key_l2norm) {
-    kern = ng == 1 ? attn_decode_kernel<1, true, false> : ng == 2 ? attn_decode_kernel<2, true, false>
-                                                                 : attn_decode_kernel<4, true, false>;
-  } else {
-    kern = ng == 1 ? attn_decode_kernel<1, false, false> : ng == 2 ? attn_decode_kernel<2, false, false>
-                                                                  : attn_decode_kernel<4, false, false>;
-  }
+      return ng == 1 ? attn_decode_kernel<1, true, false, T> : ng == 2 ? attn_decode_kernel<2, true, false, T>
+                                                                      : attn_decode_kernel<4, true, false, T>;
+    return ng == 1 ? attn_decode_kernel<1, false, false, T> : ng == 2 ? attn_decode_kernel<2, false, false, T>
+                                                                     : attn_decode_kernel<4, false, false, T>;
+  };
+  kern = parent ? pick(std::true_type{}) : pick(std::false_type{});
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ERR_CUDA;
   // the dynamic shared-memory limit is raised once per (device, kernel variant)
   static std::mutex mu;
-  static unsigned long long attr_done[12] = {};
+  static unsigned long long attr_done[24] = {};
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!(attr_done[vi] & (1ull << dev))) {
@@ -1367,6 +1422,17 @@ extern "C" int kvq_launch_attn_chunk(const kvq_config* cfg, const kvq_cache* cac
   kvq_config c = *cfg;
   c.batch = n_rows;
   return launch_attn_impl(&c, cache, q_rot, out, 0, sm_scale, max_ctx, ws, d_status, stream, cu_rows, cfg->batch);
+}
+
+// Drafted trees: as chunk queries, with the rows' own tokens masked to each row's ancestors.
+extern "C" int kvq_launch_attn_tree_rows(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot,
+                                         const int32_t* cu_rows, const int32_t* parent, int32_t n_rows, uint16_t* out,
+                                         float sm_scale, int32_t max_ctx, void* ws, int32_t* d_status,
+                                         cudaStream_t stream) {
+  kvq_config c = *cfg;
+  c.batch = n_rows;
+  return launch_attn_impl(&c, cache, q_rot, out, 1, sm_scale, max_ctx, ws, d_status, stream, cu_rows, cfg->batch,
+                          parent);
 }
 
 // ---- allocation-free variant ---------------------------------------------------------------

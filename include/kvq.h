@@ -26,6 +26,14 @@
  *                   written as BF16 ([OScaR] "系统设计与 CUDA 实现", key-quant
  *                   kernel; [OSCAR] section 4 "KV Cache Update").
  *
+ * and, for speculative decoding and a shared page pool next to them,
+ *
+ *   kv_attn_tree, kv_verify_tree, kv_tree_commit
+ *                   attention of a tree of drafted tokens over the cache, the check of
+ *                   the drafts against the target's probabilities, and the rows kept.
+ *   kv_pages_reserve, kv_seq_fork, kv_seq_free, kv_pages_compact
+ *                   pages handed out, shared by sequences, given back and made dense.
+ *
  * Conventions shared by every call
  *   - Every pointer inside a struct or argument is a DEVICE pointer unless said
  *     otherwise; the structs themselves live in host memory and are read during
@@ -301,6 +309,120 @@ KVQ_API size_t kv_attn_chunk_workspace_bytes(const kvq_config* cfg, int32_t n_ro
 KVQ_API int kv_attn_chunk(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot,
                   const int32_t* cu_rows, int32_t n_rows, float* out, float sm_scale, int32_t max_ctx,
                   void* workspace, size_t ws_bytes, int32_t* d_status, void* stream);
+
+/* ---- speculative decoding ------------------------------------------------------
+ * A draft proposes a tree of tokens per sequence; the target model scores all of them in
+ * one pass and the longest path that survives its probabilities is kept.  One step:
+ *   kv_rotate_qk    the drafts' rows at positions seq_len + i (i = 0 .. n-1 in index order;
+ *                   RoPE, which the caller applies, uses a node's depth, the slot does not),
+ *                   and their queries
+ *   kv_attn_tree    every layer's attention
+ *   kv_verify_tree  from the target's probabilities at every node
+ *   kv_tree_commit  every layer's cache: the accepted rows stay, the others go
+ *   kv_quant_flush  as after any append
+ * No flush may run between the append and the commit: the drafts are BF16 rows of the window,
+ * so ring_cap must hold them as well.
+ *
+ * The tree: cu_rows [B + 1] as for kv_append_chunk; row cu_rows[b] + i is node i of sequence b;
+ * parent [n_rows] int32 holds each node's parent, local to its sequence and smaller than the
+ * node's own index, or -1 for a root.  At most KVQ_TREE_MAX_NODES nodes per sequence. */
+#define KVQ_TREE_MAX_NODES 128
+
+/* kv_attn_tree: attention of a tree of drafted tokens.
+ *   q_rot    [n_rows][Hq][d] bf16 compensated queries (kv_rotate_qk output)
+ *   cu_rows, parent: the tree (above); the nodes are the last n tokens of their sequence
+ *   out      [n_rows][Hq][d] bf16 (16-byte aligned): the float32 result rounded once
+ * Node i of sequence b, with L0 = seq_len[b] - n, attends to tokens [0, L0), to its ancestors
+ * (token L0 + j for node j) and to itself, as the cache holds them.  A chain (parent i - 1) gives
+ * kv_attn_chunk's result; several roots are allowed.  max_ctx, sm_scale as for kv_attn_decode
+ * (max_ctx counts the nodes); workspace of kv_attn_tree_workspace_bytes(cfg, n_rows, max_ctx)
+ * bytes, zero-filled before its first use (every call leaves its counters zero).  n_rows is at
+ * most 65535 (KVQ_ERR_UNSUPPORTED beyond).  KVQ_ERR_BOUNDS in *d_status, and zeros for the rows of
+ * a sequence whose nodes are more than KVQ_TREE_MAX_NODES or do not all lie in the BF16 windows; a
+ * node whose ancestors are not in index order is reported and sees those up to the fault.
+ * Source: [OSCAR] section 4 "Decoding Attention Kernel" (attention over the mixed cache);
+ * the tree of drafts has no counterpart on the pages. */
+KVQ_API size_t kv_attn_tree_workspace_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx);
+KVQ_API int kv_attn_tree(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot,
+                 const int32_t* cu_rows, const int32_t* parent, int32_t n_rows, uint16_t* out, float sm_scale,
+                 int32_t max_ctx, void* workspace, size_t ws_bytes, int32_t* d_status, void* stream);
+
+/* kv_verify_tree: which drafted tokens the target keeps, and the token after them (speculative
+ * sampling over a tree: the tokens kept are distributed as the target's).  Node 0 of every
+ * sequence is its only root: the token sampled last, which is kept always.
+ *   token    [n_rows] int32: the drafted tokens (node 0's is not read)
+ *   p        float32 rows of `vocab` target probabilities, p_stride elements apart: row r is the
+ *            distribution of the token after node r
+ *   q        float32 rows of the draft's probabilities likewise (row r: what r's children were
+ *            drawn from, independently of one another), or NULL when the drafts were not drawn
+ *            but chosen (the draft's best tokens): a miss then only rules its token out
+ *   u        [n_rows] float32 uniform numbers in [0, 1): node c > 0's decides node c; node 0's
+ *            draws the last token
+ *   path     [n_rows] int32 out: path[cu_rows[b] + j] for j < n_accept[b] are the kept nodes from
+ *            node 0 down (strictly increasing); -1 behind them
+ *   n_accept [B] int32 out: kept nodes, node 0 counted; 0 for a sequence without rows
+ *   next_token [B] int32 out: the token after the last kept node (-1: none)
+ * Walking down from node 0, the children of the current node are tried in index order: child c with
+ * token x is kept when u_c Z q(x) < r(x), where r = p and Z = 1 at first; a miss makes r the
+ * elementwise max(r - Z q, 0) and Z its sum (with q NULL: r(x) = 0, Z less by what it was).  When
+ * nothing is left of r (rounding), r is p again and no further child is tried.  The last token is the
+ * smallest x whose cumulative sum of r exceeds u_0 sum r.  Probabilities and numbers are taken in
+ * units of 2^-60 and products rounded down to them, so the result is the same on every run.
+ * Probabilities above 1 count as 1; negative or non-finite ones as 0, with KVQ_ERR_NONFINITE, as is a
+ * distribution whose sum is 0 or at least 4 (next_token -1).  A sequence whose rows are not such a
+ * tree, or whose tokens are not below vocab: KVQ_ERR_BOUNDS, n_accept 0, next_token -1.
+ * Of cfg only batch is used (at most 65535: KVQ_ERR_UNSUPPORTED). */
+KVQ_API int kv_verify_tree(const kvq_config* cfg, const int32_t* cu_rows, const int32_t* parent, const int32_t* token,
+                   int32_t n_rows, const float* p, int64_t p_stride, const float* q, int64_t q_stride, int32_t vocab,
+                   const float* u, int32_t* path, int32_t* n_accept, int32_t* next_token, int32_t* d_status,
+                   void* stream);
+
+/* kv_tree_commit: keep the rows of the accepted path.  For every sequence with n rows and
+ * L0 = seq_len - n, token L0 + j becomes the row of node path[cu_rows[b] + j] (j < n_accept[b]; path
+ * strictly increasing, as kv_verify_tree writes it) and seq_len becomes L0 + n_accept[b].  Rows move
+ * within the BF16 sink and ring.  A sequence whose path is not one, or whose nodes are not in the
+ * BF16 windows, is left as it is, with KVQ_ERR_BOUNDS.  Once per layer, on that layer's cache. */
+KVQ_API int kv_tree_commit(const kvq_config* cfg, const kvq_cache* cache, const int32_t* cu_rows, int32_t n_rows,
+                   const int32_t* path, const int32_t* n_accept, int32_t* d_status, void* stream);
+
+/* ---- the page pool ---------------------------------------------------------------
+ * page_ref [num_pages] int32: how many page-table entries hold each physical page (0: free).  The
+ * caller zeroes it once; tables filled by hand must be counted in it.  A sequence's entries are a
+ * prefix of its row of the table, -1 behind them.  Pages are handed out lowest id first, to
+ * sequences in order, so the tables do not depend on timing.  These calls write the page table
+ * (cache->page_table must be writable memory), and any call may follow them on the stream.  They
+ * run on the stream in order like any other, one pool at a time: two of them must not overlap on
+ * the same pool.  At most KVQ_POOL_MAX_SEQS sequences (pairs) per call (KVQ_ERR_UNSUPPORTED). */
+#define KVQ_POOL_MAX_SEQS 16384
+
+/* kv_pages_reserve: pages for n_tokens[b] (device int32 [B]) more tokens of every sequence, as if
+ * they were all quantized: its row then covers [s_sink, seq_len[b] + n_tokens[b]).  n_tokens[b] <= 0
+ * reserves nothing.  Sequences are served in order; from the first one on that the pool cannot
+ * serve, none gets any (KVQ_ERR_BOUNDS, as for one that would need more than max_pages_per_seq). */
+KVQ_API int kv_pages_reserve(const kvq_config* cfg, const kvq_cache* cache, int32_t* page_ref,
+                     const int32_t* n_tokens, int32_t* d_status, void* stream);
+
+/* kv_seq_fork: sequence dst[i] becomes a copy of sequence src[i] (device int32 [n]; one source may
+ * have many copies).  Whole INT2 pages are shared; the half-filled last one gets a page of its own;
+ * the live sink and ring rows are copied; pages that src holds beyond its INT2 region are not.  dst
+ * must hold nothing (a new sequence, or after kv_seq_free).  A pair is skipped with KVQ_ERR_BOUNDS when
+ * a sequence does not exist, dst holds something, is another pair's source or an earlier pair's
+ * destination, or when the pool has no page left for it or an earlier pair. */
+KVQ_API int kv_seq_fork(const kvq_config* cfg, const kvq_cache* cache, int32_t* page_ref, const int32_t* src,
+                const int32_t* dst, int32_t n, int32_t* d_status, void* stream);
+
+/* kv_seq_free: sequences seqs[0 .. n-1] (device int32) give up their pages (free once no other
+ * sequence holds them) and become empty (seq_len 0, s_quant s_sink).  Listing one twice is harmless. */
+KVQ_API int kv_seq_free(const kvq_config* cfg, const kvq_cache* cache, int32_t* page_ref, const int32_t* seqs,
+                int32_t n, int32_t* d_status, void* stream);
+
+/* kv_pages_compact: move pages so that the held ones are 0 .. n_live - 1 (n_live: device int32, out),
+ * and rename them in every table.  The k-th held page at or above n_live moves to the k-th free page
+ * below it, so nothing moves that need not.  The table must cover every sequence that uses the
+ * pool.  Workspace of kv_pages_compact_workspace_bytes(cfg) bytes. */
+KVQ_API size_t kv_pages_compact_workspace_bytes(const kvq_config* cfg);
+KVQ_API int kv_pages_compact(const kvq_config* cfg, const kvq_cache* cache, int32_t* page_ref, int32_t* n_live,
+                     void* workspace, size_t ws_bytes, int32_t* d_status, void* stream);
 
 /* kv_attn_decode: one decode step of GQA attention for every sequence.
  *   q_rot   [B][Hq][d] bf16 compensated queries (kv_rotate_qk output)

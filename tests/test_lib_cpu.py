@@ -158,3 +158,57 @@ def test_attn_chunk_validation(kvq):
     assert call(4096, None, 64, 4096, 4096, 1 << 40) == -1           # no cu_rows
     assert call(4096, 4096, 64, 4096, 4096, 16) == -7                # workspace too small
     assert call(4104, 4096, 64, 4096, 4096, 1 << 40) == -1           # misaligned queries
+
+
+def test_tree_and_pool_validation(kvq):
+    """Host checks of the drafted-tree and page-pool calls, before any launch."""
+    lib, c = kvq.lib(), _cfg(kvq).c()
+    fake = kvq.CCache(*([4096] * 9))
+    B, F = ctypes.byref, ctypes.c_float(0.1)
+    ws = lib.kv_attn_tree_workspace_bytes(B(c), 64, 4096)
+    assert ws > 0 and lib.kv_attn_tree_workspace_bytes(B(c), 65536, 4096) == 0
+    assert lib.kv_attn_tree_workspace_bytes(B(c), -1, 4096) == 0
+    tree = lambda q=4096, cu=4096, par=4096, n=64, out=4096, w=4096, nb=1 << 40, sc=F: lib.kv_attn_tree(  # noqa: E731
+        B(c), B(fake), q, cu, par, n, out, sc, 4096, w, nb, None, None)
+    assert tree(n=0, par=None, q=None, out=None, w=None) == 0
+    assert tree(n=70000) == -2
+    assert tree(cu=None) == -1 and tree(par=None) == -1 and tree(par=4097) == -1 and tree(n=-1) == -1
+    assert tree(q=4104) == -1 and tree(out=4104) == -1 and tree(sc=ctypes.c_float(float("nan"))) == -1
+    assert tree(w=4160) == -1 and tree(w=None) == -1 and tree(nb=16) == -7
+    ver = lambda cu=4096, par=4096, tok=4096, n=8, p=4096, ps=100, q=None, qs=0, v=100, u=4096, path=4096, acc=4096, nxt=4096, cc=c: (  # noqa: E731
+        lib.kv_verify_tree(B(cc), cu, par, tok, n, p, ps, q, qs, v, u, path, acc, nxt, None, None))
+    for bad in (dict(cu=None), dict(par=None), dict(tok=None), dict(n=-1), dict(p=None), dict(ps=99), dict(q=4096, qs=99), dict(v=0),
+                dict(u=None), dict(path=None), dict(acc=None), dict(nxt=None), dict(p=4098), dict(acc=4097)):
+        assert ver(**bad) == -1, bad
+    assert ver(cc=_cfg(kvq, batch=70000).c()) == -2
+    com = lambda cu=4096, n=8, path=4096, acc=4096, k=fake: lib.kv_tree_commit(B(c), B(k), cu, n, path, acc, None, None)  # noqa: E731
+    assert com(n=0) == 0
+    for bad in (dict(cu=None), dict(n=-1), dict(path=None), dict(acc=None), dict(acc=4097), dict(k=kvq.CCache())):
+        assert com(**bad) == -1, bad
+    big = _cfg(kvq, batch=20000).c()
+    assert lib.kv_pages_reserve(B(big), B(fake), 4096, 4096, None, None) == -2
+    assert lib.kv_pages_reserve(B(c), B(fake), None, 4096, None, None) == -1
+    assert lib.kv_pages_reserve(B(c), B(fake), 4096, None, None, None) == -1
+    assert lib.kv_seq_fork(B(c), B(fake), 4096, 4096, 4096, -1, None, None) == -1
+    assert lib.kv_seq_fork(B(c), B(fake), 4096, None, 4096, 1, None, None) == -1
+    assert lib.kv_seq_fork(B(c), B(fake), 4096, 4096, 4096, 20000, None, None) == -2
+    assert lib.kv_seq_fork(B(c), B(fake), 4096, None, None, 0, None, None) == 0
+    assert lib.kv_seq_free(B(c), B(fake), 4098, 4096, 1, None, None) == -1
+    assert lib.kv_seq_free(B(c), B(fake), 4096, None, 1, None, None) == -1
+    assert lib.kv_seq_free(B(c), B(fake), 4096, 4096, 20000, None, None) == -2
+    assert lib.kv_seq_free(B(c), B(fake), 4096, None, 0, None, None) == 0
+    need = lib.kv_pages_compact_workspace_bytes(B(c))
+    assert need >= 128 * 3 * 4
+    assert lib.kv_pages_compact(B(c), B(fake), 4096, 4096, 4096, need - 1, None, None) == -7
+    assert lib.kv_pages_compact(B(c), B(fake), 4096, None, 4096, need, None, None) == -1
+    assert lib.kv_pages_compact(B(c), B(fake), 4096, 4096, 4100, need, None, None) == -1
+
+
+def test_verify_rejects_rows_that_overlap(kvq):
+    import torch
+    one = torch.zeros(1, 50).expand(3, 50)              # three rows at one address
+    i = torch.zeros(3, dtype=torch.int32)
+    for p, q in ((one, None), (torch.zeros(3, 50), one), (torch.zeros(3, 50), torch.zeros(3, 49)),
+                 (torch.zeros(2, 50), None), (torch.zeros(3, 50).double(), None), (torch.zeros(50, 3).t(), None)):
+        with pytest.raises(kvq.KVQError):
+            kvq.kv_verify_tree(_cfg(kvq), i, i, i, p, q, torch.zeros(3), i, i, i, i)
