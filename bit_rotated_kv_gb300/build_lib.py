@@ -18,7 +18,7 @@ ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libkvq.so")
-SOURCES = ["api.cu", "rotate.cu", "rotate_tc.cu", "flush.cu", "attn.cu", "chunk.cu", "spec.cu", "pages.cu"]
+SOURCES = ["api.cu", "rotate.cu", "rotate_tc.cu", "flush.cu", "attn.cu", "chunk.cu", "tree.cu", "spec.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

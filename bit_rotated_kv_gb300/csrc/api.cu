@@ -195,7 +195,7 @@ KVQ_API int kv_attn_chunk(const kvq_config* cfg, const kvq_cache* cache, const u
 
 KVQ_API size_t kv_attn_tree_workspace_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
   if (check_config(cfg) != KVQ_OK || max_ctx < 0 || n_rows < 0 || n_rows > 65535) return 0;
-  return kvq_attn_chunk_ws_bytes(cfg, n_rows, max_ctx);
+  return kvq_attn_tree_ws_bytes(cfg, n_rows, max_ctx);
 }
 
 KVQ_API int kv_attn_tree(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot, const int32_t* cu_rows,
@@ -212,9 +212,9 @@ KVQ_API int kv_attn_tree(const kvq_config* cfg, const kvq_cache* cache, const ui
   if (!q_rot || !out || !aligned(q_rot, 16) || !aligned(out, 16)) return KVQ_ERR_INVALID_ARG;
   if (!(sm_scale == sm_scale)) return KVQ_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256)) return KVQ_ERR_INVALID_ARG;
-  if (ws_bytes < kvq_attn_chunk_ws_bytes(cfg, n_rows, max_ctx)) return KVQ_ERR_WORKSPACE;
-  return kvq_launch_attn_tree_rows(cfg, cache, q_rot, cu_rows, parent, n_rows, out, sm_scale, max_ctx, workspace,
-                                   d_status, (cudaStream_t)stream);
+  if (ws_bytes < kvq_attn_tree_ws_bytes(cfg, n_rows, max_ctx)) return KVQ_ERR_WORKSPACE;
+  return kvq_launch_attn_tree(cfg, cache, q_rot, cu_rows, parent, n_rows, out, sm_scale, max_ctx, workspace, d_status,
+                              (cudaStream_t)stream);
 }
 
 KVQ_API int kv_verify_tree(const kvq_config* cfg, const int32_t* cu_rows, const int32_t* parent, const int32_t* token,

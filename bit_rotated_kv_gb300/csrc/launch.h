@@ -25,6 +25,10 @@ size_t kvq_attn_chunk_ws_bytes(const kvq_config* cfg, int32_t n_rows, int32_t ma
 int kvq_launch_attn_tree_rows(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot,
                               const int32_t* cu_rows, const int32_t* parent, int32_t n_rows, uint16_t* out,
                               float sm_scale, int32_t max_ctx, void* ws, int32_t* d_status, cudaStream_t stream);
+size_t kvq_attn_tree_ws_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx);
+int kvq_launch_attn_tree(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot, const int32_t* cu_rows,
+                         const int32_t* parent, int32_t n_rows, uint16_t* out, float sm_scale, int32_t max_ctx,
+                         void* ws, int32_t* d_status, cudaStream_t stream);
 int kvq_launch_verify_tree(const kvq_config* cfg, const int32_t* cu_rows, const int32_t* parent, const int32_t* token,
                            int32_t n_rows, const float* p, int64_t p_stride, const float* q, int64_t q_stride,
                            int32_t vocab, const float* u, int32_t* path, int32_t* n_accept, int32_t* next_token,

@@ -1,0 +1,1180 @@
+// kv_attn_tree on the tensor cores: the nodes of a drafted tree attend together, so that a
+// sequence's cache is read and its codes are expanded once for all of them.
+//
+// The mathematics.  For the rows n of one (sequence, kv head) -- a row is a (node, query head of
+// the kv head) pair -- and its tokens t:  s[t][n] = scale k_t.q_n,  o_n = sum_t 2^(s - m_n) v_t /
+// sum_t 2^(s - m_n), one pass over the tokens with a running reference m_n.
+//
+// Tile and layout.  A tile is 128 tokens (8 INT2 pages, or 128 BF16 window rows) by N = 64 or 128
+// rows.  Tokens are the tensor core's M: S^T [128 tokens x N] = K [128 x d] Q^T, and
+// O^T [128 channels x N] += V^T [128 channels x 128 tokens] P [128 x N], so
+//   * the expanded K and V^T are the A operands and live in TMEM: a page's codes are stored in the
+//     fragment order of a 16-row MMA, which is the order of tcgen05.st.16x128b -- one 16-byte load
+//     and one AND per two codes puts a page's keys into TMEM, without a pass through shared memory;
+//   * a lane of S^T is a token, so a token's scale (Delta, norm) is one number per thread, and a
+//     warp reads no scale per score;
+//   * P [token][row] goes to shared memory as the MN-major B operand, 16 bytes per 8 rows.
+// Keys.  With one group per row (G = 128) A holds the codes themselves, exact, and the zero point is
+// one more K = 16 step (z against -sum q', hi + lo); Delta multiplies the finished sum.  With more
+// groups A holds Delta c as an exact fp16 hi + lo pair (13 bits), scaled by a power of two per token.
+// q' is scaled by one power of two per CTA (exact unless a row's largest value is 2^22 below
+// another's).  Values are dequantized to fp16, Delta (c - z) in one rounding (relative 2^-11 of the
+// value and of Delta z: the output's own rounding to bf16 is 2^-8).  P is rounded to fp16, the sums l
+// are fp32.  Window rows are bf16 as they are, with P as a bf16 hi + lo pair.
+//
+// Softmax reference.  m_n moves only when a score passes it by 8 (in log2): P <= 2^8.  The four
+// warps that share a row's tokens agree by one barrier with an OR; a move rescales O in TMEM.
+//
+// Roles: 8 softmax warps (4 lane quadrants x 2 halves of the rows), 4 warps that expand codes (or
+// load window rows), one that issues the MMAs, one that streams pages (1-D bulk copies).  The tensor
+// pipe runs QK(i), PV(i-1), QK(i+1), ... while softmax(i) runs beside PV(i-1).
+//
+// What bounds it: an MMA whose A comes from TMEM takes about 67 clocks for any N <= 128 (17 to 25 of
+// them a tile), so small trees are bound by the tensor pipe's issue, wide ones by its rate.
+//
+// Several CTAs share a long sequence (splits over tiles); their partial (m, l, o) are merged by a
+// second kernel, one warp per output row.
+#include "common.cuh"
+#include "launch.h"
+
+#include <cstddef>
+#include <mutex>
+
+namespace kvq {
+namespace {
+
+constexpr int kNodes = KVQ_TREE_MAX_NODES;
+constexpr int kNodeWords = kNodes / 32;
+constexpr int kTile = 128;                       // tokens of a tile
+constexpr int kTilePages = kTile / kPage;
+constexpr int kSmWarps = 8, kDqWarps = 4;
+constexpr int kThreadsT = 32 * (kSmWarps + kDqWarps + 2);
+constexpr int kRec = 4 + kHeadDim;               // (m, l, -, -, o[d]) of a partial
+constexpr long long kSpin = 1LL << 19;          // try_wait rounds before a wait gives up
+constexpr uint32_t kTmem = 512;
+constexpr int kSlab = kTile * 128;               // 128 tokens x 64 16-bit values, 128-byte swizzled
+
+struct TreeParams {
+  const uint8_t* pages;
+  const int32_t* page_table;
+  const int32_t* seq_len;
+  const int32_t* s_quant;
+  const uint16_t* sink_k;
+  const uint16_t* sink_v;
+  const uint16_t* ring_k;
+  const uint16_t* ring_v;
+  const uint16_t* q;
+  const int32_t* cu_rows;
+  const int32_t* parent;
+  uint16_t* out;
+  float* part;           // [n_rows][Hq][splits][kRec]
+  int32_t* status;
+  int batch, hkv, gqa, gqa_log2, s_sink, ring_cap, max_pages, num_pages, page_bytes, l2;
+  int n_rows, splits, mp;
+  float scale_log2;
+};
+
+// ---- primitives --------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint64_t* b, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(saddr(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// bounded wait that also gives up when another warp has
+__device__ __noinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, volatile int* gave_up) {
+  for (long long i = 0; i < kSpin; ++i) {
+    if (bar_try(b, parity)) return true;
+    if (*gave_up) return false;
+  }
+  *gave_up = 1;
+  return false;
+}
+__device__ __forceinline__ bool bar_wait(uint64_t* b, int phase, volatile int* gave_up) {
+  return bar_try(b, (uint32_t)(phase & 1)) || bar_wait_slow(b, (uint32_t)(phase & 1), gave_up);
+}
+// the same for a whole warp, decided by lane 0 (the warp stays together)
+__device__ __forceinline__ bool warp_wait(uint64_t* b, int phase, volatile int* gave_up) {
+  if (__all_sync(0xffffffffu, bar_try(b, (uint32_t)(phase & 1)))) return true;
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = bar_wait_slow(b, (uint32_t)(phase & 1), gave_up) ? 1 : 0;
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  __syncwarp();
+  return ok != 0;
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(saddr(dst)),
+      "l"(src), "r"(bytes), "r"(saddr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// barrier of the 128 threads of one half's four softmax warps, with an OR of a predicate
+__device__ __forceinline__ bool half_or(int half, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(1 + half)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void half_sync(int half) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory"); }
+__device__ __forceinline__ void dq_sync() { asm volatile("barrier.cta.sync 3, 128;" ::: "memory"); }
+
+// shared-memory matrix descriptors, 128-byte swizzle (8 rows of 128 bytes, groups 1024 apart)
+__device__ __forceinline__ uint64_t desc_k128(uint32_t a) {                 // K-major
+  return (uint64_t)((a & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn128(uint32_t a) {                // MN-major, 64-element blocks kSlab apart
+  return (uint64_t)((a & 0x3FFFFu) >> 4) | ((uint64_t)(kSlab >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// K-major without swizzle, K = 16: 8 x 16-byte core matrices, 128 apart along the rows and
+// `lead` apart along K
+__device__ __forceinline__ uint64_t desc_plain(uint32_t a, uint32_t lead) {
+  return (uint64_t)((a & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+               "r"(a), "l"(b), "r"(idesc), "r"(acc)
+               : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+               "l"(a), "l"(b), "r"(idesc), "r"(acc)
+               : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)) : "memory");
+}
+#define KVQ_IO8(c, b) c(v[b]), c(v[b + 1]), c(v[b + 2]), c(v[b + 3]), c(v[b + 4]), c(v[b + 5]), c(v[b + 6]), c(v[b + 7])
+__device__ __forceinline__ void tm_ld32(uint32_t a, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : KVQ_IO8("=f", 0), KVQ_IO8("=f", 8), KVQ_IO8("=f", 16), KVQ_IO8("=f", 24)
+      : "r"(a));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : KVQ_IO8("+f", 0), KVQ_IO8("+f", 8), KVQ_IO8("+f", 16), KVQ_IO8("+f", 24)::"memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t a, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::KVQ_IO8("f", 0), KVQ_IO8("f", 8), KVQ_IO8("f", 16),
+      KVQ_IO8("f", 24), "r"(a)
+      : "memory");
+}
+// 16 lanes x 64 columns: registers 4 s .. 4 s + 3 are the A fragment of k-step s
+__device__ __forceinline__ void tm_st_frag16(uint32_t a, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::KVQ_IO8("r", 0), KVQ_IO8("r", 8), KVQ_IO8("r", 16),
+      KVQ_IO8("r", 24), "r"(a)
+      : "memory");
+}
+// 16 lanes x 8 columns: the A fragment of one k-step
+__device__ __forceinline__ void tm_st_frag2(uint32_t a, const uint32_t (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%4], {%0,%1,%2,%3};" ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t h2bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 bits2h(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+__device__ __forceinline__ uint32_t pack16(float a, float b) { return h2bits(__floats2half2_rn(a, b)); }
+__device__ __forceinline__ uint32_t packb16(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ uint4 lds16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ int slot_pow(int s) { return s <= 4 ? s : s - 5; }
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t w10, int s) {
+  return s <= 4 ? (w & (0x00030003u << (2 * s))) : (w10 & (0x00030003u << (2 * (s - 5))));
+}
+// Reduce 32 values per lane over the warp's lanes; lane j returns value j's result.
+template <class F>
+__device__ __forceinline__ float reduce_columns(float (&x)[32], int lane, F f) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int j = 0; j < o; ++j) {
+      const float mine = up ? x[j + o] : x[j], other = up ? x[j] : x[j + o];
+      x[j] = f(mine, __shfl_xor_sync(0xffffffffu, other, o));
+    }
+  }
+  return x[0];
+}
+
+// A sequence's rows as the kernels see them.
+struct SeqState {
+  int first, n;          // rows first .. first + n - 1
+  int len, edge, L0;     // length, INT2 edge, length before the drafts
+  bool bad;              // no tree, or its nodes are not in the BF16 windows
+};
+__device__ __forceinline__ SeqState seq_state(const TreeParams& P, int b) {
+  SeqState s;
+  s.first = P.cu_rows[b];
+  s.n = P.cu_rows[b + 1] - s.first;
+  s.len = P.seq_len[b];
+  s.edge = P.s_quant[b];
+  s.L0 = s.len - s.n;
+  s.bad = s.first < 0 || s.n > P.n_rows || s.first > P.n_rows - max(s.n, 0) || s.n > kNodes || s.L0 < 0 ||
+          s.edge > max(s.L0, P.s_sink);
+  return s;
+}
+
+// Row tiles a sequence takes (a bad one: one, which reports it).
+template <int N>
+__device__ __forceinline__ int row_tiles(const TreeParams& P, int b) {
+  const long long n = (long long)P.cu_rows[b + 1] - P.cu_rows[b];
+  if (n <= 0) return 0;
+  return n > kNodes ? 1 : (int)((n * P.gqa + N - 1) / N);
+}
+
+template <int N>
+struct Layout {          // dynamic shared memory, from a 1024-byte boundary
+  static constexpr int kQ = 0;                              // q' fp16, K-major: two slabs of N x 128 B
+  static constexpr int kQb = kQ + 2 * N * 128;              // q' bf16 likewise
+  static constexpr int kP = kQb + 2 * N * 128;              // P, two buffers of N / 64 slabs
+  static constexpr int kPBytes = N / 64 * kSlab;
+  static constexpr int kK = kP + 2 * kPBytes;               // window K rows, two slabs
+  static constexpr int kV = kK + 2 * kSlab;
+  static constexpr int kZ = kV + 2 * kSlab;                 // zero-point B operand: N x 16 fp16
+  static constexpr int kPages = kZ + N * 32;                // two stages of 8 pages
+};
+
+template <int N>
+struct TreeShared {
+  __align__(16) uint64_t page_full[2], page_free[2], k_full, v_full, s_full, s_free, p_full[2], pv_done[2];
+  uint32_t tmem;
+  int gave_up;
+  int item[3];                     // sequence, row tile, found
+  int pid[2][kTilePages];
+  float lane_scale[2][kTile];
+  uint32_t alive[2][4];            // tokens of a tile that exist, by lane quadrant
+  __align__(16) float neg_m[N];    // minus the reference of every row
+  __align__(16) float alpha[N];
+  float red[4][N];                 // per-quadrant maxima; at the end the sums
+  uint32_t seen[kNodes][kNodeWords];   // ancestors of every node, itself among them
+  float amax[kThreadsT / 32];
+};
+struct Doubling {                  // of the ancestors, at set-up (where the pages go afterwards)
+  int jump[2][kNodes];
+  uint32_t seen[kNodes][kNodeWords];
+};
+
+static_assert(offsetof(TreeShared<128>, neg_m) % 16 == 0 && offsetof(TreeShared<128>, alpha) % 16 == 0 &&
+                  offsetof(TreeShared<64>, neg_m) % 16 == 0 && offsetof(TreeShared<64>, alpha) % 16 == 0 &&
+                  Layout<64>::kPages % 1024 == 0 && Layout<128>::kPages % 1024 == 0, "vector loads");
+static_assert(Layout<128>::kPages + 2 * kTilePages * 1568 + sizeof(TreeShared<128>) <= 227 * 1024, "shared memory of an SM");
+
+template <int N, int NG>
+__global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_constant__ TreeParams P) {
+  using L = Layout<N>;
+  constexpr int kCols = N / 2;                              // rows of a softmax warp
+  constexpr int kChunks = kCols / 32;
+  constexpr int kKCols = NG == 1 ? 64 : 128;                // TMEM columns of the key operand, then 8 for zero points
+  constexpr uint32_t kColO = N, kColK = 2 * N, kColV = 2 * N + 144;
+  constexpr uint32_t kIdescF16 = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
+  constexpr uint32_t kIdescPV = kIdescF16 | (1u << 16);
+  constexpr uint32_t kIdescB16 = kIdescF16 | (1u << 7) | (1u << 10);
+  constexpr uint32_t kIdescB16PV = kIdescB16 | (1u << 15) | (1u << 16);
+  extern __shared__ __align__(1024) uint8_t sm[];           // (all of the shared memory: it starts aligned)
+  TreeShared<N>& S = *reinterpret_cast<TreeShared<N>*>(sm + L::kPages + 2 * kTilePages * P.page_bytes);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  volatile int* gave_up = &S.gave_up;
+  pdl_trigger();
+  pdl_wait();
+  if (saddr(sm) & 1023u) {                                  // (the swizzled operands need it)
+    if (tid == 0) set_status(P.status, KVQ_ERR_CUDA);
+    return;
+  }
+
+  // ---- this CTA's row tile: item blockIdx.x counts the sequences' row tiles in order
+  const int split = blockIdx.z, h = blockIdx.y;
+  if (tid == 0) {
+    S.item[2] = 0;
+    S.gave_up = 0;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int before = 0;
+    for (int b0 = 0; b0 < P.batch; b0 += 32) {
+      const int mine = b0 + lane < P.batch ? row_tiles<N>(P, b0 + lane) : 0;
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += t;
+      }
+      const int start = before + upto - mine;
+      if ((int)blockIdx.x >= start && (int)blockIdx.x < start + mine) {
+        S.item[0] = b0 + lane;
+        S.item[1] = blockIdx.x - start;
+        S.item[2] = 1;
+      }
+      before += __shfl_sync(0xffffffffu, upto, 31);
+      if (before > (int)blockIdx.x) break;
+    }
+    if (lane == 0 && blockIdx.x == 0 && h == 0 && split == 0 &&
+        (P.cu_rows[0] != 0 || P.cu_rows[P.batch] != P.n_rows))
+      set_status(P.status, KVQ_ERR_BOUNDS);
+  }
+  __syncthreads();
+  if (!S.item[2]) return;
+  const int b = S.item[0];
+  const SeqState st = seq_state(P, b);
+  const int row0 = S.item[1] * N;
+  const int ncol = min(N, st.n * P.gqa - row0);
+  // global row and query head of column c
+  auto out_row = [&](int c) {
+    const int r = row0 + c;
+    return (size_t)(st.first + (r >> P.gqa_log2)) * (P.hkv * P.gqa) + h * P.gqa + (r & (P.gqa - 1));
+  };
+  if (st.bad) {                                             // zeros (the merge writes them when there are splits)
+    if (tid == 0) set_status(P.status, KVQ_ERR_BOUNDS);
+    if (P.splits == 1 && st.first >= 0)
+      for (long long i = tid; i < (long long)st.n * P.gqa * kHeadDim; i += kThreadsT) {
+        const long long r = i / (P.gqa * kHeadDim);
+        if (st.first + r < P.n_rows)
+          P.out[((size_t)(st.first + r) * P.hkv * P.gqa + h * P.gqa) * kHeadDim + i % (P.gqa * kHeadDim)] = 0;
+      }
+    return;
+  }
+
+  // ---- tiles: window rows (sink, then ring) first, then pages
+  const int edge = min(st.edge, st.len);
+  const int n_sink = min(P.s_sink, st.len), ring0 = max(edge, P.s_sink);
+  const int n_win = n_sink + max(0, st.len - ring0);
+  const int n_tok = max(0, edge - P.s_sink);
+  int np = (n_tok + kPage - 1) / kPage;
+  if (np > P.mp) {
+    if (tid == 0 && split == 0) set_status(P.status, KVQ_ERR_BOUNDS);
+    np = P.mp;
+  }
+  const int nw = (n_win + kTile - 1) / kTile, ni = (np + kTilePages - 1) / kTilePages;
+  const int t0 = (int)((long long)(nw + ni) * split / P.splits), t1 = (int)((long long)(nw + ni) * (split + 1) / P.splits);
+  const int nt = t1 - t0;
+
+  // ---- set-up: barriers, TMEM, q' operands, ancestors
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&S.page_full[i], 1);
+      bar_init(&S.page_free[i], kDqWarps);
+      bar_init(&S.p_full[i], kSmWarps);
+      bar_init(&S.pv_done[i], 1);
+    }
+    bar_init(&S.k_full, kDqWarps);
+    bar_init(&S.v_full, kDqWarps);
+    bar_init(&S.s_full, 1);
+    bar_init(&S.s_free, kSmWarps);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&S.tmem)), "r"(kTmem) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  for (int c = tid; c < N; c += kThreadsT) S.neg_m[c] = 1e30f;
+  // bf16 rows: 16-byte chunk j of row c at slab j / 8, swizzled
+  float amax = 0.f;
+  for (int i = tid; i < N * 16; i += kThreadsT) {
+    const int c = i >> 4, j = i & 15;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (c < ncol) v = reinterpret_cast<const uint4*>(P.q + out_row(c) * kHeadDim)[j];
+    *reinterpret_cast<uint4*>(sm + L::kQb + (j >> 3) * N * 128 + (c >> 3) * 1024 + (c & 7) * 128 + (((j & 7) ^ (c & 7)) << 4)) = v;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      amax = fmaxf(amax, fabsf(__uint_as_float(w[k] << 16)));
+      amax = fmaxf(amax, fabsf(__uint_as_float(w[k] & 0xffff0000u)));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (lane == 0) S.amax[warp] = amax;
+  // parents, checked; ancestors by doubling (warps 8 .. 11: one thread a node)
+  if (warp >= kSmWarps && warp < kSmWarps + kDqWarps) {
+    const int i = tid - 32 * kSmWarps;
+    int up = -1;
+    if (i < st.n) {
+      up = P.parent[st.first + i];
+      if (up >= i || up < -1) {
+        set_status(P.status, KVQ_ERR_BOUNDS);
+        up = -1;
+      }
+    }
+    Doubling& D = *reinterpret_cast<Doubling*>(sm + L::kPages);
+    uint32_t mine[kNodeWords];
+#pragma unroll
+    for (int w = 0; w < kNodeWords; ++w) mine[w] = (i >> 5) == w ? 1u << (i & 31) : 0u;
+    // after round r: the 2^r nearest ancestors (itself counted), and where the next one is
+#pragma unroll 1
+    for (int r = 0; (1 << r) <= kNodes; ++r) {
+      uint32_t(*dst)[kNodeWords] = r & 1 ? D.seen : S.seen;
+#pragma unroll
+      for (int w = 0; w < kNodeWords; ++w) dst[i][w] = mine[w];
+      D.jump[r & 1][i] = up;
+      dq_sync();
+      if ((1 << r) == kNodes) break;
+      if (up >= 0) {
+#pragma unroll
+        for (int w = 0; w < kNodeWords; ++w) mine[w] |= dst[up][w];
+        up = D.jump[r & 1][up];
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < kNodeWords; ++w) S.seen[i][w] = mine[w];
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tb = S.tmem;
+  int sigma = 0;
+  {
+    float a = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreadsT / 32; ++w) a = fmaxf(a, S.amax[w]);
+    if (a > 0.f && a < INFINITY) {
+      int e2;
+      frexpf(a, &e2);
+      sigma = 14 - e2;                                      // a 2^sigma < 2^14
+    }
+  }
+  // fp16 rows, channel slot s scaled by 4^-s for the codes that carry 4^s
+  for (int i = tid; i < N * 16; i += kThreadsT) {
+    const int c = i >> 4, j = i & 15;
+    const uint32_t off = (j >> 3) * N * 128 + (c >> 3) * 1024 + (c & 7) * 128 + (((j & 7) ^ (c & 7)) << 4);
+    const uint4 v = lds16(sm + L::kQb + off);
+    const float f = ldexpf(1.f, sigma - 2 * slot_pow(j >> 1));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = pack16(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
+    *reinterpret_cast<uint4*>(sm + L::kQ + off) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  // zero-point operand, row c: slots 2 g, 2 g + 1: -sum of group g (hi), slot 8 + 2 g: its lo
+  for (int c = tid; c < N; c += kThreadsT) {
+    uint32_t z[8];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float acc = 0.f;
+      if (g < NG)
+        for (int j = g * (16 / NG); j < (g + 1) * (16 / NG); ++j) {
+          const uint4 v = lds16(sm + L::kQb + (j >> 3) * N * 128 + (c >> 3) * 1024 + (c & 7) * 128 + (((j & 7) ^ (c & 7)) << 4));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc += __uint_as_float(w[k] << 16) + __uint_as_float(w[k] & 0xffff0000u);
+        }
+      const float v = -acc * ldexpf(1.f, NG == 1 ? sigma - 19 : sigma - 16);
+      const float hi = __half2float(__float2half_rn(v));
+      z[g] = pack16(hi, hi);
+      z[4 + g] = pack16(v - hi, 0.f);
+    }
+    *reinterpret_cast<uint4*>(sm + L::kZ + (c >> 3) * 128 + (c & 7) * 16) = make_uint4(z[0], z[1], z[2], z[3]);
+    *reinterpret_cast<uint4*>(sm + L::kZ + N * 16 + (c >> 3) * 128 + (c & 7) * 16) = make_uint4(z[4], z[5], z[6], z[7]);
+  }
+  fence_async();
+  __syncthreads();
+
+  const int pb = P.page_bytes;
+  uint8_t* stages = sm + L::kPages;
+  if (warp == kSmWarps + kDqWarps + 1) {
+    // ---- pages
+    const int32_t* tab = P.page_table + (size_t)b * P.max_pages;
+    int k = 0;                                              // page tiles streamed
+    for (int i = 0; i < nt; ++i) {
+      if (t0 + i < nw) continue;
+      const int stage = k & 1;
+      if (k >= 2) {
+        if (!warp_wait(&S.page_free[stage], (k >> 1) - 1, gave_up)) break;
+      }
+      const int p = (t0 + i - nw) * kTilePages + lane;
+      int pid = -1;
+      if (lane < kTilePages && p < np) {
+        pid = p < P.max_pages ? tab[p] : -1;
+        if ((unsigned)pid >= (unsigned)P.num_pages) {
+          pid = -1;
+          set_status(P.status, KVQ_ERR_BOUNDS);
+        }
+      }
+      if (lane < kTilePages) S.pid[stage][lane] = pid;
+      const int live = __popc(__ballot_sync(0xffffffffu, pid >= 0));
+      if (lane == 0) {
+        if (live) bar_expect(&S.page_full[stage], (uint32_t)(live * pb));
+        else bar_arrive(&S.page_full[stage]);
+      }
+      __syncwarp();
+      if (pid >= 0)
+        bulk_load(stages + (size_t)(stage * kTilePages + lane) * pb, P.pages + ((size_t)pid * P.hkv + h) * pb, (uint32_t)pb,
+                  &S.page_full[stage]);
+      ++k;
+    }
+    if (*gave_up)                                           // copies in flight land before the CTA can end
+      for (int j = max(0, k - 2); j < k; ++j)
+        for (long long it = 0; it < kSpin && !bar_try(&S.page_full[j & 1], (uint32_t)((j >> 1) & 1)); ++it) {
+        }
+  } else if (warp == kSmWarps + kDqWarps) {
+    // ---- MMA issue
+    if (lane == 0) {
+      int done = -1;                                        // last committed PV
+      int qk = -1;
+      auto pv = [&](int i) {
+        if (!bar_wait(&S.p_full[i & 1], i >> 1, gave_up) || !bar_wait(&S.v_full, i, gave_up)) return false;
+        fence_after();
+        if (t0 + i < nw) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint64_t a = desc_mn128(saddr(sm + L::kV) + kk * 2048);
+            mma_ss(tb + kColO, a, desc_mn128(saddr(sm + L::kP) + kk * 2048), kIdescB16PV, i > 0 || kk > 0);
+            mma_ss(tb + kColO, a, desc_mn128(saddr(sm + L::kP + L::kPBytes) + kk * 2048), kIdescB16PV, 1u);
+          }
+        } else {
+          const uint32_t p = saddr(sm + L::kP + (i & 1) * L::kPBytes);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) mma_ts(tb + kColO, tb + kColV + 8 * kk, desc_mn128(p + kk * 2048), kIdescPV, i > 0 || kk > 0);
+        }
+        mma_commit(&S.pv_done[i & 1]);
+        done = i;
+        return true;
+      };
+      for (int i = 0; i < nt; ++i) {
+        if (!bar_wait(&S.k_full, i, gave_up)) break;
+        if (i > 0 && !bar_wait(&S.s_free, i - 1, gave_up)) break;
+        fence_after();
+        if (t0 + i < nw) {
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            mma_ss(tb, desc_k128(saddr(sm + L::kK) + (s >> 2) * kSlab + (s & 3) * 32),
+                   desc_k128(saddr(sm + L::kQb) + (s >> 2) * N * 128 + (s & 3) * 32), kIdescB16, s > 0);
+        } else {
+#pragma unroll
+          for (int s = 0; s < 8; ++s) {
+            const uint64_t q = desc_k128(saddr(sm + L::kQ) + (s >> 2) * N * 128 + (s & 3) * 32);
+            mma_ts(tb, tb + kColK + 8 * s, q, kIdescF16, s > 0);
+            if (NG > 1) mma_ts(tb, tb + kColK + 64 + 8 * s, q, kIdescF16, 1u);
+          }
+          mma_ts(tb, tb + kColK + kKCols, desc_plain(saddr(sm + L::kZ), N * 16), kIdescF16, 1u);
+        }
+        mma_commit(&S.s_full);
+        qk = i;
+        if (i > 0 && !pv(i - 1)) break;
+      }
+      if (nt > 0 && !*gave_up) (void)pv(nt - 1);
+      if (*gave_up) {                                       // what was issued ends before TMEM is given back
+        for (long long it = 0; it < kSpin && qk >= 0 && !bar_try(&S.s_full, (uint32_t)(qk & 1)); ++it) {
+        }
+        for (long long it = 0; it < kSpin && done >= 0 && !bar_try(&S.pv_done[done & 1], (uint32_t)((done >> 1) & 1)); ++it) {
+        }
+      }
+    }
+  } else if (warp >= kSmWarps) {
+    // ---- operands of a tile: lane quadrant q of TMEM (keys: tokens 32 q .. of the tile; values:
+    // channels 32 q ..)
+    const int q = warp - kSmWarps;
+    const uint32_t tq = tb + ((uint32_t)(32 * q) << 16);
+    const int row = lane >> 2, quad = lane & 3;
+    const float cmul = P.scale_log2 * ldexpf(1.f, 24 - sigma);
+    // value codes of channels 32 q + 16 j ..: slot m = 2 q + j
+    uint32_t vmask[2], vone[2];
+    int vshift[2];
+    __half2 vsub[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int m = 2 * q + j, s = slot_pow(m);
+      vshift[j] = m <= 4 ? 0 : 10;
+      vmask[j] = 0x00030003u << (2 * s);
+      vone[j] = (uint32_t)(25 - 2 * s) << 10;               // 2^(10 - 2 s): the code's bits then count ones
+      vone[j] |= vone[j] << 16;
+      vsub[j] = bits2h(vone[j]);
+    }
+    const int vg = 32 * q / (kHeadDim / NG);                // the group of these channels
+    int k = 0;
+    for (int i = 0; i < nt; ++i) {
+      if (t0 + i < nw) {
+        // window rows: token w of the window at slab-swizzled row w; 16 lanes a row, 16 bytes each
+        const int w0 = (t0 + i) * kTile;
+        const int t = tid - 32 * kSmWarps;
+        S.lane_scale[i & 1][t] = P.scale_log2;
+        const unsigned alive = __ballot_sync(0xffffffffu, w0 + t < n_win);
+        if (lane == 0) S.alive[i & 1][q] = alive;
+        bool ok = true;
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {
+          // keys once QK(i - 1) has read the last ones, values once PV(i - 1) has (it comes after QK(i))
+          if (i > 0) ok = side ? warp_wait(&S.pv_done[(i - 1) & 1], (i - 1) >> 1, gave_up) : warp_wait(&S.s_full, i - 1, gave_up);
+          if (!ok) break;
+          const uint16_t* sink = side ? P.sink_v : P.sink_k;
+          const uint16_t* ring = side ? P.ring_v : P.ring_k;
+          uint8_t* dst = sm + (side ? L::kV : L::kK);
+          const int j = t & 15;
+#pragma unroll 8
+          for (int r = t >> 4; r < kTile; r += 8) {
+            const int w = w0 + r;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (w < n_win) {
+              const int tok = w < n_sink ? w : ring0 + w - n_sink;
+              const uint16_t* src = w < n_sink ? sink + (((size_t)b * P.hkv + h) * P.s_sink + tok) * kHeadDim
+                                               : ring + (((size_t)b * P.hkv + h) * P.ring_cap + tok % P.ring_cap) * kHeadDim;
+              v = reinterpret_cast<const uint4*>(src)[j];
+            }
+            *reinterpret_cast<uint4*>(dst + (j >> 3) * kSlab + (r >> 3) * 1024 + (r & 7) * 128 + (((j & 7) ^ (r & 7)) << 4)) = v;
+          }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) bar_arrive(side ? &S.v_full : &S.k_full);
+        }
+        if (!ok) break;
+        continue;
+      }
+      const int stage = k & 1;
+      const int page0 = (t0 + i - nw) * kTilePages;
+      if (!warp_wait(&S.page_full[stage], k >> 1, gave_up)) break;
+      if (i > 0 && !warp_wait(&S.s_full, i - 1, gave_up)) break;
+      fence_after();
+      const uint8_t* base = stages + (size_t)stage * kTilePages * pb;
+      // ---- keys: pages 2 q, 2 q + 1
+      uint32_t alive = 0u;
+#pragma unroll 1
+      for (int j = 0; j < 2; ++j) {
+        const int pg = 2 * q + j;
+        const uint8_t* pgp = base + (size_t)pg * pb;
+        const int valid = S.pid[stage][pg] < 0 ? 0 : max(0, min(kPage, n_tok - kPage * (page0 + pg)));
+        alive |= ((1u << valid) - 1u) << (16 * j);
+        const uint32_t ta = tq + ((uint32_t)(16 * j) << 16) + kColK;
+        uint32_t v[32];
+        if (valid == 0) {                                   // (whatever the stage holds stays there)
+#pragma unroll
+          for (int x = 0; x < 32; ++x) v[x] = 0u;
+          tm_st_frag16(ta, v);
+          if (NG > 1) tm_st_frag16(ta + 64, v);
+          const uint32_t z[4] = {0u, 0u, 0u, 0u};
+          tm_st_frag2(ta + kKCols, z);
+          if (quad == 0) {
+            S.lane_scale[i & 1][16 * pg + row] = 0.f;
+            S.lane_scale[i & 1][16 * pg + row + 8] = 0.f;
+          }
+          continue;
+        }
+        const uint4 w = lds16(pgp + 16 * lane);
+        const uint32_t kw[4] = {w.x, w.y, w.z, w.w};
+        const uint32_t kw10[4] = {w.x >> 10, w.y >> 10, w.z >> 10, w.w >> 10};
+        const uint8_t* sc = pgp + k_scale_off();
+        float ls[2];
+        if constexpr (NG == 1) {
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[4 * s + r] = code_pair(kw[r], kw10[r], s);
+          tm_st_frag16(ta, v);
+          uint32_t z[4];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const __half2 dz = bits2h(*reinterpret_cast<const uint32_t*>(sc + 4 * (row + 8 * x)));
+            ls[x] = __low2float(dz);
+            const uint32_t zz = quad == 0 ? (uint32_t)__half_as_ushort(__hmul(__high2half(dz), __float2half_rn(0.03125f))) : 0u;
+            z[x] = zz;
+            z[2 + x] = zz;
+          }
+          tm_st_frag2(ta + kKCols, z);
+        } else {
+          uint32_t d2[2][NG];                               // Delta 2^k of both tokens, twice in a register
+          uint32_t z[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t dz[NG];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) dz[g] = *reinterpret_cast<const uint32_t*>(sc + 4 * NG * (row + 8 * x) + 4 * g);
+            float dm = 0.f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) dm = fmaxf(dm, __low2float(bits2h(dz[g])));
+            // largest Delta 2^k in [2^14, 2^15): its product with 3 4^s 2^-24 stays in range, and
+            // a pair hi + lo is exact for groups down to 2^-10 of it
+            const int e = (int)(__float_as_uint(dm) >> 23) - 127;
+            const int kx = dm > 0.f && dm < INFINITY ? 14 - e : 0;
+            const float up = __int_as_float((kx + 127) << 23);
+            ls[x] = __int_as_float((127 - kx) << 23);
+            float dq = 0.f, zq = 0.f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+              const float d = __low2float(bits2h(dz[g])) * up;
+              const __half2 dd = __float2half2_rn(d);
+              d2[x][g] = h2bits(dd);
+              if (g == quad) {
+                dq = __low2float(dd);
+                zq = __high2float(bits2h(dz[g]));
+              }
+            }
+            const float prod = dq * zq * 0x1p-8f;           // (11 + 11 bits: exact)
+            const float hi = __half2float(__float2half_rn(prod));
+            if (quad < NG) {
+              z[x] = pack16(hi, prod - hi);
+              z[2 + x] = pack16(hi, 0.f);
+            }
+          }
+          tm_st_frag2(ta + kKCols, z);
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              v[4 * s + r] = h2bits(__hmul2(bits2h(code_pair(kw[r], kw10[r], s)), bits2h(d2[r & 1][s * NG / 8])));
+          tm_st_frag16(ta, v);
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              v[4 * s + r] = h2bits(__hfma2(bits2h(code_pair(kw[r], kw10[r], s)), bits2h(d2[r & 1][s * NG / 8]),
+                                            __hneg2(bits2h(v[4 * s + r]))));
+          tm_st_frag16(ta + 64, v);
+        }
+        if (P.l2) {
+          const __half* nm = reinterpret_cast<const __half*>(pgp + norm_off(NG, 0));
+          ls[0] *= __half2float(nm[row]);
+          ls[1] *= __half2float(nm[row + 8]);
+        }
+        if (quad == 0) {
+          S.lane_scale[i & 1][16 * pg + row] = ls[0] * cmul;
+          S.lane_scale[i & 1][16 * pg + row + 8] = ls[1] * cmul;
+        }
+      }
+      if (lane == 0) S.alive[i & 1][q] = alive;
+      wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&S.k_full);
+      // ---- values: all pages, channels 32 q .. 32 q + 31
+      if (i > 0 && !warp_wait(&S.pv_done[(i - 1) & 1], (i - 1) >> 1, gave_up)) break;
+      fence_after();
+#pragma unroll 2
+      for (int pg = 0; pg < kTilePages; ++pg) {
+        const uint8_t* pgp = base + (size_t)pg * pb;
+        const int valid = S.pid[stage][pg] < 0 ? 0 : max(0, min(kPage, n_tok - kPage * (page0 + pg)));
+        uint32_t a[2][4];
+        if (valid == 0) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) a[j][r] = 0u;
+        } else {
+          const uint4 w = lds16(pgp + kCodeBytes + 16 * lane);
+          const uint32_t vw[4] = {w.x, w.y, w.z, w.w};
+          const uint8_t* dp = pgp + v_delta_off(NG, 2 * quad, vg);
+          uint32_t d[2], z[2];
+          d[0] = *reinterpret_cast<const uint32_t*>(dp);
+          d[1] = *reinterpret_cast<const uint32_t*>(dp + 16 * NG);
+          z[0] = *reinterpret_cast<const uint32_t*>(dp + 32 * NG);
+          z[1] = *reinterpret_cast<const uint32_t*>(dp + 48 * NG);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) z[x] = h2bits(__hneg2(__hmul2(bits2h(d[x]), bits2h(z[x]))));
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const __half2 c = __hsub2(bits2h(((vw[r] >> vshift[j]) & vmask[j]) | vone[j]), vsub[j]);
+              a[j][r] = h2bits(__hfma2(c, bits2h(d[r >> 1]), bits2h(z[r >> 1])));
+            }
+          if (valid < kPage) {                              // dead tokens: zeros, whatever the page holds there
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int tk = 2 * quad + 8 * x;
+              const uint32_t m = (tk < valid ? 0xffffu : 0u) | (tk + 1 < valid ? 0xffff0000u : 0u);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                a[j][2 * x] &= m;
+                a[j][2 * x + 1] &= m;
+              }
+            }
+          }
+        }
+        tm_st_frag2(tq + kColV + 8 * pg, a[0]);
+        tm_st_frag2(tq + (16u << 16) + kColV + 8 * pg, a[1]);
+      }
+      wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        bar_arrive(&S.v_full);
+        bar_arrive(&S.page_free[stage]);
+      }
+      ++k;
+    }
+  } else {
+    // ---- softmax: token 32 q + lane of every tile, rows kCols half ..
+    const int q = warp & 3, half = warp >> 2;
+    const uint32_t tq = tb + ((uint32_t)(32 * q) << 16);
+    const int c0 = half * kCols;
+    float l[kCols];
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) l[j] = 0.f;
+    bool lost = false;
+#pragma unroll 1
+    for (int i = 0; i < nt; ++i) {
+      const bool ok = warp_wait(&S.s_full, i, gave_up) && !lost;
+      if (half_or(half, !ok)) break;                        // (one decision for the four warps)
+      fence_after();
+      const bool win = t0 + i < nw;
+      const float ls = S.lane_scale[i & 1][32 * q + lane];
+      const uint32_t alive = S.alive[i & 1][q];
+      const bool mine = (alive >> lane) & 1u;
+      // the draft this token is (window tiles that reach into the drafts): else every row sees it
+      int node = -1;
+      if (win) {
+        const int w = (t0 + i) * kTile + 32 * q + lane;
+        node = (w < n_sink ? w : ring0 + w - n_sink) - st.L0;
+      }
+      const bool drafts = win && (n_sink > st.L0 || (t0 + i + 1) * kTile > n_win - st.n);
+      // P buffer free: PV(i - 2), or PV(i - 1) around window tiles (which use both buffers)
+      const int before = (win || (i > 0 && t0 + i - 1 < nw)) ? i - 1 : i - 2;
+      bool waited = before < 0;
+#pragma unroll
+      for (int ch = 0; ch < kChunks; ++ch) {
+        const int cc = c0 + 32 * ch;
+        float x[32];
+        auto scores = [&]() {
+          tm_ld32(tq + cc, x);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(&S.neg_m[cc + j]);
+            x[j] = fmaf(x[j], ls, m.x);
+            x[j + 1] = fmaf(x[j + 1], ls, m.y);
+            x[j + 2] = fmaf(x[j + 2], ls, m.z);
+            x[j + 3] = fmaf(x[j + 3], ls, m.w);
+          }
+        };
+        auto hide = [&](float (&y)[32]) {                   // tokens that do not exist or a row does not see
+          if (alive != 0xffffffffu) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] = mine ? y[j] : -INFINITY;
+          }
+          if (drafts) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int nd = min((row0 + cc + j) >> P.gqa_log2, kNodes - 1);
+              if (node >= 0 && !((S.seen[nd][(node >> 5) & (kNodeWords - 1)] >> (node & 31)) & 1u)) y[j] = -INFINITY;
+            }
+          }
+        };
+        scores();
+        hide(x);
+        float mx = x[0];
+#pragma unroll
+        for (int j = 1; j < 32; ++j) mx = fmaxf(mx, x[j]);
+        if (half_or(half, mx > 8.f)) {
+          // ---- the reference of these 32 rows moves to their maxima so far
+          tm_ld32(tq + cc, x);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] *= ls;
+          hide(x);
+          const float top = reduce_columns(x, lane, [](float a, float b2) { return fmaxf(a, b2); });
+          S.red[q][cc + lane] = top;
+          half_sync(half);
+          const float all = fmaxf(fmaxf(S.red[0][cc + lane], S.red[1][cc + lane]), fmaxf(S.red[2][cc + lane], S.red[3][cc + lane]));
+          const float old = -S.neg_m[cc + lane], now = fmaxf(old, all);
+          half_sync(half);                                  // (everyone has read the old reference)
+          if (q == 0) {
+            S.neg_m[cc + lane] = -now;
+            S.alpha[cc + lane] = ex2(old - now);
+          }
+          half_sync(half);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 al = *reinterpret_cast<const float4*>(&S.alpha[cc + j]);
+            l[32 * ch + j] *= al.x;
+            l[32 * ch + j + 1] *= al.y;
+            l[32 * ch + j + 2] *= al.z;
+            l[32 * ch + j + 3] *= al.w;
+          }
+          if (i > 0) {                                      // O so far, once PV(i - 1) is done
+            if (!warp_wait(&S.pv_done[(i - 1) & 1], (i - 1) >> 1, gave_up)) lost = true;
+            fence_after();
+            tm_ld32(tq + kColO + cc, x);
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float4 al = *reinterpret_cast<const float4*>(&S.alpha[cc + j]);
+              x[j] *= al.x;
+              x[j + 1] *= al.y;
+              x[j + 2] *= al.z;
+              x[j + 3] *= al.w;
+            }
+            tm_st32(tq + kColO + cc, x);
+            wait_st();
+            fence_before();
+            waited = true;
+          }
+          scores();
+          hide(x);
+        }
+        if (ch == kChunks - 1) {                            // S is read
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&S.s_free);
+        }
+        if (!waited) {
+          if (!warp_wait(&S.pv_done[before & 1], before >> 1, gave_up)) lost = true;
+          waited = true;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          x[j] = ex2(x[j]);
+          l[32 * ch + j] += x[j];
+        }
+        // P[token][row], 8 rows a chunk of 16 bytes
+        const int tok = 32 * q + lane;
+        uint8_t* dst = sm + L::kP + (win ? 0 : (i & 1) * L::kPBytes) + (cc >> 6) * kSlab + (tok >> 3) * 1024 + (tok & 7) * 128;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = ((((cc & 63) >> 3) + j) ^ (tok & 7)) << 4;
+          if (!win) {
+            *reinterpret_cast<uint4*>(dst + at) = make_uint4(pack16(x[8 * j], x[8 * j + 1]), pack16(x[8 * j + 2], x[8 * j + 3]),
+                                                             pack16(x[8 * j + 4], x[8 * j + 5]), pack16(x[8 * j + 6], x[8 * j + 7]));
+          } else {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float a0 = x[8 * j + 2 * e], a1 = x[8 * j + 2 * e + 1];
+              hi[e] = packb16(a0, a1);
+              lo[e] = packb16(a0 - __uint_as_float(hi[e] << 16), a1 - __uint_as_float(hi[e] & 0xffff0000u));
+            }
+            *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(dst + L::kPBytes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&S.p_full[i & 1]);
+    }
+    // ---- sums over the tile's tokens: lanes, then quadrants
+#pragma unroll
+    for (int ch = 0; ch < kChunks; ++ch) {
+      float y[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) y[j] = l[32 * ch + j];
+      const float sum = reduce_columns(y, lane, [](float a, float b2) { return a + b2; });
+      S.red[q][c0 + 32 * ch + lane] = sum;
+    }
+    half_sync(half);
+    bool ok = nt > 0 && !lost;
+    if (ok) ok = warp_wait(&S.pv_done[(nt - 1) & 1], (nt - 1) >> 1, gave_up);
+    fence_after();
+    if (nt == 0 || ok) {
+#pragma unroll
+      for (int ch = 0; ch < kChunks; ++ch) {
+        const int cc = c0 + 32 * ch;
+        float o[32];
+        if (nt > 0) {
+          tm_ld32(tq + kColO + cc, o);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const int c = cc + j;
+          if (c < ncol) {
+            const float sum = S.red[0][c] + S.red[1][c] + S.red[2][c] + S.red[3][c];
+            const size_t r = out_row(c);
+            const float ov = o[j];
+            if (P.splits == 1) {
+              const float v = sum > 0.f ? ov / sum : (sum == 0.f ? 0.f : ov * sum);
+              P.out[r * kHeadDim + 32 * q + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            } else {
+              float* rec = P.part + (r * P.splits + split) * kRec;
+              rec[4 + 32 * q + lane] = ov;
+              if (q == 0 && lane == 0) {
+                rec[0] = nt > 0 ? -S.neg_m[c] : -1e30f;
+                rec[1] = sum;
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (tid == 0 && *gave_up) set_status(P.status, KVQ_ERR_TIMEOUT);
+  if (warp == 0) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tb), "r"(kTmem));
+  }
+}
+
+// One warp per (row, query head): the splits' partials into the output.
+constexpr int kMThreads = 256;
+__global__ void __launch_bounds__(kMThreads) attn_tree_merge_kernel(const __grid_constant__ TreeParams P) {
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int hq = P.hkv * P.gqa;
+  const long long r = (long long)blockIdx.x * (kMThreads / 32) + (threadIdx.x >> 5);
+  if (r >= (long long)P.n_rows * hq) return;
+  const int row = (int)(r / hq);
+  if (row < P.cu_rows[0] || row >= P.cu_rows[P.batch]) return;         // a row that no sequence has
+  int lo = 0, hi = P.batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (P.cu_rows[mid] <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  const SeqState st = seq_state(P, lo);
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!st.bad) {
+    const float* rec = P.part + (size_t)r * P.splits * kRec;
+    float M = -INFINITY;
+    for (int s = lane; s < P.splits; s += 32) M = fmaxf(M, __ldcg(rec + (size_t)s * kRec));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float sum = 0.f;
+    for (int s0 = 0; s0 < P.splits; s0 += 8) {
+      float m[8], l[8];
+      float4 o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (s0 + i < P.splits) {
+          const float* p = rec + (size_t)(s0 + i) * kRec;
+          m[i] = __ldcg(p);
+          l[i] = __ldcg(p + 1);
+          o[i] = __ldcg(reinterpret_cast<const float4*>(p + 4) + lane);
+        }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (s0 + i < P.splits) {
+          const float f = exp2f(m[i] - M);
+          sum += l[i] * f;
+          O.x += o[i].x * f; O.y += o[i].y * f; O.z += o[i].z * f; O.w += o[i].w * f;
+        }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    O.x *= inv; O.y *= inv; O.z *= inv; O.w *= inv;
+  }
+  reinterpret_cast<uint2*>(P.out + (size_t)r * kHeadDim)[lane] = make_uint2(packb16(O.x, O.y), packb16(O.z, O.w));
+}
+
+// Columns (rows of a tile) and splits of a call, from its sizes alone.
+struct Shape {
+  int n, splits, items;
+};
+Shape tree_shape(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
+  const int g = cfg->n_q_heads / cfg->n_kv_heads;
+  Shape s;
+  // 128 columns cost the tensor pipe what 64 do, but twice the softmax; a tree that fits 64 takes 64
+  const long long per_seq = ((long long)n_rows * g + cfg->batch - 1) / cfg->batch;
+  s.n = per_seq > 64 ? 128 : 64;
+  s.items = (int)min((long long)n_rows, (long long)n_rows * g / s.n + cfg->batch);
+  const long long pages = max(0LL, min((long long)cfg->max_pages_per_seq, ((long long)max_ctx - cfg->s_sink + kPage - 1) / kPage));
+  const long long win = min((long long)cfg->s_sink + cfg->s_keep + cfg->s_flush + kNodes, (long long)max_ctx);
+  const long long tiles = max(1LL, (pages + kTilePages - 1) / kTilePages + (win + kTile - 1) / kTile);
+  // about as many CTAs as the row tiles there will be (a sequence's last one is half empty on average)
+  const long long units = max(1LL, min((long long)s.items, (per_seq + s.n - 1) / s.n * min((long long)cfg->batch, (long long)n_rows))) *
+                          cfg->n_kv_heads;
+  // a wave of 152 CTAs takes tiles / splits, and about 6 tiles' time for set-up and merge
+  double best = 1e300;
+  s.splits = 1;
+  for (int k = 1; k <= 64 && k <= tiles; ++k) {
+    const double waves = (double)((units * k + kSms - 1) / kSms);
+    const double cost = waves * ((double)((tiles + k - 1) / k) + 5.0) + (k > 1 ? 3.0 : 0.0);
+    if (cost < best * 0.98) {
+      best = cost;
+      s.splits = k;
+    }
+  }
+  return s;
+}
+
+}  // namespace
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" size_t kvq_attn_tree_ws_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
+  if (cfg->key_axis != KVQ_KEY_PER_TOKEN) return kvq_attn_chunk_ws_bytes(cfg, n_rows, max_ctx);
+  const Shape s = tree_shape(cfg, n_rows, max_ctx);
+  return s.splits > 1 ? (size_t)n_rows * cfg->n_q_heads * s.splits * kRec * sizeof(float) : 256;
+}
+
+extern "C" int kvq_launch_attn_tree(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot,
+                                    const int32_t* cu_rows, const int32_t* parent, int32_t n_rows, uint16_t* out,
+                                    float sm_scale, int32_t max_ctx, void* ws, int32_t* d_status, cudaStream_t stream) {
+  if (cfg->key_axis != KVQ_KEY_PER_TOKEN)
+    return kvq_launch_attn_tree_rows(cfg, cache, q_rot, cu_rows, parent, n_rows, out, sm_scale, max_ctx, ws, d_status,
+                                     stream);
+  const Shape s = tree_shape(cfg, n_rows, max_ctx);
+  TreeParams P{};
+  P.pages = (const uint8_t*)cache->pages;
+  P.page_table = cache->page_table;
+  P.seq_len = cache->seq_len;
+  P.s_quant = cache->s_quant;
+  P.sink_k = cache->sink_k;
+  P.sink_v = cache->sink_v;
+  P.ring_k = cache->ring_k;
+  P.ring_v = cache->ring_v;
+  P.q = q_rot;
+  P.cu_rows = cu_rows;
+  P.parent = parent;
+  P.out = out;
+  P.part = (float*)ws;
+  P.status = d_status;
+  P.batch = cfg->batch;
+  P.hkv = cfg->n_kv_heads;
+  P.gqa = cfg->n_q_heads / cfg->n_kv_heads;
+  P.gqa_log2 = P.gqa == 8 ? 3 : P.gqa == 4 ? 2 : P.gqa == 2 ? 1 : 0;
+  P.s_sink = cfg->s_sink;
+  P.ring_cap = cfg->ring_cap;
+  P.max_pages = cfg->max_pages_per_seq;
+  P.num_pages = cfg->num_pages;
+  P.page_bytes = page_head_bytes(cfg->group_size, cfg->key_l2norm, cfg->key_axis);
+  P.l2 = cfg->key_l2norm;
+  P.n_rows = n_rows;
+  P.splits = s.splits;
+  P.mp = (int)max(0LL, min((long long)cfg->max_pages_per_seq, ((long long)max_ctx - cfg->s_sink + kPage - 1) / kPage));
+  P.scale_log2 = sm_scale * 1.4426950408889634f;
+  if (cfg->n_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  const int ng = kHeadDim / cfg->group_size;
+  void (*kern)(const TreeParams) = s.n == 64 ? (ng == 1 ? attn_tree_kernel<64, 1> : ng == 2 ? attn_tree_kernel<64, 2> : attn_tree_kernel<64, 4>)
+                                             : (ng == 1 ? attn_tree_kernel<128, 1> : ng == 2 ? attn_tree_kernel<128, 2> : attn_tree_kernel<128, 4>);
+  const size_t smem = (s.n == 64 ? Layout<64>::kPages + sizeof(TreeShared<64>) : Layout<128>::kPages + sizeof(TreeShared<128>)) +
+                      2 * (size_t)kTilePages * P.page_bytes;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ERR_CUDA;
+  static std::mutex mu;
+  static unsigned long long done[6] = {};
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    const int vi = (s.n == 64 ? 0 : 3) + (ng == 1 ? 0 : ng == 2 ? 1 : 2);
+    if (!(done[vi] & (1ull << dev))) {
+      const size_t most = smem - 2 * (size_t)kTilePages * P.page_bytes + 2 * (size_t)kTilePages * page_head_bytes(cfg->group_size, 1, 0);
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess) return KVQ_ERR_CUDA;
+      done[vi] |= 1ull << dev;
+    }
+  }
+  if (launch_pdl(kern, dim3(s.items, cfg->n_kv_heads, s.splits), dim3(kThreadsT), smem, stream, P) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  if (s.splits > 1) {
+    const long long warps = (long long)n_rows * cfg->n_q_heads, per = kMThreads / 32;
+    if (launch_pdl(attn_tree_merge_kernel, dim3((unsigned)((warps + per - 1) / per)), dim3(kMThreads), 0, stream, P) != cudaSuccess)
+      return KVQ_ERR_CUDA;
+  }
+  return KVQ_OK;
+}
