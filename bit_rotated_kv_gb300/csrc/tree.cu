@@ -47,10 +47,19 @@ constexpr int kNodes = KVQ_TREE_MAX_NODES;
 constexpr int kNodeWords = kNodes / 32;
 constexpr int kTile = 128;                       // tokens of a tile
 constexpr int kTilePages = kTile / kPage;
-constexpr int kSmWarps = 8, kDqWarps = 4;
-constexpr int kThreadsT = 32 * (kSmWarps + kDqWarps + 2);
+constexpr int kSmWarps = 8;                      // softmax; then 4 warps for keys, 4 for values, 4 more
+constexpr int kKeyWarp = 8, kValWarp = 12, kMmaWarp = 16, kPageWarp = 17;
+constexpr int kThreadsT = 32 * 20;               // (whole warpgroups: registers are handed over by warpgroup)
+constexpr int kStages = 4;                       // page tiles in flight
+// Registers a thread by role, of the 96 that 640 threads launch with.
+constexpr int kRegsLaunch = 96;
+template <int N>
+struct Regs {
+  static constexpr int kSoftmax = N == 128 ? 152 : 112, kExpand = N == 128 ? 64 : 88, kIssue = N == 128 ? 40 : 56;
+  static_assert(256 * kSoftmax + 256 * kExpand + 128 * kIssue <= kThreadsT * kRegsLaunch, "register split");
+};
 constexpr int kRec = 4 + kHeadDim;               // (m, l, -, -, o[d]) of a partial
-constexpr long long kSpin = 1LL << 19;          // try_wait rounds before a wait gives up
+constexpr int kSpin = 1 << 15, kSuspend = 20000;  // a wait gives up after that many rounds of at most 20 us
 constexpr uint32_t kTmem = 512;
 constexpr int kSlab = kTile * 128;               // 128 tokens x 64 16-bit values, 128-byte swizzled
 
@@ -88,32 +97,30 @@ __device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
 __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(saddr(b)), "r"(parity)
+      : "r"(saddr(b)), "r"(parity), "r"(kSuspend)
       : "memory");
   return ok != 0;
 }
-// bounded wait that also gives up when another warp has
-__device__ __noinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, volatile int* gave_up) {
-  for (long long i = 0; i < kSpin; ++i) {
-    if (bar_try(b, parity)) return true;
-    if (*gave_up) return false;
-  }
-  *gave_up = 1;
-  return false;
-}
-__device__ __forceinline__ bool bar_wait(uint64_t* b, int phase, volatile int* gave_up) {
-  return bar_try(b, (uint32_t)(phase & 1)) || bar_wait_slow(b, (uint32_t)(phase & 1), gave_up);
-}
-// the same for a whole warp, decided by lane 0 (the warp stays together)
+// Bounded wait of a whole warp, decided by lane 0 (the warp stays together); gives up as well when
+// another warp has.  Inline (a call has no place beside setmaxnreg) and small.
 __device__ __forceinline__ bool warp_wait(uint64_t* b, int phase, volatile int* gave_up) {
-  if (__all_sync(0xffffffffu, bar_try(b, (uint32_t)(phase & 1)))) return true;
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = bar_wait_slow(b, (uint32_t)(phase & 1), gave_up) ? 1 : 0;
-  ok = __shfl_sync(0xffffffffu, ok, 0);
+  bool ok = __all_sync(0xffffffffu, bar_try(b, (uint32_t)(phase & 1)));
+#pragma unroll 1
+  for (int i = 0; !ok && i < kSpin; ++i) {
+    ok = __any_sync(0xffffffffu, bar_try(b, (uint32_t)(phase & 1)));
+    if (!ok && __any_sync(0xffffffffu, *gave_up)) return false;
+  }
+  if (!ok) *gave_up = 1;
   __syncwarp();
-  return ok != 0;
+  return ok;
+}
+// ... for what is in flight when a wait was given up (whatever the outcome)
+__device__ __forceinline__ void settle(uint64_t* b, int phase) {
+#pragma unroll 1
+  for (int i = 0; i < kSpin && !bar_try(b, (uint32_t)(phase & 1)); ++i) {
+  }
 }
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile(
@@ -137,6 +144,17 @@ __device__ __forceinline__ bool half_or(int half, bool v) {
 }
 __device__ __forceinline__ void half_sync(int half) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory"); }
 __device__ __forceinline__ void dq_sync() { asm volatile("barrier.cta.sync 3, 128;" ::: "memory"); }
+// one lane of a converged warp: the code around it stays uniform, so descriptors are formed in uniform
+// registers (issued from a divergent lane an MMA takes 53 clocks, so 20 .. 33 at N = 32 .. 64 are lost)
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+template <int R>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 
 // shared-memory matrix descriptors, 128-byte swizzle (8 rows of 128 bytes, groups 1024 apart)
 __device__ __forceinline__ uint64_t desc_k128(uint32_t a) {                 // K-major
@@ -166,28 +184,33 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)) : "memory");
 }
 #define KVQ_IO8(c, b) c(v[b]), c(v[b + 1]), c(v[b + 2]), c(v[b + 3]), c(v[b + 4]), c(v[b + 5]), c(v[b + 6]), c(v[b + 7])
-__device__ __forceinline__ void tm_ld32(uint32_t a, float (&v)[32]) {
+// 32 columns of this warp's lanes -> registers, not waited for
+__device__ __forceinline__ void tm_ld32(uint32_t a, float* v) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
       "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : KVQ_IO8("=f", 0), KVQ_IO8("=f", 8), KVQ_IO8("=f", 16), KVQ_IO8("=f", 24)
       : "r"(a));
+}
+// waits for this thread's loads; the registers pass through so that no use moves above it
+__device__ __forceinline__ void tm_wait32(float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : KVQ_IO8("+f", 0), KVQ_IO8("+f", 8), KVQ_IO8("+f", 16), KVQ_IO8("+f", 24)::"memory");
 }
-__device__ __forceinline__ void tm_st32(uint32_t a, const float (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::KVQ_IO8("f", 0), KVQ_IO8("f", 8), KVQ_IO8("f", 16),
-      KVQ_IO8("f", 24), "r"(a)
-      : "memory");
+__device__ __forceinline__ void tm_ld8(uint32_t a, float (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : KVQ_IO8("=f", 0) : "r"(a));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : KVQ_IO8("+f", 0)::"memory");
 }
-// 16 lanes x 64 columns: registers 4 s .. 4 s + 3 are the A fragment of k-step s
-__device__ __forceinline__ void tm_st_frag16(uint32_t a, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tm_st8(uint32_t a, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::KVQ_IO8("f", 0), "r"(a) : "memory");
+}
+// 16 lanes x 32 columns: registers 4 s .. 4 s + 3 are the A fragment of k-step s
+#define KVQ_R16(c, v) c(v[0]), c(v[1]), c(v[2]), c(v[3]), c(v[4]), c(v[5]), c(v[6]), c(v[7]), c(v[8]), c(v[9]), c(v[10]), \
+                      c(v[11]), c(v[12]), c(v[13]), c(v[14]), c(v[15])
+__device__ __forceinline__ void tm_st_frag8(uint32_t a, const uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::KVQ_IO8("r", 0), KVQ_IO8("r", 8), KVQ_IO8("r", 16),
-      KVQ_IO8("r", 24), "r"(a)
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::KVQ_R16("r", v),
+      "r"(a)
       : "memory");
 }
 // 16 lanes x 8 columns: the A fragment of one k-step
@@ -208,15 +231,18 @@ __device__ __forceinline__ uint32_t packb16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 __device__ __forceinline__ uint4 lds16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
 __device__ __forceinline__ int slot_pow(int s) { return s <= 4 ? s : s - 5; }
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t w10, int s) {
   return s <= 4 ? (w & (0x00030003u << (2 * s))) : (w10 & (0x00030003u << (2 * (s - 5))));
 }
-// Reduce 32 values per lane over the warp's lanes; lane j returns value j's result.
+// Reduce 8 values per lane over the warp's lanes; lane j returns value j % 8's result.
 template <class F>
-__device__ __forceinline__ float reduce_columns(float (&x)[32], int lane, F f) {
+__device__ __forceinline__ float reduce_columns(float (&x)[8], int lane, F f) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = 4; o > 0; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int j = 0; j < o; ++j) {
@@ -224,7 +250,8 @@ __device__ __forceinline__ float reduce_columns(float (&x)[32], int lane, F f) {
       x[j] = f(mine, __shfl_xor_sync(0xffffffffu, other, o));
     }
   }
-  return x[0];
+  x[0] = f(x[0], __shfl_xor_sync(0xffffffffu, x[0], 8));
+  return f(x[0], __shfl_xor_sync(0xffffffffu, x[0], 16));
 }
 
 // A sequence's rows as the kernels see them.
@@ -259,23 +286,29 @@ struct Layout {          // dynamic shared memory, from a 1024-byte boundary
   static constexpr int kQb = kQ + 2 * N * 128;              // q' bf16 likewise
   static constexpr int kP = kQb + 2 * N * 128;              // P, two buffers of N / 64 slabs
   static constexpr int kPBytes = N / 64 * kSlab;
-  static constexpr int kK = kP + 2 * kPBytes;               // window K rows, two slabs
+  static constexpr int kZ = kP + 2 * kPBytes;               // zero-point B operand: N x 16 fp16
+  // window K and V rows, two slabs each; where a CTA's window tiles are done (or it has none), the
+  // page stages
+  static constexpr int kK = (kZ + N * 32 + 1023) / 1024 * 1024;
   static constexpr int kV = kK + 2 * kSlab;
-  static constexpr int kZ = kV + 2 * kSlab;                 // zero-point B operand: N x 16 fp16
-  static constexpr int kPages = kZ + N * 32;                // two stages of 8 pages
+  static constexpr int kPages = kK;
+  static constexpr int kEnd = kV + 2 * kSlab;
+  static_assert(kStages * kTilePages * 1568 <= 4 * kSlab, "page stages");
 };
 
 template <int N>
 struct TreeShared {
-  __align__(16) uint64_t page_full[2], page_free[2], k_full, v_full, s_full, s_free, p_full[2], pv_done[2];
+  __align__(16) uint64_t page_full[kStages], page_free[kStages], k_full[2], v_full[2], s_full[2], s_free, p_full[2],
+      pv_done[2];
   uint32_t tmem;
   int gave_up;
   int item[3];                     // sequence, row tile, found
-  int pid[2][kTilePages];
-  float lane_scale[2][kTile];
-  uint32_t alive[2][4];            // tokens of a tile that exist, by lane quadrant
+  int pid[kStages][kTilePages];
+  float lane_scale[4][kTile];
+  uint32_t alive[4][4];            // tokens of a tile that exist, by lane quadrant
   __align__(16) float neg_m[N];    // minus the reference of every row
-  __align__(16) float alpha[N];
+  __align__(16) float alpha[N];    // a moved reference: factor of what is summed, and what the scores less it change by
+  __align__(16) float delta[N];
   float red[4][N];                 // per-quadrant maxima; at the end the sums
   uint32_t seen[kNodes][kNodeWords];   // ancestors of every node, itself among them
   float amax[kThreadsT / 32];
@@ -287,22 +320,27 @@ struct Doubling {                  // of the ancestors, at set-up (where the pag
 
 static_assert(offsetof(TreeShared<128>, neg_m) % 16 == 0 && offsetof(TreeShared<128>, alpha) % 16 == 0 &&
                   offsetof(TreeShared<64>, neg_m) % 16 == 0 && offsetof(TreeShared<64>, alpha) % 16 == 0 &&
-                  Layout<64>::kPages % 1024 == 0 && Layout<128>::kPages % 1024 == 0, "vector loads");
-static_assert(Layout<128>::kPages + 2 * kTilePages * 1568 + sizeof(TreeShared<128>) <= 227 * 1024, "shared memory of an SM");
+                  offsetof(TreeShared<128>, delta) % 16 == 0 && offsetof(TreeShared<64>, delta) % 16 == 0 &&
+                  Layout<64>::kEnd % 1024 == 0 && Layout<128>::kEnd % 1024 == 0, "vector loads");
+static_assert(Layout<128>::kEnd + sizeof(TreeShared<128>) <= 227 * 1024, "shared memory of an SM");
 
 template <int N, int NG>
 __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_constant__ TreeParams P) {
   using L = Layout<N>;
   constexpr int kCols = N / 2;                              // rows of a softmax warp
-  constexpr int kChunks = kCols / 32;
-  constexpr int kKCols = NG == 1 ? 64 : 128;                // TMEM columns of the key operand, then 8 for zero points
-  constexpr uint32_t kColO = N, kColK = 2 * N, kColV = 2 * N + 144;
+  // TMEM columns: S, O, then the key operand (64 or 128, and 8 for zero points) and the value
+  // operand, twice each where the 512 columns allow: keys are waited for by the shorter product
+  // when they are codes, and are the longer ones to expand when they are pairs
+  constexpr int kKCols = NG == 1 ? 64 : 128;
+  constexpr int kKBufs = N == 64 ? 2 : 1, kVBufs = NG == 1 ? 2 : 1;
+  constexpr uint32_t kColO = N, kColK = 2 * N, kColV = 2 * N + kKBufs * (kKCols + 8);
+  static_assert(kColV + kVBufs * 64 <= 512, "TMEM columns");
   constexpr uint32_t kIdescF16 = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
   constexpr uint32_t kIdescPV = kIdescF16 | (1u << 16);
   constexpr uint32_t kIdescB16 = kIdescF16 | (1u << 7) | (1u << 10);
   constexpr uint32_t kIdescB16PV = kIdescB16 | (1u << 15) | (1u << 16);
   extern __shared__ __align__(1024) uint8_t sm[];           // (all of the shared memory: it starts aligned)
-  TreeShared<N>& S = *reinterpret_cast<TreeShared<N>*>(sm + L::kPages + 2 * kTilePages * P.page_bytes);
+  TreeShared<N>& S = *reinterpret_cast<TreeShared<N>*>(sm + L::kEnd);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   volatile int* gave_up = &S.gave_up;
   pdl_trigger();
@@ -380,15 +418,17 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
 
   // ---- set-up: barriers, TMEM, q' operands, ancestors
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       bar_init(&S.page_full[i], 1);
-      bar_init(&S.page_free[i], kDqWarps);
+      bar_init(&S.page_free[i], 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&S.k_full[i], 4);
+      bar_init(&S.v_full[i], 4);
+      bar_init(&S.s_full[i], 1);
       bar_init(&S.p_full[i], kSmWarps);
       bar_init(&S.pv_done[i], 1);
     }
-    bar_init(&S.k_full, kDqWarps);
-    bar_init(&S.v_full, kDqWarps);
-    bar_init(&S.s_full, 1);
     bar_init(&S.s_free, kSmWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -396,9 +436,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&S.tmem)), "r"(kTmem) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  for (int c = tid; c < N; c += kThreadsT) S.neg_m[c] = 1e30f;
+  for (int c = tid; c < N; c += kThreadsT) S.neg_m[c] = 0.f;
   // bf16 rows: 16-byte chunk j of row c at slab j / 8, swizzled
   float amax = 0.f;
+#pragma unroll 1
   for (int i = tid; i < N * 16; i += kThreadsT) {
     const int c = i >> 4, j = i & 15;
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -414,9 +455,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if (lane == 0) S.amax[warp] = amax;
-  // parents, checked; ancestors by doubling (warps 8 .. 11: one thread a node)
-  if (warp >= kSmWarps && warp < kSmWarps + kDqWarps) {
-    const int i = tid - 32 * kSmWarps;
+  // parents, checked; ancestors by doubling (the key warps: one thread a node)
+  if (warp >= kKeyWarp && warp < kKeyWarp + 4) {
+    const int i = tid - 32 * kKeyWarp;
     int up = -1;
     if (i < st.n) {
       up = P.parent[st.first + i];
@@ -463,6 +504,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     }
   }
   // fp16 rows, channel slot s scaled by 4^-s for the codes that carry 4^s
+#pragma unroll 1
   for (int i = tid; i < N * 16; i += kThreadsT) {
     const int c = i >> 4, j = i & 15;
     const uint32_t off = (j >> 3) * N * 128 + (c >> 3) * 1024 + (c & 7) * 128 + (((j & 7) ^ (c & 7)) << 4);
@@ -481,6 +523,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     for (int g = 0; g < 4; ++g) {
       float acc = 0.f;
       if (g < NG)
+#pragma unroll 1
         for (int j = g * (16 / NG); j < (g + 1) * (16 / NG); ++j) {
           const uint4 v = lds16(sm + L::kQb + (j >> 3) * N * 128 + (c >> 3) * 1024 + (c & 7) * 128 + (((j & 7) ^ (c & 7)) << 4));
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -499,465 +542,502 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
   __syncthreads();
 
   const int pb = P.page_bytes;
+  const int nwc = max(0, min(t1, nw) - t0);                 // this CTA's window tiles: its first ones
   uint8_t* stages = sm + L::kPages;
-  if (warp == kSmWarps + kDqWarps + 1) {
-    // ---- pages
-    const int32_t* tab = P.page_table + (size_t)b * P.max_pages;
-    int k = 0;                                              // page tiles streamed
-    for (int i = 0; i < nt; ++i) {
-      if (t0 + i < nw) continue;
-      const int stage = k & 1;
-      if (k >= 2) {
-        if (!warp_wait(&S.page_free[stage], (k >> 1) - 1, gave_up)) break;
-      }
-      const int p = (t0 + i - nw) * kTilePages + lane;
-      int pid = -1;
-      if (lane < kTilePages && p < np) {
-        pid = p < P.max_pages ? tab[p] : -1;
-        if ((unsigned)pid >= (unsigned)P.num_pages) {
-          pid = -1;
-          set_status(P.status, KVQ_ERR_BOUNDS);
-        }
-      }
-      if (lane < kTilePages) S.pid[stage][lane] = pid;
-      const int live = __popc(__ballot_sync(0xffffffffu, pid >= 0));
-      if (lane == 0) {
-        if (live) bar_expect(&S.page_full[stage], (uint32_t)(live * pb));
-        else bar_arrive(&S.page_full[stage]);
-      }
-      __syncwarp();
-      if (pid >= 0)
-        bulk_load(stages + (size_t)(stage * kTilePages + lane) * pb, P.pages + ((size_t)pid * P.hkv + h) * pb, (uint32_t)pb,
-                  &S.page_full[stage]);
-      ++k;
-    }
-    if (*gave_up)                                           // copies in flight land before the CTA can end
-      for (int j = max(0, k - 2); j < k; ++j)
-        for (long long it = 0; it < kSpin && !bar_try(&S.page_full[j & 1], (uint32_t)((j >> 1) & 1)); ++it) {
-        }
-  } else if (warp == kSmWarps + kDqWarps) {
-    // ---- MMA issue
-    if (lane == 0) {
-      int done = -1;                                        // last committed PV
-      int qk = -1;
-      auto pv = [&](int i) {
-        if (!bar_wait(&S.p_full[i & 1], i >> 1, gave_up) || !bar_wait(&S.v_full, i, gave_up)) return false;
-        fence_after();
-        if (t0 + i < nw) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint64_t a = desc_mn128(saddr(sm + L::kV) + kk * 2048);
-            mma_ss(tb + kColO, a, desc_mn128(saddr(sm + L::kP) + kk * 2048), kIdescB16PV, i > 0 || kk > 0);
-            mma_ss(tb + kColO, a, desc_mn128(saddr(sm + L::kP + L::kPBytes) + kk * 2048), kIdescB16PV, 1u);
+  if (warp >= kMmaWarp) {
+    regs_dec<Regs<N>::kIssue>();
+    if (warp == kPageWarp) {
+      // ---- pages
+      const int32_t* tab = P.page_table + (size_t)b * P.max_pages;
+      int k = 0;                                            // page tiles streamed
+      bool ok = true;
+      if (nwc > 0 && nwc < nt) ok = warp_wait(&S.pv_done[(nwc - 1) & 1], (nwc - 1) >> 1, gave_up);
+      for (int i = nwc; ok && i < nt; ++i, ++k) {
+        const int stage = k % kStages;
+        const int p = (t0 + i - nw) * kTilePages + lane;
+        int pid = -1;
+        if (lane < kTilePages && p < np) {
+          pid = p < P.max_pages ? tab[p] : -1;
+          if ((unsigned)pid >= (unsigned)P.num_pages) {
+            pid = -1;
+            set_status(P.status, KVQ_ERR_BOUNDS);
           }
-        } else {
-          const uint32_t p = saddr(sm + L::kP + (i & 1) * L::kPBytes);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) mma_ts(tb + kColO, tb + kColV + 8 * kk, desc_mn128(p + kk * 2048), kIdescPV, i > 0 || kk > 0);
         }
-        mma_commit(&S.pv_done[i & 1]);
+        if (k >= kStages) {
+          ok = warp_wait(&S.page_free[stage], k / kStages - 1, gave_up);
+          if (!ok) break;
+        }
+        if (lane < kTilePages) S.pid[stage][lane] = pid;
+        const int live = __popc(__ballot_sync(0xffffffffu, pid >= 0));
+        __syncwarp();
+        if (lane == 0) {
+          if (live) bar_expect(&S.page_full[stage], (uint32_t)(live * pb));
+          else bar_arrive(&S.page_full[stage]);
+        }
+        __syncwarp();
+        if (pid >= 0)
+          bulk_load(stages + (size_t)(stage * kTilePages + lane) * pb, P.pages + ((size_t)pid * P.hkv + h) * pb, (uint32_t)pb,
+                    &S.page_full[stage]);
+      }
+      if (*gave_up)                                         // copies in flight land before the CTA can end
+#pragma unroll 1
+        for (int j = max(0, k - kStages); j < k; ++j) settle(&S.page_full[j % kStages], j / kStages);
+    } else if (warp == kMmaWarp) {
+      // ---- MMA issue
+      int qk = -1, done = -1;                               // last committed products
+      const uint64_t q_d = desc_k128(saddr(sm + L::kQ)), p_d = desc_mn128(saddr(sm + L::kP));
+      const uint64_t z_d = desc_plain(saddr(sm + L::kZ), N * 16);
+      auto pv = [&](int i) {
+        if (!warp_wait(&S.v_full[i & 1], i >> 1, gave_up) || !warp_wait(&S.p_full[i & 1], i >> 1, gave_up)) return false;
+        fence_after();
+        if (i < nwc) {
+          const uint64_t v_d = desc_mn128(saddr(sm + L::kV));
+          if (elect())
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              mma_ss(tb + kColO, v_d + kk * (2048 >> 4), p_d + kk * (2048 >> 4), kIdescB16PV, i > 0 || kk > 0);
+              mma_ss(tb + kColO, v_d + kk * (2048 >> 4), p_d + ((L::kPBytes + kk * 2048) >> 4), kIdescB16PV, 1u);
+            }
+        } else {
+          const uint64_t p = p_d + (uint64_t)((i & 1) * (L::kPBytes >> 4));
+          const uint32_t v = tb + kColV + (kVBufs == 2 ? 64 * (i & 1) : 0);
+          if (elect())
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) mma_ts(tb + kColO, v + 8 * kk, p + kk * (2048 >> 4), kIdescPV, i > 0 || kk > 0);
+        }
+        if (elect()) mma_commit(&S.pv_done[i & 1]);
+        __syncwarp();
         done = i;
         return true;
       };
-      for (int i = 0; i < nt; ++i) {
-        if (!bar_wait(&S.k_full, i, gave_up)) break;
-        if (i > 0 && !bar_wait(&S.s_free, i - 1, gave_up)) break;
-        fence_after();
-        if (t0 + i < nw) {
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-            mma_ss(tb, desc_k128(saddr(sm + L::kK) + (s >> 2) * kSlab + (s & 3) * 32),
-                   desc_k128(saddr(sm + L::kQb) + (s >> 2) * N * 128 + (s & 3) * 32), kIdescB16, s > 0);
-        } else {
-#pragma unroll
-          for (int s = 0; s < 8; ++s) {
-            const uint64_t q = desc_k128(saddr(sm + L::kQ) + (s >> 2) * N * 128 + (s & 3) * 32);
-            mma_ts(tb, tb + kColK + 8 * s, q, kIdescF16, s > 0);
-            if (NG > 1) mma_ts(tb, tb + kColK + 64 + 8 * s, q, kIdescF16, 1u);
-          }
-          mma_ts(tb, tb + kColK + kKCols, desc_plain(saddr(sm + L::kZ), N * 16), kIdescF16, 1u);
-        }
-        mma_commit(&S.s_full);
-        qk = i;
-        if (i > 0 && !pv(i - 1)) break;
-      }
-      if (nt > 0 && !*gave_up) (void)pv(nt - 1);
-      if (*gave_up) {                                       // what was issued ends before TMEM is given back
-        for (long long it = 0; it < kSpin && qk >= 0 && !bar_try(&S.s_full, (uint32_t)(qk & 1)); ++it) {
-        }
-        for (long long it = 0; it < kSpin && done >= 0 && !bar_try(&S.pv_done[done & 1], (uint32_t)((done >> 1) & 1)); ++it) {
-        }
-      }
-    }
-  } else if (warp >= kSmWarps) {
-    // ---- operands of a tile: lane quadrant q of TMEM (keys: tokens 32 q .. of the tile; values:
-    // channels 32 q ..)
-    const int q = warp - kSmWarps;
-    const uint32_t tq = tb + ((uint32_t)(32 * q) << 16);
-    const int row = lane >> 2, quad = lane & 3;
-    const float cmul = P.scale_log2 * ldexpf(1.f, 24 - sigma);
-    // value codes of channels 32 q + 16 j ..: slot m = 2 q + j
-    uint32_t vmask[2], vone[2];
-    int vshift[2];
-    __half2 vsub[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int m = 2 * q + j, s = slot_pow(m);
-      vshift[j] = m <= 4 ? 0 : 10;
-      vmask[j] = 0x00030003u << (2 * s);
-      vone[j] = (uint32_t)(25 - 2 * s) << 10;               // 2^(10 - 2 s): the code's bits then count ones
-      vone[j] |= vone[j] << 16;
-      vsub[j] = bits2h(vone[j]);
-    }
-    const int vg = 32 * q / (kHeadDim / NG);                // the group of these channels
-    int k = 0;
-    for (int i = 0; i < nt; ++i) {
-      if (t0 + i < nw) {
-        // window rows: token w of the window at slab-swizzled row w; 16 lanes a row, 16 bytes each
-        const int w0 = (t0 + i) * kTile;
-        const int t = tid - 32 * kSmWarps;
-        S.lane_scale[i & 1][t] = P.scale_log2;
-        const unsigned alive = __ballot_sync(0xffffffffu, w0 + t < n_win);
-        if (lane == 0) S.alive[i & 1][q] = alive;
-        bool ok = true;
-#pragma unroll 1
-        for (int side = 0; side < 2; ++side) {
-          // keys once QK(i - 1) has read the last ones, values once PV(i - 1) has (it comes after QK(i))
-          if (i > 0) ok = side ? warp_wait(&S.pv_done[(i - 1) & 1], (i - 1) >> 1, gave_up) : warp_wait(&S.s_full, i - 1, gave_up);
-          if (!ok) break;
-          const uint16_t* sink = side ? P.sink_v : P.sink_k;
-          const uint16_t* ring = side ? P.ring_v : P.ring_k;
-          uint8_t* dst = sm + (side ? L::kV : L::kK);
-          const int j = t & 15;
-#pragma unroll 8
-          for (int r = t >> 4; r < kTile; r += 8) {
-            const int w = w0 + r;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (w < n_win) {
-              const int tok = w < n_sink ? w : ring0 + w - n_sink;
-              const uint16_t* src = w < n_sink ? sink + (((size_t)b * P.hkv + h) * P.s_sink + tok) * kHeadDim
-                                               : ring + (((size_t)b * P.hkv + h) * P.ring_cap + tok % P.ring_cap) * kHeadDim;
-              v = reinterpret_cast<const uint4*>(src)[j];
-            }
-            *reinterpret_cast<uint4*>(dst + (j >> 3) * kSlab + (r >> 3) * 1024 + (r & 7) * 128 + (((j & 7) ^ (r & 7)) << 4)) = v;
-          }
-          fence_async();
-          __syncwarp();
-          if (lane == 0) bar_arrive(side ? &S.v_full : &S.k_full);
-        }
+      bool ok = true;
+      for (int i = 0; ok && i < nt; ++i) {
+        // (the first pages are streamed into the window rows' space: after the last window product)
+        if (i > 0 && i == nwc) ok = pv(i - 1);
+        if (ok) ok = warp_wait(&S.k_full[i & 1], i >> 1, gave_up);
+        if (ok && i > 0) ok = warp_wait(&S.s_free, i - 1, gave_up);
         if (!ok) break;
-        continue;
-      }
-      const int stage = k & 1;
-      const int page0 = (t0 + i - nw) * kTilePages;
-      if (!warp_wait(&S.page_full[stage], k >> 1, gave_up)) break;
-      if (i > 0 && !warp_wait(&S.s_full, i - 1, gave_up)) break;
-      fence_after();
-      const uint8_t* base = stages + (size_t)stage * kTilePages * pb;
-      // ---- keys: pages 2 q, 2 q + 1
-      uint32_t alive = 0u;
-#pragma unroll 1
-      for (int j = 0; j < 2; ++j) {
-        const int pg = 2 * q + j;
-        const uint8_t* pgp = base + (size_t)pg * pb;
-        const int valid = S.pid[stage][pg] < 0 ? 0 : max(0, min(kPage, n_tok - kPage * (page0 + pg)));
-        alive |= ((1u << valid) - 1u) << (16 * j);
-        const uint32_t ta = tq + ((uint32_t)(16 * j) << 16) + kColK;
-        uint32_t v[32];
-        if (valid == 0) {                                   // (whatever the stage holds stays there)
+        fence_after();
+        if (i < nwc) {
+          const uint64_t k_d = desc_k128(saddr(sm + L::kK)), qb_d = desc_k128(saddr(sm + L::kQb));
+          if (elect())
 #pragma unroll
-          for (int x = 0; x < 32; ++x) v[x] = 0u;
-          tm_st_frag16(ta, v);
-          if (NG > 1) tm_st_frag16(ta + 64, v);
-          const uint32_t z[4] = {0u, 0u, 0u, 0u};
-          tm_st_frag2(ta + kKCols, z);
-          if (quad == 0) {
-            S.lane_scale[i & 1][16 * pg + row] = 0.f;
-            S.lane_scale[i & 1][16 * pg + row + 8] = 0.f;
-          }
-          continue;
-        }
-        const uint4 w = lds16(pgp + 16 * lane);
-        const uint32_t kw[4] = {w.x, w.y, w.z, w.w};
-        const uint32_t kw10[4] = {w.x >> 10, w.y >> 10, w.z >> 10, w.w >> 10};
-        const uint8_t* sc = pgp + k_scale_off();
-        float ls[2];
-        if constexpr (NG == 1) {
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[4 * s + r] = code_pair(kw[r], kw10[r], s);
-          tm_st_frag16(ta, v);
-          uint32_t z[4];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const __half2 dz = bits2h(*reinterpret_cast<const uint32_t*>(sc + 4 * (row + 8 * x)));
-            ls[x] = __low2float(dz);
-            const uint32_t zz = quad == 0 ? (uint32_t)__half_as_ushort(__hmul(__high2half(dz), __float2half_rn(0.03125f))) : 0u;
-            z[x] = zz;
-            z[2 + x] = zz;
-          }
-          tm_st_frag2(ta + kKCols, z);
+            for (int s = 0; s < 8; ++s)
+              mma_ss(tb, k_d + (((s >> 2) * kSlab + (s & 3) * 32) >> 4), qb_d + (((s >> 2) * N * 128 + (s & 3) * 32) >> 4),
+                     kIdescB16, s > 0);
         } else {
-          uint32_t d2[2][NG];                               // Delta 2^k of both tokens, twice in a register
-          uint32_t z[4] = {0u, 0u, 0u, 0u};
+          const uint32_t ka = tb + kColK + (kKBufs == 2 ? (kKCols + 8) * (i & 1) : 0);
+          if (elect()) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t dz[NG];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) dz[g] = *reinterpret_cast<const uint32_t*>(sc + 4 * NG * (row + 8 * x) + 4 * g);
-            float dm = 0.f;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) dm = fmaxf(dm, __low2float(bits2h(dz[g])));
-            // largest Delta 2^k in [2^14, 2^15): its product with 3 4^s 2^-24 stays in range, and
-            // a pair hi + lo is exact for groups down to 2^-10 of it
-            const int e = (int)(__float_as_uint(dm) >> 23) - 127;
-            const int kx = dm > 0.f && dm < INFINITY ? 14 - e : 0;
-            const float up = __int_as_float((kx + 127) << 23);
-            ls[x] = __int_as_float((127 - kx) << 23);
-            float dq = 0.f, zq = 0.f;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-              const float d = __low2float(bits2h(dz[g])) * up;
-              const __half2 dd = __float2half2_rn(d);
-              d2[x][g] = h2bits(dd);
-              if (g == quad) {
-                dq = __low2float(dd);
-                zq = __high2float(bits2h(dz[g]));
-              }
+            for (int s = 0; s < 8; ++s) {
+              const uint64_t qs = q_d + (((s >> 2) * N * 128 + (s & 3) * 32) >> 4);
+              mma_ts(tb, ka + 8 * s, qs, kIdescF16, s > 0);
+              if (NG > 1) mma_ts(tb, ka + 64 + 8 * s, qs, kIdescF16, 1u);
             }
-            const float prod = dq * zq * 0x1p-8f;           // (11 + 11 bits: exact)
-            const float hi = __half2float(__float2half_rn(prod));
-            if (quad < NG) {
-              z[x] = pack16(hi, prod - hi);
-              z[2 + x] = pack16(hi, 0.f);
-            }
+            mma_ts(tb, ka + kKCols, z_d, kIdescF16, 1u);
           }
-          tm_st_frag2(ta + kKCols, z);
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              v[4 * s + r] = h2bits(__hmul2(bits2h(code_pair(kw[r], kw10[r], s)), bits2h(d2[r & 1][s * NG / 8])));
-          tm_st_frag16(ta, v);
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              v[4 * s + r] = h2bits(__hfma2(bits2h(code_pair(kw[r], kw10[r], s)), bits2h(d2[r & 1][s * NG / 8]),
-                                            __hneg2(bits2h(v[4 * s + r]))));
-          tm_st_frag16(ta + 64, v);
         }
-        if (P.l2) {
-          const __half* nm = reinterpret_cast<const __half*>(pgp + norm_off(NG, 0));
-          ls[0] *= __half2float(nm[row]);
-          ls[1] *= __half2float(nm[row + 8]);
-        }
-        if (quad == 0) {
-          S.lane_scale[i & 1][16 * pg + row] = ls[0] * cmul;
-          S.lane_scale[i & 1][16 * pg + row + 8] = ls[1] * cmul;
-        }
+        if (elect()) mma_commit(&S.s_full[i & 1]);
+        __syncwarp();
+        qk = i;
+        if (i > 0 && i != nwc) ok = pv(i - 1);
       }
-      if (lane == 0) S.alive[i & 1][q] = alive;
-      wait_st();
-      fence_before();
+      if (ok && nt > 0) ok = pv(nt - 1);
+      if (!ok) {                                            // what was issued ends before TMEM is given back
+        if (qk >= 0) settle(&S.s_full[qk & 1], qk >> 1);
+        if (done >= 0) settle(&S.pv_done[done & 1], done >> 1);
+      }
+    }
+  } else if (warp >= kKeyWarp) {
+    regs_dec<Regs<N>::kExpand>();
+    // ---- operands of a tile, lane quadrant q of TMEM.  Window tiles: 128 threads copy the rows
+    // into swizzled shared memory, 16 lanes a row
+    const bool keys = warp < kValWarp;
+    const int q = warp & 3, t = tid - 32 * (keys ? kKeyWarp : kValWarp);
+    const int row = lane >> 2, quad = lane & 3;
+    const uint32_t tq = tb + ((uint32_t)(32 * q) << 16);
+    bool ok = true;
+    for (int i = 0; i < nwc; ++i) {
+      const int w0 = (t0 + i) * kTile;
+      // keys once QK(i - 1) has read the last ones, values once PV(i - 1) has
+      if (i > 0) ok = warp_wait(keys ? &S.s_full[(i - 1) & 1] : &S.pv_done[(i - 1) & 1], (i - 1) >> 1, gave_up);
+      if (!ok) break;
+      const uint16_t* sink = keys ? P.sink_k : P.sink_v;
+      const uint16_t* ring = keys ? P.ring_k : P.ring_v;
+      uint8_t* dst = sm + (keys ? L::kK : L::kV);
+      const int j = t & 15;
+#pragma unroll 4
+      for (int r = t >> 4; r < kTile; r += 8) {
+        const int w = w0 + r;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (w < n_win) {
+          const int tok = w < n_sink ? w : ring0 + w - n_sink;
+          const uint16_t* src = w < n_sink ? sink + (((size_t)b * P.hkv + h) * P.s_sink + tok) * kHeadDim
+                                           : ring + (((size_t)b * P.hkv + h) * P.ring_cap + tok % P.ring_cap) * kHeadDim;
+          v = reinterpret_cast<const uint4*>(src)[j];
+        }
+        *reinterpret_cast<uint4*>(dst + (j >> 3) * kSlab + (r >> 3) * 1024 + (r & 7) * 128 + (((j & 7) ^ (r & 7)) << 4)) = v;
+      }
+      if (keys) {
+        S.lane_scale[i & 3][t] = P.scale_log2;
+        const unsigned alive = __ballot_sync(0xffffffffu, w0 + t < n_win);
+        if (lane == 0) S.alive[i & 3][q] = alive;
+      }
+      fence_async();
       __syncwarp();
-      if (lane == 0) bar_arrive(&S.k_full);
-      // ---- values: all pages, channels 32 q .. 32 q + 31
-      if (i > 0 && !warp_wait(&S.pv_done[(i - 1) & 1], (i - 1) >> 1, gave_up)) break;
-      fence_after();
-#pragma unroll 2
-      for (int pg = 0; pg < kTilePages; ++pg) {
-        const uint8_t* pgp = base + (size_t)pg * pb;
-        const int valid = S.pid[stage][pg] < 0 ? 0 : max(0, min(kPage, n_tok - kPage * (page0 + pg)));
-        uint32_t a[2][4];
-        if (valid == 0) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) a[j][r] = 0u;
-        } else {
-          const uint4 w = lds16(pgp + kCodeBytes + 16 * lane);
-          const uint32_t vw[4] = {w.x, w.y, w.z, w.w};
-          const uint8_t* dp = pgp + v_delta_off(NG, 2 * quad, vg);
-          uint32_t d[2], z[2];
-          d[0] = *reinterpret_cast<const uint32_t*>(dp);
-          d[1] = *reinterpret_cast<const uint32_t*>(dp + 16 * NG);
-          z[0] = *reinterpret_cast<const uint32_t*>(dp + 32 * NG);
-          z[1] = *reinterpret_cast<const uint32_t*>(dp + 48 * NG);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) z[x] = h2bits(__hneg2(__hmul2(bits2h(d[x]), bits2h(z[x]))));
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const __half2 c = __hsub2(bits2h(((vw[r] >> vshift[j]) & vmask[j]) | vone[j]), vsub[j]);
-              a[j][r] = h2bits(__hfma2(c, bits2h(d[r >> 1]), bits2h(z[r >> 1])));
-            }
-          if (valid < kPage) {                              // dead tokens: zeros, whatever the page holds there
+      if (lane == 0) bar_arrive(keys ? &S.k_full[i & 1] : &S.v_full[i & 1]);
+    }
+    if (keys) {
+      // ---- keys: tokens 32 q .. 32 q + 31 of a tile, pages 2 q and 2 q + 1
+      const float cmul = P.scale_log2 * ldexpf(1.f, 24 - sigma);
+      int k = 0;
+      for (int i = nwc; ok && i < nt; ++i, ++k) {
+        const int stage = k % kStages;
+        const int page0 = (t0 + i - nw) * kTilePages;
+        ok = warp_wait(&S.page_full[stage], k / kStages, gave_up);
+        if (ok && i >= kKBufs) ok = warp_wait(&S.s_full[(i - kKBufs) & 1], (i - kKBufs) >> 1, gave_up);
+        if (!ok) break;
+        fence_after();
+        const uint8_t* base = stages + (size_t)stage * kTilePages * pb;
+        const uint32_t tk = tq + kColK + (kKBufs == 2 ? (kKCols + 8) * (i & 1) : 0);
+        uint32_t alive = 0u;
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) {
+          const int pg = 2 * q + j;
+          const uint8_t* pgp = base + (size_t)pg * pb;
+          const int valid = S.pid[stage][pg] < 0 ? 0 : max(0, min(kPage, n_tok - kPage * (page0 + pg)));
+          alive |= ((1u << valid) - 1u) << (16 * j);
+          const uint32_t ta = tk + ((uint32_t)(16 * j) << 16);
+          // (a page that is not there leaves whatever the stage holds: its tokens are masked)
+          const uint4 w = lds16(pgp + 16 * lane);
+          const uint32_t kw[4] = {w.x, w.y, w.z, w.w};
+          const uint32_t kw10[4] = {w.x >> 10, w.y >> 10, w.z >> 10, w.w >> 10};
+          const uint8_t* sc = pgp + k_scale_off();
+          uint32_t v[16];
+          float ls[2];
+          if constexpr (NG == 1) {
+            uint32_t z[4];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const int tk = 2 * quad + 8 * x;
-              const uint32_t m = (tk < valid ? 0xffffu : 0u) | (tk + 1 < valid ? 0xffff0000u : 0u);
+              const __half2 dz = bits2h(*reinterpret_cast<const uint32_t*>(sc + 4 * (row + 8 * x)));
+              ls[x] = __low2float(dz);
+              const uint32_t zz = quad == 0 ? (uint32_t)__half_as_ushort(__hmul(__high2half(dz), __float2half_rn(0.03125f))) : 0u;
+              z[x] = zz;
+              z[2 + x] = zz;
+            }
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                a[j][2 * x] &= m;
-                a[j][2 * x + 1] &= m;
+            for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[4 * s + r] = code_pair(kw[r], kw10[r], 4 * hf + s);
+              tm_st_frag8(ta + 32 * hf, v);
+            }
+            tm_st_frag2(ta + kKCols, z);
+          } else {
+            uint32_t d2[2][NG];                             // Delta 2^k of both tokens, twice in a register
+            uint32_t z[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t dz[NG];
+#pragma unroll
+              for (int g = 0; g < NG; ++g) dz[g] = *reinterpret_cast<const uint32_t*>(sc + 4 * NG * (row + 8 * x) + 4 * g);
+              float dm = 0.f;
+#pragma unroll
+              for (int g = 0; g < NG; ++g) dm = fmaxf(dm, __low2float(bits2h(dz[g])));
+              // largest Delta 2^k in [2^14, 2^15): its product with 3 4^s 2^-24 stays in range, and
+              // a pair hi + lo is exact for groups down to 2^-10 of it
+              const int e = (int)(__float_as_uint(dm) >> 23) - 127;
+              const int kx = dm > 0.f && dm < INFINITY ? 14 - e : 0;
+              const float up = __int_as_float((kx + 127) << 23);
+              ls[x] = __int_as_float((127 - kx) << 23);
+              float dq = 0.f, zq = 0.f;
+#pragma unroll
+              for (int g = 0; g < NG; ++g) {
+                const __half2 dd = __float2half2_rn(__low2float(bits2h(dz[g])) * up);
+                d2[x][g] = h2bits(dd);
+                if (g == quad) {
+                  dq = __low2float(dd);
+                  zq = __high2float(bits2h(dz[g]));
+                }
+              }
+              const float prod = dq * zq * 0x1p-8f;         // (11 + 11 bits: exact)
+              const float hi = __half2float(__float2half_rn(prod));
+              if (quad < NG) {
+                z[x] = pack16(hi, prod - hi);
+                z[2 + x] = pack16(hi, 0.f);
               }
             }
+            tm_st_frag2(ta + kKCols, z);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  v[4 * s + r] = h2bits(__hmul2(bits2h(code_pair(kw[r], kw10[r], 4 * hf + s)), bits2h(d2[r & 1][(4 * hf + s) * NG / 8])));
+              tm_st_frag8(ta + 32 * hf, v);
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  v[4 * s + r] = h2bits(__hfma2(bits2h(code_pair(kw[r], kw10[r], 4 * hf + s)), bits2h(d2[r & 1][(4 * hf + s) * NG / 8]),
+                                                __hneg2(bits2h(v[4 * s + r]))));
+              tm_st_frag8(ta + 64 + 32 * hf, v);
+            }
+          }
+          if (P.l2) {
+            const __half* nm = reinterpret_cast<const __half*>(pgp + norm_off(NG, 0));
+            ls[0] *= __half2float(nm[row]);
+            ls[1] *= __half2float(nm[row + 8]);
+          }
+          if (quad == 0) {
+            S.lane_scale[i & 3][16 * pg + row] = ls[0] * cmul;
+            S.lane_scale[i & 3][16 * pg + row + 8] = ls[1] * cmul;
           }
         }
-        tm_st_frag2(tq + kColV + 8 * pg, a[0]);
-        tm_st_frag2(tq + (16u << 16) + kColV + 8 * pg, a[1]);
+        if (lane == 0) S.alive[i & 3][q] = alive;
+        wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(&S.k_full[i & 1]);
+          bar_arrive(&S.page_free[stage]);
+        }
       }
-      wait_st();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        bar_arrive(&S.v_full);
-        bar_arrive(&S.page_free[stage]);
+    } else {
+      // ---- values: channels 32 q .. 32 q + 31 of all pages; slots m = 2 q, 2 q + 1 of the words
+      uint32_t vmask[2], vone[2];
+      const int vshift = 2 * q + 1 <= 4 ? 0 : 10, vshift0 = 2 * q <= 4 ? 0 : 10;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int s = slot_pow(2 * q + j);
+        vmask[j] = 0x00030003u << (2 * s);
+        vone[j] = (uint32_t)(25 - 2 * s) << 10;             // 2^(10 - 2 s): the code's bits then count ones
+        vone[j] |= vone[j] << 16;
       }
-      ++k;
+      const int vg = 32 * q / (kHeadDim / NG);              // the group of these channels
+      int k = 0;
+      for (int i = nwc; ok && i < nt; ++i, ++k) {
+        const int stage = k % kStages;
+        const int page0 = (t0 + i - nw) * kTilePages;
+        ok = warp_wait(&S.page_full[stage], k / kStages, gave_up);
+        if (ok && i >= kVBufs) ok = warp_wait(&S.pv_done[(i - kVBufs) & 1], (i - kVBufs) >> 1, gave_up);
+        if (!ok) break;
+        fence_after();
+        const uint8_t* base = stages + (size_t)stage * kTilePages * pb;
+        const uint32_t tv = tq + kColV + (kVBufs == 2 ? 64 * (i & 1) : 0);
+        // every page of the tile is there in whole, except in a sequence's last tile (or next to a bad entry)
+        bool whole = n_tok >= kPage * (page0 + kTilePages);
+#pragma unroll
+        for (int pg = 0; pg < kTilePages; ++pg) whole = whole && S.pid[stage][pg] >= 0;
+#pragma unroll 1
+        for (int p4 = 0; p4 < kTilePages; p4 += 4) {
+          uint4 w[4];
+          uint32_t d[4][2], z[4][2];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint8_t* pgp = base + (size_t)(p4 + x) * pb;
+            w[x] = lds16(pgp + kCodeBytes + 16 * lane);
+            const uint8_t* dp = pgp + v_delta_off(NG, 2 * quad, vg);
+            d[x][0] = *reinterpret_cast<const uint32_t*>(dp);
+            d[x][1] = *reinterpret_cast<const uint32_t*>(dp + 16 * NG);
+            z[x][0] = *reinterpret_cast<const uint32_t*>(dp + 32 * NG);
+            z[x][1] = *reinterpret_cast<const uint32_t*>(dp + 48 * NG);
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) z[x][y] = h2bits(__hneg2(__hmul2(bits2h(d[x][y]), bits2h(z[x][y]))));
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t a[16];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t vw[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const __half2 c = __hsub2(bits2h(((vw[r] >> (j ? vshift : vshift0)) & vmask[j]) | vone[j]), bits2h(vone[j]));
+                a[4 * x + r] = h2bits(__hfma2(c, bits2h(d[x][r >> 1]), bits2h(z[x][r >> 1])));
+              }
+            }
+            if (!whole) {                                   // dead tokens: zeros, whatever the page holds there
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const int valid = S.pid[stage][p4 + x] < 0 ? 0 : max(0, min(kPage, n_tok - kPage * (page0 + p4 + x)));
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const int tk = 2 * quad + 8 * y;
+                  const uint32_t m = (tk < valid ? 0xffffu : 0u) | (tk + 1 < valid ? 0xffff0000u : 0u);
+                  a[4 * x + 2 * y] &= m;
+                  a[4 * x + 2 * y + 1] &= m;
+                }
+              }
+            }
+            tm_st_frag8(tv + ((uint32_t)(16 * j) << 16) + 8 * p4, a);
+          }
+        }
+        wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(&S.v_full[i & 1]);
+          bar_arrive(&S.page_free[stage]);
+        }
+      }
     }
   } else {
+    regs_inc<Regs<N>::kSoftmax>();
     // ---- softmax: token 32 q + lane of every tile, rows kCols half ..
     const int q = warp & 3, half = warp >> 2;
     const uint32_t tq = tb + ((uint32_t)(32 * q) << 16);
-    const int c0 = half * kCols;
-    float l[kCols];
+    const int c0 = half * kCols, tok = 32 * q + lane;
+    float2 l[kCols / 2];
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) l[j] = 0.f;
+    for (int j = 0; j < kCols / 2; ++j) l[j] = make_float2(0.f, 0.f);
     bool lost = false;
+    uint32_t unseen = (1u << (kCols / 32)) - 1u;            // lane j: rows c0 + 32 ch + j that have seen no token yet
+    bool force = true;                                      // ... there are such rows (all four warps agree)
 #pragma unroll 1
     for (int i = 0; i < nt; ++i) {
-      const bool ok = warp_wait(&S.s_full, i, gave_up) && !lost;
-      if (half_or(half, !ok)) break;                        // (one decision for the four warps)
+      const bool ok = warp_wait(&S.s_full[i & 1], i >> 1, gave_up) && !lost;
       fence_after();
-      const bool win = t0 + i < nw;
-      const float ls = S.lane_scale[i & 1][32 * q + lane];
-      const uint32_t alive = S.alive[i & 1][q];
-      const bool mine = (alive >> lane) & 1u;
+      float x[kCols];
+#pragma unroll
+      for (int ch = 0; ch < kCols / 32; ++ch) tm_ld32(tq + c0 + 32 * ch, x + 32 * ch);
+      const bool win = i < nwc;
+      const float ls = S.lane_scale[i & 3][tok];
+      const uint32_t alive = S.alive[i & 3][q];
       // the draft this token is (window tiles that reach into the drafts): else every row sees it
-      int node = -1;
-      if (win) {
-        const int w = (t0 + i) * kTile + 32 * q + lane;
-        node = (w < n_sink ? w : ring0 + w - n_sink) - st.L0;
-      }
       const bool drafts = win && (n_sink > st.L0 || (t0 + i + 1) * kTile > n_win - st.n);
       // P buffer free: PV(i - 2), or PV(i - 1) around window tiles (which use both buffers)
-      const int before = (win || (i > 0 && t0 + i - 1 < nw)) ? i - 1 : i - 2;
+      const int before = (win || (i > 0 && i - 1 < nwc)) ? i - 1 : i - 2;
+#pragma unroll
+      for (int ch = 0; ch < kCols / 32; ++ch) tm_wait32(x + 32 * ch);
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&S.s_free);
+      // scores less the reference
+      const float2 ls2 = make_float2(ls, ls);
+#pragma unroll
+      for (int j = 0; j < kCols; j += 4) {
+        const float4 m = *reinterpret_cast<const float4*>(&S.neg_m[c0 + j]);
+        const float2 a = __ffma2_rn(make_float2(x[j], x[j + 1]), ls2, make_float2(m.x, m.y));
+        const float2 b2 = __ffma2_rn(make_float2(x[j + 2], x[j + 3]), ls2, make_float2(m.z, m.w));
+        x[j] = a.x; x[j + 1] = a.y; x[j + 2] = b2.x; x[j + 3] = b2.y;
+      }
+      if (drafts || alive != 0xffffffffu) {                 // tokens that do not exist, drafts that a row does not see
+        const int w = (t0 + i) * kTile + tok;
+        const int node = win ? (w < n_sink ? w : ring0 + w - n_sink) - st.L0 : -1;
+        const bool mine = (alive >> lane) & 1u;
+        uint32_t see[kCols / 32];
+#pragma unroll
+        for (int ch = 0; ch < kCols / 32; ++ch) {
+          see[ch] = mine ? 0xffffffffu : 0u;
+          if (mine && drafts && node >= 0) {
+            see[ch] = 0u;
+            const int wd = (node >> 5) & (kNodeWords - 1);
+#pragma unroll 1
+            for (int j = 0; j < 32; ++j)
+              see[ch] |= ((S.seen[min((row0 + c0 + 32 * ch + j) >> P.gqa_log2, kNodes - 1)][wd] >> (node & 31)) & 1u) << j;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) x[j] = (see[j / 32] >> (j & 31)) & 1u ? x[j] : -INFINITY;
+      }
+      float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int j = 4; j < kCols; j += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          mx[e] = fmaxf(mx[e], x[j + e]);
+          if (j + 4 + e < kCols) mx[e] = fmaxf(mx[e], x[j + 4 + e]);
+        }
+      const bool over = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > 8.f;
       bool waited = before < 0;
+      if (half_or(half, over || force || !ok)) {
+        // ---- the references move to the rows' maxima so far (one decision for the four warps)
+        if (half_or(half, !ok)) break;
 #pragma unroll
-      for (int ch = 0; ch < kChunks; ++ch) {
-        const int cc = c0 + 32 * ch;
-        float x[32];
-        auto scores = [&]() {
-          tm_ld32(tq + cc, x);
+        for (int j = 0; j < kCols; j += 8) {
+          float y[8];
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(&S.neg_m[cc + j]);
-            x[j] = fmaf(x[j], ls, m.x);
-            x[j + 1] = fmaf(x[j + 1], ls, m.y);
-            x[j + 2] = fmaf(x[j + 2], ls, m.z);
-            x[j + 3] = fmaf(x[j + 3], ls, m.w);
-          }
-        };
-        auto hide = [&](float (&y)[32]) {                   // tokens that do not exist or a row does not see
-          if (alive != 0xffffffffu) {
+          for (int e = 0; e < 8; ++e) y[e] = x[j + e];
+          const float top = reduce_columns(y, lane, [](float a, float b2) { return fmaxf(a, b2); });
+          if (lane < 8) S.red[q][c0 + j + lane] = top;
+        }
+        half_sync(half);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) y[j] = mine ? y[j] : -INFINITY;
-          }
-          if (drafts) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int nd = min((row0 + cc + j) >> P.gqa_log2, kNodes - 1);
-              if (node >= 0 && !((S.seen[nd][(node >> 5) & (kNodeWords - 1)] >> (node & 31)) & 1u)) y[j] = -INFINITY;
-            }
-          }
-        };
-        scores();
-        hide(x);
-        float mx = x[0];
-#pragma unroll
-        for (int j = 1; j < 32; ++j) mx = fmaxf(mx, x[j]);
-        if (half_or(half, mx > 8.f)) {
-          // ---- the reference of these 32 rows moves to their maxima so far
-          tm_ld32(tq + cc, x);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] *= ls;
-          hide(x);
-          const float top = reduce_columns(x, lane, [](float a, float b2) { return fmaxf(a, b2); });
-          S.red[q][cc + lane] = top;
-          half_sync(half);
-          const float all = fmaxf(fmaxf(S.red[0][cc + lane], S.red[1][cc + lane]), fmaxf(S.red[2][cc + lane], S.red[3][cc + lane]));
-          const float old = -S.neg_m[cc + lane], now = fmaxf(old, all);
-          half_sync(half);                                  // (everyone has read the old reference)
+        for (int ch = 0; ch < kCols / 32; ++ch) {
+          const int c = c0 + 32 * ch + lane;
+          const float up = fmaxf(fmaxf(S.red[0][c], S.red[1][c]), fmaxf(S.red[2][c], S.red[3][c]));
+          // over the old reference: a first token sets it, later ones only raise it
+          const bool fresh = (unseen >> ch) & 1u, any = up > -INFINITY;
+          const float by = fresh ? (any ? up : 0.f) : fmaxf(up, 0.f);
+          if (any) unseen &= ~(1u << ch);
           if (q == 0) {
-            S.neg_m[cc + lane] = -now;
-            S.alpha[cc + lane] = ex2(old - now);
+            S.neg_m[c] -= by;
+            S.delta[c] = -by;
+            S.alpha[c] = fresh ? 0.f : ex2(-by);
           }
-          half_sync(half);
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 al = *reinterpret_cast<const float4*>(&S.alpha[cc + j]);
-            l[32 * ch + j] *= al.x;
-            l[32 * ch + j + 1] *= al.y;
-            l[32 * ch + j + 2] *= al.z;
-            l[32 * ch + j + 3] *= al.w;
-          }
-          if (i > 0) {                                      // O so far, once PV(i - 1) is done
-            if (!warp_wait(&S.pv_done[(i - 1) & 1], (i - 1) >> 1, gave_up)) lost = true;
-            fence_after();
-            tm_ld32(tq + kColO + cc, x);
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 al = *reinterpret_cast<const float4*>(&S.alpha[cc + j]);
-              x[j] *= al.x;
-              x[j + 1] *= al.y;
-              x[j + 2] *= al.z;
-              x[j + 3] *= al.w;
-            }
-            tm_st32(tq + kColO + cc, x);
-            wait_st();
-            fence_before();
-            waited = true;
-          }
-          scores();
-          hide(x);
         }
-        if (ch == kChunks - 1) {                            // S is read
+        force = __any_sync(0xffffffffu, unseen != 0u);
+        half_sync(half);
+#pragma unroll
+        for (int j = 0; j < kCols; j += 4) {
+          const float4 al = *reinterpret_cast<const float4*>(&S.alpha[c0 + j]);
+          const float4 de = *reinterpret_cast<const float4*>(&S.delta[c0 + j]);
+          l[j / 2] = __fmul2_rn(l[j / 2], make_float2(al.x, al.y));
+          l[j / 2 + 1] = __fmul2_rn(l[j / 2 + 1], make_float2(al.z, al.w));
+          x[j] += de.x; x[j + 1] += de.y; x[j + 2] += de.z; x[j + 3] += de.w;
+        }
+        if (i > 0) {                                        // O so far, once PV(i - 1) is done
+          if (!warp_wait(&S.pv_done[(i - 1) & 1], (i - 1) >> 1, gave_up)) lost = true;
+          fence_after();
+#pragma unroll 1
+          for (int j = 0; j < kCols; j += 8) {
+            float o[8];
+            tm_ld8(tq + kColO + c0 + j, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] *= S.alpha[c0 + j + e];
+            tm_st8(tq + kColO + c0 + j, o);
+          }
+          wait_st();
           fence_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(&S.s_free);
-        }
-        if (!waited) {
-          if (!warp_wait(&S.pv_done[before & 1], before >> 1, gave_up)) lost = true;
           waited = true;
         }
+        half_sync(half);                                    // (alpha and delta are read before they change again)
+      }
+      if (!waited && !warp_wait(&S.pv_done[before & 1], before >> 1, gave_up)) lost = true;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          x[j] = ex2(x[j]);
-          l[32 * ch + j] += x[j];
-        }
-        // P[token][row], 8 rows a chunk of 16 bytes
-        const int tok = 32 * q + lane;
-        uint8_t* dst = sm + L::kP + (win ? 0 : (i & 1) * L::kPBytes) + (cc >> 6) * kSlab + (tok >> 3) * 1024 + (tok & 7) * 128;
+      for (int j = 0; j < kCols; j += 2) {
+        x[j] = ex2(x[j]);
+        x[j + 1] = ex2(x[j + 1]);
+        l[j / 2] = __fadd2_rn(l[j / 2], make_float2(x[j], x[j + 1]));
+      }
+      // P[token][row], 8 rows a chunk of 16 bytes: a lane's chunks are 16 (j ^ (token % 8)) apart
+      const uint32_t p_s = saddr(sm + L::kP) + (c0 >> 6) * kSlab + (tok >> 3) * 1024 + (tok & 7) * 128;
+      const uint32_t sw = (uint32_t)(((c0 & 63) >> 3) ^ (tok & 7)) << 4;
+      if (!win) {
+        const uint32_t at = p_s + (i & 1) * L::kPBytes;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int at = ((((cc & 63) >> 3) + j) ^ (tok & 7)) << 4;
-          if (!win) {
-            *reinterpret_cast<uint4*>(dst + at) = make_uint4(pack16(x[8 * j], x[8 * j + 1]), pack16(x[8 * j + 2], x[8 * j + 3]),
-                                                             pack16(x[8 * j + 4], x[8 * j + 5]), pack16(x[8 * j + 6], x[8 * j + 7]));
-          } else {
-            uint32_t hi[4], lo[4];
+        for (int j = 0; j < kCols / 8; ++j)
+          sts16(at + (sw ^ (16u * j)), pack16(x[8 * j], x[8 * j + 1]), pack16(x[8 * j + 2], x[8 * j + 3]),
+                pack16(x[8 * j + 4], x[8 * j + 5]), pack16(x[8 * j + 6], x[8 * j + 7]));
+      } else {
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {              // bf16 hi, then what it leaves
+#pragma unroll
+          for (int j = 0; j < kCols / 8; ++j) {
+            uint32_t hi[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float a0 = x[8 * j + 2 * e], a1 = x[8 * j + 2 * e + 1];
+              float &a0 = x[8 * j + 2 * e], &a1 = x[8 * j + 2 * e + 1];
               hi[e] = packb16(a0, a1);
-              lo[e] = packb16(a0 - __uint_as_float(hi[e] << 16), a1 - __uint_as_float(hi[e] & 0xffff0000u));
+              a0 -= __uint_as_float(hi[e] << 16);
+              a1 -= __uint_as_float(hi[e] & 0xffff0000u);
             }
-            *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(dst + L::kPBytes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            sts16(p_s + part * L::kPBytes + (sw ^ (16u * j)), hi[0], hi[1], hi[2], hi[3]);
           }
         }
       }
@@ -967,43 +1047,36 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     }
     // ---- sums over the tile's tokens: lanes, then quadrants
 #pragma unroll
-    for (int ch = 0; ch < kChunks; ++ch) {
-      float y[32];
+    for (int j = 0; j < kCols; j += 8) {
+      float y[8];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) y[j] = l[32 * ch + j];
+      for (int e = 0; e < 8; ++e) y[e] = e & 1 ? l[(j + e) / 2].y : l[(j + e) / 2].x;
       const float sum = reduce_columns(y, lane, [](float a, float b2) { return a + b2; });
-      S.red[q][c0 + 32 * ch + lane] = sum;
+      if (lane < 8) S.red[q][c0 + j + lane] = sum;
     }
     half_sync(half);
     bool ok = nt > 0 && !lost;
     if (ok) ok = warp_wait(&S.pv_done[(nt - 1) & 1], (nt - 1) >> 1, gave_up);
     fence_after();
     if (nt == 0 || ok) {
+#pragma unroll 1
+      for (int j = 0; j < kCols && c0 + j < ncol; j += 8) {
+        float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (nt > 0) tm_ld8(tq + kColO + c0 + j, o);
 #pragma unroll
-      for (int ch = 0; ch < kChunks; ++ch) {
-        const int cc = c0 + 32 * ch;
-        float o[32];
-        if (nt > 0) {
-          tm_ld32(tq + kColO + cc, o);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int c = cc + j;
+        for (int e = 0; e < 8; ++e) {
+          const int c = c0 + j + e;
           if (c < ncol) {
             const float sum = S.red[0][c] + S.red[1][c] + S.red[2][c] + S.red[3][c];
             const size_t r = out_row(c);
-            const float ov = o[j];
             if (P.splits == 1) {
-              const float v = sum > 0.f ? ov / sum : (sum == 0.f ? 0.f : ov * sum);
-              P.out[r * kHeadDim + 32 * q + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+              const float v = sum > 0.f ? __fdividef(o[e], sum) : (sum == 0.f ? 0.f : o[e] * sum);
+              P.out[r * kHeadDim + tok] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
             } else {
               float* rec = P.part + (r * P.splits + split) * kRec;
-              rec[4 + 32 * q + lane] = ov;
-              if (q == 0 && lane == 0) {
-                rec[0] = nt > 0 ? -S.neg_m[c] : -1e30f;
+              rec[4 + tok] = o[e];
+              if (tok == 0) {
+                rec[0] = sum != 0.f ? -S.neg_m[c] : -1e30f;   // (a row that saw nothing here)
                 rec[1] = sum;
               }
             }
@@ -1154,8 +1227,7 @@ extern "C" int kvq_launch_attn_tree(const kvq_config* cfg, const kvq_cache* cach
   const int ng = kHeadDim / cfg->group_size;
   void (*kern)(const TreeParams) = s.n == 64 ? (ng == 1 ? attn_tree_kernel<64, 1> : ng == 2 ? attn_tree_kernel<64, 2> : attn_tree_kernel<64, 4>)
                                              : (ng == 1 ? attn_tree_kernel<128, 1> : ng == 2 ? attn_tree_kernel<128, 2> : attn_tree_kernel<128, 4>);
-  const size_t smem = (s.n == 64 ? Layout<64>::kPages + sizeof(TreeShared<64>) : Layout<128>::kPages + sizeof(TreeShared<128>)) +
-                      2 * (size_t)kTilePages * P.page_bytes;
+  const size_t smem = s.n == 64 ? Layout<64>::kEnd + sizeof(TreeShared<64>) : Layout<128>::kEnd + sizeof(TreeShared<128>);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ERR_CUDA;
   static std::mutex mu;
@@ -1164,8 +1236,10 @@ extern "C" int kvq_launch_attn_tree(const kvq_config* cfg, const kvq_cache* cach
     std::lock_guard<std::mutex> lock(mu);
     const int vi = (s.n == 64 ? 0 : 3) + (ng == 1 ? 0 : ng == 2 ? 1 : 2);
     if (!(done[vi] & (1ull << dev))) {
-      const size_t most = smem - 2 * (size_t)kTilePages * P.page_bytes + 2 * (size_t)kTilePages * page_head_bytes(cfg->group_size, 1, 0);
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess) return KVQ_ERR_CUDA;
+      // (the register split counts on what the kernel launches with: a warpgroup would wait for ever)
+      cudaFuncAttributes fa;
+      if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs < kRegsLaunch) return KVQ_ERR_CUDA;
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return KVQ_ERR_CUDA;
       done[vi] |= 1ull << dev;
     }
   }
