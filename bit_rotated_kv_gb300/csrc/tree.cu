@@ -47,17 +47,20 @@ constexpr int kNodes = KVQ_TREE_MAX_NODES;
 constexpr int kNodeWords = kNodes / 32;
 constexpr int kTile = 128;                       // tokens of a tile
 constexpr int kTilePages = kTile / kPage;
-constexpr int kSmWarps = 8;                      // softmax; then 4 warps for keys, 4 for values, 4 more
-constexpr int kKeyWarp = 8, kValWarp = 12, kMmaWarp = 16, kPageWarp = 17;
-constexpr int kThreadsT = 32 * 20;               // (whole warpgroups: registers are handed over by warpgroup)
+constexpr int kSmWarps = 8;                      // softmax; then 4 warps for keys, 8 for values, 4 more
+constexpr int kKeyWarp = 8, kValWarp = 12, kValWarps = 8, kQkWarp = 20, kPageWarp = 21, kPvWarp = 22, kSeenWarp = 23;
+constexpr int kThreadsT = 32 * 24;               // (whole warpgroups: registers are handed over by warpgroup)
 constexpr int kStages = 4;                       // page tiles in flight
-// Registers a thread by role, of the 96 that 640 threads launch with.
-constexpr int kRegsLaunch = 96;
+// Registers a thread by role, of the 80 that 768 threads launch with.
+constexpr int kRegsLaunch = 80;
 template <int N>
 struct Regs {
-  static constexpr int kSoftmax = N == 128 ? 152 : 112, kExpand = N == 128 ? 64 : 88, kIssue = N == 128 ? 40 : 56;
-  static_assert(256 * kSoftmax + 256 * kExpand + 128 * kIssue <= kThreadsT * kRegsLaunch, "register split");
+  static constexpr int kSoftmax = N == 128 ? 152 : 104, kKeys = N == 128 ? 56 : 72, kValues = N == 128 ? 40 : 56,
+                       kIssue = N == 128 ? 32 : 48;
+  static_assert(256 * kSoftmax + 128 * kKeys + 256 * kValues + 128 * kIssue <= kThreadsT * kRegsLaunch, "register split");
 };
+
+constexpr int kWinCost = 3;
 constexpr int kRec = 4 + kHeadDim;               // (m, l, -, -, o[d]) of a partial
 constexpr int kSpin = 1 << 15, kSuspend = 20000;  // a wait gives up after that many rounds of at most 20 us
 constexpr uint32_t kTmem = 512;
@@ -103,18 +106,19 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Bounded wait of a whole warp, decided by lane 0 (the warp stays together); gives up as well when
-// another warp has.  Inline (a call has no place beside setmaxnreg) and small.
+// Bounded wait of a whole warp; gives up as well when another warp has.  Inline (a call has no place
+// beside setmaxnreg) and small.
 __device__ __forceinline__ bool warp_wait(uint64_t* b, int phase, volatile int* gave_up) {
-  bool ok = __all_sync(0xffffffffu, bar_try(b, (uint32_t)(phase & 1)));
+  bool ok = bar_try(b, (uint32_t)(phase & 1));
+  if (!ok) {
 #pragma unroll 1
-  for (int i = 0; !ok && i < kSpin; ++i) {
-    ok = __any_sync(0xffffffffu, bar_try(b, (uint32_t)(phase & 1)));
-    if (!ok && __any_sync(0xffffffffu, *gave_up)) return false;
+    for (int i = 0; i < kSpin && !ok; ++i) {
+      ok = bar_try(b, (uint32_t)(phase & 1));
+      if (!ok && *gave_up) break;
+    }
+    if (!ok) *gave_up = 1;
   }
-  if (!ok) *gave_up = 1;
-  __syncwarp();
-  return ok;
+  return __all_sync(0xffffffffu, ok);
 }
 // ... for what is in flight when a wait was given up (whatever the outcome)
 __device__ __forceinline__ void settle(uint64_t* b, int phase) {
@@ -128,22 +132,14 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       "l"(src), "r"(bytes), "r"(saddr(bar))
       : "memory");
 }
+__device__ __forceinline__ void async_copy16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(saddr(dst)), "l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// barrier of the 128 threads of one half's four softmax warps, with an OR of a predicate
-__device__ __forceinline__ bool half_or(int half, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)v), "r"(1 + half)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ void half_sync(int half) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory"); }
-__device__ __forceinline__ void dq_sync() { asm volatile("barrier.cta.sync 3, 128;" ::: "memory"); }
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 4, 256;" ::: "memory"); }
 // one lane of a converged warp: the code around it stays uniform, so descriptors are formed in uniform
 // registers (issued from a divergent lane an MMA takes 53 clocks, so 20 .. 33 at N = 32 .. 64 are lost)
 __device__ __forceinline__ bool elect() {
@@ -184,18 +180,26 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)) : "memory");
 }
 #define KVQ_IO8(c, b) c(v[b]), c(v[b + 1]), c(v[b + 2]), c(v[b + 3]), c(v[b + 4]), c(v[b + 5]), c(v[b + 6]), c(v[b + 7])
-// 32 columns of this warp's lanes -> registers, not waited for
-__device__ __forceinline__ void tm_ld32(uint32_t a, float* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : KVQ_IO8("=f", 0), KVQ_IO8("=f", 8), KVQ_IO8("=f", 16), KVQ_IO8("=f", 24)
-      : "r"(a));
-}
-// waits for this thread's loads; the registers pass through so that no use moves above it
-__device__ __forceinline__ void tm_wait32(float* v) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : KVQ_IO8("+f", 0), KVQ_IO8("+f", 8), KVQ_IO8("+f", 16), KVQ_IO8("+f", 24)::"memory");
+// C columns of this warp's lanes -> registers
+template <int C>
+__device__ __forceinline__ void tm_ld(uint32_t a, float (&v)[C]) {
+  if constexpr (C == 32)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n tcgen05.wait::ld.sync.aligned;"
+        : KVQ_IO8("=f", 0), KVQ_IO8("=f", 8), KVQ_IO8("=f", 16), KVQ_IO8("=f", 24)
+        : "r"(a)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
+        "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n tcgen05.wait::ld.sync.aligned;"
+        : KVQ_IO8("=f", 0), KVQ_IO8("=f", 8), KVQ_IO8("=f", 16), KVQ_IO8("=f", 24), KVQ_IO8("=f", 32), KVQ_IO8("=f", 40),
+          KVQ_IO8("=f", 48), KVQ_IO8("=f", 56)
+        : "r"(a), "r"(a + 32)
+        : "memory");
 }
 __device__ __forceinline__ void tm_ld8(uint32_t a, float (&v)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : KVQ_IO8("=f", 0) : "r"(a));
@@ -217,6 +221,11 @@ __device__ __forceinline__ void tm_st_frag8(uint32_t a, const uint32_t (&v)[16])
 __device__ __forceinline__ void tm_st_frag2(uint32_t a, const uint32_t (&v)[4]) {
   asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%4], {%0,%1,%2,%3};" ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(a)
                : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -287,9 +296,10 @@ struct Layout {          // dynamic shared memory, from a 1024-byte boundary
   static constexpr int kP = kQb + 2 * N * 128;              // P, two buffers of N / 64 slabs
   static constexpr int kPBytes = N / 64 * kSlab;
   static constexpr int kZ = kP + 2 * kPBytes;               // zero-point B operand: N x 16 fp16
+  static constexpr int kZa = kZ + N * 32;                   // ... and A: 128 tokens x 16 fp16, two buffers
   // window K and V rows, two slabs each; where a CTA's window tiles are done (or it has none), the
   // page stages
-  static constexpr int kK = (kZ + N * 32 + 1023) / 1024 * 1024;
+  static constexpr int kK = (kZa + 2 * kTile * 32 + 1023) / 1024 * 1024;
   static constexpr int kV = kK + 2 * kSlab;
   static constexpr int kPages = kK;
   static constexpr int kEnd = kV + 2 * kSlab;
@@ -298,29 +308,27 @@ struct Layout {          // dynamic shared memory, from a 1024-byte boundary
 
 template <int N>
 struct TreeShared {
-  __align__(16) uint64_t page_full[kStages], page_free[kStages], k_full[2], v_full[2], s_full[2], s_free, p_full[2],
+  __align__(16) uint64_t page_full[kStages], page_free[kStages], q_full, seen_full, vote[2], meet[2], k_full[2], v_full[2], s_full[2], s_free[2], p_full[2],
       pv_done[2];
   uint32_t tmem;
   int gave_up;
-  int item[3];                     // sequence, row tile, found
   int pid[kStages][kTilePages];
   float lane_scale[4][kTile];
   uint32_t alive[4][4];            // tokens of a tile that exist, by lane quadrant
   __align__(16) float neg_m[N];    // minus the reference of every row
-  __align__(16) float alpha[N];    // a moved reference: factor of what is summed, and what the scores less it change by
-  __align__(16) float delta[N];
-  float red[4][N];                 // per-quadrant maxima; at the end the sums
-  uint32_t seen[kNodes][kNodeWords];   // ancestors of every node, itself among them
-  float amax[kThreadsT / 32];
-};
-struct Doubling {                  // of the ancestors, at set-up (where the pages go afterwards)
-  int jump[2][kNodes];
-  uint32_t seen[kNodes][kNodeWords];
+  __align__(16) float alpha[N];    // a moved reference: factor of what is summed so far
+  float red[4][N];                 // per-quadrant maxima; at the end parts of the sums
+  int moves[2];                    // the last tile (+ 1) in which a half's references have to move
+  __align__(16) uint32_t seen[kNodes][kNodeWords];   // ancestors of every node, itself among them
+  int jump[kNodes];                // (while they are found: the next one)
+  int whole[kStages];              // every page of the tile is there in whole
+  int row[N];                      // output rows: global row * Hq + query head
+  float amax[kSmWarps];
 };
 
+static_assert(kNodeWords == 4 && offsetof(TreeShared<128>, seen) % 16 == 0 && offsetof(TreeShared<64>, seen) % 16 == 0, "ancestor rows");
 static_assert(offsetof(TreeShared<128>, neg_m) % 16 == 0 && offsetof(TreeShared<128>, alpha) % 16 == 0 &&
                   offsetof(TreeShared<64>, neg_m) % 16 == 0 && offsetof(TreeShared<64>, alpha) % 16 == 0 &&
-                  offsetof(TreeShared<128>, delta) % 16 == 0 && offsetof(TreeShared<64>, delta) % 16 == 0 &&
                   Layout<64>::kEnd % 1024 == 0 && Layout<128>::kEnd % 1024 == 0, "vector loads");
 static_assert(Layout<128>::kEnd + sizeof(TreeShared<128>) <= 227 * 1024, "shared memory of an SM");
 
@@ -328,12 +336,11 @@ template <int N, int NG>
 __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_constant__ TreeParams P) {
   using L = Layout<N>;
   constexpr int kCols = N / 2;                              // rows of a softmax warp
-  // TMEM columns: S, O, then the key operand (64 or 128, and 8 for zero points) and the value
-  // operand, twice each where the 512 columns allow: keys are waited for by the shorter product
-  // when they are codes, and are the longer ones to expand when they are pairs
+  // TMEM columns: O, S twice (the next product runs while the softmax reads the last), then the key
+  // operand (64, or 128 as pairs) and the value operand (64), twice where there is room
   constexpr int kKCols = NG == 1 ? 64 : 128;
-  constexpr int kKBufs = N == 64 ? 2 : 1, kVBufs = NG == 1 ? 2 : 1;
-  constexpr uint32_t kColO = N, kColK = 2 * N, kColV = 2 * N + kKBufs * (kKCols + 8);
+  constexpr int kKBufs = N == 128 ? 1 : 2, kVBufs = N == 64 && NG == 1 ? 2 : 1;
+  constexpr uint32_t kColO = 0, kColS = N, kColK = 3 * N, kColV = kColK + kKBufs * kKCols;
   static_assert(kColV + kVBufs * 64 <= 512, "TMEM columns");
   constexpr uint32_t kIdescF16 = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
   constexpr uint32_t kIdescPV = kIdescF16 | (1u << 16);
@@ -350,47 +357,32 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     return;
   }
 
-  // ---- this CTA's row tile: item blockIdx.x counts the sequences' row tiles in order
+  // ---- this CTA's row tile: item blockIdx.x counts the sequences' row tiles in order (every warp
+  // looks it up for itself)
   const int split = blockIdx.z, h = blockIdx.y;
-  if (tid == 0) {
-    S.item[2] = 0;
-    S.gave_up = 0;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int before = 0;
-    for (int b0 = 0; b0 < P.batch; b0 += 32) {
-      const int mine = b0 + lane < P.batch ? row_tiles<N>(P, b0 + lane) : 0;
-      int upto = mine;
+  int b = -1, rt = 0;
+  for (int b0 = 0, before = 0; b0 < P.batch && b < 0; b0 += 32) {
+    const int mine = b0 + lane < P.batch ? row_tiles<N>(P, b0 + lane) : 0;
+    int upto = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += t;
-      }
-      const int start = before + upto - mine;
-      if ((int)blockIdx.x >= start && (int)blockIdx.x < start + mine) {
-        S.item[0] = b0 + lane;
-        S.item[1] = blockIdx.x - start;
-        S.item[2] = 1;
-      }
-      before += __shfl_sync(0xffffffffu, upto, 31);
-      if (before > (int)blockIdx.x) break;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += t;
     }
-    if (lane == 0 && blockIdx.x == 0 && h == 0 && split == 0 &&
-        (P.cu_rows[0] != 0 || P.cu_rows[P.batch] != P.n_rows))
-      set_status(P.status, KVQ_ERR_BOUNDS);
+    const unsigned past = __ballot_sync(0xffffffffu, before + upto > (int)blockIdx.x);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      b = b0 + at;
+      rt = (int)blockIdx.x - before - __shfl_sync(0xffffffffu, upto - mine, at);
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
   }
-  __syncthreads();
-  if (!S.item[2]) return;
-  const int b = S.item[0];
+  if (tid == 0 && blockIdx.x == 0 && h == 0 && split == 0 && (P.cu_rows[0] != 0 || P.cu_rows[P.batch] != P.n_rows))
+    set_status(P.status, KVQ_ERR_BOUNDS);
+  if (b < 0) return;
   const SeqState st = seq_state(P, b);
-  const int row0 = S.item[1] * N;
+  const int row0 = rt * N;
   const int ncol = min(N, st.n * P.gqa - row0);
-  // global row and query head of column c
-  auto out_row = [&](int c) {
-    const int r = row0 + c;
-    return (size_t)(st.first + (r >> P.gqa_log2)) * (P.hkv * P.gqa) + h * P.gqa + (r & (P.gqa - 1));
-  };
   if (st.bad) {                                             // zeros (the merge writes them when there are splits)
     if (tid == 0) set_status(P.status, KVQ_ERR_BOUNDS);
     if (P.splits == 1 && st.first >= 0)
@@ -413,145 +405,61 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     np = P.mp;
   }
   const int nw = (n_win + kTile - 1) / kTile, ni = (np + kTilePages - 1) / kTilePages;
-  const int t0 = (int)((long long)(nw + ni) * split / P.splits), t1 = (int)((long long)(nw + ni) * (split + 1) / P.splits);
+  // equal shares of the work, a window tile taken as kWinCost page tiles (its rows are loaded, not
+  // streamed, and its P is a pair)
+  auto first_tile = [&](int k) {
+    const int at = (int)((long long)(kWinCost * nw + ni) * k / P.splits);
+    return at < kWinCost * nw ? (at + kWinCost - 1) / kWinCost : nw + at - kWinCost * nw;
+  };
+  const int t0 = first_tile(split), t1 = first_tile(split + 1);
   const int nt = t1 - t0;
 
   // ---- set-up: barriers, TMEM, q' operands, ancestors
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       bar_init(&S.page_full[i], 1);
-      bar_init(&S.page_free[i], 8);
+      bar_init(&S.page_free[i], 4 + kValWarps);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&S.k_full[i], 4);
-      bar_init(&S.v_full[i], 4);
+      bar_init(&S.v_full[i], kValWarps);
       bar_init(&S.s_full[i], 1);
+      bar_init(&S.s_free[i], kSmWarps);
       bar_init(&S.p_full[i], kSmWarps);
       bar_init(&S.pv_done[i], 1);
     }
-    bar_init(&S.s_free, kSmWarps);
+    bar_init(&S.q_full, kSmWarps);
+    bar_init(&S.seen_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&S.vote[i], 4);
+      bar_init(&S.meet[i], 4);
+      S.moves[i] = 0;
+    }
+    S.gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&S.tmem)), "r"(kTmem) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  for (int c = tid; c < N; c += kThreadsT) S.neg_m[c] = 0.f;
-  // bf16 rows: 16-byte chunk j of row c at slab j / 8, swizzled
-  float amax = 0.f;
-#pragma unroll 1
-  for (int i = tid; i < N * 16; i += kThreadsT) {
-    const int c = i >> 4, j = i & 15;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (c < ncol) v = reinterpret_cast<const uint4*>(P.q + out_row(c) * kHeadDim)[j];
-    *reinterpret_cast<uint4*>(sm + L::kQb + (j >> 3) * N * 128 + (c >> 3) * 1024 + (c & 7) * 128 + (((j & 7) ^ (c & 7)) << 4)) = v;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      amax = fmaxf(amax, fabsf(__uint_as_float(w[k] << 16)));
-      amax = fmaxf(amax, fabsf(__uint_as_float(w[k] & 0xffff0000u)));
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (lane == 0) S.amax[warp] = amax;
-  // parents, checked; ancestors by doubling (the key warps: one thread a node)
-  if (warp >= kKeyWarp && warp < kKeyWarp + 4) {
-    const int i = tid - 32 * kKeyWarp;
-    int up = -1;
-    if (i < st.n) {
-      up = P.parent[st.first + i];
-      if (up >= i || up < -1) {
-        set_status(P.status, KVQ_ERR_BOUNDS);
-        up = -1;
-      }
-    }
-    Doubling& D = *reinterpret_cast<Doubling*>(sm + L::kPages);
-    uint32_t mine[kNodeWords];
-#pragma unroll
-    for (int w = 0; w < kNodeWords; ++w) mine[w] = (i >> 5) == w ? 1u << (i & 31) : 0u;
-    // after round r: the 2^r nearest ancestors (itself counted), and where the next one is
-#pragma unroll 1
-    for (int r = 0; (1 << r) <= kNodes; ++r) {
-      uint32_t(*dst)[kNodeWords] = r & 1 ? D.seen : S.seen;
-#pragma unroll
-      for (int w = 0; w < kNodeWords; ++w) dst[i][w] = mine[w];
-      D.jump[r & 1][i] = up;
-      dq_sync();
-      if ((1 << r) == kNodes) break;
-      if (up >= 0) {
-#pragma unroll
-        for (int w = 0; w < kNodeWords; ++w) mine[w] |= dst[up][w];
-        up = D.jump[r & 1][up];
-      }
-    }
-#pragma unroll
-    for (int w = 0; w < kNodeWords; ++w) S.seen[i][w] = mine[w];
-  }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tb = S.tmem;
-  int sigma = 0;
-  {
-    float a = 0.f;
-#pragma unroll
-    for (int w = 0; w < kThreadsT / 32; ++w) a = fmaxf(a, S.amax[w]);
-    if (a > 0.f && a < INFINITY) {
-      int e2;
-      frexpf(a, &e2);
-      sigma = 14 - e2;                                      // a 2^sigma < 2^14
-    }
-  }
-  // fp16 rows, channel slot s scaled by 4^-s for the codes that carry 4^s
-#pragma unroll 1
-  for (int i = tid; i < N * 16; i += kThreadsT) {
-    const int c = i >> 4, j = i & 15;
-    const uint32_t off = (j >> 3) * N * 128 + (c >> 3) * 1024 + (c & 7) * 128 + (((j & 7) ^ (c & 7)) << 4);
-    const uint4 v = lds16(sm + L::kQb + off);
-    const float f = ldexpf(1.f, sigma - 2 * slot_pow(j >> 1));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t o[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = pack16(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
-    *reinterpret_cast<uint4*>(sm + L::kQ + off) = make_uint4(o[0], o[1], o[2], o[3]);
-  }
-  // zero-point operand, row c: slots 2 g, 2 g + 1: -sum of group g (hi), slot 8 + 2 g: its lo
-  for (int c = tid; c < N; c += kThreadsT) {
-    uint32_t z[8];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float acc = 0.f;
-      if (g < NG)
-#pragma unroll 1
-        for (int j = g * (16 / NG); j < (g + 1) * (16 / NG); ++j) {
-          const uint4 v = lds16(sm + L::kQb + (j >> 3) * N * 128 + (c >> 3) * 1024 + (c & 7) * 128 + (((j & 7) ^ (c & 7)) << 4));
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc += __uint_as_float(w[k] << 16) + __uint_as_float(w[k] & 0xffff0000u);
-        }
-      const float v = -acc * ldexpf(1.f, NG == 1 ? sigma - 19 : sigma - 16);
-      const float hi = __half2float(__float2half_rn(v));
-      z[g] = pack16(hi, hi);
-      z[4 + g] = pack16(v - hi, 0.f);
-    }
-    *reinterpret_cast<uint4*>(sm + L::kZ + (c >> 3) * 128 + (c & 7) * 16) = make_uint4(z[0], z[1], z[2], z[3]);
-    *reinterpret_cast<uint4*>(sm + L::kZ + N * 16 + (c >> 3) * 128 + (c & 7) * 16) = make_uint4(z[4], z[5], z[6], z[7]);
-  }
-  fence_async();
-  __syncthreads();
 
   const int pb = P.page_bytes;
   const int nwc = max(0, min(t1, nw) - t0);                 // this CTA's window tiles: its first ones
   uint8_t* stages = sm + L::kPages;
-  if (warp >= kMmaWarp) {
+  if (warp >= kQkWarp) {
     regs_dec<Regs<N>::kIssue>();
     if (warp == kPageWarp) {
       // ---- pages
       const int32_t* tab = P.page_table + (size_t)b * P.max_pages;
       int k = 0;                                            // page tiles streamed
       bool ok = true;
-      if (nwc > 0 && nwc < nt) ok = warp_wait(&S.pv_done[(nwc - 1) & 1], (nwc - 1) >> 1, gave_up);
+      // the window rows' space is free once the last of their products is done (every one is waited for:
+      // a parity alone says nothing about a phase whose predecessor may not be over)
+      for (int i = 0; ok && i < nwc && nwc < nt; ++i) ok = warp_wait(&S.pv_done[i & 1], i >> 1, gave_up);
       for (int i = nwc; ok && i < nt; ++i, ++k) {
         const int stage = k % kStages;
         const int p = (t0 + i - nw) * kTilePages + lane;
@@ -569,6 +477,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         }
         if (lane < kTilePages) S.pid[stage][lane] = pid;
         const int live = __popc(__ballot_sync(0xffffffffu, pid >= 0));
+        if (lane == 0) S.whole[stage] = live == kTilePages && n_tok >= kPage * ((t0 + i - nw + 1) * kTilePages);
         __syncwarp();
         if (lane == 0) {
           if (live) bar_expect(&S.page_full[stage], (uint32_t)(live * pb));
@@ -582,74 +491,123 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       if (*gave_up)                                         // copies in flight land before the CTA can end
 #pragma unroll 1
         for (int j = max(0, k - kStages); j < k; ++j) settle(&S.page_full[j % kStages], j / kStages);
-    } else if (warp == kMmaWarp) {
-      // ---- MMA issue
-      int qk = -1, done = -1;                               // last committed products
-      const uint64_t q_d = desc_k128(saddr(sm + L::kQ)), p_d = desc_mn128(saddr(sm + L::kP));
-      const uint64_t z_d = desc_plain(saddr(sm + L::kZ), N * 16);
-      auto pv = [&](int i) {
-        if (!warp_wait(&S.v_full[i & 1], i >> 1, gave_up) || !warp_wait(&S.p_full[i & 1], i >> 1, gave_up)) return false;
+    } else if (warp == kSeenWarp) {
+      // ---- ancestors of every node by doubling (four nodes a lane); parents checked
+      constexpr int kPer = kNodes / 32;
+      int up[kPer];
+      uint32_t mine[kPer][kNodeWords];
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) {
+        const int i = lane + 32 * x;
+        up[x] = -1;
+        if (i < st.n) {
+          up[x] = P.parent[st.first + i];
+          if (up[x] >= i || up[x] < -1) {
+            set_status(P.status, KVQ_ERR_BOUNDS);
+            up[x] = -1;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < kNodeWords; ++w) mine[x][w] = x == w ? 1u << lane : 0u;
+      }
+      // after round r: the 2^r nearest ancestors (itself counted), and where the next one is
+#pragma unroll 1
+      for (int r = 0;; ++r) {
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+          *reinterpret_cast<uint4*>(S.seen[lane + 32 * x]) = make_uint4(mine[x][0], mine[x][1], mine[x][2], mine[x][3]);
+          S.jump[lane + 32 * x] = up[x];
+        }
+        __syncwarp();
+        if ((1 << r) >= kNodes) break;
+        int next[kPer];
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+          next[x] = -1;
+          if (up[x] >= 0) {
+            const uint4 v = *reinterpret_cast<const uint4*>(S.seen[up[x]]);
+            mine[x][0] |= v.x; mine[x][1] |= v.y; mine[x][2] |= v.z; mine[x][3] |= v.w;
+            next[x] = S.jump[up[x]];
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) up[x] = next[x];
+      }
+      if (lane == 0) bar_arrive(&S.seen_full);
+    } else if (warp == kQkWarp) {
+      // ---- S(i) = K(i) q', one buffer after the other.  (The two products are issued by two warps: a
+      // wait and eight issues are a few hundred clocks each, which one warp would take in turn)
+      const uint64_t q_d = desc_k128(saddr(sm + L::kQ));
+      bool ok = warp_wait(&S.q_full, 0, gave_up);
+      int i = 0;
+#pragma unroll 1
+      for (; ok && i < nt; ++i) {
+        if (i > 1) ok = warp_wait(&S.s_free[i & 1], (i >> 1) - 1, gave_up);
+        ok = ok && warp_wait(&S.k_full[i & 1], i >> 1, gave_up);
+        if (!ok) break;
+        fence_after();
+        const uint32_t ts = tb + kColS + N * (i & 1);
+        if (i < nwc) {
+          const uint64_t k_d = desc_k128(saddr(sm + L::kK)), qb_d = desc_k128(saddr(sm + L::kQb));
+#pragma unroll 1
+          for (int s = 0; s < 8; ++s)
+            if (elect())
+              mma_ss(ts, k_d + (((s >> 2) * kSlab + (s & 3) * 32) >> 4), qb_d + (((s >> 2) * N * 128 + (s & 3) * 32) >> 4),
+                     kIdescB16, s > 0);
+        } else {
+          const uint32_t ka = tb + kColK + (kKBufs == 2 ? kKCols * (i & 1) : 0);
+          const uint64_t za = desc_plain(saddr(sm + L::kZa + (i & 1) * kTile * 32), kTile * 16);
+          if (elect()) {
+#pragma unroll 2
+            for (int s = 0; s < 8; ++s) {
+              const uint64_t qs = q_d + (((s >> 2) * N * 128 + (s & 3) * 32) >> 4);
+              mma_ts(ts, ka + 8 * s, qs, kIdescF16, s > 0);
+              if (NG > 1) mma_ts(ts, ka + 64 + 8 * s, qs, kIdescF16, 1u);
+            }
+            mma_ss(ts, za, desc_plain(saddr(sm + L::kZ), N * 16), kIdescF16, 1u);
+          }
+        }
+        __syncwarp();
+        if (elect()) mma_commit(&S.s_full[i & 1]);
+        __syncwarp();
+      }
+      if (!ok && i > 0) settle(&S.s_full[(i - 1) & 1], (i - 1) >> 1);   // what was issued ends before TMEM is given back
+    } else if (warp == kPvWarp) {
+      // ---- O += V(i) P(i)
+      const uint64_t p_d = desc_mn128(saddr(sm + L::kP));
+      bool ok = true;
+      int i = 0;
+#pragma unroll 1
+      for (; i < nt; ++i) {
+        ok = warp_wait(&S.v_full[i & 1], i >> 1, gave_up) && warp_wait(&S.p_full[i & 1], i >> 1, gave_up);
+        if (!ok) break;
         fence_after();
         if (i < nwc) {
           const uint64_t v_d = desc_mn128(saddr(sm + L::kV));
-          if (elect())
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
+#pragma unroll 1
+          for (int kk = 0; kk < 8; ++kk)
+            if (elect()) {
               mma_ss(tb + kColO, v_d + kk * (2048 >> 4), p_d + kk * (2048 >> 4), kIdescB16PV, i > 0 || kk > 0);
               mma_ss(tb + kColO, v_d + kk * (2048 >> 4), p_d + ((L::kPBytes + kk * 2048) >> 4), kIdescB16PV, 1u);
             }
         } else {
           const uint64_t p = p_d + (uint64_t)((i & 1) * (L::kPBytes >> 4));
           const uint32_t v = tb + kColV + (kVBufs == 2 ? 64 * (i & 1) : 0);
-          if (elect())
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) mma_ts(tb + kColO, v + 8 * kk, p + kk * (2048 >> 4), kIdescPV, i > 0 || kk > 0);
-        }
-        if (elect()) mma_commit(&S.pv_done[i & 1]);
-        __syncwarp();
-        done = i;
-        return true;
-      };
-      bool ok = true;
-      for (int i = 0; ok && i < nt; ++i) {
-        // (the first pages are streamed into the window rows' space: after the last window product)
-        if (i > 0 && i == nwc) ok = pv(i - 1);
-        if (ok) ok = warp_wait(&S.k_full[i & 1], i >> 1, gave_up);
-        if (ok && i > 0) ok = warp_wait(&S.s_free, i - 1, gave_up);
-        if (!ok) break;
-        fence_after();
-        if (i < nwc) {
-          const uint64_t k_d = desc_k128(saddr(sm + L::kK)), qb_d = desc_k128(saddr(sm + L::kQb));
-          if (elect())
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-              mma_ss(tb, k_d + (((s >> 2) * kSlab + (s & 3) * 32) >> 4), qb_d + (((s >> 2) * N * 128 + (s & 3) * 32) >> 4),
-                     kIdescB16, s > 0);
-        } else {
-          const uint32_t ka = tb + kColK + (kKBufs == 2 ? (kKCols + 8) * (i & 1) : 0);
           if (elect()) {
-#pragma unroll
-            for (int s = 0; s < 8; ++s) {
-              const uint64_t qs = q_d + (((s >> 2) * N * 128 + (s & 3) * 32) >> 4);
-              mma_ts(tb, ka + 8 * s, qs, kIdescF16, s > 0);
-              if (NG > 1) mma_ts(tb, ka + 64 + 8 * s, qs, kIdescF16, 1u);
-            }
-            mma_ts(tb, ka + kKCols, z_d, kIdescF16, 1u);
+#pragma unroll 2
+            for (int kk = 0; kk < 8; ++kk) mma_ts(tb + kColO, v + 8 * kk, p + kk * (2048 >> 4), kIdescPV, i > 0 || kk > 0);
           }
         }
-        if (elect()) mma_commit(&S.s_full[i & 1]);
         __syncwarp();
-        qk = i;
-        if (i > 0 && i != nwc) ok = pv(i - 1);
+        if (elect()) mma_commit(&S.pv_done[i & 1]);
+        __syncwarp();
       }
-      if (ok && nt > 0) ok = pv(nt - 1);
-      if (!ok) {                                            // what was issued ends before TMEM is given back
-        if (qk >= 0) settle(&S.s_full[qk & 1], qk >> 1);
-        if (done >= 0) settle(&S.pv_done[done & 1], done >> 1);
-      }
+      if (!ok && i > 0) settle(&S.pv_done[(i - 1) & 1], (i - 1) >> 1);
     }
   } else if (warp >= kKeyWarp) {
-    regs_dec<Regs<N>::kExpand>();
+    if (warp < kValWarp) regs_dec<Regs<N>::kKeys>();
+    else regs_dec<Regs<N>::kValues>();
     // ---- operands of a tile, lane quadrant q of TMEM.  Window tiles: 128 threads copy the rows
     // into swizzled shared memory, 16 lanes a row
     const bool keys = warp < kValWarp;
@@ -667,19 +625,18 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       uint8_t* dst = sm + (keys ? L::kK : L::kV);
       const int j = t & 15;
 #pragma unroll 4
-      for (int r = t >> 4; r < kTile; r += 8) {
-        const int w = w0 + r;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (w < n_win) {
-          const int tok = w < n_sink ? w : ring0 + w - n_sink;
-          const uint16_t* src = w < n_sink ? sink + (((size_t)b * P.hkv + h) * P.s_sink + tok) * kHeadDim
-                                           : ring + (((size_t)b * P.hkv + h) * P.ring_cap + tok % P.ring_cap) * kHeadDim;
-          v = reinterpret_cast<const uint4*>(src)[j];
-        }
-        *reinterpret_cast<uint4*>(dst + (j >> 3) * kSlab + (r >> 3) * 1024 + (r & 7) * 128 + (((j & 7) ^ (r & 7)) << 4)) = v;
+      for (int r = t >> 4; r < kTile; r += keys ? 8 : 2 * kValWarps) {
+        const int w = min(w0 + r, n_win - 1);
+        const int tok = w < n_sink ? w : ring0 + w - n_sink;
+        const uint16_t* src = w < n_sink ? sink + (((size_t)b * P.hkv + h) * P.s_sink + tok) * kHeadDim
+                                         : ring + (((size_t)b * P.hkv + h) * P.ring_cap + tok % P.ring_cap) * kHeadDim;
+        // (zeros for rows behind the last: 0 bytes are read)
+        async_copy16(dst + (j >> 3) * kSlab + (r >> 3) * 1024 + (r & 7) * 128 + (((j & 7) ^ (r & 7)) << 4), src + 8 * j,
+                     w0 + r < n_win ? 16 : 0);
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       if (keys) {
-        S.lane_scale[i & 3][t] = P.scale_log2;
+        S.lane_scale[i & 3][t] = 1.f;
         const unsigned alive = __ballot_sync(0xffffffffu, w0 + t < n_win);
         if (lane == 0) S.alive[i & 3][q] = alive;
       }
@@ -689,7 +646,6 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     }
     if (keys) {
       // ---- keys: tokens 32 q .. 32 q + 31 of a tile, pages 2 q and 2 q + 1
-      const float cmul = P.scale_log2 * ldexpf(1.f, 24 - sigma);
       int k = 0;
       for (int i = nwc; ok && i < nt; ++i, ++k) {
         const int stage = k % kStages;
@@ -699,7 +655,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         if (!ok) break;
         fence_after();
         const uint8_t* base = stages + (size_t)stage * kTilePages * pb;
-        const uint32_t tk = tq + kColK + (kKBufs == 2 ? (kKCols + 8) * (i & 1) : 0);
+        const uint32_t tk = tq + kColK + (kKBufs == 2 ? kKCols * (i & 1) : 0);
         uint32_t alive = 0u;
 #pragma unroll 1
         for (int j = 0; j < 2; ++j) {
@@ -715,6 +671,12 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
           const uint8_t* sc = pgp + k_scale_off();
           uint32_t v[16];
           float ls[2];
+          // slots 2 quad, 2 quad + 1 and 8 + 2 quad, 9 + 2 quad of tokens row, row + 8 (z[0 .. 1], z[2 .. 3])
+          auto put_zero = [&](const uint32_t (&z)[4]) {
+            uint8_t* to = sm + L::kZa + (i & 1) * kTile * 32 + 2 * pg * 128 + row * 16 + quad * 4;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) *reinterpret_cast<uint32_t*>(to + (x & 1) * 128 + (x >> 1) * kTile * 16) = z[x];
+          };
           if constexpr (NG == 1) {
             uint32_t z[4];
 #pragma unroll
@@ -733,7 +695,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
                 for (int r = 0; r < 4; ++r) v[4 * s + r] = code_pair(kw[r], kw10[r], 4 * hf + s);
               tm_st_frag8(ta + 32 * hf, v);
             }
-            tm_st_frag2(ta + kKCols, z);
+            put_zero(z);
           } else {
             uint32_t d2[2][NG];                             // Delta 2^k of both tokens, twice in a register
             uint32_t z[4] = {0u, 0u, 0u, 0u};
@@ -768,7 +730,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
                 z[2 + x] = pack16(hi, 0.f);
               }
             }
-            tm_st_frag2(ta + kKCols, z);
+            put_zero(z);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
@@ -792,13 +754,14 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
             ls[1] *= __half2float(nm[row + 8]);
           }
           if (quad == 0) {
-            S.lane_scale[i & 3][16 * pg + row] = ls[0] * cmul;
-            S.lane_scale[i & 3][16 * pg + row + 8] = ls[1] * cmul;
+            S.lane_scale[i & 3][16 * pg + row] = ls[0];
+            S.lane_scale[i & 3][16 * pg + row + 8] = ls[1];
           }
         }
         if (lane == 0) S.alive[i & 3][q] = alive;
         wait_st();
         fence_before();
+        fence_async();
         __syncwarp();
         if (lane == 0) {
           bar_arrive(&S.k_full[i & 1]);
@@ -806,76 +769,68 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         }
       }
     } else {
-      // ---- values: channels 32 q .. 32 q + 31 of all pages; slots m = 2 q, 2 q + 1 of the words
-      uint32_t vmask[2], vone[2];
-      const int vshift = 2 * q + 1 <= 4 ? 0 : 10, vshift0 = 2 * q <= 4 ? 0 : 10;
+      // ---- values: channels 32 q .. 32 q + 31 of four pages; slots m = 2 q, 2 q + 1 of the words
+      const int vg = 32 * q / (kHeadDim / NG);              // the group of these channels
+      const int pages = (warp - kValWarp) >> 2;             // this warp's pages: 4 of the 8
+      // slots m = 2 q, 2 q + 1 of the words
+      uint32_t mask[2], one[2];
+      int shift[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int s = slot_pow(2 * q + j);
-        vmask[j] = 0x00030003u << (2 * s);
-        vone[j] = (uint32_t)(25 - 2 * s) << 10;             // 2^(10 - 2 s): the code's bits then count ones
-        vone[j] |= vone[j] << 16;
+        const int m = 2 * q + j, sp = slot_pow(m);
+        shift[j] = m <= 4 ? 0 : 10;
+        mask[j] = 0x00030003u << (2 * sp);
+        one[j] = (uint32_t)(25 - 2 * sp) * 0x04000400u;     // 2^(10 - 2 sp): the code's bits then count ones
       }
-      const int vg = 32 * q / (kHeadDim / NG);              // the group of these channels
       int k = 0;
+#pragma unroll 1
       for (int i = nwc; ok && i < nt; ++i, ++k) {
         const int stage = k % kStages;
-        const int page0 = (t0 + i - nw) * kTilePages;
         ok = warp_wait(&S.page_full[stage], k / kStages, gave_up);
         if (ok && i >= kVBufs) ok = warp_wait(&S.pv_done[(i - kVBufs) & 1], (i - kVBufs) >> 1, gave_up);
         if (!ok) break;
         fence_after();
-        const uint8_t* base = stages + (size_t)stage * kTilePages * pb;
-        const uint32_t tv = tq + kColV + (kVBufs == 2 ? 64 * (i & 1) : 0);
-        // every page of the tile is there in whole, except in a sequence's last tile (or next to a bad entry)
-        bool whole = n_tok >= kPage * (page0 + kTilePages);
-#pragma unroll
-        for (int pg = 0; pg < kTilePages; ++pg) whole = whole && S.pid[stage][pg] >= 0;
+        const uint8_t* pgp = stages + (size_t)(stage * kTilePages + 4 * pages) * pb;
+        uint32_t tv = tq + kColV + (kVBufs == 2 ? 64 * (i & 1) : 0) + 32 * pages;
+        const bool whole = S.whole[stage];
+        // (rolled: the roles' loops together have to stay in the instruction cache)
 #pragma unroll 1
-        for (int p4 = 0; p4 < kTilePages; p4 += 4) {
-          uint4 w[4];
-          uint32_t d[4][2], z[4][2];
+        for (int pg = 0; pg < 4; ++pg, pgp += pb, tv += 8) {
+          const uint4 w = lds16(pgp + kCodeBytes + 16 * lane);
+          const uint8_t* dp = pgp + v_delta_off(NG, 2 * quad, vg);
+          uint32_t d[2], z[2];
+          d[0] = *reinterpret_cast<const uint32_t*>(dp);
+          d[1] = *reinterpret_cast<const uint32_t*>(dp + 16 * NG);
+          z[0] = *reinterpret_cast<const uint32_t*>(dp + 32 * NG);
+          z[1] = *reinterpret_cast<const uint32_t*>(dp + 48 * NG);
+          const uint32_t vw[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint8_t* pgp = base + (size_t)(p4 + x) * pb;
-            w[x] = lds16(pgp + kCodeBytes + 16 * lane);
-            const uint8_t* dp = pgp + v_delta_off(NG, 2 * quad, vg);
-            d[x][0] = *reinterpret_cast<const uint32_t*>(dp);
-            d[x][1] = *reinterpret_cast<const uint32_t*>(dp + 16 * NG);
-            z[x][0] = *reinterpret_cast<const uint32_t*>(dp + 32 * NG);
-            z[x][1] = *reinterpret_cast<const uint32_t*>(dp + 48 * NG);
-          }
+          for (int y = 0; y < 2; ++y) z[y] = h2bits(__hmul2(bits2h(d[y]), bits2h(z[y] ^ 0x80008000u)));
+          uint32_t a[2][4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) z[x][y] = h2bits(__hneg2(__hmul2(bits2h(d[x][y]), bits2h(z[x][y]))));
+            for (int r = 0; r < 4; ++r) {
+              // 2^(10 - 2 sp) + c, then c (exact), then Delta c - Delta z
+              const __half2 c = __hsub2(bits2h(((vw[r] >> shift[j]) & mask[j]) | one[j]), bits2h(one[j]));
+              a[j][r] = h2bits(__hfma2(c, bits2h(d[r >> 1]), bits2h(z[r >> 1])));
+            }
+          if (!whole) {                                     // dead tokens: zeros, whatever the page holds there
+            const int at = 4 * pages + pg;
+            const int valid = S.pid[stage][at] < 0 ? 0 : max(0, min(kPage, n_tok - kPage * ((t0 + i - nw) * kTilePages + at)));
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t a[16];
+            for (int y = 0; y < 2; ++y) {
+              const int tk = 2 * quad + 8 * y;
+              const uint32_t m2 = (tk < valid ? 0xffffu : 0u) | (tk + 1 < valid ? 0xffff0000u : 0u);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t vw[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const __half2 c = __hsub2(bits2h(((vw[r] >> (j ? vshift : vshift0)) & vmask[j]) | vone[j]), bits2h(vone[j]));
-                a[4 * x + r] = h2bits(__hfma2(c, bits2h(d[x][r >> 1]), bits2h(z[x][r >> 1])));
+              for (int j = 0; j < 2; ++j) {
+                a[j][2 * y] &= m2;
+                a[j][2 * y + 1] &= m2;
               }
             }
-            if (!whole) {                                   // dead tokens: zeros, whatever the page holds there
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const int valid = S.pid[stage][p4 + x] < 0 ? 0 : max(0, min(kPage, n_tok - kPage * (page0 + p4 + x)));
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  const int tk = 2 * quad + 8 * y;
-                  const uint32_t m = (tk < valid ? 0xffffu : 0u) | (tk + 1 < valid ? 0xffff0000u : 0u);
-                  a[4 * x + 2 * y] &= m;
-                  a[4 * x + 2 * y + 1] &= m;
-                }
-              }
-            }
-            tm_st_frag8(tv + ((uint32_t)(16 * j) << 16) + 8 * p4, a);
           }
+          tm_st_frag2(tv, a[0]);
+          tm_st_frag2(tv + (16u << 16), a[1]);
         }
         wait_st();
         fence_before();
@@ -892,45 +847,107 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     const int q = warp & 3, half = warp >> 2;
     const uint32_t tq = tb + ((uint32_t)(32 * q) << 16);
     const int c0 = half * kCols, tok = 32 * q + lane;
-    float2 l[kCols / 2];
+    // q' operands first (these 256 threads): bf16 rows, 16-byte chunk j of row c in slab j / 8, swizzled
+    auto at = [&](int c, int j) { return (j >> 3) * N * 128 + (c >> 3) * 1024 + (c & 7) * 128 + (((j & 7) ^ (c & 7)) << 4); };
+    int sigma = 0;
+    {
+      if (tid < N) {
+        const int r = row0 + tid;
+        S.row[tid] = (st.first + (r >> P.gqa_log2)) * (P.hkv * P.gqa) + h * P.gqa + (r & (P.gqa - 1));
+        S.neg_m[tid] = 0.f;
+      }
+      softmax_sync();
+      float amax = 0.f;
+#pragma unroll 4
+      for (int i = tid; i < N * 16; i += 256) {
+        const int c = i >> 4, j = i & 15;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (c < ncol) v = reinterpret_cast<const uint4*>(P.q + (size_t)S.row[c] * kHeadDim)[j];
+        *reinterpret_cast<uint4*>(sm + L::kQb + at(c, j)) = v;
+        // (the largest magnitude: bf16 patterns without the sign compare as integers)
+        const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+        amax = fmaxf(amax, __uint_as_float(max(m << 16, m & 0xffff0000u)));
+      }
 #pragma unroll
-    for (int j = 0; j < kCols / 2; ++j) l[j] = make_float2(0.f, 0.f);
+      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      if (lane == 0) S.amax[warp] = amax;
+      softmax_sync();
+#pragma unroll
+      for (int w = 0; w < kSmWarps; ++w) amax = fmaxf(amax, S.amax[w]);
+      if (amax > 0.f && amax < INFINITY) sigma = 14 - ((int)(__float_as_uint(amax) >> 23) - 126);   // amax 2^sigma < 2^14
+      // fp16 rows, channel slot s scaled by 4^-s for the codes that carry 4^s
+#pragma unroll 2
+      for (int i = tid; i < N * 16; i += 256) {
+        const int c = i >> 4, j = i & 15;
+        const uint4 v = lds16(sm + L::kQb + at(c, j));
+        const float f = ldexpf(1.f, sigma - 2 * slot_pow(j >> 1));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = pack16(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
+        *reinterpret_cast<uint4*>(sm + L::kQ + at(c, j)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      // zero-point operand, row c: slots 2 g, 2 g + 1: -sum of group g (hi), slot 8 + 2 g: its lo
+      if (tid < N) {
+        const int c = tid;
+        const float fz = ldexpf(1.f, NG == 1 ? sigma - 19 : sigma - 16);
+        uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          float acc = 0.f;
+#pragma unroll 2
+          for (int j = g * (16 / NG); j < (g + 1) * (16 / NG); ++j) {
+            const uint4 v = lds16(sm + L::kQb + at(c, j));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc += __uint_as_float(w[k] << 16) + __uint_as_float(w[k] & 0xffff0000u);
+          }
+          const float v = -acc * fz;
+          const float hi = __half2float(__float2half_rn(v));
+          z[g] = pack16(hi, hi);
+          z[4 + g] = pack16(v - hi, 0.f);
+        }
+        *reinterpret_cast<uint4*>(sm + L::kZ + (c >> 3) * 128 + (c & 7) * 16) = make_uint4(z[0], z[1], z[2], z[3]);
+        *reinterpret_cast<uint4*>(sm + L::kZ + N * 16 + (c >> 3) * 128 + (c & 7) * 16) = make_uint4(z[4], z[5], z[6], z[7]);
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&S.q_full);
+    }
+    const float page_scale = P.scale_log2 * ldexpf(1.f, 24 - sigma);
+    float l[kCols];
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) l[j] = 0.f;
     bool lost = false;
     uint32_t unseen = (1u << (kCols / 32)) - 1u;            // lane j: rows c0 + 32 ch + j that have seen no token yet
     bool force = true;                                      // ... there are such rows (all four warps agree)
-#pragma unroll 1
-    for (int i = 0; i < nt; ++i) {
-      const bool ok = warp_wait(&S.s_full[i & 1], i >> 1, gave_up) && !lost;
-      fence_after();
-      float x[kCols];
-#pragma unroll
-      for (int ch = 0; ch < kCols / 32; ++ch) tm_ld32(tq + c0 + 32 * ch, x + 32 * ch);
-      const bool win = i < nwc;
-      const float ls = S.lane_scale[i & 3][tok];
-      const uint32_t alive = S.alive[i & 3][q];
-      // the draft this token is (window tiles that reach into the drafts): else every row sees it
-      const bool drafts = win && (n_sink > st.L0 || (t0 + i + 1) * kTile > n_win - st.n);
-      // P buffer free: PV(i - 2), or PV(i - 1) around window tiles (which use both buffers)
-      const int before = (win || (i > 0 && i - 1 < nwc)) ? i - 1 : i - 2;
-#pragma unroll
-      for (int ch = 0; ch < kCols / 32; ++ch) tm_wait32(x + 32 * ch);
-      fence_before();
+    int meets = 0;
+    // the half's four warps meet (bounded, so that a warp that gave up leaves nobody behind)
+    auto meet = [&]() {
       __syncwarp();
-      if (lane == 0) bar_arrive(&S.s_free);
-      // scores less the reference
-      const float2 ls2 = make_float2(ls, ls);
-#pragma unroll
-      for (int j = 0; j < kCols; j += 4) {
-        const float4 m = *reinterpret_cast<const float4*>(&S.neg_m[c0 + j]);
-        const float2 a = __ffma2_rn(make_float2(x[j], x[j + 1]), ls2, make_float2(m.x, m.y));
-        const float2 b2 = __ffma2_rn(make_float2(x[j + 2], x[j + 3]), ls2, make_float2(m.z, m.w));
-        x[j] = a.x; x[j + 1] = a.y; x[j + 2] = b2.x; x[j + 3] = b2.y;
+      if (lane == 0) bar_arrive(&S.meet[half]);
+      if (!warp_wait(&S.meet[half], meets++, gave_up)) lost = true;
+    };
+#pragma unroll 1
+    for (int i = 0; i < nt && !lost; ++i) {
+      if (!warp_wait(&S.s_full[i & 1], i >> 1, gave_up)) {
+        lost = true;
+        break;
       }
-      if (drafts || alive != 0xffffffffu) {                 // tokens that do not exist, drafts that a row does not see
+      fence_after();
+      const uint32_t ts = tq + kColS + N * (i & 1);
+      const bool win = i < nwc;
+      const float ls = S.lane_scale[i & 3][tok] * (win ? P.scale_log2 : page_scale);
+      const uint32_t alive = S.alive[i & 3][q];
+      // window tiles that reach into the drafts: else every row sees every token
+      const bool drafts = win && (n_sink > st.L0 || (t0 + i + 1) * kTile > n_win - st.n);
+      const bool masked = drafts || alive != 0xffffffffu;
+      uint32_t see[kCols / 32];                             // rows that see this token
+      if (masked) {
+        if (drafts && !warp_wait(&S.seen_full, 0, gave_up)) lost = true;
         const int w = (t0 + i) * kTile + tok;
         const int node = win ? (w < n_sink ? w : ring0 + w - n_sink) - st.L0 : -1;
         const bool mine = (alive >> lane) & 1u;
-        uint32_t see[kCols / 32];
 #pragma unroll
         for (int ch = 0; ch < kCols / 32; ++ch) {
           see[ch] = mine ? 0xffffffffu : 0u;
@@ -942,54 +959,89 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
               see[ch] |= ((S.seen[min((row0 + c0 + 32 * ch + j) >> P.gqa_log2, kNodes - 1)][wd] >> (node & 31)) & 1u) << j;
           }
         }
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) x[j] = (see[j / 32] >> (j & 31)) & 1u ? x[j] : -INFINITY;
       }
-      float mx[4] = {x[0], x[1], x[2], x[3]};
+      float x[kCols];
+      bool moved = false;
+#pragma unroll 1
+      for (;;) {
+        tm_ld<kCols>(ts + c0, x);
+        // scores less the reference
 #pragma unroll
-      for (int j = 4; j < kCols; j += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          mx[e] = fmaxf(mx[e], x[j + e]);
-          if (j + 4 + e < kCols) mx[e] = fmaxf(mx[e], x[j + 4 + e]);
+        for (int j = 0; j < kCols; j += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(&S.neg_m[c0 + j]);
+          x[j] = fmaf(x[j], ls, m.x);
+          x[j + 1] = fmaf(x[j + 1], ls, m.y);
+          x[j + 2] = fmaf(x[j + 2], ls, m.z);
+          x[j + 3] = fmaf(x[j + 3], ls, m.w);
         }
-      const bool over = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > 8.f;
-      bool waited = before < 0;
-      if (half_or(half, over || force || !ok)) {
-        // ---- the references move to the rows' maxima so far (one decision for the four warps)
-        if (half_or(half, !ok)) break;
+        if (masked) {
 #pragma unroll
+          for (int j = 0; j < kCols; ++j) x[j] = (see[j / 32] >> (j & 31)) & 1u ? x[j] : -INFINITY;
+        }
+        if (!moved) {
+          float mx[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(x[e], x[4 + e], x[8 + e]);
+#pragma unroll
+          for (int j = 12; j + 8 <= kCols; j += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
+          // (kCols is 4 past a multiple of 8 from 12 on: the last four)
+          const bool over = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], x[kCols - 4], x[kCols - 3]),
+                                 fmaxf(x[kCols - 2], x[kCols - 1])) > 8.f;
+          // one vote of the four warps, taken while the exponentials are already formed
+          const bool any = __any_sync(0xffffffffu, over) || force;
+          if (lane == 0) {
+            if (any) *(volatile int*)&S.moves[half] = i + 1;
+            bar_arrive(&S.vote[half]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kCols / 2; ++j) x[j] = ex2(x[j]);
+        if (moved) break;
+        if (!warp_wait(&S.vote[half], i, gave_up)) {
+          lost = true;
+          break;
+        }
+        if (*(volatile int*)&S.moves[half] != i + 1) break;
+        // ---- the references move to the rows' maxima so far
+        moved = true;
+#pragma unroll 1
         for (int j = 0; j < kCols; j += 8) {
           float y[8];
+          tm_ld8(ts + c0 + j, y);
+          const uint32_t bits = masked ? (kCols > 32 && j >= 32 ? see[kCols / 32 - 1] : see[0]) >> (j & 31) : 0xffu;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = x[j + e];
+          for (int e = 0; e < 8; ++e) y[e] = (bits >> e) & 1u ? y[e] * ls : -INFINITY;
           const float top = reduce_columns(y, lane, [](float a, float b2) { return fmaxf(a, b2); });
           if (lane < 8) S.red[q][c0 + j + lane] = top;
         }
-        half_sync(half);
+        meet();
+        float now[kCols / 32];
 #pragma unroll
         for (int ch = 0; ch < kCols / 32; ++ch) {
           const int c = c0 + 32 * ch + lane;
           const float up = fmaxf(fmaxf(S.red[0][c], S.red[1][c]), fmaxf(S.red[2][c], S.red[3][c]));
-          // over the old reference: a first token sets it, later ones only raise it
+          // a first token sets the reference, later ones only raise it
           const bool fresh = (unseen >> ch) & 1u, any = up > -INFINITY;
-          const float by = fresh ? (any ? up : 0.f) : fmaxf(up, 0.f);
+          const float old = -S.neg_m[c];
+          now[ch] = fresh ? (any ? up : 0.f) : fmaxf(old, up);
           if (any) unseen &= ~(1u << ch);
-          if (q == 0) {
-            S.neg_m[c] -= by;
-            S.delta[c] = -by;
-            S.alpha[c] = fresh ? 0.f : ex2(-by);
-          }
+          if (q == 0) S.alpha[c] = fresh ? 0.f : ex2(old - now[ch]);
         }
         force = __any_sync(0xffffffffu, unseen != 0u);
-        half_sync(half);
+        meet();                                             // (everyone has read the old references)
+        if (q == 0) {
+#pragma unroll
+          for (int ch = 0; ch < kCols / 32; ++ch) S.neg_m[c0 + 32 * ch + lane] = -now[ch];
+        }
 #pragma unroll
         for (int j = 0; j < kCols; j += 4) {
           const float4 al = *reinterpret_cast<const float4*>(&S.alpha[c0 + j]);
-          const float4 de = *reinterpret_cast<const float4*>(&S.delta[c0 + j]);
-          l[j / 2] = __fmul2_rn(l[j / 2], make_float2(al.x, al.y));
-          l[j / 2 + 1] = __fmul2_rn(l[j / 2 + 1], make_float2(al.z, al.w));
-          x[j] += de.x; x[j + 1] += de.y; x[j + 2] += de.z; x[j + 3] += de.w;
+          l[j] *= al.x;
+          l[j + 1] *= al.y;
+          l[j + 2] *= al.z;
+          l[j + 3] *= al.w;
         }
         if (i > 0) {                                        // O so far, once PV(i - 1) is done
           if (!warp_wait(&S.pv_done[(i - 1) & 1], (i - 1) >> 1, gave_up)) lost = true;
@@ -1003,62 +1055,67 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
             tm_st8(tq + kColO + c0 + j, o);
           }
           wait_st();
-          fence_before();
-          waited = true;
         }
-        half_sync(half);                                    // (alpha and delta are read before they change again)
+        meet();                                             // (the new references are there)
       }
-      if (!waited && !warp_wait(&S.pv_done[before & 1], before >> 1, gave_up)) lost = true;
-#pragma unroll
-      for (int j = 0; j < kCols; j += 2) {
-        x[j] = ex2(x[j]);
-        x[j + 1] = ex2(x[j + 1]);
-        l[j / 2] = __fadd2_rn(l[j / 2], make_float2(x[j], x[j + 1]));
-      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&S.s_free[i & 1]);
+      // P buffer free: PV(i - 2), or PV(i - 1) around window tiles (which use both buffers)
+      const int before = (win || (i > 0 && i - 1 < nwc)) ? i - 1 : i - 2;
+      if (before >= 0 && !warp_wait(&S.pv_done[before & 1], before >> 1, gave_up)) lost = true;
       // P[token][row], 8 rows a chunk of 16 bytes: a lane's chunks are 16 (j ^ (token % 8)) apart
       const uint32_t p_s = saddr(sm + L::kP) + (c0 >> 6) * kSlab + (tok >> 3) * 1024 + (tok & 7) * 128;
       const uint32_t sw = (uint32_t)(((c0 & 63) >> 3) ^ (tok & 7)) << 4;
+#pragma unroll
+      for (int j = kCols / 2; j < kCols; ++j) x[j] = ex2(x[j]);
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) l[j] += x[j];
       if (!win) {
-        const uint32_t at = p_s + (i & 1) * L::kPBytes;
+        const uint32_t to = p_s + (i & 1) * L::kPBytes;
 #pragma unroll
         for (int j = 0; j < kCols / 8; ++j)
-          sts16(at + (sw ^ (16u * j)), pack16(x[8 * j], x[8 * j + 1]), pack16(x[8 * j + 2], x[8 * j + 3]),
+          sts16(to + (sw ^ (16u * j)), pack16(x[8 * j], x[8 * j + 1]), pack16(x[8 * j + 2], x[8 * j + 3]),
                 pack16(x[8 * j + 4], x[8 * j + 5]), pack16(x[8 * j + 6], x[8 * j + 7]));
       } else {
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {              // bf16 hi, then what it leaves
+        for (int j = 0; j < kCols / 8; ++j) {               // bf16 hi, and what it leaves
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int j = 0; j < kCols / 8; ++j) {
-            uint32_t hi[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float &a0 = x[8 * j + 2 * e], &a1 = x[8 * j + 2 * e + 1];
-              hi[e] = packb16(a0, a1);
-              a0 -= __uint_as_float(hi[e] << 16);
-              a1 -= __uint_as_float(hi[e] & 0xffff0000u);
-            }
-            sts16(p_s + part * L::kPBytes + (sw ^ (16u * j)), hi[0], hi[1], hi[2], hi[3]);
+          for (int e = 0; e < 4; ++e) {
+            const float a0 = x[8 * j + 2 * e], a1 = x[8 * j + 2 * e + 1];
+            hi[e] = packb16(a0, a1);
+            lo[e] = packb16(a0 - __uint_as_float(hi[e] << 16), a1 - __uint_as_float(hi[e] & 0xffff0000u));
           }
+          sts16(p_s + (sw ^ (16u * j)), hi[0], hi[1], hi[2], hi[3]);
+          sts16(p_s + L::kPBytes + (sw ^ (16u * j)), lo[0], lo[1], lo[2], lo[3]);
         }
       }
       fence_async();
       __syncwarp();
       if (lane == 0) bar_arrive(&S.p_full[i & 1]);
     }
-    // ---- sums over the tile's tokens: lanes, then quadrants
-#pragma unroll
-    for (int j = 0; j < kCols; j += 8) {
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = e & 1 ? l[(j + e) / 2].y : l[(j + e) / 2].x;
-      const float sum = reduce_columns(y, lane, [](float a, float b2) { return a + b2; });
-      if (lane < 8) S.red[q][c0 + j + lane] = sum;
-    }
-    half_sync(half);
-    bool ok = nt > 0 && !lost;
-    if (ok) ok = warp_wait(&S.pv_done[(nt - 1) & 1], (nt - 1) >> 1, gave_up);
+    // ---- sums over the tokens: every lane's through shared memory (where P was), 16-byte chunks
+    // permuted by token; then the rows' results
+    if (!lost && nt > 0 && !warp_wait(&S.pv_done[(nt - 1) & 1], (nt - 1) >> 1, gave_up)) lost = true;
     fence_after();
-    if (nt == 0 || ok) {
+    float* scratch = reinterpret_cast<float*>(sm + L::kP);  // [128 tokens][N]
+    constexpr int kChunks = kCols / 4;
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j)
+      *reinterpret_cast<float4*>(scratch + tok * N + c0 + 4 * (j ^ (tok & (kChunks - 1)))) =
+          make_float4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
+    meet();
+    {
+      const int c = tok & (kCols - 1), part = tok / kCols;  // kCols tokens each
+      float sum = 0.f;
+#pragma unroll 8
+      for (int t = part * kCols; t < (part + 1) * kCols; ++t)
+        sum += scratch[t * N + c0 + 4 * ((c >> 2) ^ (t & (kChunks - 1))) + (c & 3)];
+      S.red[part][c0 + c] = sum;
+    }
+    meet();
+    if (!lost) {
 #pragma unroll 1
       for (int j = 0; j < kCols && c0 + j < ncol; j += 8) {
         float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -1067,8 +1124,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         for (int e = 0; e < 8; ++e) {
           const int c = c0 + j + e;
           if (c < ncol) {
-            const float sum = S.red[0][c] + S.red[1][c] + S.red[2][c] + S.red[3][c];
-            const size_t r = out_row(c);
+            float sum = S.red[0][c] + S.red[1][c];
+            if (kCols == 32) sum += S.red[2][c] + S.red[3][c];
+            const size_t r = (size_t)S.row[c];
             if (P.splits == 1) {
               const float v = sum > 0.f ? __fdividef(o[e], sum) : (sum == 0.f ? 0.f : o[e] * sum);
               P.out[r * kHeadDim + tok] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
@@ -1152,9 +1210,10 @@ struct Shape {
 Shape tree_shape(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
   const int g = cfg->n_q_heads / cfg->n_kv_heads;
   Shape s;
-  // 128 columns cost the tensor pipe what 64 do, but twice the softmax; a tree that fits 64 takes 64
+  // 128 rows share one expansion where TMEM holds two S of them (keys as codes); else, and for trees
+  // that fit, 64
   const long long per_seq = ((long long)n_rows * g + cfg->batch - 1) / cfg->batch;
-  s.n = per_seq > 64 ? 128 : 64;
+  s.n = per_seq > 64 && cfg->group_size == kHeadDim ? 128 : 64;
   s.items = (int)min((long long)n_rows, (long long)n_rows * g / s.n + cfg->batch);
   const long long pages = max(0LL, min((long long)cfg->max_pages_per_seq, ((long long)max_ctx - cfg->s_sink + kPage - 1) / kPage));
   const long long win = min((long long)cfg->s_sink + cfg->s_keep + cfg->s_flush + kNodes, (long long)max_ctx);
@@ -1225,16 +1284,16 @@ extern "C" int kvq_launch_attn_tree(const kvq_config* cfg, const kvq_cache* cach
   P.scale_log2 = sm_scale * 1.4426950408889634f;
   if (cfg->n_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
   const int ng = kHeadDim / cfg->group_size;
-  void (*kern)(const TreeParams) = s.n == 64 ? (ng == 1 ? attn_tree_kernel<64, 1> : ng == 2 ? attn_tree_kernel<64, 2> : attn_tree_kernel<64, 4>)
-                                             : (ng == 1 ? attn_tree_kernel<128, 1> : ng == 2 ? attn_tree_kernel<128, 2> : attn_tree_kernel<128, 4>);
+  void (*kern)(const TreeParams) = s.n == 128 ? attn_tree_kernel<128, 1> : ng == 1 ? attn_tree_kernel<64, 1>
+                                                    : ng == 2 ? attn_tree_kernel<64, 2> : attn_tree_kernel<64, 4>;
   const size_t smem = s.n == 64 ? Layout<64>::kEnd + sizeof(TreeShared<64>) : Layout<128>::kEnd + sizeof(TreeShared<128>);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ERR_CUDA;
   static std::mutex mu;
-  static unsigned long long done[6] = {};
+  static unsigned long long done[4] = {};
   {
     std::lock_guard<std::mutex> lock(mu);
-    const int vi = (s.n == 64 ? 0 : 3) + (ng == 1 ? 0 : ng == 2 ? 1 : 2);
+    const int vi = s.n == 128 ? 3 : ng == 1 ? 0 : ng == 2 ? 1 : 2;
     if (!(done[vi] & (1ull << dev))) {
       // (the register split counts on what the kernel launches with: a warpgroup would wait for ever)
       cudaFuncAttributes fa;
