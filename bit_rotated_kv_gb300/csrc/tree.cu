@@ -46,19 +46,16 @@ namespace {
 constexpr int kNodes = KVQ_TREE_MAX_NODES;
 constexpr int kNodeWords = kNodes / 32;
 constexpr int kTile = 128;                       // tokens of a tile
+constexpr int N = 64;                            // rows (node, query head) of a CTA
 constexpr int kTilePages = kTile / kPage;
 constexpr int kSmWarps = 8;                      // softmax; then 4 warps for keys, 8 for values, 4 more
-constexpr int kKeyWarp = 8, kValWarp = 12, kValWarps = 8, kQkWarp = 20, kPageWarp = 21, kPvWarp = 22, kSeenWarp = 23;
+constexpr int kKeyWarp = 8, kValWarp = 12, kQkWarp = 20, kPageWarp = 21, kPvWarp = 22, kSeenWarp = 23;
+constexpr int kKeyWarps = 4, kValWarps = 8;
 constexpr int kThreadsT = 32 * 24;               // (whole warpgroups: registers are handed over by warpgroup)
 constexpr int kStages = 4;                       // page tiles in flight
 // Registers a thread by role, of the 80 that 768 threads launch with.
-constexpr int kRegsLaunch = 80;
-template <int N>
-struct Regs {
-  static constexpr int kSoftmax = N == 128 ? 152 : 104, kKeys = N == 128 ? 56 : 72, kValues = N == 128 ? 40 : 56,
-                       kIssue = N == 128 ? 32 : 48;
-  static_assert(256 * kSoftmax + 128 * kKeys + 256 * kValues + 128 * kIssue <= kThreadsT * kRegsLaunch, "register split");
-};
+constexpr int kRegsLaunch = 80, kRegsSoftmax = 104, kRegsKeys = 72, kRegsValues = 56, kRegsIssue = 48;
+static_assert(256 * kRegsSoftmax + 128 * kRegsKeys + 256 * kRegsValues + 128 * kRegsIssue <= kThreadsT * kRegsLaunch, "register split");
 
 constexpr int kWinCost = 3;
 constexpr int kRec = 4 + kHeadDim;               // (m, l, -, -, o[d]) of a partial
@@ -180,26 +177,14 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)) : "memory");
 }
 #define KVQ_IO8(c, b) c(v[b]), c(v[b + 1]), c(v[b + 2]), c(v[b + 3]), c(v[b + 4]), c(v[b + 5]), c(v[b + 6]), c(v[b + 7])
-// C columns of this warp's lanes -> registers
-template <int C>
-__device__ __forceinline__ void tm_ld(uint32_t a, float (&v)[C]) {
-  if constexpr (C == 32)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n tcgen05.wait::ld.sync.aligned;"
-        : KVQ_IO8("=f", 0), KVQ_IO8("=f", 8), KVQ_IO8("=f", 16), KVQ_IO8("=f", 24)
-        : "r"(a)
-        : "memory");
-  else
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
-        "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n tcgen05.wait::ld.sync.aligned;"
-        : KVQ_IO8("=f", 0), KVQ_IO8("=f", 8), KVQ_IO8("=f", 16), KVQ_IO8("=f", 24), KVQ_IO8("=f", 32), KVQ_IO8("=f", 40),
-          KVQ_IO8("=f", 48), KVQ_IO8("=f", 56)
-        : "r"(a), "r"(a + 32)
-        : "memory");
+// 32 columns of this warp's lanes -> registers
+__device__ __forceinline__ void tm_ld32(uint32_t a, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n tcgen05.wait::ld.sync.aligned;"
+      : KVQ_IO8("=f", 0), KVQ_IO8("=f", 8), KVQ_IO8("=f", 16), KVQ_IO8("=f", 24)
+      : "r"(a)
+      : "memory");
 }
 __device__ __forceinline__ void tm_ld8(uint32_t a, float (&v)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : KVQ_IO8("=f", 0) : "r"(a));
@@ -282,14 +267,12 @@ __device__ __forceinline__ SeqState seq_state(const TreeParams& P, int b) {
 }
 
 // Row tiles a sequence takes (a bad one: one, which reports it).
-template <int N>
 __device__ __forceinline__ int row_tiles(const TreeParams& P, int b) {
   const long long n = (long long)P.cu_rows[b + 1] - P.cu_rows[b];
   if (n <= 0) return 0;
   return n > kNodes ? 1 : (int)((n * P.gqa + N - 1) / N);
 }
 
-template <int N>
 struct Layout {          // dynamic shared memory, from a 1024-byte boundary
   static constexpr int kQ = 0;                              // q' fp16, K-major: two slabs of N x 128 B
   static constexpr int kQb = kQ + 2 * N * 128;              // q' bf16 likewise
@@ -306,7 +289,6 @@ struct Layout {          // dynamic shared memory, from a 1024-byte boundary
   static_assert(kStages * kTilePages * 1568 <= 4 * kSlab, "page stages");
 };
 
-template <int N>
 struct TreeShared {
   __align__(16) uint64_t page_full[kStages], page_free[kStages], q_full, seen_full, vote[2], meet[2], k_full[2], v_full[2], s_full[2], s_free[2], p_full[2],
       pv_done[2];
@@ -314,7 +296,7 @@ struct TreeShared {
   int gave_up;
   int pid[kStages][kTilePages];
   float lane_scale[4][kTile];
-  uint32_t alive[4][4];            // tokens of a tile that exist, by lane quadrant
+  __align__(4) uint16_t alive[4][kTilePages];            // tokens of a tile that exist, by lane quadrant
   __align__(16) float neg_m[N];    // minus the reference of every row
   __align__(16) float alpha[N];    // a moved reference: factor of what is summed so far
   float red[4][N];                 // per-quadrant maxima; at the end parts of the sums
@@ -326,20 +308,20 @@ struct TreeShared {
   float amax[kSmWarps];
 };
 
-static_assert(kNodeWords == 4 && offsetof(TreeShared<128>, seen) % 16 == 0 && offsetof(TreeShared<64>, seen) % 16 == 0, "ancestor rows");
-static_assert(offsetof(TreeShared<128>, neg_m) % 16 == 0 && offsetof(TreeShared<128>, alpha) % 16 == 0 &&
-                  offsetof(TreeShared<64>, neg_m) % 16 == 0 && offsetof(TreeShared<64>, alpha) % 16 == 0 &&
-                  Layout<64>::kEnd % 1024 == 0 && Layout<128>::kEnd % 1024 == 0, "vector loads");
-static_assert(Layout<128>::kEnd + sizeof(TreeShared<128>) <= 227 * 1024, "shared memory of an SM");
+static_assert(kNodeWords == 4 && offsetof(TreeShared, seen) % 16 == 0 && offsetof(TreeShared, neg_m) % 16 == 0 &&
+                  offsetof(TreeShared, alpha) % 16 == 0 && Layout::kEnd % 1024 == 0,
+              "vector loads");
+static_assert(Layout::kEnd + sizeof(TreeShared) <= 227 * 1024, "shared memory of an SM");
 
-template <int N, int NG>
+template <int NG>
 __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_constant__ TreeParams P) {
-  using L = Layout<N>;
+  using L = Layout;
   constexpr int kCols = N / 2;                              // rows of a softmax warp
-  // TMEM columns: O, S twice (the next product runs while the softmax reads the last), then the key
-  // operand (64, or 128 as pairs) and the value operand (64), twice where there is room
+  static_assert(kCols == 32, "a softmax warp's lanes stand for its rows at times");
+  // TMEM columns: O, S twice (the next product runs while the softmax reads the last), the key operand
+  // (64, or 128 as pairs) twice and the value operand (64), twice where there is room
   constexpr int kKCols = NG == 1 ? 64 : 128;
-  constexpr int kKBufs = N == 128 ? 1 : 2, kVBufs = N == 64 && NG == 1 ? 2 : 1;
+  constexpr int kKBufs = 2, kVBufs = NG == 1 ? 2 : 1;
   constexpr uint32_t kColO = 0, kColS = N, kColK = 3 * N, kColV = kColK + kKBufs * kKCols;
   static_assert(kColV + kVBufs * 64 <= 512, "TMEM columns");
   constexpr uint32_t kIdescF16 = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
@@ -347,7 +329,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
   constexpr uint32_t kIdescB16 = kIdescF16 | (1u << 7) | (1u << 10);
   constexpr uint32_t kIdescB16PV = kIdescB16 | (1u << 15) | (1u << 16);
   extern __shared__ __align__(1024) uint8_t sm[];           // (all of the shared memory: it starts aligned)
-  TreeShared<N>& S = *reinterpret_cast<TreeShared<N>*>(sm + L::kEnd);
+  TreeShared& S = *reinterpret_cast<TreeShared*>(sm + L::kEnd);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   volatile int* gave_up = &S.gave_up;
   pdl_trigger();
@@ -362,7 +344,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
   const int split = blockIdx.z, h = blockIdx.y;
   int b = -1, rt = 0;
   for (int b0 = 0, before = 0; b0 < P.batch && b < 0; b0 += 32) {
-    const int mine = b0 + lane < P.batch ? row_tiles<N>(P, b0 + lane) : 0;
+    const int mine = b0 + lane < P.batch ? row_tiles(P, b0 + lane) : 0;
     int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -418,10 +400,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       bar_init(&S.page_full[i], 1);
-      bar_init(&S.page_free[i], 4 + kValWarps);
+      bar_init(&S.page_free[i], kKeyWarps + kValWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(&S.k_full[i], 4);
+      bar_init(&S.k_full[i], kKeyWarps);
       bar_init(&S.v_full[i], kValWarps);
       bar_init(&S.s_full[i], 1);
       bar_init(&S.s_free[i], kSmWarps);
@@ -451,7 +433,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
   const int nwc = max(0, min(t1, nw) - t0);                 // this CTA's window tiles: its first ones
   uint8_t* stages = sm + L::kPages;
   if (warp >= kQkWarp) {
-    regs_dec<Regs<N>::kIssue>();
+    regs_dec<kRegsIssue>();
     if (warp == kPageWarp) {
       // ---- pages
       const int32_t* tab = P.page_table + (size_t)b * P.max_pages;
@@ -556,7 +538,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
               mma_ss(ts, k_d + (((s >> 2) * kSlab + (s & 3) * 32) >> 4), qb_d + (((s >> 2) * N * 128 + (s & 3) * 32) >> 4),
                      kIdescB16, s > 0);
         } else {
-          const uint32_t ka = tb + kColK + (kKBufs == 2 ? kKCols * (i & 1) : 0);
+          const uint32_t ka = tb + kColK + kKCols * (i & 1);
           const uint64_t za = desc_plain(saddr(sm + L::kZa + (i & 1) * kTile * 32), kTile * 16);
           if (elect()) {
 #pragma unroll 2
@@ -606,8 +588,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       if (!ok && i > 0) settle(&S.pv_done[(i - 1) & 1], (i - 1) >> 1);
     }
   } else if (warp >= kKeyWarp) {
-    if (warp < kValWarp) regs_dec<Regs<N>::kKeys>();
-    else regs_dec<Regs<N>::kValues>();
+    if (warp < kValWarp) regs_dec<kRegsKeys>();
+    else regs_dec<kRegsValues>();
     // ---- operands of a tile, lane quadrant q of TMEM.  Window tiles: 128 threads copy the rows
     // into swizzled shared memory, 16 lanes a row
     const bool keys = warp < kValWarp;
@@ -625,7 +607,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       uint8_t* dst = sm + (keys ? L::kK : L::kV);
       const int j = t & 15;
 #pragma unroll 4
-      for (int r = t >> 4; r < kTile; r += keys ? 8 : 2 * kValWarps) {
+      for (int r = t >> 4; r < kTile; r += 2 * (keys ? kKeyWarps : kValWarps)) {
         const int w = min(w0 + r, n_win - 1);
         const int tok = w < n_sink ? w : ring0 + w - n_sink;
         const uint16_t* src = w < n_sink ? sink + (((size_t)b * P.hkv + h) * P.s_sink + tok) * kHeadDim
@@ -638,7 +620,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       if (keys) {
         S.lane_scale[i & 3][t] = 1.f;
         const unsigned alive = __ballot_sync(0xffffffffu, w0 + t < n_win);
-        if (lane == 0) S.alive[i & 3][q] = alive;
+        if (lane == 0) {
+          S.alive[i & 3][2 * q] = (uint16_t)alive;
+          S.alive[i & 3][2 * q + 1] = (uint16_t)(alive >> 16);
+        }
       }
       fence_async();
       __syncwarp();
@@ -655,14 +640,13 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         if (!ok) break;
         fence_after();
         const uint8_t* base = stages + (size_t)stage * kTilePages * pb;
-        const uint32_t tk = tq + kColK + (kKBufs == 2 ? kKCols * (i & 1) : 0);
-        uint32_t alive = 0u;
+        const uint32_t tk = tq + kColK + kKCols * (i & 1);
 #pragma unroll 1
         for (int j = 0; j < 2; ++j) {
           const int pg = 2 * q + j;
           const uint8_t* pgp = base + (size_t)pg * pb;
           const int valid = S.pid[stage][pg] < 0 ? 0 : max(0, min(kPage, n_tok - kPage * (page0 + pg)));
-          alive |= ((1u << valid) - 1u) << (16 * j);
+          if (lane == 0) S.alive[i & 3][pg] = (uint16_t)((1u << valid) - 1u);
           const uint32_t ta = tk + ((uint32_t)(16 * j) << 16);
           // (a page that is not there leaves whatever the stage holds: its tokens are masked)
           const uint4 w = lds16(pgp + 16 * lane);
@@ -758,7 +742,6 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
             S.lane_scale[i & 3][16 * pg + row + 8] = ls[1];
           }
         }
-        if (lane == 0) S.alive[i & 3][q] = alive;
         wait_st();
         fence_before();
         fence_async();
@@ -774,11 +757,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       const int pages = (warp - kValWarp) >> 2;             // this warp's pages: 4 of the 8
       // slots m = 2 q, 2 q + 1 of the words
       uint32_t mask[2], one[2];
-      int shift[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int m = 2 * q + j, sp = slot_pow(m);
-        shift[j] = m <= 4 ? 0 : 10;
+        const int sp = slot_pow(2 * q + j);
         mask[j] = 0x00030003u << (2 * sp);
         one[j] = (uint32_t)(25 - 2 * sp) * 0x04000400u;     // 2^(10 - 2 sp): the code's bits then count ones
       }
@@ -803,7 +784,15 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
           d[1] = *reinterpret_cast<const uint32_t*>(dp + 16 * NG);
           z[0] = *reinterpret_cast<const uint32_t*>(dp + 32 * NG);
           z[1] = *reinterpret_cast<const uint32_t*>(dp + 48 * NG);
-          const uint32_t vw[4] = {w.x, w.y, w.z, w.w};
+          uint32_t vw[2][4] = {{w.x, w.y, w.z, w.w}, {w.x, w.y, w.z, w.w}};
+          if (q >= 2) {                                     // slots from 5 on stand 10 bits up
+#pragma unroll
+            for (int r = 0; r < 4; ++r) vw[1][r] >>= 10;
+            if (q == 3) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) vw[0][r] = vw[1][r];
+            }
+          }
 #pragma unroll
           for (int y = 0; y < 2; ++y) z[y] = h2bits(__hmul2(bits2h(d[y]), bits2h(z[y] ^ 0x80008000u)));
           uint32_t a[2][4];
@@ -812,7 +801,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               // 2^(10 - 2 sp) + c, then c (exact), then Delta c - Delta z
-              const __half2 c = __hsub2(bits2h(((vw[r] >> shift[j]) & mask[j]) | one[j]), bits2h(one[j]));
+              const __half2 c = __hsub2(bits2h((vw[j][r] & mask[j]) | one[j]), bits2h(one[j]));
               a[j][r] = h2bits(__hfma2(c, bits2h(d[r >> 1]), bits2h(z[r >> 1])));
             }
           if (!whole) {                                     // dead tokens: zeros, whatever the page holds there
@@ -842,7 +831,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       }
     }
   } else {
-    regs_inc<Regs<N>::kSoftmax>();
+    regs_inc<kRegsSoftmax>();
     // ---- softmax: token 32 q + lane of every tile, rows kCols half ..
     const int q = warp & 3, half = warp >> 2;
     const uint32_t tq = tb + ((uint32_t)(32 * q) << 16);
@@ -874,41 +863,40 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       softmax_sync();
 #pragma unroll
       for (int w = 0; w < kSmWarps; ++w) amax = fmaxf(amax, S.amax[w]);
-      if (amax > 0.f && amax < INFINITY) sigma = 14 - ((int)(__float_as_uint(amax) >> 23) - 126);   // amax 2^sigma < 2^14
+      // amax 2^sigma < 2^14
+      if (amax > 0.f && amax < INFINITY) sigma = min(100, 14 - ((int)(__float_as_uint(amax) >> 23) - 126));
       // fp16 rows, channel slot s scaled by 4^-s for the codes that carry 4^s
 #pragma unroll 2
       for (int i = tid; i < N * 16; i += 256) {
         const int c = i >> 4, j = i & 15;
         const uint4 v = lds16(sm + L::kQb + at(c, j));
-        const float f = ldexpf(1.f, sigma - 2 * slot_pow(j >> 1));
+        const float f = __int_as_float((sigma - 2 * slot_pow(j >> 1) + 127) << 23);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t o[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] = pack16(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
         *reinterpret_cast<uint4*>(sm + L::kQ + at(c, j)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
-      // zero-point operand, row c: slots 2 g, 2 g + 1: -sum of group g (hi), slot 8 + 2 g: its lo
-      if (tid < N) {
-        const int c = tid;
-        const float fz = ldexpf(1.f, NG == 1 ? sigma - 19 : sigma - 16);
-        uint32_t z[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+      // zero-point operand, row c: slots 2 g, 2 g + 1: -sum of group g (hi), slot 8 + 2 g: its lo.  Four
+      // threads a row, 32 channels each
+      {
+        const int c = tid >> 2, part = tid & 3;
+        float acc = 0.f;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          float acc = 0.f;
-#pragma unroll 2
-          for (int j = g * (16 / NG); j < (g + 1) * (16 / NG); ++j) {
-            const uint4 v = lds16(sm + L::kQb + at(c, j));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int j = 0; j < 4; ++j) {
+          const uint4 v = lds16(sm + L::kQb + at(c, 4 * part + j));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc += __uint_as_float(w[k] << 16) + __uint_as_float(w[k] & 0xffff0000u);
-          }
-          const float v = -acc * fz;
-          const float hi = __half2float(__float2half_rn(v));
-          z[g] = pack16(hi, hi);
-          z[4 + g] = pack16(v - hi, 0.f);
+          for (int k = 0; k < 4; ++k) acc += __uint_as_float(w[k] << 16) + __uint_as_float(w[k] & 0xffff0000u);
         }
-        *reinterpret_cast<uint4*>(sm + L::kZ + (c >> 3) * 128 + (c & 7) * 16) = make_uint4(z[0], z[1], z[2], z[3]);
-        *reinterpret_cast<uint4*>(sm + L::kZ + N * 16 + (c >> 3) * 128 + (c & 7) * 16) = make_uint4(z[4], z[5], z[6], z[7]);
+        if (NG <= 2) acc += __shfl_xor_sync(0xffffffffu, acc, 1);
+        if (NG == 1) acc += __shfl_xor_sync(0xffffffffu, acc, 2);
+        const float from = __shfl_sync(0xffffffffu, acc, (lane & ~3) + (part * (4 / NG) & 3));   // slot pair `part`: group part
+        const float v = part < NG ? -from * ldexpf(1.f, NG == 1 ? sigma - 19 : sigma - 16) : 0.f;
+        const float hi = __half2float(__float2half_rn(v));
+        uint8_t* to = sm + L::kZ + (c >> 3) * 128 + (c & 7) * 16 + 4 * part;
+        *reinterpret_cast<uint32_t*>(to) = pack16(hi, hi);
+        *reinterpret_cast<uint32_t*>(to + N * 16) = pack16(v - hi, 0.f);
       }
       fence_async();
       __syncwarp();
@@ -919,7 +907,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
 #pragma unroll
     for (int j = 0; j < kCols; ++j) l[j] = 0.f;
     bool lost = false;
-    uint32_t unseen = (1u << (kCols / 32)) - 1u;            // lane j: rows c0 + 32 ch + j that have seen no token yet
+    bool unseen = true;                                     // row c0 + lane has seen no token yet
     bool force = true;                                      // ... there are such rows (all four warps agree)
     int meets = 0;
     // the half's four warps meet (bounded, so that a warp that gave up leaves nobody behind)
@@ -938,33 +926,29 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       const uint32_t ts = tq + kColS + N * (i & 1);
       const bool win = i < nwc;
       const float ls = S.lane_scale[i & 3][tok] * (win ? P.scale_log2 : page_scale);
-      const uint32_t alive = S.alive[i & 3][q];
+      const uint32_t alive = *reinterpret_cast<const uint32_t*>(&S.alive[i & 3][2 * q]);
       // window tiles that reach into the drafts: else every row sees every token
       const bool drafts = win && (n_sink > st.L0 || (t0 + i + 1) * kTile > n_win - st.n);
       const bool masked = drafts || alive != 0xffffffffu;
-      uint32_t see[kCols / 32];                             // rows that see this token
+      uint32_t see = 0xffffffffu;                           // rows that see this token
       if (masked) {
         if (drafts && !warp_wait(&S.seen_full, 0, gave_up)) lost = true;
         const int w = (t0 + i) * kTile + tok;
         const int node = win ? (w < n_sink ? w : ring0 + w - n_sink) - st.L0 : -1;
-        const bool mine = (alive >> lane) & 1u;
-#pragma unroll
-        for (int ch = 0; ch < kCols / 32; ++ch) {
-          see[ch] = mine ? 0xffffffffu : 0u;
-          if (mine && drafts && node >= 0) {
-            see[ch] = 0u;
-            const int wd = (node >> 5) & (kNodeWords - 1);
+        see = (alive >> lane) & 1u ? 0xffffffffu : 0u;
+        if (see && drafts && node >= 0) {
+          see = 0u;
+          const int wd = (node >> 5) & (kNodeWords - 1);
 #pragma unroll 1
-            for (int j = 0; j < 32; ++j)
-              see[ch] |= ((S.seen[min((row0 + c0 + 32 * ch + j) >> P.gqa_log2, kNodes - 1)][wd] >> (node & 31)) & 1u) << j;
-          }
+          for (int j = 0; j < 32; ++j)
+            see |= ((S.seen[min((row0 + c0 + j) >> P.gqa_log2, kNodes - 1)][wd] >> (node & 31)) & 1u) << j;
         }
       }
       float x[kCols];
       bool moved = false;
 #pragma unroll 1
       for (;;) {
-        tm_ld<kCols>(ts + c0, x);
+        tm_ld32(ts + c0, x);
         // scores less the reference
 #pragma unroll
         for (int j = 0; j < kCols; j += 4) {
@@ -976,7 +960,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         }
         if (masked) {
 #pragma unroll
-          for (int j = 0; j < kCols; ++j) x[j] = (see[j / 32] >> (j & 31)) & 1u ? x[j] : -INFINITY;
+          for (int j = 0; j < kCols; ++j) x[j] = (see >> j) & 1u ? x[j] : -INFINITY;
         }
         if (!moved) {
           float mx[4];
@@ -1010,31 +994,23 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         for (int j = 0; j < kCols; j += 8) {
           float y[8];
           tm_ld8(ts + c0 + j, y);
-          const uint32_t bits = masked ? (kCols > 32 && j >= 32 ? see[kCols / 32 - 1] : see[0]) >> (j & 31) : 0xffu;
+          const uint32_t bits = see >> j;
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = (bits >> e) & 1u ? y[e] * ls : -INFINITY;
           const float top = reduce_columns(y, lane, [](float a, float b2) { return fmaxf(a, b2); });
           if (lane < 8) S.red[q][c0 + j + lane] = top;
         }
         meet();
-        float now[kCols / 32];
-#pragma unroll
-        for (int ch = 0; ch < kCols / 32; ++ch) {
-          const int c = c0 + 32 * ch + lane;
-          const float up = fmaxf(fmaxf(S.red[0][c], S.red[1][c]), fmaxf(S.red[2][c], S.red[3][c]));
-          // a first token sets the reference, later ones only raise it
-          const bool fresh = (unseen >> ch) & 1u, any = up > -INFINITY;
-          const float old = -S.neg_m[c];
-          now[ch] = fresh ? (any ? up : 0.f) : fmaxf(old, up);
-          if (any) unseen &= ~(1u << ch);
-          if (q == 0) S.alpha[c] = fresh ? 0.f : ex2(old - now[ch]);
-        }
-        force = __any_sync(0xffffffffu, unseen != 0u);
+        const int c = c0 + lane;
+        const float up = fmaxf(fmaxf(S.red[0][c], S.red[1][c]), fmaxf(S.red[2][c], S.red[3][c]));
+        // a first token sets the reference, later ones only raise it
+        const bool any = up > -INFINITY;
+        const float old = -S.neg_m[c], now = unseen ? (any ? up : 0.f) : fmaxf(old, up);
+        if (q == 0) S.alpha[c] = unseen ? 0.f : ex2(old - now);
+        if (any) unseen = false;
+        force = __any_sync(0xffffffffu, unseen);
         meet();                                             // (everyone has read the old references)
-        if (q == 0) {
-#pragma unroll
-          for (int ch = 0; ch < kCols / 32; ++ch) S.neg_m[c0 + 32 * ch + lane] = -now[ch];
-        }
+        if (q == 0) S.neg_m[c] = -now;
 #pragma unroll
         for (int j = 0; j < kCols; j += 4) {
           const float4 al = *reinterpret_cast<const float4*>(&S.alpha[c0 + j]);
@@ -1116,28 +1092,25 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     }
     meet();
     if (!lost) {
+      // every thread: one channel of the half's rows, 8 rows at a time
+      const int c = c0 + lane;
+      const float sum = (S.red[0][c] + S.red[1][c]) + (S.red[2][c] + S.red[3][c]);
+      // 1 / l; a row that saw nothing gives 0, one whose sum is no number that
+      const float by = P.splits > 1 ? 1.f : sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
+      const float top = sum != 0.f ? -S.neg_m[c] : -1e30f;
+      if (P.splits > 1 && q == 0 && c < ncol)
+        *reinterpret_cast<float2*>(P.part + ((size_t)S.row[c] * P.splits + split) * kRec) = make_float2(top, sum);
 #pragma unroll 1
       for (int j = 0; j < kCols && c0 + j < ncol; j += 8) {
         float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (nt > 0) tm_ld8(tq + kColO + c0 + j, o);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int c = c0 + j + e;
-          if (c < ncol) {
-            float sum = S.red[0][c] + S.red[1][c];
-            if (kCols == 32) sum += S.red[2][c] + S.red[3][c];
-            const size_t r = (size_t)S.row[c];
-            if (P.splits == 1) {
-              const float v = sum > 0.f ? __fdividef(o[e], sum) : (sum == 0.f ? 0.f : o[e] * sum);
-              P.out[r * kHeadDim + tok] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-            } else {
-              float* rec = P.part + (r * P.splits + split) * kRec;
-              rec[4 + tok] = o[e];
-              if (tok == 0) {
-                rec[0] = sum != 0.f ? -S.neg_m[c] : -1e30f;   // (a row that saw nothing here)
-                rec[1] = sum;
-              }
-            }
+          const float v = o[e] * __shfl_sync(0xffffffffu, by, j + e);
+          const size_t r = (size_t)S.row[c0 + j + e];
+          if (c0 + j + e < ncol) {
+            if (P.splits == 1) P.out[r * kHeadDim + tok] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            else P.part[(r * P.splits + split) * kRec + 4 + tok] = v;
           }
         }
       }
@@ -1203,23 +1176,20 @@ __global__ void __launch_bounds__(kMThreads) attn_tree_merge_kernel(const __grid
   reinterpret_cast<uint2*>(P.out + (size_t)r * kHeadDim)[lane] = make_uint2(packb16(O.x, O.y), packb16(O.z, O.w));
 }
 
-// Columns (rows of a tile) and splits of a call, from its sizes alone.
+// Row tiles and splits of a call, from its sizes alone.
 struct Shape {
-  int n, splits, items;
+  int splits, items;
 };
 Shape tree_shape(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
   const int g = cfg->n_q_heads / cfg->n_kv_heads;
   Shape s;
-  // 128 rows share one expansion where TMEM holds two S of them (keys as codes); else, and for trees
-  // that fit, 64
   const long long per_seq = ((long long)n_rows * g + cfg->batch - 1) / cfg->batch;
-  s.n = per_seq > 64 && cfg->group_size == kHeadDim ? 128 : 64;
-  s.items = (int)min((long long)n_rows, (long long)n_rows * g / s.n + cfg->batch);
+  s.items = (int)min((long long)n_rows, (long long)n_rows * g / N + cfg->batch);
   const long long pages = max(0LL, min((long long)cfg->max_pages_per_seq, ((long long)max_ctx - cfg->s_sink + kPage - 1) / kPage));
   const long long win = min((long long)cfg->s_sink + cfg->s_keep + cfg->s_flush + kNodes, (long long)max_ctx);
   const long long tiles = max(1LL, (pages + kTilePages - 1) / kTilePages + (win + kTile - 1) / kTile);
   // about as many CTAs as the row tiles there will be (a sequence's last one is half empty on average)
-  const long long units = max(1LL, min((long long)s.items, (per_seq + s.n - 1) / s.n * min((long long)cfg->batch, (long long)n_rows))) *
+  const long long units = max(1LL, min((long long)s.items, (per_seq + N - 1) / N * min((long long)cfg->batch, (long long)n_rows))) *
                           cfg->n_kv_heads;
   // a wave of 152 CTAs takes tiles / splits, and about 6 tiles' time for set-up and merge
   double best = 1e300;
@@ -1284,16 +1254,15 @@ extern "C" int kvq_launch_attn_tree(const kvq_config* cfg, const kvq_cache* cach
   P.scale_log2 = sm_scale * 1.4426950408889634f;
   if (cfg->n_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
   const int ng = kHeadDim / cfg->group_size;
-  void (*kern)(const TreeParams) = s.n == 128 ? attn_tree_kernel<128, 1> : ng == 1 ? attn_tree_kernel<64, 1>
-                                                    : ng == 2 ? attn_tree_kernel<64, 2> : attn_tree_kernel<64, 4>;
-  const size_t smem = s.n == 64 ? Layout<64>::kEnd + sizeof(TreeShared<64>) : Layout<128>::kEnd + sizeof(TreeShared<128>);
+  void (*kern)(const TreeParams) = ng == 1 ? attn_tree_kernel<1> : ng == 2 ? attn_tree_kernel<2> : attn_tree_kernel<4>;
+  constexpr size_t smem = Layout::kEnd + sizeof(TreeShared);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ERR_CUDA;
   static std::mutex mu;
-  static unsigned long long done[4] = {};
+  static unsigned long long done[3] = {};
   {
     std::lock_guard<std::mutex> lock(mu);
-    const int vi = s.n == 128 ? 3 : ng == 1 ? 0 : ng == 2 ? 1 : 2;
+    const int vi = ng == 1 ? 0 : ng == 2 ? 1 : 2;
     if (!(done[vi] & (1ull << dev))) {
       // (the register split counts on what the kernel launches with: a warpgroup would wait for ever)
       cudaFuncAttributes fa;
