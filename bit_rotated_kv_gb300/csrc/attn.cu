@@ -77,9 +77,12 @@ struct AttnParams {
   // position seq_len[bc] - (cu_rows[bc + 1] - b).  nullptr: one decode query per sequence.
   const int32_t* cu_rows;
   int seqs;
-  // drafted trees (kv_attn_tree): parent node of every row, local to its sequence (-1: a root);
-  // the row then sees the tokens before the sequence's rows, its ancestors and itself.
+  // drafted trees (kv_attn_tree): parent node of every row, local to its sequence (-1: a root); a
+  // row sees the tokens before the sequence's rows, its ancestors and itself.  A grid row is then a
+  // group of nodes of one sequence, gqa (node, head) columns for heads query heads per kv head
+  // (1 << heads_log2); n_rows rows in all.
   const int32_t* parent;
+  int heads, heads_log2, gqa_log2, n_rows;
 };
 
 // Cache sequence of grid row b (-1: a chunk row outside cu_rows).  cu_rows is a per-call input:
@@ -96,32 +99,74 @@ __device__ __forceinline__ int attn_seq(const AttnParams& P, int b) {
   return lo;
 }
 
+// Drafted trees: the sequence and the first node of node group b (groups counted over the sequences
+// in order; every warp looks its group up for itself).  -1: there is no such group.
+__device__ __forceinline__ int tree_group(const AttnParams& P, int b, int& node0) {
+  const int lane = threadIdx.x & 31;
+  for (int b0 = 0, before = 0; b0 < P.seqs; b0 += 32) {
+    const long long n = b0 + lane < P.seqs ? (long long)P.cu_rows[b0 + lane + 1] - P.cu_rows[b0 + lane] : 0;
+    const int pack_log2 = P.gqa_log2 - P.heads_log2;
+    const int mine = n > 0 ? ((int)min(n, (long long)P.n_rows) + (1 << pack_log2) - 1) >> pack_log2 : 0;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += t;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + upto > b);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      node0 = (b - before - __shfl_sync(0xffffffffu, upto - mine, at)) << pack_log2;
+      return b0 + at;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return -1;
+}
+
+// A sequence's drafted nodes.
+struct TreeSeq {
+  int first, n, L0;      // rows first .. first + n - 1; length before them
+};
+
 // Length and INT2 edge that grid row b sees (after the dependency wait): a decode query sees
 // its sequence's seq_len tokens; a chunk query the tokens up to its own position.
-// TREE: L0 is the sequence's length before its rows, which must all lie in the BF16 windows
-// (otherwise the row sees nothing and the fault is reported).
-template <bool TREE = false>
-__device__ __forceinline__ void unit_state(const AttnParams& P, int b, int bc, int& L, int& sq, int* L0 = nullptr) {
+__device__ __forceinline__ void unit_state(const AttnParams& P, int b, int bc, int& L, int& sq) {
   if (bc < 0) {
     L = 0;
     sq = P.s_sink;
-    if (TREE) *L0 = 0;
     return;
   }
   L = P.seq_len[bc];
   sq = P.s_quant[bc];
-  if constexpr (TREE) {
-    const int n = __ldg(P.cu_rows + bc + 1) - __ldg(P.cu_rows + bc);
-    *L0 = L - n;
-    if (n > KVQ_TREE_MAX_NODES || *L0 < 0 || sq > max(*L0, P.s_sink)) {
-      L = 0;
-      *L0 = 0;
-      sq = P.s_sink;
-      set_status(P.status, KVQ_ERR_BOUNDS);
-      return;
-    }
-  }
   if (P.cu_rows) L = max(0, min(L, L - (__ldg(P.cu_rows + bc + 1) - b) + 1));
+}
+// ... a group of nodes from node0 on: the tokens before the drafts and the drafts up to the group's
+// last.  Drafts that are no tree or do not all lie in the BF16 windows see nothing, and are reported.
+__device__ __forceinline__ TreeSeq tree_state(const AttnParams& P, int bc, int node0, int& L, int& sq) {
+  TreeSeq t;
+  t.first = P.cu_rows[bc];
+  t.n = P.cu_rows[bc + 1] - t.first;
+  L = P.seq_len[bc];
+  sq = P.s_quant[bc];
+  t.L0 = L - t.n;
+  if (t.first < 0 || t.n < 1 || t.n > P.n_rows || t.first > P.n_rows - t.n || t.n > KVQ_TREE_MAX_NODES || t.L0 < 0 ||
+      sq > max(t.L0, P.s_sink)) {
+    L = 0;
+    t.L0 = 0;
+    sq = P.s_sink;
+    set_status(P.status, KVQ_ERR_BOUNDS);
+    return t;
+  }
+  L = t.L0 + min(t.n, node0 + (1 << (P.gqa_log2 - P.heads_log2)));
+  return t;
+}
+// Row of q / out of column c of a node group (first row t.first, first node node0), or -1.
+__device__ __forceinline__ long long tree_row(const AttnParams& P, const TreeSeq& t, int node0, int h, int c) {
+  const int node = node0 + (c >> P.heads_log2);
+  const long long row = (long long)t.first + node;
+  if (node >= t.n || row < 0 || row >= P.n_rows) return -1;
+  return (row * P.hkv + h) * P.heads + (c & (P.heads - 1));
 }
 
 // ---- PTX helpers ----------------------------------------------------------------------
@@ -330,7 +375,7 @@ __device__ __forceinline__ uint32_t dz_operand(uint32_t dz, bool odd) {
 }
 
 template <int NG, bool L2, bool KC, bool TREE>
-__device__ void int2_split(const AttnParams& P, uint8_t* smem, int b, int bc, int h, int split, float* res,
+__device__ void int2_split(const AttnParams& P, uint8_t* smem, int b, int bc, int node0, int h, int split, float* res,
                            size_t wstride) {
   // accumulators per group; with one group the k-steps alternate between two accumulators so
   // that consecutive MMAs do not wait on each other
@@ -397,8 +442,10 @@ __device__ void int2_split(const AttnParams& P, uint8_t* smem, int b, int bc, in
     const int pid = __shfl_sync(0xffffffffu, pid_a, k);
     if (lane == 0 && k < n_first) refill(k, pid);
   }
-  int Lraw, sqraw, L0raw;
-  unit_state<TREE>(P, b, bc, Lraw, sqraw, &L0raw);
+  int Lraw, sqraw;
+  TreeSeq tree;
+  if constexpr (TREE) tree = tree_state(P, bc, node0, Lraw, sqraw);
+  else unit_state(P, b, bc, Lraw, sqraw);
 
   // ---- this warp's pages inside the INT2 region
   const int L = Lraw;
@@ -416,11 +463,18 @@ __device__ void int2_split(const AttnParams& P, uint8_t* smem, int b, int bc, in
   const int hrow = lane >> 2, quad = lane & 3;
   const bool qodd = (quad & 1) != 0;
   uint32_t qraw[8][2];
+  bool has_row = hrow < g;
+  const uint16_t* qcol = qb + (size_t)hrow * kHeadDim;
+  if constexpr (TREE) {
+    const long long r = tree_row(P, tree, node0, h, hrow);
+    has_row = r >= 0;
+    qcol = P.q + r * kHeadDim;
+  }
 #pragma unroll
   for (int s = 0; s < 8; ++s) {
-    const uint16_t* src = qb + (size_t)hrow * kHeadDim + 16 * s + 2 * quad;
-    qraw[s][0] = (hrow < g) ? *reinterpret_cast<const uint32_t*>(src) : 0u;
-    qraw[s][1] = (hrow < g) ? *reinterpret_cast<const uint32_t*>(src + 8) : 0u;
+    const uint16_t* src = qcol + 16 * s + 2 * quad;
+    qraw[s][0] = has_row ? *reinterpret_cast<const uint32_t*>(src) : 0u;
+    qraw[s][1] = has_row ? *reinterpret_cast<const uint32_t*>(src + 8) : 0u;
   }
   uint32_t bq[8][2];
   uint32_t bz0 = 0u, bz1 = 0u;            // B fragment of the zero-point MMA (k = 2 quad .., + 8 ..)
@@ -876,31 +930,36 @@ __device__ void int2_split(const AttnParams& P, uint8_t* smem, int b, int bc, in
 
 // ---- BF16 windows --------------------------------------------------------------------------
 template <bool TREE>
-__device__ void window_split(const AttnParams& P, int b, int bc, int h, int wsplit, float* res, size_t wstride) {
+__device__ void window_split(const AttnParams& P, int b, int bc, int node0, int h, int wsplit, float* res,
+                             size_t wstride) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = P.gqa;
   pdl_wait();
-  int L, sqw, L0;
-  unit_state<TREE>(P, b, bc, L, sqw, &L0);
-  // TREE: bit i of seen: node i of the sequence is this row's ancestor or the row itself
-  uint32_t seen[KVQ_TREE_MAX_NODES / 32];
+  int L, sqw;
+  TreeSeq tree;
+  // TREE: bit i of seen[x]: node i of the sequence is an ancestor of column 2 (lane % 4) + x's node, or it
+  uint32_t seen[2][KVQ_TREE_MAX_NODES / 32];
   if constexpr (TREE) {
+    tree = tree_state(P, bc, node0, L, sqw);
 #pragma unroll
-    for (int w = 0; w < KVQ_TREE_MAX_NODES / 32; ++w) seen[w] = 0u;
-    if (L > 0) {
-      const int first = __ldg(P.cu_rows + bc);
-      for (int at = b - first, step = 0; at >= 0 && step < KVQ_TREE_MAX_NODES; ++step) {
+    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+      for (int w = 0; w < KVQ_TREE_MAX_NODES / 32; ++w) seen[x][w] = 0u;
+      const int node = node0 + ((2 * (lane & 3) + x) >> P.heads_log2);
+      for (int at = L > 0 && node < tree.n ? node : -1; at >= 0;) {
 #pragma unroll
         for (int w = 0; w < KVQ_TREE_MAX_NODES / 32; ++w)
-          if ((at >> 5) == w) seen[w] |= 1u << (at & 31);
-        const int up = __ldg(P.parent + first + at);
+          if ((at >> 5) == w) seen[x][w] |= 1u << (at & 31);
+        const int up = __ldg(P.parent + tree.first + at);
         if (up >= at || up < -1) {               // not a tree in index order
-          if (lane == 0) set_status(P.status, KVQ_ERR_BOUNDS);
+          set_status(P.status, KVQ_ERR_BOUNDS);
           break;
         }
         at = up;
       }
     }
+  } else {
+    unit_state(P, b, bc, L, sqw);
   }
   const int n_sink = min(P.s_sink, max(L, 0));
   const int r0 = max(min(sqw, L), P.s_sink);              // first recent token
@@ -918,9 +977,15 @@ __device__ void window_split(const AttnParams& P, int b, int bc, int h, int wspl
   uint32_t bq[8][2];
   {
     const uint16_t* qrow = P.q + (((size_t)b * P.hkv + h) * g + hrow) * kHeadDim + 32 * quad;
+    bool has_row = hrow < g;
+    if constexpr (TREE) {
+      const long long r = tree_row(P, tree, node0, h, hrow);
+      has_row = r >= 0;
+      qrow = P.q + r * kHeadDim + 32 * quad;
+    }
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
-      if (hrow < g) {
+      if (has_row) {
         uint2 v2 = *reinterpret_cast<const uint2*>(qrow + 4 * s);
         bq[s][0] = v2.x;
         bq[s][1] = v2.y;
@@ -960,14 +1025,16 @@ __device__ void window_split(const AttnParams& P, int b, int bc, int h, int wspl
       vbase = P.ring_v + off;
       rows_avail = kPage;
     }
-    auto row_ok = [&](int t) {
-      bool ok = tok0 + t >= lo && tok0 + t < hi;
+    auto row_ok = [&](int t) { return tok0 + t >= lo && tok0 + t < hi; };
+    // ... and column 2 quad + x sees the token
+    auto col_ok = [&](int t, int x) {
+      bool ok = row_ok(t);
       if constexpr (TREE) {
-        const int i = tok0 + t - L0;
+        const int i = tok0 + t - tree.L0;
         if (ok && i >= 0) {
           uint32_t word = 0u;
 #pragma unroll
-          for (int w = 0; w < KVQ_TREE_MAX_NODES / 32; ++w) word = (i >> 5) == w ? seen[w] : word;
+          for (int w = 0; w < KVQ_TREE_MAX_NODES / 32; ++w) word = (i >> 5) == w ? seen[x][w] : word;
           ok = (word >> (i & 31)) & 1u;
         }
       }
@@ -993,10 +1060,10 @@ __device__ void window_split(const AttnParams& P, int b, int bc, int h, int wspl
       }
     }
     float sc[4];
-    sc[0] = row_ok(tA) ? acc[0] * P.scale_log2 : -INFINITY;
-    sc[1] = row_ok(tA) ? acc[1] * P.scale_log2 : -INFINITY;
-    sc[2] = row_ok(tB) ? acc[2] * P.scale_log2 : -INFINITY;
-    sc[3] = row_ok(tB) ? acc[3] * P.scale_log2 : -INFINITY;
+    sc[0] = col_ok(tA, 0) ? acc[0] * P.scale_log2 : -INFINITY;
+    sc[1] = col_ok(tA, 1) ? acc[1] * P.scale_log2 : -INFINITY;
+    sc[2] = col_ok(tB, 0) ? acc[2] * P.scale_log2 : -INFINITY;
+    sc[3] = col_ok(tB, 1) ? acc[3] * P.scale_log2 : -INFINITY;
     float p[4], alpha[2];
     softmax_step(sm, sc, p, alpha);
     if (alpha[0] != 1.f || alpha[1] != 1.f) {
@@ -1089,7 +1156,9 @@ __device__ __forceinline__ void store_out(void* out, bool bf16, size_t row, int 
 // Merge n records (m, l, o[d]) per head from the workspace (other CTAs' writes: read past L1)
 // with all loads of a chunk of 8 records in flight: warp w handles head w, lane the channels
 // 4*lane .. 4*lane+3.  TO_OUT: dst[head][j] = o / l; otherwise dst holds merged records.
-__device__ __noinline__ void merge_global(const float* src, int n, int g, void* dst, bool to_out, bool bf16) {
+template <bool TREE>
+__device__ __noinline__ void merge_global(const float* src, int n, int g, void* dst, bool to_out, bool bf16,
+                                          const AttnParams* P = nullptr, int bc = 0, int node0 = 0, int h = 0) {
   const int lane = threadIdx.x & 31;
   for (int hh = threadIdx.x >> 5; hh < g; hh += kWarps) {
   const size_t stride = (size_t)g * kRow;
@@ -1128,7 +1197,13 @@ __device__ __noinline__ void merge_global(const float* src, int n, int g, void* 
   }
   if (to_out) {
     const float inv = (L > 0.f) ? 1.f / L : 0.f;
-    store_out(dst, bf16, (size_t)hh, lane, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
+    long long row = hh;
+    if constexpr (TREE) {
+      TreeSeq t{P->cu_rows[bc], P->cu_rows[bc + 1] - P->cu_rows[bc], 0};
+      row = tree_row(*P, t, node0, h, hh);
+    }
+    if (!TREE || row >= 0)
+      store_out(dst, bf16, (size_t)row, lane, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
   } else {
     float* r = reinterpret_cast<float*>(dst) + (size_t)hh * kRow;
     if (lane == 0) { r[0] = M; r[1] = L; }
@@ -1149,18 +1224,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   const int split = blockIdx.z, h = blockIdx.x, b = blockIdx.y;
   const int g = P.gqa;
   if (P.cu_rows) pdl_wait();          // (the rows' sequences: see attn_seq)
-  const int bc = attn_seq(P, b);
-  if (bc < 0 && threadIdx.x == 0 && split == 0 && h == 0) set_status(P.status, KVQ_ERR_BOUNDS);
+  int node0 = 0;
+  int bc;
+  if constexpr (TREE) {
+    bc = tree_group(P, b, node0);
+    if (b == 0 && h == 0 && split == 0 && threadIdx.x == 0 && (P.cu_rows[0] != 0 || P.cu_rows[P.seqs] != P.n_rows))
+      set_status(P.status, KVQ_ERR_BOUNDS);
+    if (bc < 0) return;               // (the grid is sized for the most groups there can be)
+  } else {
+    bc = attn_seq(P, b);
+    if (bc < 0 && threadIdx.x == 0 && split == 0 && h == 0) set_status(P.status, KVQ_ERR_BOUNDS);
+  }
   // per-warp results: an INT2 warp writes into its own (drained) page ring, a window warp
   // into a plain array; both start after the 1 KB of barriers and query data.
   float* res = reinterpret_cast<float*>(smem + 1024);
   size_t wstride;
   if (split < P.n_int2) {
     wstride = (size_t)kStages * P.page_bytes / sizeof(float);
-    int2_split<NG, L2, KC, TREE>(P, smem, b, bc, h, split, res, wstride);
+    int2_split<NG, L2, KC, TREE>(P, smem, b, bc, node0, h, split, res, wstride);
   } else {
     wstride = (size_t)g * kRow;
-    window_split<TREE>(P, b, bc, h, split - P.n_int2, res, wstride);
+    window_split<TREE>(P, b, bc, node0, h, split - P.n_int2, res, wstride);
   }
   __syncthreads();
   // ---- CTA partial: merge the warps, store to the workspace
@@ -1220,7 +1304,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       }
     }
     const float inv = (Ls > 0.f) ? 1.f / Ls : 0.f;
-    store_out(P.out, P.out_bf16 != 0, (size_t)unit * g + hh, lane, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
+    long long row = (long long)unit * g + hh;
+    if constexpr (TREE) {
+      TreeSeq t{P.cu_rows[bc], P.cu_rows[bc + 1] - P.cu_rows[bc], 0};
+      row = tree_row(P, t, node0, h, hh);
+    }
+    if (!TREE || row >= 0)
+      store_out(P.out, P.out_bf16 != 0, (size_t)row, lane, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
     }
     return;
   }
@@ -1238,14 +1328,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   }
   __syncthreads();
   if (!role) return;
-  void* out_unit = P.out_bf16 ? (void*)(reinterpret_cast<uint16_t*>(P.out) + (size_t)unit * g * kHeadDim)
+  void* out_unit = TREE ? P.out : P.out_bf16 ? (void*)(reinterpret_cast<uint16_t*>(P.out) + (size_t)unit * g * kHeadDim)
                               : (void*)(reinterpret_cast<float*>(P.out) + (size_t)unit * g * kHeadDim);
   const float* gsrc = P.part + ((size_t)unit * P.n_split + (size_t)grp * kGroup) * g * kRow;
   if (n_grp == 1) {
-    merge_global(gsrc, gsize, g, out_unit, true, P.out_bf16 != 0);
+    merge_global<TREE>(gsrc, gsize, g, out_unit, true, P.out_bf16 != 0, TREE ? &P : nullptr, bc, node0, h);
     return;
   }
-  merge_global(gsrc, gsize, g, P.part2 + ((size_t)unit * n_grp + grp) * g * kRow, false, false);
+  merge_global<false>(gsrc, gsize, g, P.part2 + ((size_t)unit * n_grp + grp) * g * kRow, false, false);
   __syncthreads();
   if (threadIdx.x == 0) {
     const int t = atomic_add_acq_rel_gpu(cnt + n_grp, 1);
@@ -1254,7 +1344,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   }
   __syncthreads();
   if (!role) return;
-  merge_global(P.part2 + (size_t)unit * n_grp * g * kRow, n_grp, g, out_unit, true, P.out_bf16 != 0);
+  merge_global<TREE>(P.part2 + (size_t)unit * n_grp * g * kRow, n_grp, g, out_unit, true, P.out_bf16 != 0, TREE ? &P : nullptr, bc, node0, h);
 }
 
 }  // namespace kvq
@@ -1322,9 +1412,14 @@ extern "C" size_t kvq_attn_ws_bytes(const kvq_config* cfg, int32_t max_ctx) {
 static int launch_attn_impl(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot, void* out,
                             int out_bf16, float sm_scale, int32_t max_ctx, void* ws, int32_t* d_status,
                             cudaStream_t stream, const int32_t* cu_rows, int seqs,
-                            const int32_t* parent = nullptr) {
+                            const int32_t* parent = nullptr, int heads = 1, int n_rows = 0) {
   AttnParams P{};
   P.parent = parent;
+  P.heads = heads;
+  P.heads_log2 = heads == 8 ? 3 : heads == 4 ? 2 : heads == 2 ? 1 : 0;
+  const int cols = cfg->n_q_heads / cfg->n_kv_heads;
+  P.gqa_log2 = cols == 8 ? 3 : cols == 4 ? 2 : cols == 2 ? 1 : 0;
+  P.n_rows = n_rows;
   P.cu_rows = cu_rows;
   P.seqs = seqs;
   P.pages = (const uint8_t*)cache->pages;
@@ -1424,15 +1519,36 @@ extern "C" int kvq_launch_attn_chunk(const kvq_config* cfg, const kvq_cache* cac
   return launch_attn_impl(&c, cache, q_rot, out, 0, sm_scale, max_ctx, ws, d_status, stream, cu_rows, cfg->batch);
 }
 
-// Drafted trees: as chunk queries, with the rows' own tokens masked to each row's ancestors.
+// Drafted trees: as chunk queries, a group of a sequence's nodes to a grid row, the drafts masked to each
+// node's ancestors.  The MMA tile has 8 columns whether they are used or not, so a group fills them with
+// 8 / g nodes (g query heads per kv head): 64 sequences of 6,000 tokens and 2 nodes, g 4, take 101 us,
+// against 138 us with a node to a grid row.  Up to 32 rows x kv heads the grid is too small to matter and
+// a row takes a node, whose joins are shorter: 8.5 against 11.6 us for 4 nodes on 500 tokens.
+// The sizes follow from a config of as many sequences as there can be groups.
+static kvq_config tree_config(const kvq_config* cfg, int32_t n_rows) {
+  kvq_config c = *cfg;
+  const long long g = cfg->n_q_heads / cfg->n_kv_heads;
+  if ((long long)n_rows * cfg->n_kv_heads <= 32) {
+    c.batch = n_rows;
+    return c;
+  }
+  c.batch = (int32_t)min((long long)n_rows, n_rows * g / kMaxGqa + cfg->batch);
+  c.n_q_heads = kMaxGqa * cfg->n_kv_heads;
+  return c;
+}
+
+extern "C" size_t kvq_attn_tree_rows_ws_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
+  const kvq_config c = tree_config(cfg, n_rows);
+  return kvq_attn_ws_bytes(&c, max_ctx);
+}
+
 extern "C" int kvq_launch_attn_tree_rows(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot,
                                          const int32_t* cu_rows, const int32_t* parent, int32_t n_rows, uint16_t* out,
                                          float sm_scale, int32_t max_ctx, void* ws, int32_t* d_status,
                                          cudaStream_t stream) {
-  kvq_config c = *cfg;
-  c.batch = n_rows;
+  const kvq_config c = tree_config(cfg, n_rows);
   return launch_attn_impl(&c, cache, q_rot, out, 1, sm_scale, max_ctx, ws, d_status, stream, cu_rows, cfg->batch,
-                          parent);
+                          parent, cfg->n_q_heads / cfg->n_kv_heads, n_rows);
 }
 
 // ---- allocation-free variant ---------------------------------------------------------------

@@ -57,7 +57,8 @@ constexpr int kStages = 4;                       // page tiles in flight
 constexpr int kRegsLaunch = 80, kRegsSoftmax = 104, kRegsKeys = 72, kRegsValues = 56, kRegsIssue = 48;
 static_assert(256 * kRegsSoftmax + 128 * kRegsKeys + 256 * kRegsValues + 128 * kRegsIssue <= kThreadsT * kRegsLaunch, "register split");
 
-constexpr int kWinCost = 3;
+constexpr int kWinCost = 3;                      // a window tile's time in page tiles'
+constexpr long long kSmallCall = 1 << 19;        // row_kernel(): rows x kv heads x tokens
 constexpr int kRec = 4 + kHeadDim;               // (m, l, -, -, o[d]) of a partial
 constexpr int kSpin = 1 << 15, kSuspend = 20000;  // a wait gives up after that many rounds of at most 20 us
 constexpr uint32_t kTmem = 512;
@@ -1210,8 +1211,23 @@ Shape tree_shape(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
 
 using namespace kvq;
 
+// Which kernel a call takes, from its sizes alone.  The row kernel (attn.cu) streams a sequence's cache once
+// for every 8 (node, head) columns, this one once for every 64 at four to five times the time: 64 sequences
+// of 6,000 tokens take 80 us a group of 8 there and 366 us a tile of 64 here.  So the row kernel has trees of
+// up to 4 groups a tile (314 against 366 us), of up to 3 on short contexts, where its windows weigh more (64
+// sequences of 1,000 tokens: 121 against 137 us with 3 groups, 153 against 140 with 4).  It has small calls as well: with 32 nodes and 8 kv heads on 500 tokens it takes 17.6 us
+// against 18.9 here, with 16 on 2,000 14.5 against 22.3, but with 64 on 500 28.9 against 26.3 and with 32 on
+// 4,000 30.6 against 24.3.  Per-channel keys are the row kernel's alone.
+static bool row_kernel(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
+  if (cfg->key_axis != KVQ_KEY_PER_TOKEN) return true;
+  const long long per_seq = ((long long)n_rows * (cfg->n_q_heads / cfg->n_kv_heads) + cfg->batch - 1) / cfg->batch;
+  const long long groups = (per_seq + 7) / 8, tiles = (per_seq + N - 1) / N;
+  const long long units = (long long)n_rows * cfg->n_kv_heads;
+  return groups <= (max_ctx < 2048 ? 3 : 4) * tiles || (units <= 256 && units * max_ctx <= kSmallCall);
+}
+
 extern "C" size_t kvq_attn_tree_ws_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
-  if (cfg->key_axis != KVQ_KEY_PER_TOKEN) return kvq_attn_chunk_ws_bytes(cfg, n_rows, max_ctx);
+  if (row_kernel(cfg, n_rows, max_ctx)) return kvq_attn_tree_rows_ws_bytes(cfg, n_rows, max_ctx);
   const Shape s = tree_shape(cfg, n_rows, max_ctx);
   return s.splits > 1 ? (size_t)n_rows * cfg->n_q_heads * s.splits * kRec * sizeof(float) : 256;
 }
@@ -1219,7 +1235,7 @@ extern "C" size_t kvq_attn_tree_ws_bytes(const kvq_config* cfg, int32_t n_rows, 
 extern "C" int kvq_launch_attn_tree(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot,
                                     const int32_t* cu_rows, const int32_t* parent, int32_t n_rows, uint16_t* out,
                                     float sm_scale, int32_t max_ctx, void* ws, int32_t* d_status, cudaStream_t stream) {
-  if (cfg->key_axis != KVQ_KEY_PER_TOKEN)
+  if (row_kernel(cfg, n_rows, max_ctx))
     return kvq_launch_attn_tree_rows(cfg, cache, q_rot, cu_rows, parent, n_rows, out, sm_scale, max_ctx, ws, d_status,
                                      stream);
   const Shape s = tree_shape(cfg, n_rows, max_ctx);
