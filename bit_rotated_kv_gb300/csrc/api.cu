@@ -226,7 +226,7 @@ KVQ_API int kv_verify_tree(const kvq_config* cfg, const int32_t* cu_rows, const 
   if (n_rows < 0 || vocab < 1 || !cu_rows || !n_accept || !next_token || !aligned(cu_rows, 4) ||
       !aligned(n_accept, 4) || !aligned(next_token, 4))
     return KVQ_ERR_INVALID_ARG;
-  if (cfg->batch > 65535) return KVQ_ERR_UNSUPPORTED;              // a grid dimension
+  if (cfg->batch > 65535 || vocab > 1 << 30) return KVQ_ERR_UNSUPPORTED;   // a grid dimension; 32-bit token indices
   if (n_rows > 0) {
     if (!parent || !token || !p || !u || !path || p_stride < vocab || (q && q_stride < vocab))
       return KVQ_ERR_INVALID_ARG;

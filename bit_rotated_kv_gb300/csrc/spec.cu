@@ -12,12 +12,17 @@
 //
 // Every probability is an integer in units of 2^-60 (a float32 p >= 2^-36 is one exactly) and
 // every product floor(a b / 2^60), so sums are exact: the result does not depend on the order in
-// which 1024 threads and 8 CTAs add, and the same bits give the same token on every run.  Float64
-// would need neither but runs at a fortieth of the integer rate on this chip.
+// which 4096 threads add, and the same bits give the same token on every run.  Float64 would need
+// neither but runs at a fortieth of the integer rate on this chip.
 //
-// What bounds it: latency.  A row of 152 K target probabilities is 0.6 MB, read by one thread
-// block cluster (8 CTAs); rows that no decision needs are not read.
+// What bounds it: for one sequence, latency -- the sampler's decisions are a chain (8 nodes, 32,000 tokens:
+// 7.7 us).  For many, integer arithmetic: a row of 152 K target probabilities is 0.6 MB, read by one
+// cluster of CTAs, with the draft's row once more for every missed child (64 trees of 16 nodes: 81 us
+// for rows that HBM delivers in 11).  Rows that no decision needs are not read, and the sums of the last miss
+// are those that the draw needs.
 #include <cooperative_groups.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "launch.h"
@@ -33,13 +38,33 @@ constexpr unsigned long long kOne = 1ull << 60;
 
 typedef unsigned long long u64;
 
-// floor(a b / 2^60); a, b < 2^63, the product's quotient < 2^64
-__device__ __forceinline__ u64 mul60(u64 a, u64 b) {
-  return (__umul64hi(a, b) << 4) | ((a * b) >> 60);
-}
+// floor(a b / 2^60); a < 2^63, b < 2^61
+__device__ __forceinline__ u64 mul60(u64 a, u64 b) { return __umul64hi(a << 1, b << 3); }
 
-// p in [0, 1] in units of 2^-60 (the product is exact, the conversion drops what lies below)
-__device__ __forceinline__ u64 units(float p) { return __float2ull_rd(p * 0x1p60f); }
+// Probabilities: more than 1 counts as 1; negative values, infinities and NaN as 0, and `odd` is set.
+template <int N>
+__device__ __forceinline__ void clean(float (&p)[N], bool& odd) {
+  uint32_t top = 0u;
+#pragma unroll
+  for (int k = 0; k < N; ++k) top = max(top, __float_as_uint(p[k]));
+  if (top <= 0x7f7fffffu) return;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (__float_as_uint(p[k]) > 0x7f7fffffu) {
+      odd |= __float_as_uint(p[k]) != 0x80000000u;
+      p[k] = 0.f;
+    }
+}
+// ... in units of 2^-60: the 24-bit significand (1.0 is 2^23 << 37), what lies below a unit dropped.  (A 64-bit
+// float-to-integer conversion does the same, slower: 102 against 81 us for 64 trees over 152 K tokens.)
+__device__ __forceinline__ u64 units(float p) {
+  const uint32_t bits = min(__float_as_uint(p), 0x3f800000u);
+  return ((u64)((bits & 0x7fffffu) | 0x800000u) << 37) >> min(127u - (bits >> 23), 63u);
+}
+// ... of a random number: [0, 1)
+__device__ __forceinline__ u64 units_below_1(float u) {
+  return u >= 0.f ? units(fminf(u, 0x1.fffffep-1f)) : 0ull;
+}
 
 struct VerifyParams {
   const int32_t* cu_rows;
@@ -58,9 +83,13 @@ struct VerifyParams {
   int32_t* status;
 };
 
-constexpr int kVThreads = 1024;
+constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
-constexpr int kVCluster = 8;
+// CTAs per sequence.  Most sequences need one sum over their row, a few need one for every missed child, and
+// those are what the call waits for: 64 trees over 152 K tokens take 81 us with 16 x 256 threads to a
+// sequence, 89 us with 8 x 512.
+constexpr int kVCluster = 16;
+constexpr int kVChunk = 128;         // tokens a warp takes at once, 4 a lane
 
 struct VerifyShared {
   u64 sum[2][kVWarps];       // per-warp sums of a pass
@@ -85,8 +114,95 @@ __device__ __forceinline__ u64 warp_sum(u64 v) {
   return v;
 }
 
-__global__ void __cluster_dims__(kVCluster, 1, 1) __launch_bounds__(kVThreads)
-    verify_tree_kernel(const __grid_constant__ VerifyParams P) {
+// A node's row of probabilities less its missed children: with a draft distribution, Z q of each miss;
+// without, the missed tokens.
+struct Row {
+  const float* p;
+  const float* q;          // nullptr: not needed
+  int misses;              // 0: the row is p
+  bool wide;               // rows start on 16 bytes and are read 16 bytes a lane
+};
+
+// Four probabilities of a row from token v on (0 from v1 on).
+__device__ __forceinline__ float4 load4(const float* row, bool wide, int v, int v1) {
+  if (wide && v + 4 <= v1) return __ldg(reinterpret_cast<const float4*>(row + v));
+  return make_float4(v < v1 ? __ldg(row + v) : 0.f, v + 1 < v1 ? __ldg(row + v + 1) : 0.f,
+                     v + 2 < v1 ? __ldg(row + v + 2) : 0.f, v + 3 < v1 ? __ldg(row + v + 3) : 0.f);
+}
+
+// Remaining weights of N tokens from their probabilities, token(k) their ids.  The misses are the outer
+// loop: the N chains of products are independent.  Nothing is missed before the first miss, so its Z is 1.
+template <bool Q, int N, class Token>
+__device__ __forceinline__ void weights(const VerifyShared& S, int misses, float (&pv)[N], float (&qv)[N], Token token,
+                                        u64 (&r)[N], bool& odd) {
+  clean(pv, odd);
+#pragma unroll
+  for (int k = 0; k < N; ++k) r[k] = units(pv[k]);
+  if (misses == 0) return;
+  if (Q) {
+    u64 w[N];
+    clean(qv, odd);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      w[k] = units(qv[k]);
+      r[k] = r[k] > w[k] ? r[k] - w[k] : 0ull;
+    }
+#pragma unroll 1
+    for (int i = 1; i < misses; ++i) {
+      const u64 z = S.z[i];
+      if (z < kOne) {
+        const u64 z4 = z << 4;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const u64 t = __umul64hi(z4, w[k]);
+          r[k] = r[k] > t ? r[k] - t : 0ull;
+        }
+      } else {                                  // (a row that sums to more than 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const u64 t = mul60(z, w[k]);
+          r[k] = r[k] > t ? r[k] - t : 0ull;
+        }
+      }
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < misses; ++i) {
+      const int gone = S.gone[i];
+#pragma unroll
+      for (int k = 0; k < N; ++k) r[k] = gone == token(k) ? 0ull : r[k];
+    }
+  }
+}
+
+// This lane's part of the sum of a row's weights over tokens v0 .. v1 - 1, one warp's.  The next chunk
+// is on its way while one is summed.
+template <bool Q>
+__device__ __forceinline__ u64 sum_chunks(const VerifyShared& S, const Row& R, int v0, int v1, bool& odd) {
+  int v = v0 + 4 * (threadIdx.x & 31);
+  const int chunks = (v1 - v0 + kVChunk - 1) / kVChunk;
+  const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 p = load4(R.p, R.wide, v, v1), q = Q ? load4(R.q, R.wide, v, v1) : none;
+  u64 acc = 0ull;
+#pragma unroll 1
+  for (int i = 0; i < chunks; ++i, v += kVChunk) {
+    float pv[4] = {p.x, p.y, p.z, p.w}, qv[4] = {q.x, q.y, q.z, q.w};
+    p = load4(R.p, R.wide, v + kVChunk, v1);
+    if (Q) q = load4(R.q, R.wide, v + kVChunk, v1);
+    u64 w[4];
+    weights<Q>(S, R.misses, pv, qv, [&](int k) { return v + k; }, w, odd);
+    acc = add_capped(acc, (w[0] + w[1]) + (w[2] + w[3]));   // (4 + 4 at most)
+  }
+  return acc;
+}
+__device__ __noinline__ u64 sum_part(const VerifyShared& S, const Row R, int v0, int v1, bool& odd) {
+  bool bad = false;
+  const u64 acc = R.q && R.misses ? sum_chunks<true>(S, R, v0, v1, bad) : sum_chunks<false>(S, R, v0, v1, bad);
+  odd |= bad;
+  return acc;
+}
+
+__global__ void __launch_bounds__(kVThreads, 4) verify_tree_kernel(const __grid_constant__ VerifyParams P) {
   __shared__ VerifyShared S;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
@@ -100,7 +216,7 @@ __global__ void __cluster_dims__(kVCluster, 1, 1) __launch_bounds__(kVThreads)
   __syncthreads();
   // a sequence without rows, or rows that cannot be one tree, ends here (the same decision in
   // every CTA of the cluster)
-  bool bad = n < 0 || n > kNodes || first < 0 || first + n > P.n_rows;
+  bool bad = n < 0 || n > kNodes || first < 0 || first > P.n_rows - n;
   int par[kNodeWords];                         // parents of nodes lane, lane + 32, ...: one copy per warp
 #pragma unroll
   for (int w = 0; w < kNodeWords; ++w) {
@@ -128,7 +244,8 @@ __global__ void __cluster_dims__(kVCluster, 1, 1) __launch_bounds__(kVThreads)
   bad = bad || S.fault;
   if (bad || n == 0) {
     if (rank == 0) {
-      if (!bad || (n > 0 && first >= 0 && first + n <= P.n_rows))
+      if (!bad || (n > 0 && first >= 0 && first <= P.n_rows - n))
+#pragma unroll 1
         for (int j = tid; j < n; j += kVThreads) P.path[first + j] = -1;
       if (tid == 0) {
         if (bad) set_status(P.status, KVQ_ERR_BOUNDS);
@@ -139,61 +256,37 @@ __global__ void __cluster_dims__(kVCluster, 1, 1) __launch_bounds__(kVThreads)
     return;                                     // (uniform over the cluster: nothing waits for it)
   }
 
-  // probabilities outside [0, 1]: larger ones count as 1; negative ones and NaN as 0, reported
-  auto clean = [&](float v) {
-    if (!(v >= 0.f) || v == INFINITY) {
-      set_status(P.status, KVQ_ERR_NONFINITE);
-      return 0.f;
-    }
-    return fminf(v, 1.f);
-  };
-  auto clean_u = [&](float v) { return v >= 0.f ? fminf(v, 0x1.fffffep-1f) : 0.f; };
-
   // this warp's contiguous segment of the vocabulary
-  const int seg = ((P.vocab + kVCluster * kVWarps * 32 - 1) / (kVCluster * kVWarps * 32)) * 32;
+  const int per = kVCluster * kVWarps * kVChunk;
+  const int seg = ((P.vocab + per - 1) / per) * kVChunk;
   const int v0 = min(P.vocab, (rank * kVWarps + warp) * seg), v1 = min(P.vocab, v0 + seg);
+  const bool wide = ((reinterpret_cast<uintptr_t>(P.p) | reinterpret_cast<uintptr_t>(P.q)) & 15) == 0 &&
+                    ((P.p_stride | P.q_stride) & 3) == 0;
+  bool odd = false;                             // saw a value that is no probability
   int misses = 0;                               // misses of the current node
   bool whole = false;                           // their residual was empty: the weights are p again
   int cur = 0, depth = 1;
   int pass = 0;
+  u64 of_rank = 0ull;                           // the last pass's sum of CTA `lane`
 
-  // remaining weight of token v at the current node
-  auto weight = [&](int v, float pv, float qv) {
-    u64 r = units(clean(pv));
-    if (whole) return r;
-    if (P.q) {
-      const u64 Q = units(clean(qv));
-      for (int i = 0; i < misses; ++i) {
-        const u64 t = mul60(S.z[i], Q);
-        r = r > t ? r - t : 0ull;
-      }
-    } else {
-      for (int i = 0; i < misses; ++i)
-        if (S.gone[i] == v) r = 0ull;
-    }
-    return r;
+  auto row = [&]() {
+    return Row{P.p + (long long)(first + cur) * P.p_stride, P.q ? P.q + (long long)(first + cur) * P.q_stride : nullptr,
+               whole ? 0 : misses, wide};
   };
   // sum over the vocabulary of the remaining weights; S.sum keeps the warps' sums and S.total the
   // CTA's of the last pass (two sets: a pass writes one while others may still read the other)
   auto sum_weights = [&]() {
-    const float* pr = P.p + (long long)(first + cur) * P.p_stride;
-    const float* qr = P.q ? P.q + (long long)(first + cur) * P.q_stride : nullptr;
-    const bool need_q = qr && misses > 0 && !whole;
-    u64 acc = 0ull;
-#pragma unroll 4
-    for (int v = v0 + lane; v < v1; v += 32) acc = add_capped(acc, weight(v, pr[v], need_q ? qr[v] : 0.f));
-    acc = warp_sum(acc);
+    const u64 acc = warp_sum(sum_part(S, row(), v0, v1, odd));
     const int set = pass++ & 1;
     if (lane == 0) S.sum[set][warp] = acc;
     __syncthreads();
     if (warp == 0) {
-      const u64 t = warp_sum(S.sum[set][lane]);
+      const u64 t = warp_sum(lane < kVWarps ? S.sum[set][lane] : 0ull);
       if (lane == 0) S.total[set] = t;
     }
     cluster.sync();
-    u64 all = 0ull;
-    for (int r = 0; r < kVCluster; ++r) all = add_capped(all, *cluster.map_shared_rank(&S.total[set], r));
-    return all;
+    of_rank = lane < kVCluster ? *cluster.map_shared_rank(&S.total[set], lane) : 0ull;
+    return warp_sum(of_rank);
   };
 
   // nodes in index order; every warp of every CTA takes the same decisions
@@ -202,6 +295,7 @@ __global__ void __cluster_dims__(kVCluster, 1, 1) __launch_bounds__(kVThreads)
     P.next_token[b] = -1;                       // (until the draw below, a cluster barrier later)
   }
   u64 mass = kOne;
+#pragma unroll 1
   for (int c = 1; c < n; ++c) {
     // the next child of the current node
     int next = n;
@@ -215,9 +309,14 @@ __global__ void __cluster_dims__(kVCluster, 1, 1) __launch_bounds__(kVThreads)
     c = next;
     if (c >= n) break;
     const int x = S.token[c];
-    const u64 w = weight(x, S.pw[c], S.qw[c]);
-    const u64 want = P.q ? mul60(mass, units(clean(S.qw[c]))) : mass;
-    if (mul60(units(clean_u(S.u[c])), want) < w) {
+    u64 at[1];
+    float pw[1] = {S.pw[c]}, qw[1] = {S.qw[c]};
+    clean(qw, odd);
+    const u64 claim = units(qw[0]);             // (1 for point-mass drafts)
+    if (P.q) weights<true>(S, misses, pw, qw, [&](int) { return x; }, at, odd);
+    else weights<false>(S, misses, pw, qw, [&](int) { return x; }, at, odd);
+    const u64 w = at[0];
+    if (mul60(mul60(mass, claim), units_below_1(S.u[c])) < w) {
       if (rank == 0 && tid == 0) P.path[first + depth] = c;
       cur = c;
       ++depth;
@@ -239,53 +338,61 @@ __global__ void __cluster_dims__(kVCluster, 1, 1) __launch_bounds__(kVThreads)
     }
   }
   if (rank == 0)
+#pragma unroll 1
     for (int j = depth + tid; j < n; j += kVThreads) P.path[first + j] = -1;
 
-  // the token after the last taken node
-  u64 total = sum_weights();
+  // the token after the last taken node (a miss with a draft distribution has left its sums)
+  u64 total = P.q && misses > 0 && !whole ? mass : sum_weights();
   if (total == 0ull && !whole) {
     whole = true;
     total = sum_weights();
   }
   const int set = (pass - 1) & 1;
   if (rank == 0 && tid == 0) P.n_accept[b] = depth;
+  if (odd) set_status(P.status, KVQ_ERR_NONFINITE);
   if (total == 0ull || total >= kTooMuch) {
     if (rank == 0 && tid == 0) set_status(P.status, KVQ_ERR_NONFINITE);
   } else {
-    u64 goal = mul60(units(clean_u(S.u[0])), total);
-    for (int r = 0; r < rank; ++r) {
-      const u64 t = *cluster.map_shared_rank(&S.total[set], r);
-      goal = goal >= t ? goal - t : ~0ull;
-      if (goal == ~0ull) break;                 // an earlier CTA holds it
-    }
-    if (goal != ~0ull && goal < S.total[set]) {
-      int owner = -1;
-      for (int i = 0; i < kVWarps; ++i) {
-        if (goal < S.sum[set][i]) {
-          owner = i;
-          break;
-        }
-        goal -= S.sum[set][i];
-      }
-      if (warp == owner) {
-        const float* pr = P.p + (long long)(first + cur) * P.p_stride;
-        const float* qr = P.q ? P.q + (long long)(first + cur) * P.q_stride : nullptr;
-        const bool need_q = qr && misses > 0 && !whole;
-        for (int base = v0; base < v1; base += 32) {
-          const int v = base + lane;
-          u64 w = v < v1 ? weight(v, pr[v], need_q ? qr[v] : 0.f) : 0ull;
-          u64 upto = w;                         // inclusive sum over the lanes
+    // the CTA, its warp, the chunk, the lane and the token in which the sum passes the goal
+    u64 goal = mul60(total, units_below_1(S.u[0]));
+    auto narrow = [&](u64 mine) {               // lane whose sum passes it (goal: what is left there), or -1
+      u64 upto = mine;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const u64 t = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += t;
+      for (int o = 1; o < 32; o <<= 1) {
+        const u64 t = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += t;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, upto > goal);
+      if (hit) {
+        goal -= __shfl_sync(0xffffffffu, upto - mine, __ffs(hit) - 1);
+        return __ffs(hit) - 1;
+      }
+      goal -= __shfl_sync(0xffffffffu, upto, 31);
+      return -1;
+    };
+    if (narrow(of_rank) == rank && narrow(lane < kVWarps ? S.sum[set][lane] : 0ull) == warp) {
+      const Row R = row();
+      const bool need_q = R.q && R.misses;
+#pragma unroll 1
+      for (int v = v0 + 4 * lane; v - 4 * lane < v1; v += kVChunk) {
+        const float4 a = load4(R.p, wide, v, v1), c = need_q ? load4(R.q, wide, v, v1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float pv[4] = {a.x, a.y, a.z, a.w}, qv[4] = {c.x, c.y, c.z, c.w};
+        u64 w[4];
+        if (need_q) weights<true>(S, R.misses, pv, qv, [&](int k) { return v + k; }, w, odd);
+        else weights<false>(S, R.misses, pv, qv, [&](int k) { return v + k; }, w, odd);
+        const int at = narrow((w[0] + w[1]) + (w[2] + w[3]));
+        if (at >= 0) {
+          if (lane == at) {
+            int k = 0;
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+              if (k == i && goal >= w[i]) {
+                goal -= w[i];
+                ++k;
+              }
+            P.next_token[b] = v + k;
           }
-          const unsigned hit = __ballot_sync(0xffffffffu, upto > goal);
-          if (hit) {
-            if (lane == 0) P.next_token[b] = base + __ffs(hit) - 1;
-            break;
-          }
-          goal -= __shfl_sync(0xffffffffu, upto, 31);
+          break;
         }
       }
     }
@@ -323,7 +430,7 @@ __global__ void __launch_bounds__(kCThreads) tree_commit_kernel(const __grid_con
   const int n = P.cu_rows[b + 1] - first;
   const int len = P.seq_len[b], edge = P.s_quant[b], keep = P.n_accept[b];
   const int L0 = len - n;
-  int bad = n < 0 || n > kNodes || first < 0 || first + n > P.n_rows || keep < 0 || keep > n || L0 < 0 ||
+  int bad = n < 0 || n > kNodes || first < 0 || first > P.n_rows - n || keep < 0 || keep > n || L0 < 0 ||
             edge > max(L0, P.s_sink);
   if (!bad && tid < keep) {
     const int at = P.path[first + tid], before = tid ? P.path[first + tid - 1] : -1;
@@ -382,7 +489,17 @@ extern "C" int kvq_launch_verify_tree(const kvq_config* cfg, const int32_t* cu_r
   P.n_accept = n_accept;
   P.next_token = next_token;
   P.status = d_status;
-  return launch_pdl(verify_tree_kernel, dim3(kVCluster, cfg->batch), dim3(kVThreads), 0, stream, P) == cudaSuccess
+  // clusters of more than 8 CTAs, once per device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ERR_CUDA;
+  static std::atomic<unsigned long long> allowed{0};
+  if (!(allowed.load() & (1ull << dev))) {
+    if (cudaFuncSetAttribute((const void*)verify_tree_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return KVQ_ERR_CUDA;
+    allowed.fetch_or(1ull << dev);
+  }
+  return launch_pdl_cluster(verify_tree_kernel, kVCluster, dim3(kVCluster, cfg->batch), dim3(kVThreads), 0, stream, P) ==
+                 cudaSuccess
              ? KVQ_OK
              : KVQ_ERR_CUDA;
 }
