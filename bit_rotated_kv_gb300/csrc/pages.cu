@@ -241,27 +241,37 @@ __global__ void __cluster_dims__(kPCluster, 1, 1) __launch_bounds__(kPThreads)
     P.ref[id] = 1;
   });
   cluster.sync();                              // (counts of free pages are taken before references change)
-  for (int i = 0; i < P.n; ++i) {
-    const int full = shared_pages[i];
-    if (full < 0) continue;
-    if (end[i] > free_pages) {                 // the pool ran out: this pair and the later ones stay unforked
-      if (rank == 0 && tid == 0) set_status(P.status, KVQ_ERR_BOUNDS);
-      continue;
-    }
-    const int src = P.a[i], dst = P.b[i];
-    for (int c = rank * kPThreads + tid; c < full; c += kPCluster * kPThreads) {
-      const int id = P.table[(size_t)src * P.max_pages + c];
-      if ((unsigned)id < (unsigned)P.num_pages) {
-        atomicAdd(P.ref + id, 1);
-        P.table[(size_t)dst * P.max_pages + c] = id;
-      } else {
-        set_status(P.status, KVQ_ERR_BOUNDS);
-      }
-    }
-    if (rank == 0 && tid == 0) {
+  // pairs that the pool could serve (from the first one on that it could not, none is) take their shares:
+  // a warp takes 128 entries of a pair at once
+  for (int i = rank * kPThreads + tid; i < P.n; i += kPCluster * kPThreads) {
+    if (shared_pages[i] < 0) continue;
+    if (end[i] > free_pages) {
+      set_status(P.status, KVQ_ERR_BOUNDS);
+    } else {
+      const int src = P.a[i], dst = P.b[i];
       P.seq_len[dst] = P.seq_len[src];
       P.s_quant[dst] = P.s_quant[src];
       P.counters[dst] = P.parts;               // the copying CTAs count it back to zero
+    }
+  }
+  const int lane = tid & 31, per_pair = (P.max_pages + 127) / 128;
+  for (long long k = rank * kPWarps + (tid >> 5); k < (long long)P.n * per_pair; k += kPCluster * kPWarps) {
+    const int i = (int)(k / per_pair), c0 = (int)(k % per_pair) * 128 + lane, full = shared_pages[i];
+    if (c0 - lane >= full || end[i] > free_pages) continue;
+    const int32_t* from = P.table + (size_t)P.a[i] * P.max_pages;
+    int32_t* to = P.table + (size_t)P.b[i] * P.max_pages;
+    int id[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) id[x] = c0 + 32 * x < full ? from[c0 + 32 * x] : 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (c0 + 32 * x >= full) continue;
+      if ((unsigned)id[x] < (unsigned)P.num_pages) {
+        atomicAdd(P.ref + id[x], 1);
+        to[c0 + 32 * x] = id[x];
+      } else {
+        set_status(P.status, KVQ_ERR_BOUNDS);
+      }
     }
   }
   cluster.sync();
@@ -269,6 +279,7 @@ __global__ void __cluster_dims__(kPCluster, 1, 1) __launch_bounds__(kPThreads)
 
 constexpr int kCopyThreads = 256;
 constexpr int kRowParts = 4;         // CTAs per (pair, kv head)
+constexpr int kRowBatch = 8;         // rows a thread has in flight
 
 __global__ void __launch_bounds__(kCopyThreads) seq_fork_rows_kernel(const __grid_constant__ PageParams P) {
   const int i = blockIdx.y, h = blockIdx.x / kRowParts, part = blockIdx.x % kRowParts;
@@ -284,19 +295,28 @@ __global__ void __launch_bounds__(kCopyThreads) seq_fork_rows_kernel(const __gri
   const int n_sink = min(P.s_sink, len), first = max(edge, P.s_sink), n_ring = min(max(0, len - first), P.ring_cap);
   constexpr int kLanes = kHeadDim * 2 / 16;
   const int sub = tid % kLanes;
-  for (int side = 0; side < 2; ++side) {
-    uint16_t* sink = side ? P.sink_v : P.sink_k;
-    uint16_t* ring = side ? P.ring_v : P.ring_k;
-    const size_t hs = ((size_t)src * P.hkv + h), hd = ((size_t)dst * P.hkv + h);
-#pragma unroll 4
-    for (int r = part * (kCopyThreads / kLanes) + tid / kLanes; r < n_sink + n_ring; r += kRowParts * (kCopyThreads / kLanes)) {
-      const bool in_sink = r < n_sink;
-      const size_t slot = in_sink ? r : (size_t)((first + r - n_sink) % P.ring_cap);
-      uint16_t* base = in_sink ? sink : ring;
-      const size_t rows = in_sink ? P.s_sink : P.ring_cap;
-      reinterpret_cast<uint4*>(base + (hd * rows + slot) * kHeadDim)[sub] =
-          reinterpret_cast<const uint4*>(base + (hs * rows + slot) * kHeadDim)[sub];
+  const int rows = n_sink + n_ring;
+  const size_t hs = (size_t)src * P.hkv + h, hd = (size_t)dst * P.hkv + h;
+  constexpr int kStep = kRowParts * (kCopyThreads / kLanes);
+  for (int r0 = part * (kCopyThreads / kLanes) + tid / kLanes; r0 < 2 * rows; r0 += kRowBatch * kStep) {
+    uint4 v[kRowBatch];
+    uint4* to[kRowBatch];
+#pragma unroll
+    for (int k = 0; k < kRowBatch; ++k) {
+      const int both = r0 + k * kStep, side = both >= rows, r = both - (side ? rows : 0);
+      to[k] = nullptr;
+      if (both < 2 * rows) {
+        const bool in_sink = r < n_sink;
+        const size_t slot = in_sink ? r : (size_t)((first + r - n_sink) % P.ring_cap);
+        uint16_t* base = in_sink ? (side ? P.sink_v : P.sink_k) : (side ? P.ring_v : P.ring_k);
+        const size_t cap = in_sink ? P.s_sink : P.ring_cap;
+        v[k] = reinterpret_cast<const uint4*>(base + (hs * cap + slot) * kHeadDim)[sub];
+        to[k] = reinterpret_cast<uint4*>(base + (hd * cap + slot) * kHeadDim) + sub;
+      }
     }
+#pragma unroll
+    for (int k = 0; k < kRowBatch; ++k)
+      if (to[k]) *to[k] = v[k];
   }
   // the half-filled page
   const int tokens = max(0, edge - P.s_sink);
