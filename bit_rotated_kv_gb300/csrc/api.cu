@@ -195,6 +195,7 @@ KVQ_API int kv_attn_chunk(const kvq_config* cfg, const kvq_cache* cache, const u
 
 KVQ_API size_t kv_attn_tree_workspace_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
   if (check_config(cfg) != KVQ_OK || max_ctx < 0 || n_rows < 0 || n_rows > 65535) return 0;
+  if (n_rows > (long long)cfg->batch * KVQ_TREE_MAX_NODES) return 0;
   return kvq_attn_tree_ws_bytes(cfg, n_rows, max_ctx);
 }
 
@@ -207,6 +208,7 @@ KVQ_API int kv_attn_tree(const kvq_config* cfg, const kvq_cache* cache, const ui
   if (rc) return rc;
   if (n_rows < 0 || max_ctx < 0 || !cu_rows || !aligned(cu_rows, 4)) return KVQ_ERR_INVALID_ARG;
   if (n_rows > 65535) return KVQ_ERR_UNSUPPORTED;
+  if (n_rows > (long long)cfg->batch * KVQ_TREE_MAX_NODES) return KVQ_ERR_INVALID_ARG;
   if (n_rows == 0) return KVQ_OK;
   if (!parent || !aligned(parent, 4)) return KVQ_ERR_INVALID_ARG;
   if (!q_rot || !out || !aligned(q_rot, 16) || !aligned(out, 16)) return KVQ_ERR_INVALID_ARG;

@@ -1075,7 +1075,7 @@ __device__ void window_split(const AttnParams& P, int b, int bc, int node0, int 
     }
     // ---- P V: P = P_hi + P_lo in bf16, two MMAs per 16 channels
     uint32_t bh[2], bl[2];
-    {
+    auto pack_p = [&]() {
       uint32_t h0 = pack_bf162(p[0], p[1]);
       uint32_t h1 = pack_bf162(p[2], p[3]);
       float2 f0 = unpack_bf162(h0), f1 = unpack_bf162(h1);
@@ -1083,7 +1083,8 @@ __device__ void window_split(const AttnParams& P, int b, int bc, int node0, int 
       uint32_t l1 = pack_bf162(p[2] - f1.x, p[3] - f1.y);
       bh[0] = movmatrix_trans(h0); bh[1] = movmatrix_trans(h1);
       bl[0] = movmatrix_trans(l0); bl[1] = movmatrix_trans(l1);
-    }
+    };
+    pack_p();
     // V rows 2q, 2q+1, 2q+8, 2q+9, channels 16*(lane/4) .. +16
     uint32_t vr[4][8];
     const int vt[4] = {2 * quad, 2 * quad + 1, 2 * quad + 8, 2 * quad + 9};
@@ -1094,6 +1095,33 @@ __device__ void window_split(const AttnParams& P, int b, int bc, int node0, int 
       const bool ok = row_ok(vt[i]);
       vr[i][0] = ok ? x.x : 0u; vr[i][1] = ok ? x.y : 0u; vr[i][2] = ok ? x.z : 0u; vr[i][3] = ok ? x.w : 0u;
       vr[i][4] = ok ? y.x : 0u; vr[i][5] = ok ? y.y : 0u; vr[i][6] = ok ? y.z : 0u; vr[i][7] = ok ? y.w : 0u;
+    }
+    if constexpr (TREE) {
+      // a draft whose value row is not finite makes the columns that see it NaN, and (0 x NaN) only those
+      if (hi > tree.L0) {
+        unsigned odd[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          bool inf = false;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) inf |= bf16_pair_odd(vr[i][k]);
+          odd[i] = __ballot_sync(0xffffffffu, inf && tok0 + vt[i] >= tree.L0);
+        }
+        if (odd[0] | odd[1] | odd[2] | odd[3]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (odd[i] & (0x11111111u << quad))
+#pragma unroll
+              for (int k = 0; k < 8; ++k) vr[i][k] = 0u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {         // p[i]: token tA or tB, column 2 quad + i % 2
+            const int t = i < 2 ? tA : tB;
+            const unsigned at = (t & 1 ? (i < 2 ? odd[1] : odd[3]) : (i < 2 ? odd[0] : odd[2])) & (0x11111111u << ((t & 7) >> 1));
+            if (at && col_ok(t, i & 1)) p[i] = __int_as_float(0x7fffffff);
+          }
+          pack_p();
+        }
+      }
     }
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) {
@@ -1412,7 +1440,7 @@ extern "C" size_t kvq_attn_ws_bytes(const kvq_config* cfg, int32_t max_ctx) {
 static int launch_attn_impl(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot, void* out,
                             int out_bf16, float sm_scale, int32_t max_ctx, void* ws, int32_t* d_status,
                             cudaStream_t stream, const int32_t* cu_rows, int seqs,
-                            const int32_t* parent = nullptr, int heads = 1, int n_rows = 0) {
+                            const int32_t* parent = nullptr, int heads = 1, int n_rows = 0, size_t counter_bytes = 0) {
   AttnParams P{};
   P.parent = parent;
   P.heads = heads;
@@ -1450,7 +1478,7 @@ static int launch_attn_impl(const kvq_config* cfg, const kvq_cache* cache, const
   P.scale_log2 = sm_scale * 1.4426950408889634f;
   const size_t units = (size_t)cfg->batch * cfg->n_kv_heads;
   P.count = (int32_t*)ws;
-  P.part = (float*)((char*)ws + kvq_attn_counter_bytes(cfg, max_ctx));
+  P.part = (float*)((char*)ws + (counter_bytes ? counter_bytes : kvq_attn_counter_bytes(cfg, max_ctx)));
   P.part2 = P.part + units * (size_t)P.n_split * P.gqa * kRow;
   const int ng = kHeadDim / cfg->group_size;
   const size_t ring_bytes = (size_t)kWarps * kStages * P.page_bytes;
@@ -1537,9 +1565,21 @@ static kvq_config tree_config(const kvq_config* cfg, int32_t n_rows) {
   return c;
 }
 
+// Head of a kv_attn_tree workspace: room for the tickets of any call of this config, whatever its n_rows and
+// max_ctx, and nothing else, so that one workspace serves calls of different sizes (trees grow and shrink
+// from step to step, and the other kernel has no tickets).  Tickets are units x (groups of splits + 1); at
+// most 2 x 152 splits fall to all units together, unless the config asks for more.
+extern "C" size_t kvq_attn_tree_head_bytes(const kvq_config* cfg) {
+  const size_t units = min(65535ull, (unsigned long long)cfg->batch * KVQ_TREE_MAX_NODES) * (size_t)cfg->n_kv_heads;
+  const size_t wtiles = (size_t)(cfg->s_sink + kPage - 1) / kPage + (cfg->s_keep + cfg->s_flush + kPage - 1) / kPage + 1;
+  const size_t splits = cfg->attn_splits > 0 ? cfg->attn_splits + wtiles : 1;
+  const size_t tickets = units * ((splits + kGroup - 1) / kGroup + 2) + kCtasPerSm * kSms;
+  return (tickets * 4 + 255) / 256 * 256;
+}
+
 extern "C" size_t kvq_attn_tree_rows_ws_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
   const kvq_config c = tree_config(cfg, n_rows);
-  return kvq_attn_ws_bytes(&c, max_ctx);
+  return kvq_attn_tree_head_bytes(cfg) + kvq_attn_ws_bytes(&c, max_ctx) - kvq_attn_counter_bytes(&c, max_ctx);
 }
 
 extern "C" int kvq_launch_attn_tree_rows(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot,
@@ -1548,7 +1588,7 @@ extern "C" int kvq_launch_attn_tree_rows(const kvq_config* cfg, const kvq_cache*
                                          cudaStream_t stream) {
   const kvq_config c = tree_config(cfg, n_rows);
   return launch_attn_impl(&c, cache, q_rot, out, 1, sm_scale, max_ctx, ws, d_status, stream, cu_rows, cfg->batch,
-                          parent, cfg->n_q_heads / cfg->n_kv_heads, n_rows);
+                          parent, cfg->n_q_heads / cfg->n_kv_heads, n_rows, kvq_attn_tree_head_bytes(cfg));
 }
 
 // ---- allocation-free variant ---------------------------------------------------------------

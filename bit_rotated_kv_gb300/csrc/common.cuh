@@ -149,6 +149,11 @@ __device__ __forceinline__ void prefetch_l2_line(const void* src) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(src) : "memory");
 }
 
+// Whether one of two bf16 is infinite or NaN.
+__device__ __forceinline__ bool bf16_pair_odd(uint32_t v) {
+  return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
+}
+
 template <typename... Args>
 inline cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                               Args... args) {

@@ -301,6 +301,7 @@ struct TreeShared {
   __align__(16) float neg_m[N];    // minus the reference of every row
   __align__(16) float alpha[N];    // a moved reference: factor of what is summed so far
   float red[4][N];                 // per-quadrant maxima; at the end parts of the sums
+  uint8_t v_odd[2][kTile];         // window tiles with drafts: whether a token's value row is not finite
   int moves[2];                    // the last tile (+ 1) in which a half's references have to move
   __align__(16) uint32_t seen[kNodes][kNodeWords];   // ancestors of every node, itself among them
   int jump[kNodes];                // (while they are found: the next one)
@@ -618,6 +619,20 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
                      w0 + r < n_win ? 16 : 0);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!keys && (n_sink > st.L0 || w0 + kTile > n_win - st.n)) {
+        // drafts: a value row that is not finite is taken out here (0 x NaN would reach rows that do not see
+        // it) and the softmax makes the rows that see it NaN
+#pragma unroll 1
+        for (int r = t >> 4; r < kTile; r += 2 * kValWarps) {
+          uint4* at = reinterpret_cast<uint4*>(dst + (j >> 3) * kSlab + (r >> 3) * 1024 + (r & 7) * 128 + (((j & 7) ^ (r & 7)) << 4));
+          const uint4 v = *at;
+          const int tok = w0 + r < n_sink ? w0 + r : ring0 + w0 + r - n_sink;
+          const bool inf = tok >= st.L0 && (bf16_pair_odd(v.x) || bf16_pair_odd(v.y) || bf16_pair_odd(v.z) || bf16_pair_odd(v.w));
+          const bool any = (__ballot_sync(0xffffffffu, inf) >> (lane & 16)) & 0xffffu;
+          if (any) *at = make_uint4(0u, 0u, 0u, 0u);
+          if (j == 0) S.v_odd[i & 1][r] = any;
+        }
+      }
       if (keys) {
         S.lane_scale[i & 3][t] = 1.f;
         const unsigned alive = __ballot_sync(0xffffffffu, w0 + t < n_win);
@@ -926,14 +941,17 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       fence_after();
       const uint32_t ts = tq + kColS + N * (i & 1);
       const bool win = i < nwc;
-      const float ls = S.lane_scale[i & 3][tok] * (win ? P.scale_log2 : page_scale);
+      float ls = S.lane_scale[i & 3][tok] * (win ? P.scale_log2 : page_scale);
       const uint32_t alive = *reinterpret_cast<const uint32_t*>(&S.alive[i & 3][2 * q]);
       // window tiles that reach into the drafts: else every row sees every token
       const bool drafts = win && (n_sink > st.L0 || (t0 + i + 1) * kTile > n_win - st.n);
       const bool masked = drafts || alive != 0xffffffffu;
       uint32_t see = 0xffffffffu;                           // rows that see this token
       if (masked) {
-        if (drafts && !warp_wait(&S.seen_full, 0, gave_up)) lost = true;
+        if (drafts) {
+          if (!warp_wait(&S.seen_full, 0, gave_up) || !warp_wait(&S.v_full[i & 1], i >> 1, gave_up)) lost = true;
+          if (S.v_odd[i & 1][tok]) ls = __int_as_float(0x7fffffff);   // (see where the values are loaded)
+        }
         const int w = (t0 + i) * kTile + tok;
         const int node = win ? (w < n_sink ? w : ring0 + w - n_sink) - st.L0 : -1;
         see = (alive >> lane) & 1u ? 0xffffffffu : 0u;
@@ -1229,7 +1247,8 @@ static bool row_kernel(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
 extern "C" size_t kvq_attn_tree_ws_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
   if (row_kernel(cfg, n_rows, max_ctx)) return kvq_attn_tree_rows_ws_bytes(cfg, n_rows, max_ctx);
   const Shape s = tree_shape(cfg, n_rows, max_ctx);
-  return s.splits > 1 ? (size_t)n_rows * cfg->n_q_heads * s.splits * kRec * sizeof(float) : 256;
+  return kvq_attn_tree_head_bytes(cfg) +
+         (s.splits > 1 ? (size_t)n_rows * cfg->n_q_heads * s.splits * kRec * sizeof(float) : 0);
 }
 
 extern "C" int kvq_launch_attn_tree(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot,
@@ -1252,7 +1271,7 @@ extern "C" int kvq_launch_attn_tree(const kvq_config* cfg, const kvq_cache* cach
   P.cu_rows = cu_rows;
   P.parent = parent;
   P.out = out;
-  P.part = (float*)ws;
+  P.part = (float*)((char*)ws + kvq_attn_tree_head_bytes(cfg));    // (behind the row kernel's tickets)
   P.status = d_status;
   P.batch = cfg->batch;
   P.hkv = cfg->n_kv_heads;

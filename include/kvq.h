@@ -336,10 +336,18 @@ KVQ_API int kv_attn_chunk(const kvq_config* cfg, const kvq_cache* cache, const u
  * (token L0 + j for node j) and to itself, as the cache holds them.  A chain (parent i - 1) gives
  * kv_attn_chunk's result; several roots are allowed.  max_ctx, sm_scale as for kv_attn_decode
  * (max_ctx counts the nodes); workspace of kv_attn_tree_workspace_bytes(cfg, n_rows, max_ctx)
- * bytes, zero-filled before its first use (every call leaves its counters zero).  n_rows is at
- * most 65535 (KVQ_ERR_UNSUPPORTED beyond).  KVQ_ERR_BOUNDS in *d_status, and zeros for the rows of
- * a sequence whose nodes are more than KVQ_TREE_MAX_NODES or do not all lie in the BF16 windows; a
- * node whose ancestors are not in index order is reported and sees those up to the fault.
+ * bytes, zero-filled before its first use (every call leaves its counters zero).  One workspace
+ * of the largest size serves calls of any n_rows and max_ctx with the same config, one after another;
+ * calls that may run at the same time need one each.  n_rows is at most 65535 (KVQ_ERR_UNSUPPORTED beyond)
+ * and batch * KVQ_TREE_MAX_NODES (KVQ_ERR_INVALID_ARG).  KVQ_ERR_BOUNDS in *d_status, and zeros for
+ * the rows of a sequence whose nodes are more than KVQ_TREE_MAX_NODES or do not all lie in the BF16
+ * windows; a node whose ancestors are not in index order is reported and sees those up to the fault.
+ * Rows behind the last sequence are not written (KVQ_ERR_BOUNDS when cu_rows does not cover n_rows).  A
+ * draft whose K or V is not finite changes the rows of the nodes that see it, and only those.
+ * Execution: trees of up to about 32 columns (nodes x query heads per kv head), and small calls, run the
+ * decode kernel with eight columns to a grid row; wider ones a tensor-core kernel that reads a
+ * sequence's cache once for every 64 columns.  The two round differently (both within the attention's
+ * error); which one runs follows from cfg, n_rows and max_ctx alone.
  * Source: [OSCAR] section 4 "Decoding Attention Kernel" (attention over the mixed cache);
  * the tree of drafts has no counterpart on the pages. */
 KVQ_API size_t kv_attn_tree_workspace_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx);

@@ -98,6 +98,17 @@ CASES = {
     "quest": (BASE.replace(batch=1, ctx_lo=900, ctx_hi=900, quantizer="quest"), [12], "random"),
     "per_channel_keys": (synth.QWEN3_32B_128K.replace(batch=2, ctx_lo=500, ctx_hi=900, key_axis="channel"), [6, 14], "random"),
     "per_channel_plain": (BASE.replace(batch=1, ctx_lo=600, ctx_hi=600, key_axis="channel", s_flush=16, kappa_k=1.0), [21], "random"),
+    # the same edges with trees wide enough for the tensor-core kernel
+    "wide_short_contexts": (BASE.replace(batch=4, ctx_lo=0, ctx_hi=70), [40, 90, 128, 33], "random"),
+    "wide_empty_contexts": (BASE.replace(batch=4, ctx_lo=0, ctx_hi=0), [17, 64, 128, 1], "random"),
+    "wide_g32_l2": (synth.QWEN3_32B_128K.replace(batch=2, ctx_lo=500, ctx_hi=1500), [64, 100], "random"),
+    "wide_g32_gqa1": (BASE.replace(batch=2, n_q_heads=8, ctx_lo=600, ctx_hi=700, group_size=32), [128, 101], "random"),
+    "wide_g64_l2": (synth.QWEN3_32B_128K.replace(batch=2, ctx_lo=1030, ctx_hi=1030, group_size=64), [70, 40], "random"),
+    "wide_g128_l2": (synth.QWEN3_32B_128K.replace(batch=2, ctx_lo=1030, ctx_hi=1030, group_size=128), [70, 40], "random"),
+    "wide_flush1": (BASE.replace(batch=3, ctx_lo=340, ctx_hi=420, s_flush=1), [50, 40, 17], "random"),
+    "wide_odd_sink": (BASE.replace(batch=2, ctx_lo=500, ctx_hi=600, s_sink=5, s_keep=48), [50, 31], "random"),
+    "wide_quest": (BASE.replace(batch=2, ctx_lo=900, ctx_hi=900, quantizer="quest"), [42, 43], "random"),
+    "wide_gqa2": (BASE.replace(batch=3, n_q_heads=16, ctx_lo=900, ctx_hi=1200), [60, 70, 80], "random"),
     "mid_context": (BASE.replace(batch=1, n_q_heads=8, n_kv_heads=2, ctx_lo=9000, ctx_hi=9000), [48], "random"),
 }
 
@@ -156,6 +167,55 @@ def test_captured_and_replayed_on_another_stream():
         torch.cuda.synchronize()
         assert torch.equal(out.view(torch.int16), first.view(torch.int16))
     assert int(r.status.item()) == 0
+
+
+@pytest.mark.parametrize("counts", [[6], [16, 20, 16, 30]], ids=["narrow", "wide"])
+@pytest.mark.parametrize("side", ["k", "v"])
+def test_a_draft_that_is_not_finite_reaches_the_nodes_that_see_it_only(counts, side):
+    w = BASE.replace(batch=len(counts), ctx_lo=500, ctx_hi=700)
+    run, q, cu, parent = _drafted(w, counts, "random", seed=5)
+    r, cap = run.runner, run.cfg.ring_cap
+    bad = 3                                          # node 3 of every sequence: one channel of one kv head
+    ring = r.cache.ring_k if side == "k" else r.cache.ring_v
+    before = ring.clone()
+    for b, n in enumerate(counts):
+        slot = (int(r.cache.seq_len[b]) - n + bad) % cap
+        ring[b, 0, slot, 77] = float("inf") if b % 2 else float("nan")
+    out = _call(run, q, cu, parent)
+    assert int(r.status.item()) == 0
+    ring.copy_(before)
+    clean = _call(run, q, cu, parent)
+    g = run.w.gqa
+    for b, n in enumerate(counts):
+        par = parent[int(cu[b]):int(cu[b + 1])]
+        for i in range(n):
+            at, sees = i, False
+            while at >= 0:
+                sees |= at == bad
+                at = int(par[at])
+            o, c = out[int(cu[b]) + i], clean[int(cu[b]) + i]
+            assert torch.equal(o[g:], c[g:])         # the other kv heads
+            if sees:
+                # (an infinite key against a negative query is a score of -inf: the token has no weight)
+                none = (q[int(cu[b]) + i, :g, 77] < 0) if side == "k" and b % 2 else torch.zeros(g, dtype=torch.bool, device="cuda")
+                assert torch.equal(torch.isfinite(o[:g]), none[:, None].expand(g, 128))
+            else:                                    # within both results' error
+                tol = c[:g].float().abs() * 2.0 ** -7 + 2 * ATTN_TOL * c[:g].float().abs().amax(-1, keepdim=True)
+                assert ((o[:g].float() - c[:g].float()).abs() <= tol).all()
+
+
+def test_one_workspace_serves_trees_of_any_size():
+    """Calls of both kernels and of many sizes in turn: the tickets of each are as it needs them."""
+    import bit_rotated_kv_gb300 as kvq
+    runs = [_drafted(BASE.replace(batch=2, ctx_lo=ctx, ctx_hi=ctx + 300), counts, "random")
+            for ctx, counts in ((500, [64, 30]), (500, [3, 2]), (3000, [1, 1]), (500, [40, 128]), (3000, [9, 9]), (900, [2, 5]))]
+    sizes = [kvq.kv_attn_tree_workspace_bytes(r[0].cfg, r[1].shape[0], int(r[0].runner.cache.seq_len.max())) for r in runs]
+    ws = torch.zeros(max(sizes), dtype=torch.uint8, device="cuda")
+    own = [_call(*r) for r in runs]
+    for _ in range(2):
+        for r, want in zip(runs, own):
+            assert torch.equal(_call(*r, ws=ws).view(torch.int16), want.view(torch.int16))
+            assert int(r[0].runner.status.item()) == 0
 
 
 def test_rows_behind_the_last_sequence_are_left():
