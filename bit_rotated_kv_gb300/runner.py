@@ -1,5 +1,7 @@
-"""Drive the C-ABI calls for a batch of sequences: chunked prefill of the cache and one
-serving step (append n_new tokens, flush, decode -- or the fused append, then decode).  Argument marshalling only --
+"""Drive the C-ABI calls for a batch of sequences: chunked prefill of the cache, one serving
+step (append n_new tokens, flush, decode -- or the fused append, then decode), one speculative step
+(a tree of drafts appended and attended to, checked, the kept path's rows left in the cache), and
+the page pool behind them (reserve, fork, free, compact).  Argument marshalling only --
 torch is used for device buffers, gathers of input rows and streams; every step of the
 method runs in the library's kernels."""
 
@@ -11,7 +13,9 @@ import numpy as np
 import torch
 
 from . import (KVCache, KVConfig, Transform, kv_append_chunk, kv_attn_chunk, kv_attn_chunk_workspace_bytes,
-               kv_attn_decode, kv_quant_flush, kv_rotate_qk, workspace)
+               kv_attn_decode, kv_attn_tree, kv_attn_tree_workspace_bytes, kv_pages_compact,
+               kv_pages_compact_workspace_bytes, kv_pages_reserve, kv_quant_flush, kv_rotate_qk, kv_seq_fork, kv_seq_free,
+               kv_tree_commit, kv_verify_tree, workspace)
 
 
 def _rows_for(k_all: torch.Tensor, lengths_lo, lengths_hi):
@@ -51,9 +55,15 @@ class DecodeRunner:
         self.out = torch.empty((cfg.batch, cfg.n_q_heads, cfg.head_dim), dtype=torch.float32,
                                device=self.device)
         self.sm_scale = 1.0 / math.sqrt(cfg.head_dim)
+        # the page pool: how many table entries hold each page (set_page_table counts them)
+        self.page_ref = torch.zeros(cfg.num_pages, dtype=torch.int32, device=self.device)
+        self.n_live = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     def set_page_table(self, table: np.ndarray) -> None:
-        self.cache.page_table.copy_(torch.from_numpy(np.ascontiguousarray(table, np.int32)))
+        table = np.ascontiguousarray(table, np.int32)
+        self.cache.page_table.copy_(torch.from_numpy(table))
+        held = table[(table >= 0) & (table < self.cfg.num_pages)]
+        self.page_ref.copy_(torch.from_numpy(np.bincount(held, minlength=self.cfg.num_pages).astype(np.int32)))
 
     def append(self, k_rows, v_rows, seq_idx, pos, q=None, q_out=None, stream=None) -> None:
         kv_rotate_qk(self.cfg, self.tr, q, q_out, k_rows, v_rows, seq_idx, pos, self.cache, self.status,
@@ -119,3 +129,50 @@ class DecodeRunner:
         self.append(k_rows, v_rows, seq_idx, pos, q, self.q_out, stream)
         self.flush(n_new + self.cfg.s_flush, stream)
         self.decode(self.q_out, self.out, stream)
+
+    # ---- speculative decoding: tree_step, then accept --------------------------------------------
+    def tree_workspace(self, n_rows: int) -> torch.Tensor:
+        """A zeroed workspace for trees of up to n_rows nodes in all."""
+        n = max(kv_attn_tree_workspace_bytes(self.cfg, r, self.max_ctx) for r in range(1, max(1, n_rows) + 1))
+        return torch.zeros(max(n, 256), dtype=torch.uint8, device=self.device)
+
+    def tree_step(self, q, k_rows, v_rows, seq_idx, pos, cu_rows, parent, q_out, out, ws, stream=None) -> None:
+        """Append the drafted nodes (row cu_rows[b] + i is node i of sequence b, at position length + i)
+        and attend from each to the tokens before the drafts, its ancestors and itself: out [n, Hq, d] bf16."""
+        self.append(k_rows, v_rows, seq_idx, pos, q, q_out, stream)
+        kv_attn_tree(self.cfg, self.cache, q_out, cu_rows, parent, out, self.sm_scale, self.max_ctx, ws, self.status,
+                     self.stream if stream is None else stream)
+
+    def accept(self, cu_rows, parent, token, p, q, u, path, n_accept, next_token, max_nodes: int, stream=None) -> None:
+        """Check the drafts against the target's probabilities p (q: the draft's, or None), keep the rows of
+        the path that holds, drop the others, and flush."""
+        stream = self.stream if stream is None else stream
+        kv_verify_tree(self.cfg, cu_rows, parent, token, p, q, u, path, n_accept, next_token, self.status, stream)
+        self.commit(cu_rows, path, n_accept, max_nodes, stream)
+
+    def commit(self, cu_rows, path, n_accept, max_nodes: int, stream=None) -> None:
+        """Keep the rows of the given paths only (every layer's cache takes the same ones), and flush."""
+        kv_tree_commit(self.cfg, self.cache, cu_rows, path, n_accept, self.status, self.stream if stream is None else stream)
+        self.flush(max_nodes + self.cfg.s_flush, stream)
+
+    # ---- the page pool -----------------------------------------------------------------------------
+    def reserve(self, n_tokens, stream=None) -> None:
+        """Pages for n_tokens[b] (device int32 [batch]) more tokens of every sequence."""
+        kv_pages_reserve(self.cfg, self.cache, self.page_ref, n_tokens, self.status, self.stream if stream is None else stream)
+
+    def fork(self, src, dst, stream=None) -> None:
+        """Sequence dst[i] becomes a copy of src[i] (device int32 [n]); whole INT2 pages are shared."""
+        kv_seq_fork(self.cfg, self.cache, self.page_ref, src, dst, self.status, self.stream if stream is None else stream)
+
+    def free(self, seqs, stream=None) -> None:
+        """Sequences seqs (device int32 [n]) give up their pages and become empty."""
+        kv_seq_free(self.cfg, self.cache, self.page_ref, seqs, self.status, self.stream if stream is None else stream)
+
+    def compact_workspace(self) -> torch.Tensor:
+        return torch.zeros(max(256, kv_pages_compact_workspace_bytes(self.cfg)), dtype=torch.uint8, device=self.device)
+
+    def compact(self, ws, stream=None) -> torch.Tensor:
+        """Move the held pages to the front of the pool; their number is in the device tensor returned."""
+        kv_pages_compact(self.cfg, self.cache, self.page_ref, self.n_live, ws, self.status,
+                         self.stream if stream is None else stream)
+        return self.n_live
