@@ -5,8 +5,8 @@
 // the kv head) pair -- and its tokens t:  s[t][n] = scale k_t.q_n,  o_n = sum_t 2^(s - m_n) v_t /
 // sum_t 2^(s - m_n), one pass over the tokens with a running reference m_n.
 //
-// Tile and layout.  A tile is 128 tokens (8 INT2 pages, or 128 BF16 window rows) by N = 64 or 128
-// rows.  Tokens are the tensor core's M: S^T [128 tokens x N] = K [128 x d] Q^T, and
+// Tile and layout.  A tile is 128 tokens (8 INT2 pages, or 128 BF16 window rows) by N = 64 rows.
+// Tokens are the tensor core's M: S^T [128 tokens x N] = K [128 x d] Q^T, and
 // O^T [128 channels x N] += V^T [128 channels x 128 tokens] P [128 x N], so
 //   * the expanded K and V^T are the A operands and live in TMEM: a page's codes are stored in the
 //     fragment order of a 16-row MMA, which is the order of tcgen05.st.16x128b -- one 16-byte load
@@ -14,6 +14,8 @@
 //   * a lane of S^T is a token, so a token's scale (Delta, norm) is one number per thread, and a
 //     warp reads no scale per score;
 //   * P [token][row] goes to shared memory as the MN-major B operand, 16 bytes per 8 rows.
+// 128 rows a CTA were tried: the expansion is shared by twice the rows, but the softmax and P, which are not,
+// already took as long, and the second score buffer no longer fits.
 // Keys.  With one group per row (G = 128) A holds the codes themselves, exact, and the zero point is
 // one more K = 16 step (z against -sum q', hi + lo); Delta multiplies the finished sum.  With more
 // groups A holds Delta c as an exact fp16 hi + lo pair (13 bits), scaled by a power of two per token.
@@ -23,14 +25,27 @@
 // are fp32.  Window rows are bf16 as they are, with P as a bf16 hi + lo pair.
 //
 // Softmax reference.  m_n moves only when a score passes it by 8 (in log2): P <= 2^8.  The four
-// warps that share a row's tokens agree by one barrier with an OR; a move rescales O in TMEM.
+// warps that share a row's tokens agree by one barrier, whose answer is read when the exponentials are
+// formed already; a move rescales O in TMEM.
 //
-// Roles: 8 softmax warps (4 lane quadrants x 2 halves of the rows), 4 warps that expand codes (or
-// load window rows), one that issues the MMAs, one that streams pages (1-D bulk copies).  The tensor
-// pipe runs QK(i), PV(i-1), QK(i+1), ... while softmax(i) runs beside PV(i-1).
+// Roles: 8 softmax warps (4 lane quadrants x 2 halves of the rows), 4 warps that expand keys (or load window
+// rows), 8 that expand values, a warp each that issues QK and PV, one that streams pages (1-D bulk copies)
+// and one that finds the nodes' ancestors; registers are handed from the latter to the softmax.  S has two
+// buffers, so QK(i + 1) and the keys of i + 2 run beside softmax(i) and PV(i - 1).
 //
-// What bounds it: an MMA whose A comes from TMEM takes about 67 clocks for any N <= 128 (17 to 25 of
-// them a tile), so small trees are bound by the tensor pipe's issue, wide ones by its rate.
+// What bounds it: instructions, not the tensor pipe or memory.  A tile of 128 tokens takes 6,500 to 7,900
+// warp instructions, of which 2,700 are softmax, 2,300 the values and 1,000 (G = 128) the keys, in 2,600
+// clocks (1.26 us): the schedulers issue in 58% of their clocks, the pipe of logic, maxima and half precision
+// (one warp instruction in two clocks) is busy for 38%, the tensor pipe for 16%, DRAM reads each byte once;
+// the rest is the chain score - vote - exponential - P of the 8 softmax warps.  Measured: 64 nodes of 4 heads
+// on 32 K tokens 109 us (315 TFLOP/s), 16 nodes of 8 heads on 4 x 128 K tokens 870 us (237 TFLOP/s).
+// What those figures hang on:
+//   * MMAs are issued from code that the whole warp runs, by one elected lane: from a divergent branch each
+//     costs 53 clocks at least, whatever N is;
+//   * the roles' loops together stay within 32 KB, which is what an SM keeps of its code: a version with the
+//     value loop unrolled over its pages ran at half the speed, waiting for instructions;
+//   * about 12 us a CTA of set-up, q' operands, first reference and epilogue, which is why short contexts and
+//     narrow trees go to the row kernel (see row_kernel).
 //
 // Several CTAs share a long sequence (splits over tiles); their partial (m, l, o) are merged by a
 // second kernel, one warp per output row.
