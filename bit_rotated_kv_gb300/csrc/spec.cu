@@ -16,9 +16,9 @@
 // neither but runs at a fortieth of the integer rate on this chip.
 //
 // What bounds it: for one sequence, latency -- the sampler's decisions are a chain (8 nodes, 32,000 tokens:
-// 7.7 us).  For many, integer arithmetic: a row of 152 K target probabilities is 0.6 MB, read by one
-// cluster of CTAs, with the draft's row once more for every missed child (64 trees of 16 nodes: 81 us
-// for rows that HBM delivers in 11).  Rows that no decision needs are not read, and the sums of the last miss
+// 7.8 us).  For many, integer arithmetic: a row of 152 K target probabilities is 0.6 MB, read by one
+// cluster of CTAs, with the draft's row once more for every missed child (64 trees of 16 nodes: 71 us
+// for rows that HBM delivers in 11; four of them wait for four sums, one after another).  Rows that no decision needs are not read, and the sums of the last miss
 // are those that the draw needs.
 #include <cooperative_groups.h>
 
@@ -56,7 +56,7 @@ __device__ __forceinline__ void clean(float (&p)[N], bool& odd) {
     }
 }
 // ... in units of 2^-60: the 24-bit significand (1.0 is 2^23 << 37), what lies below a unit dropped.  (A 64-bit
-// float-to-integer conversion does the same, slower: 102 against 81 us for 64 trees over 152 K tokens.)
+// float-to-integer conversion does the same, slower: the whole call took 102 instead of 81 us with it.)
 __device__ __forceinline__ u64 units(float p) {
   const uint32_t bits = min(__float_as_uint(p), 0x3f800000u);
   return ((u64)((bits & 0x7fffffu) | 0x800000u) << 37) >> min(127u - (bits >> 23), 63u);
@@ -87,7 +87,7 @@ constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
 // CTAs per sequence.  Most sequences need one sum over their row, a few need one for every missed child, and
 // those are what the call waits for: 64 trees over 152 K tokens take 81 us with 16 x 256 threads to a
-// sequence, 89 us with 8 x 512.
+// sequence, 89 us with 8 x 512 (before the sums of limbs).
 constexpr int kVCluster = 16;
 constexpr int kVChunk = 128;         // tokens a warp takes at once, 4 a lane
 
@@ -175,29 +175,90 @@ __device__ __forceinline__ void weights(const VerifyShared& S, int misses, float
   }
 }
 
+// A probability's units as three limbs of 23, 23 and 14 bits, each the low bits of a float32: adding 1 (2^23)
+// and rounding down leaves a limb in the significand, and what it leaves out is exact.  Bits of floats with
+// one exponent are integers, so sums of limbs are sums of bits less their number times the exponent's.
+// (Eight float instructions for 11 of the integer pipe and a 64-bit sum: 80 -> 71 us for 64 trees of 16 nodes over
+// 152 K tokens.)
+struct Limbs {
+  uint32_t a, b, c;
+};
+constexpr uint32_t kLimbAB = 0x3f800000u, kLimbC = 0x4b000000u;
+__device__ __forceinline__ Limbs limbs(float p) {
+  p = __saturatef(p);
+  const float y1 = __fadd_rd(p, 1.f), r1 = __fsub_rn(p, __fsub_rn(y1, 1.f));
+  const float y2 = __fmaf_rd(r1, 0x1p23f, 1.f), r2 = __fmaf_rn(r1, 0x1p23f, -__fsub_rn(y2, 1.f));
+  const float y3 = __fmaf_rd(r2, 0x1p37f, 0x1p23f);
+  return {__float_as_uint(y1), __float_as_uint(y2), __float_as_uint(y3)};
+}
+// The sum of units that sums of limbs stand for, at most kTooMuch.  (a of at least 5 x 2^23 is more than 4
+// whatever b and c, which stay below 2^31 either way, are.)
+__device__ __forceinline__ u64 limb_sum(uint32_t a, int32_t b, int32_t c) {
+  if (a >= 5u << 23) return kTooMuch;
+  const long long t = ((long long)a << 37) + ((long long)b << 14) + c;
+  return min((u64)t, kTooMuch);
+}
+
 // This lane's part of the sum of a row's weights over tokens v0 .. v1 - 1, one warp's.  The next chunk
-// is on its way while one is summed.
-template <bool Q>
+// is on its way while one is summed.  No miss: sum p; one miss of a drawn draft: sum max(p - q, 0), as Z is
+// 1; otherwise token by token.
+enum { kPlain, kOneMiss, kMisses, kGone };
+template <int kMode>
 __device__ __forceinline__ u64 sum_chunks(const VerifyShared& S, const Row& R, int v0, int v1, bool& odd) {
+  constexpr bool Q = kMode == kOneMiss || kMode == kMisses;
+  constexpr int kBlock = 32;                    // chunks between conversions: 128 limbs below 2^23 each
   int v = v0 + 4 * (threadIdx.x & 31);
   const int chunks = (v1 - v0 + kVChunk - 1) / kVChunk;
   const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
   float4 p = load4(R.p, R.wide, v, v1), q = Q ? load4(R.q, R.wide, v, v1) : none;
   u64 acc = 0ull;
 #pragma unroll 1
-  for (int i = 0; i < chunks; ++i, v += kVChunk) {
-    float pv[4] = {p.x, p.y, p.z, p.w}, qv[4] = {q.x, q.y, q.z, q.w};
-    p = load4(R.p, R.wide, v + kVChunk, v1);
-    if (Q) q = load4(R.q, R.wide, v + kVChunk, v1);
-    u64 w[4];
-    weights<Q>(S, R.misses, pv, qv, [&](int k) { return v + k; }, w, odd);
-    acc = add_capped(acc, (w[0] + w[1]) + (w[2] + w[3]));   // (4 + 4 at most)
+  for (int i0 = 0; i0 < chunks; i0 += kBlock) {
+    uint32_t a = 0u, b = 0u, c = 0u;
+    const int here = min(kBlock, chunks - i0);
+#pragma unroll 1
+    for (int i = 0; i < here; ++i, v += kVChunk) {
+      float pv[4] = {p.x, p.y, p.z, p.w}, qv[4] = {q.x, q.y, q.z, q.w};
+      p = load4(R.p, R.wide, v + kVChunk, v1);
+      if (Q) q = load4(R.q, R.wide, v + kVChunk, v1);
+      if constexpr (kMode == kPlain || kMode == kOneMiss) {
+        clean(pv, odd);
+        if (Q) clean(qv, odd);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const Limbs x = limbs(pv[k]);
+          if constexpr (Q) {
+            const Limbs y = limbs(fminf(pv[k], qv[k]));
+            a += x.a - y.a;
+            b += x.b - y.b;
+            c += x.c - y.c;
+          } else {
+            a += x.a;
+            b += x.b;
+            c += x.c;
+          }
+        }
+      } else {
+        u64 w[4];
+        weights<Q>(S, R.misses, pv, qv, [&](int k) { return v + k; }, w, odd);
+        acc = add_capped(acc, (w[0] + w[1]) + (w[2] + w[3]));   // (4 + 4 at most)
+      }
+    }
+    if constexpr (kMode == kPlain) {
+      a -= 4u * here * kLimbAB;
+      b -= 4u * here * kLimbAB;
+      c -= 4u * here * kLimbC;
+    }
+    if constexpr (kMode == kPlain || kMode == kOneMiss) acc = add_capped(acc, limb_sum(a, (int32_t)b, (int32_t)c));
   }
   return acc;
 }
 __device__ __noinline__ u64 sum_part(const VerifyShared& S, const Row R, int v0, int v1, bool& odd) {
   bool bad = false;
-  const u64 acc = R.q && R.misses ? sum_chunks<true>(S, R, v0, v1, bad) : sum_chunks<false>(S, R, v0, v1, bad);
+  const u64 acc = R.misses == 0   ? sum_chunks<kPlain>(S, R, v0, v1, bad)
+                  : !R.q          ? sum_chunks<kGone>(S, R, v0, v1, bad)
+                  : R.misses == 1 ? sum_chunks<kOneMiss>(S, R, v0, v1, bad)
+                                  : sum_chunks<kMisses>(S, R, v0, v1, bad);
   odd |= bad;
   return acc;
 }
