@@ -12,14 +12,14 @@
 //
 // Every probability is an integer in units of 2^-60 (a float32 p >= 2^-36 is one exactly) and
 // every product floor(a b / 2^60), so sums are exact: the result does not depend on the order in
-// which 4096 threads add, and the same bits give the same token on every run.  Float64 would need
-// neither but runs at a fortieth of the integer rate on this chip.
+// which 4096 threads add, and the same bits give the same token on every run.  (Float64 sums would
+// depend on the order, and this chip has few units for them.)
 //
-// What bounds it: for one sequence, latency -- the sampler's decisions are a chain (8 nodes, 32,000 tokens:
-// 7.8 us).  For many, integer arithmetic: a row of 152 K target probabilities is 0.6 MB, read by one
-// cluster of CTAs, with the draft's row once more for every missed child (64 trees of 16 nodes: 71 us
-// for rows that HBM delivers in 11; four of them wait for four sums, one after another).  Rows that no decision needs are not read, and the sums of the last miss
-// are those that the draw needs.
+// What bounds it: for one sequence, latency -- the sampler's decisions are a chain (8 nodes, 32,000
+// tokens: 7.8 us).  For many, integer arithmetic: a row of 152 K target probabilities is 0.6 MB, read by
+// one cluster of CTAs, with the draft's row once more for every missed child (64 trees of 16 nodes: 71 us
+// for rows that HBM delivers in 11; four of them wait for four sums, one after another).  Rows that no
+// decision needs are not read, and the sums of the last miss are those that the draw needs.
 #include <cooperative_groups.h>
 
 #include <atomic>

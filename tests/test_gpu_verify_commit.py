@@ -99,6 +99,44 @@ def test_edges_of_the_numbers():
     assert acc[0] in (1, 2) and p[0][nxt[0]] > 0
 
 
+@pytest.mark.parametrize("dist", [False, True])
+def test_probabilities_at_the_ends_of_their_range(dist):
+    """Ones, values a step below, at and under the unit 2^-60, denormals, both zeros, more than 1 -- with misses."""
+    ends = np.array([0.0, -0.0, 1.0, np.nextafter(np.float32(1), np.float32(0)), 2.0 ** -23, 2.0 ** -24, 2.0 ** -36, 1.9999999 * 2.0 ** -37,
+                     1.5 * 2.0 ** -46, 2.0 ** -60, 1.5 * 2.0 ** -60, 2.0 ** -61, 2.0 ** -126, 2.0 ** -149, 0.3, 1.5], np.float32)
+    below = np.float32(1) - np.float32(2.0 ** -24)
+    for seed in range(12):
+        rng = np.random.default_rng(seed)
+        n, vocab = 7, 300
+        p, q = np.zeros((n, vocab), np.float32), np.zeros((n, vocab), np.float32)
+        for m in (p, q):
+            for r in range(n):                       # at most two of the large ones a row: its sum stays under 4
+                at = rng.choice(vocab, 60, replace=False)
+                m[r, at] = rng.choice(ends[[0, 1, *range(4, 14)]], 60)
+                m[r, at[:2]] = rng.choice(ends[[2, 3, 14, 15]], 2)
+        parent = np.array([-1, 0, 0, 0, 0, 3, 3], np.int32)
+        token = np.array([0] + [int(rng.choice(np.nonzero(q[max(0, parent[i])])[0])) for i in range(1, n)], np.int32)
+        u = rng.choice(np.array([0.0, 0.5, below, 2.0 ** -40], np.float32), n)
+        want, last = spec_ref.verify(parent, token, p, q if dist else None, u)
+        path, acc, nxt, _ = _run(np.array([0, n], np.int32), parent, token, p, q if dist else None, u, pad=seed % 4)
+        assert path[:acc[0]].tolist() == want and nxt[0] == last, seed
+
+
+def test_sums_over_a_vocabulary_of_many_chunks():
+    # 700,003 tokens: 43 chunks of 128 a warp; a draft that is missed once, and twice
+    rng = np.random.default_rng(3)
+    vocab, below = 700003, np.float32(1) - np.float32(2.0 ** -24)
+    p, q = (_softmax(rng.standard_normal((3, vocab))) for _ in range(2))
+    token = np.array([0, int(np.argmax(q[0] - 9 * p[0])), int(np.argmax(q[0] - 5 * p[0]))], np.int32)
+    parent, cu = np.array([-1, 0, 0], np.int32), np.array([0, 3], np.int32)
+    for us in ([0.37, below, below], [0.9999, below, 0.0], [below, 0.0, below]):
+        u = np.array(us, np.float32)
+        for draft in (None, q):
+            want, last = spec_ref.verify(parent, token, p, draft, u)
+            path, acc, nxt, _ = _run(cu, parent, token, p, draft, u, pad=1)
+            assert path[:acc[0]].tolist() == want and nxt[0] == last
+
+
 def test_tokens_are_distributed_as_the_target():
     """First new token over 20000 independent sequences with two sampled siblings: each of 5 tokens'
     frequency within 5 standard deviations of the target's probability."""
