@@ -106,6 +106,7 @@ __device__ __forceinline__ int tree_group(const AttnParams& P, int b, int& node0
   for (int b0 = 0, before = 0; b0 < P.seqs; b0 += 32) {
     const long long n = b0 + lane < P.seqs ? (long long)P.cu_rows[b0 + lane + 1] - P.cu_rows[b0 + lane] : 0;
     const int pack_log2 = P.gqa_log2 - P.heads_log2;
+    if (n < 0) set_status(P.status, KVQ_ERR_BOUNDS);       // (the other sequences have their rows)
     const int mine = n > 0 ? ((int)min(n, (long long)P.n_rows) + (1 << pack_log2) - 1) >> pack_log2 : 0;
     int upto = mine;
 #pragma unroll

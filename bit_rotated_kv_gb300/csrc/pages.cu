@@ -51,29 +51,30 @@ struct PageParams {
   int32_t* moved;        // compact workspace: count, then source and target lists and the new ids
 };
 
-// Block-wide inclusive sum of one int per thread; returns the thread's own prefix, `all` the total.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& all) {
+// Block-wide inclusive sum of one T per thread; returns the thread's own prefix, `all` the total.
+template <class T>
+__device__ __forceinline__ T block_scan(T v, T* warp_sums, T& all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, v, o);
+    const T t = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += t;
   }
   __syncthreads();
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
   if (warp == 0) {
-    int w = warp_sums[lane];
+    T w = warp_sums[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, w, o);
+      const T t = __shfl_up_sync(0xffffffffu, w, o);
       if (lane >= o) w += t;
     }
     warp_sums[lane] = w;
   }
   __syncthreads();
   all = warp_sums[kPWarps - 1];
-  return v + (warp ? warp_sums[warp - 1] : 0);
+  return v + (warp ? warp_sums[warp - 1] : T(0));
 }
 
 // Entries of a table row that hold a page: they are a prefix of it (searched 32 ways at a time).
@@ -103,6 +104,7 @@ __device__ __forceinline__ bool fork_pair_ok(const PageParams& P, int i) {
 
 struct PageShared {
   int warp_sums[kPWarps];
+  long long wide_sums[kPWarps];
   int count[2];          // this CTA's counts, read by the others of the cluster
 };
 
@@ -113,13 +115,14 @@ struct PageShared {
 template <class Give>
 __device__ int hand_out(const PageParams& P, cg::cluster_group& cluster, PageShared& S, int* end, int n, Give give) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)cluster.block_rank();
-  // prefix sums of the needs, the same in every CTA
-  int before = 0;
+  // prefix sums of the needs, the same in every CTA (in 64 bits: thousands of sequences may ask for more than
+  // any pool has)
+  long long before = 0;
   for (int u0 = 0; u0 < n; u0 += kPThreads) {
-    int all;
-    const int v = u0 + tid < n ? end[u0 + tid] : 0;
-    const int upto = block_scan(v, S.warp_sums, all);
-    if (u0 + tid < n) end[u0 + tid] = before + upto;
+    long long all;
+    const long long v = u0 + tid < n ? end[u0 + tid] : 0;
+    const long long upto = block_scan(v, S.wide_sums, all);
+    if (u0 + tid < n) end[u0 + tid] = (int)min(before + upto, (long long)INT32_MAX);
     before += all;
   }
   // free pages of this warp's slice of the pool

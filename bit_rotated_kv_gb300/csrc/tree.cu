@@ -63,14 +63,16 @@ constexpr int kNodeWords = kNodes / 32;
 constexpr int kTile = 128;                       // tokens of a tile
 constexpr int N = 64;                            // rows (node, query head) of a CTA
 constexpr int kTilePages = kTile / kPage;
-constexpr int kSmWarps = 8;                      // softmax; then 4 warps for keys, 8 for values, 4 more
-constexpr int kKeyWarp = 8, kValWarp = 12, kQkWarp = 20, kPageWarp = 21, kPvWarp = 22, kSeenWarp = 23;
+constexpr int kSmWarps = 16;                     // softmax; then 4 warps for keys, 8 for values, 4 more
+constexpr int kKeyWarp = 16, kValWarp = 20, kQkWarp = 28, kPageWarp = 29, kPvWarp = 30, kSeenWarp = 31;
+constexpr int kShares = kSmWarps / 4;            // shares of the rows, four warps (128 tokens) each
+constexpr int kCols = N / kShares;               // rows of a softmax warp
 constexpr int kKeyWarps = 4, kValWarps = 8;
-constexpr int kThreadsT = 32 * 24;               // (whole warpgroups: registers are handed over by warpgroup)
+constexpr int kThreadsT = 32 * 32;               // (whole warpgroups: registers are handed over by warpgroup)
 constexpr int kStages = 4;                       // page tiles in flight
-// Registers a thread by role, of the 80 that 768 threads launch with.
-constexpr int kRegsLaunch = 80, kRegsSoftmax = 104, kRegsKeys = 72, kRegsValues = 56, kRegsIssue = 48;
-static_assert(256 * kRegsSoftmax + 128 * kRegsKeys + 256 * kRegsValues + 128 * kRegsIssue <= kThreadsT * kRegsLaunch, "register split");
+// Registers a thread by role, of the 64 that 1024 threads launch with.
+constexpr int kRegsLaunch = 64, kRegsSoftmax = 72, kRegsKeys = 64, kRegsValues = 56, kRegsIssue = 48;
+static_assert(32 * kSmWarps * kRegsSoftmax + 128 * kRegsKeys + 256 * kRegsValues + 128 * kRegsIssue <= kThreadsT * kRegsLaunch, "register split");
 
 constexpr int kWinCost = 3;                      // a window tile's time in page tiles'
 constexpr long long kSmallCall = 1 << 19;        // row_kernel(): rows x kv heads x tokens
@@ -152,7 +154,7 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 4, 256;" ::: "memory"); }
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 4, %0;" ::"n"(32 * kSmWarps) : "memory"); }
 // one lane of a converged warp: the code around it stays uniform, so descriptors are formed in uniform
 // registers (issued from a divergent lane an MMA takes 53 clocks, so 20 .. 33 at N = 32 .. 64 are lost)
 __device__ __forceinline__ bool elect() {
@@ -193,12 +195,12 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)) : "memory");
 }
 #define KVQ_IO8(c, b) c(v[b]), c(v[b + 1]), c(v[b + 2]), c(v[b + 3]), c(v[b + 4]), c(v[b + 5]), c(v[b + 6]), c(v[b + 7])
-// 32 columns of this warp's lanes -> registers
-__device__ __forceinline__ void tm_ld32(uint32_t a, float (&v)[32]) {
+// 16 (8) columns of this warp's lanes -> registers
+__device__ __forceinline__ void tm_ld16(uint32_t a, float (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n tcgen05.wait::ld.sync.aligned;"
-      : KVQ_IO8("=f", 0), KVQ_IO8("=f", 8), KVQ_IO8("=f", 16), KVQ_IO8("=f", 24)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n "
+      "tcgen05.wait::ld.sync.aligned;"
+      : KVQ_IO8("=f", 0), KVQ_IO8("=f", 8)
       : "r"(a)
       : "memory");
 }
@@ -285,6 +287,7 @@ __device__ __forceinline__ SeqState seq_state(const TreeParams& P, int b) {
 // Row tiles a sequence takes (a bad one: one, which reports it).
 __device__ __forceinline__ int row_tiles(const TreeParams& P, int b) {
   const long long n = (long long)P.cu_rows[b + 1] - P.cu_rows[b];
+  if (n < 0) set_status(P.status, KVQ_ERR_BOUNDS);         // (the other sequences have their rows)
   if (n <= 0) return 0;
   return n > kNodes ? 1 : (int)((n * P.gqa + N - 1) / N);
 }
@@ -306,7 +309,7 @@ struct Layout {          // dynamic shared memory, from a 1024-byte boundary
 };
 
 struct TreeShared {
-  __align__(16) uint64_t page_full[kStages], page_free[kStages], q_full, seen_full, vote[2], meet[2], k_full[2], v_full[2], s_full[2], s_free[2], p_full[2],
+  __align__(16) uint64_t page_full[kStages], page_free[kStages], q_full, seen_full, vote[kShares], meet[kShares], k_full[2], v_full[2], s_full[2], s_free[2], p_full[2],
       pv_done[2];
   uint32_t tmem;
   int gave_up;
@@ -315,9 +318,9 @@ struct TreeShared {
   __align__(4) uint16_t alive[4][kTilePages];            // tokens of a tile that exist, by lane quadrant
   __align__(16) float neg_m[N];    // minus the reference of every row
   __align__(16) float alpha[N];    // a moved reference: factor of what is summed so far
-  float red[4][N];                 // per-quadrant maxima; at the end parts of the sums
+  float red[kTile / kCols][N];     // per-quadrant maxima; at the end parts of the sums
   uint8_t v_odd[2][kTile];         // window tiles with drafts: whether a token's value row is not finite
-  int moves[2];                    // the last tile (+ 1) in which a half's references have to move
+  int moves[kShares];              // the last tile (+ 1) in which a share's references have to move
   __align__(16) uint32_t seen[kNodes][kNodeWords];   // ancestors of every node, itself among them
   int jump[kNodes];                // (while they are found: the next one)
   int whole[kStages];              // every page of the tile is there in whole
@@ -333,8 +336,7 @@ static_assert(Layout::kEnd + sizeof(TreeShared) <= 227 * 1024, "shared memory of
 template <int NG>
 __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_constant__ TreeParams P) {
   using L = Layout;
-  constexpr int kCols = N / 2;                              // rows of a softmax warp
-  static_assert(kCols == 32, "a softmax warp's lanes stand for its rows at times");
+  static_assert(kCols == 16, "a softmax warp's lanes stand for its rows (twice) at times");
   // TMEM columns: O, S twice (the next product runs while the softmax reads the last), the key operand
   // (64, or 128 as pairs) twice and the value operand (64), twice where there is room
   constexpr int kKCols = NG == 1 ? 64 : 128;
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     }
     bar_init(&S.q_full, kSmWarps);
     bar_init(&S.seen_full, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kShares; ++i) {
       bar_init(&S.vote[i], 4);
       bar_init(&S.meet[i], 4);
       S.moves[i] = 0;
@@ -863,11 +865,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     }
   } else {
     regs_inc<kRegsSoftmax>();
-    // ---- softmax: token 32 q + lane of every tile, rows kCols half ..
-    const int q = warp & 3, half = warp >> 2;
+    // ---- softmax: token 32 q + lane of every tile, rows kCols share ..
+    const int q = warp & 3, share = warp >> 2;
     const uint32_t tq = tb + ((uint32_t)(32 * q) << 16);
-    const int c0 = half * kCols, tok = 32 * q + lane;
-    // q' operands first (these 256 threads): bf16 rows, 16-byte chunk j of row c in slab j / 8, swizzled
+    const int c0 = share * kCols, tok = 32 * q + lane;
+    // q' operands first (these threads): bf16 rows, 16-byte chunk j of row c in slab j / 8, swizzled
     auto at = [&](int c, int j) { return (j >> 3) * N * 128 + (c >> 3) * 1024 + (c & 7) * 128 + (((j & 7) ^ (c & 7)) << 4); };
     int sigma = 0;
     {
@@ -879,7 +881,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       softmax_sync();
       float amax = 0.f;
 #pragma unroll 4
-      for (int i = tid; i < N * 16; i += 256) {
+      for (int i = tid; i < N * 16; i += 32 * kSmWarps) {
         const int c = i >> 4, j = i & 15;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (c < ncol) v = reinterpret_cast<const uint4*>(P.q + (size_t)S.row[c] * kHeadDim)[j];
@@ -898,7 +900,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       if (amax > 0.f && amax < INFINITY) sigma = min(100, 14 - ((int)(__float_as_uint(amax) >> 23) - 126));
       // fp16 rows, channel slot s scaled by 4^-s for the codes that carry 4^s
 #pragma unroll 2
-      for (int i = tid; i < N * 16; i += 256) {
+      for (int i = tid; i < N * 16; i += 32 * kSmWarps) {
         const int c = i >> 4, j = i & 15;
         const uint4 v = lds16(sm + L::kQb + at(c, j));
         const float f = __int_as_float((sigma - 2 * slot_pow(j >> 1) + 127) << 23);
@@ -910,7 +912,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       }
       // zero-point operand, row c: slots 2 g, 2 g + 1: -sum of group g (hi), slot 8 + 2 g: its lo.  Four
       // threads a row, 32 channels each
-      {
+      if (tid < 4 * N) {
         const int c = tid >> 2, part = tid & 3;
         float acc = 0.f;
 #pragma unroll
@@ -938,14 +940,14 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
 #pragma unroll
     for (int j = 0; j < kCols; ++j) l[j] = 0.f;
     bool lost = false;
-    bool unseen = true;                                     // row c0 + lane has seen no token yet
+    bool unseen = true;                                     // row c0 + lane % kCols has seen no token yet
     bool force = true;                                      // ... there are such rows (all four warps agree)
     int meets = 0;
-    // the half's four warps meet (bounded, so that a warp that gave up leaves nobody behind)
+    // the share's four warps meet (bounded, so that a warp that gave up leaves nobody behind)
     auto meet = [&]() {
       __syncwarp();
-      if (lane == 0) bar_arrive(&S.meet[half]);
-      if (!warp_wait(&S.meet[half], meets++, gave_up)) lost = true;
+      if (lane == 0) bar_arrive(&S.meet[share]);
+      if (!warp_wait(&S.meet[share], meets++, gave_up)) lost = true;
     };
 #pragma unroll 1
     for (int i = 0; i < nt && !lost; ++i) {
@@ -974,7 +976,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
           see = 0u;
           const int wd = (node >> 5) & (kNodeWords - 1);
 #pragma unroll 1
-          for (int j = 0; j < 32; ++j)
+          for (int j = 0; j < kCols; ++j)
             see |= ((S.seen[min((row0 + c0 + j) >> P.gqa_log2, kNodes - 1)][wd] >> (node & 31)) & 1u) << j;
         }
       }
@@ -982,7 +984,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       bool moved = false;
 #pragma unroll 1
       for (;;) {
-        tm_ld32(ts + c0, x);
+        tm_ld16(ts + c0, x);
         // scores less the reference
 #pragma unroll
         for (int j = 0; j < kCols; j += 4) {
@@ -1010,18 +1012,18 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
           // one vote of the four warps, taken while the exponentials are already formed
           const bool any = __any_sync(0xffffffffu, over) || force;
           if (lane == 0) {
-            if (any) *(volatile int*)&S.moves[half] = i + 1;
-            bar_arrive(&S.vote[half]);
+            if (any) *(volatile int*)&S.moves[share] = i + 1;
+            bar_arrive(&S.vote[share]);
           }
         }
 #pragma unroll
         for (int j = 0; j < kCols / 2; ++j) x[j] = ex2(x[j]);
         if (moved) break;
-        if (!warp_wait(&S.vote[half], i, gave_up)) {
+        if (!warp_wait(&S.vote[share], i, gave_up)) {
           lost = true;
           break;
         }
-        if (*(volatile int*)&S.moves[half] != i + 1) break;
+        if (*(volatile int*)&S.moves[share] != i + 1) break;
         // ---- the references move to the rows' maxima so far
         moved = true;
 #pragma unroll 1
@@ -1035,7 +1037,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
           if (lane < 8) S.red[q][c0 + j + lane] = top;
         }
         meet();
-        const int c = c0 + lane;
+        const int c = c0 + lane % kCols;
         const float up = fmaxf(fmaxf(S.red[0][c], S.red[1][c]), fmaxf(S.red[2][c], S.red[3][c]));
         // a first token sets the reference, later ones only raise it
         const bool any = up > -INFINITY;
@@ -1126,13 +1128,15 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     }
     meet();
     if (!lost) {
-      // every thread: one channel of the half's rows, 8 rows at a time
-      const int c = c0 + lane;
-      const float sum = (S.red[0][c] + S.red[1][c]) + (S.red[2][c] + S.red[3][c]);
+      // every thread: one channel of the share's rows, 8 rows at a time
+      const int c = c0 + lane % kCols;
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kTile / kCols; ++k) sum += S.red[k][c];
       // 1 / l; a row that saw nothing gives 0, one whose sum is no number that
       const float by = P.splits > 1 ? 1.f : sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
       const float top = sum != 0.f ? -S.neg_m[c] : -1e30f;
-      if (P.splits > 1 && q == 0 && c < ncol)
+      if (P.splits > 1 && q == 0 && lane < kCols && c < ncol)
         *reinterpret_cast<float2*>(P.part + ((size_t)S.row[c] * P.splits + split) * kRec) = make_float2(top, sum);
 #pragma unroll 1
       for (int j = 0; j < kCols && c0 + j < ncol; j += 8) {

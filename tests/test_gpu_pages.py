@@ -127,6 +127,21 @@ def test_reserve_stops_where_the_pool_ends():
     d.check(p)
 
 
+def test_needs_whose_sum_passes_32_bits():
+    # 2,099 sequences that ask for 2^20 pages each, behind one that asks for 3
+    kvq = _kvq()
+    cfg = kvq.KVConfig(n_q_heads=1, n_kv_heads=1, batch=2100, max_pages_per_seq=1 << 20, num_pages=50, ring_cap=16, s_sink=0, s_keep=8,
+                       s_flush=1)
+    c = kvq.KVCache(cfg)
+    ref, status = (torch.zeros(k, dtype=torch.int32, device="cuda") for k in (50, 1))
+    want = torch.full((2100,), 16 << 20, dtype=torch.int32, device="cuda")
+    want[0] = 48
+    kvq.kv_pages_reserve(cfg, c, ref, want, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == kvq.KVQ_ERR_BOUNDS
+    assert c.page_table[0, :4].tolist() == [0, 1, 2, -1] and int((c.page_table >= 0).sum()) == 3 and int(ref.sum()) == 3
+
+
 def test_reserve_extends_what_a_sequence_holds():
     d = Device(batch=3, num_pages=64, max_pages=40)
     p = d.plain()
