@@ -94,12 +94,15 @@ __device__ __forceinline__ int pages_held(const int32_t* row, int max_pages) {
 }
 
 // Whether pair i of a fork is one: both sequences exist, and its destination is the destination of
-// no earlier pair and the source of none.  Called by whole blocks.
+// no earlier pair and the source of none.  Called by whole blocks (kBlock) or warps.
+template <bool kBlock>
 __device__ __forceinline__ bool fork_pair_ok(const PageParams& P, int i) {
   const int src = P.a[i], dst = P.b[i];
   int bad = src < 0 || src >= P.batch || dst < 0 || dst >= P.batch;
-  for (int j = threadIdx.x; j < P.n; j += blockDim.x) bad |= P.a[j] == dst || (j < i && P.b[j] == dst);
-  return !__syncthreads_or(bad);
+#pragma unroll 4
+  for (int j = kBlock ? threadIdx.x : threadIdx.x & 31; j < P.n; j += kBlock ? blockDim.x : 32)
+    bad |= P.a[j] == dst || (j < i && P.b[j] == dst);
+  return kBlock ? !__syncthreads_or(bad) : !__any_sync(0xffffffffu, bad);
 }
 
 struct PageShared {
@@ -179,6 +182,7 @@ __global__ void __cluster_dims__(kPCluster, 1, 1) __launch_bounds__(kPThreads)
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int* held = end + P.batch;
+  cluster.sync();                              // (every CTA has started: its shared memory can be written)
   for (int u = rank * kPWarps + warp; u < P.batch; u += kPCluster * kPWarps) {
     const long long tokens = P.a[u];
     int need = 0, have = 0;
@@ -216,8 +220,10 @@ __global__ void __cluster_dims__(kPCluster, 1, 1) __launch_bounds__(kPThreads)
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), tid = threadIdx.x;
   int* shared_pages = end + P.n;               // -1: not a pair
-  for (int i = rank; i < P.n; i += kPCluster) {
-    bool ok = fork_pair_ok(P, i);
+  cluster.sync();                              // (every CTA has started: its shared memory can be written)
+  const int lane = tid & 31, gwarp = rank * kPWarps + (tid >> 5);
+  for (int i = gwarp; i < P.n; i += kPCluster * kPWarps) {
+    bool ok = fork_pair_ok<false>(P, i);
     int full = -1, need = 0;
     if (ok) {
       const int src = P.a[i], dst = P.b[i];
@@ -230,12 +236,11 @@ __global__ void __cluster_dims__(kPCluster, 1, 1) __launch_bounds__(kPThreads)
     if (!ok) {
       full = -1;
       need = 0;
-      if (tid == 0) set_status(P.status, KVQ_ERR_BOUNDS);
+      if (lane == 0) set_status(P.status, KVQ_ERR_BOUNDS);
     }
-    __syncthreads();
-    if (tid < kPCluster) {
-      cluster.map_shared_rank(end, tid)[i] = need;
-      cluster.map_shared_rank(shared_pages, tid)[i] = full;
+    if (lane < kPCluster) {
+      cluster.map_shared_rank(end, lane)[i] = need;
+      cluster.map_shared_rank(shared_pages, lane)[i] = full;
     }
   }
   cluster.sync();
@@ -257,8 +262,8 @@ __global__ void __cluster_dims__(kPCluster, 1, 1) __launch_bounds__(kPThreads)
       P.counters[dst] = P.parts;               // the copying CTAs count it back to zero
     }
   }
-  const int lane = tid & 31, per_pair = (P.max_pages + 127) / 128;
-  for (long long k = rank * kPWarps + (tid >> 5); k < (long long)P.n * per_pair; k += kPCluster * kPWarps) {
+  const int per_pair = (P.max_pages + 127) / 128;
+  for (long long k = gwarp; k < (long long)P.n * per_pair; k += kPCluster * kPWarps) {
     const int i = (int)(k / per_pair), c0 = (int)(k % per_pair) * 128 + lane, full = shared_pages[i];
     if (c0 - lane >= full || end[i] > free_pages) continue;
     const int32_t* from = P.table + (size_t)P.a[i] * P.max_pages;
@@ -286,7 +291,7 @@ constexpr int kRowBatch = 8;         // rows a thread has in flight
 
 __global__ void __launch_bounds__(kCopyThreads) seq_fork_rows_kernel(const __grid_constant__ PageParams P) {
   const int i = blockIdx.y, h = blockIdx.x / kRowParts, part = blockIdx.x % kRowParts;
-  if (!fork_pair_ok(P, i)) return;
+  if (!fork_pair_ok<true>(P, i)) return;
   const int src = P.a[i], dst = P.b[i], tid = threadIdx.x;
   __shared__ int live;
   if (tid == 0) live = *(volatile int32_t*)(P.counters + dst);
