@@ -33,14 +33,14 @@
 // and one that finds the nodes' ancestors; registers are handed from the latter to the softmax.  S has two
 // buffers, so QK(i + 1) and the keys of i + 2 run beside softmax(i) and PV(i - 1).
 //
-// What bounds it: instructions and their latency, not the tensor pipe or memory.  A tile of 128 tokens takes
-// 6,500 to 7,900 warp instructions, of which 2,700 are softmax, 2,300 the values and 1,000 (G = 128) the keys,
-// in 2,600 clocks (1.26 us): the schedulers issue in 58% of their clocks, the pipe of logic, maxima and half
-// precision (one warp instruction in two clocks) is busy for 38%, the tensor pipe for 16%, DRAM reads each
-// byte once.  No part stands out: with its exponentials, its stores of P or the values' stores to TMEM left
-// out the kernel takes as long within 2%, without the keys' stores 3 to 8% less; 8 softmax warps of 32 rows
-// were 2.5% slower than 16 of 16.  Measured: 64 nodes of 4 heads on 32 K tokens 107 us (322 TFLOP/s), 16
-// nodes of 8 heads on 4 x 128 K tokens 853 us (242 TFLOP/s).
+// What bounds it: instruction issue, not the tensor pipe or memory.  A tile of 128 tokens takes 9,400 warp
+// instructions (G = 128), more than half of them softmax, 2,300 the values and 1,000 the keys, in 2,600 clocks
+// (1.26 us): the schedulers issue in 72% of their clocks, the pipe of logic, maxima and half precision (one
+// warp instruction in two clocks) is busy for 49%, the tensor pipe for 16%, DRAM reads each byte once.  No
+// part stands out: with its exponentials, its stores of P or the values' stores to TMEM left out the kernel
+// takes as long within 2%, without the keys' stores 3 to 8% less.  8 softmax warps of 32 rows execute 7,900
+// instructions a tile at 58% and take 2.5% longer.  Measured: 64 nodes of 4 heads on 32 K tokens 107 us (322
+// TFLOP/s), 16 nodes of 8 heads on 4 x 128 K tokens 853 us (242 TFLOP/s).
 // What those figures hang on:
 //   * MMAs are issued from code that the whole warp runs, by one elected lane: from a divergent branch each
 //     costs 53 clocks at least, whatever N is;

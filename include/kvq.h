@@ -379,7 +379,7 @@ KVQ_API int kv_attn_tree(const kvq_config* cfg, const kvq_cache* cache, const ui
  * Probabilities above 1 count as 1; negative or non-finite ones as 0, with KVQ_ERR_NONFINITE, as is a
  * distribution whose sum is 0 or at least 4 (next_token -1).  A sequence whose rows are not such a
  * tree, or whose tokens are not below vocab: KVQ_ERR_BOUNDS, n_accept 0, next_token -1.
- * Of cfg only batch is used (at most 65535: KVQ_ERR_UNSUPPORTED). */
+ * Of cfg only batch is used (at most 65535, and vocab at most 2^30: KVQ_ERR_UNSUPPORTED). */
 KVQ_API int kv_verify_tree(const kvq_config* cfg, const int32_t* cu_rows, const int32_t* parent, const int32_t* token,
                    int32_t n_rows, const float* p, int64_t p_stride, const float* q, int64_t q_stride, int32_t vocab,
                    const float* u, int32_t* path, int32_t* n_accept, int32_t* next_token, int32_t* d_status,

@@ -212,3 +212,13 @@ def test_verify_rejects_rows_that_overlap(kvq):
                  (torch.zeros(2, 50), None), (torch.zeros(3, 50).double(), None), (torch.zeros(50, 3).t(), None)):
         with pytest.raises(kvq.KVQError):
             kvq.kv_verify_tree(_cfg(kvq), i, i, i, p, q, torch.zeros(3), i, i, i, i)
+
+
+def test_sizes_that_no_tree_has_are_refused(kvq):
+    lib, c = kvq.lib(), _cfg(kvq).c()
+    fake = kvq.CCache(*([4096] * 9))
+    B, F, most = ctypes.byref, ctypes.c_float(0.1), _cfg(kvq).batch * kvq.KVQ_TREE_MAX_NODES
+    tree = lambda n: lib.kv_attn_tree(B(c), B(fake), 4096, 4096, 4096, n, 4096, F, 4096, 4096, 16, None, None)  # noqa: E731
+    assert tree(most) == -7 and tree(most + 1) == -1
+    assert lib.kv_attn_tree_workspace_bytes(B(c), most, 4096) > 0 and lib.kv_attn_tree_workspace_bytes(B(c), most + 1, 4096) == 0
+    assert lib.kv_verify_tree(B(c), 4096, 4096, 4096, 8, 4096, 1 << 31, None, 0, (1 << 30) + 1, 4096, 4096, 4096, 4096, None, None) == -2
