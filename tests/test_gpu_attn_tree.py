@@ -109,6 +109,10 @@ CASES = {
     "wide_odd_sink": (BASE.replace(batch=2, ctx_lo=500, ctx_hi=600, s_sink=5, s_keep=48), [50, 31], "random"),
     "wide_quest": (BASE.replace(batch=2, ctx_lo=900, ctx_hi=900, quantizer="quest"), [42, 43], "random"),
     "wide_gqa2": (BASE.replace(batch=3, n_q_heads=16, ctx_lo=900, ctx_hi=1200), [60, 70, 80], "random"),
+    "no_sink": (BASE.replace(batch=1, ctx_lo=333, ctx_hi=333, s_sink=0, s_keep=32), [7], "random"),
+    "wide_no_sink": (BASE.replace(batch=2, ctx_lo=333, ctx_hi=420, s_sink=0, s_keep=32), [66, 40], "random"),
+    "drafts_are_the_window": (BASE.replace(batch=1, ctx_lo=333, ctx_hi=333, s_sink=0, s_keep=0, s_flush=1), [7], "random"),
+    "wide_drafts_are_the_window": (BASE.replace(batch=2, ctx_lo=333, ctx_hi=420, s_sink=0, s_keep=0, s_flush=1), [66, 40], "random"),
     "mid_context": (BASE.replace(batch=1, n_q_heads=8, n_kv_heads=2, ctx_lo=9000, ctx_hi=9000), [48], "random"),
 }
 
