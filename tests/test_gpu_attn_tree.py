@@ -208,6 +208,22 @@ def test_a_draft_that_is_not_finite_reaches_the_nodes_that_see_it_only(counts, s
                 assert ((o[:g].float() - c[:g].float()).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("counts", [[6], [40, 33]], ids=["narrow", "wide"])
+def test_pages_beyond_4_gib(counts):
+    w = BASE.replace(batch=len(counts), ctx_lo=900, ctx_hi=1100)
+    run, q, cu, parent = _drafted(w, counts, "random")
+    want = _call(run, q, cu, parent)
+    c = run.runner.cache
+    few = run.cfg.num_pages
+    many = (5 << 30) // c.pages[0].numel() + few     # the same pages, at the far end of a pool of more than 5 GiB
+    pool = torch.zeros((many, *c.pages.shape[1:]), dtype=torch.uint8, device=run.device)
+    pool[many - few:] = c.pages
+    run.cfg.num_pages, c.pages = many, pool
+    c.page_table += torch.where(c.page_table >= 0, many - few, 0).to(torch.int32)
+    assert torch.equal(_call(run, q, cu, parent).view(torch.int16), want.view(torch.int16))
+    assert int(run.runner.status.item()) == 0
+
+
 def test_one_workspace_serves_trees_of_any_size():
     """Calls of both kernels and of many sizes in turn: the tickets of each are as it needs them."""
     import bit_rotated_kv_gb300 as kvq

@@ -168,6 +168,33 @@ def test_pool_larger_than_one_scan():
     d.check(p)
 
 
+def test_pages_beyond_4_gib():
+    # six pages at the far end of a pool of more than 5 GiB: forked (the half-filled one is copied), then moved to its front
+    kvq = _kvq()
+    cfg = kvq.KVConfig(n_q_heads=8, n_kv_heads=8, batch=2, max_pages_per_seq=8, num_pages=1, ring_cap=96, s_sink=5, s_keep=48, s_flush=1,
+                       group_size=64)
+    cfg.num_pages = many = (5 << 30) // (8 * kvq.kvq_page_head_bytes(cfg))
+    c = kvq.KVCache(cfg)
+    ids = torch.arange(many - 6, many, dtype=torch.int32, device="cuda")
+    c.pages[many - 6:] = torch.randint(0, 256, c.pages[:6].shape, device="cuda", dtype=torch.uint8)
+    was = c.pages[many - 6:].clone()
+    c.page_table[0, :6] = ids
+    c.s_quant[0], c.seq_len[0] = 5 + 5 * 16 + 7, 5 + 5 * 16 + 7 + 48
+    ref, status, n_live = (torch.zeros(k, dtype=torch.int32, device="cuda") for k in (many, 1, 1))
+    ref[many - 6:] = 1
+    one = lambda x: torch.tensor([x], dtype=torch.int32, device="cuda")  # noqa: E731
+    kvq.kv_seq_fork(cfg, c, ref, one(0), one(1), status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and c.page_table[1, :7].tolist() == [*ids[:5].tolist(), 0, -1]
+    assert torch.equal(c.pages[0], was[5])
+    ws = torch.zeros(kvq.kv_pages_compact_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+    kvq.kv_pages_compact(cfg, c, ref, n_live, ws, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and int(n_live.item()) == 7
+    assert c.page_table[0, :6].tolist() == [1, 2, 3, 4, 5, 6] and c.page_table[1, :6].tolist() == [1, 2, 3, 4, 5, 0]
+    assert torch.equal(c.pages[1:7], was) and ref[:8].tolist() == [1, 2, 2, 2, 2, 2, 1, 0] and int(ref.sum()) == 12
+
+
 def test_fork_refusals():
     kvq = _kvq()
     d = Device()
