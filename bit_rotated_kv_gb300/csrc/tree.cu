@@ -19,12 +19,13 @@
 // Keys.  With one group per row (G = 128) A holds the codes themselves, exact, and the zero point is
 // one more K = 16 step (z against -sum q', hi + lo); Delta multiplies the finished sum.  With more
 // groups A holds Delta c as an exact fp16 hi + lo pair (13 bits), scaled by a power of two per token.
-// q' is scaled by one power of two per CTA (exact unless a row's largest value is 2^22 below
-// another's).  Values are dequantized to fp16, Delta (c - z) in one rounding (relative 2^-11 of the
+// q' is scaled by a power of two of its row, its largest value to 2^13 .. 2^14: exact down to 2^-22 of that value
+// (8 bits above fp16's last step 2^-24, in slots that carry 4^-4), below it off by at most 2^-30 of it.  Values are dequantized to fp16, Delta (c - z) in one rounding (relative 2^-11 of the
 // value and of Delta z: the output's own rounding to bf16 is 2^-8).  P is rounded to fp16, the sums l
 // are fp32.  Window rows are bf16 as they are, with P as a bf16 hi + lo pair.
 //
-// Softmax reference.  m_n moves only when a score passes it by 8 (in log2): P <= 2^8.  The four
+// Softmax reference.  m_n moves only when a score passes it by 14 (in log2): P <= 2^14, and fp16 ends at 2^16
+// (with 8 the moves, each some 2,000 clocks, cost 7% more on 32 K tokens and 1% on 128 K).  The four
 // warps that share a row's tokens agree by one barrier, whose answer is read when the exponentials are
 // formed already; a move rescales O in TMEM.
 //
@@ -38,9 +39,10 @@
 // (1.26 us): the schedulers issue in 72% of their clocks, the pipe of logic, maxima and half precision (one
 // warp instruction in two clocks) is busy for 49%, the tensor pipe for 16%, DRAM reads each byte once.  No
 // part stands out: with its exponentials, its stores of P or the values' stores to TMEM left out the kernel
-// takes as long within 2%, without the keys' stores 3 to 8% less.  8 softmax warps of 32 rows execute 7,900
-// instructions a tile at 58% and take 2.5% longer.  Measured: 64 nodes of 4 heads on 32 K tokens 107 us (322
-// TFLOP/s), 16 nodes of 8 heads on 4 x 128 K tokens 853 us (242 TFLOP/s).
+// takes as long within 2%, without the keys' stores 3 to 8% less.  8 softmax warps of 32 rows executed 7,900
+// instructions a tile at 58% and took 2.5% longer.  Measured: 64 nodes of 4 heads on 32 K tokens 104 us (330
+// TFLOP/s), 16 nodes of 8 heads on 4 x 128 K tokens 877 us (235 TFLOP/s); a power of two a row, not a CTA, is 4%
+// of that (a query may be of any size beside its neighbours').
 // What those figures hang on:
 //   * MMAs are issued from code that the whole warp runs, by one elected lane: from a divergent branch each
 //     costs 53 clocks at least, whatever N is;
@@ -76,6 +78,7 @@ constexpr int kStages = 4;                       // page tiles in flight
 constexpr int kRegsLaunch = 64, kRegsSoftmax = 72, kRegsKeys = 64, kRegsValues = 56, kRegsIssue = 48;
 static_assert(32 * kSmWarps * kRegsSoftmax + 128 * kRegsKeys + 256 * kRegsValues + 128 * kRegsIssue <= kThreadsT * kRegsLaunch, "register split");
 
+constexpr float kRefSlack = 14.f;                // log2 of the largest P before a row's reference moves
 constexpr int kWinCost = 3;                      // a window tile's time in page tiles'
 constexpr long long kSmallCall = 1 << 19;        // row_kernel(): rows x kv heads x tokens
 constexpr int kRec = 4 + kHeadDim;               // (m, l, -, -, o[d]) of a partial
@@ -227,6 +230,13 @@ __device__ __forceinline__ void tm_st_frag2(uint32_t a, const uint32_t (&v)[4]) 
   asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%4], {%0,%1,%2,%3};" ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(a)
                : "memory");
 }
+// a s f + c for two float32 at once
+__device__ __forceinline__ void scale2(float& a, float& b, float s, float fa, float fb, float ca, float cb) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n mul.rn.f32x2 x, x, y;\n mov.b64 y, {%3, %4};\n"
+      " mov.b64 z, {%5, %6};\n fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(a), "+f"(b)
+      : "f"(s), "f"(fa), "f"(fb), "f"(ca), "f"(cb));
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
@@ -327,11 +337,12 @@ struct TreeShared {
   int jump[kNodes];                // (while they are found: the next one)
   int whole[kStages];              // every page of the tile is there in whole
   int row[N];                      // output rows: global row * Hq + query head
-  float amax[kSmWarps];
+  __align__(16) float mul[2][N];   // scores' factors of every row: page tiles, window tiles
+  int sigma[N];                    // q' in fp16 is 2^sigma q'
 };
 
 static_assert(kNodeWords == 4 && offsetof(TreeShared, seen) % 16 == 0 && offsetof(TreeShared, neg_m) % 16 == 0 &&
-                  offsetof(TreeShared, alpha) % 16 == 0 && Layout::kEnd % 1024 == 0,
+                  offsetof(TreeShared, alpha) % 16 == 0 && offsetof(TreeShared, mul) % 16 == 0 && Layout::kEnd % 1024 == 0,
               "vector loads");
 static_assert(Layout::kEnd + sizeof(TreeShared) <= 227 * 1024, "shared memory of an SM");
 
@@ -873,7 +884,6 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     const int c0 = share * kCols, tok = 32 * q + lane;
     // q' operands first (these threads): bf16 rows, 16-byte chunk j of row c in slab j / 8, swizzled
     auto at = [&](int c, int j) { return (j >> 3) * N * 128 + (c >> 3) * 1024 + (c & 7) * 128 + (((j & 7) ^ (c & 7)) << 4); };
-    int sigma = 0;
     {
       if (tid < N) {
         const int r = row0 + tid;
@@ -881,8 +891,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         S.neg_m[tid] = 0.f;
       }
       softmax_sync();
-      float amax = 0.f;
-#pragma unroll 4
+      // 16 lanes a row: bf16 as it is, for the windows; fp16 times a power of two of the row, channel slot s
+      // scaled by 4^-s for the codes that carry 4^s
+#pragma unroll 2
       for (int i = tid; i < N * 16; i += 32 * kSmWarps) {
         const int c = i >> 4, j = i & 15;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -890,21 +901,16 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         *reinterpret_cast<uint4*>(sm + L::kQb + at(c, j)) = v;
         // (the largest magnitude: bf16 patterns without the sign compare as integers)
         const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-        amax = fmaxf(amax, __uint_as_float(max(m << 16, m & 0xffff0000u)));
-      }
+        uint32_t top = max(m << 16, m & 0xffff0000u);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      if (lane == 0) S.amax[warp] = amax;
-      softmax_sync();
-#pragma unroll
-      for (int w = 0; w < kSmWarps; ++w) amax = fmaxf(amax, S.amax[w]);
-      // amax 2^sigma < 2^14
-      if (amax > 0.f && amax < INFINITY) sigma = min(100, 14 - ((int)(__float_as_uint(amax) >> 23) - 126));
-      // fp16 rows, channel slot s scaled by 4^-s for the codes that carry 4^s
-#pragma unroll 2
-      for (int i = tid; i < N * 16; i += 32 * kSmWarps) {
-        const int c = i >> 4, j = i & 15;
-        const uint4 v = lds16(sm + L::kQb + at(c, j));
+        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // amax 2^sigma < 2^14 (a row that is not finite stays so)
+        const int sigma = top > 0u && top < 0x7f800000u ? min(100, 14 - ((int)(top >> 23) - 126)) : 0;
+        if (j == 0) {
+          S.sigma[c] = sigma;
+          S.mul[0][c] = P.scale_log2 * ldexpf(1.f, 24 - sigma);
+          S.mul[1][c] = P.scale_log2;
+        }
         const float f = __int_as_float((sigma - 2 * slot_pow(j >> 1) + 127) << 23);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t o[4];
@@ -912,10 +918,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         for (int k = 0; k < 4; ++k) o[k] = pack16(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
         *reinterpret_cast<uint4*>(sm + L::kQ + at(c, j)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
+      softmax_sync();
       // zero-point operand, row c: slots 2 g, 2 g + 1: -sum of group g (hi), slot 8 + 2 g: its lo.  Four
       // threads a row, 32 channels each
       if (tid < 4 * N) {
-        const int c = tid >> 2, part = tid & 3;
+        const int c = tid >> 2, part = tid & 3, sigma = S.sigma[c];
         float acc = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -937,7 +944,6 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) bar_arrive(&S.q_full);
     }
-    const float page_scale = P.scale_log2 * ldexpf(1.f, 24 - sigma);
     float l[kCols];
 #pragma unroll
     for (int j = 0; j < kCols; ++j) l[j] = 0.f;
@@ -960,7 +966,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       fence_after();
       const uint32_t ts = tq + kColS + N * (i & 1);
       const bool win = i < nwc;
-      float ls = S.lane_scale[i & 3][tok] * (win ? P.scale_log2 : page_scale);
+      float ls = S.lane_scale[i & 3][tok];
+      const float* mul = S.mul[win] + c0;                   // the rows' factors
       const uint32_t alive = *reinterpret_cast<const uint32_t*>(&S.alive[i & 3][2 * q]);
       // window tiles that reach into the drafts: else every row sees every token
       const bool drafts = win && (n_sink > st.L0 || (t0 + i + 1) * kTile > n_win - st.n);
@@ -990,11 +997,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         // scores less the reference
 #pragma unroll
         for (int j = 0; j < kCols; j += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(&S.neg_m[c0 + j]);
-          x[j] = fmaf(x[j], ls, m.x);
-          x[j + 1] = fmaf(x[j + 1], ls, m.y);
-          x[j + 2] = fmaf(x[j + 2], ls, m.z);
-          x[j + 3] = fmaf(x[j + 3], ls, m.w);
+          const float4 m = *reinterpret_cast<const float4*>(&S.neg_m[c0 + j]), f = *reinterpret_cast<const float4*>(mul + j);
+          scale2(x[j], x[j + 1], ls, f.x, f.y, m.x, m.y);
+          scale2(x[j + 2], x[j + 3], ls, f.z, f.w, m.z, m.w);
         }
         if (masked) {
 #pragma unroll
@@ -1010,7 +1015,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
             for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
           // (kCols is 4 past a multiple of 8 from 12 on: the last four)
           const bool over = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], x[kCols - 4], x[kCols - 3]),
-                                 fmaxf(x[kCols - 2], x[kCols - 1])) > 8.f;
+                                 fmaxf(x[kCols - 2], x[kCols - 1])) > kRefSlack;
           // one vote of the four warps, taken while the exponentials are already formed
           const bool any = __any_sync(0xffffffffu, over) || force;
           if (lane == 0) {
@@ -1034,7 +1039,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
           tm_ld8(ts + c0 + j, y);
           const uint32_t bits = see >> j;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = (bits >> e) & 1u ? y[e] * ls : -INFINITY;
+          for (int e = 0; e < 8; ++e) y[e] = (bits >> e) & 1u ? y[e] * ls * mul[j + e] : -INFINITY;
           const float top = reduce_columns(y, lane, [](float a, float b2) { return fmaxf(a, b2); });
           if (lane < 8) S.red[q][c0 + j + lane] = top;
         }

@@ -208,6 +208,23 @@ def test_a_draft_that_is_not_finite_reaches_the_nodes_that_see_it_only(counts, s
                 assert ((o[:g].float() - c[:g].float()).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("counts", [[6], [16, 20, 16, 30]], ids=["narrow", "wide"])
+@pytest.mark.parametrize("factor", [1e20, 1e-20, float("inf"), float("nan")])
+def test_queries_of_one_node_do_not_reach_the_others(counts, factor):
+    w = BASE.replace(batch=len(counts), ctx_lo=500, ctx_hi=700)
+    run, q, cu, parent = _drafted(w, counts, "random", seed=6)
+    odd = [int(cu[b]) + 4 for b in range(len(counts))]   # node 4 of every sequence, two of its heads
+    q[odd, 1::2] *= factor
+    out = _call(run, q, cu, parent)
+    assert int(run.runner.status.item()) == 0
+    # the others against float64, and the odd rows where they are finite and small
+    clean = q.clone()
+    if factor != 1e-20:
+        clean[odd] = 0
+        out[odd] = _call(run, clean, cu, parent)[odd]
+    _compare(run, clean, cu, parent, out, [(b, h) for b in range(len(counts)) for h in (0, 7)])
+
+
 @pytest.mark.parametrize("counts", [[6], [40, 33]], ids=["narrow", "wide"])
 def test_pages_beyond_4_gib(counts):
     w = BASE.replace(batch=len(counts), ctx_lo=900, ctx_hi=1100)
