@@ -86,8 +86,8 @@ struct VerifyParams {
 constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
 // CTAs per sequence.  Most sequences need one sum over their row, a few need one for every missed child, and
-// those are what the call waits for: 64 trees over 152 K tokens take 81 us with 16 x 256 threads to a
-// sequence, 89 us with 8 x 512 (before the sums of limbs).
+// those are what the call waits for: 64 trees over 152 K tokens take 71 us with 16 x 256 threads to a
+// sequence, 86 us with 8 x 512, 80 us with 16 x 192, 97 us with 16 x 384.
 constexpr int kVCluster = 16;
 constexpr int kVChunk = 128;         // tokens a warp takes at once, 4 a lane
 
