@@ -76,7 +76,6 @@ struct VerifyParams {
   long long p_stride, q_stride;
   int vocab;
   int n_rows;
-  int batch;
   int32_t* path;
   int32_t* n_accept;
   int32_t* next_token;
@@ -545,7 +544,6 @@ extern "C" int kvq_launch_verify_tree(const kvq_config* cfg, const int32_t* cu_r
   P.q_stride = q_stride;
   P.vocab = vocab;
   P.n_rows = n_rows;
-  P.batch = cfg->batch;
   P.path = path;
   P.n_accept = n_accept;
   P.next_token = next_token;
