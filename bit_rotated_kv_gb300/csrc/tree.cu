@@ -1256,18 +1256,18 @@ Shape tree_shape(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
 using namespace kvq;
 
 // Which kernel a call takes, from its sizes alone.  The row kernel (attn.cu) streams a sequence's cache once
-// for every 8 (node, head) columns, this one once for every 64 at four to five times the time: 64 sequences
-// of 6,000 tokens take 80 us a group of 8 there and 366 us a tile of 64 here.  So the row kernel has trees of
-// up to 4 groups a tile (314 against 366 us), of up to 3 on short contexts, where its windows weigh more (64
-// sequences of 1,000 tokens: 121 against 137 us with 3 groups, 153 against 140 with 4).  It has small calls as well: with 32 nodes and 8 kv heads on 500 tokens it takes 17.6 us
-// against 18.9 here, with 16 on 2,000 14.5 against 22.3, but with 64 on 500 28.9 against 26.3 and with 32 on
-// 4,000 30.6 against 24.3.  Per-channel keys are the row kernel's alone.
+// for every 8 (node, head) columns, this one once for every 64 at four to five times the time.  So the row
+// kernel has trees of up to 4 groups a tile: 64 sequences of 6,000 tokens take 331 us there and 376 us here with 4,
+// 394 against 377 with 5.  On short contexts, where its windows weigh more, up to 3: 64 sequences of 1,000
+// tokens take 129 against 137 us with 3, 163 against 138 with 4.  It has small calls as well: 16 nodes on 8
+// kv heads take 14.8 us there and 21.6 us here on 2,000 tokens, 20.2 and 21.8 on 4,000; 32 nodes 19.0 and 18.0 on
+// 500, 30.6 and 22.6 on 4,000.  Per-channel keys are the row kernel's alone.
 static bool row_kernel(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
   if (cfg->key_axis != KVQ_KEY_PER_TOKEN) return true;
   const long long per_seq = ((long long)n_rows * (cfg->n_q_heads / cfg->n_kv_heads) + cfg->batch - 1) / cfg->batch;
   const long long groups = (per_seq + 7) / 8, tiles = (per_seq + N - 1) / N;
   const long long units = (long long)n_rows * cfg->n_kv_heads;
-  return groups <= (max_ctx < 2048 ? 3 : 4) * tiles || (units <= 256 && units * max_ctx <= kSmallCall);
+  return groups <= (max_ctx < 2048 ? 3 : 4) * tiles || (units <= 128 && units * max_ctx <= kSmallCall);
 }
 
 extern "C" size_t kvq_attn_tree_ws_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
