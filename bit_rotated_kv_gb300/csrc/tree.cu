@@ -322,7 +322,7 @@ struct Layout {          // dynamic shared memory, from a 1024-byte boundary
 
 struct TreeShared {
   __align__(16) uint64_t page_full[kStages], page_free[kStages], q_full, seen_full, vote[kShares], meet[kShares], k_full[2], v_full[2], s_full[2], s_free[2], p_full[2],
-      pv_done[2];
+      pv_done[2], win_done;
   uint32_t tmem;
   int gave_up;
   int pid[kStages][kTilePages];
@@ -444,6 +444,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     }
     bar_init(&S.q_full, kSmWarps);
     bar_init(&S.seen_full, 1);
+    bar_init(&S.win_done, 1);
     for (int i = 0; i < kShares; ++i) {
       bar_init(&S.vote[i], 4);
       bar_init(&S.meet[i], 4);
@@ -471,9 +472,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       const int32_t* tab = P.page_table + (size_t)b * P.max_pages;
       int k = 0;                                            // page tiles streamed
       bool ok = true;
-      // the window rows' space is free once the last of their products is done (every one is waited for:
-      // a parity alone says nothing about a phase whose predecessor may not be over)
-      for (int i = 0; ok && i < nwc && nwc < nt; ++i) ok = warp_wait(&S.pv_done[i & 1], i >> 1, gave_up);
+      // the window rows' space is free once the last of their products is done.  (A barrier of its own:
+      // nothing holds PV(i + 2) back until this warp has seen PV(i), so the parity of pv_done could move on
+      // twice while it waits, and the wait would then be for a page tile that only this warp can bring)
+      if (nwc > 0 && nwc < nt) ok = warp_wait(&S.win_done, 0, gave_up);
       for (int i = nwc; ok && i < nt; ++i, ++k) {
         const int stage = k % kStages;
         const int p = (t0 + i - nw) * kTilePages + lane;
@@ -613,6 +615,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
             for (int kk = 0; kk < 8; ++kk) mma_ts(tb + kColO, v + 8 * kk, p + kk * (2048 >> 4), kIdescPV, i > 0 || kk > 0);
           }
         }
+        __syncwarp();
+        if (i == nwc - 1 && elect()) mma_commit(&S.win_done);
         __syncwarp();
         if (elect()) mma_commit(&S.pv_done[i & 1]);
         __syncwarp();
