@@ -24,9 +24,15 @@
 // value and of Delta z: the output's own rounding to bf16 is 2^-8).  P is rounded to fp16, the sums l
 // are fp32.  Window rows are bf16 as they are, with P as a bf16 hi + lo pair.
 //
-// Softmax reference.  m_n moves only when a score passes it by 14 (in log2): P <= 2^14, and fp16 ends at 2^16
-// (with 8 the moves, each some 2,000 clocks, cost 7% more on 32 K tokens and 1% on 128 K).  The four
-// warps that share a row's tokens agree by one barrier, whose answer is read when the exponentials are
+// Softmax reference.  m_n moves only when a score passes it by 15 (in log2): P <= 2^15, and fp16 ends at 2^16.
+// It is set to the row's maximum, or up to 12 below it, as far as the maxima of the tile's four quarters lie apart
+// by more than 8: where one token leads the others by far, they keep up to 36 binades of fp16 below it (a token
+// that takes nearly all of the weight may give nearly nothing, and then the others are the output), and elsewhere
+// the row can grow by 15 before a move, which takes some 2,000 clocks (4 below throughout: 106 us instead of 103.5
+// for 64 nodes on 32 K tokens).  A CTA takes its pages first, then its window rows, whose P is a pair of bf16 and loses
+// nothing beside a reference that is far off: a sink never sets the pages' reference.  (Windows first, reference
+// at the maximum: a sink with a zero value row that leads by 20 nats left nothing of the pages' output.)  The
+// four warps that share a row's tokens agree by one barrier, whose answer is read when the exponentials are
 // formed already; a move rescales O in TMEM.
 //
 // Roles: 16 softmax warps (4 lane quadrants x 4 shares of the rows), 4 warps that expand keys (or load window
@@ -41,7 +47,7 @@
 // part stands out: with its exponentials, its stores of P or the values' stores to TMEM left out the kernel
 // takes as long within 2%, without the keys' stores 3 to 8% less.  8 softmax warps of 32 rows executed 7,900
 // instructions a tile at 58% and took 2.5% longer.  Measured: 64 nodes of 4 heads on 32 K tokens 104 us (330
-// TFLOP/s), 16 nodes of 8 heads on 4 x 128 K tokens 877 us (235 TFLOP/s); a power of two a row, not a CTA, is 4%
+// TFLOP/s), 16 nodes of 8 heads on 4 x 128 K tokens 905 us (228 TFLOP/s); a power of two a row, not a CTA, is 4%
 // of that (a query may be of any size beside its neighbours').
 // What those figures hang on:
 //   * MMAs are issued from code that the whole warp runs, by one elected lane: from a divergent branch each
@@ -78,8 +84,10 @@ constexpr int kStages = 4;                       // page tiles in flight
 constexpr int kRegsLaunch = 64, kRegsSoftmax = 72, kRegsKeys = 64, kRegsValues = 56, kRegsIssue = 48;
 static_assert(32 * kSmWarps * kRegsSoftmax + 128 * kRegsKeys + 256 * kRegsValues + 128 * kRegsIssue <= kThreadsT * kRegsLaunch, "register split");
 
-constexpr float kRefSlack = 14.f;                // log2 of the largest P before a row's reference moves
-constexpr int kWinCost = 3;                      // a window tile's time in page tiles'
+// log2 of the largest P before a row's reference moves: page tiles (fp16), window tiles (bf16 pairs); a lead that
+// is ordinary, and how far below the maximum a reference is set at most
+constexpr float kRefSlack = 15.f, kWinSlack = 30.f, kRefLead = 8.f, kRefBelow = 12.f;
+constexpr int kWinCost = 4;                      // a window tile's time in page tiles'
 constexpr long long kSmallCall = 1 << 19;        // row_kernel(): rows x kv heads x tokens
 constexpr int kRec = 4 + kHeadDim;               // (m, l, -, -, o[d]) of a partial
 constexpr int kSpin = 1 << 15, kSuspend = 20000;  // a wait gives up after that many rounds of at most 20 us
@@ -311,8 +319,7 @@ struct Layout {          // dynamic shared memory, from a 1024-byte boundary
   static constexpr int kPBytes = N / 64 * kSlab;
   static constexpr int kZ = kP + 2 * kPBytes;               // zero-point B operand: N x 16 fp16
   static constexpr int kZa = kZ + N * 32;                   // ... and A: 128 tokens x 16 fp16, two buffers
-  // window K and V rows, two slabs each; where a CTA's window tiles are done (or it has none), the
-  // page stages
+  // window K and V rows, two slabs each; before them, while a CTA has page tiles, the page stages
   static constexpr int kK = (kZa + 2 * kTile * 32 + 1023) / 1024 * 1024;
   static constexpr int kV = kK + 2 * kSlab;
   static constexpr int kPages = kK;
@@ -322,7 +329,7 @@ struct Layout {          // dynamic shared memory, from a 1024-byte boundary
 
 struct TreeShared {
   __align__(16) uint64_t page_full[kStages], page_free[kStages], q_full, seen_full, vote[kShares], meet[kShares], k_full[2], v_full[2], s_full[2], s_free[2], p_full[2],
-      pv_done[2], win_done;
+      pv_done[2];
   uint32_t tmem;
   int gave_up;
   int pid[kStages][kTilePages];
@@ -408,7 +415,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     return;
   }
 
-  // ---- tiles: window rows (sink, then ring) first, then pages
+  // ---- tiles: pages first, then window rows (sink, then ring)
   const int edge = min(st.edge, st.len);
   const int n_sink = min(P.s_sink, st.len), ring0 = max(edge, P.s_sink);
   const int n_win = n_sink + max(0, st.len - ring0);
@@ -423,7 +430,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
   // streamed, and its P is a pair)
   auto first_tile = [&](int k) {
     const int at = (int)((long long)(kWinCost * nw + ni) * k / P.splits);
-    return at < kWinCost * nw ? (at + kWinCost - 1) / kWinCost : nw + at - kWinCost * nw;
+    return at < ni ? at : ni + (at - ni + kWinCost - 1) / kWinCost;
   };
   const int t0 = first_tile(split), t1 = first_tile(split + 1);
   const int nt = t1 - t0;
@@ -444,7 +451,6 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     }
     bar_init(&S.q_full, kSmWarps);
     bar_init(&S.seen_full, 1);
-    bar_init(&S.win_done, 1);
     for (int i = 0; i < kShares; ++i) {
       bar_init(&S.vote[i], 4);
       bar_init(&S.meet[i], 4);
@@ -463,7 +469,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
   const uint32_t tb = S.tmem;
 
   const int pb = P.page_bytes;
-  const int nwc = max(0, min(t1, nw) - t0);                 // this CTA's window tiles: its first ones
+  const int npt = max(0, min(t1, ni) - t0);                 // this CTA's page tiles: its first ones
   uint8_t* stages = sm + L::kPages;
   if (warp >= kQkWarp) {
     regs_dec<kRegsIssue>();
@@ -471,14 +477,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       // ---- pages
       const int32_t* tab = P.page_table + (size_t)b * P.max_pages;
       int k = 0;                                            // page tiles streamed
-      bool ok = true;
-      // the window rows' space is free once the last of their products is done.  (A barrier of its own:
-      // nothing holds PV(i + 2) back until this warp has seen PV(i), so the parity of pv_done could move on
-      // twice while it waits, and the wait would then be for a page tile that only this warp can bring)
-      if (nwc > 0 && nwc < nt) ok = warp_wait(&S.win_done, 0, gave_up);
-      for (int i = nwc; ok && i < nt; ++i, ++k) {
+      for (; k < npt; ++k) {
         const int stage = k % kStages;
-        const int p = (t0 + i - nw) * kTilePages + lane;
+        const int p = (t0 + k) * kTilePages + lane;
         int pid = -1;
         if (lane < kTilePages && p < np) {
           pid = p < P.max_pages ? tab[p] : -1;
@@ -487,13 +488,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
             set_status(P.status, KVQ_ERR_BOUNDS);
           }
         }
-        if (k >= kStages) {
-          ok = warp_wait(&S.page_free[stage], k / kStages - 1, gave_up);
-          if (!ok) break;
-        }
+        if (k >= kStages && !warp_wait(&S.page_free[stage], k / kStages - 1, gave_up)) break;
         if (lane < kTilePages) S.pid[stage][lane] = pid;
         const int live = __popc(__ballot_sync(0xffffffffu, pid >= 0));
-        if (lane == 0) S.whole[stage] = live == kTilePages && n_tok >= kPage * ((t0 + i - nw + 1) * kTilePages);
+        if (lane == 0) S.whole[stage] = live == kTilePages && n_tok >= kPage * ((t0 + k + 1) * kTilePages);
         __syncwarp();
         if (lane == 0) {
           if (live) bar_expect(&S.page_full[stage], (uint32_t)(live * pb));
@@ -564,7 +562,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         if (!ok) break;
         fence_after();
         const uint32_t ts = tb + kColS + N * (i & 1);
-        if (i < nwc) {
+        if (i >= npt) {
           const uint64_t k_d = desc_k128(saddr(sm + L::kK)), qb_d = desc_k128(saddr(sm + L::kQb));
 #pragma unroll 1
           for (int s = 0; s < 8; ++s)
@@ -599,7 +597,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         ok = warp_wait(&S.v_full[i & 1], i >> 1, gave_up) && warp_wait(&S.p_full[i & 1], i >> 1, gave_up);
         if (!ok) break;
         fence_after();
-        if (i < nwc) {
+        if (i >= npt) {
           const uint64_t v_d = desc_mn128(saddr(sm + L::kV));
 #pragma unroll 1
           for (int kk = 0; kk < 8; ++kk)
@@ -616,8 +614,6 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
           }
         }
         __syncwarp();
-        if (i == nwc - 1 && elect()) mma_commit(&S.win_done);
-        __syncwarp();
         if (elect()) mma_commit(&S.pv_done[i & 1]);
         __syncwarp();
       }
@@ -626,67 +622,27 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
   } else if (warp >= kKeyWarp) {
     if (warp < kValWarp) regs_dec<kRegsKeys>();
     else regs_dec<kRegsValues>();
-    // ---- operands of a tile, lane quadrant q of TMEM.  Window tiles: 128 threads copy the rows
-    // into swizzled shared memory, 16 lanes a row
+    // ---- operands of a tile, lane quadrant q of TMEM.  Window tiles: the threads copy the rows into
+    // swizzled shared memory, 16 lanes a row
     const bool keys = warp < kValWarp;
     const int q = warp & 3, t = tid - 32 * (keys ? kKeyWarp : kValWarp);
     const int row = lane >> 2, quad = lane & 3;
     const uint32_t tq = tb + ((uint32_t)(32 * q) << 16);
     bool ok = true;
-    for (int i = 0; i < nwc; ++i) {
-      const int w0 = (t0 + i) * kTile;
-      // keys once QK(i - 1) has read the last ones, values once PV(i - 1) has
-      if (i > 0) ok = warp_wait(keys ? &S.s_full[(i - 1) & 1] : &S.pv_done[(i - 1) & 1], (i - 1) >> 1, gave_up);
-      if (!ok) break;
-      const uint16_t* sink = keys ? P.sink_k : P.sink_v;
-      const uint16_t* ring = keys ? P.ring_k : P.ring_v;
-      uint8_t* dst = sm + (keys ? L::kK : L::kV);
-      const int j = t & 15;
-#pragma unroll 4
-      for (int r = t >> 4; r < kTile; r += 2 * (keys ? kKeyWarps : kValWarps)) {
-        const int w = min(w0 + r, n_win - 1);
-        const int tok = w < n_sink ? w : ring0 + w - n_sink;
-        const uint16_t* src = w < n_sink ? sink + (((size_t)b * P.hkv + h) * P.s_sink + tok) * kHeadDim
-                                         : ring + (((size_t)b * P.hkv + h) * P.ring_cap + tok % P.ring_cap) * kHeadDim;
-        // (zeros for rows behind the last: 0 bytes are read)
-        async_copy16(dst + (j >> 3) * kSlab + (r >> 3) * 1024 + (r & 7) * 128 + (((j & 7) ^ (r & 7)) << 4), src + 8 * j,
-                     w0 + r < n_win ? 16 : 0);
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if (!keys && (n_sink > st.L0 || w0 + kTile > n_win - st.n)) {
-        // drafts: a value row that is not finite is taken out here (0 x NaN would reach rows that do not see
-        // it) and the softmax makes the rows that see it NaN
-#pragma unroll 1
-        for (int r = t >> 4; r < kTile; r += 2 * kValWarps) {
-          uint4* at = reinterpret_cast<uint4*>(dst + (j >> 3) * kSlab + (r >> 3) * 1024 + (r & 7) * 128 + (((j & 7) ^ (r & 7)) << 4));
-          const uint4 v = *at;
-          const int tok = w0 + r < n_sink ? w0 + r : ring0 + w0 + r - n_sink;
-          const bool inf = tok >= st.L0 && (bf16_pair_odd(v.x) || bf16_pair_odd(v.y) || bf16_pair_odd(v.z) || bf16_pair_odd(v.w));
-          const bool any = (__ballot_sync(0xffffffffu, inf) >> (lane & 16)) & 0xffffu;
-          if (any) *at = make_uint4(0u, 0u, 0u, 0u);
-          if (j == 0) S.v_odd[i & 1][r] = any;
-        }
-      }
-      if (keys) {
-        S.lane_scale[i & 3][t] = 1.f;
-        const unsigned alive = __ballot_sync(0xffffffffu, w0 + t < n_win);
-        if (lane == 0) {
-          S.alive[i & 3][2 * q] = (uint16_t)alive;
-          S.alive[i & 3][2 * q + 1] = (uint16_t)(alive >> 16);
-        }
-      }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) bar_arrive(keys ? &S.k_full[i & 1] : &S.v_full[i & 1]);
-    }
+    // products up to tile `last` are done, QK's for keys, PV's for values; waited for one after the other (a
+    // parity alone says nothing about a phase whose predecessor may not be over)
+    int seen_products = 0;
+    auto products = [&](int last) {
+      for (; ok && seen_products <= last; ++seen_products)
+        ok = warp_wait(keys ? &S.s_full[seen_products & 1] : &S.pv_done[seen_products & 1], seen_products >> 1, gave_up);
+    };
     if (keys) {
       // ---- keys: tokens 32 q .. 32 q + 31 of a tile, pages 2 q and 2 q + 1
-      int k = 0;
-      for (int i = nwc; ok && i < nt; ++i, ++k) {
-        const int stage = k % kStages;
-        const int page0 = (t0 + i - nw) * kTilePages;
-        ok = warp_wait(&S.page_full[stage], k / kStages, gave_up);
-        if (ok && i >= kKBufs) ok = warp_wait(&S.s_full[(i - kKBufs) & 1], (i - kKBufs) >> 1, gave_up);
+      for (int i = 0; i < npt; ++i) {
+        const int stage = i % kStages;
+        const int page0 = (t0 + i) * kTilePages;
+        ok = warp_wait(&S.page_full[stage], i / kStages, gave_up);
+        products(i - kKBufs);
         if (!ok) break;
         fence_after();
         const uint8_t* base = stages + (size_t)stage * kTilePages * pb;
@@ -813,12 +769,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         mask[j] = 0x00030003u << (2 * sp);
         one[j] = (uint32_t)(25 - 2 * sp) * 0x04000400u;     // 2^(10 - 2 sp): the code's bits then count ones
       }
-      int k = 0;
 #pragma unroll 1
-      for (int i = nwc; ok && i < nt; ++i, ++k) {
-        const int stage = k % kStages;
-        ok = warp_wait(&S.page_full[stage], k / kStages, gave_up);
-        if (ok && i >= kVBufs) ok = warp_wait(&S.pv_done[(i - kVBufs) & 1], (i - kVBufs) >> 1, gave_up);
+      for (int i = 0; i < npt; ++i) {
+        const int stage = i % kStages;
+        ok = warp_wait(&S.page_full[stage], i / kStages, gave_up);
+        products(i - kVBufs);
         if (!ok) break;
         fence_after();
         const uint8_t* pgp = stages + (size_t)(stage * kTilePages + 4 * pages) * pb;
@@ -856,7 +811,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
             }
           if (!whole) {                                     // dead tokens: zeros, whatever the page holds there
             const int at = 4 * pages + pg;
-            const int valid = S.pid[stage][at] < 0 ? 0 : max(0, min(kPage, n_tok - kPage * ((t0 + i - nw) * kTilePages + at)));
+            const int valid = S.pid[stage][at] < 0 ? 0 : max(0, min(kPage, n_tok - kPage * ((t0 + i) * kTilePages + at)));
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               const int tk = 2 * quad + 8 * y;
@@ -879,6 +834,55 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
           bar_arrive(&S.page_free[stage]);
         }
       }
+    }
+    // ---- window tiles: the rows take the page stages' space, once every warp has read the last pages
+    for (int k = max(0, npt - kStages); ok && nt > npt && k < npt; ++k) ok = warp_wait(&S.page_free[k % kStages], k / kStages, gave_up);
+#pragma unroll 1
+    for (int i = npt; ok && i < nt; ++i) {
+      const int w0 = (t0 + i - ni) * kTile;
+      // keys once QK(i - 1) has read the last window rows, values once PV(i - 1) has
+      products(i > npt ? i - 1 : i - 2);
+      if (!ok) break;
+      const uint16_t* sink = keys ? P.sink_k : P.sink_v;
+      const uint16_t* ring = keys ? P.ring_k : P.ring_v;
+      uint8_t* dst = sm + (keys ? L::kK : L::kV);
+      const int j = t & 15;
+#pragma unroll 4
+      for (int r = t >> 4; r < kTile; r += 2 * (keys ? kKeyWarps : kValWarps)) {
+        const int w = min(w0 + r, n_win - 1);
+        const int tok = w < n_sink ? w : ring0 + w - n_sink;
+        const uint16_t* src = w < n_sink ? sink + (((size_t)b * P.hkv + h) * P.s_sink + tok) * kHeadDim
+                                         : ring + (((size_t)b * P.hkv + h) * P.ring_cap + tok % P.ring_cap) * kHeadDim;
+        // (zeros for rows behind the last: 0 bytes are read)
+        async_copy16(dst + (j >> 3) * kSlab + (r >> 3) * 1024 + (r & 7) * 128 + (((j & 7) ^ (r & 7)) << 4), src + 8 * j,
+                     w0 + r < n_win ? 16 : 0);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!keys && (n_sink > st.L0 || w0 + kTile > n_win - st.n)) {
+        // drafts: a value row that is not finite is taken out here (0 x NaN would reach rows that do not see
+        // it) and the softmax makes the rows that see it NaN
+#pragma unroll 1
+        for (int r = t >> 4; r < kTile; r += 2 * kValWarps) {
+          uint4* at = reinterpret_cast<uint4*>(dst + (j >> 3) * kSlab + (r >> 3) * 1024 + (r & 7) * 128 + (((j & 7) ^ (r & 7)) << 4));
+          const uint4 v = *at;
+          const int tok = w0 + r < n_sink ? w0 + r : ring0 + w0 + r - n_sink;
+          const bool inf = tok >= st.L0 && (bf16_pair_odd(v.x) || bf16_pair_odd(v.y) || bf16_pair_odd(v.z) || bf16_pair_odd(v.w));
+          const bool any = (__ballot_sync(0xffffffffu, inf) >> (lane & 16)) & 0xffffu;
+          if (any) *at = make_uint4(0u, 0u, 0u, 0u);
+          if (j == 0) S.v_odd[i & 1][r] = any;
+        }
+      }
+      if (keys) {
+        S.lane_scale[i & 3][t] = 1.f;
+        const unsigned alive = __ballot_sync(0xffffffffu, w0 + t < n_win);
+        if (lane == 0) {
+          S.alive[i & 3][2 * q] = (uint16_t)alive;
+          S.alive[i & 3][2 * q + 1] = (uint16_t)(alive >> 16);
+        }
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) bar_arrive(keys ? &S.k_full[i & 1] : &S.v_full[i & 1]);
     }
   } else {
     regs_inc<kRegsSoftmax>();
@@ -954,7 +958,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     bool lost = false;
     bool unseen = true;                                     // row c0 + lane % kCols has seen no token yet
     bool force = true;                                      // ... there are such rows (all four warps agree)
-    int meets = 0;
+    int meets = 0, pv_seen = 0;
+    auto pv_until = [&](int last) {                         // products with V up to tile `last` are done
+      for (; pv_seen <= last; ++pv_seen)
+        if (!warp_wait(&S.pv_done[pv_seen & 1], pv_seen >> 1, gave_up)) lost = true;
+    };
     // the share's four warps meet (bounded, so that a warp that gave up leaves nobody behind)
     auto meet = [&]() {
       __syncwarp();
@@ -969,20 +977,21 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       }
       fence_after();
       const uint32_t ts = tq + kColS + N * (i & 1);
-      const bool win = i < nwc;
+      const bool win = i >= npt;
       float ls = S.lane_scale[i & 3][tok];
       const float* mul = S.mul[win] + c0;                   // the rows' factors
       const uint32_t alive = *reinterpret_cast<const uint32_t*>(&S.alive[i & 3][2 * q]);
       // window tiles that reach into the drafts: else every row sees every token
-      const bool drafts = win && (n_sink > st.L0 || (t0 + i + 1) * kTile > n_win - st.n);
+      const bool drafts = win && (n_sink > st.L0 || (t0 + i - ni + 1) * kTile > n_win - st.n);
       const bool masked = drafts || alive != 0xffffffffu;
       uint32_t see = 0xffffffffu;                           // rows that see this token
       if (masked) {
         if (drafts) {
+          pv_until(i - 2);                                  // (and so V(i - 2) has been there: see products())
           if (!warp_wait(&S.seen_full, 0, gave_up) || !warp_wait(&S.v_full[i & 1], i >> 1, gave_up)) lost = true;
           if (S.v_odd[i & 1][tok]) ls = __int_as_float(0x7fffffff);   // (see where the values are loaded)
         }
-        const int w = (t0 + i) * kTile + tok;
+        const int w = (t0 + i - ni) * kTile + tok;
         const int node = win ? (w < n_sink ? w : ring0 + w - n_sink) - st.L0 : -1;
         see = (alive >> lane) & 1u ? 0xffffffffu : 0u;
         if (see && drafts && node >= 0) {
@@ -1019,7 +1028,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
             for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[j + e], x[j + 4 + e]);
           // (kCols is 4 past a multiple of 8 from 12 on: the last four)
           const bool over = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], x[kCols - 4], x[kCols - 3]),
-                                 fmaxf(x[kCols - 2], x[kCols - 1])) > kRefSlack;
+                                 fmaxf(x[kCols - 2], x[kCols - 1])) > (win ? kWinSlack : kRefSlack);
           // one vote of the four warps, taken while the exponentials are already formed
           const bool any = __any_sync(0xffffffffu, over) || force;
           if (lane == 0) {
@@ -1050,9 +1059,12 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         meet();
         const int c = c0 + lane % kCols;
         const float up = fmaxf(fmaxf(S.red[0][c], S.red[1][c]), fmaxf(S.red[2][c], S.red[3][c]));
-        // a first token sets the reference, later ones only raise it
+        const float low = fminf(fminf(S.red[0][c], S.red[1][c]), fminf(S.red[2][c], S.red[3][c]));
+        // a first token sets the reference, later ones only raise it; how far below the maximum: see the
+        // head of this file
         const bool any = up > -INFINITY;
-        const float old = -S.neg_m[c], now = unseen ? (any ? up : 0.f) : fmaxf(old, up);
+        const float ref = up - fminf(fmaxf(up - low - kRefLead, 0.f), kRefBelow);
+        const float old = -S.neg_m[c], now = unseen ? (any ? ref : 0.f) : fmaxf(old, ref);
         if (q == 0) S.alpha[c] = unseen ? 0.f : ex2(old - now);
         if (any) unseen = false;
         force = __any_sync(0xffffffffu, unseen);
@@ -1084,9 +1096,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(&S.s_free[i & 1]);
-      // P buffer free: PV(i - 2), or PV(i - 1) around window tiles (which use both buffers)
-      const int before = (win || (i > 0 && i - 1 < nwc)) ? i - 1 : i - 2;
-      if (before >= 0 && !warp_wait(&S.pv_done[before & 1], before >> 1, gave_up)) lost = true;
+      // P buffer free: PV(i - 2), or PV(i - 1) for window tiles (which use both buffers)
+      pv_until(win ? i - 1 : i - 2);
       // P[token][row], 8 rows a chunk of 16 bytes: a lane's chunks are 16 (j ^ (token % 8)) apart
       const uint32_t p_s = saddr(sm + L::kP) + (c0 >> 6) * kSlab + (tok >> 3) * 1024 + (tok & 7) * 128;
       const uint32_t sw = (uint32_t)(((c0 & 63) >> 3) ^ (tok & 7)) << 4;

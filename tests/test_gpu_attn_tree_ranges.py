@@ -7,6 +7,7 @@ rounding of the output) plus the attention parity tolerance of 2e-3 of the row's
 import pytest
 import torch
 
+from tests import spec_ref
 from tests.test_gpu_attn_tree import BASE, _call, _compare, _drafted
 
 pytestmark = pytest.mark.gpu
@@ -27,3 +28,77 @@ def test_window_tiles_and_page_tiles_of_one_cta(keep):
     for _ in range(20):
         assert torch.equal(_call(run, q, cu, parent).view(torch.int16), first.view(torch.int16))
     assert int(run.runner.status.item()) == 0
+
+
+def _heads(w, h):
+    return slice(h * w.gqa, (h + 1) * w.gqa)
+
+
+def _rows(cu, b):
+    return slice(int(cu[b]), int(cu[b + 1]))
+
+
+WEIGHT_SHAPES = {
+    "one_split": (ONE_SPLIT.replace(ctx_lo=7900, ctx_hi=8000), [64] * 19),
+    "one_split_g32": (ONE_SPLIT.replace(ctx_lo=7900, ctx_hi=8000, group_size=32), [64] * 19),
+    "splits": (BASE.replace(batch=1, n_q_heads=8, n_kv_heads=2, ctx_lo=32000, ctx_hi=32000), [64]),
+    "narrow": (BASE.replace(batch=1, n_q_heads=8, n_kv_heads=2, ctx_lo=8000, ctx_hi=8000), [6]),
+}
+
+
+@pytest.mark.parametrize("lead", [13.3, 15.7, 18.0, 20.0, 24.0])
+@pytest.mark.parametrize("shape", sorted(WEIGHT_SHAPES))
+def test_a_sink_takes_the_weight_and_gives_nothing(shape, lead):
+    """Token 0's key agrees with every query by `lead` nats, and its value row is zero: the output is what the
+    other tokens leave (at 13.3 nats a tenth of the weight on 32 K tokens, at 24 nats 2 in 10^6)."""
+    w, counts = WEIGHT_SHAPES[shape]
+    run, q, cu, parent = _drafted(w, counts, "random")
+    c, scale, gen = run.runner.cache, run.runner.sm_scale, torch.Generator("cuda").manual_seed(9)
+    for b in range(w.batch):
+        for h in range(w.n_kv_heads):
+            u = torch.randn(128, generator=gen, device="cuda")
+            u /= u.norm()
+            q[_rows(cu, b), _heads(w, h)] += (8 * u).to(torch.bfloat16)
+            c.sink_k[b, h, 0] = (u * (lead / (8 * scale))).to(torch.bfloat16)
+    c.sink_v[:, :, 0] = 0
+    out = _call(run, q, cu, parent)
+    assert int(run.runner.status.item()) == 0
+    _compare(run, q, cu, parent, out, [(0, 0), (w.batch - 1, 1)])
+
+
+def _key_scales(run):
+    """(Delta16, z16) of every key token and group, [pages, heads, 16, G, 2], a view of the pool."""
+    ng = 128 // run.cfg.group_size
+    p = run.runner.cache.pages
+    return p[:, :, 1024:1024 + 64 * ng].view(torch.float16).unflatten(-1, (16, ng, 2))
+
+
+def _value_deltas(run):
+    """Value Delta16, [pages, heads, 8 token pairs, G, 2], a view of the pool."""
+    ng = 128 // run.cfg.group_size
+    p = run.runner.cache.pages
+    return p[:, :, 1024 + 64 * ng:1024 + 96 * ng].view(torch.float16).unflatten(-1, (8, ng, 2))
+
+
+@pytest.mark.parametrize("where", ["first_page", "middle"])
+@pytest.mark.parametrize("lead", [13.3, 20.0])
+@pytest.mark.parametrize("shape", ["one_split", "one_split_g32", "splits"])
+def test_a_token_of_the_pages_takes_the_weight_and_gives_nothing(shape, lead, where):
+    """The same with a quantized token: every query agrees with it, its key is stretched, its values are zero."""
+    w, counts = WEIGHT_SHAPES[shape]
+    w = w.replace(s_sink=0)
+    run, q, cu, parent = _drafted(w, counts, "random")
+    scale, snap = run.runner.sm_scale, run.snapshot()
+    keys, dv = _key_scales(run), _value_deltas(run)
+    for b in range(w.batch):
+        t = 0 if where == "first_page" else int(snap["s_quant"][b]) // 2
+        pid = int(run.table[b, t // 16])
+        for h in range(w.n_kv_heads):
+            k = torch.from_numpy(spec_ref.unit_kv(run.cfg, snap, run.table, b, h)[0][t]).cuda()
+            norm = float(k.norm())
+            q[_rows(cu, b), _heads(w, h)] += (8 * k / norm).to(torch.bfloat16)
+            keys[pid, h, t % 16, :, 0] *= lead / (8 * norm * scale)
+            dv[pid, h, t % 16 // 2, :, t % 2] = 0
+    out = _call(run, q, cu, parent)
+    assert int(run.runner.status.item()) == 0
+    _compare(run, q, cu, parent, out, [(0, 0), (w.batch - 1, 1)])
