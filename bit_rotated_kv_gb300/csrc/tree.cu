@@ -47,7 +47,7 @@
 // part stands out: with its exponentials, its stores of P or the values' stores to TMEM left out the kernel
 // takes as long within 2%, without the keys' stores 3 to 8% less.  8 softmax warps of 32 rows executed 7,900
 // instructions a tile at 58% and took 2.5% longer.  Measured: 64 nodes of 4 heads on 32 K tokens 104 us (330
-// TFLOP/s), 16 nodes of 8 heads on 4 x 128 K tokens 905 us (228 TFLOP/s); a power of two a row, not a CTA, is 4%
+// TFLOP/s), 16 nodes of 8 heads on 4 x 128 K tokens 915 us (225 TFLOP/s); a power of two a row, not a CTA, is 4%
 // of that (a query may be of any size beside its neighbours').
 // What those figures hang on:
 //   * MMAs are issued from code that the whole warp runs, by one elected lane: from a divergent branch each
@@ -696,9 +696,13 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
               for (int g = 0; g < NG; ++g) dz[g] = *reinterpret_cast<const uint32_t*>(sc + 4 * NG * (row + 8 * x) + 4 * g);
               float dm = 0.f;
 #pragma unroll
-              for (int g = 0; g < NG; ++g) dm = fmaxf(dm, __low2float(bits2h(dz[g])));
-              // largest Delta 2^k in [2^14, 2^15): its product with 3 4^s 2^-24 stays in range, and
-              // a pair hi + lo is exact for groups down to 2^-10 of it
+              for (int g = 0; g < NG; ++g) {
+                const float2 f = __half22float2(bits2h(dz[g]));
+                dm = fmaxf(dm, fmaxf(f.x, fabsf(f.x * f.y) * 0x1p-8f));
+              }
+              // 2^k: the largest Delta 2^k below 2^15, so that its product with 3 4^s 2^-24 stays in range, and the
+              // largest |Delta z| 2^k below 2^23, so that the zero point's operand (times 2^-8) does: z16 may be
+              // anything up to 65504, in keys far from 0
               const int e = (int)(__float_as_uint(dm) >> 23) - 127;
               const int kx = dm > 0.f && dm < INFINITY ? 14 - e : 0;
               const float up = __int_as_float((kx + 127) << 23);

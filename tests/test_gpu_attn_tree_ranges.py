@@ -102,3 +102,25 @@ def test_a_token_of_the_pages_takes_the_weight_and_gives_nothing(shape, lead, wh
     out = _call(run, q, cu, parent)
     assert int(run.runner.status.item()) == 0
     _compare(run, q, cu, parent, out, [(0, 0), (w.batch - 1, 1)])
+
+
+OFFSET_COUNTS = {"wide": [64, 40], "narrow": [6, 3]}
+
+
+@pytest.mark.parametrize("zero", [600.0, 5000.0, 60000.0])
+@pytest.mark.parametrize("trees", sorted(OFFSET_COUNTS))
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("l2", [False, True])
+def test_keys_far_from_zero(group, trees, zero, l2):
+    """Every group of every key lies about one away from 0, its codes a z-th of that apart."""
+    base = BASE.replace(transform="hadamard", key_l2norm=True) if l2 else BASE
+    w = base.replace(batch=2, n_q_heads=8, n_kv_heads=2, ctx_lo=900, ctx_hi=1500, group_size=group)
+    run, q, cu, parent = _drafted(w, OFFSET_COUNTS[trees], "random")
+    keys = _key_scales(run)
+    gen = torch.Generator("cuda").manual_seed(11)
+    off = torch.randn(keys.shape[:-1], generator=gen, device="cuda")
+    keys[..., 1] = (-torch.sign(off) * zero * (1 + 0.08 * torch.rand(off.shape, generator=gen, device="cuda"))).half()
+    keys[..., 0] = (off.abs() / (zero * (128 ** 0.5 if l2 else 1))).half()
+    out = _call(run, q, cu, parent)
+    assert int(run.runner.status.item()) == 0
+    _compare(run, q, cu, parent, out, [(0, 0), (1, 1)])
