@@ -18,11 +18,13 @@
 // already took as long, and the second score buffer no longer fits.
 // Keys.  With one group per row (G = 128) A holds the codes themselves, exact, and the zero point is
 // one more K = 16 step (z against -sum q', hi + lo); Delta multiplies the finished sum.  With more
-// groups A holds Delta c as an exact fp16 hi + lo pair (13 bits), scaled by a power of two per token.
+// groups A holds Delta c as an fp16 hi + lo pair (13 bits), scaled by a power of two per token, exact for groups down
+// to 2^-25 of the token's largest, and the zero point's step takes Delta z (22 bits, hi + lo).
 // q' is scaled by a power of two of its row, its largest value to 2^13 .. 2^14: exact down to 2^-22 of that value
-// (8 bits above fp16's last step 2^-24, in slots that carry 4^-4), below it off by at most 2^-30 of it.  Values are dequantized to fp16, Delta (c - z) in one rounding (relative 2^-11 of the
-// value and of Delta z: the output's own rounding to bf16 is 2^-8).  P is rounded to fp16, the sums l
-// are fp32.  Window rows are bf16 as they are, with P as a bf16 hi + lo pair.
+// (8 bits above fp16's last step 2^-24, in slots that carry 4^-4), below it off by at most 2^-30 of it; with more
+// groups to 2^8 .. 2^9 and no slots, exact down to 2^-25, off by at most 2^-33.  Values are dequantized to fp16,
+// Delta (c - z) in one rounding (relative 2^-11 of the value and of Delta z: the output's own rounding to bf16 is
+// 2^-8).  P is rounded to fp16, the sums l are fp32.  Window rows are bf16 as they are, with P as a bf16 hi + lo pair.
 //
 // Softmax reference.  m_n moves only when a score passes it by 15 (in log2): P <= 2^15, and fp16 ends at 2^16.
 // It is set to the row's maximum, or up to 12 below it, as far as the maxima of the tile's four quarters lie apart
@@ -47,7 +49,7 @@
 // part stands out: with its exponentials, its stores of P or the values' stores to TMEM left out the kernel
 // takes as long within 2%, without the keys' stores 3 to 8% less.  8 softmax warps of 32 rows executed 7,900
 // instructions a tile at 58% and took 2.5% longer.  Measured: 64 nodes of 4 heads on 32 K tokens 104 us (330
-// TFLOP/s), 16 nodes of 8 heads on 4 x 128 K tokens 915 us (225 TFLOP/s); a power of two a row, not a CTA, is 4%
+// TFLOP/s), 16 nodes of 8 heads on 4 x 128 K tokens 910 us (227 TFLOP/s); a power of two a row, not a CTA, is 4%
 // of that (a query may be of any size beside its neighbours').
 // What those figures hang on:
 //   * MMAs are issued from code that the whole warp runs, by one elected lane: from a divergent branch each
@@ -233,6 +235,10 @@ __device__ __forceinline__ void tm_st_frag8(uint32_t a, const uint32_t (&v)[16])
       "r"(a)
       : "memory");
 }
+// 16 lanes x 16 columns: two k-steps
+__device__ __forceinline__ void tm_st_frag4(uint32_t a, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::KVQ_IO8("r", 0), "r"(a) : "memory");
+}
 // 16 lanes x 8 columns: the A fragment of one k-step
 __device__ __forceinline__ void tm_st_frag2(uint32_t a, const uint32_t (&v)[4]) {
   asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%4], {%0,%1,%2,%3};" ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(a)
@@ -265,6 +271,17 @@ __device__ __forceinline__ uint32_t packb16(float a, float b) {
 __device__ __forceinline__ uint4 lds16(const void* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// a token's (Delta, z) pairs, one a group
+template <int NG>
+__device__ __forceinline__ void load_scales(const uint8_t* p, uint32_t (&v)[NG]) {
+  if constexpr (NG == 4) {
+    const uint4 w = lds16(p);
+    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+  } else {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    v[0] = w.x; v[1] = w.y;
+  }
 }
 __device__ __forceinline__ int slot_pow(int s) { return s <= 4 ? s : s - 5; }
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t w10, int s) {
@@ -659,7 +676,6 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
           const uint32_t kw[4] = {w.x, w.y, w.z, w.w};
           const uint32_t kw10[4] = {w.x >> 10, w.y >> 10, w.z >> 10, w.w >> 10};
           const uint8_t* sc = pgp + k_scale_off();
-          uint32_t v[16];
           float ls[2];
           // slots 2 quad, 2 quad + 1 and 8 + 2 quad, 9 + 2 quad of tokens row, row + 8 (z[0 .. 1], z[2 .. 3])
           auto put_zero = [&](const uint32_t (&z)[4]) {
@@ -679,6 +695,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
             }
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
+              uint32_t v[16];
 #pragma unroll
               for (int s = 0; s < 4; ++s)
 #pragma unroll
@@ -692,32 +709,22 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               uint32_t dz[NG];
+              load_scales<NG>(sc + 4 * NG * (row + 8 * x), dz);
+              // (the quad's lanes have a group each)
+              const float2 f = __half22float2(bits2h(*reinterpret_cast<const uint32_t*>(sc + 4 * NG * (row + 8 * x) + 4 * (quad & (NG - 1)))));
+              float top = fmaxf(4.f * f.x, fabsf(f.x * f.y));
 #pragma unroll
-              for (int g = 0; g < NG; ++g) dz[g] = *reinterpret_cast<const uint32_t*>(sc + 4 * NG * (row + 8 * x) + 4 * g);
-              float dm = 0.f;
-#pragma unroll
-              for (int g = 0; g < NG; ++g) {
-                const float2 f = __half22float2(bits2h(dz[g]));
-                dm = fmaxf(dm, fmaxf(f.x, fabsf(f.x * f.y) * 0x1p-8f));
-              }
-              // 2^k: the largest Delta 2^k below 2^15, so that its product with 3 4^s 2^-24 stays in range, and the
-              // largest |Delta z| 2^k below 2^23, so that the zero point's operand (times 2^-8) does: z16 may be
-              // anything up to 65504, in keys far from 0
-              const int e = (int)(__float_as_uint(dm) >> 23) - 127;
-              const int kx = dm > 0.f && dm < INFINITY ? 14 - e : 0;
+              for (int o = 1; o < NG; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              // 2^k: the largest of 4 Delta 2^k and |Delta z| 2^k (z16 may be anything up to 65504, in keys far from 0)
+              // in [2^14, 2^15).  A pair hi + lo of c Delta 2^k has 13 bits and fp16 ends at 2^-24: it is exact for
+              // groups down to 2^-25 of the largest
+              const int e = (int)(__float_as_uint(top) >> 23) - 127;
+              const int kx = top > 0.f && top < INFINITY ? 14 - e : 0;
               const float up = __int_as_float((kx + 127) << 23);
               ls[x] = __int_as_float((127 - kx) << 23);
-              float dq = 0.f, zq = 0.f;
 #pragma unroll
-              for (int g = 0; g < NG; ++g) {
-                const __half2 dd = __float2half2_rn(__low2float(bits2h(dz[g])) * up);
-                d2[x][g] = h2bits(dd);
-                if (g == quad) {
-                  dq = __low2float(dd);
-                  zq = __high2float(bits2h(dz[g]));
-                }
-              }
-              const float prod = dq * zq * 0x1p-8f;         // (11 + 11 bits: exact)
+              for (int g = 0; g < NG; ++g) d2[x][g] = h2bits(__float2half2_rn(__low2float(bits2h(dz[g])) * up));
+              const float prod = f.x * up * f.y;            // (11 + 11 bits: exact)
               const float hi = __half2float(__float2half_rn(prod));
               if (quad < NG) {
                 z[x] = pack16(hi, prod - hi);
@@ -726,20 +733,19 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
             }
             put_zero(z);
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
+            for (int s0 = 0; s0 < 8; s0 += 2) {
+              uint32_t hi[8], lo[8];
 #pragma unroll
-              for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  v[4 * s + r] = h2bits(__hmul2(bits2h(code_pair(kw[r], kw10[r], 4 * hf + s)), bits2h(d2[r & 1][(4 * hf + s) * NG / 8])));
-              tm_st_frag8(ta + 32 * hf, v);
-#pragma unroll
-              for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                  v[4 * s + r] = h2bits(__hfma2(bits2h(code_pair(kw[r], kw10[r], 4 * hf + s)), bits2h(d2[r & 1][(4 * hf + s) * NG / 8]),
-                                                __hneg2(bits2h(v[4 * s + r]))));
-              tm_st_frag8(ta + 64 + 32 * hf, v);
+              for (int k = 0; k < 8; ++k) {
+                // 2^(10 - 2 sp) + c, then c, then Delta 2^k c
+                const int s = s0 + (k >> 2), r = k & 3, sp = slot_pow(s);
+                const uint32_t one = (uint32_t)(25 - 2 * sp) * 0x04000400u, d = d2[r & 1][s * NG / 8];
+                const __half2 c = __hsub2(bits2h(code_pair(kw[r], kw10[r], s) | one), bits2h(one));
+                hi[k] = h2bits(__hmul2(c, bits2h(d)));
+                lo[k] = h2bits(__hfma2(c, bits2h(d), __hneg2(bits2h(hi[k]))));
+              }
+              tm_st_frag4(ta + 8 * s0, hi);
+              tm_st_frag4(ta + 64 + 8 * s0, lo);
             }
           }
           if (P.l2) {
@@ -851,7 +857,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       const uint16_t* ring = keys ? P.ring_k : P.ring_v;
       uint8_t* dst = sm + (keys ? L::kK : L::kV);
       const int j = t & 15;
-#pragma unroll 4
+#pragma unroll 1
       for (int r = t >> 4; r < kTile; r += 2 * (keys ? kKeyWarps : kValWarps)) {
         const int w = min(w0 + r, n_win - 1);
         const int tok = w < n_sink ? w : ring0 + w - n_sink;
@@ -903,9 +909,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         S.neg_m[tid] = 0.f;
       }
       softmax_sync();
-      // 16 lanes a row: bf16 as it is, for the windows; fp16 times a power of two of the row, channel slot s
-      // scaled by 4^-s for the codes that carry 4^s
-#pragma unroll 2
+      // 16 lanes a row: bf16 as it is, for the windows; fp16 times a power of two of the row, with one group
+      // channel slot s by 4^-s too, for the codes that carry 4^s 2^-24
+#pragma unroll 1
       for (int i = tid; i < N * 16; i += 32 * kSmWarps) {
         const int c = i >> 4, j = i & 15;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -916,14 +922,14 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         uint32_t top = max(m << 16, m & 0xffff0000u);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // amax 2^sigma < 2^14 (a row that is not finite stays so)
-        const int sigma = top > 0u && top < 0x7f800000u ? min(100, 14 - ((int)(top >> 23) - 126)) : 0;
+        // amax 2^sigma < 2^14, or 2^9, so that sums of groups stay in range (a row that is not finite stays so)
+        const int sigma = top > 0u && top < 0x7f800000u ? min(100, (NG == 1 ? 14 : 9) - ((int)(top >> 23) - 126)) : 0;
         if (j == 0) {
           S.sigma[c] = sigma;
-          S.mul[0][c] = P.scale_log2 * ldexpf(1.f, 24 - sigma);
+          S.mul[0][c] = P.scale_log2 * ldexpf(1.f, (NG == 1 ? 24 : 0) - sigma);
           S.mul[1][c] = P.scale_log2;
         }
-        const float f = __int_as_float((sigma - 2 * slot_pow(j >> 1) + 127) << 23);
+        const float f = __int_as_float((sigma - (NG == 1 ? 2 * slot_pow(j >> 1) : 0) + 127) << 23);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t o[4];
 #pragma unroll
@@ -946,7 +952,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
         if (NG <= 2) acc += __shfl_xor_sync(0xffffffffu, acc, 1);
         if (NG == 1) acc += __shfl_xor_sync(0xffffffffu, acc, 2);
         const float from = __shfl_sync(0xffffffffu, acc, (lane & ~3) + (part * (4 / NG) & 3));   // slot pair `part`: group part
-        const float v = part < NG ? -from * ldexpf(1.f, NG == 1 ? sigma - 19 : sigma - 16) : 0.f;
+        const float v = part < NG ? -from * ldexpf(1.f, NG == 1 ? sigma - 19 : sigma) : 0.f;
         const float hi = __half2float(__float2half_rn(v));
         uint8_t* to = sm + L::kZ + (c >> 3) * 128 + (c & 7) * 16 + 4 * part;
         *reinterpret_cast<uint32_t*>(to) = pack16(hi, hi);
@@ -1147,7 +1153,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
     {
       const int c = tok & (kCols - 1), part = tok / kCols;  // kCols tokens each
       float sum = 0.f;
-#pragma unroll 8
+#pragma unroll 2
       for (int t = part * kCols; t < (part + 1) * kCols; ++t)
         sum += scratch[t * N + c0 + 4 * ((c >> 2) ^ (t & (kChunks - 1))) + (c & 3)];
       S.red[part][c0 + c] = sum;

@@ -124,3 +124,27 @@ def test_keys_far_from_zero(group, trees, zero, l2):
     out = _call(run, q, cu, parent)
     assert int(run.runner.status.item()) == 0
     _compare(run, q, cu, parent, out, [(0, 0), (1, 1)])
+
+
+@pytest.mark.parametrize("apart", [6, 10, 14])
+@pytest.mark.parametrize("trees", sorted(OFFSET_COUNTS))
+@pytest.mark.parametrize("group", [32, 64])
+def test_a_group_of_small_keys_under_large_queries(group, trees, apart):
+    """One group's keys 2^-apart of the others', its queries 2^apart times theirs: all groups weigh alike."""
+    w = BASE.replace(batch=2, n_q_heads=8, n_kv_heads=2, ctx_lo=900, ctx_hi=1500, group_size=group)
+    run, q, cu, parent = _drafted(w, OFFSET_COUNTS[trees], "random")
+    keys, c = _key_scales(run), run.runner.cache
+    for g in range(128 // group):
+        small = slice(g * group, (g + 1) * group)
+        pages, rows = keys.clone(), [t.clone() for t in (c.sink_k, c.ring_k)]
+        keys[..., g, 0] = (keys[..., g, 0].float() * 2.0 ** -apart).half()
+        for t in (c.sink_k, c.ring_k):
+            t[..., small] *= 2.0 ** -apart
+        qg = q.clone()
+        qg[..., small] *= 2.0 ** apart
+        out = _call(run, qg, cu, parent)
+        assert int(run.runner.status.item()) == 0
+        _compare(run, qg, cu, parent, out, [(0, 0), (1, 1)])
+        keys.copy_(pages)
+        c.sink_k.copy_(rows[0])
+        c.ring_k.copy_(rows[1])
