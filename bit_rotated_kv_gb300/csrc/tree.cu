@@ -1170,6 +1170,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
       const float top = sum != 0.f ? -S.neg_m[c] : -1e30f;
       if (P.splits > 1 && q == 0 && lane < kCols && c < ncol)
         *reinterpret_cast<float2*>(P.part + ((size_t)S.row[c] * P.splits + split) * kRec) = make_float2(top, sum);
+      const unsigned finite = __ballot_sync(0xffffffffu, fabsf(sum) < INFINITY);
+      bool beyond = false;                                  // weights that are numbers, and a sum that is none
 #pragma unroll 1
       for (int j = 0; j < kCols && c0 + j < ncol; j += 8) {
         float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -1179,11 +1181,13 @@ __global__ void __launch_bounds__(kThreadsT, 1) attn_tree_kernel(const __grid_co
           const float v = o[e] * __shfl_sync(0xffffffffu, by, j + e);
           const size_t r = (size_t)S.row[c0 + j + e];
           if (c0 + j + e < ncol) {
+            beyond |= ((finite >> (j + e)) & 1u) && !(fabsf(o[e]) < INFINITY);
             if (P.splits == 1) P.out[r * kHeadDim + tok] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
             else P.part[(r * P.splits + split) * kRec + 4 + tok] = v;
           }
         }
       }
+      if (beyond) set_status(P.status, KVQ_ERR_NONFINITE);  // (a value beyond fp16's 65504, or not finite)
     }
   }
   fence_before();

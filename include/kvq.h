@@ -344,6 +344,8 @@ KVQ_API int kv_attn_chunk(const kvq_config* cfg, const kvq_cache* cache, const u
  * windows; a node whose ancestors are not in index order is reported and sees those up to the fault.
  * Rows behind the last sequence are not written (KVQ_ERR_BOUNDS when cu_rows does not cover n_rows).  A
  * draft whose K or V is not finite changes the rows of the nodes that see it, and only those.
+ * An INT2 value beyond fp16's 65504 is more than the tensor-core kernel (below) can hold: it reports
+ * KVQ_ERR_NONFINITE, as for a value before the drafts that is not finite, and the results are not finite.
  * Execution: trees of up to about 32 columns (nodes x query heads per kv head), and small calls, run the
  * decode kernel with eight columns to a grid row; wider ones a tensor-core kernel that reads a
  * sequence's cache once for every 64 columns.  The two round differently (both within the attention's

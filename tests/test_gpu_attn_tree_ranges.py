@@ -148,3 +148,44 @@ def test_a_group_of_small_keys_under_large_queries(group, trees, apart):
         keys.copy_(pages)
         c.sink_k.copy_(rows[0])
         c.ring_k.copy_(rows[1])
+
+
+def _value_zeros(run):
+    """Value z16, as _value_deltas."""
+    ng = 128 // run.cfg.group_size
+    p = run.runner.cache.pages
+    return p[:, :, 1024 + 96 * ng:1024 + 128 * ng].view(torch.float16).unflatten(-1, (8, ng, 2))
+
+
+@pytest.mark.parametrize("zero", [1.5, 600.0, 60000.0])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_values_up_to_the_end_of_fp16(group, zero):
+    """Values of up to 65504 in magnitude are held; one beyond that is reported.
+
+    The values' signs are drawn, so that a row may cancel far below them, and its error is that of the terms:
+    p is rounded to fp16 (at most 2^-11 p), Delta z likewise (2^-11 |Delta z|, and |Delta z| <= |v| + 3 Delta), and
+    Delta c - Delta z once more (2^-11 |v|).  So sum p v is off by at most 2^-11 (3 sum p |v| + 3 Delta sum p), and the
+    output's rounding to bf16 adds 2^-8 of it.  (The scores' errors, some 2^-20, are far below that bound's slack:
+    it adds up the roundings of all tokens in one direction.)"""
+    import bit_rotated_kv_gb300 as kvq
+    w = BASE.replace(batch=2, n_q_heads=8, n_kv_heads=2, ctx_lo=900, ctx_hi=1500, group_size=group)
+    run, q, cu, parent = _drafted(w, [64, 40], "random")
+    d, z = _value_deltas(run), _value_zeros(run)
+    gen = torch.Generator("cuda").manual_seed(12)
+    sign = torch.randint(0, 2, z.shape, generator=gen, device="cuda") * 2 - 1
+    z[...] = (sign * zero).half()
+    delta = 60000.0 / (zero + 3)
+    d[...] = delta
+    out = _call(run, q, cu, parent)
+    assert int(run.runner.status.item()) == 0
+    qf, of, snap = q.double().cpu().numpy(), out.double().cpu().numpy(), run.snapshot()
+    for b, h in ((0, 0), (1, 1)):
+        rows, heads = _rows(cu, b), _heads(w, h)
+        K, V = spec_ref.unit_kv(run.cfg, snap, run.table, b, h)
+        at = lambda v: spec_ref.tree_attention(qf[rows, heads], K, v, parent[rows], run.runner.sm_scale)  # noqa: E731
+        ref, size = at(V), at(abs(V))
+        assert (abs(of[rows, heads] - ref) <= 2.0 ** -8 * abs(ref) + 2.0 ** -11 * 3 * (size + delta)).all(), (b, h)
+    d[...] = 30000.0                                  # (1.5 + 3) x 30000, and more
+    z[...] = (-zero * sign.abs()).half()
+    _call(run, q, cu, parent)
+    assert int(run.runner.status.item()) == kvq.KVQ_ERR_NONFINITE
