@@ -1578,9 +1578,20 @@ extern "C" size_t kvq_attn_tree_head_bytes(const kvq_config* cfg) {
   return (tickets * 4 + 255) / 256 * 256;
 }
 
-extern "C" size_t kvq_attn_tree_rows_ws_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
-  const kvq_config c = tree_config(cfg, n_rows);
-  return kvq_attn_tree_head_bytes(cfg) + kvq_attn_ws_bytes(&c, max_ctx) - kvq_attn_counter_bytes(&c, max_ctx);
+// Bytes of partials that a call of up to n_rows rows and max_ctx tokens can need.  The splits of u grid rows x kv
+// heads are, all together (kvq_attn_splits): at most max(u, 304) pages' and max(u, 304) windows', and as many
+// pages' as the config asks for where it does; one more record a group of kGroup, rounded up.
+extern "C" size_t kvq_attn_tree_rows_part_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
+  const auto bytes = [&](int32_t n) {
+    const kvq_config c = tree_config(cfg, n);
+    const size_t u = (size_t)c.batch * c.n_kv_heads, wave = max(u, (size_t)(kCtasPerSm * kSms));
+    const size_t pages = c.attn_splits > 0 ? u * (size_t)min(c.attn_splits, max(1, kvq_attn_pages(&c, max_ctx))) : wave;
+    const size_t splits = pages + wave, groups = splits / kGroup + u;
+    return (splits + groups) * (size_t)(c.n_q_heads / c.n_kv_heads) * kRow * sizeof(float);
+  };
+  // (fewer rows may take a group of nodes less to a grid row: see tree_config)
+  const int32_t alone = 32 / cfg->n_kv_heads;
+  return max(bytes(n_rows), n_rows > alone && alone > 0 ? bytes(alone) : (size_t)0);
 }
 
 extern "C" int kvq_launch_attn_tree_rows(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot,

@@ -23,7 +23,7 @@ int kvq_launch_attn_chunk(const kvq_config* cfg, const kvq_cache* cache, const u
                           cudaStream_t stream);
 size_t kvq_attn_chunk_ws_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx);
 size_t kvq_attn_tree_head_bytes(const kvq_config* cfg);
-size_t kvq_attn_tree_rows_ws_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx);
+size_t kvq_attn_tree_rows_part_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx);
 int kvq_launch_attn_tree_rows(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot,
                               const int32_t* cu_rows, const int32_t* parent, int32_t n_rows, uint16_t* out,
                               float sm_scale, int32_t max_ctx, void* ws, int32_t* d_status, cudaStream_t stream);

@@ -89,6 +89,7 @@ static_assert(32 * kSmWarps * kRegsSoftmax + 128 * kRegsKeys + 256 * kRegsValues
 // log2 of the largest P before a row's reference moves: page tiles (fp16), window tiles (bf16 pairs); a lead that
 // is ordinary, and how far below the maximum a reference is set at most
 constexpr float kRefSlack = 15.f, kWinSlack = 30.f, kRefLead = 8.f, kRefBelow = 12.f;
+constexpr int kMostSplits = 64;
 constexpr int kWinCost = 4;                      // a window tile's time in page tiles'
 constexpr long long kSmallCall = 1 << 19;        // row_kernel(): rows x kv heads x tokens
 constexpr int kRec = 4 + kHeadDim;               // (m, l, -, -, o[d]) of a partial
@@ -1254,21 +1255,33 @@ __global__ void __launch_bounds__(kMThreads) attn_tree_merge_kernel(const __grid
 struct Shape {
   int splits, items;
 };
-Shape tree_shape(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
-  const int g = cfg->n_q_heads / cfg->n_kv_heads;
-  Shape s;
-  const long long per_seq = ((long long)n_rows * g + cfg->batch - 1) / cfg->batch;
-  s.items = (int)min((long long)n_rows, (long long)n_rows * g / N + cfg->batch);
+// Tiles of the longest sequence there may be, and CTAs of one split: about as many as the row tiles there will be
+// (a sequence's last one is half empty on average).  Both grow with n_rows and max_ctx.
+long long tree_tiles(const kvq_config* cfg, int32_t max_ctx) {
   const long long pages = max(0LL, min((long long)cfg->max_pages_per_seq, ((long long)max_ctx - cfg->s_sink + kPage - 1) / kPage));
   const long long win = min((long long)cfg->s_sink + cfg->s_keep + cfg->s_flush + kNodes, (long long)max_ctx);
-  const long long tiles = max(1LL, (pages + kTilePages - 1) / kTilePages + (win + kTile - 1) / kTile);
-  // about as many CTAs as the row tiles there will be (a sequence's last one is half empty on average)
-  const long long units = max(1LL, min((long long)s.items, (per_seq + N - 1) / N * min((long long)cfg->batch, (long long)n_rows))) *
-                          cfg->n_kv_heads;
+  return max(1LL, (pages + kTilePages - 1) / kTilePages + (win + kTile - 1) / kTile);
+}
+int tree_items(const kvq_config* cfg, int32_t n_rows) {
+  const long long g = cfg->n_q_heads / cfg->n_kv_heads;
+  return (int)min((long long)n_rows, n_rows * g / N + cfg->batch);
+}
+long long tree_units(const kvq_config* cfg, int32_t n_rows) {
+  const long long g = cfg->n_q_heads / cfg->n_kv_heads, per_seq = (n_rows * g + cfg->batch - 1) / cfg->batch;
+  return max(1LL, min((long long)tree_items(cfg, n_rows), (per_seq + N - 1) / N * min((long long)cfg->batch, (long long)n_rows))) *
+         cfg->n_kv_heads;
+}
+// CTAs that splits may make of so many: 12 waves, or 24 of more than one wave.  (So that the workspace has a bound.
+// Without it 2% of the sizes would take other splits, estimated to be up to 6% faster.)
+long long most_ctas(long long units) { return (long long)kSms * (units <= kSms ? 12 : 24); }
+Shape tree_shape(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
+  Shape s;
+  s.items = tree_items(cfg, n_rows);
+  const long long tiles = tree_tiles(cfg, max_ctx), units = tree_units(cfg, n_rows);
   // a wave of 152 CTAs takes tiles / splits, and about 6 tiles' time for set-up and merge
   double best = 1e300;
   s.splits = 1;
-  for (int k = 1; k <= 64 && k <= tiles; ++k) {
+  for (int k = 1; k <= kMostSplits && k <= tiles && (k == 1 || units * k <= most_ctas(units)); ++k) {
     const double waves = (double)((units * k + kSms - 1) / kSms);
     const double cost = waves * ((double)((tiles + k - 1) / k) + 5.0) + (k > 1 ? 3.0 : 0.0);
     if (cost < best * 0.98) {
@@ -1277,6 +1290,13 @@ Shape tree_shape(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
     }
   }
   return s;
+}
+// Bytes of partials that a call of up to n_rows rows and max_ctx tokens can need.  A split CTA has at most N rows, so
+// there are no more partials than N for each of most_ctas(), nor than splits of all rows.
+size_t tree_part_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
+  const long long tiles = tree_tiles(cfg, max_ctx), k = min((long long)kMostSplits, tiles);
+  if (k <= 1) return 0;
+  return (size_t)min((long long)n_rows * cfg->n_q_heads * k, N * most_ctas(tree_units(cfg, n_rows))) * kRec * sizeof(float);
 }
 
 }  // namespace
@@ -1299,11 +1319,11 @@ static bool row_kernel(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
   return groups <= (max_ctx < 2048 ? 3 : 4) * tiles || (units <= 128 && units * max_ctx <= kSmallCall);
 }
 
+// Enough for every call of up to n_rows rows and max_ctx tokens, whichever kernel it takes.
 extern "C" size_t kvq_attn_tree_ws_bytes(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
-  if (row_kernel(cfg, n_rows, max_ctx)) return kvq_attn_tree_rows_ws_bytes(cfg, n_rows, max_ctx);
-  const Shape s = tree_shape(cfg, n_rows, max_ctx);
-  return kvq_attn_tree_head_bytes(cfg) +
-         (s.splits > 1 ? (size_t)n_rows * cfg->n_q_heads * s.splits * kRec * sizeof(float) : 0);
+  const size_t rows = kvq_attn_tree_rows_part_bytes(cfg, n_rows, max_ctx);
+  const size_t tiles = cfg->key_axis == KVQ_KEY_PER_TOKEN ? tree_part_bytes(cfg, n_rows, max_ctx) : 0;
+  return kvq_attn_tree_head_bytes(cfg) + max(rows, tiles);
 }
 
 extern "C" int kvq_launch_attn_tree(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot,

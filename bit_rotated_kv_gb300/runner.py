@@ -12,7 +12,7 @@ import math
 import numpy as np
 import torch
 
-from . import (KVCache, KVConfig, Transform, kv_append_chunk, kv_attn_chunk, kv_attn_chunk_workspace_bytes,
+from . import (KVQ_TREE_MAX_NODES, KVCache, KVConfig, Transform, kv_append_chunk, kv_attn_chunk, kv_attn_chunk_workspace_bytes,
                kv_attn_decode, kv_attn_tree, kv_attn_tree_workspace_bytes, kv_pages_compact,
                kv_pages_compact_workspace_bytes, kv_pages_reserve, kv_quant_flush, kv_rotate_qk, kv_seq_fork, kv_seq_free,
                kv_tree_commit, kv_verify_tree, workspace)
@@ -133,7 +133,8 @@ class DecodeRunner:
     # ---- speculative decoding: tree_step, then accept --------------------------------------------
     def tree_workspace(self, n_rows: int) -> torch.Tensor:
         """A zeroed workspace for trees of up to n_rows nodes in all."""
-        n = max(kv_attn_tree_workspace_bytes(self.cfg, r, self.max_ctx) for r in range(1, max(1, n_rows) + 1))
+        n_rows = max(1, min(n_rows, self.cfg.batch * KVQ_TREE_MAX_NODES, 65535))
+        n = kv_attn_tree_workspace_bytes(self.cfg, n_rows, self.max_ctx)
         return torch.zeros(max(n, 256), dtype=torch.uint8, device=self.device)
 
     def tree_step(self, q, k_rows, v_rows, seq_idx, pos, cu_rows, parent, q_out, out, ws, stream=None) -> None:

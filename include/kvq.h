@@ -336,9 +336,9 @@ KVQ_API int kv_attn_chunk(const kvq_config* cfg, const kvq_cache* cache, const u
  * (token L0 + j for node j) and to itself, as the cache holds them.  A chain (parent i - 1) gives
  * kv_attn_chunk's result; several roots are allowed.  max_ctx, sm_scale as for kv_attn_decode
  * (max_ctx counts the nodes); workspace of kv_attn_tree_workspace_bytes(cfg, n_rows, max_ctx)
- * bytes, zero-filled before its first use (every call leaves its counters zero).  One workspace
- * of the largest size serves calls of any n_rows and max_ctx with the same config, one after another;
- * calls that may run at the same time need one each.  n_rows is at most 65535 (KVQ_ERR_UNSUPPORTED beyond)
+ * bytes, zero-filled before its first use (every call leaves its counters zero).  That size is enough for every
+ * call of up to n_rows rows and max_ctx tokens with the same config, one after another (it does not shrink as they
+ * grow; 0 for sizes that are refused); calls that may run at the same time need a workspace each.  n_rows is at most 65535 (KVQ_ERR_UNSUPPORTED beyond)
  * and batch * KVQ_TREE_MAX_NODES (KVQ_ERR_INVALID_ARG).  KVQ_ERR_BOUNDS in *d_status, and zeros for
  * the rows of a sequence whose nodes are more than KVQ_TREE_MAX_NODES or do not all lie in the BF16
  * windows; a node whose ancestors are not in index order is reported and sees those up to the fault.

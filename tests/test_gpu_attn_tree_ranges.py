@@ -189,3 +189,29 @@ def test_values_up_to_the_end_of_fp16(group, zero):
     z[...] = (-zero * sign.abs()).half()
     _call(run, q, cu, parent)
     assert int(run.runner.status.item()) == kvq.KVQ_ERR_NONFINITE
+
+
+def test_a_workspace_of_the_largest_size_serves_smaller_calls():
+    """Calls of fewer rows and shorter contexts than the workspace was sized for, through both kernels; the bytes
+    behind it are left."""
+    import bit_rotated_kv_gb300 as kvq
+    runs = [_drafted(BASE.replace(batch=4, ctx_lo=ctx, ctx_hi=ctx + 300), counts, "random")
+            for ctx, counts in ((500, [128, 30, 90, 128]), (9000, [128, 128, 128, 128]), (9000, [20, 30, 10, 20]), (9000, [5, 1, 2, 1]),
+                                (2000, [1, 1, 1, 1]), (9000, [0, 0, 60, 0]), (700, [0, 2, 0, 0]))]
+    big = max(runs, key=lambda r: r[0].runner.cfg.max_pages_per_seq)[0]
+    n = kvq.kv_attn_tree_workspace_bytes(big.cfg, 512, int(big.runner.cache.seq_len.max()))
+    room = torch.zeros(n + 4096, dtype=torch.uint8, device="cuda")
+    room[n:] = 77
+    ws = room[:n]
+    for _ in range(2):
+        for run, q, cu, parent in runs:
+            run.cfg.max_pages_per_seq, was = big.cfg.max_pages_per_seq, run.cfg.max_pages_per_seq
+            table = run.runner.cache.page_table
+            wide = torch.full((4, big.cfg.max_pages_per_seq), -1, dtype=torch.int32, device="cuda")
+            wide[:, :was] = table
+            run.runner.cache.page_table = wide
+            out = _call(run, q, cu, parent, ws)
+            assert int(run.runner.status.item()) == 0
+            _compare(run, q, cu, parent, out, [(2, 3)])
+            run.cfg.max_pages_per_seq, run.runner.cache.page_table = was, table
+    assert bool((room[n:] == 77).all())
