@@ -356,6 +356,41 @@ def kv_attn_decode_noalloc(cfg: KVConfig, cache: KVCache, q_rot, out, sm_scale: 
     _check(rc, "kv_attn_decode_noalloc")
 
 
+def _current_device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _addr(dev: int, t, dtype, least: int, what: str) -> int:
+    """Address of a tensor of this type with at least so many elements, one after another, on the current device.
+    Anything else is refused: the kernels take addresses, and would read other numbers or write past the end.
+    None stands for no elements."""
+    if t is None:
+        if least > 0:
+            raise KVQError(KVQ_ERR_INVALID_ARG, what)
+        return 0
+    if t.dtype is not dtype or t.numel() < least or not t.is_contiguous():
+        raise KVQError(KVQ_ERR_INVALID_ARG, what)
+    if t.get_device() != dev:
+        raise KVQError(KVQ_ERR_INVALID_ARG, f"{what} (another device)")
+    return t.data_ptr()
+
+
+def _status(dev: int, status, where: str) -> int:
+    return 0 if status is None else _addr(dev, status, torch.int32, 1, f"{where}: status")
+
+
+def _cache(dev: int, cache: KVCache, where: str):
+    if cache.pages.get_device() != dev:
+        raise KVQError(KVQ_ERR_INVALID_ARG, f"{where}: cache (another device)")
+    return ctypes.byref(cache.c())
+
+
+def _stream_of(dev: int, stream) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return int(getattr(stream, "cuda_stream", stream))
+
+
 def _nbytes(t) -> int:
     return int(t.numel() * t.element_size())
 
@@ -369,60 +404,94 @@ def kv_attn_tree(cfg: KVConfig, cache: KVCache, q_rot, cu_rows, parent, out, sm_
     """q_rot [n, Hq, d] (rows cu_rows[b] .. cu_rows[b+1]-1 the drafted nodes of sequence b, its last
     tokens; parent [n] int32 local to the sequence, -1 for a root) -> out [n, Hq, d] bf16: every node
     attends to the tokens before the drafts, its ancestors and itself."""
-    n = int(q_rot.shape[0])
-    c, cc = cfg.c(), cache.c()
-    rc = lib().kv_attn_tree(ctypes.byref(c), ctypes.byref(cc), _ptr(q_rot), _ptr(cu_rows), _ptr(parent), n, _ptr(out),
-                            float(sm_scale), int(max_ctx), _ptr(workspace), _nbytes(workspace), _ptr(status),
-                            _stream(stream))
+    n, dev, i32, bf16 = q_rot.shape[0], _current_device(), torch.int32, torch.bfloat16
+    size = n * cfg.n_q_heads * cfg.head_dim
+    q = _addr(dev, q_rot, bf16, size, "kv_attn_tree: q_rot")
+    cu = _addr(dev, cu_rows, i32, cfg.batch + 1, "kv_attn_tree: cu_rows")
+    par = _addr(dev, parent, i32, n, "kv_attn_tree: parent")
+    o = _addr(dev, out, bf16, size, "kv_attn_tree: out")
+    ws = _addr(dev, workspace, workspace.dtype, 0, "kv_attn_tree: workspace")
+    rc = lib().kv_attn_tree(ctypes.byref(cfg.c()), _cache(dev, cache, "kv_attn_tree"), q, cu, par, n, o, float(sm_scale),
+                            int(max_ctx), ws, _nbytes(workspace), _status(dev, status, "kv_attn_tree"), _stream_of(dev, stream))
     _check(rc, "kv_attn_tree")
+
+
+def _prob_rows(dev: int, t, n: int, vocab: int, what: str):
+    """Address and row stride of n rows of float32 probabilities, each row's one after another."""
+    if t is None:
+        return 0, 0
+    if (t.dim() != 2 or t.dtype is not torch.float32 or t.shape[0] != n or t.shape[1] != vocab or (vocab > 1 and t.stride(1) != 1)
+            or (n > 1 and t.stride(0) < vocab)):
+        raise KVQError(KVQ_ERR_INVALID_ARG, what)
+    if t.get_device() != dev:
+        raise KVQError(KVQ_ERR_INVALID_ARG, f"{what} (another device)")
+    return t.data_ptr(), max(t.stride(0), vocab)
 
 
 def kv_verify_tree(cfg: KVConfig, cu_rows, parent, token, p, q, u, path, n_accept, next_token, status,
                    stream=None) -> None:
     """p (and q, or None for chosen drafts) [n, vocab] float32 with contiguous rows; token, parent, path [n]
     int32; u [n] float32; n_accept, next_token [batch] int32."""
-    n = int(token.shape[0])
-    for t in (p, q):
-        if t is not None and (t.dim() != 2 or t.dtype != torch.float32 or (t.shape[1] > 1 and t.stride(1) != 1)
-                              or t.shape[0] != n or t.shape[1] != p.shape[1] or (n > 1 and t.stride(0) < t.shape[1])):
-            raise KVQError(KVQ_ERR_INVALID_ARG, "kv_verify_tree")
-    rc = lib().kv_verify_tree(ctypes.byref(cfg.c()), _ptr(cu_rows), _ptr(parent), _ptr(token), n, _ptr(p), _row_stride(p),
-                              _ptr(q), 0 if q is None else _row_stride(q), int(p.shape[1]), _ptr(u), _ptr(path),
-                              _ptr(n_accept), _ptr(next_token), _ptr(status), _stream(stream))
+    n, dev, i32, batch = token.shape[0], _current_device(), torch.int32, cfg.batch
+    if p is None:
+        raise KVQError(KVQ_ERR_INVALID_ARG, "kv_verify_tree: p")
+    vocab = p.shape[-1]
+    pa, ps = _prob_rows(dev, p, n, vocab, "kv_verify_tree: p")
+    qa, qs = _prob_rows(dev, q, n, vocab, "kv_verify_tree: q")
+    cu = _addr(dev, cu_rows, i32, batch + 1, "kv_verify_tree: cu_rows")
+    par = _addr(dev, parent, i32, n, "kv_verify_tree: parent")
+    tok = _addr(dev, token, i32, n, "kv_verify_tree: token")
+    uu = _addr(dev, u, torch.float32, n, "kv_verify_tree: u")
+    out = _addr(dev, path, i32, n, "kv_verify_tree: path")
+    acc = _addr(dev, n_accept, i32, batch, "kv_verify_tree: n_accept")
+    nxt = _addr(dev, next_token, i32, batch, "kv_verify_tree: next_token")
+    rc = lib().kv_verify_tree(ctypes.byref(cfg.c()), cu, par, tok, n, pa, ps, qa, qs, vocab, uu, out, acc, nxt,
+                              _status(dev, status, "kv_verify_tree"), _stream_of(dev, stream))
     _check(rc, "kv_verify_tree")
-
-
-def _row_stride(t) -> int:
-    return max(int(t.stride(0)), int(t.shape[1]))
 
 
 def kv_tree_commit(cfg: KVConfig, cache: KVCache, cu_rows, path, n_accept, status, stream=None) -> None:
     """Keep the rows of the accepted paths (kv_verify_tree's path and n_accept); seq_len drops the others."""
-    rc = lib().kv_tree_commit(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(cu_rows), int(path.shape[0]),
-                              _ptr(path), _ptr(n_accept), _ptr(status), _stream(stream))
+    dev, i32 = _current_device(), torch.int32
+    cu = _addr(dev, cu_rows, i32, cfg.batch + 1, "kv_tree_commit: cu_rows")
+    at = _addr(dev, path, i32, 0, "kv_tree_commit: path")
+    acc = _addr(dev, n_accept, i32, cfg.batch, "kv_tree_commit: n_accept")
+    rc = lib().kv_tree_commit(ctypes.byref(cfg.c()), _cache(dev, cache, "kv_tree_commit"), cu, path.numel(), at, acc,
+                              _status(dev, status, "kv_tree_commit"), _stream_of(dev, stream))
     _check(rc, "kv_tree_commit")
 
 
 def kv_pages_reserve(cfg: KVConfig, cache: KVCache, page_ref, n_tokens, status, stream=None) -> None:
     """Pages for n_tokens[b] (int32 [batch]) more tokens of every sequence, lowest free ids first."""
-    rc = lib().kv_pages_reserve(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(page_ref), _ptr(n_tokens),
-                                _ptr(status), _stream(stream))
+    dev, i32 = _current_device(), torch.int32
+    ref = _addr(dev, page_ref, i32, cfg.num_pages, "kv_pages_reserve: page_ref")
+    tokens = _addr(dev, n_tokens, i32, cfg.batch, "kv_pages_reserve: n_tokens")
+    rc = lib().kv_pages_reserve(ctypes.byref(cfg.c()), _cache(dev, cache, "kv_pages_reserve"), ref, tokens,
+                                _status(dev, status, "kv_pages_reserve"), _stream_of(dev, stream))
     _check(rc, "kv_pages_reserve")
 
 
 def kv_seq_fork(cfg: KVConfig, cache: KVCache, page_ref, src, dst, status, stream=None) -> None:
     """Sequence dst[i] becomes a copy of sequence src[i] (int32 [n] each), sharing its whole INT2 pages."""
-    if src.shape != dst.shape:
-        raise KVQError(KVQ_ERR_INVALID_ARG, "kv_seq_fork")
-    rc = lib().kv_seq_fork(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(page_ref), _ptr(src), _ptr(dst),
-                           int(src.shape[0]), _ptr(status), _stream(stream))
+    dev, i32 = _current_device(), torch.int32
+    n = src.numel()
+    ref = _addr(dev, page_ref, i32, cfg.num_pages, "kv_seq_fork: page_ref")
+    a = _addr(dev, src, i32, 0, "kv_seq_fork: src")
+    b = _addr(dev, dst, i32, 0, "kv_seq_fork: dst")
+    if dst.numel() != n:
+        raise KVQError(KVQ_ERR_INVALID_ARG, "kv_seq_fork: src and dst")
+    rc = lib().kv_seq_fork(ctypes.byref(cfg.c()), _cache(dev, cache, "kv_seq_fork"), ref, a, b, n,
+                           _status(dev, status, "kv_seq_fork"), _stream_of(dev, stream))
     _check(rc, "kv_seq_fork")
 
 
 def kv_seq_free(cfg: KVConfig, cache: KVCache, page_ref, seqs, status, stream=None) -> None:
     """Sequences seqs (int32 [n]) give up their pages and become empty."""
-    rc = lib().kv_seq_free(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(page_ref), _ptr(seqs),
-                           int(seqs.shape[0]), _ptr(status), _stream(stream))
+    dev, i32 = _current_device(), torch.int32
+    ref = _addr(dev, page_ref, i32, cfg.num_pages, "kv_seq_free: page_ref")
+    at = _addr(dev, seqs, i32, 0, "kv_seq_free: seqs")
+    rc = lib().kv_seq_free(ctypes.byref(cfg.c()), _cache(dev, cache, "kv_seq_free"), ref, at, seqs.numel(),
+                           _status(dev, status, "kv_seq_free"), _stream_of(dev, stream))
     _check(rc, "kv_seq_free")
 
 
@@ -432,8 +501,12 @@ def kv_pages_compact_workspace_bytes(cfg: KVConfig) -> int:
 
 def kv_pages_compact(cfg: KVConfig, cache: KVCache, page_ref, n_live, workspace, status, stream=None) -> None:
     """Held pages move to ids 0 .. n_live - 1 (n_live int32 [1], out) and the tables follow them."""
-    rc = lib().kv_pages_compact(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), _ptr(page_ref), _ptr(n_live),
-                                _ptr(workspace), _nbytes(workspace), _ptr(status), _stream(stream))
+    dev, i32 = _current_device(), torch.int32
+    ref = _addr(dev, page_ref, i32, cfg.num_pages, "kv_pages_compact: page_ref")
+    live = _addr(dev, n_live, i32, 1, "kv_pages_compact: n_live")
+    ws = _addr(dev, workspace, workspace.dtype, 0, "kv_pages_compact: workspace")
+    rc = lib().kv_pages_compact(ctypes.byref(cfg.c()), _cache(dev, cache, "kv_pages_compact"), ref, live, ws, _nbytes(workspace),
+                                _status(dev, status, "kv_pages_compact"), _stream_of(dev, stream))
     _check(rc, "kv_pages_compact")
 
 
