@@ -215,3 +215,22 @@ def test_a_workspace_of_the_largest_size_serves_smaller_calls():
             _compare(run, q, cu, parent, out, [(2, 3)])
             run.cfg.max_pages_per_seq, run.runner.cache.page_table = was, table
     assert bool((room[n:] == 77).all())
+
+
+@pytest.mark.parametrize("splits", [0, 40])
+def test_tickets_are_zero_after_every_call(splits):
+    """The row kernel's joins of one and of two levels (40 splits of 8 columns): same bits each time, and the
+    tickets at the head of the workspace, three or more a grid row, as they were."""
+    import bit_rotated_kv_gb300 as kvq
+    w = BASE.replace(batch=3, n_q_heads=8, n_kv_heads=2, ctx_lo=3000, ctx_hi=5000)
+    run, q, cu, parent = _drafted(w, [5, 0, 7], "random")
+    run.cfg.attn_splits = splits
+    n = kvq.kv_attn_tree_workspace_bytes(run.cfg, q.shape[0], int(run.runner.cache.seq_len.max()))
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    tickets = ws[:4 * 3 * w.batch * kvq.KVQ_TREE_MAX_NODES * w.n_kv_heads]
+    first = _call(run, q, cu, parent, ws)
+    _compare(run, q, cu, parent, first, [(0, 0), (2, 1)])
+    assert bool((ws != 0).any())                      # (partials were joined through it)
+    for _ in range(3):
+        assert int(run.runner.status.item()) == 0 and not bool(tickets.any())
+        assert torch.equal(_call(run, q, cu, parent, ws).view(torch.int16), first.view(torch.int16))
