@@ -14,12 +14,16 @@
 //   * a lane of S^T is a token, so a token's scale (Delta, norm) is one number per thread, and a
 //     warp reads no scale per score;
 //   * P [token][row] goes to shared memory as the MN-major B operand, 16 bytes per 8 rows.
-// 128 rows a CTA were tried: the expansion is shared by twice the rows, but the softmax and P, which are not,
-// already took as long, and the second score buffer no longer fits.
+// 128 rows a CTA were tried, early on: the expansion is shared by twice the rows, the second score buffer no longer
+// fits.  With groups of 128 it took as long; 16 nodes of 8 heads on 4 x 128 K tokens in groups of 32 took 733 us then,
+// 862 with 64 rows, and the two have not been compared since.
 // Keys.  With one group per row (G = 128) A holds the codes themselves, exact, and the zero point is
 // one more K = 16 step (z against -sum q', hi + lo); Delta multiplies the finished sum.  With more
 // groups A holds Delta c as an fp16 hi + lo pair (13 bits), scaled by a power of two per token, exact for groups down
-// to 2^-25 of the token's largest, and the zero point's step takes Delta z (22 bits, hi + lo).
+// to 2^-25 of the token's largest, and the zero point's step takes Delta z (22 bits, hi + lo).  (Products of the codes as
+// they stand, c 4^s 2^-24, lose bits of groups below 2^-4 of the largest, which large queries of that group bring
+// out; whole numbers are one more instruction a register: 64 sequences of 6,000 tokens, 16 nodes of 4 heads, groups
+// of 64: 385 -> 411 us, groups of 32 and 128 K tokens 782 -> 809.)
 // q' is scaled by a power of two of its row, its largest value to 2^13 .. 2^14: exact down to 2^-22 of that value
 // (8 bits above fp16's last step 2^-24, in slots that carry 4^-4), below it off by at most 2^-30 of it; with more
 // groups to 2^8 .. 2^9 and no slots, exact down to 2^-25, off by at most 2^-33.  Values are dequantized to fp16,
@@ -42,15 +46,17 @@
 // and one that finds the nodes' ancestors; registers are handed from the latter to the softmax.  S has two
 // buffers, so QK(i + 1) and the keys of i + 2 run beside softmax(i) and PV(i - 1).
 //
-// What bounds it: instruction issue, not the tensor pipe or memory.  A tile of 128 tokens takes 9,400 warp
-// instructions (G = 128), more than half of them softmax, 2,300 the values and 1,000 the keys, in 2,600 clocks
-// (1.26 us): the schedulers issue in 72% of their clocks, the pipe of logic, maxima and half precision (one
-// warp instruction in two clocks) is busy for 49%, the tensor pipe for 16%, DRAM reads each byte once.  No
-// part stands out: with its exponentials, its stores of P or the values' stores to TMEM left out the kernel
-// takes as long within 2%, without the keys' stores 3 to 8% less.  8 softmax warps of 32 rows executed 7,900
-// instructions a tile at 58% and took 2.5% longer.  Measured: 64 nodes of 4 heads on 32 K tokens 104 us (330
-// TFLOP/s), 16 nodes of 8 heads on 4 x 128 K tokens 910 us (227 TFLOP/s); a power of two a row, not a CTA, is 4%
-// of that (a query may be of any size beside its neighbours').
+// What bounds it: instruction issue, not the tensor pipe or memory.  A tile of 128 tokens takes 10,000 warp
+// instructions (G = 128; a CTA's set-up included), more than half of them softmax, 2,300 the values and 1,000 the
+// keys, in 2,700 clocks (1.3 us): the schedulers issue in 75% of their clocks, the pipe of logic, maxima and half
+// precision (one warp instruction in two clocks) is busy for 50%, the tensor pipe for 16%, DRAM reads each byte
+// once.  Groups of 32 take 11,700.  No part stands out: with its exponentials, its stores of P or the values' stores
+// to TMEM left out an earlier version took as long within 2%, without the keys' stores 3 to 8% less; 8 softmax
+// warps of 32 rows executed 16% fewer instructions, at 58%, and took 2.5% longer.  Measured: 64 nodes of 4 heads on
+// 32 K tokens 103.6 us (332 TFLOP/s), 16 nodes of 8 heads on 4 x 128 K tokens, groups of 32, 910 us (227 TFLOP/s).  Of
+// those, what keeps results right at the ends of the number range: a power of two a row, not a CTA (a query may
+// be of any size beside its neighbours'), 4% of the latter when it came; pages before windows, which cost the latter
+// 2.5% and sped the former up by 2%.
 // What those figures hang on:
 //   * MMAs are issued from code that the whole warp runs, by one elected lane: from a divergent branch each
 //     costs 53 clocks at least, whatever N is;
@@ -1306,11 +1312,13 @@ using namespace kvq;
 
 // Which kernel a call takes, from its sizes alone.  The row kernel (attn.cu) streams a sequence's cache once
 // for every 8 (node, head) columns, this one once for every 64 at four to five times the time.  So the row
-// kernel has trees of up to 4 groups a tile: 64 sequences of 6,000 tokens take 331 us there and 376 us here with 4,
-// 394 against 377 with 5.  On short contexts, where its windows weigh more, up to 3: 64 sequences of 1,000
-// tokens take 129 against 137 us with 3, 163 against 138 with 4.  It has small calls as well: 16 nodes on 8
-// kv heads take 14.8 us there and 21.6 us here on 2,000 tokens, 20.2 and 21.8 on 4,000; 32 nodes 19.0 and 18.0 on
-// 500, 30.6 and 22.6 on 4,000.  Per-channel keys are the row kernel's alone.
+// kernel has trees of up to 4 groups a tile, the batch's average taken: 64 sequences of 6,000 tokens (groups of 64 /
+// 128) take 393 / 373 us there and 409 / 335 us here with 4, 506 / 481 against 410 / 336 with 5.  On short contexts,
+// where its windows weigh more, up to 3: 64 sequences of 1,000 tokens take 125 against 130 us with 3, 158 against
+// 131 with 4.  It has small calls as well: 16 nodes on 8 kv heads take 15.1 us there and 22.8 us here on 2,000
+// tokens, 20.3 and 22.7 on 4,000; 32 nodes 18.8 and 18.7 on 500, 30.7 and 21.7 on 4,000.  Between those it can be off:
+// one sequence of 100,000 tokens with 8 nodes of 4 heads takes 93 us there and 71 here with 8 kv heads, 26 and
+// 35 with one.  Per-channel keys are the row kernel's alone.
 static bool row_kernel(const kvq_config* cfg, int32_t n_rows, int32_t max_ctx) {
   if (cfg->key_axis != KVQ_KEY_PER_TOKEN) return true;
   const long long per_seq = ((long long)n_rows * (cfg->n_q_heads / cfg->n_kv_heads) + cfg->batch - 1) / cfg->batch;

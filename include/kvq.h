@@ -402,7 +402,9 @@ KVQ_API int kv_tree_commit(const kvq_config* cfg, const kvq_cache* cache, const 
  * sequences in order, so the tables do not depend on timing.  These calls write the page table
  * (cache->page_table must be writable memory), and any call may follow them on the stream.  They
  * run on the stream in order like any other, one pool at a time: two of them must not overlap on
- * the same pool.  At most KVQ_POOL_MAX_SEQS sequences (pairs) per call (KVQ_ERR_UNSUPPORTED). */
+ * the same pool.  A pool is one layer's: every layer has its own pages, page table, lengths and page_ref, and takes
+ * each call itself (kv_seq_fork copies that layer's rows and half-filled page).  A call of n sequences or pairs
+ * looks at every page count of the pool and, kv_seq_fork, at all n pairs for each.  At most KVQ_POOL_MAX_SEQS sequences (pairs) per call (KVQ_ERR_UNSUPPORTED). */
 #define KVQ_POOL_MAX_SEQS 16384
 
 /* kv_pages_reserve: pages for n_tokens[b] (device int32 [B]) more tokens of every sequence, as if
@@ -456,7 +458,7 @@ KVQ_API int kv_attn_decode(const kvq_config* cfg, const kvq_cache* cache, const 
  *           once to bf16 (nearest-even) -- the same kernel, only the final store differs.
  * Arguments, workspace and errors as kv_attn_decode.  For callers whose next GEMM (the
  * output projection, in the T_V space) takes bf16 activations; the rounding adds up to
- * 2^-9 relative per element on top of the float32 result.
+ * 2^-8 relative per element on top of the float32 result.
  * Source: [OSCAR] section 4 "Decoding Attention Kernel" (decode attention over the mixed
  * cache); the output precision is not fixed by the pages. */
 KVQ_API int kv_attn_decode_bf16(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot,
