@@ -66,7 +66,7 @@ KVQ_API const char* kvq_status_string(int code) {
     case KVQ_ERR_UNSUPPORTED: return "unsupported shape or option";
     case KVQ_ERR_CUDA: return "CUDA error";
     case KVQ_ERR_BOUNDS: return "page id, position or ring slot out of range (device)";
-    case KVQ_ERR_NONFINITE: return "non-finite scale, zero point or norm (device)";
+    case KVQ_ERR_NONFINITE: return "non-finite scale, zero point, norm, value or probability (device)";
     case KVQ_ERR_TIMEOUT: return "bounded wait on an asynchronous copy ran out (device)";
     case KVQ_ERR_WORKSPACE: return "workspace too small";
     default: return "unknown status";

@@ -85,7 +85,7 @@ extern "C" {
 #define KVQ_ERR_UNSUPPORTED   (-2)  /* valid but not implemented (head_dim, G, GQA ratio)  */
 #define KVQ_ERR_CUDA          (-3)  /* a CUDA runtime call or launch failed                */
 #define KVQ_ERR_BOUNDS        (-4)  /* device: page id / position / ring slot out of range */
-#define KVQ_ERR_NONFINITE     (-5)  /* device: a scale, zero point or norm is not finite   */
+#define KVQ_ERR_NONFINITE     (-5)  /* device: a scale, zero point, norm, value or probability is not finite */
 #define KVQ_ERR_TIMEOUT       (-6)  /* device: a bounded wait on an async copy ran out     */
 #define KVQ_ERR_WORKSPACE     (-7)  /* workspace smaller than kv_attn_workspace_bytes()    */
 
