@@ -213,8 +213,8 @@ def _prepare_rope(case, seed):
         for name in ("seq_len", "s_quant", "sink_k", "sink_v", "ring_k", "ring_v"):
             setattr(c, name, s[name])
         s["cache"] = c
-        s["tr"] = kvq.Transform(kvq.KVQ_TRANSFORM_HADAMARD if case["transform"] == "hadamard" else kvq.KVQ_TRANSFORM_DENSE, s["tk"], s["tkit"],
-                                s["tv"])
+        s["tr"] = kvq.Transform(kvq.KVQ_TRANSFORM_HADAMARD if case["transform"] == "hadamard" else kvq.KVQ_TRANSFORM_DENSE,
+                                *(t if t is None else t.contiguous() for t in (s["tk"], s["tkit"], s["tv"])))
         kinds = {"none": kvq.KVQ_ROPE_PLAIN, "linear": kvq.KVQ_ROPE_LINEAR, "ntk": kvq.KVQ_ROPE_NTK, "bands": kvq.KVQ_ROPE_BANDS,
                  "yarn": kvq.KVQ_ROPE_YARN}
         context, a, b = {"bands": (8192.0, 1.0, 4.0), "yarn": (32768.0, 32.0, 1.0)}.get(case["scaling"], (0.0, 0.0, 0.0))
