@@ -9,8 +9,10 @@ Entry points (same names as the C ABI in include/kvq.h):
   kv_rotate_qk, kv_quant_flush, kv_attn_decode, kv_attn_decode_bf16, kv_attn_workspace_bytes,
   kv_attn_tree, kv_verify_tree, kv_tree_commit (a tree of drafted tokens: attention, check, rows kept),
   kv_pages_reserve, kv_seq_fork, kv_seq_free, kv_pages_compact (the page pool),
+  kv_rope_qk, kvq_rope_frequencies (norm, rotary positions, transform and append of a step's rows),
+  kv_logits_probs, kv_token_counts (logits to probabilities, and what the penalties go by),
   kvq_page_head_bytes, kvq_page_bytes, kvq_status_string
-plus ``KVConfig`` / ``KVCache`` helpers that allocate the caller-owned buffers.
+plus ``KVConfig`` / ``KVCache`` / ``Rope`` helpers that allocate the caller-owned buffers.
 """
 
 from __future__ import annotations
@@ -41,11 +43,26 @@ KVQ_KEY_PER_TOKEN = 0
 KVQ_KEY_PER_CHANNEL = 1
 KVQ_TREE_MAX_NODES = 128
 KVQ_POOL_MAX_SEQS = 16384
+KVQ_ROPE_HALF = 0
+KVQ_ROPE_INTERLEAVED = 1
+KVQ_ROPE_PLAIN = 0
+KVQ_ROPE_LINEAR = 1
+KVQ_ROPE_NTK = 2
+KVQ_ROPE_BANDS = 3
+KVQ_ROPE_YARN = 4
+KVQ_COUNT_MOST = 32767
+KVQ_COUNT_PROMPT = 0
+KVQ_COUNT_OUTPUT = 1
+KVQ_LOGITS_F32 = 0
+KVQ_LOGITS_BF16 = 1
+KVQ_LOGITS_F16 = 2
+KVQ_LOGITS_MAX_VOCAB = 524288
 
 EXPORTED = ("kv_rotate_qk", "kv_quant_flush", "kv_append_chunk", "kv_attn_chunk", "kv_attn_chunk_workspace_bytes", "kv_attn_decode", "kv_attn_decode_bf16", "kv_attn_decode_noalloc",
             "kv_attn_workspace_bytes",
             "kv_attn_tree", "kv_attn_tree_workspace_bytes", "kv_verify_tree", "kv_tree_commit",
             "kv_pages_reserve", "kv_seq_fork", "kv_seq_free", "kv_pages_compact", "kv_pages_compact_workspace_bytes",
+            "kv_rope_qk", "kvq_rope_frequencies", "kv_logits_probs", "kv_token_counts",
             "kvq_page_head_bytes", "kvq_page_bytes", "kvq_status_string", "kvq_version",
             "kvq_selftest_scale_division", "kvq_selftest_tc_integer_sums")
 
@@ -66,6 +83,19 @@ class CCache(ctypes.Structure):
 class CTransform(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("reserved", ctypes.c_int32), ("t_k", ctypes.c_void_p),
                 ("t_k_inv_t", ctypes.c_void_p), ("t_v", ctypes.c_void_p)]
+
+
+class CRope(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("scale", ctypes.c_float), ("norm_eps", ctypes.c_float),
+                ("freq", ctypes.c_void_p), ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p)]
+
+
+class CLogitRules(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_void_p), ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p), ("counts", ctypes.c_void_p), ("count_stride", ctypes.c_int64),
+                ("bias_cu", ctypes.c_void_p), ("bias_token", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+                ("mask_stride", ctypes.c_int64), ("mask_row", ctypes.c_void_p), ("n_bias", ctypes.c_int32),
+                ("n_masks", ctypes.c_int32)]
 
 
 class KVQError(RuntimeError):
@@ -116,6 +146,16 @@ def lib() -> ctypes.CDLL:
         l.kv_pages_compact.restype = ctypes.c_int
         l.kv_pages_compact_workspace_bytes.argtypes = [P(CConfig)]
         l.kv_pages_compact_workspace_bytes.restype = sz
+        dbl = ctypes.c_double
+        l.kvq_rope_frequencies.argtypes = [i32, dbl, i32, dbl, dbl, dbl, dbl, vp, vp]
+        l.kvq_rope_frequencies.restype = ctypes.c_int
+        l.kv_rope_qk.argtypes = [P(CConfig), P(CTransform), P(CRope), vp, i64, vp, vp, i32, vp, i64, vp, i64, vp, vp, vp, i32,
+                                 P(CCache), vp, vp]
+        l.kv_rope_qk.restype = ctypes.c_int
+        l.kv_logits_probs.argtypes = [P(CConfig), P(CLogitRules), vp, i32, i64, i32, vp, vp, vp, i32, vp, i64, vp, vp]
+        l.kv_logits_probs.restype = ctypes.c_int
+        l.kv_token_counts.argtypes = [P(CConfig), vp, i64, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp]
+        l.kv_token_counts.restype = ctypes.c_int
         l.kv_attn_decode.argtypes = [P(CConfig), P(CCache), vp, vp, ctypes.c_float, i32, vp, sz, vp, vp]
         l.kv_attn_decode.restype = ctypes.c_int
         l.kv_attn_decode_bf16.argtypes = [P(CConfig), P(CCache), vp, vp, ctypes.c_float, i32, vp, sz, vp, vp]
@@ -508,6 +548,195 @@ def kv_pages_compact(cfg: KVConfig, cache: KVCache, page_ref, n_live, workspace,
     rc = lib().kv_pages_compact(ctypes.byref(cfg.c()), _cache(dev, cache, "kv_pages_compact"), ref, live, ws, _nbytes(workspace),
                                 _status(dev, status, "kv_pages_compact"), _stream_of(dev, stream))
     _check(rc, "kv_pages_compact")
+
+
+def kvq_rope_frequencies(rot_dim: int, theta: float, scaling: int = KVQ_ROPE_PLAIN, factor: float = 1.0, context: float = 0.0,
+                         a: float = 0.0, b: float = 0.0):
+    """(freq, scale): turns per token of every pair in units of 2^-64, as an int64 host tensor of the same bits,
+    and the factor of the rotated channels."""
+    freq = torch.zeros(max(0, int(rot_dim) // 2), dtype=torch.int64)
+    scale = ctypes.c_float(1.0)
+    rc = lib().kvq_rope_frequencies(int(rot_dim), float(theta), int(scaling), float(factor), float(context), float(a), float(b),
+                                    freq.data_ptr() if len(freq) else None, ctypes.byref(scale))
+    _check(rc, "kvq_rope_frequencies")
+    return freq, float(scale.value)
+
+
+@dataclass
+class Rope:
+    """Rotary positions and the norms of query and key heads (see kvq_rope in include/kvq.h)."""
+    layout: int
+    rot_dim: int
+    freq: torch.Tensor | None            # [rot_dim / 2] int64 (the bits of uint64) on the device
+    scale: float = 1.0
+    q_norm: torch.Tensor | None = None   # [d] float32 on the device
+    k_norm: torch.Tensor | None = None
+    norm_eps: float = 1e-6
+
+    @classmethod
+    def make(cls, layout: int, rot_dim: int, theta: float, scaling: int = KVQ_ROPE_PLAIN, factor: float = 1.0, context: float = 0.0,
+             a: float = 0.0, b: float = 0.0, q_norm=None, k_norm=None, norm_eps: float = 1e-6, device="cuda") -> "Rope":
+        """With the frequencies of kvq_rope_frequencies."""
+        freq, scale = kvq_rope_frequencies(rot_dim, theta, scaling, factor, context, a, b)
+        return cls(layout, int(rot_dim), freq.to(device), scale, q_norm, k_norm, norm_eps)
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name != "_cc":
+            object.__setattr__(self, "_cc", None)
+
+    def c(self, dev: int) -> CRope:
+        """The C struct (built once for a device, again after a field changes)."""
+        cc = self.__dict__.get("_cc")
+        if cc is None or cc[0] != dev:
+            f32 = torch.float32
+            norm = [0 if w is None else _addr(dev, w, f32, 128, f"kv_rope_qk: {n}") for n, w in (("q_norm", self.q_norm), ("k_norm", self.k_norm))]
+            cc = (dev, CRope(int(self.layout), int(self.rot_dim), float(self.scale), float(self.norm_eps),
+                             _addr(dev, self.freq, torch.int64, max(0, int(self.rot_dim) // 2), "kv_rope_qk: freq"), *norm))
+            object.__setattr__(self, "_cc", cc)
+        return cc[1]
+
+
+def _head_rows(dev: int, t, n: int, heads: int, what: str):
+    """Address and row stride of [n, heads, 128] bf16, each row's heads one after another."""
+    if t is None:
+        if n > 0:
+            raise KVQError(KVQ_ERR_INVALID_ARG, what)
+        return 0, heads * 128
+    if (t.dim() != 3 or t.dtype is not torch.bfloat16 or t.shape[0] != n or t.shape[1] != heads or t.shape[2] != 128 or t.stride(2) != 1
+            or (heads > 1 and t.stride(1) != 128) or (n > 1 and t.stride(0) < heads * 128)):
+        raise KVQError(KVQ_ERR_INVALID_ARG, what)
+    if t.get_device() != dev:
+        raise KVQError(KVQ_ERR_INVALID_ARG, f"{what} (another device)")
+    return t.data_ptr(), t.stride(0) if n > 1 else heads * 128
+
+
+def kv_rope_qk(cfg: KVConfig, tr: Transform, rope: Rope | None, q, q_out, q_pos, k, v, seq_idx, pos, rope_pos, cache: KVCache,
+               status, stream=None) -> None:
+    """q [n, Hq, d] -> q_out (contiguous); k, v [m, Hkv, d] into the cache at (seq_idx[r], pos[r]): norm of the heads, rotation
+    by q_pos [n] and rope_pos [m] (None: pos), transform.  q, k, v may be views of one fused projection [n, Hq + 2 Hkv, d]."""
+    dev, i32 = _current_device(), torch.int32
+    n_q = 0 if q is None else q.shape[0]
+    n_kv = 0 if k is None else k.shape[0]
+    qa, qs = _head_rows(dev, q, n_q, cfg.n_q_heads, "kv_rope_qk: q")
+    ka, ks = _head_rows(dev, k, n_kv, cfg.n_kv_heads, "kv_rope_qk: k")
+    va, vs = _head_rows(dev, v, n_kv, cfg.n_kv_heads, "kv_rope_qk: v")
+    out = _addr(dev, q_out, torch.bfloat16, n_q * cfg.n_q_heads * 128, "kv_rope_qk: q_out")
+    turned = rope is not None and rope.rot_dim > 0
+    qp = _addr(dev, q_pos, i32, n_q, "kv_rope_qk: q_pos") if turned or q_pos is not None else 0
+    seq = _addr(dev, seq_idx, i32, n_kv, "kv_rope_qk: seq_idx")
+    at = _addr(dev, pos, i32, n_kv, "kv_rope_qk: pos")
+    far = 0 if rope_pos is None else _addr(dev, rope_pos, i32, n_kv, "kv_rope_qk: rope_pos")
+    rc = lib().kv_rope_qk(ctypes.byref(cfg.c()), ctypes.byref(_transform(dev, tr, cfg)),
+                          None if rope is None else ctypes.byref(rope.c(dev)), qa, qs, out, qp, n_q, ka, ks, va, vs, seq, at, far, n_kv,
+                          _cache(dev, cache, "kv_rope_qk"), _status(dev, status, "kv_rope_qk"), _stream_of(dev, stream))
+    _check(rc, "kv_rope_qk")
+
+
+def _transform(dev: int, tr: Transform, cfg: KVConfig) -> CTransform:
+    for name in ("t_k", "t_k_inv_t", "t_v"):
+        t = getattr(tr, name)
+        if t is not None:
+            _addr(dev, t, torch.float32, cfg.n_kv_heads * 128 * 128, f"kv_rope_qk: {name}")
+    return tr.c()
+
+
+@dataclass
+class LogitRules:
+    """What kv_logits_probs applies (see kvq_logit_rules in include/kvq.h); None: not that rule."""
+    temperature: torch.Tensor | None = None   # [batch] float32; so the next three
+    repetition: torch.Tensor | None = None
+    frequency: torch.Tensor | None = None
+    presence: torch.Tensor | None = None
+    counts: torch.Tensor | None = None        # [batch, >= vocab] int16 (the bits of uint16), as kv_token_counts keeps it
+    bias_cu: torch.Tensor | None = None       # [batch + 1] int32
+    bias_token: torch.Tensor | None = None    # [n] int32
+    bias: torch.Tensor | None = None          # [n] float32
+    mask: torch.Tensor | None = None          # [masks, >= vocab / 32] int32
+    mask_row: torch.Tensor | None = None      # [rows] int32
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name != "_cc":
+            object.__setattr__(self, "_cc", None)
+
+    def c(self, dev: int, batch: int, rows: int, vocab: int) -> CLogitRules:
+        """The C struct (built once for these sizes, again after a field changes)."""
+        key = (dev, batch, rows, vocab)
+        cc = self.__dict__.get("_cc")
+        if cc is None or cc[0] != key:
+            w, i32, f32 = "kv_logits_probs", torch.int32, torch.float32
+            per_seq = [0 if t is None else _addr(dev, t, f32, batch, f"{w}: {n}")
+                       for n, t in (("temperature", self.temperature), ("repetition", self.repetition), ("frequency", self.frequency),
+                                    ("presence", self.presence))]
+            counts, stride = (0, 0) if self.counts is None else _count_rows(dev, self.counts, batch, vocab, w)
+            n_bias = 0 if self.bias_token is None else self.bias_token.numel()
+            biases = [0, 0, 0]
+            if self.bias_cu is not None:
+                biases = [_addr(dev, self.bias_cu, i32, batch + 1, f"{w}: bias_cu"), _addr(dev, self.bias_token, i32, 0, f"{w}: bias_token"),
+                          _addr(dev, self.bias, f32, n_bias, f"{w}: bias")]
+            mask, mask_stride, masks, mask_row = 0, 0, 0, 0
+            if self.mask is not None:
+                m = self.mask
+                if m.dim() != 2 or m.dtype is not i32 or m.shape[1] < (vocab + 31) // 32 or not m.is_contiguous():
+                    raise KVQError(KVQ_ERR_INVALID_ARG, f"{w}: mask")
+                mask, mask_stride, masks = _addr(dev, m, i32, 0, f"{w}: mask"), m.shape[1], m.shape[0]
+                mask_row = 0 if self.mask_row is None else _addr(dev, self.mask_row, i32, rows, f"{w}: mask_row")
+            cc = (key, CLogitRules(*per_seq, counts, stride, *biases, mask, mask_stride, mask_row, n_bias, masks))
+            object.__setattr__(self, "_cc", cc)
+        return cc[1]
+
+
+def _count_rows(dev: int, t, batch: int, vocab: int, where: str):
+    """Address and row stride of [batch, >= vocab] counts."""
+    if (t is None or t.dim() != 2 or t.dtype is not torch.int16 or t.shape[0] != batch or t.shape[1] < vocab or t.shape[1] % 2
+            or not t.is_contiguous()):
+        raise KVQError(KVQ_ERR_INVALID_ARG, f"{where}: counts")
+    return _addr(dev, t, torch.int16, 0, f"{where}: counts"), t.shape[1]
+
+
+_LOGIT_TYPES = {torch.float32: KVQ_LOGITS_F32, torch.bfloat16: KVQ_LOGITS_BF16, torch.float16: KVQ_LOGITS_F16}
+
+
+def kv_logits_probs(cfg: KVConfig, rules: LogitRules | None, logits, cu_rows, parent, token, p, status, stream=None) -> None:
+    """logits [n, vocab] (float32, bfloat16 or float16; rows contiguous) -> p [n, vocab] float32 (for float32 logits it may be
+    the same tensor): rows cu_rows[b] .. cu_rows[b+1]-1 are sequence b's.  parent, token [n] int32: a tree of drafts, or None."""
+    dev, i32, w = _current_device(), torch.int32, "kv_logits_probs"
+    if logits.dim() != 2 or logits.dtype not in _LOGIT_TYPES:
+        raise KVQError(KVQ_ERR_INVALID_ARG, f"{w}: logits")
+    n, vocab = logits.shape
+    if (vocab > 1 and logits.stride(1) != 1) or (n > 1 and logits.stride(0) < vocab):
+        raise KVQError(KVQ_ERR_INVALID_ARG, f"{w}: logits")
+    if logits.get_device() != dev:
+        raise KVQError(KVQ_ERR_INVALID_ARG, f"{w}: logits (another device)")
+    if p is None:
+        raise KVQError(KVQ_ERR_INVALID_ARG, f"{w}: p")
+    pa, ps = _prob_rows(dev, p, n, vocab, f"{w}: p")
+    cu = _addr(dev, cu_rows, i32, cfg.batch + 1, f"{w}: cu_rows")
+    par = 0 if parent is None else _addr(dev, parent, i32, n, f"{w}: parent")
+    tok = 0 if token is None else _addr(dev, token, i32, n, f"{w}: token")
+    rc = lib().kv_logits_probs(ctypes.byref(cfg.c()), None if rules is None else ctypes.byref(rules.c(dev, cfg.batch, n, vocab)),
+                               logits.data_ptr(), _LOGIT_TYPES[logits.dtype], logits.stride(0) if n > 1 else vocab, vocab, cu, par, tok, n,
+                               pa, ps if n > 1 else vocab, _status(dev, status, w), _stream_of(dev, stream))
+    _check(rc, w)
+
+
+def kv_token_counts(cfg: KVConfig, counts, vocab: int, kind: int, cu_rows, token, path, n_accept, next_token, status,
+                    stream=None) -> None:
+    """counts [batch, >= vocab, even] int16 (the bits of uint16; zero for a new sequence): rows cu_rows[b] .. cu_rows[b+1]-1 of
+    token [n] marked as sequence b's prompt or counted as generated; with path [n] and n_accept [batch] the kept nodes' only, and
+    with next_token [batch] the token behind them."""
+    dev, i32, w = _current_device(), torch.int32, "kv_token_counts"
+    n = 0 if token is None else token.numel()
+    at, stride = _count_rows(dev, counts, cfg.batch, vocab, w)
+    cu = _addr(dev, cu_rows, i32, cfg.batch + 1 if n else 0, f"{w}: cu_rows")
+    tok = _addr(dev, token, i32, n, f"{w}: token")
+    kept = 0 if path is None else _addr(dev, path, i32, n, f"{w}: path")
+    acc = 0 if n_accept is None else _addr(dev, n_accept, i32, cfg.batch, f"{w}: n_accept")
+    nxt = 0 if next_token is None else _addr(dev, next_token, i32, cfg.batch, f"{w}: next_token")
+    rc = lib().kv_token_counts(ctypes.byref(cfg.c()), at, stride, int(vocab), int(kind), cu, tok, n, kept, acc, nxt,
+                               _status(dev, status, w), _stream_of(dev, stream))
+    _check(rc, w)
 
 
 def kvq_selftest_scale_division(mismatches, stream=None) -> None:

@@ -3,6 +3,8 @@
 #include "common.cuh"
 #include "launch.h"
 
+#include <cmath>
+
 namespace {
 
 using namespace kvq;
@@ -43,6 +45,16 @@ int check_cache(const kvq_config* c, const kvq_cache* k) {
   return KVQ_OK;
 }
 
+// Whether [a, a + na) and [b, b + nb) have bytes in common.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  return (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
+}
+
+// Rows of bf16 heads, `stride` elements apart, read 16 bytes at a time.
+bool head_rows(const void* p, int64_t stride, int32_t heads) {
+  return p && aligned(p, 16) && stride >= (int64_t)heads * kHeadDim && stride % 8 == 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -66,7 +78,7 @@ KVQ_API const char* kvq_status_string(int code) {
     case KVQ_ERR_UNSUPPORTED: return "unsupported shape or option";
     case KVQ_ERR_CUDA: return "CUDA error";
     case KVQ_ERR_BOUNDS: return "page id, position or ring slot out of range (device)";
-    case KVQ_ERR_NONFINITE: return "non-finite scale, zero point, norm, value or probability (device)";
+    case KVQ_ERR_NONFINITE: return "non-finite scale, zero point, norm, value, logit or probability (device)";
     case KVQ_ERR_TIMEOUT: return "bounded wait on an asynchronous copy ran out (device)";
     case KVQ_ERR_WORKSPACE: return "workspace too small";
     default: return "unknown status";
@@ -112,6 +124,128 @@ KVQ_API int kv_rotate_qk(const kvq_config* cfg, const kvq_transform* tr, const u
   kvq_cache empty{};
   return kvq_launch_rotate(cfg, tr, q, q_out, n_q_rows, k, v, seq_idx, pos, n_kv_rows,
                            n_kv_rows > 0 ? cache : &empty, d_status, (cudaStream_t)stream);
+}
+
+KVQ_API int kvq_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling, double factor, double context, double a,
+                                 double b, uint64_t* freq, float* scale) {
+  if (rot_dim < 0 || rot_dim > kHeadDim || rot_dim % 2 || (rot_dim > 0 && !freq)) return KVQ_ERR_INVALID_ARG;
+  if (!(theta > 1.0) || !std::isfinite(theta) || !(factor > 0.0) || !std::isfinite(factor)) return KVQ_ERR_INVALID_ARG;
+  if (scaling < KVQ_ROPE_PLAIN || scaling > KVQ_ROPE_YARN) return KVQ_ERR_INVALID_ARG;
+  if (scaling == KVQ_ROPE_NTK && rot_dim <= 2) return KVQ_ERR_INVALID_ARG;
+  const bool ranged = scaling == KVQ_ROPE_BANDS || scaling == KVQ_ROPE_YARN;
+  if (ranged && !(std::isfinite(context) && std::isfinite(a) && std::isfinite(b) && context > 0.0 && a > 0.0 && b > 0.0 &&
+                  (scaling == KVQ_ROPE_BANDS ? a < b : a > b)))
+    return KVQ_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925;
+  if (scaling == KVQ_ROPE_NTK) theta *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+  double lo = 0.0, hi = 0.0;
+  if (scaling == KVQ_ROPE_YARN) {
+    auto at = [&](double turns) { return rot_dim * std::log(context / (turns * two_pi)) / (2.0 * std::log(theta)); };
+    lo = std::fmin(std::fmax(std::floor(at(a)), 0.0), rot_dim - 1.0);
+    hi = std::fmin(std::fmax(std::ceil(at(b)), 0.0), rot_dim - 1.0);
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double w = std::pow(theta, -2.0 * i / rot_dim);
+    double kept = 1.0;                                    // the share that is not divided by factor
+    if (scaling == KVQ_ROPE_LINEAR) kept = 0.0;
+    if (scaling == KVQ_ROPE_BANDS) kept = std::fmin(std::fmax((context * w / two_pi - a) / (b - a), 0.0), 1.0);
+    if (scaling == KVQ_ROPE_YARN) kept = 1.0 - std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 1e-3), 0.0), 1.0);
+    w = w / factor * (1.0 - kept) + w * kept;
+    const double turns = w / two_pi;                      // of a turn; whole turns drop out
+    freq[i] = (uint64_t)std::ldexp(turns - std::floor(turns), 64);
+  }
+  if (scale) *scale = scaling == KVQ_ROPE_YARN && factor > 1.0 ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+  return KVQ_OK;
+}
+
+KVQ_API int kv_rope_qk(const kvq_config* cfg, const kvq_transform* tr, const kvq_rope* rope, const uint16_t* q,
+                       int64_t q_stride, uint16_t* q_out, const int32_t* q_pos, int32_t n_q_rows, const uint16_t* k,
+                       int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* seq_idx, const int32_t* pos,
+                       const int32_t* rope_pos, int32_t n_kv_rows, const kvq_cache* cache, int32_t* d_status,
+                       void* stream) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  if (!tr || (tr->kind != KVQ_TRANSFORM_DENSE && tr->kind != KVQ_TRANSFORM_HADAMARD)) return KVQ_ERR_INVALID_ARG;
+  if (n_q_rows < 0 || n_kv_rows < 0) return KVQ_ERR_INVALID_ARG;
+  if (rope) {
+    if (rope->layout != KVQ_ROPE_HALF && rope->layout != KVQ_ROPE_INTERLEAVED) return KVQ_ERR_INVALID_ARG;
+    if (rope->rot_dim < 0 || rope->rot_dim > kHeadDim || rope->rot_dim % 2) return KVQ_ERR_INVALID_ARG;
+    if (rope->rot_dim > 0 && (!rope->freq || !aligned(rope->freq, 8) || !std::isfinite(rope->scale)))
+      return KVQ_ERR_INVALID_ARG;
+    if (!aligned(rope->q_norm, 16) || !aligned(rope->k_norm, 16)) return KVQ_ERR_INVALID_ARG;
+    if ((rope->q_norm || rope->k_norm) && !(std::isfinite(rope->norm_eps) && rope->norm_eps >= 0.0f))
+      return KVQ_ERR_INVALID_ARG;
+  }
+  const bool turned = rope && rope->rot_dim > 0;
+  if (n_q_rows > 0) {
+    if (!head_rows(q, q_stride, cfg->n_q_heads) || !q_out || !aligned(q_out, 16)) return KVQ_ERR_INVALID_ARG;
+    if ((turned && !q_pos) || !aligned(q_pos, 4)) return KVQ_ERR_INVALID_ARG;
+    if (tr->kind == KVQ_TRANSFORM_DENSE && (!tr->t_k_inv_t || !aligned(tr->t_k_inv_t, 16))) return KVQ_ERR_INVALID_ARG;
+    const size_t row = (size_t)cfg->n_q_heads * kHeadDim * 2;
+    if (overlap(q, (size_t)(n_q_rows - 1) * q_stride * 2 + row, q_out, n_q_rows * row)) return KVQ_ERR_INVALID_ARG;
+  }
+  if (n_kv_rows > 0) {
+    rc = check_cache(cfg, cache);
+    if (rc) return rc;
+    if (!head_rows(k, k_stride, cfg->n_kv_heads) || !head_rows(v, v_stride, cfg->n_kv_heads) || !seq_idx || !pos)
+      return KVQ_ERR_INVALID_ARG;
+    if (!aligned(seq_idx, 4) || !aligned(pos, 4) || !aligned(rope_pos, 4)) return KVQ_ERR_INVALID_ARG;
+    if (tr->kind == KVQ_TRANSFORM_DENSE && (!tr->t_k || !aligned(tr->t_k, 16))) return KVQ_ERR_INVALID_ARG;
+    if (tr->t_v && !aligned(tr->t_v, 16)) return KVQ_ERR_INVALID_ARG;
+  }
+  if (n_q_rows == 0 && n_kv_rows == 0) return KVQ_OK;
+  kvq_cache empty{};
+  return kvq_launch_rope(cfg, tr, rope, q, q_stride, q_out, q_pos, n_q_rows, k, k_stride, v, v_stride, seq_idx, pos,
+                         rope_pos, n_kv_rows, n_kv_rows > 0 ? cache : &empty, d_status, (cudaStream_t)stream);
+}
+
+KVQ_API int kv_logits_probs(const kvq_config* cfg, const kvq_logit_rules* rules, const void* logits, int32_t logits_type,
+                            int64_t l_stride, int32_t vocab, const int32_t* cu_rows, const int32_t* parent,
+                            const int32_t* token, int32_t n_rows, float* p, int64_t p_stride, int32_t* d_status,
+                            void* stream) {
+  const int rc = check_config(cfg);
+  if (rc) return rc;
+  if (logits_type != KVQ_LOGITS_F32 && logits_type != KVQ_LOGITS_BF16 && logits_type != KVQ_LOGITS_F16)
+    return KVQ_ERR_INVALID_ARG;
+  if (n_rows < 0 || vocab < 1 || !cu_rows || !aligned(cu_rows, 4)) return KVQ_ERR_INVALID_ARG;
+  if (vocab > KVQ_LOGITS_MAX_VOCAB) return KVQ_ERR_UNSUPPORTED;
+  if (!parent != !token || !aligned(parent, 4) || !aligned(token, 4)) return KVQ_ERR_INVALID_ARG;
+  if (rules) {
+    const kvq_logit_rules& u = *rules;
+    if (!aligned(u.temperature, 4) || !aligned(u.repetition, 4) || !aligned(u.frequency, 4) || !aligned(u.presence, 4))
+      return KVQ_ERR_INVALID_ARG;
+    if (u.counts && (!aligned(u.counts, 4) || u.count_stride < vocab || u.count_stride % 2)) return KVQ_ERR_INVALID_ARG;
+    if (u.bias_cu && (u.n_bias < 0 || !aligned(u.bias_cu, 4) || (u.n_bias > 0 && (!u.bias_token || !u.bias)) ||
+                      !aligned(u.bias_token, 4) || !aligned(u.bias, 4)))
+      return KVQ_ERR_INVALID_ARG;
+    if (u.mask && (u.n_masks < 0 || !aligned(u.mask, 4) || u.mask_stride < (vocab + 31) / 32 || !aligned(u.mask_row, 4)))
+      return KVQ_ERR_INVALID_ARG;
+  }
+  if (n_rows == 0) return KVQ_OK;
+  const size_t size = logits_type == KVQ_LOGITS_F32 ? 4 : 2;
+  if (!logits || !aligned(logits, size) || !p || !aligned(p, 4) || l_stride < vocab || p_stride < vocab)
+    return KVQ_ERR_INVALID_ARG;
+  const bool in_place = size == 4 && logits == (const void*)p && l_stride == p_stride;
+  if (!in_place && overlap(logits, ((size_t)(n_rows - 1) * l_stride + vocab) * size, p, ((size_t)(n_rows - 1) * p_stride + vocab) * 4))
+    return KVQ_ERR_INVALID_ARG;
+  return kvq_launch_logits_probs(cfg, rules, logits, logits_type, l_stride, vocab, cu_rows, parent, token, n_rows, p,
+                                 p_stride, d_status, (cudaStream_t)stream);
+}
+
+KVQ_API int kv_token_counts(const kvq_config* cfg, uint16_t* counts, int64_t count_stride, int32_t vocab, int32_t kind,
+                            const int32_t* cu_rows, const int32_t* token, int32_t n_rows, const int32_t* path,
+                            const int32_t* n_accept, const int32_t* next_token, int32_t* d_status, void* stream) {
+  const int rc = check_config(cfg);
+  if (rc) return rc;
+  if (kind != KVQ_COUNT_PROMPT && kind != KVQ_COUNT_OUTPUT) return KVQ_ERR_INVALID_ARG;
+  if (n_rows < 0 || vocab < 1 || !counts || !aligned(counts, 4) || count_stride < vocab || count_stride % 2)
+    return KVQ_ERR_INVALID_ARG;
+  if (kind == KVQ_COUNT_PROMPT && (path || n_accept || next_token)) return KVQ_ERR_INVALID_ARG;
+  if (!path != !n_accept || !aligned(path, 4) || !aligned(n_accept, 4) || !aligned(next_token, 4))
+    return KVQ_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!cu_rows || !token || !aligned(cu_rows, 4) || !aligned(token, 4))) return KVQ_ERR_INVALID_ARG;
+  return kvq_launch_token_counts(cfg, counts, count_stride, vocab, kind, cu_rows, token, n_rows, path, n_accept, next_token,
+                                 d_status, (cudaStream_t)stream);
 }
 
 KVQ_API int kv_quant_flush(const kvq_config* cfg, const kvq_cache* cache, int32_t max_tokens_per_seq,

@@ -48,6 +48,18 @@ int kvq_launch_pages_compact(const kvq_config* cfg, const kvq_cache* cache, int3
                              void* ws, int32_t* d_status, cudaStream_t stream);
 int kvq_launch_attn_noalloc(const kvq_config* cfg, const kvq_cache* cache, const uint16_t* q_rot, float* out,
                             float sm_scale, int32_t max_ctx, int32_t* d_status, cudaStream_t stream);
+int kvq_launch_rope(const kvq_config* cfg, const kvq_transform* tr, const kvq_rope* rope, const uint16_t* q,
+                    int64_t q_stride, uint16_t* q_out, const int32_t* q_pos, int32_t n_q_rows, const uint16_t* k,
+                    int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* seq_idx, const int32_t* pos,
+                    const int32_t* rope_pos, int32_t n_kv_rows, const kvq_cache* cache, int32_t* d_status,
+                    cudaStream_t stream);
+int kvq_launch_logits_probs(const kvq_config* cfg, const kvq_logit_rules* rules, const void* logits, int32_t logits_type,
+                            int64_t l_stride, int32_t vocab, const int32_t* cu_rows, const int32_t* parent,
+                            const int32_t* token, int32_t n_rows, float* p, int64_t p_stride, int32_t* d_status,
+                            cudaStream_t stream);
+int kvq_launch_token_counts(const kvq_config* cfg, uint16_t* counts, int64_t count_stride, int32_t vocab, int32_t kind,
+                            const int32_t* cu_rows, const int32_t* token, int32_t n_rows, const int32_t* path,
+                            const int32_t* n_accept, const int32_t* next_token, int32_t* d_status, cudaStream_t stream);
 int kvq_launch_div_selftest(unsigned long long* d_mismatches, cudaStream_t stream);
 int kvq_launch_tc_selftest(unsigned long long* d_mismatches, cudaStream_t stream);
 size_t kvq_attn_counter_bytes(const kvq_config* cfg, int32_t max_ctx);

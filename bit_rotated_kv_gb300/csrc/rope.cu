@@ -1,0 +1,241 @@
+// kv_rope_qk: norm of the heads, rotary positions, per-head transform and append of a step's rows.
+//
+// Source: [WUSH] inference algorithm and [OScaR] algorithm, key and query processing (the transform follows
+// the rotation); the norm and the rotation are the models' own.
+//   y = w x / sqrt(mean x^2 + eps);  (y_a, y_b) <- s (y_a cos f - y_b sin f, y_b cos f + y_a sin f);  out = T y
+// in float32 with one rounding to bf16 at the end.  A phase f is position * freq mod 2^64 (units of 2^-64 turns):
+// whole numbers lose nothing at far positions, where a float32 angle of 10^5 radians is off by 2^-8.
+//
+// This file: the kernel for the rows of few tokens, on the CUDA cores.  A CTA takes a slice of 32 outputs of one
+// matrix and a chunk of the (row, head) pairs that share it: a whole matrix to a CTA would leave most SMs without
+// one at a single token (8 kv heads, 3 matrices each), and its 64 KB would be the longest wait of the call.  The
+// four slices of a pair each place its row (norm and rotation), which costs less than passing it on would.
+#include "rope.cuh"
+
+#include <algorithm>
+
+namespace kvq {
+namespace {
+
+constexpr int kSlice = 32;                        // outputs of a CTA
+constexpr int kSlices = kHeadDim / kSlice;
+constexpr int kRopeThreads = 4 * kSlice;          // four threads to an output, 32 inputs each
+constexpr int kRopeWarps = kRopeThreads / 32;
+constexpr int kMaxRows = 16;                      // pairs of a chunk
+constexpr int kMaxCopies = 8;                     // rows a warp copies
+
+// One warp places a row: norm and rotation, float32, into shared memory.  False when the row is not finite.
+__device__ __forceinline__ bool place_row(const RopeParams& P, int tt, int row, int head, float* y, int lane) {
+  const uint2 raw = *reinterpret_cast<const uint2*>(rope_src(P, tt, row, head) + 4 * lane);
+  float x[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u), __uint_as_float(raw.y << 16),
+                __uint_as_float(raw.y & 0xffff0000u)};
+  bool fine = !bf16_pair_odd(raw.x) && !bf16_pair_odd(raw.y);
+  const float* w = P.norm[tt];
+  if (w) {
+    float ss = fmaf(x[3], x[3], fmaf(x[2], x[2], fmaf(x[1], x[1], x[0] * x[0])));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    fine &= ss <= 3.4e38f;
+    const float r = fine ? rsqrtf(fmaf(ss, 1.0f / kHeadDim, P.eps)) : __int_as_float(0x7fffffff);
+    const float4 w4 = __ldg(reinterpret_cast<const float4*>(w) + lane);
+    x[0] *= r * w4.x;
+    x[1] *= r * w4.y;
+    x[2] *= r * w4.z;
+    x[3] *= r * w4.w;
+  }
+  *reinterpret_cast<float4*>(y + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
+  fine = __all_sync(0xffffffffu, fine);
+  if (P.rpos[tt]) {
+    __syncwarp();
+    const int pos = __ldg(P.rpos[tt] + row);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = lane + 32 * h;
+      if (i < P.half_rot) {
+        int a, b;
+        rope_pair(P.interleaved, P.half_rot, i, a, b);
+        float s, c;
+        rope_sincos(__ldg(P.freq + i), pos, s, c);
+        s *= P.scale;
+        c *= P.scale;
+        const float ya = y[a], yb = y[b];
+        y[a] = fmaf(ya, c, -(yb * s));
+        y[b] = fmaf(yb, c, ya * s);
+      }
+    }
+  }
+  return fine;
+}
+
+// Rows of values that are copied: a warp takes up to rpw of them, 16 lanes of 16 bytes each, two at a time.
+__device__ __forceinline__ void copy_rows(const RopeParams& P, int item, int lane) {
+  const RotTensor& T = P.r.t[2];
+  const int total = T.rows * T.heads;
+  const int p0 = item * P.r.rpw, p1 = min(total, p0 + P.r.rpw);
+#pragma unroll 4
+  for (int p = p0 + (lane >> 4); p < p1; p += 2) {
+    const int row = p / T.heads, head = p % T.heads;
+    const uint4 x = *(reinterpret_cast<const uint4*>(rope_src(P, 2, row, head)) + (lane & 15));
+    uint16_t* dst = rot_dst(P.r, T, row, head, __ldg(P.r.seq_idx + row), __ldg(P.r.pos + row), (lane & 15) == 0);
+    if (dst) reinterpret_cast<uint4*>(dst)[lane & 15] = x;
+  }
+}
+
+__global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_constant__ RopeParams P) {
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if ((int)blockIdx.x >= P.r.dense_total) {
+    pdl_wait();
+    const int item = ((int)blockIdx.x - P.r.dense_total) * kRopeWarps + warp;
+    if (item < P.r.warp_total) copy_rows(P, item, lane);
+    return;
+  }
+  __shared__ __align__(16) float ys[kMaxRows][kHeadDim];
+  __shared__ uint16_t* dst_sh[kMaxRows];
+  int tt, tile;
+  find_item(P.r.n_dense, blockIdx.x, tt, tile);
+  const RotTensor& T = P.r.t[tt];
+  const int slice = tile % kSlices;
+  tile /= kSlices;
+  const int pairs = T.rows * T.head_div;
+  const int chunks = (pairs + P.r.rt - 1) / P.r.rt;
+  const int tiles_per_mat = (chunks + P.r.rpc - 1) / P.r.rpc;
+  const int mh = tile / tiles_per_mat, c0 = (tile % tiles_per_mat) * P.r.rpc, c1 = min(chunks, c0 + P.r.rpc);
+  // this thread's part of output o's matrix row: four threads share it, 16-byte pieces in turn (shared memory
+  // then serves the four from different banks)
+  const int o = kSlice * slice + (tid >> 2), part = tid & 3;
+  float t[32];
+  if (T.mode == ROT_WHT) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) t[j] = hadamard_sign(o, 16 * (j >> 2) + 4 * part + (j & 3)) * kInvSqrtDim;
+  } else {
+    const float4* m = reinterpret_cast<const float4*>(T.mat + ((size_t)mh * kHeadDim + o) * kHeadDim);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 v = __ldg(m + 4 * j + part);
+      t[4 * j] = v.x;
+      t[4 * j + 1] = v.y;
+      t[4 * j + 2] = v.z;
+      t[4 * j + 3] = v.w;
+    }
+  }
+  pdl_wait();
+  for (int c = c0; c < c1; ++c) {
+    const int p0 = c * P.r.rt, np = min(P.r.rt, pairs - p0);
+    for (int j = warp; j < np; j += kRopeWarps) {
+      int row, head;
+      tile_row(T, mh, p0 + j, row, head);
+      const bool fine = place_row(P, tt, row, head, ys[j], lane);
+      if (lane == 0) {
+        const int b = T.is_query ? 0 : __ldg(P.r.seq_idx + row), p = T.is_query ? 0 : __ldg(P.r.pos + row);
+        dst_sh[j] = rot_dst(P.r, T, row, head, b, p, slice == 0);
+        if (!fine && slice == 0 && dst_sh[j]) set_status(P.r.status, KVQ_ERR_NONFINITE);
+      }
+    }
+    __syncthreads();
+    for (int j0 = 0; j0 < np; j0 += 4) {
+      float acc[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[j] = 0.f;
+        if (j0 + j < np) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 y = *reinterpret_cast<const float4*>(&ys[j0 + j][16 * i + 4 * part]);
+            acc[j] = fmaf(t[4 * i], y.x, acc[j]);
+            acc[j] = fmaf(t[4 * i + 1], y.y, acc[j]);
+            acc[j] = fmaf(t[4 * i + 2], y.z, acc[j]);
+            acc[j] = fmaf(t[4 * i + 3], y.w, acc[j]);
+          }
+        }
+      }
+      // sums over the four parts; thread `part` ends with row j0 + part
+      const bool up = part & 2, odd = part & 1;
+      float u0 = up ? acc[2] : acc[0], u1 = up ? acc[3] : acc[1];
+      u0 += __shfl_xor_sync(0xffffffffu, up ? acc[0] : acc[2], 2);
+      u1 += __shfl_xor_sync(0xffffffffu, up ? acc[1] : acc[3], 2);
+      const float s = (odd ? u1 : u0) + __shfl_xor_sync(0xffffffffu, odd ? u0 : u1, 1);
+      uint16_t* dst = j0 + part < np ? dst_sh[j0 + part] : nullptr;
+      if (dst) dst[o] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" int kvq_launch_rope(const kvq_config* cfg, const kvq_transform* tr, const kvq_rope* rope, const uint16_t* q,
+                               int64_t q_stride, uint16_t* q_out, const int32_t* q_pos, int32_t n_q_rows,
+                               const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                               const int32_t* seq_idx, const int32_t* pos, const int32_t* rope_pos, int32_t n_kv_rows,
+                               const kvq_cache* cache, int32_t* d_status, cudaStream_t stream) {
+  RopeParams P{};
+  RotParams& R = P.r;
+  const int gqa = cfg->n_q_heads / cfg->n_kv_heads;
+  const bool had = tr->kind == KVQ_TRANSFORM_HADAMARD;
+  R.t[0] = RotTensor{q, n_q_rows, cfg->n_q_heads, had ? ROT_WHT : ROT_DENSE, tr->t_k_inv_t, gqa, 1,
+                     q_out, nullptr, nullptr, 0, 0};
+  R.t[1] = RotTensor{k, n_kv_rows, cfg->n_kv_heads, had ? ROT_WHT : ROT_DENSE, tr->t_k, 1, 0,
+                     nullptr, cache->sink_k, cache->ring_k, 1, 0};
+  R.t[2] = RotTensor{v, n_kv_rows, cfg->n_kv_heads, tr->t_v ? ROT_DENSE : ROT_COPY, tr->t_v, 1, 0,
+                     nullptr, cache->sink_v, cache->ring_v, 0, 1};
+  R.seq_idx = seq_idx;
+  R.pos = pos;
+  R.seq_len = cache->seq_len;
+  R.s_quant = cache->s_quant;
+  R.s_sink = cfg->s_sink;
+  R.ring_cap = cfg->ring_cap;
+  R.batch = cfg->batch;
+  R.hkv = cfg->n_kv_heads;
+  R.status = d_status;
+  P.stride[0] = q_stride;
+  P.stride[1] = k_stride;
+  P.stride[2] = v_stride;
+  if (rope) {
+    if (rope->rot_dim > 0) {
+      P.rpos[0] = q_pos;
+      P.rpos[1] = rope_pos ? rope_pos : pos;
+    }
+    P.norm[0] = rope->q_norm;
+    P.norm[1] = rope->k_norm;
+    P.freq = rope->freq;
+    P.half_rot = rope->rot_dim / 2;
+    P.interleaved = rope->layout == KVQ_ROPE_INTERLEAVED;
+    P.scale = rope->scale;
+    P.eps = rope->norm_eps;
+  }
+  long long pairs = 0;
+  for (int i = 0; i < 3; ++i) {
+    if ((long long)R.t[i].rows * R.t[i].heads > 0x3fffffffLL) return KVQ_ERR_UNSUPPORTED;
+    if (R.t[i].mode != ROT_COPY) pairs += (long long)R.t[i].rows * R.t[i].heads;
+  }
+  const long long copies = R.t[2].mode == ROT_COPY ? (long long)n_kv_rows * cfg->n_kv_heads : 0;
+  const long long cslots = 2LL * kSms * 16;
+  R.rpw = (int)(copies > cslots ? std::min((copies + cslots - 1) / cslots, (long long)kMaxCopies) : 1);
+  R.warp_total = (int)((copies + R.rpw - 1) / R.rpw);
+  // pairs of a chunk: as many as make about eight CTAs an SM of all the slices (128 threads and 8 KB each); chunks
+  // of a CTA: more than one once the chunks are full
+  const long long slots = 8LL * kSms;
+  R.rt = (int)std::min((long long)kMaxRows, std::max(4LL, (pairs * kSlices + slots - 1) / slots));
+  const long long per_cta = (pairs * kSlices + slots * R.rt - 1) / (slots * R.rt);
+  R.rpc = (int)std::min(std::max(per_cta, 1LL), 1LL << 20);
+  long long total = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (R.t[i].mode == ROT_COPY) continue;
+    const long long here = (long long)R.t[i].rows * R.t[i].head_div;
+    const long long chunks = (here + R.rt - 1) / R.rt;
+    const long long tiles = (R.t[i].heads / R.t[i].head_div) * ((chunks + R.rpc - 1) / R.rpc) * kSlices;
+    if (tiles > 0x3fffffffLL) return KVQ_ERR_UNSUPPORTED;
+    R.n_dense[i] = (int)tiles;
+    total += tiles;
+  }
+  R.dense_total = (int)total;
+  const long long blocks = total + (R.warp_total + kRopeWarps - 1) / kRopeWarps;
+  if (blocks > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
+  return launch_pdl(rope_rows_kernel, dim3((unsigned)blocks), dim3(kRopeThreads), 0, stream, P) == cudaSuccess
+             ? KVQ_OK
+             : KVQ_ERR_CUDA;
+}

@@ -34,6 +34,13 @@
  *   kv_pages_reserve, kv_seq_fork, kv_seq_free, kv_pages_compact
  *                   pages handed out, shared by sequences, given back and made dense.
  *
+ * and, for the two ends of a step, from the projections' rows and to the tokens,
+ *
+ *   kv_rope_qk      head norm, rotary positions, transform and append in one call.
+ *   kv_logits_probs penalties, biases, a grammar's mask and the temperature on logits: the
+ *                   probabilities that kv_verify_tree takes.
+ *   kv_token_counts what the penalties go by: the tokens each sequence holds.
+ *
  * Conventions shared by every call
  *   - Every pointer inside a struct or argument is a DEVICE pointer unless said
  *     otherwise; the structs themselves live in host memory and are read during
@@ -56,7 +63,7 @@
  *     before it -- the caller's or this library's -- to complete before it reads a
  *     per-call input (q, k, v, seq_idx, pos, cu_rows) or touches the cache state.
  *     Configuration is read before that wait: the transform matrices (kv_rotate_qk,
- *     kv_append_chunk) and the page table (kv_attn_decode, kv_attn_chunk).  These
+ *     kv_append_chunk, kv_rope_qk) and the page table (kv_attn_decode, kv_attn_chunk).  These
  *     must not be written by the kernel launched immediately before the call on
  *     the same stream; a copy, or any earlier kernel, may write them.
  *
@@ -85,7 +92,7 @@ extern "C" {
 #define KVQ_ERR_UNSUPPORTED   (-2)  /* valid but not implemented (head_dim, G, GQA ratio)  */
 #define KVQ_ERR_CUDA          (-3)  /* a CUDA runtime call or launch failed                */
 #define KVQ_ERR_BOUNDS        (-4)  /* device: page id / position / ring slot out of range */
-#define KVQ_ERR_NONFINITE     (-5)  /* device: a scale, zero point, norm, value or probability is not finite */
+#define KVQ_ERR_NONFINITE     (-5)  /* device: a scale, zero point, norm, value, logit or probability is not finite */
 #define KVQ_ERR_TIMEOUT       (-6)  /* device: a bounded wait on an async copy ran out     */
 #define KVQ_ERR_WORKSPACE     (-7)  /* workspace smaller than kv_attn_workspace_bytes()    */
 
@@ -435,6 +442,132 @@ KVQ_API int kv_seq_free(const kvq_config* cfg, const kvq_cache* cache, int32_t* 
 KVQ_API size_t kv_pages_compact_workspace_bytes(const kvq_config* cfg);
 KVQ_API int kv_pages_compact(const kvq_config* cfg, const kvq_cache* cache, int32_t* page_ref, int32_t* n_live,
                      void* workspace, size_t ws_bytes, int32_t* d_status, void* stream);
+
+/* ---- from the projections' rows ----------------------------------------------------
+ * Rotary positions: channels (a, b) of a head turn by position * f_i, f_i falling with i = 0 ..
+ * rot_dim/2 - 1.  Phases are kept as whole numbers, position * freq[i] mod 2^64 in units of 2^-64
+ * turns, so that they are exact at any position. */
+#define KVQ_ROPE_HALF        0   /* pair i: channels i and i + rot_dim/2 */
+#define KVQ_ROPE_INTERLEAVED 1   /* pair i: channels 2i and 2i + 1       */
+
+typedef struct kvq_rope {
+  int32_t         layout;    /* KVQ_ROPE_*                                                        */
+  int32_t         rot_dim;   /* rotated channels, a head's first: even, 0 .. d; the others pass   */
+  float           scale;     /* multiplies the rotated channels (1, or a scaling's factor)        */
+  float           norm_eps;  /* of the norms below                                                */
+  const uint64_t* freq;      /* [rot_dim/2] device: turns per token in units of 2^-64             */
+  const float*    q_norm;    /* [d] device: weights of the RMS norm of every query head before    */
+  const float*    k_norm;    /*     the rotation; of every key head (NULL: no norm)               */
+} kvq_rope;
+
+/* kvq_rope_frequencies: freq and scale of the usual choices (freq is HOST memory, [rot_dim/2]; computed in
+ * float64).  w_i = theta^(-2 i / rot_dim) radians a token, and by `scaling`:
+ *   KVQ_ROPE_PLAIN   w_i
+ *   KVQ_ROPE_LINEAR  w_i / factor (position interpolation)
+ *   KVQ_ROPE_NTK     w_i with theta * factor^(rot_dim / (rot_dim - 2)) for theta (rot_dim > 2)
+ *   KVQ_ROPE_BANDS   by wavelength, context / lambda_i = context w_i / 2 pi: below a: w_i / factor; above b:
+ *                    w_i; between them the two mixed, b's share (context / lambda_i - a) / (b - a)
+ *   KVQ_ROPE_YARN    YaRN (Peng et al., 2023): by index, w_i mixed with w_i / factor along a ramp from pair
+ *                    floor(at(a)) to ceil(at(b)), at(t) = rot_dim ln(context / (2 pi t)) / (2 ln theta), clipped to
+ *                    0 .. rot_dim - 1; scale = 0.1 ln(factor) + 1 (1 for factor <= 1)
+ * scale (HOST, may be NULL) is 1 for the others.  context, a, b are read by the last two only (a < b and a > b >
+ * 0 there).  theta > 1, factor > 0: KVQ_ERR_INVALID_ARG otherwise. */
+#define KVQ_ROPE_PLAIN  0
+#define KVQ_ROPE_LINEAR 1
+#define KVQ_ROPE_NTK    2
+#define KVQ_ROPE_BANDS  3
+#define KVQ_ROPE_YARN   4
+KVQ_API int kvq_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling, double factor, double context, double a,
+                         double b, uint64_t* freq, float* scale);
+
+/* kv_rope_qk: the rows of the query, key and value projections as they come: norm of the heads, rotation by
+ * position, transform, and the append.
+ *   q        [n_q_rows][Hq][d] bf16, rows q_stride elements apart (so for k and v: three parts of one fused
+ *            projection do; strides are multiples of 8 and at least H d, bases 16-byte aligned)
+ *   q_out    [n_q_rows][Hq][d] bf16 (16-byte aligned): T_K^{-T} rope(norm(q)); must not overlap q
+ *   q_pos    [n_q_rows] int32: each query's position in the text (any value; NULL when n_q_rows == 0)
+ *   k, v     [n_kv_rows][Hkv][d] bf16 likewise; seq_idx, pos [n_kv_rows] int32 as for kv_rotate_qk
+ *   rope_pos [n_kv_rows] int32: each key's position in the text where it is not its token's number (the nodes
+ *            of a drafted tree: the number of tokens before the drafts plus the node's depth); NULL: pos
+ * Keys become T_K rope(norm(k)), values T_V v or copies of v, written to sink and ring as kv_rotate_qk does:
+ * the same bounds, status and seq_len.  n_kv_rows and n_q_rows may differ, and either may be 0.
+ * Arithmetic is float32 to the end (the norm's mean, the rotation, the transform's sums) with one rounding to
+ * bf16: an error of 2^-19 sum_j |T_ij x_j| at most besides it, not kv_rotate_qk's exact product, whose input
+ * rows are rounded after the rotation.  Copied values are exact.  A head whose row holds an infinity or NaN, or (with a
+ * norm) whose squares sum to more than float32 holds, gets a row that is not finite, and KVQ_ERR_NONFINITE.
+ * rope NULL: no norm and no rotation (q_pos may then be NULL).
+ * Execution: the rows of few tokens run on the CUDA cores, a slice of a matrix to a CTA; prefill-sized calls on
+ * the tensor cores, both operands as pairs of fp16 under powers of two.  The two round differently.
+ * Source: [WUSH] inference algorithm and [OScaR] algorithm, key and query processing (the transform follows RoPE);
+ * norm and rotation are the models' own (Qwen3's heads). */
+KVQ_API int kv_rope_qk(const kvq_config* cfg, const kvq_transform* tr, const kvq_rope* rope, const uint16_t* q,
+               int64_t q_stride, uint16_t* q_out, const int32_t* q_pos, int32_t n_q_rows, const uint16_t* k,
+               int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* seq_idx, const int32_t* pos,
+               const int32_t* rope_pos, int32_t n_kv_rows, const kvq_cache* cache, int32_t* d_status, void* stream);
+
+/* ---- from logits to tokens ------------------------------------------------------------
+ * counts [B][count_stride] uint16 (device, 4-byte aligned, count_stride even and at least vocab): what sequence b holds
+ * of each token: the highest bit for one that its prompt holds, below it how often it has been generated (no more
+ * than KVQ_COUNT_MOST is kept).  The caller zeroes a row when a sequence takes its place (and copies it when one is
+ * forked); kv_token_counts writes it, kv_logits_probs reads it. */
+#define KVQ_COUNT_MOST   32767
+#define KVQ_COUNT_PROMPT 0
+#define KVQ_COUNT_OUTPUT 1
+
+#define KVQ_LOGITS_F32  0
+#define KVQ_LOGITS_BF16 1
+#define KVQ_LOGITS_F16  2
+#define KVQ_LOGITS_MAX_VOCAB 524288
+
+typedef struct kvq_logit_rules {         /* device pointers; NULL: that rule is not applied */
+  const float*    temperature; /* [B] >= 0; 0: the best token alone, the lowest id among equals (NULL: 1)        */
+  const float*    repetition;  /* [B] > 0: logits of tokens held, prompt or generated: l > 0: l / r, else l * r */
+  const float*    frequency;   /* [B]: less by this for every time the token has been generated                 */
+  const float*    presence;    /* [B]: less by this once the token has been generated                           */
+  const uint16_t* counts;      /* as above (NULL: nothing is held yet)                                          */
+  int64_t         count_stride;
+  const int32_t*  bias_cu;     /* [B + 1]: sequence b's biases are entries bias_cu[b] .. bias_cu[b+1] - 1 of    */
+  const int32_t*  bias_token;  /* [n_bias]: token ids, strictly increasing within a sequence, and               */
+  const float*    bias;        /* [n_bias]: what is added to their logits (-infinity bans a token)              */
+  const uint32_t* mask;        /* [n_masks][mask_stride]: bit v % 32 of word v / 32 set: token v is allowed     */
+  int64_t         mask_stride; /* words, at least vocab / 32 rounded up                                         */
+  const int32_t*  mask_row;    /* [n_rows]: the mask of each row, -1: none (NULL: mask r for row r)             */
+  int32_t         n_bias;
+  int32_t         n_masks;
+} kvq_logit_rules;
+
+/* kv_logits_probs: the rows of probabilities that kv_verify_tree takes (with one row a sequence: the next token's).
+ *   logits   n_rows rows of `vocab` numbers, l_stride elements apart, of type KVQ_LOGITS_* (aligned to their size)
+ *   cu_rows  [B + 1] as for kv_append_chunk: rows of sequence b
+ *   parent, token [n_rows] int32: the tree as for kv_verify_tree, or NULL: the rows are no drafts.  The tokens of a
+ *            node and its ancestors count as generated in its row, roots left out: theirs has been counted
+ *   p        n_rows rows of `vocab` float32, p_stride elements apart; may be the logits themselves (float32, equal
+ *            strides), and must not overlap them otherwise
+ * In this order, in float32, one rounding an operation: l + bias; repetition; less frequency * times; less presence;
+ * masked tokens to -infinity, whatever stood there; softmax of l / temperature.
+ * KVQ_ERR_NONFINITE and a row of zeros: where nothing is left (every token masked or at -infinity), where a logit that
+ * is not masked becomes NaN or +infinity, or where a number of the sequence's rules is not finite, the temperature
+ * negative or the repetition not positive.  KVQ_ERR_BOUNDS and a row of zeros: a mask that does not exist, more than KVQ_TREE_MAX_NODES nodes
+ * in a sequence.  KVQ_ERR_BOUNDS: a parent that is not a lower node (the row goes by the path up to there), a token of the path or of a
+ * bias outside the vocabulary (left out), biases out of order (an entry that is not above the one before it may be left out), and cu_rows that do not cover n_rows:
+ * rows behind the last sequence are not written.  Sums are taken in one order: the same bits on every run.
+ * vocab is at most KVQ_LOGITS_MAX_VOCAB.  Of cfg only batch is used.
+ * Execution: a cluster of CTAs holds a row in shared memory: one read of the logits, one write of p.  Logits of
+ * four masked neighbours are not read. */
+KVQ_API int kv_logits_probs(const kvq_config* cfg, const kvq_logit_rules* rules, const void* logits, int32_t logits_type,
+                    int64_t l_stride, int32_t vocab, const int32_t* cu_rows, const int32_t* parent, const int32_t* token,
+                    int32_t n_rows, float* p, int64_t p_stride, int32_t* d_status, void* stream);
+
+/* kv_token_counts: tokens into counts.  Rows cu_rows[b] .. cu_rows[b+1] - 1 of token [n_rows] are sequence b's:
+ *   KVQ_COUNT_PROMPT  they are marked as its prompt's (path, n_accept, next_token NULL);
+ *   KVQ_COUNT_OUTPUT  they are counted as generated: all of them (path and n_accept NULL), or, after
+ *                     kv_verify_tree, those of the kept nodes path[cu_rows[b] + j], 0 < j < n_accept[b] (node 0
+ *                     was counted when it was drawn), and with next_token [B] the token behind them (-1: none).
+ * Equal tokens may come any number of times.  Tokens outside the vocabulary, nodes outside the tree and rows of no
+ * sequence are left out, with KVQ_ERR_BOUNDS.  Of cfg only batch is used. */
+KVQ_API int kv_token_counts(const kvq_config* cfg, uint16_t* counts, int64_t count_stride, int32_t vocab, int32_t kind,
+                    const int32_t* cu_rows, const int32_t* token, int32_t n_rows, const int32_t* path,
+                    const int32_t* n_accept, const int32_t* next_token, int32_t* d_status, void* stream);
 
 /* kv_attn_decode: one decode step of GQA attention for every sequence.
  *   q_rot   [B][Hq][d] bf16 compensated queries (kv_rotate_qk output)
