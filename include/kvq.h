@@ -492,9 +492,10 @@ KVQ_API int kvq_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling,
  * Keys become T_K rope(norm(k)), values T_V v or copies of v, written to sink and ring as kv_rotate_qk does:
  * the same bounds, status and seq_len.  n_kv_rows and n_q_rows may differ, and either may be 0.
  * Arithmetic is float32 to the end (the norm's mean, the rotation, the transform's sums) with one rounding to
- * bf16: an error of 2^-19 sum_j |T_ij x_j| at most besides it, not kv_rotate_qk's exact product, whose input
- * rows are rounded after the rotation.  Copied values are exact.  A head whose row holds an infinity or NaN, or (with a
- * norm) whose squares sum to more than float32 holds, gets a row that is not finite, and KVQ_ERR_NONFINITE.
+ * bf16; besides that rounding the error is at most 2^-17 sum_j |T_ij| m_j, m_j the length of channel j's pair
+ * after the norm.  It is not kv_rotate_qk's exact product, whose input rows are rounded after the rotation.  Copied
+ * values are exact.  A head whose row holds an infinity or NaN, or (with a norm) whose squares sum to more than
+ * float32 holds, gets a row that is not finite, and KVQ_ERR_NONFINITE (copied values aside).
  * rope NULL: no norm and no rotation (q_pos may then be NULL).
  * Execution: the rows of few tokens run on the CUDA cores, a slice of a matrix to a CTA; prefill-sized calls on
  * the tensor cores, both operands as pairs of fp16 under powers of two.  The two round differently.
