@@ -19,7 +19,7 @@ SRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libkvq.so")
 SOURCES = ["api.cu", "rotate.cu", "rotate_tc.cu", "flush.cu", "attn.cu", "chunk.cu", "tree.cu", "spec.cu", "pages.cu",
-           "rope.cu", "logits.cu"]
+           "rope.cu", "rope_tc.cu", "logits.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -38,6 +38,11 @@ __device__ __forceinline__ const uint16_t* rope_src(const RopeParams& P, int tt,
 __device__ __forceinline__ float hadamard_sign(int i, int j) {
   return __uint_as_float(0x3f800000u | ((uint32_t)(__popc(i & j) & 1) << 31));
 }
+// (row, head) pairs from which a call's products run on the tensor cores.
+constexpr long long kRopeTcPairs = kTcMinPairs;
+// ... which this launches (P.r.n_dense is set there; copies are the caller's).
+int launch_rope_tc(RopeParams P, cudaStream_t stream);
+
 constexpr float kInvSqrtDim = 0.08838834764831845f;
 
 }  // namespace kvq

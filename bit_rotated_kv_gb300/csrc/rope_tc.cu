@@ -1,0 +1,746 @@
+// kv_rope_qk for prefill-sized calls: norm and rotation on the CUDA cores, the per-head products on the tensor
+// cores (tcgen05).
+//
+// Bytes bound it: a row is read once and written once (512 bytes a row and head; the 2048-token chunk of 16 sequences
+// with 32 + 8 heads moves 671 MB, 99 us at the measured copy rate), which leaves the CUDA cores about 1.6 K clocks and the
+// tensor cores as many for 64 rows of an SM.  Both products therefore take two fp16 parts of each operand rather than the integer digits
+// of rotate_tc.cu: T row i and x row r are brought under powers of two so that their largest entry lies below 2^15,
+// and split as hi + lo, 11 bits each.  hi hi + lo hi + hi lo, summed in float32 by the tensor cores, leaves out 2^-20
+// of sum |T_ij x_j| at most (bf16's half step is 2^-8 of the result); three MMAs of 16 inputs instead of nine.  Entries 2^-29 of their
+// row's largest lose bits of lo, 2^-40 of that largest.  A Walsh-Hadamard matrix is +-1, its 1/sqrt(128) left to the end: two MMAs.
+//
+// The norm's factor belongs to a row, so it too is left to the end, and the weights take the power of two: norm and
+// scaling cost one product a channel.  Sine and cosine are the SFU's (2^-20.9 of the pair's length), from phases in
+// whole numbers.  Lanes hold both channels of a pair: eight lanes to a row, two vectors of eight channels each.
+//
+// Layout: two CTAs on an SM.  A CTA takes a run of chunks of 64 (row, head) pairs; T hi and lo of its matrix stay in TMEM (the A
+// operand, lane = output, 64 columns each), rows come by asynchronous copies two chunks ahead and go through swizzled shared memory (B,
+// two buffers of hi and lo), accumulators take two sets of 64 TMEM columns.  Eight warps place rows, one issues the MMAs, four write results out through
+// the shared memory that the rows came from, a row's 256 bytes at a time, two ask
+// for rows, one finds out where they go.
+#include "rope.cuh"
+#include "tc.cuh"
+
+#include <algorithm>
+#include <mutex>
+
+namespace kvq {
+namespace {
+
+// Warps 0-7 place rows, 8-11 write results out, 12 issues the MMAs, 13 and 15 ask for rows, 14 finds out where they
+// go.  Registers a thread: 64 at launch (32 warps an SM), shared out again 8 x 88 + 4 x 48 + 4 x 32 = 16 x 64.
+constexpr int kRtWarps = 8, kRtOut = 4, kRtMma = 12, kRtLoad = 13, kRtDst = 14;
+constexpr int kRtThreads = 512;
+constexpr int kPlaceRegs = 88, kOutRegs = 48, kLastRegs = 32;
+constexpr int kRtRows = kUmRows;                         // pairs of a chunk (N of every MMA): 64
+constexpr int kHalfBuf = kRtRows * kHeadDim * 2;         // hi or lo of a chunk: 16 KB
+constexpr int kRtXBuf = 2 * kHalfBuf;
+constexpr int kRtRaw = 2 * kRtXBuf;                      // two chunks of rows as they come, 256 bytes each
+constexpr int kRtRawBuf = kRtRows * kHeadDim * 2;
+constexpr int kRtMeta = kRtRaw + 2 * kRtRawBuf;
+constexpr int kMetaSets = 4;
+constexpr int kRtFac = kRtMeta + kMetaSets * kRtRows * 8;
+constexpr int kRtPos = kRtFac + 2 * kRtRows * 4;
+constexpr int kRtNorm = kRtPos + 2 * kRtRows * 4;
+constexpr int kRtFreq = kRtNorm + kHeadDim * 4;
+constexpr int kRtExch = kRtFreq + 64 * 8;                // a T row's largest exponent, by halves
+constexpr int kRtRowFac = kRtExch + 2 * kHeadDim * 4;    // what takes an output's power of two back, where they differ
+constexpr int kRtUsed = kRtRowFac + kHeadDim * 4;
+constexpr int kRtSmem = kRtUsed + 1024;
+static_assert(2 * (kRtSmem + 1024) <= 227 * 1024, "two CTAs on an SM");
+constexpr uint32_t kRtCols = 256;                        // TMEM: T hi, T lo, two accumulators
+constexpr uint32_t kRtLo = 64, kRtAcc = 128;
+// kind::f16: D f32, A and B fp16, both K-major, N = 64, M = 128
+constexpr uint32_t kRtIdesc = (1u << 4) | ((uint32_t)(kRtRows >> 3) << 17) | ((128u >> 4) << 24);
+
+__device__ __forceinline__ bool rt_elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void rt_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(kRtIdesc), "r"(acc)
+      : "memory");
+}
+// The warps meet at named barriers, where the hardware holds them: warps that ask an mbarrier again and again took a third
+// of the SM's issue slots.  Only the end of the MMAs comes by mbarrier, and one warp asks (bounded).
+constexpr int kBarPlace = 1, kBarOut = 2, kBarX = 3, kBarFree = 5, kBarMma = 7, kBarRaw = 8;   // (X, Free, Raw: one for each buffer)
+__device__ __forceinline__ void rt_sync(int id, int warps) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(32 * warps) : "memory"); }
+__device__ __forceinline__ void rt_arrive(int id, int warps) { asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(32 * warps) : "memory"); }
+// those who place rows, the one who finds destinations and the one who issues the MMAs; those who empty a buffer and those who
+// fill it; those who read a raw buffer and the two who fill it
+
+constexpr int kXWarps = kRtWarps + 2, kFreeWarps = kRtOut + kRtWarps, kRawWarps = kRtWarps + 2;
+__device__ __forceinline__ bool rt_wait(uint64_t* bar, uint32_t parity) {
+  if (um_mbar_try(bar, parity)) return true;
+  unsigned long long began, now;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(began));
+  do {
+    if (um_mbar_try(bar, parity)) return true;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+  } while (now - began < 1000000000ull);                 // a second
+  return false;
+}
+template <int R>
+__device__ __forceinline__ void rt_regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void rt_regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// The leading 11 bits of a float (towards zero): an exact fp16 where it is in fp16's normal range.
+__device__ __forceinline__ float lead11(float v) { return __uint_as_float(__float_as_uint(v) & 0xffffe000u); }
+
+// The power of two that brings numbers below 2^(e - 126) below 2^15 (e: an exponent field).
+__device__ __forceinline__ int fit_pow2(int e) { return min(max(141 - e, -126), 126); }
+__device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }
+
+// How a lane's two vectors of eight channels form pairs.
+enum { kNone, kHalf, kInter, kAny };
+
+// The chunk's place: tensor, matrix, chunk of the matrix.
+struct Place {
+  int tt, mh, c, cpm;
+};
+__device__ __forceinline__ Place place_of(const RopeParams& P, int chunk) {
+  Place w;
+  int item;
+  find_item(P.r.n_dense, chunk, w.tt, item);
+  const RotTensor& T = P.r.t[w.tt];
+  w.cpm = (T.rows * T.head_div + kRtRows - 1) / kRtRows;
+  w.mh = item / w.cpm;
+  w.c = item % w.cpm;
+  return w;
+}
+
+// What a run of chunks of one matrix has in common (in shared memory: read once a chunk, it would cost the loops their
+// registers).
+struct Seg {
+  bool same;                 // a slot's rows are heads of one token
+  bool norm;
+  bool weighted;             // channels have weights: the norm's, the rotation's factor
+  int grow;                  // what weights and rotation may add to a channel's exponent
+  float up, back;            // with a norm: the power of two that rows take
+  float t_back;              // takes the matrix's power of two back (and a Hadamard matrix's 1/sqrt(128) in)
+};
+
+// Asks for half of a chunk's rows and for their positions, two rows at a time (one warp).  Behind the last row: that row again.  (Bulk copies
+// of a token's heads, 1 KB, took one warp 200 clocks each.)
+__device__ __forceinline__ void ask_rows(const RopeParams& P, const Place& w, int half, uint32_t raw, uint32_t pos, uint64_t* bar, int lane) {
+  const RotTensor& T = P.r.t[w.tt];
+  const int lg = __ffs(T.head_div) - 1, last = (T.rows << lg) - 1, mask = T.head_div - 1;
+  const uint16_t* src = T.src + (long long)(w.mh << lg) * kHeadDim + 8 * (lane & 15);
+  const long long stride = P.stride[w.tt];
+  const int r0 = 32 * half + (lane >> 4), p0 = w.c * kRtRows + r0;
+  raw += 256u * (uint32_t)r0 + 16u * (uint32_t)(lane & 15);
+#pragma unroll 4
+  for (int k = 0; k < 16; ++k) {
+    const int p = min(p0 + 2 * k, last);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(raw + 512u * k), "l"(src + (p >> lg) * stride + (p & mask) * kHeadDim)
+                 : "memory");
+  }
+  const int32_t* rpos = P.rpos[w.tt];
+  if (rpos) {
+    const int p = min(w.c * kRtRows + 32 * half + lane, last);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(pos + 4u * (uint32_t)(32 * half + lane)), "l"(rpos + (p >> lg)) : "memory");
+  }
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(um_saddr(bar)) : "memory");
+}
+
+// Rotation of eight pairs, two at a time.
+__device__ __forceinline__ void turn(float2 (&a)[4], float2 (&b)[4], const float2 (&c)[4], const float2 (&s)[4]) {
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const float2 u = mul2(a[m], s[m]), v = mul2(b[m], make_float2(-1.f, -1.f));
+    a[m] = fma2(v, s[m], mul2(a[m], c[m]));
+    b[m] = fma2(b[m], c[m], u);
+  }
+}
+// Where pair i stands in the table: the eight lanes of a row, which ask for pairs eight (kInter: four) apart, find theirs
+// side by side.
+__device__ __forceinline__ int freq_slot(bool inter, int i) { return inter ? (i & 3) * 16 + (i >> 2) : (i & 7) * 8 + (i >> 3); }
+// Cosine and sine of a pair's phase.  (Pairs that are not rotated stand in the table with frequency 0.)
+__device__ __forceinline__ void phase_sincos(uint32_t freq_at, int pos, float& c, float& s) {
+  const uint2 f = lds_v2(freq_at);
+  // the upper 32 bits of freq * pos mod 2^64, pos signed
+  const uint32_t up = f.y * (uint32_t)pos + __umulhi(f.x, (uint32_t)pos) - (pos < 0 ? f.x : 0u);
+  const float x = (float)(int32_t)up * (0x1p-31f * 3.14159265358979f);
+  s = __sinf(x);
+  c = __cosf(x);
+}
+
+// Results of a chunk stand where its rows were (its MMAs are done with them): 16-byte piece c of row r, in what the
+// warp that placed the row owns, so that only that warp, which writes the row out, overwrites it with the next.
+__device__ __forceinline__ uint32_t out_at(int r, int c) {
+  return (uint32_t)((c >> 3) * 8192 + (r >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// 16 TMEM lanes x 32 columns: registers 4 k + 2 h + e hold lane (lane >> 2) + 8 h, column 8 k + 2 (lane & 3) + e.
+__device__ __forceinline__ void tmem_ld_tiles(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+
+// Eight numbers as hi and lo in 16 bytes each.
+__device__ __forceinline__ void split_store(const float (&v)[8], uint32_t hi_at, uint32_t lo_at) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const float2 x = make_float2(v[2 * m], v[2 * m + 1]);
+    const float2 y = make_float2(lead11(x.x), lead11(x.y));
+    const float2 z = fma2(y, make_float2(-1.f, -1.f), x);
+    h[m] = half2_bits(y.x, y.y);
+    l[m] = half2_bits(z.x, z.y);
+  }
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(hi_at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(lo_at), "r"(l[0]), "r"(l[1]), "r"(l[2]), "r"(l[3]) : "memory");
+}
+
+__device__ __forceinline__ uint32_t amax16(const uint4& v) {
+  return __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+}
+
+// Places a slot's two rows: hi and lo into the chunk's buffer, destination and factor into its metadata.
+template <int kMode>
+__device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, int left, uint32_t pos_s, int r0, int sub, int va,
+                                           int vb, uint32_t at_a, uint32_t at_b, uint32_t raw, int bar_raw, uint32_t xb, uint32_t norm_s, uint32_t freq_s,
+                                           uint32_t fac_s) {
+  float2 c[4], s[4];
+  const bool norm = g.norm;
+  int2 pos2 = make_int2(0, 0);
+  if (kMode != kNone) {
+    const uint2 x = lds_v2(pos_s + 4u * r0);
+    pos2 = make_int2((int)x.x, (int)x.y);
+  }
+  uint4 ra2[2], rb2[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    ra2[j] = lds_v4(raw + 256u * (r0 + j) + 16u * va);
+    rb2[j] = lds_v4(raw + 256u * (r0 + j) + 16u * vb);
+  }
+  rt_arrive(bar_raw, kRawWarps);                         // (the next rows but one may come)
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint4 ra = ra2[j], rb = rb2[j];
+    const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+    // the number that brings the row's channels below 2^15, the one that takes it back at the end
+    float up, back;
+    bool fine;
+    if (norm) {
+      // |x| / rms(x) <= sqrt(128): the norm's own factor, and the weights' power of two
+      float2 acc[2];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const float2 x = make_float2(lo16(wa[m]), hi16(wa[m])), y = make_float2(lo16(wb[m]), hi16(wb[m]));
+        acc[0] = m ? fma2(x, x, acc[0]) : mul2(x, x);
+        acc[1] = m ? fma2(y, y, acc[1]) : mul2(y, y);
+      }
+      float ss = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      fine = ss <= 3.4e38f;
+      up = fine ? rsqrtf(fmaf(ss, 1.0f / kHeadDim, P.eps)) * g.up : __int_as_float(0x7fffffff);
+      back = g.back;
+    } else {
+      uint32_t top = __vmaxu2(amax16(ra), amax16(rb));   // (bf16 bits order as integers)
+      top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int k = fit_pow2((int)(top >> 7) + g.grow);
+      fine = top < 0x7f80u;
+      up = pow2(k);
+      back = pow2(-k) * g.t_back;
+    }
+    const float2 u2 = make_float2(up, up);
+    // the pairs' members a, b (kInter: even and odd channels of va, then of vb) under the weights and that number
+    float2 a[4], b[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if (kMode == kInter) {
+        const uint32_t x = m < 2 ? wa[2 * m] : wb[2 * m - 4], y = m < 2 ? wa[2 * m + 1] : wb[2 * m - 3];
+        a[m] = make_float2(lo16(x), lo16(y));
+        b[m] = make_float2(hi16(x), hi16(y));
+      } else {
+        a[m] = make_float2(lo16(wa[m]), hi16(wa[m]));
+        b[m] = make_float2(lo16(wb[m]), hi16(wb[m]));
+      }
+    }
+    if (g.weighted) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 x = lds_v4(norm_s + (uint32_t)(h * 256 + va * 16)), y = lds_v4(norm_s + (uint32_t)(h * 256 + vb * 16));
+        const float2 x0 = make_float2(__uint_as_float(x.x), __uint_as_float(x.y)), x1 = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
+        const float2 y0 = make_float2(__uint_as_float(y.x), __uint_as_float(y.y)), y1 = make_float2(__uint_as_float(y.z), __uint_as_float(y.w));
+        if (kMode == kInter) {
+          a[h] = mul2(a[h], mul2(make_float2(x0.x, x1.x), u2));
+          b[h] = mul2(b[h], mul2(make_float2(x0.y, x1.y), u2));
+          a[2 + h] = mul2(a[2 + h], mul2(make_float2(y0.x, y1.x), u2));
+          b[2 + h] = mul2(b[2 + h], mul2(make_float2(y0.y, y1.y), u2));
+        } else {
+          a[2 * h] = mul2(a[2 * h], mul2(x0, u2));
+          a[2 * h + 1] = mul2(a[2 * h + 1], mul2(x1, u2));
+          b[2 * h] = mul2(b[2 * h], mul2(y0, u2));
+          b[2 * h + 1] = mul2(b[2 * h + 1], mul2(y1, u2));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        a[m] = mul2(a[m], u2);
+        b[m] = mul2(b[m], u2);
+      }
+    }
+    const int r = r0 + j, pos = j ? pos2.y : pos2.x;
+    if (kMode == kHalf || kMode == kInter) {
+      if (j == 0 || !g.same) {                         // (else the two rows are heads of one token)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          // (freq_slot of pairs 8 va + 2 m and the next; kInter: 4 va + 2 m, then of vb)
+          constexpr uint32_t step = kMode == kHalf ? 64 : 128;
+          const uint32_t at = freq_s + (kMode == kHalf ? 8u * min(va, 7) + 2u * m * step : 8u * (m < 2 ? va : vb) + 2u * (m & 1) * step);
+          phase_sincos(at, pos, c[m].x, s[m].x);
+          phase_sincos(at + step, pos, c[m].y, s[m].y);
+        }
+        if (kMode == kHalf && 8 * va >= P.half_rot) {    // (vectors that are no pair)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            c[m] = make_float2(1.f, 1.f);
+            s[m] = make_float2(0.f, 0.f);
+          }
+        }
+      }
+      turn(a, b, c, s);
+    }
+    float va8[8], vb8[8];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if (kMode == kInter) {
+        float* d = m < 2 ? va8 + 4 * m : vb8 + 4 * (m - 2);
+        d[0] = a[m].x;
+        d[1] = b[m].x;
+        d[2] = a[m].y;
+        d[3] = b[m].y;
+      } else {
+        va8[2 * m] = a[m].x;
+        va8[2 * m + 1] = a[m].y;
+        vb8[2 * m] = b[m].x;
+        vb8[2 * m + 1] = b[m].y;
+      }
+    }
+    if (kMode == kAny) {
+      // pairs that no lane holds: through the row's own place in the buffer, 512 bytes as float32 in four lines
+      const uint32_t line = xb + (uint32_t)((r >> 3) * 1024 + (r & 7) * 128);
+      auto at = [&](int ch) {
+        return line + (uint32_t)(((ch >> 5) & 1) * 8192 + (ch >> 6) * kHalfBuf + (ch & 31) * 4);
+      };
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        sts_v2(at(8 * va + e), __float_as_uint(va8[e]), __float_as_uint(va8[e + 1]));
+        sts_v2(at(8 * vb + e), __float_as_uint(vb8[e]), __float_as_uint(vb8[e + 1]));
+      }
+      __syncwarp();
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        float* d = v ? vb8 : va8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int ch = 8 * (v ? vb : va) + e, h = P.half_rot;
+          const int i = ch < h ? ch : ch - h, other = ch < h ? ch + h : ch - h;
+          if (ch < 2 * h) {
+            float cs, sn;
+            phase_sincos(freq_s + 8u * (uint32_t)freq_slot(false, i), pos, cs, sn);
+            uint32_t o;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(o) : "r"(at(other)) : "memory");
+            d[e] = fmaf(d[e], cs, (ch < h ? -sn : sn) * __uint_as_float(o));
+          }
+        }
+      }
+      __syncwarp();
+    }
+    // (r0 is even: row r0 + 1 stands 128 bytes on, its pieces exchanged in twos)
+    const uint32_t to_a = xb + (at_a ^ (16u * j)) + 128u * j, to_b = xb + (at_b ^ (16u * j)) + 128u * j;
+    split_store(va8, to_a, to_a + kHalfBuf);
+    split_store(vb8, to_b, to_b + kHalfBuf);
+    if (sub == 0) {
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(fac_s + 4u * (uint32_t)r), "f"(back) : "memory");
+      if (!fine && left > j) set_status(P.r.status, KVQ_ERR_NONFINITE);
+    }
+  }
+}
+
+// Half of a matrix row (row: its 64 entries; none: row i of the Walsh-Hadamard matrix) as hi and lo into TMEM.
+__device__ __forceinline__ void split_matrix(const float* row, int i, int part, float up, uint32_t taddr) {
+#pragma unroll 1
+  for (int blk = 0; blk < 4; ++blk) {
+    uint32_t h[8], l[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float t[4];
+      if (row) {
+        const float4 t4 = __ldg(reinterpret_cast<const float4*>(row) + 4 * blk + j);
+        t[0] = t4.x * up;
+        t[1] = t4.y * up;
+        t[2] = t4.z * up;
+        t[3] = t4.w * up;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = hadamard_sign(i, 64 * part + 16 * blk + 4 * j + e);
+      }
+      float y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = lead11(t[e]);
+      h[2 * j] = half2_bits(y[0], y[1]);
+      h[2 * j + 1] = half2_bits(y[2], y[3]);
+      l[2 * j] = half2_bits(t[0] - y[0], t[1] - y[1]);
+      l[2 * j + 1] = half2_bits(t[2] - y[2], t[3] - y[3]);
+    }
+    tmem_st8(taddr + 32u * (uint32_t)part + 8u * (uint32_t)blk, h);
+    tmem_st8(taddr + kRtLo + 32u * (uint32_t)part + 8u * (uint32_t)blk, l);
+  }
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// The largest exponent field of 64 entries.
+__device__ __forceinline__ uint32_t top_exponent(const float* row) {
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int j = 0; j < 16; ++j) {
+    const float4 t = __ldg(reinterpret_cast<const float4*>(row) + j);
+    top = max(max(top, __float_as_uint(fabsf(t.x))), max(__float_as_uint(fabsf(t.y)), max(__float_as_uint(fabsf(t.z)), __float_as_uint(fabsf(t.w)))));
+  }
+  return top >> 23;
+}
+
+__global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_constant__ RopeParams P) {
+  __shared__ uint32_t tbase_sh;
+  __shared__ __align__(8) uint64_t bar_mma[2], bar_raw[2];
+  __shared__ volatile int abort_sh;
+  __shared__ int uneven_sh;
+  __shared__ Seg seg_sh;
+  extern __shared__ uint8_t um_smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(um_smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t sb = um_saddr(sm);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    abort_sh = 0;
+    for (int i = 0; i < 2; ++i) {
+      um_mbar_init(&bar_mma[i]);
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 64;" ::"r"(um_saddr(&bar_raw[i])) : "memory");
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(um_saddr(&tbase_sh)), "r"(kRtCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // Only now may the next kernel begin: one that takes all of TMEM could otherwise have it before this CTA does, and
+  // wait for this grid.  For the same reason this kernel itself does not begin before the one ahead of it has ended.
+  pdl_trigger();
+  const uint32_t tb = tbase_sh;
+  const int c_lo = (int)((long long)P.r.dense_total * blockIdx.x / gridDim.x);
+  const int c_hi = (int)((long long)P.r.dense_total * (blockIdx.x + 1) / gridDim.x);
+  const int total = c_hi - c_lo;
+  const int q = warp & 3;
+  const uint32_t tlane = (uint32_t)(32 * q) << 16;       // this warp's TMEM lanes
+
+  if (warp >= kRtMma) {
+    rt_regs_dec<kLastRegs>();
+    if (warp == kRtMma) {
+      // ---- the MMAs of a chunk, once its rows are placed (code that the whole warp runs, one lane issues) ----
+      Place w = place_of(P, c_lo);
+      for (int n = 0; n < total; ++n) {
+        const int s = n & 1;
+        const uint32_t d = tb + kRtAcc + 64u * (uint32_t)s;
+        const bool dense = P.r.t[w.tt].mode == ROT_DENSE;
+        const uint64_t xd = sw128_desc(sb + (uint32_t)(s * kRtXBuf));
+        rt_sync(kBarX + s, kXWarps);
+        tc_fence_after();
+        if (rt_elect()) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint64_t hi = xd + (uint64_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), lo = hi + (kHalfBuf >> 4);
+            rt_mma(d, tb + 8u * (uint32_t)kk, lo, kk > 0);
+            rt_mma(d, tb + 8u * (uint32_t)kk, hi, 1u);
+            if (dense) rt_mma(d, tb + kRtLo + 8u * (uint32_t)kk, hi, 1u);
+          }
+          umma_commit(&bar_mma[s]);
+        }
+        __syncwarp();
+        if (++w.c == w.cpm && n + 1 < total) w = place_of(P, c_lo + n + 1);
+      }
+    } else if (warp != kRtDst) {
+      // ---- rows, two chunks ahead ----
+      Place w = place_of(P, c_lo);
+      for (int n = 0; n < total; ++n) {
+        const int s = n & 1;
+        if (n >= 2) rt_sync(kBarRaw + s, kRawWarps);
+        ask_rows(P, w, (warp - kRtLoad) >> 1, sb + (uint32_t)(kRtRaw + s * kRtRawBuf), sb + (uint32_t)(kRtPos + s * kRtRows * 4), &bar_raw[s], lane);
+        if (++w.c == w.cpm && n + 1 < total) w = place_of(P, c_lo + n + 1);
+      }
+      for (int n = max(total - 2, 0); n < total; ++n) rt_sync(kBarRaw + (n & 1), kRawWarps);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+      // ---- where a chunk's rows go, two to a lane ----
+      Place w = place_of(P, c_lo);
+      for (int n = 0; n < total; ++n) {
+        const RotTensor& T = P.r.t[w.tt];
+        const int lg = __ffs(T.head_div) - 1, pairs = T.rows << lg;
+        const uint32_t meta = sb + (uint32_t)(kRtMeta + (n & (kMetaSets - 1)) * kRtRows * 8);
+        unsigned long long dst[2] = {0ull, 0ull};
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) {
+          const int p = w.c * kRtRows + 32 * j + lane;
+          if (p < pairs) {
+            const int row = p >> lg, head = (w.mh << lg) + (p & (T.head_div - 1));
+            const int b = T.is_query ? 0 : __ldg(P.r.seq_idx + row), at = T.is_query ? 0 : __ldg(P.r.pos + row);
+            const unsigned long long d = (unsigned long long)rot_dst(P.r, T, row, head, b, at, true);
+            (j ? dst[1] : dst[0]) = d;
+          }
+        }
+        // (chunk n - 1 is placed, so what chunk n - 4 had here has been used)
+        sts_u64(meta + 8u * (uint32_t)lane, dst[0]);
+        sts_u64(meta + 8u * (uint32_t)(32 + lane), dst[1]);
+        rt_sync(kBarX + (n & 1), kXWarps);
+        if (++w.c == w.cpm && n + 1 < total) w = place_of(P, c_lo + n + 1);
+      }
+    }
+  } else if (warp >= kRtWarps) {
+    // ---- results: four warps, 32 outputs each ----
+    rt_regs_dec<kOutRegs>();
+    // stmatrix takes 8 x 8 tiles, rows 8 k + lane % 8, 16-byte piece 4 q + lane / 8, and stores them the other way
+    // round; a warp then writes rows 16 q .. out, two at a time
+    const uint32_t put = out_at(lane & 7, 4 * q + (lane >> 3)), get = out_at(lane >> 4, lane & 15);
+    for (int n = 0; n < total; ++n) {
+      const int s = n & 1;
+      const uint32_t xb = sb + (uint32_t)(s * kRtXBuf), acc_at = tb + tlane + kRtAcc + 64u * (uint32_t)s;
+      const uint32_t fac = sb + (uint32_t)(kRtFac + s * kRtRows * 4), meta = sb + (uint32_t)(kRtMeta + (n & (kMetaSets - 1)) * kRtRows * 8);
+      if (warp == kRtWarps && !abort_sh && !__all_sync(0xffffffffu, rt_wait(&bar_mma[s], (uint32_t)((n >> 1) & 1)))) abort_sh = 1;
+      rt_sync(kBarMma, kRtOut);
+      const bool ok = !abort_sh;
+      if (ok) {
+        tc_fence_after();
+        const bool uneven = *reinterpret_cast<volatile int*>(&uneven_sh) != 0;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          // outputs (lane >> 2) + 8 j of this warp's 32, rows 8 k + 2 (lane & 3) and the next
+          uint32_t acc[2][16];
+          tmem_ld_tiles(acc_at + 32u * half, acc[0]);
+          tmem_ld_tiles(acc_at + (16u << 16) + 32u * half, acc[1]);
+          tmem_wait_ld16(acc[0]);
+          tmem_wait_ld16(acc[1]);
+          if (uneven) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float f = reinterpret_cast<const float*>(sm + kRtRowFac)[32 * q + (lane >> 2) + 8 * j];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  uint32_t& v = acc[j >> 1][4 * k + 2 * (j & 1) + e];
+                  v = __float_as_uint(__uint_as_float(v) * f);
+                }
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint2 f = lds_v2(fac + 4u * (uint32_t)(32 * half + 8 * k + 2 * (lane & 3)));
+            const float2 f2 = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
+            uint32_t d[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t* v = acc[j >> 1] + 4 * k + 2 * (j & 1);
+              const float2 x = mul2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), f2);
+              d[j] = pack_digits(x.x, x.y);              // (two bf16, to nearest)
+            }
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(xb + put + 1024u * (4 * half + k)),
+                         "r"(d[0]), "r"(d[1]), "r"(d[2]), "r"(d[3])
+                         : "memory");
+          }
+        }
+        tc_fence_before();
+      }
+      rt_sync(kBarOut, kRtOut);
+      if (ok) {
+        // (all loads before the first store, which may be left out)
+        unsigned long long dst[4];
+        uint4 x[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            dst[j] = lds_u64(meta + 8u * (uint32_t)(16 * q + 8 * h + 2 * j + (lane >> 4)));
+            x[j] = lds_v4(xb + (uint32_t)(1024 * (2 * q + h) + 256 * j) + (get ^ (32u * j)));
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (dst[j]) __stcg(reinterpret_cast<uint4*>(dst[j]) + (lane & 15), x[j]);
+        }
+      }
+      rt_arrive(kBarFree + s, kFreeWarps);
+    }
+    // after a time-out: what was issued ends before TMEM is given back (bounded)
+    if (abort_sh && warp == kRtWarps)
+      for (int n = max(total - 2, 0); n < total; ++n) rt_wait(&bar_mma[n & 1], (uint32_t)((n >> 1) & 1));
+  } else {
+    // ---- rows: placed two to a slot of eight lanes ----
+    rt_regs_inc<kPlaceRegs>();
+    const int part = warp >> 2, i = 32 * q + lane;       // set-up: matrix row i, half of its inputs
+    const int slot = lane >> 3, sub = lane & 7, r0 = 8 * warp + 2 * slot;
+    const uint32_t norm_s = sb + kRtNorm, freq_s = sb + kRtFreq;
+    uint32_t* exch = reinterpret_cast<uint32_t*>(sm + kRtExch);
+    const Seg& g = seg_sh;
+    int mode = kNone, va = sub, vb = sub + 8;
+    uint32_t at_a = 0, at_b = 0;                         // this thread's vectors of row r0 in a buffer
+    if (tid < 64)
+      reinterpret_cast<uint64_t*>(sm + kRtFreq)[freq_slot(P.interleaved, tid)] = tid < P.half_rot ? __ldg(P.freq + tid) : 0ull;
+
+    // ---- a matrix: T hi and lo into TMEM, the channels' weights, the lanes' pairs ----
+    auto set_up = [&](const Place& w) {
+      const RotTensor& T = P.r.t[w.tt];
+      const float* trow = T.mat + ((size_t)w.mh * kHeadDim + i) * kHeadDim + 64 * part;
+      const bool had = T.mode == ROT_WHT;
+      const bool turned = P.rpos[w.tt] != nullptr;
+      if (!had) exch[128 * part + i] = top_exponent(trow);
+      // weights: float32, the first halves of all vectors of eight, then the second
+      const bool norm = P.norm[w.tt] != nullptr, weighted = norm || (turned && P.scale != 1.f);
+      if (part == 0) {
+        float x = norm ? __ldg(P.norm[w.tt] + i) : 1.f;
+        if (turned && i < 2 * P.half_rot) x *= P.scale;
+        reinterpret_cast<float*>(sm + kRtNorm)[((i >> 2) & 1) * 64 + (i >> 3) * 4 + (i & 3)] = x;
+      }
+      rt_sync(kBarPlace, kRtWarps);
+      // the matrix's power of two; a row's own where it would lose bits under that one
+      int k = 0;
+      bool uneven = false;
+      if (!had) {
+        uint32_t low = 255, high = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t e = max(exch[lane + 32 * j], exch[128 + lane + 32 * j]);
+          low = e ? min(low, e) : low;                   // (rows of zeros have no say)
+          high = max(high, e);
+        }
+        low = __reduce_min_sync(0xffffffffu, low);
+        high = __reduce_max_sync(0xffffffffu, high);
+        uneven = low + 8 < high;
+        k = fit_pow2((int)(uneven ? max(exch[i], exch[128 + i]) : high));
+        if (uneven && part == 0) reinterpret_cast<float*>(sm + kRtRowFac)[i] = pow2(-k);
+      }
+      if (tid == 0) uneven_sh = uneven;
+      const float t_back = had ? kInvSqrtDim : uneven ? 1.f : pow2(-k);
+      split_matrix(had ? nullptr : trow, i, part, pow2(k), tb + tlane);
+      // which channels a lane holds
+      mode = !turned ? kNone : P.interleaved ? kInter : P.half_rot % 8 == 0 ? kHalf : kAny;
+      va = sub;
+      vb = sub + 8;
+      if (mode == kHalf) {
+        const int h8 = P.half_rot / 8;
+        va = sub < h8 ? sub : 2 * h8 + 2 * (sub - h8);
+        vb = sub < h8 ? sub + h8 : va + 1;
+      }
+      uint32_t wtop = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) wtop = max(wtop, __float_as_uint(fabsf(reinterpret_cast<const float*>(sm + kRtNorm)[4 * lane + j])));
+      wtop = __reduce_max_sync(0xffffffffu, wtop);
+      // the largest weight and the rotation's sqrt 2, by exponents, rounded up; after the norm rows are below 2^4
+      const int grow = (weighted ? (int)(wtop >> 23) - 126 : 0) + (turned ? 1 : 0), kn = fit_pow2(130 + grow);
+      if (tid == 0) seg_sh = Seg{T.head_div > 1, norm, weighted, grow, pow2(kn), pow2(-kn) * t_back, t_back};
+      rt_sync(kBarPlace, kRtWarps);
+      at_a = (uint32_t)xs_offset(r0, 8 * va);
+      at_b = (uint32_t)xs_offset(r0, 8 * vb);
+    };
+
+    bool fresh = true;                                   // the chunk begins a matrix (or this CTA's work)
+    int freed = 0;                                       // chunks whose buffer is known to be free again
+    Place w = place_of(P, c_lo);
+    for (int n = 0; n < total; ++n) {
+      const int s = n & 1;
+      // (at a new matrix the last one's results are out: TMEM and what its set-up left may be overwritten)
+      for (const int want = fresh ? n : n - 1; freed < want; ++freed) rt_sync(kBarFree + (freed & 1), kFreeWarps);
+      if (fresh) {
+        tc_fence_after();
+        set_up(w);
+      }
+      if (!abort_sh && !__all_sync(0xffffffffu, rt_wait(&bar_raw[s], (uint32_t)((n >> 1) & 1)))) abort_sh = 1;
+      const uint32_t xb = sb + (uint32_t)(s * kRtXBuf), raw = sb + (uint32_t)(kRtRaw + s * kRtRawBuf);
+      const uint32_t fac = sb + (uint32_t)(kRtFac + s * kRtRows * 4), pos = sb + (uint32_t)(kRtPos + s * kRtRows * 4);
+      const int left = P.r.t[w.tt].rows * P.r.t[w.tt].head_div - w.c * kRtRows - r0;
+      if (mode == kHalf) place_rows<kHalf>(P, g, left, pos, r0, sub, va, vb, at_a, at_b, raw, kBarRaw + s, xb, norm_s, freq_s, fac);
+      else if (mode == kInter) place_rows<kInter>(P, g, left, pos, r0, sub, va, vb, at_a, at_b, raw, kBarRaw + s, xb, norm_s, freq_s, fac);
+      else if (mode == kAny) place_rows<kAny>(P, g, left, pos, r0, sub, va, vb, at_a, at_b, raw, kBarRaw + s, xb, norm_s, freq_s, fac);
+      else place_rows<kNone>(P, g, left, pos, r0, sub, va, vb, at_a, at_b, raw, kBarRaw + s, xb, norm_s, freq_s, fac);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      tc_fence_before();
+      rt_arrive(kBarX + s, kXWarps);
+      fresh = ++w.c == w.cpm;
+      if (fresh && n + 1 < total) w = place_of(P, c_lo + n + 1);
+    }
+    for (; freed < total; ++freed) rt_sync(kBarFree + (freed & 1), kFreeWarps);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0 && abort_sh) set_status(P.r.status, KVQ_ERR_TIMEOUT);
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tb), "r"(kRtCols) : "memory");
+}
+
+}  // namespace
+
+int launch_rope_tc(RopeParams P, cudaStream_t stream) {
+  long long total = 0;
+  for (int t = 0; t < 3; ++t) {
+    P.r.n_dense[t] = 0;
+    if (P.r.t[t].mode == ROT_COPY) continue;
+    const long long cpm = ((long long)P.r.t[t].rows * P.r.t[t].head_div + kRtRows - 1) / kRtRows;
+    const long long here = (P.r.t[t].heads / P.r.t[t].head_div) * cpm;
+    P.r.n_dense[t] = (int)here;                          // (fewer than 2^30: the caller has checked rows x heads)
+    total += here;
+  }
+  if (total == 0) return KVQ_OK;
+  if (total > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
+  P.r.dense_total = (int)total;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ERR_CUDA;
+  static std::mutex mu;
+  static unsigned long long attr_done = 0;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!(attr_done & (1ull << dev))) {
+      if (cudaFuncSetAttribute(rope_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRtSmem) != cudaSuccess)
+        return KVQ_ERR_CUDA;
+      attr_done |= 1ull << dev;
+    }
+  }
+  const int ctas = (int)std::min(total, 2LL * kSms);
+  rope_tc_kernel<<<(unsigned)ctas, kRtThreads, kRtSmem, stream>>>(P);
+  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+}  // namespace kvq
