@@ -6,14 +6,18 @@
 // Every operation rounds to float32 by itself (no contraction), sums are float32 in one fixed order.
 //
 // Bytes bound it: a logit is read once and a probability written once (64 rows of 152 K tokens: 2 + 2 + 4 bytes each
-// with the counts), which needs the row on the chip between the two passes.  A row of 152 K float32 is 0.6 MB, more than an
+// with the counts), which needs the row on the chip between the two.  A row of 152 K float32 is 0.6 MB, more than an
 // SM's shared memory, so a cluster of CTAs takes a row, a contiguous slice each, and they exchange one (maximum, sum) pair
-// through distributed shared memory.  Biases and the drafted path touch few tokens: the pass over the slice does without them and the
+// through distributed shared memory.  At 6.8 TB/s an SM has about thirty instructions a token to spare in all.  Penalties are therefore
+// taken without branches (in a history of thousands nearly every warp meets a counted token: behind one they took 64 instructions a
+// token, and 64 trees of 16 nodes over 152 K 531 us instead of 231), and loads come in batches that are all on their way
+// before the first is used.  Biases and the drafted path touch few tokens: the pass over the slice does without them and the
 // tokens concerned are computed again afterwards, by token, so that one that is in both lists is right either way.
 #include <cooperative_groups.h>
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -23,9 +27,10 @@ namespace cg = cooperative_groups;
 namespace kvq {
 namespace {
 
-constexpr int kLThreads = 512;
+constexpr int kLThreads = 256;
 constexpr int kLWarps = kLThreads / 32;
 constexpr int kMaxCluster = 16;
+constexpr int kBatch = 6;            // fours that a thread asks for at once
 constexpr int kNodes = KVQ_TREE_MAX_NODES;
 constexpr float kInf = __builtin_huge_valf();
 
@@ -55,56 +60,48 @@ __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 
-// Four logits from token v on.
+// Four logits as they lie, and as numbers.
 template <typename T>
-__device__ __forceinline__ void load_logits(const T* row, bool wide, int v, int v1, float (&x)[4]) {
-  if (wide && v + 4 <= v1) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 t = *reinterpret_cast<const float4*>(row + v);
-      x[0] = t.x;
-      x[1] = t.y;
-      x[2] = t.z;
-      x[3] = t.w;
-    } else {
-      const uint2 t = *reinterpret_cast<const uint2*>(row + v);
-      const T* h = reinterpret_cast<const T*>(&t);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = to_float(h[k]);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = v + k < v1 ? to_float(row[v + k]) : -kInf;
+struct Four {
+  using Raw = std::conditional_t<sizeof(T) == 4, uint4, uint2>;
+  static __device__ __forceinline__ Raw none() {
+    if constexpr (sizeof(T) == 4) return make_uint4(0u, 0u, 0u, 0u);
+    else return make_uint2(0u, 0u);
   }
-}
-__device__ __forceinline__ void load_counts(const uint16_t* row, bool wide, int v, int v1, uint32_t (&n)[4]) {
-  if (wide && v + 4 <= v1) {
-    const uint2 t = __ldg(reinterpret_cast<const uint2*>(row + v));
-    n[0] = t.x & 0xffffu;
-    n[1] = t.x >> 16;
-    n[2] = t.y & 0xffffu;
-    n[3] = t.y >> 16;
-  } else {
+  static __device__ __forceinline__ void numbers(const Raw& r, float (&x)[4]) {
+    const T* h = reinterpret_cast<const T*>(&r);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) n[k] = v + k < v1 ? (uint32_t)__ldg(row + v + k) : 0u;
+    for (int k = 0; k < 4; ++k) x[k] = to_float(h[k]);
   }
-}
+};
 
 struct Rules {
   float rep, freq, pres;
+  float inv;                 // 1 / rep, to nearest
 };
-// n: the token's count as it is kept, times: how often it has been generated.
-__device__ __forceinline__ float penalized(const Rules& R, float x, bool held, uint32_t times) {
-  if (held) x = x > 0.f ? __fdiv_rn(x, R.rep) : __fmul_rn(x, R.rep);
-  if (times) {
-    x = __fsub_rn(x, __fmul_rn(R.freq, (float)times));
-    x = __fsub_rn(x, R.pres);
-  }
-  return x;
+// A value under the penalties of its token; count: as it is kept (or more, with the path's).  x / rep is the product with
+// the rounded reciprocal, and its remainder: the quotient to nearest where nothing vanishes on the way (Markstein's theorem).
+__device__ __forceinline__ float penalized(const Rules& R, float x, uint32_t count, uint32_t times) {
+  const float q = __fmul_rn(x, R.inv);
+  float y = x > 0.f ? __fmaf_rn(__fmaf_rn(-q, R.rep, x), R.inv, q) : __fmul_rn(x, R.rep);
+  y = __fsub_rn(y, __fmul_rn(R.freq, (float)times));
+  y = __fsub_rn(y, times ? R.pres : 0.f);
+  return count ? y : x;
+}
+
+// (x - r) k of two numbers, each operation rounded
+__device__ __forceinline__ float2 scaled_below(float x, float y, float2 minus_r, float2 k) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " add.rn.f32x2 x, x, y;\n mul.rn.f32x2 x, x, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(x), "f"(y), "f"(minus_r.x), "f"(minus_r.y), "f"(k.x), "f"(k.y));
+  return d;
 }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));   // (what is below 2^-126 is 0)
   return y;
 }
 
@@ -119,31 +116,70 @@ __device__ __forceinline__ float warp_add(float v) {
   return v;
 }
 
-template <typename T>
+// The row's sequence: how many of them end at or before it.  A warp looks at 32 ends at a time.
+__device__ __forceinline__ int sequences_before(const int32_t* cu_rows, int batch, int row, int lane) {
+  int lo = 0, hi = batch;                                // (the answer lies between them)
+  if (batch <= 128) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = 32 * k + lane;
+      n += __popc(__ballot_sync(0xffffffffu, i < batch && cu_rows[min(i, batch - 1) + 1] <= row));
+    }
+    return n;
+  }
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step - 1;
+    const int n = __popc(__ballot_sync(0xffffffffu, i < hi && cu_rows[min(i, batch - 1) + 1] <= row));
+    lo = min(lo + n * step, hi);
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+template <typename T, bool kCounts, bool kMask>
 __global__ void __launch_bounds__(kLThreads) logits_kernel(const __grid_constant__ LogitParams P) {
   extern __shared__ __align__(16) float xs[];          // the slice
   __shared__ float wred[kLWarps];
   __shared__ int wbest[kLWarps];
   __shared__ int par[kNodes], tok[kNodes], path[kNodes], n_path_sh;
-  __shared__ Share mine;
+  __shared__ Share shares[kMaxCluster];                // of every CTA of the cluster, written by it
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = (int)(blockIdx.x / (unsigned)ranks);
   const bool lead = rank == 0 && tid == 0;
+  const int v0 = min(P.vocab, rank * P.per), v1 = min(P.vocab, v0 + P.per);
+  const int fours = (v1 - v0) >> 2, rest = (v1 - v0) & 3;
+  using F = Four<T>;
+  using Raw = typename F::Raw;
+  const T* l = static_cast<const T*>(P.logits) + (long long)row * P.l_stride;
+  const Raw* lw = reinterpret_cast<const Raw*>(l + v0);
+  const bool l_wide = (reinterpret_cast<uintptr_t>(l) & (4 * sizeof(T) - 1)) == 0;
   pdl_trigger();
+  cluster_arrive();                                      // (waited for before a CTA writes to another)
   pdl_wait();
-
-  // ---- the row's sequence: how many of the sequences end at or before it ----
-  int before = 0;
-  for (int i0 = 0; i0 < P.batch; i0 += kLThreads) {
-    const int i = i0 + tid;
-    before += __syncthreads_count(i < P.batch && P.cu_rows[i + 1] <= row);
+  // the first logits and the rest of the slice are on their way while the row's sequence and its rules are found
+  Raw r[kBatch];
+  if (!kMask) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = tid + k * kLThreads;
+      r[k] = F::none();
+      if (l_wide && i < fours) r[k] = lw[i];
+    }
+    for (int v = v0 + 4 * kBatch * kLThreads + tid * (128 / (int)sizeof(T)); v < v1; v += kLThreads * (128 / (int)sizeof(T)))
+      prefetch_l2_line(l + v);
   }
-  const int b = before;
+
+  const int b = sequences_before(P.cu_rows, P.batch, row, lane);
   const bool covered = b < P.batch && P.cu_rows[b] >= 0 && P.cu_rows[b] <= row && P.cu_rows[b + 1] > row;
   if (!covered) {                                        // (the same in all CTAs of the cluster)
     if (lead) set_status(P.status, KVQ_ERR_BOUNDS);
+    cluster_wait();
     return;
   }
   const int first = P.cu_rows[b], node = row - first;
@@ -155,14 +191,15 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(const __grid_constant
   R.rep = U.repetition ? U.repetition[b] : 1.f;
   R.freq = U.frequency ? U.frequency[b] : 0.f;
   R.pres = U.presence ? U.presence[b] : 0.f;
+  R.inv = __frcp_rn(R.rep);
   const float heat = U.temperature ? U.temperature[b] : 1.f;
-  const bool sound = R.rep > 0.f && R.rep < kInf && fabsf(R.freq) < kInf && fabsf(R.pres) < kInf && heat >= 0.f && heat < kInf;
+  const bool sound = R.rep >= 0x1p-60f && R.rep <= 0x1p60f && fabsf(R.freq) < kInf && fabsf(R.pres) < kInf && heat >= 0.f && heat < kInf;
   const bool greedy = heat < 0x1p-120f;                  // (1 / T must be a float32)
   const float k2 = greedy ? 0.f : __fdiv_rn(1.4426950408889634f, heat);
-  const uint16_t* counts = U.counts ? U.counts + (long long)b * U.count_stride : nullptr;
+  const uint16_t* counts = kCounts ? U.counts + (long long)b * U.count_stride : nullptr;
   const uint32_t* mask = nullptr;
   bool fault = false, skip = !sound;                     // skip: a row of zeros
-  if (U.mask) {
+  if (kMask) {
     const int m = U.mask_row ? U.mask_row[row] : row;
     if (m < -1 || m >= U.n_masks) fault = skip = true;
     else if (m >= 0) mask = U.mask + (long long)m * U.mask_stride;
@@ -179,15 +216,14 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(const __grid_constant
   const bool tree = P.parent != nullptr;
   if (tree && n > kNodes) fault = skip = true;
 
-  // ---- the node's path: tokens of the node and its ancestors, roots left out ----
-  if (tid == 0) n_path_sh = 0;
-  if (tree && !skip) {
-    for (int i = tid; i <= node; i += kLThreads) {
+  // ---- the node's path: tokens of the node and its ancestors, roots left out (the last warp; the others go on) ----
+  if (tree && !skip && warp == kLWarps - 1) {
+    for (int i = lane; i <= node; i += 32) {
       par[i] = P.parent[first + i];
       tok[i] = P.token[first + i];
     }
-    __syncthreads();
-    if (tid == 0) {
+    __syncwarp();
+    if (lane == 0) {
       int at = node, np = 0;
       while (par[at] >= 0 && par[at] < at) {             // (at falls: at most kNodes steps)
         if (tok[at] >= 0 && tok[at] < P.vocab) path[np++] = tok[at];
@@ -198,47 +234,96 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(const __grid_constant
       n_path_sh = np;
     }
   }
-  __syncthreads();
-  const int n_path = n_path_sh;
-  const bool later = n_path > 0 || b1 > b0;              // some tokens are computed again
   if (fault && rank == 0) set_status(P.status, KVQ_ERR_BOUNDS);
   if (!sound && lead) set_status(P.status, KVQ_ERR_NONFINITE);
 
-  const int v0 = min(P.vocab, rank * P.per), v1 = min(P.vocab, v0 + P.per);
-  const T* l = static_cast<const T*>(P.logits) + (long long)row * P.l_stride;
   float* out = P.p + (long long)row * P.p_stride;
-  const bool l_wide = (reinterpret_cast<uintptr_t>(l) & (4 * sizeof(T) - 1)) == 0;
   const bool c_wide = (reinterpret_cast<uintptr_t>(counts) & 7) == 0;
   const bool p_wide = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-  bool bad = false;
   float top = -kInf;
 
-  // ---- pass 1: the slice's values, without biases and the path ----
   if (!skip) {
-#pragma unroll 4
-    for (int v = v0 + 4 * tid; v < v1; v += 4 * kLThreads) {
-      const uint32_t allowed = mask ? mask[v >> 5] >> (v & 31) : 15u;
-      float x[4] = {-kInf, -kInf, -kInf, -kInf};
-      if (allowed & 15u) {
-        load_logits(l, l_wide, v, v1, x);
-        if (counts) {
-          uint32_t c[4];
-          load_counts(counts, c_wide, v, v1, c);
-          if (c[0] | c[1] | c[2] | c[3])
+    // ---- pass 1: the slice's values, without biases and the path ----
+    auto keep = [&](int i, float (&x)[4], uint32_t allowed, uint2 c) {
+      if (kCounts) {
+        const uint32_t n[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = penalized(R, x[k], c[k] != 0u, c[k] & KVQ_COUNT_MOST);
-        }
+        for (int k = 0; k < 4; ++k) x[k] = penalized(R, x[k], n[k], n[k] & KVQ_COUNT_MOST);
+      }
+      if (kMask)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (!((allowed >> k) & 1u)) x[k] = -kInf;
-          top = fmaxf(top, x[k]);
-          if (!later) bad |= !(x[k] < kInf);
+        for (int k = 0; k < 4; ++k) x[k] = (allowed >> k) & 1u ? x[k] : -kInf;
+      top = fmaxf(fmaxf(fmaxf(top, x[0]), fmaxf(x[1], x[2])), x[3]);   // (drops a NaN: the sum will not)
+      *reinterpret_cast<float4*>(xs + 4 * i) = make_float4(x[0], x[1], x[2], x[3]);
+    };
+    const uint2* cw = reinterpret_cast<const uint2*>(counts + (kCounts ? v0 : 0));
+    auto batch = [&](int i0, auto whole) {               // whole: all kBatch of them are there
+      uint2 c[kBatch];
+      uint32_t m[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kLThreads;
+        m[k] = whole.value || i < fours ? 15u : 0u;
+        if (kMask && mask && m[k]) m[k] = (mask[(v0 >> 5) + (i >> 3)] >> (4 * (i & 7))) & 15u;
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kLThreads;
+        c[k] = make_uint2(0u, 0u);
+        if ((whole.value && !kMask) || m[k]) {
+          if (kMask || i0 != tid) r[k] = lw[i];          // (without a mask the first ones are here)
+          if (kCounts) c[k] = __ldg(cw + i);
         }
       }
-      *reinterpret_cast<float4*>(xs + (v - v0)) = make_float4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kLThreads;
+        if (whole.value || i < fours) {
+          float x[4];
+          F::numbers(r[k], x);
+          keep(i, x, m[k], c[k]);
+        }
+      }
+    };
+    const bool wide = l_wide && (!kCounts || c_wide);
+    if (wide) {
+      int i0 = 0;
+      for (; i0 + kBatch * kLThreads <= fours; i0 += kBatch * kLThreads) batch(i0 + tid, std::true_type{});
+      if (i0 + tid < fours) batch(i0 + tid, std::false_type{});
     }
-    if (later) {
-      __syncthreads();
+    // (rows that do not begin on a boundary, and the slice's last tokens: token by token)
+    constexpr int kFew = 3;
+    for (int i0 = (wide ? fours : 0) + tid; i0 < fours + (rest > 0); i0 += kFew * kLThreads) {
+      uint32_t m[kFew], n[kFew][2];
+      float x[kFew][4];
+#pragma unroll
+      for (int k = 0; k < kFew; ++k) {
+        const int i = i0 + k * kLThreads;
+        m[k] = i < fours ? 15u : i == fours ? (1u << rest) - 1u : 0u;
+        if (kMask && mask && m[k]) m[k] &= mask[(v0 >> 5) + (i >> 3)] >> (4 * (i & 7));
+      }
+#pragma unroll
+      for (int k = 0; k < kFew; ++k) {
+        const int v = v0 + 4 * (i0 + k * kLThreads);
+        uint32_t c[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool on = (m[k] >> e) & 1u;
+          x[k][e] = on ? to_float(l[v + e]) : -kInf;
+          c[e] = on && kCounts ? (uint32_t)__ldg(counts + v + e) : 0u;
+        }
+        n[k][0] = c[0] | c[1] << 16;
+        n[k][1] = c[2] | c[3] << 16;
+      }
+#pragma unroll
+      for (int k = 0; k < kFew; ++k) {
+        const int i = i0 + k * kLThreads;
+        if (i < fours + (rest > 0)) keep(i, x[k], m[k], make_uint2(n[k][0], n[k][1]));
+      }
+    }
+    if (tree || b1 > b0) __syncthreads();
+    const int n_path = tree ? n_path_sh : 0;
+    if (n_path > 0 || b1 > b0) {
       // ---- tokens of the path and the biases: again, by token ----
       for (int i = tid; i < n_path + (b1 - b0); i += kLThreads) {
         int t;
@@ -256,6 +341,7 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(const __grid_constant
         float x = -kInf;
         if (!mask || ((mask[t >> 5] >> (t & 31)) & 1u)) {
           x = to_float(l[t]);
+          const uint32_t c = kCounts ? (uint32_t)counts[t] : 0u;
           int lo = b0, hi = b1;                          // the first entry that is not below t
           while (lo < hi) {
             const int mid = (lo + hi) >> 1;
@@ -263,19 +349,18 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(const __grid_constant
             else hi = mid;
           }
           if (lo < b1 && U.bias_token[lo] == t) x = __fadd_rn(x, U.bias[lo]);
-          const uint32_t c = counts ? (uint32_t)counts[t] : 0u;
           uint32_t times = c & KVQ_COUNT_MOST;
           for (int j = 0; j < n_path; ++j) times += path[j] == t;
-          x = penalized(R, x, (c | times) != 0u, times);
+          x = penalized(R, x, c | times, times);
         }
         xs[t - v0] = x;
       }
       __syncthreads();
       top = -kInf;
+#pragma unroll 4
       for (int v = 4 * tid; v < v1 - v0; v += 4 * kLThreads) {
         const float4 x = *reinterpret_cast<const float4*>(xs + v);
         top = fmaxf(fmaxf(fmaxf(top, x.x), fmaxf(x.y, x.z)), x.w);
-        bad |= !(x.x < kInf && x.y < kInf && x.z < kInf && x.w < kInf);
       }
     }
   }
@@ -283,7 +368,7 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(const __grid_constant
   // ---- the slice's maximum ----
   top = warp_max(top);
   if (lane == 0) wred[warp] = top;
-  bad = __syncthreads_or(bad);
+  __syncthreads();
   top = wred[0];
 #pragma unroll
   for (int w = 1; w < kLWarps; ++w) top = fmaxf(top, wred[w]);
@@ -292,41 +377,40 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(const __grid_constant
   // ---- pass 2: exponentials and their sum, or the lowest token of the maximum ----
   if (!skip && !greedy) {
     const float ref = top == -kInf ? 0.f : top;
+    const float2 r2 = make_float2(-ref, -ref), kk = make_float2(k2, k2);
     float s = 0.f;
 #pragma unroll 4
     for (int v = 4 * tid; v < v1 - v0; v += 4 * kLThreads) {
       float4 x = *reinterpret_cast<const float4*>(xs + v);
-      x.x = ex2((x.x - ref) * k2);
-      x.y = ex2((x.y - ref) * k2);
-      x.z = ex2((x.z - ref) * k2);
-      x.w = ex2((x.w - ref) * k2);
+      const float2 y = scaled_below(x.x, x.y, r2, kk), z = scaled_below(x.z, x.w, r2, kk);
+      x = make_float4(ex2(y.x), ex2(y.y), ex2(z.x), ex2(z.y));
       *reinterpret_cast<float4*>(xs + v) = x;
       s += (x.x + x.y) + (x.z + x.w);
     }
     s = warp_add(s);
     if (lane == 0) wred[warp] = s;
   } else if (!skip) {
-    int best = P.vocab;
-    for (int v = tid; v < v1 - v0; v += kLThreads)
-      if (xs[v] == top) best = min(best, v0 + v);
+    int best = P.vocab;                                  // (-1: a value that is none)
+    for (int v = tid; v < v1 - v0; v += kLThreads) {
+      const float x = xs[v];
+      if (x == top) best = min(best, v0 + v);
+      if (!(x < kInf)) best = -1;
+    }
     best = __reduce_min_sync(0xffffffffu, best);
     if (lane == 0) wbest[warp] = best;
   }
   __syncthreads();
-  if (tid == 0) {
-    float s = 0.f;
-    int best = P.vocab;
-    if (!skip) {
-      if (greedy)
-        for (int w = 0; w < kLWarps; ++w) best = min(best, wbest[w]);
-      else
-        for (int w = 0; w < kLWarps; ++w) s += wred[w];
-    }
-    mine = Share{top, s, best, bad ? 1 : 0};
+  cluster_wait();                                        // (every CTA of the cluster has begun)
+  if (warp == 0) {
+    const float s = warp_add(!skip && !greedy && lane < kLWarps ? wred[lane] : 0.f);
+    const int best = __reduce_min_sync(0xffffffffu, !skip && greedy && lane < kLWarps ? wbest[lane] : P.vocab);
+    // (a NaN or an infinity in the slice makes its sum a NaN)
+    if (lane < ranks) *cluster.map_shared_rank(&shares[rank], lane) = Share{top, s, best, best < 0 || !(s < kInf)};
   }
-  cluster.sync();
+  cluster_arrive();
+  cluster_wait();
   Share other{-kInf, 0.f, P.vocab, 0};
-  if (lane < ranks) other = *cluster.map_shared_rank(&mine, lane);
+  if (lane < ranks) other = shares[lane];
   const float whole = warp_max(other.top);
   const float share = other.top == -kInf ? 0.f : ex2((other.top - whole) * k2);
   const float sum = warp_add(other.sum * share);
@@ -337,31 +421,23 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(const __grid_constant
 
   // ---- pass 3: the slice's probabilities ----
   const bool zeros = skip || none;
+  if (p_wide) {
 #pragma unroll 4
-  for (int v = v0 + 4 * tid; v < v1; v += 4 * kLThreads) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (!zeros && !greedy) {
-      x = *reinterpret_cast<const float4*>(xs + (v - v0));
-      x.x *= factor;
-      x.y *= factor;
-      x.z *= factor;
-      x.w *= factor;
-    } else if (!zeros) {
-      x.x = v == best ? 1.f : 0.f;
-      x.y = v + 1 == best ? 1.f : 0.f;
-      x.z = v + 2 == best ? 1.f : 0.f;
-      x.w = v + 3 == best ? 1.f : 0.f;
-    }
-    if (p_wide && v + 4 <= v1) {
+    for (int i = tid; i < fours; i += kLThreads) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int v = v0 + 4 * i;
+      if (!zeros && !greedy) {
+        x = *reinterpret_cast<const float4*>(xs + 4 * i);
+        x = make_float4(x.x * factor, x.y * factor, x.z * factor, x.w * factor);
+      } else if (!zeros) {
+        x = make_float4(v == best ? 1.f : 0.f, v + 1 == best ? 1.f : 0.f, v + 2 == best ? 1.f : 0.f, v + 3 == best ? 1.f : 0.f);
+      }
       *reinterpret_cast<float4*>(out + v) = x;
-    } else {
-      out[v] = x.x;
-      if (v + 1 < v1) out[v + 1] = x.y;
-      if (v + 2 < v1) out[v + 2] = x.z;
-      if (v + 3 < v1) out[v + 3] = x.w;
     }
   }
-  cluster.sync();                                        // (the others have read `mine`)
+#pragma unroll 4
+  for (int i = (p_wide ? 4 * fours : 0) + tid; i < v1 - v0; i += kLThreads)
+    out[v0 + i] = zeros ? 0.f : greedy ? (v0 + i == best ? 1.f : 0.f) : xs[i] * factor;
 }
 
 // ---- counts ------------------------------------------------------------------------------------
@@ -445,8 +521,9 @@ __global__ void __launch_bounds__(256) count_kernel(const __grid_constant__ Coun
   }
 }
 
-template <typename T>
+template <typename T, bool kCounts, bool kMask>
 int launch_logits(LogitParams& P, cudaStream_t stream) {
+  const auto kernel = logits_kernel<T, kCounts, kMask>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ERR_CUDA;
   static std::mutex mu;
@@ -454,23 +531,28 @@ int launch_logits(LogitParams& P, cudaStream_t stream) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!(attr_done & (1ull << dev))) {
-      if (cudaFuncSetAttribute(logits_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, KVQ_LOGITS_MAX_VOCAB / kMaxCluster * 4) !=
-              cudaSuccess ||
-          cudaFuncSetAttribute(logits_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, KVQ_LOGITS_MAX_VOCAB / kMaxCluster * 4) != cudaSuccess ||
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return KVQ_ERR_CUDA;
       attr_done |= 1ull << dev;
     }
   }
-  // CTAs of a row: slices of at most 20,480 tokens (80 KB: two CTAs on an SM), and more of them while the rows do
-  // not fill the SMs
-  int c = 1;
-  while (c < kMaxCluster && ((P.vocab + c - 1) / c > 20480 || (c * (long long)P.n_rows < kSms && P.vocab / c > 2048))) c *= 2;
+  // CTAs of a row: slices of at most 13,000 tokens (51 KB: four CTAs of 256 threads on an SM; 64 trees of 16 nodes over 152 K tokens
+  // take 231 us so, 245 us in slices of 17 K and 384 threads, 254 in slices of 25 K and 512, 264 in slices of 9.5 K and 256), and more of them while the rows do not fill the SMs
+  int c = std::max(1, (P.vocab + 12999) / 13000);
+  while (c < kMaxCluster && c * (long long)P.n_rows < kSms && P.vocab / c > 2048) ++c;
+  c = std::min(c, kMaxCluster);
   P.per = ((P.vocab + c - 1) / c + 31) / 32 * 32;
   if ((long long)P.n_rows * c > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
-  return launch_pdl_cluster(logits_kernel<T>, c, dim3((unsigned)((long long)P.n_rows * c)), dim3(kLThreads),
-                            (size_t)P.per * 4, stream, P) == cudaSuccess
+  return launch_pdl_cluster(kernel, c, dim3((unsigned)((long long)P.n_rows * c)), dim3(kLThreads), (size_t)P.per * 4, stream, P) ==
+                 cudaSuccess
              ? KVQ_OK
              : KVQ_ERR_CUDA;
+}
+template <typename T>
+int launch_logits(LogitParams& P, cudaStream_t stream) {
+  if (P.u.mask) return P.u.counts ? launch_logits<T, true, true>(P, stream) : launch_logits<T, false, true>(P, stream);
+  return P.u.counts ? launch_logits<T, true, false>(P, stream) : launch_logits<T, false, false>(P, stream);
 }
 
 }  // namespace

@@ -522,7 +522,7 @@ KVQ_API int kv_rope_qk(const kvq_config* cfg, const kvq_transform* tr, const kvq
 
 typedef struct kvq_logit_rules {         /* device pointers; NULL: that rule is not applied */
   const float*    temperature; /* [B] >= 0; 0: the best token alone, the lowest id among equals (NULL: 1)        */
-  const float*    repetition;  /* [B] > 0: logits of tokens held, prompt or generated: l > 0: l / r, else l * r */
+  const float*    repetition;  /* [B] 2^-60 .. 2^60: logits of tokens held, prompt or generated: l > 0: l / r, else l * r */
   const float*    frequency;   /* [B]: less by this for every time the token has been generated                 */
   const float*    presence;    /* [B]: less by this once the token has been generated                           */
   const uint16_t* counts;      /* as above (NULL: nothing is held yet)                                          */
@@ -548,7 +548,7 @@ typedef struct kvq_logit_rules {         /* device pointers; NULL: that rule is 
  * masked tokens to -infinity, whatever stood there; softmax of l / temperature.
  * KVQ_ERR_NONFINITE and a row of zeros: where nothing is left (every token masked or at -infinity), where a logit that
  * is not masked becomes NaN or +infinity, or where a number of the sequence's rules is not finite, the temperature
- * negative or the repetition not positive.  KVQ_ERR_BOUNDS and a row of zeros: a mask that does not exist, more than KVQ_TREE_MAX_NODES nodes
+ * negative or the repetition not within 2^-60 .. 2^60.  Probabilities below 2^-126 are 0.  KVQ_ERR_BOUNDS and a row of zeros: a mask that does not exist, more than KVQ_TREE_MAX_NODES nodes
  * in a sequence.  KVQ_ERR_BOUNDS: a parent that is not a lower node (the row goes by the path up to there), a token of the path or of a
  * bias outside the vocabulary (left out), biases out of order (an entry that is not above the one before it may be left out), and cu_rows that do not cover n_rows:
  * rows behind the last sequence are not written.  Sums are taken in one order: the same bits on every run.
