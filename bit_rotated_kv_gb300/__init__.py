@@ -603,12 +603,29 @@ def _head_rows(dev: int, t, n: int, heads: int, what: str):
         if n > 0:
             raise KVQError(KVQ_ERR_INVALID_ARG, what)
         return 0, heads * 128
-    if (t.dim() != 3 or t.dtype is not torch.bfloat16 or t.shape[0] != n or t.shape[1] != heads or t.shape[2] != 128 or t.stride(2) != 1
-            or (heads > 1 and t.stride(1) != 128) or (n > 1 and t.stride(0) < heads * 128)):
+    if t.dtype is not torch.bfloat16 or t.shape != (n, heads, 128):
+        raise KVQError(KVQ_ERR_INVALID_ARG, what)
+    row, head, channel = t.stride()
+    if channel != 1 or (heads > 1 and head != 128) or (n > 1 and row < heads * 128):
         raise KVQError(KVQ_ERR_INVALID_ARG, what)
     if t.get_device() != dev:
         raise KVQError(KVQ_ERR_INVALID_ARG, f"{what} (another device)")
-    return t.data_ptr(), t.stride(0) if n > 1 else heads * 128
+    return t.data_ptr(), row if n > 1 else heads * 128
+
+
+def _transform(dev: int, tr: Transform, cfg: KVConfig):
+    """The C struct of a transform whose matrices have been looked at (once for a device and a number of heads, again after a
+    field changes)."""
+    cc, key = tr.c(), (dev, cfg.n_kv_heads)
+    seen = tr.__dict__.get("_seen")
+    if seen is None or seen[0] is not cc or seen[1] != key:
+        for name in ("t_k", "t_k_inv_t", "t_v"):
+            t = getattr(tr, name)
+            if t is not None:
+                _addr(dev, t, torch.float32, cfg.n_kv_heads * 128 * 128, f"kv_rope_qk: {name}")
+        seen = (cc, key, ctypes.byref(cc))
+        object.__setattr__(tr, "_seen", seen)
+    return seen[2]
 
 
 def kv_rope_qk(cfg: KVConfig, tr: Transform, rope: Rope | None, q, q_out, q_pos, k, v, seq_idx, pos, rope_pos, cache: KVCache,
@@ -618,27 +635,19 @@ def kv_rope_qk(cfg: KVConfig, tr: Transform, rope: Rope | None, q, q_out, q_pos,
     dev, i32 = _current_device(), torch.int32
     n_q = 0 if q is None else q.shape[0]
     n_kv = 0 if k is None else k.shape[0]
-    qa, qs = _head_rows(dev, q, n_q, cfg.n_q_heads, "kv_rope_qk: q")
-    ka, ks = _head_rows(dev, k, n_kv, cfg.n_kv_heads, "kv_rope_qk: k")
-    va, vs = _head_rows(dev, v, n_kv, cfg.n_kv_heads, "kv_rope_qk: v")
-    out = _addr(dev, q_out, torch.bfloat16, n_q * cfg.n_q_heads * 128, "kv_rope_qk: q_out")
-    turned = rope is not None and rope.rot_dim > 0
-    qp = _addr(dev, q_pos, i32, n_q, "kv_rope_qk: q_pos") if turned or q_pos is not None else 0
+    hq, hkv = cfg.n_q_heads, cfg.n_kv_heads
+    qa, qs = _head_rows(dev, q, n_q, hq, "kv_rope_qk: q")
+    ka, ks = _head_rows(dev, k, n_kv, hkv, "kv_rope_qk: k")
+    va, vs = _head_rows(dev, v, n_kv, hkv, "kv_rope_qk: v")
+    out = _addr(dev, q_out, torch.bfloat16, n_q * hq * 128, "kv_rope_qk: q_out")
+    qp = _addr(dev, q_pos, i32, n_q, "kv_rope_qk: q_pos") if q_pos is not None or (rope is not None and rope.rot_dim > 0) else 0
     seq = _addr(dev, seq_idx, i32, n_kv, "kv_rope_qk: seq_idx")
     at = _addr(dev, pos, i32, n_kv, "kv_rope_qk: pos")
     far = 0 if rope_pos is None else _addr(dev, rope_pos, i32, n_kv, "kv_rope_qk: rope_pos")
-    rc = lib().kv_rope_qk(ctypes.byref(cfg.c()), ctypes.byref(_transform(dev, tr, cfg)),
-                          None if rope is None else ctypes.byref(rope.c(dev)), qa, qs, out, qp, n_q, ka, ks, va, vs, seq, at, far, n_kv,
-                          _cache(dev, cache, "kv_rope_qk"), _status(dev, status, "kv_rope_qk"), _stream_of(dev, stream))
-    _check(rc, "kv_rope_qk")
-
-
-def _transform(dev: int, tr: Transform, cfg: KVConfig) -> CTransform:
-    for name in ("t_k", "t_k_inv_t", "t_v"):
-        t = getattr(tr, name)
-        if t is not None:
-            _addr(dev, t, torch.float32, cfg.n_kv_heads * 128 * 128, f"kv_rope_qk: {name}")
-    return tr.c()
+    rc = lib().kv_rope_qk(cfg.c(), _transform(dev, tr, cfg), None if rope is None else rope.c(dev), qa, qs, out, qp, n_q, ka, ks, va, vs,
+                          seq, at, far, n_kv, _cache(dev, cache, "kv_rope_qk"), _status(dev, status, "kv_rope_qk"), _stream_of(dev, stream))
+    if rc:
+        _check(rc, "kv_rope_qk")
 
 
 @dataclass
@@ -689,10 +698,12 @@ class LogitRules:
 
 def _count_rows(dev: int, t, batch: int, vocab: int, where: str):
     """Address and row stride of [batch, >= vocab] counts."""
-    if (t is None or t.dim() != 2 or t.dtype is not torch.int16 or t.shape[0] != batch or t.shape[1] < vocab or t.shape[1] % 2
-            or not t.is_contiguous()):
+    if t is None or t.dim() != 2:
         raise KVQError(KVQ_ERR_INVALID_ARG, f"{where}: counts")
-    return _addr(dev, t, torch.int16, 0, f"{where}: counts"), t.shape[1]
+    n, width = t.shape
+    if n != batch or width < vocab or width % 2:
+        raise KVQError(KVQ_ERR_INVALID_ARG, f"{where}: counts")
+    return _addr(dev, t, torch.int16, 0, f"{where}: counts"), width
 
 
 _LOGIT_TYPES = {torch.float32: KVQ_LOGITS_F32, torch.bfloat16: KVQ_LOGITS_BF16, torch.float16: KVQ_LOGITS_F16}
@@ -702,23 +713,25 @@ def kv_logits_probs(cfg: KVConfig, rules: LogitRules | None, logits, cu_rows, pa
     """logits [n, vocab] (float32, bfloat16 or float16; rows contiguous) -> p [n, vocab] float32 (for float32 logits it may be
     the same tensor): rows cu_rows[b] .. cu_rows[b+1]-1 are sequence b's.  parent, token [n] int32: a tree of drafts, or None."""
     dev, i32, w = _current_device(), torch.int32, "kv_logits_probs"
-    if logits.dim() != 2 or logits.dtype not in _LOGIT_TYPES:
-        raise KVQError(KVQ_ERR_INVALID_ARG, f"{w}: logits")
+    kind = _LOGIT_TYPES.get(logits.dtype)
+    if kind is None or logits.dim() != 2 or p is None or p.dtype is not torch.float32 or p.shape != logits.shape:
+        raise KVQError(KVQ_ERR_INVALID_ARG, f"{w}: p" if kind is not None and logits.dim() == 2 else f"{w}: logits")
     n, vocab = logits.shape
-    if (vocab > 1 and logits.stride(1) != 1) or (n > 1 and logits.stride(0) < vocab):
-        raise KVQError(KVQ_ERR_INVALID_ARG, f"{w}: logits")
-    if logits.get_device() != dev:
-        raise KVQError(KVQ_ERR_INVALID_ARG, f"{w}: logits (another device)")
-    if p is None:
-        raise KVQError(KVQ_ERR_INVALID_ARG, f"{w}: p")
-    pa, ps = _prob_rows(dev, p, n, vocab, f"{w}: p")
-    cu = _addr(dev, cu_rows, i32, cfg.batch + 1, f"{w}: cu_rows")
-    par = 0 if parent is None else _addr(dev, parent, i32, n, f"{w}: parent")
-    tok = 0 if token is None else _addr(dev, token, i32, n, f"{w}: token")
-    rc = lib().kv_logits_probs(ctypes.byref(cfg.c()), None if rules is None else ctypes.byref(rules.c(dev, cfg.batch, n, vocab)),
-                               logits.data_ptr(), _LOGIT_TYPES[logits.dtype], logits.stride(0) if n > 1 else vocab, vocab, cu, par, tok, n,
-                               pa, ps if n > 1 else vocab, _status(dev, status, w), _stream_of(dev, stream))
-    _check(rc, w)
+    rows = []
+    for t, name in ((logits, "logits"), (p, "p")):
+        row, token_step = t.stride()
+        if (vocab > 1 and token_step != 1) or (n > 1 and row < vocab):
+            raise KVQError(KVQ_ERR_INVALID_ARG, f"{w}: {name}")
+        if t.get_device() != dev:
+            raise KVQError(KVQ_ERR_INVALID_ARG, f"{w}: {name} (another device)")
+        rows += t.data_ptr(), row if n > 1 else vocab
+    cu = _addr(dev, cu_rows, i32, cfg.batch + 1, "kv_logits_probs: cu_rows")
+    par = 0 if parent is None else _addr(dev, parent, i32, n, "kv_logits_probs: parent")
+    tok = 0 if token is None else _addr(dev, token, i32, n, "kv_logits_probs: token")
+    rc = lib().kv_logits_probs(cfg.c(), None if rules is None else rules.c(dev, cfg.batch, n, vocab), rows[0], kind, rows[1], vocab, cu, par,
+                               tok, n, rows[2], rows[3], _status(dev, status, w), _stream_of(dev, stream))
+    if rc:
+        _check(rc, w)
 
 
 def kv_token_counts(cfg: KVConfig, counts, vocab: int, kind: int, cu_rows, token, path, n_accept, next_token, status,
@@ -734,9 +747,10 @@ def kv_token_counts(cfg: KVConfig, counts, vocab: int, kind: int, cu_rows, token
     kept = 0 if path is None else _addr(dev, path, i32, n, f"{w}: path")
     acc = 0 if n_accept is None else _addr(dev, n_accept, i32, cfg.batch, f"{w}: n_accept")
     nxt = 0 if next_token is None else _addr(dev, next_token, i32, cfg.batch, f"{w}: next_token")
-    rc = lib().kv_token_counts(ctypes.byref(cfg.c()), at, stride, int(vocab), int(kind), cu, tok, n, kept, acc, nxt,
-                               _status(dev, status, w), _stream_of(dev, stream))
-    _check(rc, w)
+    rc = lib().kv_token_counts(cfg.c(), at, stride, int(vocab), int(kind), cu, tok, n, kept, acc, nxt, _status(dev, status, w),
+                               _stream_of(dev, stream))
+    if rc:
+        _check(rc, w)
 
 
 def kvq_selftest_scale_division(mismatches, stream=None) -> None:

@@ -244,6 +244,7 @@ KVQ_API int kv_token_counts(const kvq_config* cfg, uint16_t* counts, int64_t cou
   if (!path != !n_accept || !aligned(path, 4) || !aligned(n_accept, 4) || !aligned(next_token, 4))
     return KVQ_ERR_INVALID_ARG;
   if (n_rows > 0 && (!cu_rows || !token || !aligned(cu_rows, 4) || !aligned(token, 4))) return KVQ_ERR_INVALID_ARG;
+  if (n_rows > 1 << 30) return KVQ_ERR_UNSUPPORTED;
   return kvq_launch_token_counts(cfg, counts, count_stride, vocab, kind, cu_rows, token, n_rows, path, n_accept, next_token,
                                  d_status, (cudaStream_t)stream);
 }

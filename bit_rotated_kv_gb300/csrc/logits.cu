@@ -454,70 +454,116 @@ struct CountParams {
   int32_t* status;
 };
 
-// The sequence of row r: the last one that begins at or before it (cu_rows must cover it).
-__device__ __forceinline__ int row_seq(const int32_t* cu_rows, int batch, int r) {
-  int lo = 0, hi = batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(cu_rows + mid) <= r) lo = mid;
-    else hi = mid - 1;
-  }
-  return (__ldg(cu_rows + lo) <= r && r < __ldg(cu_rows + lo + 1)) ? lo : -1;
-}
-
-// One token more for a sequence.  16-bit halves of a 32-bit word: what the other half holds is left alone.
-__device__ __forceinline__ void count_token(const CountParams& P, int b, int t) {
+// One 16-bit half of a 32-bit word of counts: what the other half holds is left alone.
+struct Half {
+  uint32_t* word;
+  int shift;
+};
+__device__ __forceinline__ Half half_of(const CountParams& P, int b, int t) {
   const long long at = (long long)b * P.stride + t;
-  uint32_t* word = reinterpret_cast<uint32_t*>(P.counts) + (at >> 1);
-  const int shift = (int)(at & 1) * 16;
-  if (P.kind == KVQ_COUNT_PROMPT) {
-    const uint32_t bit = 0x8000u << shift;
-    if (!(*reinterpret_cast<volatile uint32_t*>(word) & bit)) atomicOr(word, bit);
+  return {reinterpret_cast<uint32_t*>(P.counts) + (at >> 1), (int)(at & 1) * 16};
+}
+// `more` tokens more, up to the most; old: what the word held a moment ago; all: as many as the call may add to it after that.
+// (Far from the most an addition will do: of the warps that meet at an answer's most frequent token only one would have
+// its exchange accepted at a time.)
+__device__ __forceinline__ void add_tokens(const Half& h, uint32_t old, uint32_t more, uint32_t all) {
+  if (((old >> h.shift) & KVQ_COUNT_MOST) + all <= KVQ_COUNT_MOST) {
+    atomicAdd(h.word, more << h.shift);
     return;
   }
-  uint32_t old = *reinterpret_cast<volatile uint32_t*>(word);
-  while (((old >> shift) & KVQ_COUNT_MOST) != KVQ_COUNT_MOST) {
-    const uint32_t seen = atomicCAS(word, old, old + (1u << shift));   // (a count below its most does not carry)
-    if (seen == old) break;
+  for (;;) {
+    const uint32_t have = (old >> h.shift) & KVQ_COUNT_MOST, room = KVQ_COUNT_MOST - have;
+    if (room == 0u) return;
+    const uint32_t seen = atomicCAS(h.word, old, old + (min(more, room) << h.shift));   // (no carry: a count stays below its most)
+    if (seen == old) return;
     old = seen;
   }
 }
 
+constexpr int kPerLane = 4;          // rows of a lane: a warp takes 128 in a row, and their loads are on their way together
+
+// Latency bounds a step's few tokens (a chain of four loads and an atomic); a prompt's many, the random words that they
+// mark: 16 prompts of up to 128 K tokens, most of which hold what others have marked before, take @@ us, 60 with a row
+// to a thread.  Equal tokens of a warp are counted with one atomic (an answer's most frequent ones meet there).
 __global__ void __launch_bounds__(256) count_kernel(const __grid_constant__ CountParams P) {
   pdl_trigger();
   pdl_wait();
-  const long long total = (long long)P.n_rows + (P.next_token ? P.batch : 0);
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    int b, t;
-    if (i < P.n_rows) {
-      const int r = (int)i;
-      b = row_seq(P.cu_rows, P.batch, r);
-      if (b < 0) {
-        set_status(P.status, KVQ_ERR_BOUNDS);
+  const int lane = threadIdx.x & 31;
+  const int warp = (int)(blockIdx.x * 8 + (threadIdx.x >> 5)), warps = (P.n_rows + 32 * kPerLane - 1) / (32 * kPerLane);
+  int b[kPerLane], t[kPerLane];
+  uint32_t all[kPerLane];                                // tokens that the call may count for the sequence
+  bool odd = false;
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k) {
+    b[k] = -1;
+    all[k] = ~0u >> 1;
+  }
+  if (warp < warps) {
+    const int r0 = warp * 32 * kPerLane;
+    int from[kPerLane];
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+      const int r = r0 + 32 * k + lane;
+      from[k] = r < P.n_rows ? __ldg((P.path ? P.path : P.token) + r) : -1;
+    }
+    const int before = sequences_before(P.cu_rows, P.batch, r0, lane);
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+      const int r = r0 + 32 * k + lane;
+      if (r >= P.n_rows) continue;
+      int s = before;
+      while (s < P.batch && __ldg(P.cu_rows + s + 1) <= r) ++s;
+      const int first = s < P.batch ? __ldg(P.cu_rows + s) : -1;
+      if (first < 0 || first > r) {
+        odd = true;
         continue;
       }
-      int from = r;
+      t[k] = from[k];
+      const int n = __ldg(P.cu_rows + s + 1) - first;    // (more than 0: r is among them)
+      all[k] = min((uint32_t)n, 1u << 30) + 1u;
       if (P.path) {
-        const int first = __ldg(P.cu_rows + b), n = __ldg(P.cu_rows + b + 1) - first, j = r - first;
-        if (j == 0 || j >= __ldg(P.n_accept + b)) continue;
-        const int node = __ldg(P.path + r);
-        if (node < 0 || node >= n || first < 0 || first > P.n_rows - n) {
-          set_status(P.status, KVQ_ERR_BOUNDS);
+        const int j = r - first;
+        if (j == 0 || j >= __ldg(P.n_accept + s)) continue;
+        if (from[k] < 0 || from[k] >= n || first > P.n_rows - n) {
+          odd = true;
           continue;
         }
-        from = first + node;
+        t[k] = __ldg(P.token + first + from[k]);
       }
-      t = __ldg(P.token + from);
+      b[k] = s;
+    }
+  } else {
+    // the tokens behind the paths: a sequence to a lane (and nothing for the warps that fill the last block up)
+    const int s = (warp - warps) * 32 + lane;
+    if (P.next_token && s < P.batch) {
+      t[0] = __ldg(P.next_token + s);
+      b[0] = t[0] == -1 ? -1 : s;
+    }
+  }
+  Half h[kPerLane];
+  uint32_t old[kPerLane];
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k) {
+    if (b[k] >= 0 && (t[k] < 0 || t[k] >= P.vocab)) {
+      odd = true;
+      b[k] = -1;
+    }
+    if (b[k] >= 0) {
+      h[k] = half_of(P, b[k], t[k]);
+      old[k] = *reinterpret_cast<volatile uint32_t*>(h[k].word);
+    }
+  }
+  if (odd) set_status(P.status, KVQ_ERR_BOUNDS);
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k) {
+    if (P.kind == KVQ_COUNT_PROMPT) {
+      const uint32_t bit = 0x8000u << (b[k] >= 0 ? h[k].shift : 0);
+      if (b[k] >= 0 && !(old[k] & bit)) atomicOr(h[k].word, bit);
     } else {
-      b = (int)(i - P.n_rows);
-      t = __ldg(P.next_token + b);
-      if (t == -1) continue;
+      const unsigned long long key = b[k] >= 0 ? (unsigned long long)(b[k] + 1) << 32 | (uint32_t)t[k] : (unsigned long long)lane;
+      const unsigned same = __match_any_sync(0xffffffffu, key);
+      if (b[k] >= 0 && lane == __ffs(same) - 1) add_tokens(h[k], old[k], __popc(same), all[k]);
     }
-    if (t < 0 || t >= P.vocab) {
-      set_status(P.status, KVQ_ERR_BOUNDS);
-      continue;
-    }
-    count_token(P, b, t);
   }
 }
 
@@ -587,8 +633,7 @@ extern "C" int kvq_launch_token_counts(const kvq_config* cfg, uint16_t* counts, 
                                        const int32_t* path, const int32_t* n_accept, const int32_t* next_token,
                                        int32_t* d_status, cudaStream_t stream) {
   const CountParams P{counts, count_stride, vocab, kind, cu_rows, token, path, n_accept, next_token, cfg->batch, n_rows, d_status};
-  const long long total = (long long)n_rows + (next_token ? cfg->batch : 0);
-  if (total == 0) return KVQ_OK;
-  const int blocks = (int)std::min((total + 255) / 256, 8LL * kSms);
-  return launch_pdl(count_kernel, dim3(blocks), dim3(256), 0, stream, P) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  const long long warps = ((long long)n_rows + 32 * kPerLane - 1) / (32 * kPerLane) + (next_token ? (cfg->batch + 31) / 32 : 0);
+  if (warps == 0) return KVQ_OK;
+  return launch_pdl(count_kernel, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, P) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }

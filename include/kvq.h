@@ -565,7 +565,7 @@ KVQ_API int kv_logits_probs(const kvq_config* cfg, const kvq_logit_rules* rules,
  *                     kv_verify_tree, those of the kept nodes path[cu_rows[b] + j], 0 < j < n_accept[b] (node 0
  *                     was counted when it was drawn), and with next_token [B] the token behind them (-1: none).
  * Equal tokens may come any number of times.  Tokens outside the vocabulary, nodes outside the tree and rows of no
- * sequence are left out, with KVQ_ERR_BOUNDS.  Of cfg only batch is used. */
+ * sequence are left out, with KVQ_ERR_BOUNDS.  Of cfg only batch is used; n_rows is at most 2^30 (KVQ_ERR_UNSUPPORTED). */
 KVQ_API int kv_token_counts(const kvq_config* cfg, uint16_t* counts, int64_t count_stride, int32_t vocab, int32_t kind,
                     const int32_t* cu_rows, const int32_t* token, int32_t n_rows, const int32_t* path,
                     const int32_t* n_accept, const int32_t* next_token, int32_t* d_status, void* stream);
