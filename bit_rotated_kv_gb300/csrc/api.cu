@@ -173,7 +173,7 @@ KVQ_API int kv_rope_qk(const kvq_config* cfg, const kvq_transform* tr, const kvq
     if (rope->rot_dim > 0 && (!rope->freq || !aligned(rope->freq, 8) || !std::isfinite(rope->scale)))
       return KVQ_ERR_INVALID_ARG;
     if (!aligned(rope->q_norm, 16) || !aligned(rope->k_norm, 16)) return KVQ_ERR_INVALID_ARG;
-    if ((rope->q_norm || rope->k_norm) && !(std::isfinite(rope->norm_eps) && rope->norm_eps >= 0.0f))
+    if ((rope->q_norm || rope->k_norm) && !(std::isfinite(rope->norm_eps) && rope->norm_eps >= 1e-30f))
       return KVQ_ERR_INVALID_ARG;
   }
   const bool turned = rope && rope->rot_dim > 0;

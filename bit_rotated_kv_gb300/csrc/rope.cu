@@ -6,7 +6,7 @@
 // in float32 with one rounding to bf16 at the end.  A phase f is position * freq mod 2^64 (units of 2^-64 turns):
 // whole numbers lose nothing at far positions, where a float32 angle of 10^5 radians is off by 2^-8.
 //
-// This file: the kernel for the rows of few tokens, on the CUDA cores.  A CTA takes a slice of 32 outputs of one
+// This file: the kernel for few rows, on the CUDA cores (rope_tc.cu: the others).  A CTA takes a slice of 32 outputs of one
 // matrix and a chunk of the (row, head) pairs that share it: a whole matrix to a CTA would leave most SMs without
 // one at a single token (8 kv heads, 3 matrices each), and its 64 KB would be the longest wait of the call.  The
 // four slices of a pair each place its row (norm and rotation), which costs less than passing it on would.
@@ -25,12 +25,10 @@ constexpr int kMaxRows = 16;                      // pairs of a chunk
 constexpr int kMaxCopies = 8;                     // rows a warp copies
 
 // One warp places a row: norm and rotation, float32, into shared memory.  False when the row is not finite.
-__device__ __forceinline__ bool place_row(const RopeParams& P, int tt, int row, int head, float* y, int lane) {
-  const uint2 raw = *reinterpret_cast<const uint2*>(rope_src(P, tt, row, head) + 4 * lane);
+__device__ __forceinline__ bool place_row(const RopeParams& P, const float* w, bool turned, uint2 raw, int pos, float* y, int lane) {
   float x[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u), __uint_as_float(raw.y << 16),
                 __uint_as_float(raw.y & 0xffff0000u)};
   bool fine = !bf16_pair_odd(raw.x) && !bf16_pair_odd(raw.y);
-  const float* w = P.norm[tt];
   if (w) {
     float ss = fmaf(x[3], x[3], fmaf(x[2], x[2], fmaf(x[1], x[1], x[0] * x[0])));
 #pragma unroll
@@ -45,9 +43,8 @@ __device__ __forceinline__ bool place_row(const RopeParams& P, int tt, int row, 
   }
   *reinterpret_cast<float4*>(y + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
   fine = __all_sync(0xffffffffu, fine);
-  if (P.rpos[tt]) {
+  if (turned) {
     __syncwarp();
-    const int pos = __ldg(P.rpos[tt] + row);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int i = lane + 32 * h;
@@ -122,15 +119,36 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
   pdl_wait();
   for (int c = c0; c < c1; ++c) {
     const int p0 = c * P.r.rt, np = min(P.r.rt, pairs - p0);
-    for (int j = warp; j < np; j += kRopeWarps) {
+    // a warp's rows (warp, warp + 4, ..) are all asked for before the first is placed, and lane k finds out where the
+    // k-th goes: one after another, each row's four dependent loads would be waited for in turn
+    constexpr int kMine = kMaxRows / kRopeWarps;
+    const int32_t* rpos = P.rpos[tt];
+    uint2 raw[kMine];
+    int pos[kMine];
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int j = warp + kRopeWarps * k;
       int row, head;
-      tile_row(T, mh, p0 + j, row, head);
-      const bool fine = place_row(P, tt, row, head, ys[j], lane);
-      if (lane == 0) {
-        const int b = T.is_query ? 0 : __ldg(P.r.seq_idx + row), p = T.is_query ? 0 : __ldg(P.r.pos + row);
-        dst_sh[j] = rot_dst(P.r, T, row, head, b, p, slice == 0);
-        if (!fine && slice == 0 && dst_sh[j]) set_status(P.r.status, KVQ_ERR_NONFINITE);
+      tile_row(T, mh, p0 + min(j, np - 1), row, head);
+      raw[k] = __ldg(reinterpret_cast<const uint2*>(rope_src(P, tt, row, head)) + lane);
+      pos[k] = rpos ? __ldg(rpos + row) : 0;
+    }
+    bool fine = true;                                    // of the lane's own row
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int j = warp + kRopeWarps * k;
+      if (j < np) {
+        const bool f = place_row(P, P.norm[tt], rpos != nullptr, raw[k], pos[k], ys[j], lane);
+        if (lane == k) fine = f;
       }
+    }
+    const int own = warp + kRopeWarps * lane;
+    if (lane < kMine && own < np) {
+      int row, head;
+      tile_row(T, mh, p0 + own, row, head);
+      const int b = T.is_query ? 0 : __ldg(P.r.seq_idx + row), p = T.is_query ? 0 : __ldg(P.r.pos + row);
+      dst_sh[own] = rot_dst(P.r, T, row, head, b, p, slice == 0);
+      if (!fine && slice == 0 && dst_sh[own]) set_status(P.r.status, KVQ_ERR_NONFINITE);
     }
     __syncthreads();
     for (int j0 = 0; j0 < np; j0 += 4) {
@@ -217,7 +235,7 @@ extern "C" int kvq_launch_rope(const kvq_config* cfg, const kvq_transform* tr, c
   R.rpw = (int)(copies > cslots ? std::min((copies + cslots - 1) / cslots, (long long)kMaxCopies) : 1);
   R.warp_total = (int)((copies + R.rpw - 1) / R.rpw);
   if (pairs >= kRopeTcPairs) {
-    // prefill sizes: the copies on their own, then the products on the tensor cores
+    // the copies on their own, then the products on the tensor cores
     if (R.warp_total > 0 &&
         launch_pdl(rope_rows_kernel, dim3((unsigned)((R.warp_total + kRopeWarps - 1) / kRopeWarps)), dim3(kRopeThreads), 0, stream, P) !=
             cudaSuccess)

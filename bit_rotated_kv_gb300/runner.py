@@ -1,7 +1,8 @@
 """Drive the C-ABI calls for a batch of sequences: chunked prefill of the cache, one serving
 step (append n_new tokens, flush, decode -- or the fused append, then decode), one speculative step
-(a tree of drafts appended and attended to, checked, the kept path's rows left in the cache), and
-the page pool behind them (reserve, fork, free, compact).  Argument marshalling only --
+(a tree of drafts appended and attended to, checked, the kept path's rows left in the cache), the two
+ends of a step (from the projections' rows, and from logits to tokens), and the page pool behind
+them (reserve, fork, free, compact).  Argument marshalling only --
 torch is used for device buffers, gathers of input rows and streams; every step of the
 method runs in the library's kernels."""
 
@@ -12,10 +13,10 @@ import math
 import numpy as np
 import torch
 
-from . import (KVQ_TREE_MAX_NODES, KVCache, KVConfig, Transform, kv_append_chunk, kv_attn_chunk, kv_attn_chunk_workspace_bytes,
-               kv_attn_decode, kv_attn_tree, kv_attn_tree_workspace_bytes, kv_pages_compact,
-               kv_pages_compact_workspace_bytes, kv_pages_reserve, kv_quant_flush, kv_rotate_qk, kv_seq_fork, kv_seq_free,
-               kv_tree_commit, kv_verify_tree, workspace)
+from . import (KVQ_COUNT_OUTPUT, KVQ_COUNT_PROMPT, KVQ_TREE_MAX_NODES, KVCache, KVConfig, Transform, kv_append_chunk, kv_attn_chunk, kv_attn_chunk_workspace_bytes,
+               kv_attn_decode, kv_attn_tree, kv_attn_tree_workspace_bytes, kv_logits_probs, kv_pages_compact,
+               kv_pages_compact_workspace_bytes, kv_pages_reserve, kv_quant_flush, kv_rope_qk, kv_rotate_qk, kv_seq_fork, kv_seq_free,
+               kv_token_counts, kv_tree_commit, kv_verify_tree, workspace)
 
 
 def _rows_for(k_all: torch.Tensor, lengths_lo, lengths_hi):
@@ -130,6 +131,50 @@ class DecodeRunner:
         self.flush(n_new + self.cfg.s_flush, stream)
         self.decode(self.q_out, self.out, stream)
 
+    # ---- from the projections' rows ----------------------------------------------------------------
+    def rope_append(self, rope, k_rows, v_rows, seq_idx, pos, q=None, q_out=None, q_pos=None, rope_pos=None, stream=None) -> None:
+        """append for rows as the projections leave them (views of one fused tensor do): norm of the heads, rotation by
+        position, transform, write.  q_pos, rope_pos: positions in the text (rope_pos None: pos)."""
+        kv_rope_qk(self.cfg, self.tr, rope, q, q_out, q_pos, k_rows, v_rows, seq_idx, pos, rope_pos, self.cache, self.status,
+                   self.stream if stream is None else stream)
+
+    def rope_step(self, rope, q, k_rows, v_rows, seq_idx, pos, q_pos, n_new: int, stream=None) -> None:
+        """step for such rows: q_pos [batch] is each sequence's newest position."""
+        self.rope_append(rope, k_rows, v_rows, seq_idx, pos, q, self.q_out, q_pos, None, stream)
+        self.flush(n_new + self.cfg.s_flush, stream)
+        self.decode(self.q_out, self.out, stream)
+
+    # ---- from logits to tokens -----------------------------------------------------------------------
+    def next_tokens(self, rules, logits, p, u, next_token, stream=None) -> None:
+        """A token for every sequence (next_token [batch]) from its row of logits [batch, vocab] under `rules` and a uniform
+        number u [batch]; p [batch, vocab] holds the probabilities, and rules.counts, where given, counts the tokens."""
+        stream = self.stream if stream is None else stream
+        if not hasattr(self, "_ones"):                  # trees of one node: a sequence to a row
+            i32 = dict(dtype=torch.int32, device=self.device)
+            self._ones = (torch.arange(self.cfg.batch + 1, **i32), torch.full((self.cfg.batch,), -1, **i32),
+                          torch.zeros(self.cfg.batch, **i32), torch.zeros(self.cfg.batch, **i32))
+        cu, root, path, n_accept = self._ones
+        kv_logits_probs(self.cfg, rules, logits, cu, None, None, p, self.status, stream)
+        kv_verify_tree(self.cfg, cu, root, path, p, None, u, path, n_accept, next_token, self.status, stream)
+        if rules is not None and rules.counts is not None:
+            kv_token_counts(self.cfg, rules.counts, logits.shape[1], KVQ_COUNT_OUTPUT, None, None, None, None, next_token, self.status, stream)
+
+    def accept_logits(self, rules, cu_rows, parent, token, logits, p, q, u, path, n_accept, next_token, max_nodes: int,
+                      stream=None) -> None:
+        """accept from the target's logits [n, vocab] under `rules`, every node's by the penalties of its own path; p [n, vocab]
+        holds the probabilities (for float32 logits it may be the logits), and rules.counts, where given, counts the tokens kept."""
+        stream = self.stream if stream is None else stream
+        kv_logits_probs(self.cfg, rules, logits, cu_rows, parent, token, p, self.status, stream)
+        self.accept(cu_rows, parent, token, p, q, u, path, n_accept, next_token, max_nodes, stream)
+        if rules is not None and rules.counts is not None:
+            kv_token_counts(self.cfg, rules.counts, logits.shape[1], KVQ_COUNT_OUTPUT, cu_rows, token, path, n_accept, next_token,
+                            self.status, stream)
+
+    def count_prompts(self, counts, vocab: int, cu_rows, token, stream=None) -> None:
+        """Rows cu_rows[b] .. cu_rows[b+1]-1 of token are sequence b's prompt (its row of counts zeroed by the caller)."""
+        kv_token_counts(self.cfg, counts, vocab, KVQ_COUNT_PROMPT, cu_rows, token, None, None, None, self.status,
+                        self.stream if stream is None else stream)
+
     # ---- speculative decoding: tree_step, then accept --------------------------------------------
     def tree_workspace(self, n_rows: int) -> torch.Tensor:
         """A zeroed workspace for trees of up to n_rows nodes in all."""
@@ -137,10 +182,15 @@ class DecodeRunner:
         n = kv_attn_tree_workspace_bytes(self.cfg, n_rows, self.max_ctx)
         return torch.zeros(max(n, 256), dtype=torch.uint8, device=self.device)
 
-    def tree_step(self, q, k_rows, v_rows, seq_idx, pos, cu_rows, parent, q_out, out, ws, stream=None) -> None:
+    def tree_step(self, q, k_rows, v_rows, seq_idx, pos, cu_rows, parent, q_out, out, ws, stream=None, rope=None,
+                  rope_pos=None) -> None:
         """Append the drafted nodes (row cu_rows[b] + i is node i of sequence b, at position length + i)
-        and attend from each to the tokens before the drafts, its ancestors and itself: out [n, Hq, d] bf16."""
-        self.append(k_rows, v_rows, seq_idx, pos, q, q_out, stream)
+        and attend from each to the tokens before the drafts, its ancestors and itself: out [n, Hq, d] bf16.
+        With rope the rows are the projections': rope_pos [n] is each node's position in the text, length + depth."""
+        if rope is None:
+            self.append(k_rows, v_rows, seq_idx, pos, q, q_out, stream)
+        else:
+            self.rope_append(rope, k_rows, v_rows, seq_idx, pos, q, q_out, rope_pos, rope_pos, stream)
         kv_attn_tree(self.cfg, self.cache, q_out, cu_rows, parent, out, self.sm_scale, self.max_ctx, ws, self.status,
                      self.stream if stream is None else stream)
 

@@ -454,7 +454,7 @@ typedef struct kvq_rope {
   int32_t         layout;    /* KVQ_ROPE_*                                                        */
   int32_t         rot_dim;   /* rotated channels, a head's first: even, 0 .. d; the others pass   */
   float           scale;     /* multiplies the rotated channels (1, or a scaling's factor)        */
-  float           norm_eps;  /* of the norms below                                                */
+  float           norm_eps;  /* of the norms below (1e-30 or more)                                */
   const uint64_t* freq;      /* [rot_dim/2] device: turns per token in units of 2^-64             */
   const float*    q_norm;    /* [d] device: weights of the RMS norm of every query head before    */
   const float*    k_norm;    /*     the rotation; of every key head (NULL: no norm)               */
@@ -497,8 +497,8 @@ KVQ_API int kvq_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling,
  * values are exact.  A head whose row holds an infinity or NaN, or (with a norm) whose squares sum to more than
  * float32 holds, gets a row that is not finite, and KVQ_ERR_NONFINITE (copied values aside).
  * rope NULL: no norm and no rotation (q_pos may then be NULL).
- * Execution: the rows of few tokens run on the CUDA cores, a slice of a matrix to a CTA; prefill-sized calls on
- * the tensor cores, both operands as pairs of fp16 under powers of two.  The two round differently.
+ * Execution: up to 2048 (row, head) pairs that have a matrix run on the CUDA cores, a slice of a matrix to a CTA; larger calls
+ * on the tensor cores, both operands as pairs of fp16 under powers of two.  The two round differently.
  * Source: [WUSH] inference algorithm and [OScaR] algorithm, key and query processing (the transform follows RoPE);
  * norm and rotation are the models' own (Qwen3's heads). */
 KVQ_API int kv_rope_qk(const kvq_config* cfg, const kvq_transform* tr, const kvq_rope* rope, const uint16_t* q,
