@@ -483,8 +483,8 @@ __device__ __forceinline__ void add_tokens(const Half& h, uint32_t old, uint32_t
 constexpr int kPerLane = 4;          // rows of a lane: a warp takes 128 in a row, and their loads are on their way together
 
 // Latency bounds a step's few tokens (a chain of four loads and an atomic); a prompt's many, the random words that they
-// mark: 16 prompts of up to 128 K tokens, most of which hold what others have marked before, take @@ us, 60 with a row
-// to a thread.  Equal tokens of a warp are counted with one atomic (an answer's most frequent ones meet there).
+// mark: 8 K tokens of each of 16
+// sequences take 6 us with the clearing of their counts.  Equal tokens of a warp are counted with one atomic (an answer's most frequent ones meet there).
 __global__ void __launch_bounds__(256) count_kernel(const __grid_constant__ CountParams P) {
   pdl_trigger();
   pdl_wait();
@@ -567,6 +567,54 @@ __global__ void __launch_bounds__(256) count_kernel(const __grid_constant__ Coun
   }
 }
 
+// Long prompts: a CTA takes a sequence and a slice of the vocabulary, looks at all of the prompt's tokens, gathers those of
+// its slice as bits in shared memory, and marks them in one sweep over the slice's counts, which are nobody else's in this call.
+constexpr int kSweepThreads = 1024;
+constexpr int kSweepRows = 1 << 19;  // (fewer rows are marked one by one)
+constexpr int kSweepSlice = 16384;   // tokens of a slice (2 KB of bits)
+__global__ void __launch_bounds__(kSweepThreads) prompt_kernel(const __grid_constant__ CountParams P) {
+  __shared__ uint32_t bits[kSweepSlice / 32];
+  pdl_trigger();
+  const int tid = threadIdx.x, b = blockIdx.y;
+  const int v0 = blockIdx.x * kSweepSlice, v1 = min(P.vocab, v0 + kSweepSlice);
+  for (int i = tid; i < kSweepSlice / 32; i += kSweepThreads) bits[i] = 0u;
+  pdl_wait();
+  const int first = P.cu_rows[b], last = P.cu_rows[b + 1];
+  // rows of no sequence: before the first, behind the last, or where cu_rows falls
+  bool odd = first < 0 || last < first || last > P.n_rows || (b == 0 && first > 0) || (b == P.batch - 1 && last < P.n_rows);
+  __syncthreads();
+  if (first >= 0 && last <= P.n_rows) {
+    auto mark = [&](int t) {
+      if (t >= v0 && t < v1) atomicOr(&bits[(t - v0) >> 5], 1u << (t & 31));
+      odd |= t < 0 || t >= P.vocab;
+    };
+    // four tokens at a time from a boundary on, the others one by one
+    const int32_t* from = P.token + first;
+    const int n = max(0, last - first), head = min(n, (int)(((16 - (reinterpret_cast<uintptr_t>(from) & 15)) & 15) >> 2));
+    const int fours = (n - head) >> 2;
+    const int4* wide = reinterpret_cast<const int4*>(from + head);
+    if (tid < head) mark(__ldg(from + tid));
+    if (tid < n - head - 4 * fours) mark(__ldg(from + head + 4 * fours + tid));
+#pragma unroll 4
+    for (int i = tid; i < fours; i += kSweepThreads) {
+      const int4 t = __ldg(wide + i);
+      mark(t.x);
+      mark(t.y);
+      mark(t.z);
+      mark(t.w);
+    }
+  }
+  if (odd && blockIdx.x == 0) set_status(P.status, KVQ_ERR_BOUNDS);
+  __syncthreads();
+  // two tokens to a word (rows begin on one: the stride is even)
+  uint32_t* row = reinterpret_cast<uint32_t*>(P.counts + (long long)b * P.stride + v0);
+#pragma unroll 4
+  for (int i = tid; i < (v1 - v0 + 1) >> 1; i += kSweepThreads) {
+    const uint32_t two = bits[i >> 4] >> (2 * (i & 15)) & 3u;
+    if (two) row[i] |= (two & 1u) << 15 | (two & 2u) << 30;
+  }
+}
+
 template <typename T, bool kCounts, bool kMask>
 int launch_logits(LogitParams& P, cudaStream_t stream) {
   const auto kernel = logits_kernel<T, kCounts, kMask>;
@@ -633,6 +681,12 @@ extern "C" int kvq_launch_token_counts(const kvq_config* cfg, uint16_t* counts, 
                                        const int32_t* path, const int32_t* n_accept, const int32_t* next_token,
                                        int32_t* d_status, cudaStream_t stream) {
   const CountParams P{counts, count_stride, vocab, kind, cu_rows, token, path, n_accept, next_token, cfg->batch, n_rows, d_status};
+  // many long prompts: 16 of 64 K to 128 K tokens over 152 K (1.6 M rows) take 24 us swept and 36 one by one, the clearing of their
+  // counts among it; 16 of 16 K tokens 9.4 and 8.5, one of 128 K 16 and 14
+  if (kind == KVQ_COUNT_PROMPT && cfg->batch <= 65535 && n_rows >= kSweepRows && n_rows / cfg->batch >= vocab / 4) {
+    const dim3 grid((unsigned)((vocab + kSweepSlice - 1) / kSweepSlice), (unsigned)cfg->batch);
+    return launch_pdl(prompt_kernel, grid, dim3(kSweepThreads), 0, stream, P) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  }
   const long long warps = ((long long)n_rows + 32 * kPerLane - 1) / (32 * kPerLane) + (next_token ? (cfg->batch + 31) / 32 : 0);
   if (warps == 0) return KVQ_OK;
   return launch_pdl(count_kernel, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, P) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;

@@ -304,6 +304,32 @@ def test_counts(vocab, n):
         assert int(status.item()) == 0 and np.array_equal(got.cpu().numpy().view(np.uint16), want)
 
 
+@pytest.mark.parametrize("vocab,n", [(1001, [200000, 0, 300001, 100003]), (70001, [524288 + 5]), (16384, [3, 400000, 200000])])
+def test_long_prompts(vocab, n):
+    """Enough rows for the sweep: slices' ends, tokens outside the vocabulary, rows of no sequence, counts that are there already."""
+    rng, batch = np.random.default_rng(6), len(n)
+    stride = vocab + vocab % 2
+    cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    token = np.minimum(vocab - 1, vocab * rng.random(int(cu[-1])) ** 3).astype(np.int32)
+    token[rng.integers(0, len(token), 100)] = vocab - 1
+    have = rng.integers(0, 9, (batch, stride)).astype(np.uint16)
+    for cut, outside in ((0, False), (7, False), (0, True)):
+        tok = token.copy()
+        if outside:
+            tok[rng.integers(0, len(tok), 50)] = rng.choice([-1, vocab, 1 << 30], 50)
+        at = cu.copy()
+        at[0], at[-1] = cut, cu[-1] - cut
+        got, status = torch.tensor(have.view(np.int16), device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        kvq.kv_token_counts(_cfg(batch), got, vocab, kvq.KVQ_COUNT_PROMPT, _dev(at), _dev(tok), None, None, None, status)
+        want = have.copy()
+        for b in range(batch):
+            t = tok[at[b]:at[b + 1]]
+            want[b, t[(t >= 0) & (t < vocab)]] |= 0x8000
+        torch.cuda.synchronize()
+        assert int(status.item()) == (kvq.KVQ_ERR_BOUNDS if cut or outside else 0)
+        assert np.array_equal(got.cpu().numpy().view(np.uint16), want)
+
+
 def test_counts_of_kept_paths():
     rng = np.random.default_rng(5)
     n, vocab = [1, 9, 0, 128], 77
