@@ -64,17 +64,35 @@ __device__ __forceinline__ bool place_row(const RopeParams& P, const float* w, b
   return fine;
 }
 
-// Rows of values that are copied: a warp takes up to rpw of them, 16 lanes of 16 bytes each, two at a time.
+// Rows of values that are copied: a warp takes up to kMaxCopies of them, 16 lanes of 16 bytes each.  Everything that is loaded
+// for them is asked for before the first is placed.
 __device__ __forceinline__ void copy_rows(const RopeParams& P, int item, int lane) {
   const RotTensor& T = P.r.t[2];
   const int total = T.rows * T.heads;
-  const int p0 = item * P.r.rpw, p1 = min(total, p0 + P.r.rpw);
-#pragma unroll 4
-  for (int p = p0 + (lane >> 4); p < p1; p += 2) {
-    const int row = p / T.heads, head = p % T.heads;
-    const uint4 x = *(reinterpret_cast<const uint4*>(rope_src(P, 2, row, head)) + (lane & 15));
-    uint16_t* dst = rot_dst(P.r, T, row, head, __ldg(P.r.seq_idx + row), __ldg(P.r.pos + row), (lane & 15) == 0);
-    if (dst) reinterpret_cast<uint4*>(dst)[lane & 15] = x;
+  constexpr int kEach = kMaxCopies / 2;
+  const int p0 = item * P.r.rpw + (lane >> 4), p1 = min(total, (item + 1) * P.r.rpw);
+  uint4 x[kEach];
+  int row[kEach], head[kEach], b[kEach], at[kEach], sq[kEach];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int p = min(p0 + 2 * k, total - 1);
+    row[k] = p / T.heads;
+    head[k] = p - row[k] * T.heads;
+    if (p0 + 2 * k < p1) {
+      x[k] = __ldg(reinterpret_cast<const uint4*>(rope_src(P, 2, row[k], head[k])) + (lane & 15));
+      b[k] = __ldg(P.r.seq_idx + row[k]);
+      at[k] = __ldg(P.r.pos + row[k]);
+    } else {
+      b[k] = -1;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) sq[k] = b[k] >= 0 && b[k] < P.r.batch ? __ldg(P.r.s_quant + b[k]) : -1;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    if (p0 + 2 * k >= p1) continue;
+    uint16_t* dst = rot_dst(P.r, T, row[k], head[k], b[k], at[k], (lane & 15) == 0, sq[k]);
+    if (dst) __stcg(reinterpret_cast<uint4*>(dst) + (lane & 15), x[k]);
   }
 }
 
@@ -180,6 +198,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
   }
 }
 
+// The copies beside products on the tensor cores.
+__global__ void __launch_bounds__(kRopeThreads, 10) rope_copy_kernel(const __grid_constant__ RopeParams P) {
+  pdl_trigger();
+  pdl_wait();
+  const int item = (int)blockIdx.x * kRopeWarps + (int)(threadIdx.x >> 5);
+  if (item < P.r.warp_total) copy_rows(P, item, threadIdx.x & 31);
+}
+
 }  // namespace
 }  // namespace kvq
 
@@ -237,7 +263,7 @@ extern "C" int kvq_launch_rope(const kvq_config* cfg, const kvq_transform* tr, c
   if (pairs >= kRopeTcPairs) {
     // the copies on their own, then the products on the tensor cores
     if (R.warp_total > 0 &&
-        launch_pdl(rope_rows_kernel, dim3((unsigned)((R.warp_total + kRopeWarps - 1) / kRopeWarps)), dim3(kRopeThreads), 0, stream, P) !=
+        launch_pdl(rope_copy_kernel, dim3((unsigned)((R.warp_total + kRopeWarps - 1) / kRopeWarps)), dim3(kRopeThreads), 0, stream, P) !=
             cudaSuccess)
       return KVQ_ERR_CUDA;
     return launch_rope_tc(P, stream);
