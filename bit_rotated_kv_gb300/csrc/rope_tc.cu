@@ -1,23 +1,30 @@
 // kv_rope_qk for prefill-sized calls: norm and rotation on the CUDA cores, the per-head products on the tensor
 // cores (tcgen05).
 //
-// Bytes bound it: a row is read once and written once (512 bytes a row and head; the 2048-token chunk of 16 sequences
-// with 32 + 8 heads moves 671 MB, 99 us at the measured copy rate), which leaves the CUDA cores about 1.6 K clocks and the
-// tensor cores as many for 64 rows of an SM.  Both products therefore take two fp16 parts of each operand rather than the integer digits
+// A row is read once and written once, 512 bytes a row and head: the 2048-token chunk of 16 sequences with 32 + 8 heads
+// moves 671 MB, 99 us at the measured copy rate, which leaves the CUDA cores about 1.6 K clocks and the tensor cores as
+// many for 64 rows of an SM.  Both products therefore take two fp16 parts of each operand rather than the integer digits
 // of rotate_tc.cu: T row i and x row r are brought under powers of two so that their largest entry lies below 2^15,
 // and split as hi + lo, 11 bits each.  hi hi + lo hi + hi lo, summed in float32 by the tensor cores, leaves out 2^-20
-// of sum |T_ij x_j| at most (bf16's half step is 2^-8 of the result); three MMAs of 16 inputs instead of nine.  Entries 2^-29 of their
-// row's largest lose bits of lo, 2^-40 of that largest.  A Walsh-Hadamard matrix is +-1, its 1/sqrt(128) left to the end: two MMAs.
+// of sum |T_ij x_j| at most (bf16's half step is 2^-8 of the result); three MMAs of 16 inputs instead of nine.  Entries
+// 2^-29 of their row's largest lose bits of lo, 2^-40 of that largest.  A Walsh-Hadamard matrix is +-1, its 1/sqrt(128)
+// left to the end: two MMAs.
 //
 // The norm's factor belongs to a row, so it too is left to the end, and the weights take the power of two: norm and
 // scaling cost one product a channel.  Sine and cosine are the SFU's (2^-20.9 of the pair's length), from phases in
 // whole numbers.  Lanes hold both channels of a pair: eight lanes to a row, two vectors of eight channels each.
 //
-// Layout: two CTAs on an SM.  A CTA takes a run of chunks of 64 (row, head) pairs; T hi and lo of its matrix stay in TMEM (the A
-// operand, lane = output, 64 columns each), rows come by asynchronous copies two chunks ahead and go through swizzled shared memory (B,
-// two buffers of hi and lo), accumulators take two sets of 64 TMEM columns.  Eight warps place rows, one issues the MMAs, four write results out through
-// the shared memory that the rows came from, a row's 256 bytes at a time, two ask
-// for rows, one finds out where they go.
+// Layout: two CTAs on an SM.  A CTA takes a run of chunks of 64 (row, head) pairs.  T hi and lo of its matrix stay in
+// TMEM (the A operand, lane = output, 64 columns each); rows come by asynchronous copies two chunks ahead and go through
+// swizzled shared memory (B, two buffers of hi and lo); accumulators take two sets of 64 TMEM columns.  Eight warps
+// place rows, one issues the MMAs, four write results out through the shared memory that the rows came from, a row's 256
+// bytes at a time, two ask for rows, one finds out where they go.
+//
+// That chunk of 16 x 2048 tokens takes 215 us with its values' copies, 190 without (3.5 TB/s).  What bounds it are the
+// operations of placing rows: the schedulers issue in 58% of the clocks, and a CTA's chunk of 64 rows takes 5 K
+// clocks, 3.5 K of them from its rows to the buffer; DRAM is busy 36%, the tensor cores 28%.  What was tried: rows kept in registers a chunk
+// ahead with three buffers 267 us; bulk copies of rows by one warp 289; 96 registers for those who place and 40, 24 for
+// the others 276.
 #include "rope.cuh"
 #include "tc.cuh"
 
@@ -43,7 +50,8 @@ constexpr int kRtFac = kRtMeta + kMetaSets * kRtRows * 8;
 constexpr int kRtPos = kRtFac + 2 * kRtRows * 4;
 constexpr int kRtNorm = kRtPos + 2 * kRtRows * 4;
 constexpr int kRtFreq = kRtNorm + kHeadDim * 4;
-constexpr int kRtExch = kRtFreq + 64 * 8;                // a T row's largest exponent, by halves
+// (behind the pairs' frequencies: a frequency of 0)
+constexpr int kRtExch = kRtFreq + 66 * 8;                // a T row's largest exponent, by halves
 constexpr int kRtRowFac = kRtExch + 2 * kHeadDim * 4;    // what takes an output's power of two back, where they differ
 constexpr int kRtUsed = kRtRowFac + kHeadDim * 4;
 constexpr int kRtSmem = kRtUsed + 1024;
@@ -64,15 +72,17 @@ __device__ __forceinline__ void rt_mma(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(kRtIdesc), "r"(acc)
       : "memory");
 }
-// The warps meet at named barriers, where the hardware holds them: warps that ask an mbarrier again and again took a third
-// of the SM's issue slots.  Only the end of the MMAs comes by mbarrier, and one warp asks (bounded).
-constexpr int kBarPlace = 1, kBarOut = 2, kBarX = 3, kBarFree = 5, kBarMma = 7, kBarRaw = 8;   // (X, Free, Raw: one for each buffer)
+// Warps of one kind meet at named barriers; one kind waits for another at mbarriers, every wait bounded.
+constexpr int kBarPlace = 1, kBarOut = 2, kBarMma = 3;
 __device__ __forceinline__ void rt_sync(int id, int warps) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(32 * warps) : "memory"); }
-__device__ __forceinline__ void rt_arrive(int id, int warps) { asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(32 * warps) : "memory"); }
-// those who place rows, the one who finds destinations and the one who issues the MMAs; those who empty a buffer and those who
-// fill it; those who read a raw buffer and the two who fill it
-
-constexpr int kXWarps = kRtWarps + 2, kFreeWarps = kRtOut + kRtWarps, kRawWarps = kRtWarps + 2;
+__device__ __forceinline__ void rt_init(uint64_t* bar, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(um_saddr(bar)), "r"(count) : "memory");
+}
+// What a warp has done, for those who wait for it.
+__device__ __forceinline__ void rt_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) um_arrive(bar);
+}
 __device__ __forceinline__ bool rt_wait(uint64_t* bar, uint32_t parity) {
   if (um_mbar_try(bar, parity)) return true;
   unsigned long long began, now;
@@ -81,6 +91,13 @@ __device__ __forceinline__ bool rt_wait(uint64_t* bar, uint32_t parity) {
     if (um_mbar_try(bar, parity)) return true;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
   } while (now - began < 1000000000ull);                 // a second
+  return false;
+}
+// Use n of a pair of barriers (a whole warp waits; after a time-out nobody waits any more: every role runs to its end).
+__device__ __forceinline__ bool rt_wait_use(uint64_t* bars, int n, volatile int* abort_sh) {
+  if (*abort_sh) return false;
+  if (__all_sync(0xffffffffu, rt_wait(bars + (n & 1), (uint32_t)((n >> 1) & 1)))) return true;
+  *abort_sh = 1;
   return false;
 }
 template <int R>
@@ -134,6 +151,33 @@ __device__ __forceinline__ Place place_of(const RopeParams& P, int chunk) {
   return w;
 }
 
+// The first chunk of a CTA.  Where CTAs have many chunks (sixteen on average), those whose rows share a token count kCostSame, others, which
+// come in shorter pieces and with a sine and cosine each, kCostOwn, and the grid's first half gets kShare / 32: of the two CTAs on an
+// SM the first comes to issue more often.  (16 x 2048 tokens, 40 heads: 239 us by chunks alone, 230 by 7 : 8 in
+// halves, 215 so.)  Where
+// they have few, a chunk more is what counts (3 x 777 tokens: 25.5 us by chunks, 28.4 so).
+constexpr int kCostSame = 7, kCostOwn = 8, kShare = 17;
+__device__ __forceinline__ int first_chunk(const RopeParams& P, int cta) {
+  if (P.r.dense_total < 16 * 2 * kSms) return (int)((long long)P.r.dense_total * cta / gridDim.x);
+  long long sum = 0;
+  int cost[3];
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    cost[t] = P.r.t[t].head_div > 1 ? kCostSame : kCostOwn;
+    sum += (long long)P.r.n_dense[t] * cost[t];
+  }
+  // (the grid is 2 kSms)
+  long long at = sum * (cta <= kSms ? kShare * cta : (32 - kShare) * cta + (2 * kShare - 32) * kSms) / (32 * kSms);
+  int c = 0;
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    const long long here = (long long)P.r.n_dense[t] * cost[t], x = min(at, here);
+    c += (int)(x / cost[t]);
+    at -= x;
+  }
+  return c;
+}
+
 // What a run of chunks of one matrix has in common (in shared memory: read once a chunk, it would cost the loops their
 // registers).
 struct Seg {
@@ -145,8 +189,8 @@ struct Seg {
   float t_back;              // takes the matrix's power of two back (and a Hadamard matrix's 1/sqrt(128) in)
 };
 
-// Asks for half of a chunk's rows and for their positions, two rows at a time (one warp).  Behind the last row: that row again.  (Bulk copies
-// of a token's heads, 1 KB, took one warp 200 clocks each.)
+// Asks for half of a chunk's rows and for their positions, two rows at a time (one warp).  Behind the last row: that row
+// again.  (Bulk copies of a token's heads, 1 KB, took one warp 200 clocks each.)
 __device__ __forceinline__ void ask_rows(const RopeParams& P, const Place& w, int half, uint32_t raw, uint32_t pos, uint64_t* bar, int lane) {
   const RotTensor& T = P.r.t[w.tt];
   const int lg = __ffs(T.head_div) - 1, last = (T.rows << lg) - 1, mask = T.head_div - 1;
@@ -168,15 +212,6 @@ __device__ __forceinline__ void ask_rows(const RopeParams& P, const Place& w, in
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(um_saddr(bar)) : "memory");
 }
 
-// Rotation of eight pairs, two at a time.
-__device__ __forceinline__ void turn(float2 (&a)[4], float2 (&b)[4], const float2 (&c)[4], const float2 (&s)[4]) {
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    const float2 u = mul2(a[m], s[m]), v = mul2(b[m], make_float2(-1.f, -1.f));
-    a[m] = fma2(v, s[m], mul2(a[m], c[m]));
-    b[m] = fma2(b[m], c[m], u);
-  }
-}
 // Where pair i stands in the table: the eight lanes of a row, which ask for pairs eight (kInter: four) apart, find theirs
 // side by side.
 __device__ __forceinline__ int freq_slot(bool inter, int i) { return inter ? (i & 3) * 16 + (i >> 2) : (i & 7) * 8 + (i >> 3); }
@@ -205,152 +240,153 @@ __device__ __forceinline__ void tmem_ld_tiles(uint32_t taddr, uint32_t* v) {
       : "r"(taddr));
 }
 
-// Eight numbers as hi and lo in 16 bytes each.
-__device__ __forceinline__ void split_store(const float (&v)[8], uint32_t hi_at, uint32_t lo_at) {
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    const float2 x = make_float2(v[2 * m], v[2 * m + 1]);
-    const float2 y = make_float2(lead11(x.x), lead11(x.y));
-    const float2 z = fma2(y, make_float2(-1.f, -1.f), x);
-    h[m] = half2_bits(y.x, y.y);
-    l[m] = half2_bits(z.x, z.y);
-  }
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(hi_at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(lo_at), "r"(l[0]), "r"(l[1]), "r"(l[2]), "r"(l[3]) : "memory");
+// Two numbers as hi and lo.
+__device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const float2 v = make_float2(x, y), h = make_float2(lead11(x), lead11(y));
+  const float2 l = fma2(h, make_float2(-1.f, -1.f), v);
+  hi = half2_bits(h.x, h.y);
+  lo = half2_bits(l.x, l.y);
+}
+__device__ __forceinline__ void sts_v4(uint32_t a, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
 
-__device__ __forceinline__ uint32_t amax16(const uint4& v) {
-  return __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-}
+// What a lane needs to place its two rows.
+struct Lane {
+  int r0, sub;               // the slot's first row; the lane of the slot
+  int va, vb;                // its vectors of eight channels
+  uint32_t at_a, at_b;       // where those of row r0 go in a buffer (row r0 + 1: 128 bytes on, pieces exchanged in twos)
+  uint32_t freq_at, freq_step;   // the first of its pairs in the table of frequencies, bytes to the next
+};
 
-// Places a slot's two rows: hi and lo into the chunk's buffer, destination and factor into its metadata.
-template <int kMode>
-__device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, int left, uint32_t pos_s, int r0, int sub, int va,
-                                           int vb, uint32_t at_a, uint32_t at_b, uint32_t raw, int bar_raw, uint32_t xb, uint32_t norm_s, uint32_t freq_s,
-                                           uint32_t fac_s) {
-  float2 c[4], s[4];
-  const bool norm = g.norm;
-  int2 pos2 = make_int2(0, 0);
+// Places a slot's two rows: hi and lo into the chunk's buffer, the factor that goes with a row beside its destination.
+// kW: 0: as they are, 1: norm and weights, 2: weights without a norm.  kSame: the two rows are heads of one token.
+// Nothing branches, and pairs are the outer loop: the two rows' chains of operations run side by side.
+template <int kMode, int kW, bool kSame>
+__device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, const Lane& L, int left, uint32_t pos_s, uint32_t raw, uint64_t* bar_read,
+                                           uint32_t xb, uint32_t norm_s, uint32_t freq_s, uint32_t fac_s) {
+  int pos[2] = {0, 0};
   if (kMode != kNone) {
-    const uint2 x = lds_v2(pos_s + 4u * r0);
-    pos2 = make_int2((int)x.x, (int)x.y);
+    const uint2 x = lds_v2(pos_s + 4u * L.r0);
+    pos[0] = (int)x.x;
+    pos[1] = (int)x.y;
   }
-  uint4 ra2[2], rb2[2];
+  uint32_t wa[2][4], wb[2][4];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    ra2[j] = lds_v4(raw + 256u * (r0 + j) + 16u * va);
-    rb2[j] = lds_v4(raw + 256u * (r0 + j) + 16u * vb);
+    const uint4 x = lds_v4(raw + 256u * (L.r0 + j) + 16u * L.va), y = lds_v4(raw + 256u * (L.r0 + j) + 16u * L.vb);
+    wa[j][0] = x.x, wa[j][1] = x.y, wa[j][2] = x.z, wa[j][3] = x.w;
+    wb[j][0] = y.x, wb[j][1] = y.y, wb[j][2] = y.z, wb[j][3] = y.w;
   }
-  rt_arrive(bar_raw, kRawWarps);                         // (the next rows but one may come)
+  rt_arrive(bar_read, threadIdx.x & 31);                 // (the next rows but one may come)
+  // the number that brings a row's channels below 2^15, the one that takes it back at the end
+  float2 up[2];
+  float back[2];
+  bool fine[2];
+  if (kW == 1) {
+    // |x| / rms(x) <= sqrt(128): the norm's own factor, and the weights' power of two
+    float ss[2];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const uint4 ra = ra2[j], rb = rb2[j];
-    const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
-    // the number that brings the row's channels below 2^15, the one that takes it back at the end
-    float up, back;
-    bool fine;
-    if (norm) {
-      // |x| / rms(x) <= sqrt(128): the norm's own factor, and the weights' power of two
+    for (int j = 0; j < 2; ++j) {
       float2 acc[2];
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const float2 x = make_float2(lo16(wa[m]), hi16(wa[m])), y = make_float2(lo16(wb[m]), hi16(wb[m]));
+        const float2 x = make_float2(lo16(wa[j][m]), hi16(wa[j][m])), y = make_float2(lo16(wb[j][m]), hi16(wb[j][m]));
         acc[0] = m ? fma2(x, x, acc[0]) : mul2(x, x);
         acc[1] = m ? fma2(y, y, acc[1]) : mul2(y, y);
       }
-      float ss = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      fine = ss <= 3.4e38f;
-      up = fine ? rsqrtf(fmaf(ss, 1.0f / kHeadDim, P.eps)) * g.up : __int_as_float(0x7fffffff);
-      back = g.back;
-    } else {
-      uint32_t top = __vmaxu2(amax16(ra), amax16(rb));   // (bf16 bits order as integers)
-      top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int k = fit_pow2((int)(top >> 7) + g.grow);
-      fine = top < 0x7f80u;
-      up = pow2(k);
-      back = pow2(-k) * g.t_back;
+      ss[j] = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
     }
-    const float2 u2 = make_float2(up, up);
-    // the pairs' members a, b (kInter: even and odd channels of va, then of vb) under the weights and that number
-    float2 a[4], b[4];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
+    for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) ss[j] += __shfl_xor_sync(0xffffffffu, ss[j], o);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      fine[j] = ss[j] <= 3.4e38f;
+      const float u = fine[j] ? rsqrtf(fmaf(ss[j], 1.0f / kHeadDim, P.eps)) * g.up : __int_as_float(0x7fffffff);
+      up[j] = make_float2(u, u);
+      back[j] = g.back;
+    }
+  } else {
+    uint32_t top[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {                        // (bf16 bits order as integers)
+      uint32_t t = 0u;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) t = __vmaxu2(t, __vmaxu2(wa[j][m] & 0x7fff7fffu, wb[j][m] & 0x7fff7fffu));
+      top[j] = max(t & 0xffffu, t >> 16);
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int k = fit_pow2((int)(top[j] >> 7) + g.grow);
+      fine[j] = top[j] < 0x7f80u;
+      up[j] = make_float2(pow2(k), pow2(k));
+      back[j] = pow2(-k) * g.t_back;
+    }
+  }
+  uint32_t ha[2][4], la[2][4], hb[2][4], lb[2][4];
+  float any_a[2][8], any_b[2][8];                        // (kAny: before the rotation)
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    // two pairs' members a, b (kHalf and others: channels 2 m, + 1 of va and of vb; kInter: even and odd channels of four)
+    float2 ka, kb, c, s;
+    if (kW != 0) {
       if (kMode == kInter) {
-        const uint32_t x = m < 2 ? wa[2 * m] : wb[2 * m - 4], y = m < 2 ? wa[2 * m + 1] : wb[2 * m - 3];
-        a[m] = make_float2(lo16(x), lo16(y));
-        b[m] = make_float2(hi16(x), hi16(y));
+        const uint4 x = lds_v4(norm_s + (uint32_t)((m & 1) * 256 + (m < 2 ? L.va : L.vb) * 16));
+        ka = make_float2(__uint_as_float(x.x), __uint_as_float(x.z));
+        kb = make_float2(__uint_as_float(x.y), __uint_as_float(x.w));
       } else {
-        a[m] = make_float2(lo16(wa[m]), hi16(wa[m]));
-        b[m] = make_float2(lo16(wb[m]), hi16(wb[m]));
+        const uint32_t at = norm_s + (uint32_t)((m >> 1) * 256 + (m & 1) * 8);
+        const uint2 x = lds_v2(at + 16u * L.va), y = lds_v2(at + 16u * L.vb);
+        ka = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
+        kb = make_float2(__uint_as_float(y.x), __uint_as_float(y.y));
       }
     }
-    if (g.weighted) {
+    const uint32_t f = kMode == kHalf ? L.freq_at + 2u * m * L.freq_step
+                                      : freq_s + 8u * (m < 2 ? L.va : L.vb) + 2u * (m & 1) * 128u;     // (freq_slot)
+    const uint32_t f_step = kMode == kHalf ? L.freq_step : 128u;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 x = lds_v4(norm_s + (uint32_t)(h * 256 + va * 16)), y = lds_v4(norm_s + (uint32_t)(h * 256 + vb * 16));
-        const float2 x0 = make_float2(__uint_as_float(x.x), __uint_as_float(x.y)), x1 = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
-        const float2 y0 = make_float2(__uint_as_float(y.x), __uint_as_float(y.y)), y1 = make_float2(__uint_as_float(y.z), __uint_as_float(y.w));
-        if (kMode == kInter) {
-          a[h] = mul2(a[h], mul2(make_float2(x0.x, x1.x), u2));
-          b[h] = mul2(b[h], mul2(make_float2(x0.y, x1.y), u2));
-          a[2 + h] = mul2(a[2 + h], mul2(make_float2(y0.x, y1.x), u2));
-          b[2 + h] = mul2(b[2 + h], mul2(make_float2(y0.y, y1.y), u2));
-        } else {
-          a[2 * h] = mul2(a[2 * h], mul2(x0, u2));
-          a[2 * h + 1] = mul2(a[2 * h + 1], mul2(x1, u2));
-          b[2 * h] = mul2(b[2 * h], mul2(y0, u2));
-          b[2 * h + 1] = mul2(b[2 * h + 1], mul2(y1, u2));
-        }
-      }
-    } else {
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        a[m] = mul2(a[m], u2);
-        b[m] = mul2(b[m], u2);
-      }
-    }
-    const int r = r0 + j, pos = j ? pos2.y : pos2.x;
-    if (kMode == kHalf || kMode == kInter) {
-      if (j == 0 || !g.same) {                         // (else the two rows are heads of one token)
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          // (freq_slot of pairs 8 va + 2 m and the next; kInter: 4 va + 2 m, then of vb)
-          constexpr uint32_t step = kMode == kHalf ? 64 : 128;
-          const uint32_t at = freq_s + (kMode == kHalf ? 8u * min(va, 7) + 2u * m * step : 8u * (m < 2 ? va : vb) + 2u * (m & 1) * step);
-          phase_sincos(at, pos, c[m].x, s[m].x);
-          phase_sincos(at + step, pos, c[m].y, s[m].y);
-        }
-        if (kMode == kHalf && 8 * va >= P.half_rot) {    // (vectors that are no pair)
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            c[m] = make_float2(1.f, 1.f);
-            s[m] = make_float2(0.f, 0.f);
-          }
-        }
-      }
-      turn(a, b, c, s);
-    }
-    float va8[8], vb8[8];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
+    for (int j = 0; j < 2; ++j) {
+      float2 a, b;
       if (kMode == kInter) {
-        float* d = m < 2 ? va8 + 4 * m : vb8 + 4 * (m - 2);
-        d[0] = a[m].x;
-        d[1] = b[m].x;
-        d[2] = a[m].y;
-        d[3] = b[m].y;
+        const uint32_t x = m < 2 ? wa[j][2 * m] : wb[j][2 * m - 4], y = m < 2 ? wa[j][2 * m + 1] : wb[j][2 * m - 3];
+        a = make_float2(lo16(x), lo16(y));
+        b = make_float2(hi16(x), hi16(y));
       } else {
-        va8[2 * m] = a[m].x;
-        va8[2 * m + 1] = a[m].y;
-        vb8[2 * m] = b[m].x;
-        vb8[2 * m + 1] = b[m].y;
+        a = make_float2(lo16(wa[j][m]), hi16(wa[j][m]));
+        b = make_float2(lo16(wb[j][m]), hi16(wb[j][m]));
+      }
+      a = mul2(a, kW != 0 ? mul2(ka, up[j]) : up[j]);
+      b = mul2(b, kW != 0 ? mul2(kb, up[j]) : up[j]);
+      if (kMode == kHalf || kMode == kInter) {
+        if (j == 0 || !kSame) {
+          phase_sincos(f, pos[j], c.x, s.x);
+          phase_sincos(f + f_step, pos[j], c.y, s.y);
+        }
+        const float2 x = fma2(mul2(b, s), make_float2(-1.f, -1.f), mul2(a, c));
+        b = fma2(b, c, mul2(a, s));
+        a = x;
+      }
+      if (kMode == kInter) {
+        split(a.x, b.x, m < 2 ? ha[j][2 * m] : hb[j][2 * m - 4], m < 2 ? la[j][2 * m] : lb[j][2 * m - 4]);
+        split(a.y, b.y, m < 2 ? ha[j][2 * m + 1] : hb[j][2 * m - 3], m < 2 ? la[j][2 * m + 1] : lb[j][2 * m - 3]);
+      } else if (kMode == kAny) {
+        any_a[j][2 * m] = a.x, any_a[j][2 * m + 1] = a.y;
+        any_b[j][2 * m] = b.x, any_b[j][2 * m + 1] = b.y;
+      } else {
+        split(a.x, a.y, ha[j][m], la[j][m]);
+        split(b.x, b.y, hb[j][m], lb[j][m]);
       }
     }
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int r = L.r0 + j;
     if (kMode == kAny) {
       // pairs that no lane holds: through the row's own place in the buffer, 512 bytes as float32 in four lines
       const uint32_t line = xb + (uint32_t)((r >> 3) * 1024 + (r & 7) * 128);
@@ -359,20 +395,20 @@ __device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, in
       };
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
-        sts_v2(at(8 * va + e), __float_as_uint(va8[e]), __float_as_uint(va8[e + 1]));
-        sts_v2(at(8 * vb + e), __float_as_uint(vb8[e]), __float_as_uint(vb8[e + 1]));
+        sts_v2(at(8 * L.va + e), __float_as_uint(any_a[j][e]), __float_as_uint(any_a[j][e + 1]));
+        sts_v2(at(8 * L.vb + e), __float_as_uint(any_b[j][e]), __float_as_uint(any_b[j][e + 1]));
       }
       __syncwarp();
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        float* d = v ? vb8 : va8;
+        float* d = v ? any_b[j] : any_a[j];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int ch = 8 * (v ? vb : va) + e, h = P.half_rot;
+          const int ch = 8 * (v ? L.vb : L.va) + e, h = P.half_rot;
           const int i = ch < h ? ch : ch - h, other = ch < h ? ch + h : ch - h;
           if (ch < 2 * h) {
             float cs, sn;
-            phase_sincos(freq_s + 8u * (uint32_t)freq_slot(false, i), pos, cs, sn);
+            phase_sincos(freq_s + 8u * (uint32_t)freq_slot(false, i), j && !kSame ? pos[1] : pos[0], cs, sn);
             uint32_t o;
             asm volatile("ld.shared.u32 %0, [%1];" : "=r"(o) : "r"(at(other)) : "memory");
             d[e] = fmaf(d[e], cs, (ch < h ? -sn : sn) * __uint_as_float(o));
@@ -380,16 +416,35 @@ __device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, in
         }
       }
       __syncwarp();
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        split(any_a[j][2 * m], any_a[j][2 * m + 1], ha[j][m], la[j][m]);
+        split(any_b[j][2 * m], any_b[j][2 * m + 1], hb[j][m], lb[j][m]);
+      }
     }
-    // (r0 is even: row r0 + 1 stands 128 bytes on, its pieces exchanged in twos)
-    const uint32_t to_a = xb + (at_a ^ (16u * j)) + 128u * j, to_b = xb + (at_b ^ (16u * j)) + 128u * j;
-    split_store(va8, to_a, to_a + kHalfBuf);
-    split_store(vb8, to_b, to_b + kHalfBuf);
-    if (sub == 0) {
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(fac_s + 4u * (uint32_t)r), "f"(back) : "memory");
-      if (!fine && left > j) set_status(P.r.status, KVQ_ERR_NONFINITE);
+    const uint32_t to_a = xb + (L.at_a ^ (16u * j)) + 128u * j, to_b = xb + (L.at_b ^ (16u * j)) + 128u * j;
+    sts_v4(to_a, ha[j]);
+    sts_v4(to_a + kHalfBuf, la[j]);
+    sts_v4(to_b, hb[j]);
+    sts_v4(to_b + kHalfBuf, lb[j]);
+    if (L.sub == 0) {
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(fac_s + 4u * (uint32_t)r), "f"(back[j]) : "memory");
+      if (!fine[j] && left > j) set_status(P.r.status, KVQ_ERR_NONFINITE);
     }
   }
+}
+template <int kMode, int kW>
+__device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, const Lane& L, int left, uint32_t pos_s, uint32_t raw, uint64_t* bar_read,
+                                           uint32_t xb, uint32_t norm_s, uint32_t freq_s, uint32_t fac_s) {
+  if (kMode == kNone || g.same) place_rows<kMode, kW, true>(P, g, L, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
+  else place_rows<kMode, kW, false>(P, g, L, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
+}
+template <int kMode>
+__device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, const Lane& L, int left, uint32_t pos_s, uint32_t raw, uint64_t* bar_read,
+                                           uint32_t xb, uint32_t norm_s, uint32_t freq_s, uint32_t fac_s) {
+  if (g.norm) place_rows<kMode, 1>(P, g, L, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
+  else if (kMode != kNone && g.weighted) place_rows<kMode, 2>(P, g, L, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
+  else place_rows<kMode, 0>(P, g, L, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
 }
 
 // Half of a matrix row (row: its 64 entries; none: row i of the Walsh-Hadamard matrix) as hi and lo into TMEM.
@@ -436,7 +491,7 @@ __device__ __forceinline__ uint32_t top_exponent(const float* row) {
 
 __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_constant__ RopeParams P) {
   __shared__ uint32_t tbase_sh;
-  __shared__ __align__(8) uint64_t bar_mma[2], bar_raw[2];
+  __shared__ __align__(8) uint64_t bar_mma[2], bar_raw[2], bar_read[2], bar_x[2], bar_free[2];
   __shared__ volatile int abort_sh;
   __shared__ int uneven_sh;
   __shared__ Seg seg_sh;
@@ -448,7 +503,10 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
     abort_sh = 0;
     for (int i = 0; i < 2; ++i) {
       um_mbar_init(&bar_mma[i]);
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 64;" ::"r"(um_saddr(&bar_raw[i])) : "memory");
+      rt_init(&bar_raw[i], 64);                          // rows are there
+      rt_init(&bar_read[i], kRtWarps);                   // rows are in registers
+      rt_init(&bar_x[i], kRtWarps + 1);                  // rows are placed, their destinations known
+      rt_init(&bar_free[i], kRtOut);                     // results are out
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -463,8 +521,7 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
   // wait for this grid.  For the same reason this kernel itself does not begin before the one ahead of it has ended.
   pdl_trigger();
   const uint32_t tb = tbase_sh;
-  const int c_lo = (int)((long long)P.r.dense_total * blockIdx.x / gridDim.x);
-  const int c_hi = (int)((long long)P.r.dense_total * (blockIdx.x + 1) / gridDim.x);
+  const int c_lo = first_chunk(P, blockIdx.x), c_hi = first_chunk(P, blockIdx.x + 1);
   const int total = c_hi - c_lo;
   const int q = warp & 3;
   const uint32_t tlane = (uint32_t)(32 * q) << 16;       // this warp's TMEM lanes
@@ -479,9 +536,9 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
         const uint32_t d = tb + kRtAcc + 64u * (uint32_t)s;
         const bool dense = P.r.t[w.tt].mode == ROT_DENSE;
         const uint64_t xd = sw128_desc(sb + (uint32_t)(s * kRtXBuf));
-        rt_sync(kBarX + s, kXWarps);
+        const bool ok = rt_wait_use(bar_x, n, &abort_sh);
         tc_fence_after();
-        if (rt_elect()) {
+        if (ok && rt_elect()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint64_t hi = xd + (uint64_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), lo = hi + (kHalfBuf >> 4);
@@ -499,11 +556,10 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
       Place w = place_of(P, c_lo);
       for (int n = 0; n < total; ++n) {
         const int s = n & 1;
-        if (n >= 2) rt_sync(kBarRaw + s, kRawWarps);
+        if (n >= 2) rt_wait_use(bar_read, n - 2, &abort_sh);
         ask_rows(P, w, (warp - kRtLoad) >> 1, sb + (uint32_t)(kRtRaw + s * kRtRawBuf), sb + (uint32_t)(kRtPos + s * kRtRows * 4), &bar_raw[s], lane);
         if (++w.c == w.cpm && n + 1 < total) w = place_of(P, c_lo + n + 1);
       }
-      for (int n = max(total - 2, 0); n < total; ++n) rt_sync(kBarRaw + (n & 1), kRawWarps);
       asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
       // ---- where a chunk's rows go, two to a lane ----
@@ -523,10 +579,11 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
             (j ? dst[1] : dst[0]) = d;
           }
         }
-        // (chunk n - 1 is placed, so what chunk n - 4 had here has been used)
+        // (once chunk n - 2 is placed, what chunk n - 4 had here has been used)
+        if (n >= 2) rt_wait_use(bar_x, n - 2, &abort_sh);
         sts_u64(meta + 8u * (uint32_t)lane, dst[0]);
         sts_u64(meta + 8u * (uint32_t)(32 + lane), dst[1]);
-        rt_sync(kBarX + (n & 1), kXWarps);
+        rt_arrive(&bar_x[n & 1], lane);
         if (++w.c == w.cpm && n + 1 < total) w = place_of(P, c_lo + n + 1);
       }
     }
@@ -540,7 +597,7 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
       const int s = n & 1;
       const uint32_t xb = sb + (uint32_t)(s * kRtXBuf), acc_at = tb + tlane + kRtAcc + 64u * (uint32_t)s;
       const uint32_t fac = sb + (uint32_t)(kRtFac + s * kRtRows * 4), meta = sb + (uint32_t)(kRtMeta + (n & (kMetaSets - 1)) * kRtRows * 8);
-      if (warp == kRtWarps && !abort_sh && !__all_sync(0xffffffffu, rt_wait(&bar_mma[s], (uint32_t)((n >> 1) & 1)))) abort_sh = 1;
+      if (warp == kRtWarps) rt_wait_use(bar_mma, n, &abort_sh);
       rt_sync(kBarMma, kRtOut);
       const bool ok = !abort_sh;
       if (ok) {
@@ -602,7 +659,7 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
             if (dst[j]) __stcg(reinterpret_cast<uint4*>(dst[j]) + (lane & 15), x[j]);
         }
       }
-      rt_arrive(kBarFree + s, kFreeWarps);
+      rt_arrive(&bar_free[s], lane);
     }
     // after a time-out: what was issued ends before TMEM is given back (bounded)
     if (abort_sh && warp == kRtWarps)
@@ -615,8 +672,9 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
     const uint32_t norm_s = sb + kRtNorm, freq_s = sb + kRtFreq;
     uint32_t* exch = reinterpret_cast<uint32_t*>(sm + kRtExch);
     const Seg& g = seg_sh;
-    int mode = kNone, va = sub, vb = sub + 8;
-    uint32_t at_a = 0, at_b = 0;                         // this thread's vectors of row r0 in a buffer
+    int mode = kNone;
+    Lane L{r0, sub, sub, sub + 8, 0u, 0u, 0u, 0u};
+    if (tid == 64) reinterpret_cast<uint64_t*>(sm + kRtFreq)[64] = 0ull;
     if (tid < 64)
       reinterpret_cast<uint64_t*>(sm + kRtFreq)[freq_slot(P.interleaved, tid)] = tid < P.half_rot ? __ldg(P.freq + tid) : 0ull;
 
@@ -657,12 +715,18 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
       split_matrix(had ? nullptr : trow, i, part, pow2(k), tb + tlane);
       // which channels a lane holds
       mode = !turned ? kNone : P.interleaved ? kInter : P.half_rot % 8 == 0 ? kHalf : kAny;
-      va = sub;
-      vb = sub + 8;
+      L.va = sub;
+      L.vb = sub + 8;
+      L.freq_at = freq_s + 8u * sub;                     // (freq_slot of pair 8 va; the next eight positions on)
+      L.freq_step = 64u;
       if (mode == kHalf) {
         const int h8 = P.half_rot / 8;
-        va = sub < h8 ? sub : 2 * h8 + 2 * (sub - h8);
-        vb = sub < h8 ? sub + h8 : va + 1;
+        L.va = sub < h8 ? sub : 2 * h8 + 2 * (sub - h8);
+        L.vb = sub < h8 ? sub + h8 : L.va + 1;
+        if (sub >= h8) {                                 // (two vectors that are no pair: a frequency of 0)
+          L.freq_at = freq_s + 8u * 64u;
+          L.freq_step = 0u;
+        }
       }
       uint32_t wtop = 0;
 #pragma unroll
@@ -672,8 +736,8 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
       const int grow = (weighted ? (int)(wtop >> 23) - 126 : 0) + (turned ? 1 : 0), kn = fit_pow2(130 + grow);
       if (tid == 0) seg_sh = Seg{T.head_div > 1, norm, weighted, grow, pow2(kn), pow2(-kn) * t_back, t_back};
       rt_sync(kBarPlace, kRtWarps);
-      at_a = (uint32_t)xs_offset(r0, 8 * va);
-      at_b = (uint32_t)xs_offset(r0, 8 * vb);
+      L.at_a = (uint32_t)xs_offset(r0, 8 * L.va);
+      L.at_b = (uint32_t)xs_offset(r0, 8 * L.vb);
     };
 
     bool fresh = true;                                   // the chunk begins a matrix (or this CTA's work)
@@ -682,26 +746,25 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
     for (int n = 0; n < total; ++n) {
       const int s = n & 1;
       // (at a new matrix the last one's results are out: TMEM and what its set-up left may be overwritten)
-      for (const int want = fresh ? n : n - 1; freed < want; ++freed) rt_sync(kBarFree + (freed & 1), kFreeWarps);
+      for (const int want = fresh ? n : n - 1; freed < want; ++freed) rt_wait_use(bar_free, freed, &abort_sh);
       if (fresh) {
         tc_fence_after();
         set_up(w);
       }
-      if (!abort_sh && !__all_sync(0xffffffffu, rt_wait(&bar_raw[s], (uint32_t)((n >> 1) & 1)))) abort_sh = 1;
+      rt_wait_use(bar_raw, n, &abort_sh);
       const uint32_t xb = sb + (uint32_t)(s * kRtXBuf), raw = sb + (uint32_t)(kRtRaw + s * kRtRawBuf);
       const uint32_t fac = sb + (uint32_t)(kRtFac + s * kRtRows * 4), pos = sb + (uint32_t)(kRtPos + s * kRtRows * 4);
       const int left = P.r.t[w.tt].rows * P.r.t[w.tt].head_div - w.c * kRtRows - r0;
-      if (mode == kHalf) place_rows<kHalf>(P, g, left, pos, r0, sub, va, vb, at_a, at_b, raw, kBarRaw + s, xb, norm_s, freq_s, fac);
-      else if (mode == kInter) place_rows<kInter>(P, g, left, pos, r0, sub, va, vb, at_a, at_b, raw, kBarRaw + s, xb, norm_s, freq_s, fac);
-      else if (mode == kAny) place_rows<kAny>(P, g, left, pos, r0, sub, va, vb, at_a, at_b, raw, kBarRaw + s, xb, norm_s, freq_s, fac);
-      else place_rows<kNone>(P, g, left, pos, r0, sub, va, vb, at_a, at_b, raw, kBarRaw + s, xb, norm_s, freq_s, fac);
+      if (mode == kHalf) place_rows<kHalf>(P, g, L, left, pos, raw, bar_read + s, xb, norm_s, freq_s, fac);
+      else if (mode == kInter) place_rows<kInter>(P, g, L, left, pos, raw, bar_read + s, xb, norm_s, freq_s, fac);
+      else if (mode == kAny) place_rows<kAny>(P, g, L, left, pos, raw, bar_read + s, xb, norm_s, freq_s, fac);
+      else place_rows<kNone>(P, g, L, left, pos, raw, bar_read + s, xb, norm_s, freq_s, fac);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc_fence_before();
-      rt_arrive(kBarX + s, kXWarps);
+      rt_arrive(&bar_x[s], lane);
       fresh = ++w.c == w.cpm;
       if (fresh && n + 1 < total) w = place_of(P, c_lo + n + 1);
     }
-    for (; freed < total; ++freed) rt_sync(kBarFree + (freed & 1), kFreeWarps);
   }
   tc_fence_before();
   __syncthreads();

@@ -127,6 +127,12 @@ def test_prefill_sizes(rows, hq, hkv, kind, tv, layout, rot, norm):
     Call(rows, hq, hkv, kind, tv, layout, rot, norm, gap=8).run().check()
 
 
+# (the sizes from which on runs of work differ in length: no pair left out at either end)
+@pytest.mark.parametrize("rows,hq,hkv,tv", [(7801, 32, 8, False), (7800, 32, 8, False), (155_701, 1, 1, True), (20_011, 8, 8, False)])
+def test_long_prefill(rows, hq, hkv, tv):
+    Call(rows, hq, hkv, tv=tv).run().check()
+
+
 @pytest.mark.parametrize("rows", [3, 3001])
 def test_positions(rows):
     """Positions in the text that are not the tokens' numbers: far, negative, at the ends of the type."""
