@@ -59,6 +59,10 @@ class DecodeRunner:
         # the page pool: how many table entries hold each page (set_page_table counts them)
         self.page_ref = torch.zeros(cfg.num_pages, dtype=torch.int32, device=self.device)
         self.n_live = torch.zeros(1, dtype=torch.int32, device=self.device)
+        # next_tokens: trees of one node, a sequence to a row (cu_rows, token and parent, path, n_accept)
+        i32 = dict(dtype=torch.int32, device=self.device)
+        self._ones = (torch.arange(cfg.batch + 1, **i32), torch.full((cfg.batch,), -1, **i32), torch.zeros(cfg.batch, **i32),
+                      torch.zeros(cfg.batch, **i32))
 
     def set_page_table(self, table: np.ndarray) -> None:
         table = np.ascontiguousarray(table, np.int32)
@@ -149,10 +153,6 @@ class DecodeRunner:
         """A token for every sequence (next_token [batch]) from its row of logits [batch, vocab] under `rules` and a uniform
         number u [batch]; p [batch, vocab] holds the probabilities, and rules.counts, where given, counts the tokens."""
         stream = self.stream if stream is None else stream
-        if not hasattr(self, "_ones"):                  # trees of one node: a sequence to a row
-            i32 = dict(dtype=torch.int32, device=self.device)
-            self._ones = (torch.arange(self.cfg.batch + 1, **i32), torch.full((self.cfg.batch,), -1, **i32),
-                          torch.zeros(self.cfg.batch, **i32), torch.zeros(self.cfg.batch, **i32))
         cu, root, path, n_accept = self._ones
         kv_logits_probs(self.cfg, rules, logits, cu, None, None, p, self.status, stream)
         kv_verify_tree(self.cfg, cu, root, path, p, None, u, path, n_accept, next_token, self.status, stream)

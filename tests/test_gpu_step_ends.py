@@ -183,3 +183,25 @@ def test_plain_steps():
     for b in range(B):
         want[b, seen[b]] = 1
     assert np.array_equal(counts.cpu().numpy(), want)
+
+
+def test_next_tokens_captured_first():
+    """The runner's first call is captured; one beside the graph, before it has run, is right too."""
+    a = Loop()
+    rng, B = a.rng, W.batch
+    logits = torch.from_numpy(rng.standard_normal((B, VOCAB)).astype(np.float32) * 3).cuda()
+    random = rng.random(B).astype(np.float32)
+    u = torch.from_numpy(random).cuda()
+    p, p2 = (torch.zeros((B, VOCAB), device="cuda") for _ in range(2))
+    nxt, nxt2 = (torch.full((B,), -7, dtype=torch.int32, device="cuda") for _ in range(2))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.r.next_tokens(None, logits, p, u, nxt, stream=torch.cuda.current_stream().cuda_stream)
+    a.r.next_tokens(None, logits, p2, u, nxt2)
+    torch.cuda.synchronize()
+    want = [spec_ref.verify([-1], [0], p2.cpu().numpy()[b:b + 1], None, random[b:b + 1])[1] for b in range(B)]
+    assert nxt2.tolist() == want and int(a.r.status.item()) == 0 and nxt.tolist() == [-7] * B
+    graph.replay()
+    torch.cuda.synchronize()
+    assert nxt.tolist() == want and torch.equal(p, p2) and int(a.r.status.item()) == 0
