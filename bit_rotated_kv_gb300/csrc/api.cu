@@ -192,6 +192,10 @@ KVQ_API int kv_rope_qk(const kvq_config* cfg, const kvq_transform* tr, const kvq
     if (!aligned(seq_idx, 4) || !aligned(pos, 4) || !aligned(rope_pos, 4)) return KVQ_ERR_INVALID_ARG;
     if (tr->kind == KVQ_TRANSFORM_DENSE && (!tr->t_k || !aligned(tr->t_k, 16))) return KVQ_ERR_INVALID_ARG;
     if (tr->t_v && !aligned(tr->t_v, 16)) return KVQ_ERR_INVALID_ARG;
+    const size_t row = (size_t)cfg->n_kv_heads * kHeadDim * 2, out = (size_t)n_q_rows * cfg->n_q_heads * kHeadDim * 2;
+    if (n_q_rows > 0 && (overlap(k, (size_t)(n_kv_rows - 1) * k_stride * 2 + row, q_out, out) ||
+                         overlap(v, (size_t)(n_kv_rows - 1) * v_stride * 2 + row, q_out, out)))
+      return KVQ_ERR_INVALID_ARG;
   }
   if (n_q_rows == 0 && n_kv_rows == 0) return KVQ_OK;
   kvq_cache empty{};

@@ -484,7 +484,7 @@ KVQ_API int kvq_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling,
  * position, transform, and the append.
  *   q        [n_q_rows][Hq][d] bf16, rows q_stride elements apart (so for k and v: three parts of one fused
  *            projection do; strides are multiples of 8 and at least H d, bases 16-byte aligned)
- *   q_out    [n_q_rows][Hq][d] bf16 (16-byte aligned): T_K^{-T} rope(norm(q)); must not overlap q
+ *   q_out    [n_q_rows][Hq][d] bf16 (16-byte aligned): T_K^{-T} rope(norm(q)); must not overlap the rows of q, k or v
  *   q_pos    [n_q_rows] int32: each query's position in the text (any value; NULL when n_q_rows == 0)
  *   k, v     [n_kv_rows][Hkv][d] bf16 likewise; seq_idx, pos [n_kv_rows] int32 as for kv_rotate_qk
  *   rope_pos [n_kv_rows] int32: each key's position in the text where it is not its token's number (the nodes
@@ -497,8 +497,10 @@ KVQ_API int kvq_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling,
  * values are exact.  A head whose row holds an infinity or NaN, or (with a norm) whose squares sum to more than
  * float32 holds, gets a row that is not finite, and KVQ_ERR_NONFINITE (copied values aside).
  * rope NULL: no norm and no rotation (q_pos may then be NULL).
- * Execution: up to 2048 (row, head) pairs that have a matrix run on the CUDA cores, a slice of a matrix to a CTA; larger calls
- * on the tensor cores, both operands as pairs of fp16 under powers of two.  The two round differently.
+ * Of cfg the heads, batch, s_sink and ring_cap are used.
+ * Execution: fewer than 2048 (row, head) pairs that have a matrix run on the CUDA cores, a slice of a matrix to a CTA;
+ * larger calls on the tensor cores, both operands as pairs of fp16 under powers of two, values that are copied in a
+ * launch before.  The two round differently.
  * Source: [WUSH] inference algorithm and [OScaR] algorithm, key and query processing (the transform follows RoPE);
  * norm and rotation are the models' own (Qwen3's heads). */
 KVQ_API int kv_rope_qk(const kvq_config* cfg, const kvq_transform* tr, const kvq_rope* rope, const uint16_t* q,
@@ -548,10 +550,12 @@ typedef struct kvq_logit_rules {         /* device pointers; NULL: that rule is 
  * masked tokens to -infinity, whatever stood there; softmax of l / temperature.
  * KVQ_ERR_NONFINITE and a row of zeros: where nothing is left (every token masked or at -infinity), where a logit that
  * is not masked becomes NaN or +infinity, or where a number of the sequence's rules is not finite, the temperature
- * negative or the repetition not within 2^-60 .. 2^60.  Probabilities below 2^-126 are 0.  KVQ_ERR_BOUNDS and a row of zeros: a mask that does not exist, more than KVQ_TREE_MAX_NODES nodes
- * in a sequence.  KVQ_ERR_BOUNDS: a parent that is not a lower node (the row goes by the path up to there), a token of the path or of a
- * bias outside the vocabulary (left out), biases out of order (an entry that is not above the one before it may be left out), and cu_rows that do not cover n_rows:
- * rows behind the last sequence are not written.  Sums are taken in one order: the same bits on every run.
+ * negative or the repetition not within 2^-60 .. 2^60.  Probabilities below 2^-126 are 0.  KVQ_ERR_BOUNDS and a row
+ * of zeros: a mask that does not exist, more than KVQ_TREE_MAX_NODES nodes in a sequence.  KVQ_ERR_BOUNDS: a parent that
+ * is not a lower node (the row goes by the path up to there), a token of the path or of a bias outside the vocabulary
+ * (left out), biases out of order (an entry that is not above the one before it may be left out), and cu_rows that do
+ * not cover n_rows: rows behind the last sequence are not written.  Sums are taken in one order: the same bits on every
+ * run.
  * vocab is at most KVQ_LOGITS_MAX_VOCAB.  Of cfg only batch is used.
  * Execution: a cluster of CTAs holds a row in shared memory: one read of the logits, one write of p.  Logits of
  * four masked neighbours are not read. */
@@ -565,7 +569,10 @@ KVQ_API int kv_logits_probs(const kvq_config* cfg, const kvq_logit_rules* rules,
  *                     kv_verify_tree, those of the kept nodes path[cu_rows[b] + j], 0 < j < n_accept[b] (node 0
  *                     was counted when it was drawn), and with next_token [B] the token behind them (-1: none).
  * Equal tokens may come any number of times.  Tokens outside the vocabulary, nodes outside the tree and rows of no
- * sequence are left out, with KVQ_ERR_BOUNDS.  Of cfg only batch is used; n_rows is at most 2^30 (KVQ_ERR_UNSUPPORTED). */
+ * sequence are left out, with KVQ_ERR_BOUNDS.  Of cfg only batch is used; n_rows is at most 2^30 (KVQ_ERR_UNSUPPORTED).
+ * Execution: an atomic for each of a warp's different tokens.  Prompts of 2^19 rows or more, a quarter of the vocabulary a
+ * sequence: CTAs take slices of the vocabulary and mark them in one sweep, without atomics: no other call may then
+ * write the same rows of counts at the same time (elsewhere calls may, up to KVQ_COUNT_MOST / 2 tokens). */
 KVQ_API int kv_token_counts(const kvq_config* cfg, uint16_t* counts, int64_t count_stride, int32_t vocab, int32_t kind,
                     const int32_t* cu_rows, const int32_t* token, int32_t n_rows, const int32_t* path,
                     const int32_t* n_accept, const int32_t* next_token, int32_t* d_status, void* stream);

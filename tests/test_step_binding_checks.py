@@ -182,3 +182,11 @@ def test_counts_refusals():
         assert _counts(**bad) == inval, bad
     assert _counts(n=(1 << 30) + 1) == kvq.KVQ_ERR_UNSUPPORTED
     assert _counts(n=0, nxt=0, path=0, acc=0) == 0
+
+
+def test_rope_rows_under_the_output():
+    """q_out anywhere on the rows of q, of k or of v: refused (a fused projection's rows reach from its first q to its last v)."""
+    far = dict(q=1 << 32, k=1 << 33, v=1 << 34)
+    for name, size in (("q", 4 * 1024 + 1024), ("k", 4 * 256 + 256), ("v", 4 * 256 + 256)):
+        for out in (X - 5 * 1024 + 16, X, X + size - 16):
+            assert _rope(**{**far, name: X}, out=out) == kvq.KVQ_ERR_INVALID_ARG, (name, out)
