@@ -274,3 +274,40 @@ def test_offsets_beyond_32_bits():
     wide.copy_(c.fused[:3, :12 * D].unflatten(1, (12, D)))
     c.q, c.k, c.v = wide[:, :8], wide[:, 8:10], wide[:, 10:]
     c.run().check()
+
+
+def test_calls_at_once():
+    """Three streams at once: two calls on the tensor cores and kv_rotate_qk's, which take tensor memory of the same SMs."""
+    a, b, c = Call(4003, 8, 8, kind="orthogonal"), Call(3001, 16, 4, layout=1, seed=2), Call(3001, 8, 8, seed=3)
+    d, x = Call(3001, 8, 8, seed=3), [_i32(v) for v in (a.seq, a.pos, b.seq, b.pos, c.seq, c.pos)]
+    rot = lambda z, s: kvq.kv_rotate_qk(z.cfg, z.tr, z.q.contiguous(), z.q_out, z.k.contiguous(), z.v.contiguous(), x[4], x[5], z.cache, z.status, s)  # noqa: E731
+    rot(d, None)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    rows = [t.contiguous() for t in (c.q, c.k, c.v)]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for z, s, i in ((a, streams[0], 0), (b, streams[1], 2)):
+            kvq.kv_rope_qk(z.cfg, z.tr, z.rope, z.q, z.q_out, x[i + 1], z.k, z.v, x[i], x[i + 1], None, z.cache, z.status, s)
+        kvq.kv_rotate_qk(c.cfg, c.tr, rows[0], c.q_out, rows[1], rows[2], x[4], x[5], c.cache, c.status, streams[2])
+    torch.cuda.synchronize()
+    a.check()
+    b.check()
+    assert torch.equal(c.q_out, d.q_out) and torch.equal(c.cache.ring_k, d.cache.ring_k) and int(c.status.item()) == 0
+
+
+def test_a_call_behind_it():
+    """The next call in the stream begins while this one's last blocks run: what it reads is whole."""
+    a = Call(3001)
+    seq, pos = _i32(a.seq), _i32(a.pos)
+    again = torch.full_like(a.q_out, 7.0)
+    for _ in range(6):
+        a.q_out.fill_(7.0)
+        kvq.kv_rope_qk(a.cfg, a.tr, a.rope, a.q, a.q_out, pos, a.k, a.v, seq, pos, None, a.cache, a.status)
+        kvq.kv_rope_qk(a.cfg, a.tr, None, a.q_out, again, None, None, None, None, None, None, a.cache, a.status)
+    torch.cuda.synchronize()
+    a.check()
+    first = again.clone()
+    kvq.kv_rope_qk(a.cfg, a.tr, None, a.q_out, again, None, None, None, None, None, None, a.cache, a.status)
+    torch.cuda.synchronize()
+    assert torch.equal(first, again)
