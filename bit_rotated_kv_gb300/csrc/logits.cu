@@ -8,11 +8,14 @@
 // Bytes bound it: a logit is read once and a probability written once (64 rows of 152 K tokens: 2 + 2 + 4 bytes each
 // with the counts), which needs the row on the chip between the two.  A row of 152 K float32 is 0.6 MB, more than an
 // SM's shared memory, so a cluster of CTAs takes a row, a contiguous slice each, and they exchange one (maximum, sum) pair
-// through distributed shared memory.  At 6.8 TB/s an SM has about thirty instructions a token to spare in all.  Penalties are therefore
-// taken without branches (in a history of thousands nearly every warp meets a counted token: behind one they took 64 instructions a
-// token, and 64 trees of 16 nodes over 152 K 531 us instead of 231), and loads come in batches that are all on their way
-// before the first is used.  Biases and the drafted path touch few tokens: the pass over the slice does without them and the
-// tokens concerned are computed again afterwards, by token, so that one that is in both lists is right either way.
+// through distributed shared memory.  At 6.8 TB/s an SM has about thirty instructions a token to spare in all.  Penalties
+// are therefore taken without branches (in a history of thousands nearly every warp meets a counted token: behind one they
+// took 64 instructions a token, and 64 trees of 16 nodes over 152 K 531 us instead of 229), and loads come in batches that
+// are all on their way before the first is used.  Biases and the drafted path touch few tokens: the pass over the slice
+// does without them and the tokens concerned are computed again afterwards, by token, so that one that is in both lists is
+// right either way.
+// What it measured: those 64 x 16 rows 229 us (floor by bytes 106: the instructions of three passes and the waits between
+// them bound it), 64 rows of 152 K 25 us (11.5), one row of 32 K 4.6 us (a launch and four waits one after another).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -483,8 +486,8 @@ __device__ __forceinline__ void add_tokens(const Half& h, uint32_t old, uint32_t
 constexpr int kPerLane = 4;          // rows of a lane: a warp takes 128 in a row, and their loads are on their way together
 
 // Latency bounds a step's few tokens (a chain of four loads and an atomic); a prompt's many, the random words that they
-// mark: 8 K tokens of each of 16
-// sequences take 6 us with the clearing of their counts.  Equal tokens of a warp are counted with one atomic (an answer's most frequent ones meet there).
+// mark: 8 K tokens of each of 16 sequences take 6.6 us with the clearing of their counts.  Equal tokens of a warp are counted
+// with one atomic (an answer's most frequent ones meet there).
 __global__ void __launch_bounds__(256) count_kernel(const __grid_constant__ CountParams P) {
   pdl_trigger();
   pdl_wait();
@@ -567,17 +570,20 @@ __global__ void __launch_bounds__(256) count_kernel(const __grid_constant__ Coun
   }
 }
 
-// Long prompts: a CTA takes a sequence and a slice of the vocabulary, looks at all of the prompt's tokens, gathers those of
-// its slice as bits in shared memory, and marks them in one sweep over the slice's counts, which are nobody else's in this call.
+// Long prompts: a cluster of CTAs takes a sequence.  Each gathers its share of the tokens as bits of the vocabulary in its shared
+// memory, then puts a slice of them all together and marks it in one sweep over the slice's counts, which are nobody else's in
+// this call.  (Each CTA looking at all of the prompt for the bits of its slice alone took 24 us for 16 of 64 K to 128 K tokens, 12 us so.)
 constexpr int kSweepThreads = 1024;
-constexpr int kSweepRows = 1 << 19;  // (fewer rows are marked one by one)
-constexpr int kSweepSlice = 16384;   // tokens of a slice (2 KB of bits)
+constexpr int kSweepCtas = 8;         // of a sequence
+constexpr int kSweepRows = 1 << 16, kSweepEach = 1 << 14;   // (fewer rows, of the call or a sequence, are marked one by one)
 __global__ void __launch_bounds__(kSweepThreads) prompt_kernel(const __grid_constant__ CountParams P) {
-  __shared__ uint32_t bits[kSweepSlice / 32];
+  extern __shared__ __align__(16) uint32_t bits[];       // the vocabulary's, then the slice's of all CTAs
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  const int tid = threadIdx.x, b = (int)(blockIdx.x / (unsigned)ranks);
+  const int words = (P.vocab + 31) >> 5, per = (words + ranks - 1) / ranks, w0 = min(words, rank * per), w1 = min(words, w0 + per);
   pdl_trigger();
-  const int tid = threadIdx.x, b = blockIdx.y;
-  const int v0 = blockIdx.x * kSweepSlice, v1 = min(P.vocab, v0 + kSweepSlice);
-  for (int i = tid; i < kSweepSlice / 32; i += kSweepThreads) bits[i] = 0u;
+  for (int i = tid; i < words; i += kSweepThreads) bits[i] = 0u;
   pdl_wait();
   const int first = P.cu_rows[b], last = P.cu_rows[b + 1];
   // rows of no sequence: before the first, behind the last, or where cu_rows falls
@@ -585,18 +591,18 @@ __global__ void __launch_bounds__(kSweepThreads) prompt_kernel(const __grid_cons
   __syncthreads();
   if (first >= 0 && last <= P.n_rows) {
     auto mark = [&](int t) {
-      if (t >= v0 && t < v1) atomicOr(&bits[(t - v0) >> 5], 1u << (t & 31));
-      odd |= t < 0 || t >= P.vocab;
+      if (t >= 0 && t < P.vocab) atomicOr(&bits[t >> 5], 1u << (t & 31));
+      else odd = true;
     };
     // four tokens at a time from a boundary on, the others one by one
     const int32_t* from = P.token + first;
     const int n = max(0, last - first), head = min(n, (int)(((16 - (reinterpret_cast<uintptr_t>(from) & 15)) & 15) >> 2));
     const int fours = (n - head) >> 2;
     const int4* wide = reinterpret_cast<const int4*>(from + head);
-    if (tid < head) mark(__ldg(from + tid));
-    if (tid < n - head - 4 * fours) mark(__ldg(from + head + 4 * fours + tid));
+    if (rank == 0 && tid < head) mark(__ldg(from + tid));
+    if (rank == 0 && tid < n - head - 4 * fours) mark(__ldg(from + head + 4 * fours + tid));
 #pragma unroll 4
-    for (int i = tid; i < fours; i += kSweepThreads) {
+    for (int i = rank * kSweepThreads + tid; i < fours; i += ranks * kSweepThreads) {
       const int4 t = __ldg(wide + i);
       mark(t.x);
       mark(t.y);
@@ -604,15 +610,25 @@ __global__ void __launch_bounds__(kSweepThreads) prompt_kernel(const __grid_cons
       mark(t.w);
     }
   }
-  if (odd && blockIdx.x == 0) set_status(P.status, KVQ_ERR_BOUNDS);
+  if (odd) set_status(P.status, KVQ_ERR_BOUNDS);
+  cluster.sync();
+  uint32_t* all = bits + words;
+  for (int i = tid; i < w1 - w0; i += kSweepThreads) {
+    uint32_t x = 0u;
+#pragma unroll 4
+    for (int r = 0; r < ranks; ++r) x |= *cluster.map_shared_rank(bits + w0 + i, r);
+    all[i] = x;
+  }
+  cluster_arrive();                                      // (this CTA has read the others')
   __syncthreads();
   // two tokens to a word (rows begin on one: the stride is even)
-  uint32_t* row = reinterpret_cast<uint32_t*>(P.counts + (long long)b * P.stride + v0);
+  uint32_t* row = reinterpret_cast<uint32_t*>(P.counts + (long long)b * P.stride) + 16 * (long long)w0;
 #pragma unroll 4
-  for (int i = tid; i < (v1 - v0 + 1) >> 1; i += kSweepThreads) {
-    const uint32_t two = bits[i >> 4] >> (2 * (i & 15)) & 3u;
-    if (two) row[i] |= (two & 1u) << 15 | (two & 2u) << 30;
+  for (int i = tid; i < 16 * (w1 - w0); i += kSweepThreads) {
+    const uint32_t two = all[i >> 4] >> (2 * (i & 15)) & 3u;
+    if (two) row[i] |= (two & 1u) << 15 | (two & 2u) << 30;   // (no bit stands behind the vocabulary)
   }
+  cluster_wait();
 }
 
 template <typename T, bool kCounts, bool kMask>
@@ -632,7 +648,7 @@ int launch_logits(LogitParams& P, cudaStream_t stream) {
     }
   }
   // CTAs of a row: slices of at most 13,000 tokens (51 KB: four CTAs of 256 threads on an SM; 64 trees of 16 nodes over 152 K tokens
-  // take 231 us so, 245 us in slices of 17 K and 384 threads, 254 in slices of 25 K and 512, 264 in slices of 9.5 K and 256), and more of them while the rows do not fill the SMs
+  // take 229 us so, 245 us in slices of 17 K and 384 threads, 254 in slices of 25 K and 512, 264 in slices of 9.5 K and 256), and more of them while the rows do not fill the SMs
   int c = std::max(1, (P.vocab + 12999) / 13000);
   while (c < kMaxCluster && c * (long long)P.n_rows < kSms && P.vocab / c > 2048) ++c;
   c = std::min(c, kMaxCluster);
@@ -681,11 +697,30 @@ extern "C" int kvq_launch_token_counts(const kvq_config* cfg, uint16_t* counts, 
                                        const int32_t* path, const int32_t* n_accept, const int32_t* next_token,
                                        int32_t* d_status, cudaStream_t stream) {
   const CountParams P{counts, count_stride, vocab, kind, cu_rows, token, path, n_accept, next_token, cfg->batch, n_rows, d_status};
-  // many long prompts: 16 of 64 K to 128 K tokens over 152 K (1.6 M rows) take 24 us swept and 36 one by one, the clearing of their
-  // counts among it; 16 of 16 K tokens 9.4 and 8.5, one of 128 K 16 and 14
-  if (kind == KVQ_COUNT_PROMPT && cfg->batch <= 65535 && n_rows >= kSweepRows && n_rows / cfg->batch >= vocab / 4) {
-    const dim3 grid((unsigned)((vocab + kSweepSlice - 1) / kSweepSlice), (unsigned)cfg->batch);
-    return launch_pdl(prompt_kernel, grid, dim3(kSweepThreads), 0, stream, P) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  // long prompts: 16 of 96 K tokens over 152 K take 11.7 us swept and 34.9 one by one, the clearing of their counts among it;
+  // 16 of 32 K 10.7 and 13.6, one of 128 K 8.5 and 14.0; 16 of 8 K 10.5 and 6.6, 64 of 8 K 20.8 and 14.5, one of 16 K 7.5 and 5.1,
+  // 64 of 1 K over a thousand 9.6 and 4.9
+  // (clusters of 16 CTAs: 14.8 for the 16 of 96 K, 7.6 for the one of 128 K)
+  if (kind == KVQ_COUNT_PROMPT && vocab <= KVQ_LOGITS_MAX_VOCAB && n_rows >= kSweepRows && n_rows / cfg->batch >= std::max(vocab / 6, kSweepEach)) {
+    const int words = (vocab + 31) / 32;
+    const size_t smem = 4 * ((size_t)words + (words + kSweepCtas - 1) / kSweepCtas);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KVQ_ERR_CUDA;
+    static std::mutex mu;
+    static unsigned long long attr_done = 0;
+    {
+      std::lock_guard<std::mutex> lock(mu);
+      if (!(attr_done & (1ull << dev))) {
+        if (cudaFuncSetAttribute(prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, KVQ_LOGITS_MAX_VOCAB / 8 + KVQ_LOGITS_MAX_VOCAB / 8 / kSweepCtas) !=
+            cudaSuccess)
+          return KVQ_ERR_CUDA;
+        attr_done |= 1ull << dev;
+      }
+    }
+    if ((long long)cfg->batch * kSweepCtas > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
+    return launch_pdl_cluster(prompt_kernel, kSweepCtas, dim3((unsigned)cfg->batch * kSweepCtas), dim3(kSweepThreads), smem, stream, P) == cudaSuccess
+               ? KVQ_OK
+               : KVQ_ERR_CUDA;
   }
   const long long warps = ((long long)n_rows + 32 * kPerLane - 1) / (32 * kPerLane) + (next_token ? (cfg->batch + 31) / 32 : 0);
   if (warps == 0) return KVQ_OK;

@@ -570,9 +570,9 @@ KVQ_API int kv_logits_probs(const kvq_config* cfg, const kvq_logit_rules* rules,
  *                     was counted when it was drawn), and with next_token [B] the token behind them (-1: none).
  * Equal tokens may come any number of times.  Tokens outside the vocabulary, nodes outside the tree and rows of no
  * sequence are left out, with KVQ_ERR_BOUNDS.  Of cfg only batch is used; n_rows is at most 2^30 (KVQ_ERR_UNSUPPORTED).
- * Execution: an atomic for each of a warp's different tokens.  Prompts of 2^19 rows or more, a quarter of the vocabulary a
- * sequence: CTAs take slices of the vocabulary and mark them in one sweep, without atomics: no other call may then
- * write the same rows of counts at the same time (elsewhere calls may, up to KVQ_COUNT_MOST / 2 tokens). */
+ * Execution: an atomic for each of a warp's different tokens; prompts of 2^16 rows or more, and on average 2^14 and a sixth of
+ * the vocabulary a sequence, in one sweep over the counts, without atomics.  No other call may write the same rows of counts at
+ * the same time. */
 KVQ_API int kv_token_counts(const kvq_config* cfg, uint16_t* counts, int64_t count_stride, int32_t vocab, int32_t kind,
                     const int32_t* cu_rows, const int32_t* token, int32_t n_rows, const int32_t* path,
                     const int32_t* n_accept, const int32_t* next_token, int32_t* d_status, void* stream);

@@ -304,7 +304,8 @@ def test_counts(vocab, n):
         assert int(status.item()) == 0 and np.array_equal(got.cpu().numpy().view(np.uint16), want)
 
 
-@pytest.mark.parametrize("vocab,n", [(1001, [200000, 0, 300001, 100003]), (70001, [524288 + 5]), (16384, [3, 400000, 200000])])
+@pytest.mark.parametrize("vocab,n", [(1001, [200000, 0, 300001, 100003]), (70001, [524288 + 5]), (16384, [3, 400000, 200000]), (524288, [100003]), (600001, [120000]),
+                                     (33, [70000, 6]), (131072, [65536 + 3, 0, 1])])
 def test_long_prompts(vocab, n):
     """Enough rows for the sweep: slices' ends, tokens outside the vocabulary, rows of no sequence, counts that are there already."""
     rng, batch = np.random.default_rng(6), len(n)
