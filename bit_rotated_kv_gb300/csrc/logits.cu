@@ -10,11 +10,11 @@
 // SM's shared memory, so a cluster of CTAs takes a row, a contiguous slice each, and they exchange one (maximum, sum) pair
 // through distributed shared memory.  At 6.8 TB/s an SM has about thirty instructions a token to spare in all.  Penalties
 // are therefore taken without branches (in a history of thousands nearly every warp meets a counted token: behind one they
-// took 64 instructions a token, and 64 trees of 16 nodes over 152 K 531 us instead of 229), and loads come in batches that
+// took 64 instructions a token, and 64 trees of 16 nodes over 152 K 531 us instead of 221), and loads come in batches that
 // are all on their way before the first is used.  Biases and the drafted path touch few tokens: the pass over the slice
 // does without them and the tokens concerned are computed again afterwards, by token, so that one that is in both lists is
 // right either way.
-// What it measured: those 64 x 16 rows 229 us (floor by bytes 106: the instructions of three passes and the waits between
+// What it measured: those 64 x 16 rows 221 us (floor by bytes 106: the instructions of three passes and the waits between
 // them bound it), 64 rows of 152 K 25 us (11.5), one row of 32 K 4.6 us (a launch and four waits one after another).
 #include <cooperative_groups.h>
 
@@ -141,6 +141,8 @@ __device__ __forceinline__ int sequences_before(const int32_t* cu_rows, int batc
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// (for a warp that has written nothing for the others: it need not wait for its stores; 228 us became 221 for 64 x 16 rows)
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <typename T, bool kCounts, bool kMask>
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(const __grid_constant
   const Raw* lw = reinterpret_cast<const Raw*>(l + v0);
   const bool l_wide = (reinterpret_cast<uintptr_t>(l) & (4 * sizeof(T) - 1)) == 0;
   pdl_trigger();
-  cluster_arrive();                                      // (waited for before a CTA writes to another)
+  cluster_arrive_relaxed();                              // (waited for before a CTA writes to another)
   pdl_wait();
   // the first logits and the rest of the slice are on their way while the row's sequence and its rules are found
   Raw r[kBatch];
@@ -410,7 +412,8 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(const __grid_constant
     // (a NaN or an infinity in the slice makes its sum a NaN)
     if (lane < ranks) *cluster.map_shared_rank(&shares[rank], lane) = Share{top, s, best, best < 0 || !(s < kInf)};
   }
-  cluster_arrive();
+  if (warp == 0) cluster_arrive();
+  else cluster_arrive_relaxed();
   cluster_wait();
   Share other{-kInf, 0.f, P.vocab, 0};
   if (lane < ranks) other = shares[lane];
@@ -647,8 +650,9 @@ int launch_logits(LogitParams& P, cudaStream_t stream) {
       attr_done |= 1ull << dev;
     }
   }
-  // CTAs of a row: slices of at most 13,000 tokens (51 KB: four CTAs of 256 threads on an SM; 64 trees of 16 nodes over 152 K tokens
-  // take 229 us so, 245 us in slices of 17 K and 384 threads, 254 in slices of 25 K and 512, 264 in slices of 9.5 K and 256), and more of them while the rows do not fill the SMs
+  // CTAs of a row: slices of at most 13,000 tokens (51 KB: four CTAs of 256 threads on an SM; 64 trees of 16 nodes over
+  // 152 K tokens took 231 us so, 245 us in slices of 17 K and 384 threads, 254 in slices of 25 K and 512, 264 in slices of
+  // 9.5 K and 256), and more of them while the rows do not fill the SMs
   int c = std::max(1, (P.vocab + 12999) / 13000);
   while (c < kMaxCluster && c * (long long)P.n_rows < kSms && P.vocab / c > 2048) ++c;
   c = std::min(c, kMaxCluster);
