@@ -510,6 +510,8 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // No TMEM is taken before the grid ahead has ended: its blocks could be waiting for that TMEM, and this one for them.
+  pdl_wait();
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(um_saddr(&tbase_sh)), "r"(kRtCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   // Only now may the next kernel begin: one that takes all of TMEM could otherwise have it before this CTA does, and
-  // wait for this grid.  For the same reason this kernel itself does not begin before the one ahead of it has ended.
+  // wait for this grid.
   pdl_trigger();
   const uint32_t tb = tbase_sh;
   const int c_lo = first_chunk(P, blockIdx.x), c_hi = first_chunk(P, blockIdx.x + 1);
@@ -802,8 +804,7 @@ int launch_rope_tc(RopeParams P, cudaStream_t stream) {
     }
   }
   const int ctas = (int)std::min(total, 2LL * kSms);
-  rope_tc_kernel<<<(unsigned)ctas, kRtThreads, kRtSmem, stream>>>(P);
-  return cudaGetLastError() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+  return launch_pdl(rope_tc_kernel, dim3((unsigned)ctas), dim3(kRtThreads), (size_t)kRtSmem, stream, P) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 }  // namespace kvq
