@@ -260,7 +260,7 @@ extern "C" int kvq_launch_rope(const kvq_config* cfg, const kvq_transform* tr, c
   const long long cslots = 2LL * kSms * 16;
   R.rpw = (int)(copies > cslots ? std::min((copies + cslots - 1) / cslots, (long long)kMaxCopies) : 1);
   R.warp_total = (int)((copies + R.rpw - 1) / R.rpw);
-  if (pairs >= kRopeTcPairs) {
+  if (pairs >= (had ? kRopeTcPairsHad : kRopeTcPairs)) {
     // the copies on their own, then the products on the tensor cores
     if (R.warp_total > 0 &&
         launch_pdl(rope_copy_kernel, dim3((unsigned)((R.warp_total + kRopeWarps - 1) / kRopeWarps)), dim3(kRopeThreads), 0, stream, P) !=

@@ -20,11 +20,14 @@
 // place rows, one issues the MMAs, four write results out through the shared memory that the rows came from, a row's 256
 // bytes at a time, two ask for rows, one finds out where they go.
 //
-// That chunk of 16 x 2048 tokens takes 215 us with its values' copies, 190 without (3.5 TB/s).  What bounds it are the
-// operations of placing rows: the schedulers issue in 58% of the clocks, and a CTA's chunk of 64 rows takes 5 K
-// clocks, 3.5 K of them from its rows to the buffer; DRAM is busy 36%, the tensor cores 28%.  What was tried: rows kept in registers a chunk
-// ahead with three buffers 267 us; bulk copies of rows by one warp 289; 96 registers for those who place and 40, 24 for
-// the others 276.
+// A call of a chunk or less for each SM takes 7 us, half of it the matrix's way into TMEM (through shared memory, asked for before
+// the grid ahead has ended).
+//
+// That chunk of 16 x 2048 tokens takes 208 us with its values' copies, 183 without (3.7 TB/s).  What bounds it are the
+// operations of placing rows: the schedulers issue in 62% of the clocks, the shared-memory pipe is busy 65%, and a CTA's
+// chunk of 64 rows takes 4.6 K clocks, 3.5 K of them from its rows to the buffer; DRAM is busy 41%, the tensor cores 30%.  What
+// was tried: rows kept in registers a chunk ahead with three buffers 267 us against 217; bulk copies of rows by one warp 289,
+// and 96 registers for those who place and 40, 24 for the others 276, against 248.
 #include "rope.cuh"
 #include "tc.cuh"
 
@@ -151,11 +154,11 @@ __device__ __forceinline__ Place place_of(const RopeParams& P, int chunk) {
   return w;
 }
 
-// The first chunk of a CTA.  Where CTAs have many chunks (sixteen on average), those whose rows share a token count kCostSame, others, which
-// come in shorter pieces and with a sine and cosine each, kCostOwn, and the grid's first half gets kShare / 32: of the two CTAs on an
-// SM the first comes to issue more often.  (16 x 2048 tokens, 40 heads: 239 us by chunks alone, 230 by 7 : 8 in
-// halves, 215 so.)  Where
-// they have few, a chunk more is what counts (3 x 777 tokens: 25.5 us by chunks, 28.4 so).
+// The first chunk of a CTA.  Where CTAs have many chunks (sixteen on average), those whose rows share a token count
+// kCostSame, others, which come in shorter pieces and with a sine and cosine each, kCostOwn, and the grid's first half gets
+// kShare / 32: of the two CTAs on an SM the first comes to issue more often.  (16 x 2048 tokens, 40 heads: 239 us by chunks
+// alone, 230 by 7 : 8 in halves, 215 so.)  Where they have few, a chunk more is what counts (3 x 777 tokens: 25.5 us by
+// chunks, 28.4 so).
 constexpr int kCostSame = 7, kCostOwn = 8, kShare = 17;
 __device__ __forceinline__ int first_chunk(const RopeParams& P, int cta) {
   if (P.r.dense_total < 16 * 2 * kSms) return (int)((long long)P.r.dense_total * cta / gridDim.x);
@@ -447,16 +450,32 @@ __device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, co
   else place_rows<kMode, 0>(P, g, L, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
 }
 
-// Half of a matrix row (row: its 64 entries; none: row i of the Walsh-Hadamard matrix) as hi and lo into TMEM.
-__device__ __forceinline__ void split_matrix(const float* row, int i, int part, float up, uint32_t taddr) {
+// A matrix on its way to TMEM lies where rows go (64 KB: all of it), 16-byte piece c of row i so that the lanes of a warp,
+// a row each, read from different banks.  (Lanes that read their rows from global memory, 16 of each 512 bytes at a time,
+// took 10 to 16 K clocks; 5 K so.  3 x 777 tokens: 25.6 us, now 16.5.)
+static_assert(kRtXBuf * 2 == kHeadDim * kHeadDim * 4, "a matrix fills the rows' buffers");
+__device__ __forceinline__ uint32_t mat_at(int i, int c) { return 512u * (uint32_t)i + 16u * (uint32_t)(c ^ (i & 7)); }
+__device__ __forceinline__ void ask_matrix(const float* mat, uint32_t mat_s, int warp, int lane) {
+#pragma unroll 4
+  for (int j = 0; j < kHeadDim / kRtWarps; ++j) {
+    const int i = warp * (kHeadDim / kRtWarps) + j;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(mat_s + mat_at(i, lane)), "l"(mat + (size_t)i * kHeadDim + 4 * lane) : "memory");
+  }
+}
+__device__ __forceinline__ float4 mat_v4(uint32_t mat_s, int i, int c) {
+  const uint4 x = lds_v4(mat_s + mat_at(i, c));
+  return make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w));
+}
+// Half of row i of a matrix (had: of the Walsh-Hadamard matrix) as hi and lo into TMEM.
+__device__ __forceinline__ void split_matrix(bool had, uint32_t mat_s, int i, int part, float up, uint32_t taddr) {
 #pragma unroll 1
   for (int blk = 0; blk < 4; ++blk) {
     uint32_t h[8], l[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float t[4];
-      if (row) {
-        const float4 t4 = __ldg(reinterpret_cast<const float4*>(row) + 4 * blk + j);
+      if (!had) {
+        const float4 t4 = mat_v4(mat_s, i, 16 * part + 4 * blk + j);
         t[0] = t4.x * up;
         t[1] = t4.y * up;
         t[2] = t4.z * up;
@@ -478,12 +497,12 @@ __device__ __forceinline__ void split_matrix(const float* row, int i, int part, 
   }
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// The largest exponent field of 64 entries.
-__device__ __forceinline__ uint32_t top_exponent(const float* row) {
+// The largest exponent field of half a row's entries.
+__device__ __forceinline__ uint32_t top_exponent(uint32_t mat_s, int i, int part) {
   uint32_t top = 0;
 #pragma unroll 4
   for (int j = 0; j < 16; ++j) {
-    const float4 t = __ldg(reinterpret_cast<const float4*>(row) + j);
+    const float4 t = mat_v4(mat_s, i, 16 * part + j);
     top = max(max(top, __float_as_uint(fabsf(t.x))), max(__float_as_uint(fabsf(t.y)), max(__float_as_uint(fabsf(t.z)), __float_as_uint(fabsf(t.w)))));
   }
   return top >> 23;
@@ -510,6 +529,12 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  const int c_lo = first_chunk(P, blockIdx.x), c_hi = first_chunk(P, blockIdx.x + 1);
+  const int total = c_hi - c_lo;
+  if (warp < kRtWarps && total > 0) {                    // (matrices do not come from the grid ahead)
+    const Place w = place_of(P, c_lo);
+    if (P.r.t[w.tt].mode == ROT_DENSE) ask_matrix(P.r.t[w.tt].mat + (size_t)w.mh * kHeadDim * kHeadDim, sb, warp, lane);
+  }
   // No TMEM is taken before the grid ahead has ended: its blocks could be waiting for that TMEM, and this one for them.
   pdl_wait();
   if (warp == 0) {
@@ -523,8 +548,6 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
   // wait for this grid.
   pdl_trigger();
   const uint32_t tb = tbase_sh;
-  const int c_lo = first_chunk(P, blockIdx.x), c_hi = first_chunk(P, blockIdx.x + 1);
-  const int total = c_hi - c_lo;
   const int q = warp & 3;
   const uint32_t tlane = (uint32_t)(32 * q) << 16;       // this warp's TMEM lanes
 
@@ -681,18 +704,22 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
       reinterpret_cast<uint64_t*>(sm + kRtFreq)[freq_slot(P.interleaved, tid)] = tid < P.half_rot ? __ldg(P.freq + tid) : 0ull;
 
     // ---- a matrix: T hi and lo into TMEM, the channels' weights, the lanes' pairs ----
-    auto set_up = [&](const Place& w) {
+    auto set_up = [&](const Place& w, bool first) {
       const RotTensor& T = P.r.t[w.tt];
-      const float* trow = T.mat + ((size_t)w.mh * kHeadDim + i) * kHeadDim + 64 * part;
       const bool had = T.mode == ROT_WHT;
       const bool turned = P.rpos[w.tt] != nullptr;
-      if (!had) exch[128 * part + i] = top_exponent(trow);
+      if (!had && !first) ask_matrix(T.mat + (size_t)w.mh * kHeadDim * kHeadDim, sb, warp, lane);
       // weights: float32, the first halves of all vectors of eight, then the second
       const bool norm = P.norm[w.tt] != nullptr, weighted = norm || (turned && P.scale != 1.f);
       if (part == 0) {
         float x = norm ? __ldg(P.norm[w.tt] + i) : 1.f;
         if (turned && i < 2 * P.half_rot) x *= P.scale;
         reinterpret_cast<float*>(sm + kRtNorm)[((i >> 2) & 1) * 64 + (i >> 3) * 4 + (i & 3)] = x;
+      }
+      if (!had) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        rt_sync(kBarPlace, kRtWarps);
+        exch[128 * part + i] = top_exponent(sb, i, part);
       }
       rt_sync(kBarPlace, kRtWarps);
       // the matrix's power of two; a row's own where it would lose bits under that one
@@ -714,7 +741,7 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
       }
       if (tid == 0) uneven_sh = uneven;
       const float t_back = had ? kInvSqrtDim : uneven ? 1.f : pow2(-k);
-      split_matrix(had ? nullptr : trow, i, part, pow2(k), tb + tlane);
+      split_matrix(had, sb, i, part, pow2(k), tb + tlane);
       // which channels a lane holds
       mode = !turned ? kNone : P.interleaved ? kInter : P.half_rot % 8 == 0 ? kHalf : kAny;
       L.va = sub;
@@ -751,7 +778,7 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
       for (const int want = fresh ? n : n - 1; freed < want; ++freed) rt_wait_use(bar_free, freed, &abort_sh);
       if (fresh) {
         tc_fence_after();
-        set_up(w);
+        set_up(w, n == 0);
       }
       rt_wait_use(bar_raw, n, &abort_sh);
       const uint32_t xb = sb + (uint32_t)(s * kRtXBuf), raw = sb + (uint32_t)(kRtRaw + s * kRtRawBuf);

@@ -498,7 +498,7 @@ KVQ_API int kvq_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling,
  * float32 holds, gets a row that is not finite, and KVQ_ERR_NONFINITE (copied values aside).
  * rope NULL: no norm and no rotation (q_pos may then be NULL).
  * Of cfg the heads, batch, s_sink and ring_cap are used.
- * Execution: fewer than 2048 (row, head) pairs that have a matrix run on the CUDA cores, a slice of a matrix to a CTA;
+ * Execution: fewer than 896 (row, head) pairs that have a matrix (Hadamard: 1280) run on the CUDA cores, a slice of a matrix to a CTA;
  * larger calls on the tensor cores, both operands as pairs of fp16 under powers of two, values that are copied in a
  * launch before.  The two round differently.
  * Source: [WUSH] inference algorithm and [OScaR] algorithm, key and query processing (the transform follows RoPE);

@@ -127,6 +127,12 @@ def test_prefill_sizes(rows, hq, hkv, kind, tv, layout, rot, norm):
     Call(rows, hq, hkv, kind, tv, layout, rot, norm, gap=8).run().check()
 
 
+# (the sizes at which calls go to the tensor cores: 12 pairs a row, with Hadamard matrices 10)
+@pytest.mark.parametrize("kind,rows", [("orthogonal", 74), ("invertible", 75), ("hadamard", 127), ("hadamard", 128), ("orthogonal", 160)])
+def test_sizes_about_the_choice(kind, rows):
+    Call(rows, kind=kind, tv=kind != "hadamard", rot=96, layout=rows % 2).run().check()
+
+
 # (the sizes from which on runs of work differ in length: no pair left out at either end)
 @pytest.mark.parametrize("rows,hq,hkv,tv", [(7801, 32, 8, False), (7800, 32, 8, False), (155_701, 1, 1, True), (20_011, 8, 8, False)])
 def test_long_prefill(rows, hq, hkv, tv):
