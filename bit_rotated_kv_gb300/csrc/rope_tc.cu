@@ -466,24 +466,30 @@ __device__ __forceinline__ float4 mat_v4(uint32_t mat_s, int i, int c) {
   const uint4 x = lds_v4(mat_s + mat_at(i, c));
   return make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w));
 }
-// Half of row i of a matrix (had: of the Walsh-Hadamard matrix) as hi and lo into TMEM.
-__device__ __forceinline__ void split_matrix(bool had, uint32_t mat_s, int i, int part, float up, uint32_t taddr) {
+// Half of row i of the Walsh-Hadamard matrix into TMEM: entry j is -1 where i & j has an odd number of bits (no lo).
+__device__ __forceinline__ void put_hadamard(int i, int part, uint32_t taddr) {
+  uint32_t odd = 0u;                                     // of j's lowest four bits
+#pragma unroll
+  for (int e = 0; e < 16; ++e) odd |= (uint32_t)(__popc(i & e) & 1) << e;
+#pragma unroll 1
+  for (int blk = 0; blk < 4; ++blk) {
+    const uint32_t o = __popc(i & (64 * part + 16 * blk)) & 1 ? ~odd : odd;
+    uint32_t h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = 0x3c003c00u | ((o >> (2 * j)) & 1u) << 15 | ((o >> (2 * j + 1)) & 1u) << 31;
+    tmem_st8(taddr + 32u * (uint32_t)part + 8u * (uint32_t)blk, h);
+  }
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// Half of row i of a matrix as hi and lo into TMEM.
+__device__ __forceinline__ void split_matrix(uint32_t mat_s, int i, int part, float up, uint32_t taddr) {
 #pragma unroll 1
   for (int blk = 0; blk < 4; ++blk) {
     uint32_t h[8], l[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float t[4];
-      if (!had) {
-        const float4 t4 = mat_v4(mat_s, i, 16 * part + 4 * blk + j);
-        t[0] = t4.x * up;
-        t[1] = t4.y * up;
-        t[2] = t4.z * up;
-        t[3] = t4.w * up;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] = hadamard_sign(i, 64 * part + 16 * blk + 4 * j + e);
-      }
+      const float4 t4 = mat_v4(mat_s, i, 16 * part + 4 * blk + j);
+      const float t[4] = {t4.x * up, t4.y * up, t4.z * up, t4.w * up};
       float y[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = lead11(t[e]);
@@ -741,7 +747,8 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
       }
       if (tid == 0) uneven_sh = uneven;
       const float t_back = had ? kInvSqrtDim : uneven ? 1.f : pow2(-k);
-      split_matrix(had, sb, i, part, pow2(k), tb + tlane);
+      if (had) put_hadamard(i, part, tb + tlane);
+      else split_matrix(sb, i, part, pow2(k), tb + tlane);
       // which channels a lane holds
       mode = !turned ? kNone : P.interleaved ? kInter : P.half_rot % 8 == 0 ? kHalf : kAny;
       L.va = sub;
