@@ -317,3 +317,27 @@ def test_a_call_behind_it():
     kvq.kv_rope_qk(a.cfg, a.tr, None, a.q_out, again, None, None, None, None, None, None, a.cache, a.status)
     torch.cuda.synchronize()
     assert torch.equal(first, again)
+
+
+@pytest.mark.parametrize("rows", [4, 100, 3001])
+def test_matrices_written_just_before(rows):
+    """A call sees what the stream wrote into the matrices just before it."""
+    a, b = Call(rows, kind="invertible", tv=True, seed=1), Call(rows, kind="invertible", tv=True, seed=2)
+    b.fused.copy_(a.fused)
+    own = [[t.clone() for t in (z.tr.t_k, z.tr.t_k_inv_t, z.tr.t_v)] for z in (a, b)]
+    a.run()
+    b.rope = a.rope
+    b.run()
+    want = [(z.q_out.clone(), z.cache.ring_k.clone(), z.cache.ring_v.clone()) for z in (a, b)]
+    assert not torch.equal(want[0][0], want[1][0])
+    seq, pos = _i32(a.seq), _i32(a.pos)
+    torch.cuda.synchronize()
+    got = []
+    for i in range(12):
+        for t, w in zip((a.tr.t_k, a.tr.t_k_inv_t, a.tr.t_v), own[i % 2], strict=True):
+            t.copy_(w)
+        kvq.kv_rope_qk(a.cfg, a.tr, a.rope, a.q, a.q_out, pos, a.k, a.v, seq, pos, None, a.cache, a.status)
+        got.append((a.q_out.clone(), a.cache.ring_k.clone(), a.cache.ring_v.clone()))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(g, want[i % 2], strict=True)), i
