@@ -9,7 +9,8 @@
 // This file: the kernel for few rows, on the CUDA cores (rope_tc.cu: the others).  A CTA takes a slice of 32 outputs of one
 // matrix and a chunk of the (row, head) pairs that share it: a whole matrix to a CTA would leave most SMs without
 // one at a single token (8 kv heads, 3 matrices each), and its 64 KB would be the longest wait of the call.  The
-// four slices of a pair each place its row (norm and rotation), which costs less than passing it on would.
+// four slices of a pair each place its row (norm and rotation), which costs less than passing it on would.  Latency
+// bounds it (launch, matrix slice, row, destination, one after another): one token of 32 + 8 + 8 heads 3.5 us, sixteen 5.2.
 #include "rope.cuh"
 
 #include <algorithm>
@@ -198,7 +199,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
   }
 }
 
-// The copies beside products on the tensor cores.
+// The copies beside products on the tensor cores, before them (behind them took as long).  16 x 2048 tokens of 8 heads, 67 MB
+// read and as many written: 25 us (5.4 TB/s).
 __global__ void __launch_bounds__(kRopeThreads, 10) rope_copy_kernel(const __grid_constant__ RopeParams P) {
   pdl_trigger();
   pdl_wait();
