@@ -188,7 +188,10 @@ struct Seg {
   bool norm;
   bool weighted;             // channels have weights: the norm's, the rotation's factor
   int grow;                  // what weights and rotation may add to a channel's exponent
+  bool turned;
   float up, back;            // with a norm: the power of two that rows take
+  float least;               // with a norm: rows whose squares sum to less take a power of two of their own (size_rows)
+  int most;                  // what a row's power of two may be (with the matrix's it is taken back by 2^-149 or more)
   float t_back;              // takes the matrix's power of two back (and a Hadamard matrix's 1/sqrt(128) in)
 };
 
@@ -262,33 +265,67 @@ struct Lane {
   uint32_t freq_at, freq_step;   // the first of its pairs in the table of frequencies, bytes to the next
 };
 
-// Places a slot's two rows: hi and lo into the chunk's buffer, the factor that goes with a row beside its destination.
-// kW: 0: as they are, 1: norm and weights, 2: weights without a norm.  kSame: the two rows are heads of one token.
-// Nothing branches, and pairs are the outer loop: the two rows' chains of operations run side by side.
-template <int kMode, int kW, bool kSame>
-__device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, const Lane& L, int left, uint32_t pos_s, uint32_t raw, uint64_t* bar_read,
-                                           uint32_t xb, uint32_t norm_s, uint32_t freq_s, uint32_t fac_s) {
-  int pos[2] = {0, 0};
-  if (kMode != kNone) {
-    const uint2 x = lds_v2(pos_s + 4u * L.r0);
-    pos[0] = (int)x.x;
-    pos[1] = (int)x.y;
-  }
-  uint32_t wa[2][4], wb[2][4];
+// The largest of eight lanes' numbers, which share a row.
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// The powers of two of a slot's two rows from their channels as they are after norm and weights.  The one that all rows of a
+// normed head share (Seg) is that of the largest numbers such a row can hold: it suits rows whose mean square is not far below
+// the norm's epsilon, and costs one product a channel.  Below, 1 / sqrt(eps) leaves a row as small as it came, and under the shared
+// power hi and lo would lose its digits: 2^-24 where the row ends at 2^-24 or less.  Here the row's digits (bfloat16: exactly) are brought to
+// 1 .. 2 first, so that neither they nor their products with the weights vanish on the way, whatever their size.
+__device__ __forceinline__ void size_rows(const Seg& g, const Lane& L, uint32_t norm_s, const float (&r)[2], uint32_t (&wa)[2][4], uint32_t (&wb)[2][4],
+                                          float2 (&up)[2], float (&back)[2]) {
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const uint4 x = lds_v4(raw + 256u * (L.r0 + j) + 16u * L.va), y = lds_v4(raw + 256u * (L.r0 + j) + 16u * L.vb);
-    wa[j][0] = x.x, wa[j][1] = x.y, wa[j][2] = x.z, wa[j][3] = x.w;
-    wb[j][0] = y.x, wb[j][1] = y.y, wb[j][2] = y.z, wb[j][3] = y.w;
+    uint32_t t = 0u;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) t = __vmaxu2(t, __vmaxu2(wa[j][m] & 0x7fff7fffu, wb[j][m] & 0x7fff7fffu));
+    t = row_max(max(t & 0xffffu, t >> 16));
+    const int p = min(max(127 - (int)(t >> 7), -126), 126);
+    const uint32_t by = (uint32_t)(p + 127) << 7 | (uint32_t)(p + 127) << 23;
+    float top = 0.f;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {                        // (halves of va, then of vb)
+      const uint4 w = lds_v4(norm_s + 256u * (uint32_t)(h & 1) + 16u * (uint32_t)(h < 2 ? L.va : L.vb));
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t& x = h < 2 ? wa[j][2 * (h & 1) + e] : wb[j][2 * (h & 1) + e];
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(by));
+        top = fmaxf(top, fmaxf(fabsf(lo16(x) * __uint_as_float(e ? w.z : w.x)), fabsf(hi16(x) * __uint_as_float(e ? w.w : w.y))));
+      }
+    }
+    top = __uint_as_float(row_max(__float_as_uint(top)));
+    // y = x 2^-p r w, r = u 2^e with u in 1 .. 2: rows take u 2^k and are taken back by 2^(e - p - k).  No weight overflows under it
+    // (grow: the largest weight's exponent), nor does what takes the row back vanish
+    const int e = (int)(__float_as_uint(r[j]) >> 23) - 127;
+    int k = fit_pow2((int)(__float_as_uint(top) >> 23) + 1 + (g.turned ? 1 : 0));
+    k = max(min(k, min(125 - g.grow, g.most + e - p)), -126);
+    const float u = __uint_as_float((__float_as_uint(r[j]) & 0x007fffffu) | 0x3f800000u) * pow2(k);
+    if (r[j] > 0.f) {                                    // (a row that is not finite: no number comes back)
+      up[j] = make_float2(u, u);
+      back[j] = pow2(min(max(e - p - k, -126), 127)) * g.t_back;
+    }
   }
-  rt_arrive(bar_read, threadIdx.x & 31);                 // (the next rows but one may come)
+}
+
+// A slot's two rows: hi and lo into the chunk's buffer, the factor that goes with a row beside its destination.
+// kW: 0: as they are, 1: norm and weights, 2: weights without a norm, 3: norm and weights, every row under a power of two of its own.
+// kSame: the two rows are heads of one token.  Nothing branches, and pairs are the outer loop: the two rows' chains of operations run
+// side by side.  True where a row is too small for the power that it took (kW = 1).
+template <int kMode, int kW, bool kSame>
+__device__ __forceinline__ bool place_words(const RopeParams& P, const Seg& g, const Lane& L, int left, const int (&pos)[2], uint32_t (&wa)[2][4],
+                                            uint32_t (&wb)[2][4], uint32_t xb, uint32_t norm_s, uint32_t freq_s, uint32_t fac_s) {
   // the number that brings a row's channels below 2^15, the one that takes it back at the end
   float2 up[2];
   float back[2];
-  bool fine[2];
-  if (kW == 1) {
+  bool fine[2], small = false;
+  if (kW == 1 || kW == 3) {
     // |x| / rms(x) <= sqrt(128): the norm's own factor, and the weights' power of two
-    float ss[2];
+    float ss[2], r[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       float2 acc[2];
@@ -307,10 +344,12 @@ __device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, co
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       fine[j] = ss[j] <= 3.4e38f;
-      const float u = fine[j] ? rsqrtf(fmaf(ss[j], 1.0f / kHeadDim, P.eps)) * g.up : __int_as_float(0x7fffffff);
-      up[j] = make_float2(u, u);
+      r[j] = fine[j] ? rsqrtf(fmaf(ss[j], 1.0f / kHeadDim, P.eps)) : __int_as_float(0x7fffffff);
+      up[j] = make_float2(r[j] * g.up, r[j] * g.up);
       back[j] = g.back;
     }
+    if (kW == 3) size_rows(g, L, norm_s, r, wa, wb, up, back);
+    small = ss[0] < g.least || ss[1] < g.least;
   } else {
     uint32_t top[2];
 #pragma unroll
@@ -435,19 +474,62 @@ __device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, co
       if (!fine[j] && left > j) set_status(P.r.status, KVQ_ERR_NONFINITE);
     }
   }
+  return kW == 1 && small;
+}
+// A warp's rows again, from where they came from, each under a power of two of its own.
+template <int kMode>
+__device__ __noinline__ void place_again(const RopeParams& P, const Seg& g, Lane L, Place w, int left, int pos0, int pos1, uint32_t xb, uint32_t norm_s,
+                                         uint32_t freq_s, uint32_t fac_s) {
+  const RotTensor& T = P.r.t[w.tt];
+  const int pos[2] = {pos0, pos1};
+  uint32_t wa[2][4], wb[2][4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    int row, head;
+    tile_row(T, w.mh, min(w.c * kRtRows + L.r0 + j, T.rows * T.head_div - 1), row, head);   // (as ask_rows)
+    const uint4* src = reinterpret_cast<const uint4*>(rope_src(P, w.tt, row, head));
+    const uint4 x = __ldg(src + L.va), y = __ldg(src + L.vb);
+    wa[j][0] = x.x, wa[j][1] = x.y, wa[j][2] = x.z, wa[j][3] = x.w;
+    wb[j][0] = y.x, wb[j][1] = y.y, wb[j][2] = y.z, wb[j][3] = y.w;
+  }
+  __syncwarp();
+  place_words<kMode, 3, false>(P, g, L, left, pos, wa, wb, xb, norm_s, freq_s, fac_s);
+}
+// Places a slot's two rows.
+template <int kMode, int kW, bool kSame>
+__device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, const Lane& L, const Place& w, int left, uint32_t pos_s, uint32_t raw,
+                                           uint64_t* bar_read, uint32_t xb, uint32_t norm_s, uint32_t freq_s, uint32_t fac_s) {
+  int pos[2] = {0, 0};
+  if (kMode != kNone) {
+    const uint2 x = lds_v2(pos_s + 4u * L.r0);
+    pos[0] = (int)x.x;
+    pos[1] = (int)x.y;
+  }
+  uint32_t wa[2][4], wb[2][4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint4 x = lds_v4(raw + 256u * (L.r0 + j) + 16u * L.va), y = lds_v4(raw + 256u * (L.r0 + j) + 16u * L.vb);
+    wa[j][0] = x.x, wa[j][1] = x.y, wa[j][2] = x.z, wa[j][3] = x.w;
+    wb[j][0] = y.x, wb[j][1] = y.y, wb[j][2] = y.z, wb[j][3] = y.w;
+  }
+  rt_arrive(bar_read, threadIdx.x & 31);                 // (the next rows but one may come)
+  const bool small = place_words<kMode, kW, kSame>(P, g, L, left, pos, wa, wb, xb, norm_s, freq_s, fac_s);
+  // (the buffer that the rows came from may hold others by now.  A branch before the products, on the rows as they were read, kept the
+  // products from covering the sums' latency: 16 x 2048 tokens took 219 us instead of 209)
+  if (kW == 1 && __any_sync(0xffffffffu, small)) place_again<kMode>(P, g, L, w, left, pos[0], pos[1], xb, norm_s, freq_s, fac_s);
 }
 template <int kMode, int kW>
-__device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, const Lane& L, int left, uint32_t pos_s, uint32_t raw, uint64_t* bar_read,
-                                           uint32_t xb, uint32_t norm_s, uint32_t freq_s, uint32_t fac_s) {
-  if (kMode == kNone || g.same) place_rows<kMode, kW, true>(P, g, L, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
-  else place_rows<kMode, kW, false>(P, g, L, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
+__device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, const Lane& L, const Place& w, int left, uint32_t pos_s, uint32_t raw,
+                                           uint64_t* bar_read, uint32_t xb, uint32_t norm_s, uint32_t freq_s, uint32_t fac_s) {
+  if (kMode == kNone || g.same) place_rows<kMode, kW, true>(P, g, L, w, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
+  else place_rows<kMode, kW, false>(P, g, L, w, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
 }
 template <int kMode>
-__device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, const Lane& L, int left, uint32_t pos_s, uint32_t raw, uint64_t* bar_read,
-                                           uint32_t xb, uint32_t norm_s, uint32_t freq_s, uint32_t fac_s) {
-  if (g.norm) place_rows<kMode, 1>(P, g, L, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
-  else if (kMode != kNone && g.weighted) place_rows<kMode, 2>(P, g, L, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
-  else place_rows<kMode, 0>(P, g, L, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
+__device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, const Lane& L, const Place& w, int left, uint32_t pos_s, uint32_t raw,
+                                           uint64_t* bar_read, uint32_t xb, uint32_t norm_s, uint32_t freq_s, uint32_t fac_s) {
+  if (g.norm) place_rows<kMode, 1>(P, g, L, w, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
+  else if (kMode != kNone && g.weighted) place_rows<kMode, 2>(P, g, L, w, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
+  else place_rows<kMode, 0>(P, g, L, w, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
 }
 
 // A matrix on its way to TMEM lies where rows go (64 KB: all of it), 16-byte piece c of row i so that the lanes of a warp,
@@ -770,7 +852,10 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
       wtop = __reduce_max_sync(0xffffffffu, wtop);
       // the largest weight and the rotation's sqrt 2, by exponents, rounded up; after the norm rows are below 2^4
       const int grow = (weighted ? (int)(wtop >> 23) - 126 : 0) + (turned ? 1 : 0), kn = fit_pow2(130 + grow);
-      if (tid == 0) seg_sh = Seg{T.head_div > 1, norm, weighted, grow, pow2(kn), pow2(-kn) * t_back, t_back};
+      // (rms r < 1/2, r the norm's factor, where the squares sum to less than 128 eps / 3)
+      const float least = norm ? P.eps * (kHeadDim / 3.f) : 0.f;
+      const int most = min(126, 149 - (had ? 4 : uneven ? 0 : k));
+      if (tid == 0) seg_sh = Seg{T.head_div > 1, norm, weighted, grow, turned, pow2(kn), pow2(-kn) * t_back, least, most, t_back};
       rt_sync(kBarPlace, kRtWarps);
       L.at_a = (uint32_t)xs_offset(r0, 8 * L.va);
       L.at_b = (uint32_t)xs_offset(r0, 8 * L.vb);
@@ -791,10 +876,10 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
       const uint32_t xb = sb + (uint32_t)(s * kRtXBuf), raw = sb + (uint32_t)(kRtRaw + s * kRtRawBuf);
       const uint32_t fac = sb + (uint32_t)(kRtFac + s * kRtRows * 4), pos = sb + (uint32_t)(kRtPos + s * kRtRows * 4);
       const int left = P.r.t[w.tt].rows * P.r.t[w.tt].head_div - w.c * kRtRows - r0;
-      if (mode == kHalf) place_rows<kHalf>(P, g, L, left, pos, raw, bar_read + s, xb, norm_s, freq_s, fac);
-      else if (mode == kInter) place_rows<kInter>(P, g, L, left, pos, raw, bar_read + s, xb, norm_s, freq_s, fac);
-      else if (mode == kAny) place_rows<kAny>(P, g, L, left, pos, raw, bar_read + s, xb, norm_s, freq_s, fac);
-      else place_rows<kNone>(P, g, L, left, pos, raw, bar_read + s, xb, norm_s, freq_s, fac);
+      if (mode == kHalf) place_rows<kHalf>(P, g, L, w, left, pos, raw, bar_read + s, xb, norm_s, freq_s, fac);
+      else if (mode == kInter) place_rows<kInter>(P, g, L, w, left, pos, raw, bar_read + s, xb, norm_s, freq_s, fac);
+      else if (mode == kAny) place_rows<kAny>(P, g, L, w, left, pos, raw, bar_read + s, xb, norm_s, freq_s, fac);
+      else place_rows<kNone>(P, g, L, w, left, pos, raw, bar_read + s, xb, norm_s, freq_s, fac);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc_fence_before();
       rt_arrive(&bar_x[s], lane);
