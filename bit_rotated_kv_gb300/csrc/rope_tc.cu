@@ -189,6 +189,7 @@ struct Seg {
   bool weighted;             // channels have weights: the norm's, the rotation's factor
   int grow;                  // what weights and rotation may add to a channel's exponent
   bool turned;
+  bool wide;                 // weights so far apart, or so far from 1, that every row takes a power of two of its own
   float up, back;            // with a norm: the power of two that rows take
   float least;               // with a norm: rows whose squares sum to less take a power of two of their own (size_rows)
   int most;                  // what a row's power of two may be (with the matrix's it is taken back by 2^-149 or more)
@@ -274,17 +275,18 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
 
 // The powers of two of a slot's two rows from their channels as they are after norm and weights.  The one that all rows of a
 // normed head share (Seg) is that of the largest numbers such a row can hold: it suits rows whose mean square is not far below
-// the norm's epsilon, and costs one product a channel.  Below, 1 / sqrt(eps) leaves a row as small as it came, and under the shared
-// power hi and lo would lose its digits: 2^-24 where the row ends at 2^-24 or less.  Here the row's digits (bfloat16: exactly) are brought to
+// the norm's epsilon under weights that are not far apart, and costs one product a channel.  Elsewhere hi and lo would lose digits under it:
+// a row far below epsilon stays as small as it came, and one may have nothing where the large weights are.  Here the row's digits (bfloat16: exactly) are brought to
 // 1 .. 2 first, so that neither they nor their products with the weights vanish on the way, whatever their size.
 __device__ __forceinline__ void size_rows(const Seg& g, const Lane& L, uint32_t norm_s, const float (&r)[2], uint32_t (&wa)[2][4], uint32_t (&wb)[2][4],
-                                          float2 (&up)[2], float (&back)[2]) {
+                                          float2 (&up)[2], float (&back)[2], bool (&fine)[2]) {
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     uint32_t t = 0u;
 #pragma unroll
     for (int m = 0; m < 4; ++m) t = __vmaxu2(t, __vmaxu2(wa[j][m] & 0x7fff7fffu, wb[j][m] & 0x7fff7fffu));
     t = row_max(max(t & 0xffffu, t >> 16));
+    if (!g.norm) fine[j] = t < 0x7f80u;
     const int p = min(max(127 - (int)(t >> 7), -126), 126);
     const uint32_t by = (uint32_t)(p + 127) << 7 | (uint32_t)(p + 127) << 23;
     float top = 0.f;
@@ -313,7 +315,8 @@ __device__ __forceinline__ void size_rows(const Seg& g, const Lane& L, uint32_t 
 }
 
 // A slot's two rows: hi and lo into the chunk's buffer, the factor that goes with a row beside its destination.
-// kW: 0: as they are, 1: norm and weights, 2: weights without a norm, 3: norm and weights, every row under a power of two of its own.
+// kW: 0: as they are, 1: norm and weights, 2: weights without a norm, 3: weights, with or without a norm, every row under a power of two
+// of its own.
 // kSame: the two rows are heads of one token.  Nothing branches, and pairs are the outer loop: the two rows' chains of operations run
 // side by side.  True where a row is too small for the power that it took (kW = 1).
 template <int kMode, int kW, bool kSame>
@@ -344,11 +347,11 @@ __device__ __forceinline__ bool place_words(const RopeParams& P, const Seg& g, c
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       fine[j] = ss[j] <= 3.4e38f;
-      r[j] = fine[j] ? rsqrtf(fmaf(ss[j], 1.0f / kHeadDim, P.eps)) : __int_as_float(0x7fffffff);
+      r[j] = kW == 3 && !g.norm ? 1.f : fine[j] ? rsqrtf(fmaf(ss[j], 1.0f / kHeadDim, P.eps)) : __int_as_float(0x7fffffff);
       up[j] = make_float2(r[j] * g.up, r[j] * g.up);
       back[j] = g.back;
     }
-    if (kW == 3) size_rows(g, L, norm_s, r, wa, wb, up, back);
+    if (kW == 3) size_rows(g, L, norm_s, r, wa, wb, up, back, fine);
     small = ss[0] < g.least || ss[1] < g.least;
   } else {
     uint32_t top[2];
@@ -476,9 +479,9 @@ __device__ __forceinline__ bool place_words(const RopeParams& P, const Seg& g, c
   }
   return kW == 1 && small;
 }
-// A warp's rows again, from where they came from, each under a power of two of its own.
+// A slot's two rows from where they came from, each under a power of two of its own.
 template <int kMode>
-__device__ __noinline__ void place_again(const RopeParams& P, const Seg& g, Lane L, Place w, int left, int pos0, int pos1, uint32_t xb, uint32_t norm_s,
+__device__ __noinline__ void place_apart(const RopeParams& P, const Seg& g, Lane L, Place w, int left, int pos0, int pos1, uint32_t xb, uint32_t norm_s,
                                          uint32_t freq_s, uint32_t fac_s) {
   const RotTensor& T = P.r.t[w.tt];
   const int pos[2] = {pos0, pos1};
@@ -505,18 +508,25 @@ __device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, co
     pos[0] = (int)x.x;
     pos[1] = (int)x.y;
   }
-  uint32_t wa[2][4], wb[2][4];
+  bool apart = kW == 1 && g.wide;                        // (that of weights without a norm comes here too)
+  if (!apart) {
+    uint32_t wa[2][4], wb[2][4];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const uint4 x = lds_v4(raw + 256u * (L.r0 + j) + 16u * L.va), y = lds_v4(raw + 256u * (L.r0 + j) + 16u * L.vb);
-    wa[j][0] = x.x, wa[j][1] = x.y, wa[j][2] = x.z, wa[j][3] = x.w;
-    wb[j][0] = y.x, wb[j][1] = y.y, wb[j][2] = y.z, wb[j][3] = y.w;
+    for (int j = 0; j < 2; ++j) {
+      const uint4 x = lds_v4(raw + 256u * (L.r0 + j) + 16u * L.va), y = lds_v4(raw + 256u * (L.r0 + j) + 16u * L.vb);
+      wa[j][0] = x.x, wa[j][1] = x.y, wa[j][2] = x.z, wa[j][3] = x.w;
+      wb[j][0] = y.x, wb[j][1] = y.y, wb[j][2] = y.z, wb[j][3] = y.w;
+    }
+    rt_arrive(bar_read, threadIdx.x & 31);               // (the next rows but one may come)
+    const bool small = place_words<kMode, kW, kSame>(P, g, L, left, pos, wa, wb, xb, norm_s, freq_s, fac_s);
+    apart = kW == 1 && __any_sync(0xffffffffu, small);
+  } else {
+    rt_arrive(bar_read, threadIdx.x & 31);
   }
-  rt_arrive(bar_read, threadIdx.x & 31);                 // (the next rows but one may come)
-  const bool small = place_words<kMode, kW, kSame>(P, g, L, left, pos, wa, wb, xb, norm_s, freq_s, fac_s);
-  // (the buffer that the rows came from may hold others by now.  A branch before the products, on the rows as they were read, kept the
-  // products from covering the sums' latency: 16 x 2048 tokens took 219 us instead of 209)
-  if (kW == 1 && __any_sync(0xffffffffu, small)) place_again<kMode>(P, g, L, w, left, pos[0], pos[1], xb, norm_s, freq_s, fac_s);
+  // (Behind the products, and from global memory: the buffer that the rows came from may hold others by now, and a branch between the sums of
+  // squares and the products kept these from covering those, 219 us for 16 x 2048 tokens instead of 210.  With the weights' choice
+  // it is 213; 321 where the weights are far apart, 419 where all rows are small.)
+  if (apart) place_apart<kMode>(P, g, L, w, left, pos[0], pos[1], xb, norm_s, freq_s, fac_s);
 }
 template <int kMode, int kW>
 __device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, const Lane& L, const Place& w, int left, uint32_t pos_s, uint32_t raw,
@@ -527,7 +537,7 @@ __device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, co
 template <int kMode>
 __device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, const Lane& L, const Place& w, int left, uint32_t pos_s, uint32_t raw,
                                            uint64_t* bar_read, uint32_t xb, uint32_t norm_s, uint32_t freq_s, uint32_t fac_s) {
-  if (g.norm) place_rows<kMode, 1>(P, g, L, w, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
+  if (g.norm || g.wide) place_rows<kMode, 1>(P, g, L, w, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
   else if (kMode != kNone && g.weighted) place_rows<kMode, 2>(P, g, L, w, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
   else place_rows<kMode, 0>(P, g, L, w, left, pos_s, raw, bar_read, xb, norm_s, freq_s, fac_s);
 }
@@ -846,16 +856,26 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
           L.freq_step = 0u;
         }
       }
-      uint32_t wtop = 0;
+      uint32_t wtop = 0, wlow = ~0u;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) wtop = max(wtop, __float_as_uint(fabsf(reinterpret_cast<const float*>(sm + kRtNorm)[4 * lane + j])));
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t x = __float_as_uint(fabsf(reinterpret_cast<const float*>(sm + kRtNorm)[4 * lane + j]));
+        wtop = max(wtop, x);
+        wlow = min(wlow, x);
+      }
       wtop = __reduce_max_sync(0xffffffffu, wtop);
+      wlow = __reduce_min_sync(0xffffffffu, wlow);
       // the largest weight and the rotation's sqrt 2, by exponents, rounded up; after the norm rows are below 2^4
       const int grow = (weighted ? (int)(wtop >> 23) - 126 : 0) + (turned ? 1 : 0), kn = fit_pow2(130 + grow);
       // (rms r < 1/2, r the norm's factor, where the squares sum to less than 128 eps / 3)
       const float least = norm ? P.eps * (kHeadDim / 3.f) : 0.f;
-      const int most = min(126, 149 - (had ? 4 : uneven ? 0 : k));
-      if (tid == 0) seg_sh = Seg{T.head_div > 1, norm, weighted, grow, turned, pow2(kn), pow2(-kn) * t_back, least, most, t_back};
+      const int k_t = had ? 4 : uneven ? 0 : k, most = min(126, 149 - k_t);
+      // One power of two for all rows (or that of a row's largest channel before its weight) brings a row's largest channel to 2^-2 or more,
+      // 2^-22 of which hi and lo keep, where the smallest weight is not 2^10 below the largest, and no product overflows or vanishes where
+      // the largest is near 1.
+      const int top_at = (int)(wtop >> 23);
+      const bool wide = weighted && (top_at - (int)(wlow >> 23) > 9 || top_at < 97 || top_at > 187 || kn > most);
+      if (tid == 0) seg_sh = Seg{T.head_div > 1, norm, weighted, grow, turned, wide, pow2(kn), pow2(-kn) * t_back, least, most, t_back};
       rt_sync(kBarPlace, kRtWarps);
       L.at_a = (uint32_t)xs_offset(r0, 8 * L.va);
       L.at_b = (uint32_t)xs_offset(r0, 8 * L.vb);

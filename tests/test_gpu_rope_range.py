@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_rope import Call
+from tests.test_gpu_rope import D, Call
 
 pytestmark = pytest.mark.gpu
 
@@ -14,6 +14,12 @@ pytestmark = pytest.mark.gpu
 def _sized(c, exponents):
     """Row r of the projection times 2^exponents[r] (exact: bfloat16 keeps its digits)."""
     c.fused.mul_(torch.from_numpy(2.0 ** np.asarray(exponents, np.float64))[:, None].cuda())
+    return c
+
+
+def _weights(c, wq, wk):
+    c.wq, c.wk = (np.asarray(w, np.float32) for w in (wq, wk))
+    c.rope.q_norm, c.rope.k_norm = (torch.from_numpy(w).cuda() for w in (c.wq, c.wk))
     return c
 
 
@@ -41,4 +47,46 @@ def test_epsilons(rows, eps):
     c = Call(rows, 16, 4)
     c.eps = c.rope.norm_eps = eps
     _sized(c, -(np.arange(rows) % 5 * 25.0))
+    c.run().check()
+
+
+# ---- norm weights ----------------------------------------------------------------------------------
+@pytest.mark.parametrize("rows", [5, 403])
+@pytest.mark.parametrize("rot", [128, 64])
+def test_norm_weights_of_zero(rows, rot):
+    """Weights that are all zero (rows of zeros, not NaN), beside ordinary ones."""
+    c = _weights(Call(rows, 16, 4, rot=rot, size=0.01), np.zeros(D), np.linspace(-1, 1, D))
+    c.run().check()
+    assert not bool(c.q_out[:rows].any())
+
+
+@pytest.mark.parametrize("rows", [5, 403])
+@pytest.mark.parametrize("layout,rot", [(0, 128), (1, 128), (0, 64), (1, 64), (0, 6), (0, 0)])
+@pytest.mark.parametrize("low,high", [(-12, 0), (-40, 20), (20, 60), (-90, -80), (-125, -120)])
+@pytest.mark.parametrize("size", [0, -20])
+def test_norm_weights_of_any_size(rows, layout, rot, low, high, size):
+    """Weights that lie far apart, far above 1 or far below: the largest ones at channels where some rows have nothing."""
+    c = Call(rows, 16, 4, layout=layout, rot=rot)
+    rng = np.random.default_rng(2)
+    w = [rng.choice([-1.0, 1.0], D) * 2.0 ** rng.uniform(low, high, D) for _ in range(2)]
+    big = np.zeros((rows, 24, D), bool)
+    for heads, x in ((slice(0, 16), w[0]), (slice(16, 20), w[1])):
+        big[:, heads] = np.abs(x) > 2.0 ** (low + 2)
+    big[::2] = False
+    c.fused.masked_fill_(torch.from_numpy(big.reshape(rows, -1)).cuda(), 0.0)
+    _sized(_weights(c, *w), np.full(rows, float(size)))
+    c.run().check()
+
+
+@pytest.mark.parametrize("rows", [5, 403])
+@pytest.mark.parametrize("layout,rot", [(0, 64), (1, 64), (0, 126), (1, 30)])
+@pytest.mark.parametrize("scale", [2.0**-40, 0.0, 2.0**40])
+@pytest.mark.parametrize("size", [-90, 0, 60])
+def test_factors_far_from_the_other_channels(rows, layout, rot, scale, size):
+    """The rotated channels' factor takes them far from the others; rows that hold the one kind alone, or the other, or both."""
+    c = Call(rows, 16, 4, "orthogonal", layout=layout, rot=rot, norm=False, scale=scale, seed=4)
+    heads = c.fused.unflatten(1, (24, D))
+    heads[0::3, :20, rot:] = 0
+    heads[1::3, :20, :rot] = 0
+    _sized(c, np.full(rows, float(size)))
     c.run().check()
