@@ -368,7 +368,7 @@ __device__ __forceinline__ bool place_words(const RopeParams& P, const Seg& g, c
       for (int j = 0; j < 2; ++j) top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int k = fit_pow2((int)(top[j] >> 7) + g.grow);
+      const int k = min(fit_pow2((int)(top[j] >> 7) + g.grow), g.most);
       fine[j] = top[j] < 0x7f80u;
       up[j] = make_float2(pow2(k), pow2(k));
       back[j] = pow2(-k) * g.t_back;

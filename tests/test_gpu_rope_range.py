@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_rope import D, Call
+from tests.test_gpu_rope import D, Call, _f64
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,16 @@ def test_factors_far_from_the_other_channels(rows, layout, rot, scale, size):
     heads[1::3, :20, :rot] = 0
     _sized(c, np.full(rows, float(size)))
     c.run().check()
+
+
+# ---- rows and matrices at the ends of the range ----------------------------------------------------
+@pytest.mark.parametrize("rows", [5, 403])
+@pytest.mark.parametrize("x,t", [(-64, -60), (-100, -20), (-20, -96), (40, -100), (-100, 40), (90, -110)])
+def test_small_products(rows, x, t):
+    """Rows and matrices whose products come near the smallest numbers, or whose sizes make up for each other."""
+    c = _sized(Call(rows, 16, 4, norm=False, rot=64), np.full(rows, float(x)))
+    for m in (c.tr.t_k, c.tr.t_k_inv_t, c.tr.t_v):
+        m.mul_(2.0**t)
+    c.tk, c.tkit, c.tv = (_f64(m) for m in (c.tr.t_k, c.tr.t_k_inv_t, c.tr.t_v))
+    c.run().check()
+    assert bool(c.q_out[:rows].any(-1).all())
