@@ -25,7 +25,7 @@ constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kMaxRows = 16;                      // pairs of a chunk
 constexpr int kMaxCopies = 8;                     // rows a warp copies
 
-// One warp places a row: norm and rotation, float32, into shared memory.  False when the row is not finite.
+// One warp places a row: norm and rotation, float32, into shared memory.  False when the row or a weight is not finite.
 __device__ __forceinline__ bool place_row(const RopeParams& P, const float* w, bool turned, uint2 raw, int pos, float* y, int lane) {
   float x[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u), __uint_as_float(raw.y << 16),
                 __uint_as_float(raw.y & 0xffff0000u)};
@@ -37,6 +37,7 @@ __device__ __forceinline__ bool place_row(const RopeParams& P, const float* w, b
     fine &= ss <= 3.4e38f;
     const float r = fine ? rsqrtf(fmaf(ss, 1.0f / kHeadDim, P.eps)) : __int_as_float(0x7fffffff);
     const float4 w4 = __ldg(reinterpret_cast<const float4*>(w) + lane);
+    fine &= max(max(__float_as_uint(fabsf(w4.x)), __float_as_uint(fabsf(w4.y))), max(__float_as_uint(fabsf(w4.z)), __float_as_uint(fabsf(w4.w)))) < 0x7f800000u;
     x[0] *= r * w4.x;
     x[1] *= r * w4.y;
     x[2] *= r * w4.z;

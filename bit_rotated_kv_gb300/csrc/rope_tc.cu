@@ -874,6 +874,7 @@ __global__ void __launch_bounds__(kRtThreads, 2) rope_tc_kernel(const __grid_con
       // 2^-22 of which hi and lo keep, where the smallest weight is not 2^10 below the largest, and no product overflows or vanishes where
       // the largest is near 1.
       const int top_at = (int)(wtop >> 23);
+      if (tid == 0 && norm && top_at == 255) set_status(P.r.status, KVQ_ERR_NONFINITE);
       const bool wide = weighted && (top_at - (int)(wlow >> 23) > 9 || top_at < 97 || top_at > 187 || kn > most);
       if (tid == 0) seg_sh = Seg{T.head_div > 1, norm, weighted, grow, turned, wide, pow2(kn), pow2(-kn) * t_back, least, most, t_back};
       rt_sync(kBarPlace, kRtWarps);

@@ -495,7 +495,8 @@ KVQ_API int kvq_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling,
  * bf16; besides that rounding the error is at most 2^-17 sum_j |T_ij| m_j, m_j the length of channel j's pair
  * after the norm.  It is not kv_rotate_qk's exact product, whose input rows are rounded after the rotation.  Copied
  * values are exact.  A head whose row holds an infinity or NaN, or (with a norm) whose squares sum to more than
- * float32 holds, gets a row that is not finite, and KVQ_ERR_NONFINITE (copied values aside).
+ * float32 holds, gets a row that is not finite, and KVQ_ERR_NONFINITE (copied values aside); so do all heads of a norm with a
+ * weight that is not finite.
  * rope NULL: no norm and no rotation (q_pos may then be NULL).
  * Of cfg the heads, batch, s_sink and ring_cap are used.
  * Execution: fewer than 896 (row, head) pairs that have a matrix (Hadamard: 1280) run on the CUDA cores, a slice of a matrix to a CTA;

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import bit_rotated_kv_gb300 as kvq
 from tests.test_gpu_rope import D, Call, _f64
 
 pytestmark = pytest.mark.gpu
@@ -103,3 +104,17 @@ def test_small_products(rows, x, t):
     c.tk, c.tkit, c.tv = (_f64(m) for m in (c.tr.t_k, c.tr.t_k_inv_t, c.tr.t_v))
     c.run().check()
     assert bool(c.q_out[:rows].any(-1).all())
+
+
+@pytest.mark.parametrize("rows", [5, 403])
+@pytest.mark.parametrize("which", ["q_norm", "k_norm"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_norm_weights_that_are_not_finite(rows, which, value):
+    c = Call(rows, 16, 4)
+    getattr(c.rope, which)[77] = value
+    c.run()
+    assert int(c.status.item()) == kvq.KVQ_ERR_NONFINITE
+    if which == "k_norm":                                  # (the queries are what they were)
+        c.status.zero_()
+        d = Call(rows, 16, 4).run()
+        assert torch.equal(c.q_out, d.q_out)
