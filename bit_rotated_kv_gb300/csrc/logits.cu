@@ -199,8 +199,8 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(const __grid_constant
   R.inv = __frcp_rn(R.rep);
   const float heat = U.temperature ? U.temperature[b] : 1.f;
   const bool sound = R.rep >= 0x1p-60f && R.rep <= 0x1p60f && fabsf(R.freq) < kInf && fabsf(R.pres) < kInf && heat >= 0.f && heat < kInf;
-  const bool greedy = heat < 0x1p-120f;                  // (1 / T must be a float32)
-  const float k2 = greedy ? 0.f : __fdiv_rn(1.4426950408889634f, heat);
+  const bool greedy = heat < 0x1p-149f;                  // (0.  Written == 0 the compiler gives bf16 with counts 48 registers instead of 63: 245 us)
+  const float k2 = greedy ? 0.f : __fdiv_rn(1.4426950408889634f, fmaxf(heat, 0x1p-120f));   // (1 / T must be a float32)
   const uint16_t* counts = kCounts ? U.counts + (long long)b * U.count_stride : nullptr;
   const uint32_t* mask = nullptr;
   bool fault = false, skip = !sound;                     // skip: a row of zeros

@@ -548,7 +548,8 @@ typedef struct kvq_logit_rules {         /* device pointers; NULL: that rule is 
  *   p        n_rows rows of `vocab` float32, p_stride elements apart; may be the logits themselves (float32, equal
  *            strides), and must not overlap them otherwise
  * In this order, in float32, one rounding an operation: l + bias; repetition; less frequency * times; less presence;
- * masked tokens to -infinity, whatever stood there; softmax of l / temperature.
+ * masked tokens to -infinity, whatever stood there; softmax of l / temperature (one between 0 and 2^-120 counts as 2^-120, which only
+ * logits within 2^-113 of the largest can tell from it).
  * KVQ_ERR_NONFINITE and a row of zeros: where nothing is left (every token masked or at -infinity), where a logit that
  * is not masked becomes NaN or +infinity, or where a number of the sequence's rules is not finite, the temperature
  * negative or the repetition not within 2^-60 .. 2^60.  Probabilities below 2^-126 are 0.  KVQ_ERR_BOUNDS and a row
