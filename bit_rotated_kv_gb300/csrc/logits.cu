@@ -506,6 +506,8 @@ __global__ void __launch_bounds__(256) count_kernel(const __grid_constant__ Coun
   }
   if (warp < warps) {
     const int r0 = warp * 32 * kPerLane;
+    // (an end behind the last row: the rows that there are belong to the sequence all the same)
+    if (warp == 0 && lane == 0) odd = __ldg(P.cu_rows + P.batch) > P.n_rows;
     int from[kPerLane];
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
@@ -588,18 +590,18 @@ __global__ void __launch_bounds__(kSweepThreads) prompt_kernel(const __grid_cons
   pdl_trigger();
   for (int i = tid; i < words; i += kSweepThreads) bits[i] = 0u;
   pdl_wait();
-  const int first = P.cu_rows[b], last = P.cu_rows[b + 1];
-  // rows of no sequence: before the first, behind the last, or where cu_rows falls
-  bool odd = first < 0 || last < first || last > P.n_rows || (b == 0 && first > 0) || (b == P.batch - 1 && last < P.n_rows);
+  const int first = P.cu_rows[b], end = P.cu_rows[b + 1], last = min(end, P.n_rows);
+  // rows of no sequence: before the first, behind the last, or where cu_rows falls; ends behind the last row
+  bool odd = first < 0 || end < first || end > P.n_rows || (b == 0 && first > 0) || (b == P.batch - 1 && end < P.n_rows);
   __syncthreads();
-  if (first >= 0 && last <= P.n_rows) {
+  if (first >= 0 && first < last) {
     auto mark = [&](int t) {
       if (t >= 0 && t < P.vocab) atomicOr(&bits[t >> 5], 1u << (t & 31));
       else odd = true;
     };
     // four tokens at a time from a boundary on, the others one by one
     const int32_t* from = P.token + first;
-    const int n = max(0, last - first), head = min(n, (int)(((16 - (reinterpret_cast<uintptr_t>(from) & 15)) & 15) >> 2));
+    const int n = last - first, head = min(n, (int)(((16 - (reinterpret_cast<uintptr_t>(from) & 15)) & 15) >> 2));
     const int fours = (n - head) >> 2;
     const int4* wide = reinterpret_cast<const int4*>(from + head);
     if (rank == 0 && tid < head) mark(__ldg(from + tid));

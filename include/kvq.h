@@ -571,7 +571,8 @@ KVQ_API int kv_logits_probs(const kvq_config* cfg, const kvq_logit_rules* rules,
  *                     kv_verify_tree, those of the kept nodes path[cu_rows[b] + j], 0 < j < n_accept[b] (node 0
  *                     was counted when it was drawn), and with next_token [B] the token behind them (-1: none).
  * Equal tokens may come any number of times.  Tokens outside the vocabulary, nodes outside the tree and rows of no
- * sequence are left out, with KVQ_ERR_BOUNDS.  Of cfg only batch is used; n_rows is at most 2^30 (KVQ_ERR_UNSUPPORTED).
+ * sequence are left out, with KVQ_ERR_BOUNDS; KVQ_ERR_BOUNDS also where cu_rows ends behind n_rows (the rows that there are
+ * are taken).  cu_rows does not fall: which rows are taken where it does is not said.  Of cfg only batch is used; n_rows is at most 2^30 (KVQ_ERR_UNSUPPORTED).
  * Execution: an atomic for each of a warp's different tokens; prompts of 2^16 rows or more, and on average 2^14 and a sixth of
  * the vocabulary a sequence, in one sweep over the counts, without atomics.  No other call may write the same rows of counts at
  * the same time. */
