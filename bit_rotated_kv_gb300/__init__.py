@@ -652,7 +652,8 @@ def kv_rope_qk(cfg: KVConfig, tr: Transform, rope: Rope | None, q, q_out, q_pos,
 
 @dataclass
 class LogitRules:
-    """What kv_logits_probs applies (see kvq_logit_rules in include/kvq.h); None: not that rule."""
+    """What kv_logits_probs applies (see kvq_logit_rules in include/kvq.h); None: not that rule.  Biases need bias_cu, a mask_row
+    its mask: the other tensors without them are refused."""
     temperature: torch.Tensor | None = None   # [batch] float32; so the next three
     repetition: torch.Tensor | None = None
     frequency: torch.Tensor | None = None
@@ -675,6 +676,10 @@ class LogitRules:
         cc = self.__dict__.get("_cc")
         if cc is None or cc[0] != key:
             w, i32, f32 = "kv_logits_probs", torch.int32, torch.float32
+            for part, rest in (("bias_cu", ("bias_token", "bias")), ("mask", ("mask_row",))):
+                for n in rest:                             # (a rule that its other half is missing for would not be applied)
+                    if getattr(self, part) is None and getattr(self, n) is not None:
+                        raise KVQError(KVQ_ERR_INVALID_ARG, f"{w}: {n} without {part}")
             per_seq = [0 if t is None else _addr(dev, t, f32, batch, f"{w}: {n}")
                        for n, t in (("temperature", self.temperature), ("repetition", self.repetition), ("frequency", self.frequency),
                                     ("presence", self.presence))]

@@ -190,3 +190,14 @@ def test_rope_rows_under_the_output():
     for name, size in (("q", 4 * 1024 + 1024), ("k", 4 * 256 + 256), ("v", 4 * 256 + 256)):
         for out in (X - 5 * 1024 + 16, X, X + size - 16):
             assert _rope(**{**far, name: X}, out=out) == kvq.KVQ_ERR_INVALID_ARG, (name, out)
+
+
+@pytest.mark.parametrize("part,kept", [("bias_cu", ("bias_token", "bias")), ("bias_cu", ("bias",)), ("bias_cu", ("bias_token",)), ("mask", ("mask_row",))])
+def test_halves_of_a_rule_are_refused(here, part, kept):
+    """Tensors of a rule without the one that turns it on: the rule would not be applied, a forgotten bias_cu unban what is banned."""
+    good = _args()["kv_logits_probs"][1]["rules"]
+    rules = kvq.LogitRules(**{f: None if f[:4] == part[:4] and f not in kept else getattr(good, f) for f in good.__dataclass_fields__})
+    assert f"without {part}" in _refusal("kv_logits_probs", rules=rules)
+    for f in kept:
+        setattr(rules, f, None)
+    assert "parent" in _refusal("kv_logits_probs", rules=rules, parent=_i(1))      # (nothing of it: that rule is not applied)
