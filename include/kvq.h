@@ -485,18 +485,21 @@ KVQ_API int kvq_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling,
  *   q        [n_q_rows][Hq][d] bf16, rows q_stride elements apart (so for k and v: three parts of one fused
  *            projection do; strides are multiples of 8 and at least H d, bases 16-byte aligned)
  *   q_out    [n_q_rows][Hq][d] bf16 (16-byte aligned): T_K^{-T} rope(norm(q)); must not overlap the rows of q, k or v
+ *            (each from its first row's beginning to its last one's end)
  *   q_pos    [n_q_rows] int32: each query's position in the text (any value; NULL when n_q_rows == 0)
  *   k, v     [n_kv_rows][Hkv][d] bf16 likewise; seq_idx, pos [n_kv_rows] int32 as for kv_rotate_qk
  *   rope_pos [n_kv_rows] int32: each key's position in the text where it is not its token's number (the nodes
  *            of a drafted tree: the number of tokens before the drafts plus the node's depth); NULL: pos
  * Keys become T_K rope(norm(k)), values T_V v or copies of v, written to sink and ring as kv_rotate_qk does:
  * the same bounds, status and seq_len.  n_kv_rows and n_q_rows may differ, and either may be 0.
- * Arithmetic is float32 to the end (the norm's mean, the rotation, the transform's sums) with one rounding to
- * bf16; besides that rounding the error is at most 2^-17 sum_j |T_ij| m_j, m_j the length of channel j's pair
- * after the norm.  It is not kv_rotate_qk's exact product, whose input rows are rounded after the rotation.  Copied
- * values are exact.  A head whose row holds an infinity or NaN, or (with a norm) whose squares sum to more than
- * float32 holds, gets a row that is not finite, and KVQ_ERR_NONFINITE (copied values aside); so do all heads of a norm with a
- * weight that is not finite.
+ * Arithmetic is float32 (the norm's mean, the rotation, the transform's sums) with one rounding to bf16 at the end; on the
+ * tensor cores (Execution) sines and cosines have 20 bits, and the transform's operands 21, as pairs of fp16.  With m_j the
+ * length of channel j's pair after the norm, and besides that rounding, output i is off by at most 2^-17 sum_j |T_ij| m_j, and on
+ * the tensor cores by 2^-22 (max_j m_j sum_j |T_ij| + max_j |T_ij| sum_j m_j) more: that counts where T_i is next to nothing at the
+ * row's large channels (identity, diagonal), below which 22 bits are kept.  It is not kv_rotate_qk's exact product, whose
+ * input rows are rounded after the rotation.  Copied values are exact.  A head whose row holds an infinity or NaN, or (with a norm)
+ * whose squares sum to more than float32 holds, gets a row that is not finite, and KVQ_ERR_NONFINITE (copied values aside); so
+ * do all heads of a norm with a weight that is not finite.
  * rope NULL: no norm and no rotation (q_pos may then be NULL).
  * Of cfg the heads, batch, s_sink and ring_cap are used.
  * Execution: fewer than 896 (row, head) pairs that have a matrix (Hadamard: 1280) run on the CUDA cores, a slice of a matrix to a CTA;
@@ -546,10 +549,11 @@ typedef struct kvq_logit_rules {         /* device pointers; NULL: that rule is 
  *   parent, token [n_rows] int32: the tree as for kv_verify_tree, or NULL: the rows are no drafts.  The tokens of a
  *            node and its ancestors count as generated in its row, roots left out: theirs has been counted
  *   p        n_rows rows of `vocab` float32, p_stride elements apart; may be the logits themselves (float32, equal
- *            strides), and must not overlap them otherwise
+ *            strides), and must not overlap them otherwise (from the first row's beginning to the last one's end)
  * In this order, in float32, one rounding an operation: l + bias; repetition; less frequency * times; less presence;
  * masked tokens to -infinity, whatever stood there; softmax of l / temperature (one between 0 and 2^-120 counts as 2^-120, which only
- * logits within 2^-113 of the largest can tell from it).
+ * logits within 2^-113 of the largest can tell from it).  The softmax takes the special function units' exponential: besides the
+ * roundings before it, p is off by at most 2^-17 + 2^-22 (max l - l) / temperature of itself.
  * KVQ_ERR_NONFINITE and a row of zeros: where nothing is left (every token masked or at -infinity), where a logit that
  * is not masked becomes NaN or +infinity, or where a number of the sequence's rules is not finite, the temperature
  * negative or the repetition not within 2^-60 .. 2^60.  Probabilities below 2^-126 are 0.  KVQ_ERR_BOUNDS and a row

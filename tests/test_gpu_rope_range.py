@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import bit_rotated_kv_gb300 as kvq
+from tests import step_ref
 from tests.test_gpu_rope import D, Call, _f64
 
 pytestmark = pytest.mark.gpu
@@ -118,3 +119,42 @@ def test_norm_weights_that_are_not_finite(rows, which, value):
         c.status.zero_()
         d = Call(rows, 16, 4).run()
         assert torch.equal(c.q_out, d.q_out)
+
+
+# ---- channels far apart under matrices that do not mix them ---------------------------------------
+def _within(got, want, m, mats, gqa):
+    """The header's bound: half a step of bf16, 2^-17 sum |T_ij| m_j, and 2^-22 of (max m_j) sum |T_ij| + (max |T_ij|) sum m_j.
+
+    (Placed entries and the matrix's are two fp16 under powers of two that put a row's largest pair, and each matrix row's largest entry, at 2^-2 or
+    above and below 2^15.  hi takes 11 bits exactly down to 2^-14, lo the next 11 of them to nearest, both in steps of 2^-24 at the finest: an entry
+    is off by 2^-21 of itself and 2 * 2^-25, that is 2^-22 of its row's largest.)"""
+    for h in range(got.shape[1]):
+        t = np.abs(np.asarray(mats[h // gqa], np.float64))
+        bound = 2.0**-17 * (m[:, h] @ t.T) + 2.0**-22 * (m[:, h].max(-1, keepdims=True) * t.sum(-1) + m[:, h].sum(-1, keepdims=True) * t.max(-1))
+        off = np.abs(got[:, h] - want[:, h])
+        assert (off <= 2.0**-8 * np.abs(want[:, h]) * (1 + 2.0**-8) + bound + 2.0**-133).all(), h
+
+
+@pytest.mark.parametrize("rows", [6, 403])
+@pytest.mark.parametrize("kind", ["identity", "diagonal", "invertible"])
+@pytest.mark.parametrize("norm", [False, True], ids=["plain", "norm"])
+def test_channels_far_apart(rows, kind, norm):
+    """Channels up to 60 binades apart within a row, under matrices that leave them apart."""
+    c = Call(rows, 16, 4, "identity" if kind == "diagonal" else kind, norm=norm, rot=64, tv=kind != "identity")
+    rng = np.random.default_rng(5)
+    c.fused.mul_(torch.from_numpy(2.0 ** -rng.integers(0, 60, c.fused.shape)).cuda().to(torch.bfloat16))
+    if kind == "diagonal":
+        d = [torch.from_numpy(2.0 ** rng.integers(-30, 1, D)).float().cuda() for _ in range(2)]
+        for t, x in zip((c.tr.t_k, c.tr.t_k_inv_t), d, strict=True):
+            t.mul_(x)                                      # (each column by its own: rows of different sizes)
+        c.tk, c.tkit = _f64(c.tr.t_k), _f64(c.tr.t_k_inv_t)
+    c.run()
+    assert int(c.status.item()) == 0
+    angle = step_ref.phases(c.rope.freq.cpu().tolist(), c.pos)
+    y, m = step_ref.placed(_f64(c.q), angle, False, 1.0, c.wq, c.eps)
+    _within(_f64(c.q_out[:rows]), step_ref.transformed(y, m, c.tkit, 4)[0], m, c.tkit, 4)
+    y, m = step_ref.placed(_f64(c.k), angle, False, 1.0, c.wk, c.eps)
+    want = step_ref.transformed(y, m, c.tk, 1)[0]
+    sink, ring = _f64(c.cache.sink_k), _f64(c.cache.ring_k)
+    got = np.stack([sink[s, :, p] if p < c.cfg.s_sink else ring[s, :, p % c.cap] for s, p in zip(c.seq, c.pos, strict=True)])
+    _within(got, want, m, c.tk, 1)
