@@ -158,3 +158,28 @@ def test_channels_far_apart(rows, kind, norm):
     sink, ring = _f64(c.cache.sink_k), _f64(c.cache.ring_k)
     got = np.stack([sink[s, :, p] if p < c.cfg.s_sink else ring[s, :, p % c.cap] for s, p in zip(c.seq, c.pos, strict=True)])
     _within(got, want, m, c.tk, 1)
+
+
+# ---- forms of the tensor-core kernel that need a call of their own --------------------------------
+@pytest.mark.parametrize("rows", [7, 403])
+@pytest.mark.parametrize("layout,rot", [(0, 128), (1, 128), (0, 96), (1, 64), (0, 6), (0, 126)])
+@pytest.mark.parametrize("scale", [1.25, 0.0, 2.0**-20, 2.0**30])
+def test_scales_without_a_norm(rows, layout, rot, scale):
+    """YaRN's factor on heads that have no norm; factors that take the rotated channels far from the others."""
+    for kind in ("orthogonal", "hadamard"):
+        Call(rows, 16, 4, kind, layout=layout, rot=rot, norm=False, scale=scale, seed=4).run().check()
+
+
+@pytest.mark.parametrize("rows", [7, 403])
+@pytest.mark.parametrize("norm", [False, True], ids=["plain", "norm"])
+def test_matrices_whose_rows_differ_in_size(rows, norm):
+    """Rows of one matrix up to 2^40 apart, rows of zeros among them."""
+    c = Call(rows, 16, 4, norm=norm, rot=64)
+    rng = np.random.default_rng(8)
+    for t in (c.tr.t_k, c.tr.t_k_inv_t, c.tr.t_v):
+        f = 2.0 ** rng.integers(-20, 21, (t.shape[0], D))
+        f[:, 5] = 0
+        f[1] = np.where(np.arange(D) == 9, 2.0**9, 1.0)    # (one matrix: a row alone)
+        t.mul_(torch.from_numpy(f).float().cuda()[:, :, None])
+    c.tk, c.tkit, c.tv = (_f64(m) for m in (c.tr.t_k, c.tr.t_k_inv_t, c.tr.t_v))
+    c.run().check()
