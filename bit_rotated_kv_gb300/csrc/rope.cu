@@ -10,7 +10,7 @@
 // matrix and a chunk of the (row, head) pairs that share it: a whole matrix to a CTA would leave most SMs without
 // one at a single token (8 kv heads, 3 matrices each), and its 64 KB would be the longest wait of the call.  The
 // four slices of a pair each place its row (norm and rotation), which costs less than passing it on would.  Latency
-// bounds it (launch, matrix slice, row, destination, one after another): one token of 32 + 8 + 8 heads 3.5 us, sixteen 5.2.
+// bounds it (launch, matrix slice, row, destination, one after another): one token of 32 + 8 + 8 heads 2.5 us, sixteen 5.1.
 #include "rope.cuh"
 
 #include <algorithm>
@@ -22,7 +22,9 @@ constexpr int kSlice = 32;                        // outputs of a CTA
 constexpr int kSlices = kHeadDim / kSlice;
 constexpr int kRopeThreads = 4 * kSlice;          // four threads to an output, 32 inputs each
 constexpr int kRopeWarps = kRopeThreads / 32;
-constexpr int kMaxRows = 16;                      // pairs of a chunk
+constexpr int kMaxRows = 8;                       // pairs of a chunk: more than calls of this kernel come to (5)
+constexpr int kRopeSlots = 8 * kSms;              // CTAs that the chunks are made for
+static_assert(kRopeTcPairs <= kRopeTcPairsHad && kRopeTcPairsHad * kSlices <= (long long)kRopeSlots * kMaxRows, "pairs of a chunk");
 constexpr int kMaxCopies = 8;                     // rows a warp copies
 
 // One warp places a row: norm and rotation, float32, into shared memory.  False when the row or a weight is not finite.
@@ -116,8 +118,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
   tile /= kSlices;
   const int pairs = T.rows * T.head_div;
   const int chunks = (pairs + P.r.rt - 1) / P.r.rt;
-  const int tiles_per_mat = (chunks + P.r.rpc - 1) / P.r.rpc;
-  const int mh = tile / tiles_per_mat, c0 = (tile % tiles_per_mat) * P.r.rpc, c1 = min(chunks, c0 + P.r.rpc);
+  const int mh = tile / chunks, p0 = (tile % chunks) * P.r.rt, np = min(P.r.rt, pairs - p0);
   // this thread's part of output o's matrix row: four threads share it, 16-byte pieces in turn (shared memory
   // then serves the four from different banks)
   const int o = kSlice * slice + (tid >> 2), part = tid & 3;
@@ -137,66 +138,62 @@ __global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(const __grid_co
     }
   }
   pdl_wait();
-  for (int c = c0; c < c1; ++c) {
-    const int p0 = c * P.r.rt, np = min(P.r.rt, pairs - p0);
-    // a warp's rows (warp, warp + 4, ..) are all asked for before the first is placed, and lane k finds out where the
-    // k-th goes: one after another, each row's four dependent loads would be waited for in turn
-    constexpr int kMine = kMaxRows / kRopeWarps;
-    const int32_t* rpos = P.rpos[tt];
-    uint2 raw[kMine];
-    int pos[kMine];
+  // a warp's rows (warp, warp + 4) are both asked for before the first is placed, and lane k finds out where the
+  // k-th goes: one after another, each row's four dependent loads would be waited for in turn
+  constexpr int kMine = kMaxRows / kRopeWarps;
+  const int32_t* rpos = P.rpos[tt];
+  uint2 raw[kMine];
+  int pos[kMine];
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-      const int j = warp + kRopeWarps * k;
-      int row, head;
-      tile_row(T, mh, p0 + min(j, np - 1), row, head);
-      raw[k] = __ldg(reinterpret_cast<const uint2*>(rope_src(P, tt, row, head)) + lane);
-      pos[k] = rpos ? __ldg(rpos + row) : 0;
+  for (int k = 0; k < kMine; ++k) {
+    const int j = warp + kRopeWarps * k;
+    int row, head;
+    tile_row(T, mh, p0 + min(j, np - 1), row, head);
+    raw[k] = __ldg(reinterpret_cast<const uint2*>(rope_src(P, tt, row, head)) + lane);
+    pos[k] = rpos ? __ldg(rpos + row) : 0;
+  }
+  bool fine = true;                                      // of the lane's own row
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    const int j = warp + kRopeWarps * k;
+    if (j < np) {
+      const bool f = place_row(P, P.norm[tt], rpos != nullptr, raw[k], pos[k], ys[j], lane);
+      if (lane == k) fine = f;
     }
-    bool fine = true;                                    // of the lane's own row
+  }
+  const int own = warp + kRopeWarps * lane;
+  if (lane < kMine && own < np) {
+    int row, head;
+    tile_row(T, mh, p0 + own, row, head);
+    const int b = T.is_query ? 0 : __ldg(P.r.seq_idx + row), p = T.is_query ? 0 : __ldg(P.r.pos + row);
+    dst_sh[own] = rot_dst(P.r, T, row, head, b, p, slice == 0);
+    if (!fine && slice == 0 && dst_sh[own]) set_status(P.r.status, KVQ_ERR_NONFINITE);
+  }
+  __syncthreads();
+  for (int j0 = 0; j0 < np; j0 += 4) {
+    float acc[4];
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-      const int j = warp + kRopeWarps * k;
-      if (j < np) {
-        const bool f = place_row(P, P.norm[tt], rpos != nullptr, raw[k], pos[k], ys[j], lane);
-        if (lane == k) fine = f;
-      }
-    }
-    const int own = warp + kRopeWarps * lane;
-    if (lane < kMine && own < np) {
-      int row, head;
-      tile_row(T, mh, p0 + own, row, head);
-      const int b = T.is_query ? 0 : __ldg(P.r.seq_idx + row), p = T.is_query ? 0 : __ldg(P.r.pos + row);
-      dst_sh[own] = rot_dst(P.r, T, row, head, b, p, slice == 0);
-      if (!fine && slice == 0 && dst_sh[own]) set_status(P.r.status, KVQ_ERR_NONFINITE);
-    }
-    __syncthreads();
-    for (int j0 = 0; j0 < np; j0 += 4) {
-      float acc[4];
+    for (int j = 0; j < 4; ++j) {
+      acc[j] = 0.f;
+      if (j0 + j < np) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[j] = 0.f;
-        if (j0 + j < np) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 y = *reinterpret_cast<const float4*>(&ys[j0 + j][16 * i + 4 * part]);
-            acc[j] = fmaf(t[4 * i], y.x, acc[j]);
-            acc[j] = fmaf(t[4 * i + 1], y.y, acc[j]);
-            acc[j] = fmaf(t[4 * i + 2], y.z, acc[j]);
-            acc[j] = fmaf(t[4 * i + 3], y.w, acc[j]);
-          }
+        for (int i = 0; i < 8; ++i) {
+          const float4 y = *reinterpret_cast<const float4*>(&ys[j0 + j][16 * i + 4 * part]);
+          acc[j] = fmaf(t[4 * i], y.x, acc[j]);
+          acc[j] = fmaf(t[4 * i + 1], y.y, acc[j]);
+          acc[j] = fmaf(t[4 * i + 2], y.z, acc[j]);
+          acc[j] = fmaf(t[4 * i + 3], y.w, acc[j]);
         }
       }
-      // sums over the four parts; thread `part` ends with row j0 + part
-      const bool up = part & 2, odd = part & 1;
-      float u0 = up ? acc[2] : acc[0], u1 = up ? acc[3] : acc[1];
-      u0 += __shfl_xor_sync(0xffffffffu, up ? acc[0] : acc[2], 2);
-      u1 += __shfl_xor_sync(0xffffffffu, up ? acc[1] : acc[3], 2);
-      const float s = (odd ? u1 : u0) + __shfl_xor_sync(0xffffffffu, odd ? u0 : u1, 1);
-      uint16_t* dst = j0 + part < np ? dst_sh[j0 + part] : nullptr;
-      if (dst) dst[o] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
     }
-    __syncthreads();
+    // sums over the four parts; thread `part` ends with row j0 + part
+    const bool up = part & 2, odd = part & 1;
+    float u0 = up ? acc[2] : acc[0], u1 = up ? acc[3] : acc[1];
+    u0 += __shfl_xor_sync(0xffffffffu, up ? acc[0] : acc[2], 2);
+    u1 += __shfl_xor_sync(0xffffffffu, up ? acc[1] : acc[3], 2);
+    const float s = (odd ? u1 : u0) + __shfl_xor_sync(0xffffffffu, odd ? u0 : u1, 1);
+    uint16_t* dst = j0 + part < np ? dst_sh[j0 + part] : nullptr;
+    if (dst) dst[o] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
   }
 }
 
@@ -271,26 +268,14 @@ extern "C" int kvq_launch_rope(const kvq_config* cfg, const kvq_transform* tr, c
       return KVQ_ERR_CUDA;
     return launch_rope_tc(P, stream);
   }
-  // pairs of a chunk: as many as make about eight CTAs an SM of all the slices (128 threads and 8 KB each); chunks
-  // of a CTA: more than one once the chunks are full
-  const long long slots = 8LL * kSms;
-  R.rt = (int)std::min((long long)kMaxRows, std::max(4LL, (pairs * kSlices + slots - 1) / slots));
-  const long long per_cta = (pairs * kSlices + slots * R.rt - 1) / (slots * R.rt);
-  R.rpc = (int)std::min(std::max(per_cta, 1LL), 1LL << 20);
-  long long total = 0;
+  // pairs of a chunk: as many as make about eight CTAs an SM of all the slices (128 threads and 4 KB each)
+  R.rt = (int)std::max(4LL, (pairs * kSlices + kRopeSlots - 1) / kRopeSlots);
   for (int i = 0; i < 3; ++i) {
     if (R.t[i].mode == ROT_COPY) continue;
-    const long long here = (long long)R.t[i].rows * R.t[i].head_div;
-    const long long chunks = (here + R.rt - 1) / R.rt;
-    const long long tiles = (R.t[i].heads / R.t[i].head_div) * ((chunks + R.rpc - 1) / R.rpc) * kSlices;
-    if (tiles > 0x3fffffffLL) return KVQ_ERR_UNSUPPORTED;
-    R.n_dense[i] = (int)tiles;
-    total += tiles;
+    const int chunks = (R.t[i].rows * R.t[i].head_div + R.rt - 1) / R.rt;
+    R.n_dense[i] = R.t[i].heads / R.t[i].head_div * chunks * kSlices;
+    R.dense_total += R.n_dense[i];
   }
-  R.dense_total = (int)total;
-  const long long blocks = total + (R.warp_total + kRopeWarps - 1) / kRopeWarps;
-  if (blocks > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
-  return launch_pdl(rope_rows_kernel, dim3((unsigned)blocks), dim3(kRopeThreads), 0, stream, P) == cudaSuccess
-             ? KVQ_OK
-             : KVQ_ERR_CUDA;
+  const unsigned blocks = (unsigned)(R.dense_total + (R.warp_total + kRopeWarps - 1) / kRopeWarps);
+  return launch_pdl(rope_rows_kernel, dim3(blocks), dim3(kRopeThreads), 0, stream, P) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }

@@ -39,8 +39,8 @@ __device__ __forceinline__ float hadamard_sign(int i, int j) {
   return __uint_as_float(0x3f800000u | ((uint32_t)(__popc(i & j) & 1) << 31));
 }
 // (row, head) pairs from which a call's products run on the tensor cores, where anything of up to a chunk an SM takes
-// 7 us (with the launch of copies 7.4).  The CUDA cores take 5.2 us for 16 rows of 32 + 8 + 8 heads (768 pairs), 7.6 for 20,
-// 10.1 for 32; 4.7 for 16 rows of 64 + 8 Hadamard heads (1,152), 7.2 for 20, 9.1 for 24.
+// 7 us (with the launch of copies 7.4).  The CUDA cores take 5.1 us for 18 rows of 32 + 8 + 8 heads (864 pairs), 7.6 for 20,
+// 10.1 for 32; 5.2 for 16 rows of 64 + 8 Hadamard heads (1,152), 7.2 for 20, 9.1 for 24.
 constexpr long long kRopeTcPairs = 896, kRopeTcPairsHad = 1280;
 // ... which this launches (P.r.n_dense is set there; copies are the caller's).
 int launch_rope_tc(RopeParams P, cudaStream_t stream);
