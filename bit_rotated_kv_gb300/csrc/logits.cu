@@ -14,8 +14,10 @@
 // are all on their way before the first is used.  Biases and the drafted path touch few tokens: the pass over the slice
 // does without them and the tokens concerned are computed again afterwards, by token, so that one that is in both lists is
 // right either way.
-// What it measured: those 64 x 16 rows 221 us (floor by bytes 106: the instructions of three passes and the waits between
-// them bound it), 64 rows of 152 K 25 us (11.5), one row of 32 K 4.6 us (a launch and four waits one after another).
+// What it measured: those 64 x 16 rows 221 us (floor by bytes 106: neither issue, 52%, nor DRAM, 37%, is at its limit; a slice goes
+// through shared memory four times, between barriers that are the largest stall), 64 rows of 152 K 25 us (11.5: 768 CTAs, of which
+// four an SM, 608, are on the chip at once: a second wave that is mostly empty), 48 rows of 100,003 16 us (3.3: three of four such rows
+// begin off a boundary and go token by token), one row of 32 K 4.4 us (a launch and four waits one after another).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -489,7 +491,8 @@ __device__ __forceinline__ void add_tokens(const Half& h, uint32_t old, uint32_t
 constexpr int kPerLane = 4;          // rows of a lane: a warp takes 128 in a row, and their loads are on their way together
 
 // Latency bounds a step's few tokens (a chain of four loads and an atomic); a prompt's many, the random words that they
-// mark: 8 K tokens of each of 16 sequences take 6.6 us with the clearing of their counts.  Equal tokens of a warp are counted
+// mark: 8 K tokens of each of 16 sequences take 6.6 us with the clearing of their counts.  4 K answered tokens of each of 16 take 9 us
+// (0.3 MB): 500 warps of 128 rows are 63 CTAs, fewer than half of the SMs.  Equal tokens of a warp are counted
 // with one atomic (an answer's most frequent ones meet there).
 __global__ void __launch_bounds__(256) count_kernel(const __grid_constant__ CountParams P) {
   pdl_trigger();

@@ -6,13 +6,13 @@
 // many for 64 rows of an SM.  Both products therefore take two fp16 parts of each operand rather than the integer digits
 // of rotate_tc.cu: T row i and x row r are brought under powers of two so that their largest entry lies below 2^15,
 // and split as hi + lo, 11 bits each.  hi hi + lo hi + hi lo, summed in float32 by the tensor cores, leaves out 2^-20
-// of sum |T_ij x_j| at most (bf16's half step is 2^-8 of the result); three MMAs of 16 inputs instead of nine.  Entries
-// 2^-29 of their row's largest lose bits of lo, 2^-40 of that largest.  A Walsh-Hadamard matrix is +-1, its 1/sqrt(128)
-// left to the end: two MMAs.
+// of sum |T_ij x_j| at most (bf16's half step is 2^-8 of the result); three MMAs of 16 inputs instead of nine.  fp16 steps by 2^-24
+// at the finest, so an entry is also off by 2^-24 of a row's unit: 2^-37 of its largest entry where the power of two goes by
+// that, 2^-22 at worst where a norm's rows share one.  A Walsh-Hadamard matrix is +-1, its 1/sqrt(128) left to the end: two MMAs.
 //
-// The norm's factor belongs to a row, so it too is left to the end, and the weights take the power of two: norm and
-// scaling cost one product a channel.  Sine and cosine are the SFU's (2^-20.9 of the pair's length), from phases in
-// whole numbers.  Lanes hold both channels of a pair: eight lanes to a row, two vectors of eight channels each.
+// The norm's factor belongs to a row, so the weights take the power of two with it: norm and scaling cost one product a channel.
+// Rows far below the norm's epsilon and weights far apart take another way (size_rows).  Sine and cosine are the SFU's (2^-20.9 of
+// the pair's length), from phases in whole numbers.  Lanes hold both channels of a pair: eight lanes to a row, two vectors of eight channels each.
 //
 // Layout: two CTAs on an SM.  A CTA takes a run of chunks of 64 (row, head) pairs.  T hi and lo of its matrix stay in
 // TMEM (the A operand, lane = output, 64 columns each); rows come by asynchronous copies two chunks ahead and go through
@@ -23,10 +23,11 @@
 // A call of a chunk or less for each SM takes 7 us, half of it the matrix's way into TMEM (through shared memory, asked for before
 // the grid ahead has ended).
 //
-// That chunk of 16 x 2048 tokens takes 208 us with its values' copies, 183 without (3.7 TB/s).  What bounds it are the
-// operations of placing rows: the schedulers issue in 62% of the clocks, the shared-memory pipe is busy 65%, and a CTA's
-// chunk of 64 rows takes 4.6 K clocks, 3.5 K of them from its rows to the buffer; DRAM is busy 41%, the tensor cores 30%.  What
-// was tried: rows kept in registers a chunk ahead with three buffers 267 us against 217; bulk copies of rows by one warp 289,
+// That chunk of 16 x 2048 tokens takes 211 us with its values' copies, 186 without (3.6 TB/s).  What bounds it are the two
+// buffers: a chunk of 64 rows is placed in 3.4 to 3.9 K clocks, its MMAs end 2.3 K later and its results are out of the same buffer 2.4 K
+// after that, so that two buffers give a chunk every 4.15 K at best; it is 4.6 K, and those who place wait a quarter of it.  The
+// schedulers issue in 63% of the clocks, the shared-memory pipe is busy 65%, DRAM 42%, the tensor cores 30%.  What was tried:
+// rows kept in registers a chunk ahead with three buffers 267 us against 217; bulk copies of rows by one warp 289,
 // and 96 registers for those who place and 40, 24 for the others 276, against 248.
 #include "rope.cuh"
 #include "tc.cuh"
@@ -157,8 +158,9 @@ __device__ __forceinline__ Place place_of(const RopeParams& P, int chunk) {
 // The first chunk of a CTA.  Where CTAs have many chunks (sixteen on average), those whose rows share a token count
 // kCostSame, others, which come in shorter pieces and with a sine and cosine each, kCostOwn, and the grid's first half gets
 // kShare / 32: of the two CTAs on an SM the first comes to issue more often.  (16 x 2048 tokens, 40 heads: 239 us by chunks
-// alone, 230 by 7 : 8 in halves, 215 so.)  Where they have few, a chunk more is what counts (3 x 777 tokens: 25.5 us by
-// chunks, 28.4 so).
+// alone, 230 by 7 : 8 in halves, 215 so.  Where they have few, a chunk more is what counts (3 x 777 tokens: 25.5 us by
+// chunks, 28.4 so.)  Both numbers are that shape's: chunks without a norm or a rotation, interleaved or odd layouts, and values under
+// T_V cost other than these, and are divided by them all the same.
 constexpr int kCostSame = 7, kCostOwn = 8, kShare = 17;
 __device__ __forceinline__ int first_chunk(const RopeParams& P, int cta) {
   if (P.r.dense_total < 16 * 2 * kSms) return (int)((long long)P.r.dense_total * cta / gridDim.x);
@@ -276,8 +278,8 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
 // The powers of two of a slot's two rows from their channels as they are after norm and weights.  The one that all rows of a
 // normed head share (Seg) is that of the largest numbers such a row can hold: it suits rows whose mean square is not far below
 // the norm's epsilon under weights that are not far apart, and costs one product a channel.  Elsewhere hi and lo would lose digits under it:
-// a row far below epsilon stays as small as it came, and one may have nothing where the large weights are.  Here the row's digits (bfloat16: exactly) are brought to
-// 1 .. 2 first, so that neither they nor their products with the weights vanish on the way, whatever their size.
+// a row far below epsilon stays as small as it came, and one may have nothing where the large weights are.  Here the row's digits
+// (bfloat16: exactly) are brought to 1 .. 2 first, so that neither they nor their products with the weights vanish on the way, whatever their size.
 __device__ __forceinline__ void size_rows(const Seg& g, const Lane& L, uint32_t norm_s, const float (&r)[2], uint32_t (&wa)[2][4], uint32_t (&wb)[2][4],
                                           float2 (&up)[2], float (&back)[2], bool (&fine)[2]) {
 #pragma unroll
@@ -525,7 +527,7 @@ __device__ __forceinline__ void place_rows(const RopeParams& P, const Seg& g, co
   }
   // (Behind the products, and from global memory: the buffer that the rows came from may hold others by now, and a branch between the sums of
   // squares and the products kept these from covering those, 219 us for 16 x 2048 tokens instead of 210.  With the weights' choice
-  // it is 213; 321 where the weights are far apart, 419 where all rows are small.)
+  // it is 211; 316 where the weights are far apart, 421 where all rows are small.)
   if (apart) place_apart<kMode>(P, g, L, w, left, pos[0], pos[1], xb, norm_s, freq_s, fac_s);
 }
 template <int kMode, int kW>
